@@ -56,6 +56,23 @@ EXPORTED = (
     "tp_attn_workspace_offset",
 )
 
+# The same for tp_rope.h and tp_grad.h.
+EXPORTED_ROPE = (
+    "tp_rope_create", "tp_rope_destroy", "tp_rope_frequencies",
+    "tp_rope_apply", "tp_qk_norm_forward", "tp_qk_norm_workspace_bytes",
+    "tp_qk_norm_backward",
+)
+EXPORTED_GRAD = ("tp_grad_workspace_bytes", "tp_grad_norm", "tp_grad_clip")
+
+TPROPE_MAX_HEAD_DIM = 256
+TPROPE_SCALE_NONE = 0
+TPROPE_SCALE_LINEAR = 1
+TPROPE_SCALE_NTK = 2
+TPROPE_SCALE_YARN = 3
+TPROPE_SCALE_CUSTOM = 4
+TPQK_RMSNORM = 1
+TPQK_LAYERNORM = 2
+
 TPMLP_FP8_PACK_SCALES = 0
 TPMLP_FP8_PACK_AQT = 1
 TPMLP_FP8_PACK_BQT = 2
@@ -97,6 +114,45 @@ class tp_attn_config(ctypes.Structure):
                 ("seq_len", ctypes.c_int), ("causal", ctypes.c_int),
                 ("use_layernorm", ctypes.c_int), ("ln_eps", ctypes.c_float),
                 ("use_residual", ctypes.c_int)]
+
+
+class tp_rope_config(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_length", ctypes.c_double),
+                ("slow_turns", ctypes.c_double),
+                ("fast_turns", ctypes.c_double),
+                ("amplitude", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+class tp_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_longlong),
+                ("group_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("heads", ctypes.c_int),
+                ("group", ctypes.c_int)]
+
+
+class tp_positions(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("is_int64", ctypes.c_int),
+                ("offset", ctypes.c_longlong), ("seq_len", ctypes.c_longlong)]
+
+
+class tp_qk_norm(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int), ("eps", ctypes.c_float),
+                ("q_gamma", ctypes.c_void_p), ("q_beta", ctypes.c_void_p),
+                ("k_gamma", ctypes.c_void_p), ("k_beta", ctypes.c_void_p)]
+
+
+class tp_qk_norm_grads(ctypes.Structure):
+    _fields_ = [("q_gamma", ctypes.c_void_p), ("q_beta", ctypes.c_void_p),
+                ("k_gamma", ctypes.c_void_p), ("k_beta", ctypes.c_void_p)]
+
+
+class tp_grad_tensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("numel", ctypes.c_longlong), ("dtype", ctypes.c_int)]
 
 
 class TPMLPError(RuntimeError):
@@ -218,6 +274,30 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.tp_attn_set_ln_prologue.restype = _i
     L.tp_attn_set_wait_budget.argtypes = [_vp, ctypes.c_ulonglong]
     L.tp_attn_set_wait_budget.restype = _i
+    # Structures travel as addresses: ctypes.byref of the classes above.
+    L.tp_rope_create.argtypes = [ctypes.POINTER(tp_rope_config),
+                                 ctypes.POINTER(_vp)]
+    L.tp_rope_create.restype = _i
+    L.tp_rope_destroy.argtypes = [_vp]
+    L.tp_rope_destroy.restype = _i
+    L.tp_rope_frequencies.argtypes = [_vp, ctypes.POINTER(ctypes.c_double),
+                                      ctypes.POINTER(ctypes.c_double)]
+    L.tp_rope_frequencies.restype = _i
+    L.tp_rope_apply.argtypes = [_vp, _i, _i, _i] + [_vp] * 6
+    L.tp_rope_apply.restype = _i
+    L.tp_qk_norm_forward.argtypes = [_vp, _i, _i] + [_vp] * 7
+    L.tp_qk_norm_forward.restype = _i
+    L.tp_qk_norm_workspace_bytes.argtypes = [_vp]
+    L.tp_qk_norm_workspace_bytes.restype = _sz
+    L.tp_qk_norm_backward.argtypes = ([_vp, _i, _i] + [_vp] * 10 + [_sz, _vp])
+    L.tp_qk_norm_backward.restype = _i
+    L.tp_grad_workspace_bytes.argtypes = [_i]
+    L.tp_grad_workspace_bytes.restype = _sz
+    L.tp_grad_norm.argtypes = [_i, _vp, _vp, _vp, _sz, _vp]
+    L.tp_grad_norm.restype = _i
+    L.tp_grad_clip.argtypes = [_i, _vp, ctypes.c_double, ctypes.c_double, _vp,
+                               _vp, _sz, _vp]
+    L.tp_grad_clip.restype = _i
     if path is None:
         _lib = L
     return L
@@ -527,3 +607,80 @@ def tp_attn_set_ln_prologue(handle, enable: bool) -> None:
 
 def tp_attn_set_wait_budget(handle, ns: int) -> None:
     _check(lib().tp_attn_set_wait_budget(handle, ns), "tp_attn_set_wait_budget")
+
+
+# ---------------------------------------------------------- queries, keys --
+
+def tp_rope_create(config: tp_rope_config) -> int:
+    h = _vp()
+    _check(lib().tp_rope_create(ctypes.byref(config), ctypes.byref(h)),
+           "tp_rope_create")
+    return h.value
+
+
+def tp_rope_destroy(handle: int) -> None:
+    _check(lib().tp_rope_destroy(handle), "tp_rope_destroy")
+
+
+def tp_rope_frequencies(handle, rot_dim: int):
+    """(list of the rot_dim / 2 frequencies, amplitude)."""
+    f = (ctypes.c_double * max(1, rot_dim // 2))()
+    amp = ctypes.c_double()
+    _check(lib().tp_rope_frequencies(handle, f, ctypes.byref(amp)),
+           "tp_rope_frequencies")
+    return list(f)[:rot_dim // 2], amp.value
+
+
+def _ref(s):
+    """The address of a structure, or None."""
+    return None if s is None else ctypes.byref(s)
+
+
+def tp_rope_apply(handle, tokens, dtype, inverse, q_in, q_out, k_in, k_out,
+                  positions, stream=None):
+    _check(lib().tp_rope_apply(
+        handle, tokens, dtype, inverse, _ref(q_in), _ref(q_out), _ref(k_in),
+        _ref(k_out), _ref(positions), _stream(stream)), "tp_rope_apply")
+
+
+def tp_qk_norm_forward(handle, tokens, dtype, norm, q_in, q_out, k_in, k_out,
+                       positions, stream=None):
+    _check(lib().tp_qk_norm_forward(
+        handle, tokens, dtype, _ref(norm), _ref(q_in), _ref(q_out), _ref(k_in),
+        _ref(k_out), _ref(positions), _stream(stream)), "tp_qk_norm_forward")
+
+
+def tp_qk_norm_workspace_bytes(handle) -> int:
+    return int(lib().tp_qk_norm_workspace_bytes(handle))
+
+
+def tp_qk_norm_backward(handle, tokens, dtype, norm, dq, q_in, dq_out, dk,
+                        k_in, dk_out, positions, grads, workspace,
+                        workspace_bytes, stream=None):
+    _check(lib().tp_qk_norm_backward(
+        handle, tokens, dtype, _ref(norm), _ref(dq), _ref(q_in), _ref(dq_out),
+        _ref(dk), _ref(k_in), _ref(dk_out), _ref(positions), _ref(grads),
+        _ptr(workspace), workspace_bytes, _stream(stream)),
+        "tp_qk_norm_backward")
+
+
+# ------------------------------------------------------------- gradients --
+
+def tp_grad_workspace_bytes(count: int) -> int:
+    return int(lib().tp_grad_workspace_bytes(count))
+
+
+def tp_grad_norm(count, tensors, norm, workspace, workspace_bytes,
+                 stream=None):
+    """tensors: a ctypes array of tp_grad_tensor."""
+    _check(lib().tp_grad_norm(count, tensors, _ptr(norm), _ptr(workspace),
+                              workspace_bytes, _stream(stream)),
+           "tp_grad_norm")
+
+
+def tp_grad_clip(count, tensors, max_norm, eps, norm, workspace,
+                 workspace_bytes, stream=None):
+    """tensors: a ctypes array of tp_grad_tensor."""
+    _check(lib().tp_grad_clip(count, tensors, max_norm, eps, _ptr(norm),
+                              _ptr(workspace), workspace_bytes,
+                              _stream(stream)), "tp_grad_clip")

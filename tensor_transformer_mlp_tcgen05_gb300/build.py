@@ -31,7 +31,8 @@ CHECKS_LIB_PATH = os.path.join(PKG, "libtpmlp_checks.so")
 
 SOURCES = ["gemm_tc2.cu", "rowops.cu", "simt.cu",
            "tp_mlp_host.cu", "noalloc.cu", "attn_fwd.cu", "attn_bwd.cu",
-           "attn_host.cu", "fp8.cu", "probe.cu"]
+           "attn_host.cu", "fp8.cu", "probe.cu",
+           "qk_rows.cu", "rope_host.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
           "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]
@@ -49,6 +50,8 @@ def _inputs():
              if f.endswith((".cu", ".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "tp_mlp.h"))
     files.append(os.path.join(INCLUDE, "tp_attn.h"))
+    files.append(os.path.join(INCLUDE, "tp_rope.h"))
+    files.append(os.path.join(INCLUDE, "tp_grad.h"))
     files.append(os.path.abspath(__file__))
     return files
 

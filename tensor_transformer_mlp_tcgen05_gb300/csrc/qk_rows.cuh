@@ -1,0 +1,72 @@
+// Arguments and launchers of the query/key head-row kernels (qk_rows.cu).
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "tp_rope.h"
+
+namespace tpmlp {
+namespace qk {
+
+// Threads of a block; each warp takes one task (a token's heads, or a run of
+// them) at a time.
+constexpr int WARPS = 4;
+constexpr int THREADS = 32 * WARPS;
+constexpr int MAX_PAIRS = TPROPE_MAX_HEAD_DIM / 2;
+// Blocks of the backward kernel (four on each of the 152 SMs; a constant, so
+// that the order of the parameter gradients' sums depends on the shapes only).
+constexpr int BWD_BLOCKS = 608;
+
+// tp_heads for the kernels.  A head's group is (head * magic) >> 32 with
+// magic = floor(2^32 / group) + 1: exact for heads and groups below 2^16.
+struct View {
+  char* p;
+  long long ts, gs, hs;
+  unsigned long long magic;
+  unsigned group;
+};
+
+struct Side {
+  View in;               // forward: x; backward: dy
+  View x;                // backward: x
+  View out;
+  const float* gamma;    // nullable
+  const float* beta;     // nullable
+  int heads;
+  unsigned segs;         // tasks per token
+  int heads_per_task;
+};
+
+struct Args {
+  Side side[2];          // q, k
+  int tokens;            // tokens * segs < 2^31
+  int d;
+  int rot;               // r
+  int units;             // 2V-element units of a head row
+  int rot_units;         // the first of them, which are rotated
+  int rows;              // head rows a warp holds at once
+  unsigned segs;         // side[0].segs + side[1].segs
+  const void* pos;       // nullable
+  int pos64;
+  long long offset;
+  unsigned seq_len;      // 0: tokens are positions
+  float amp, sign;       // sign: -1 turns back
+  float eps, inv_d;
+  float* part;           // backward: [blocks][2][d] sums of dgamma, dbeta
+  int q_blocks;          // backward: blocks that take q's tasks
+  unsigned long long freq[MAX_PAIRS];  // turns per position, 2^-64
+};
+
+// norm: 0 (rotation only), TPQK_RMSNORM or TPQK_LAYERNORM.  vec: elements of
+// one load or store, a power of two up to 16 bytes that divides r / 2, d,
+// every stride and every pointer.
+cudaError_t launch_forward(const Args& a, bool bf16, int vec, int norm,
+                           bool interleaved, cudaStream_t s);
+cudaError_t launch_backward(const Args& a, bool bf16, int vec, int norm,
+                            bool interleaved, int blocks, cudaStream_t s);
+// out[side][0 dgamma, 1 dbeta], each nullable, from `blocks` blocks' sums.
+cudaError_t launch_param_sums(const float* part, int d, int q_blocks,
+                              int blocks, float* const out[4], cudaStream_t s);
+
+}  // namespace qk
+}  // namespace tpmlp
