@@ -13,6 +13,8 @@
  *
  *     Xn     = LayerNorm(X)                optional pre-LN
  *     QKV    = Xn W_qkv + b_qkv            W_qkv [h, 3h], shard-grouped
+ *     [Q, K  = rotary positions of (the per-head norm of) Q, K    optional,
+ *              tp_attn_set_rope, tp_attn_set_qk_norm; see tp_rope.h]
  *     Ctx_j  = softmax(Q_j K_j^T / sqrt(d) [causal mask]) V_j   per head j
  *     Z      = sum_{i=0}^{t-1} Ctx_i W_o,i + b_o     W_o split by rows
  *     [Z    += X]                          optional residual
@@ -49,6 +51,7 @@
 #include <stddef.h>
 
 #include "tp_mlp.h"
+#include "tp_rope.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -115,6 +118,50 @@ int tp_attn_backward(tp_attn_handle* handle, int tokens, const void* dZ,
                      float* dWo, float* dbqkv, float* dbo, float* dgamma,
                      float* dbeta, void* stream);
 
+/* Rotary positions on the heads of Q and K between the projection and the
+ * core, with the frequencies of `config` (its head_dim must be h / H), and the
+ * norm of every head of Q and K before that rotation (or without one).
+ * config = NULL and norm = 0 turn them off (the default).  They count from the
+ * next tp_attn_workspace_bytes / tp_attn_forward call: a training forward with
+ * the norm keeps Q and K both as projected and normalised, so the workspace
+ * grows; a backward call needs its forward's settings.  TPMLP_ERR_ARG /
+ * TPMLP_ERR_SHAPE for a NULL handle or a bad value; the earlier setting then
+ * stays. */
+int tp_attn_set_rope(tp_attn_handle* handle, const tp_rope_config* config);
+int tp_attn_set_qk_norm(tp_attn_handle* handle, int norm, float eps);
+
+/* What those two steps take per call: the tokens' positions (a device pointer
+ * to T int32, or int64 with positions_int64 = 1; NULL: each token's place in
+ * its sequence), only with tp_attn_set_rope; and the norm's parameters as in
+ * tp_rope.h, [d] fp32 each, each may be NULL, only with tp_attn_set_qk_norm. */
+typedef struct tp_attn_qk {
+  const void*  positions;
+  int          positions_int64;
+  const float* q_gamma;
+  const float* q_beta;
+  const float* k_gamma;
+  const float* k_beta;
+} tp_attn_qk;
+
+/* tp_attn_forward / tp_attn_backward with these (qk = NULL: none given, as in
+ * tp_attn_forward).  The backward takes the forward's qk again (beta is not
+ * read) and writes the norm's parameter gradients, each of which may be NULL,
+ * as may qk_grads; dbqkv and dWqkv are those of the projection, before norm and
+ * rotation. */
+int tp_attn_forward_qk(tp_attn_handle* handle, int tokens, const void* X,
+                       const void* Wqkv, const void* Wo, const float* bqkv,
+                       const float* bo, const float* ln_gamma,
+                       const float* ln_beta, void* Z, void* workspace,
+                       size_t workspace_bytes, int training,
+                       const tp_attn_qk* qk, void* stream);
+int tp_attn_backward_qk(tp_attn_handle* handle, int tokens, const void* dZ,
+                        const void* X, const void* Wqkv, const void* Wo,
+                        const float* ln_gamma, void* workspace,
+                        size_t workspace_bytes, void* dX, float* dWqkv,
+                        float* dWo, float* dbqkv, float* dbo, float* dgamma,
+                        float* dbeta, const tp_attn_qk* qk,
+                        const tp_qk_norm_grads* qk_grads, void* stream);
+
 /* Waits for `stream`, then reads and clears the workspace's status word:
  * TPMLP_OK, TPMLP_ERR_TIMEOUT (a bounded device wait gave up; outputs of
  * that call are undefined) or TPMLP_ERR_CUDA. */
@@ -147,7 +194,10 @@ int tp_attn_set_ln_prologue(tp_attn_handle* handle, int enable);
 /* Offsets in bytes, inside a workspace laid out for (tokens, training), of
  * the saved QKV [T,3h] bf16, Ctx [T,h] bf16, log-sum-exp [H,T] fp32 and
  * (training layouts only) dQKV [T,3h] bf16, for inspection by tests; -1 for
- * a NULL handle or an unknown `which`.  The log-sum-exp is kept in base 2 of
+ * a NULL handle or an unknown `which`.  TPATTN_WS_QKR is where the core reads Q
+ * and K: a buffer laid out as QKV (its V columns unused) in a training layout
+ * with tp_attn_set_qk_norm, otherwise QKV itself, in which the norm and the
+ * rotation then take place.  The log-sum-exp is kept in base 2 of
  * the scores scaled by log2(e)/sqrt(d): lse2 = log2 sum_j 2^(s_j log2(e) /
  * sqrt(d)), i.e. the natural-log value times log2(e). */
 long long tp_attn_workspace_offset(const tp_attn_handle* handle, int tokens,
@@ -156,6 +206,7 @@ long long tp_attn_workspace_offset(const tp_attn_handle* handle, int tokens,
 #define TPATTN_WS_CTX 1
 #define TPATTN_WS_LSE 2
 #define TPATTN_WS_DQKV 3
+#define TPATTN_WS_QKR 4
 
 #ifdef __cplusplus
 }

@@ -53,7 +53,8 @@ EXPORTED = (
     "tp_attn_launch_count", "tp_attn_set_timing", "tp_attn_timing_get",
     "tp_attn_timing_reset", "tp_attn_set_wait_budget", "tp_attn_set_nvtx",
     "tp_attn_set_ln_prologue",
-    "tp_attn_workspace_offset",
+    "tp_attn_workspace_offset", "tp_attn_set_rope", "tp_attn_set_qk_norm",
+    "tp_attn_forward_qk", "tp_attn_backward_qk",
 )
 
 # The same for tp_rope.h and tp_grad.h.
@@ -96,6 +97,7 @@ TPATTN_WS_QKV = 0
 TPATTN_WS_CTX = 1
 TPATTN_WS_LSE = 2
 TPATTN_WS_DQKV = 3
+TPATTN_WS_QKR = 4
 
 TPMLP_NOALLOC_SCRATCH_FLOATS = 1 << 20
 
@@ -147,6 +149,13 @@ class tp_qk_norm(ctypes.Structure):
 
 class tp_qk_norm_grads(ctypes.Structure):
     _fields_ = [("q_gamma", ctypes.c_void_p), ("q_beta", ctypes.c_void_p),
+                ("k_gamma", ctypes.c_void_p), ("k_beta", ctypes.c_void_p)]
+
+
+class tp_attn_qk(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p),
+                ("positions_int64", ctypes.c_int),
+                ("q_gamma", ctypes.c_void_p), ("q_beta", ctypes.c_void_p),
                 ("k_gamma", ctypes.c_void_p), ("k_beta", ctypes.c_void_p)]
 
 
@@ -274,6 +283,16 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.tp_attn_set_ln_prologue.restype = _i
     L.tp_attn_set_wait_budget.argtypes = [_vp, ctypes.c_ulonglong]
     L.tp_attn_set_wait_budget.restype = _i
+    L.tp_attn_set_rope.argtypes = [_vp, ctypes.POINTER(tp_rope_config)]
+    L.tp_attn_set_rope.restype = _i
+    L.tp_attn_set_qk_norm.argtypes = [_vp, _i, ctypes.c_float]
+    L.tp_attn_set_qk_norm.restype = _i
+    L.tp_attn_forward_qk.argtypes = (L.tp_attn_forward.argtypes[:-1] +
+                                     [_vp, _vp])
+    L.tp_attn_forward_qk.restype = _i
+    L.tp_attn_backward_qk.argtypes = (L.tp_attn_backward.argtypes[:-1] +
+                                      [_vp, _vp, _vp])
+    L.tp_attn_backward_qk.restype = _i
     # Structures travel as addresses: ctypes.byref of the classes above.
     L.tp_rope_create.argtypes = [ctypes.POINTER(tp_rope_config),
                                  ctypes.POINTER(_vp)]
@@ -559,6 +578,40 @@ def tp_attn_backward(handle, tokens, dZ, X, Wqkv, Wo, ln_gamma, workspace,
         _ptr(ln_gamma), _ptr(workspace), workspace_bytes, _ptr(dX),
         _ptr(dWqkv), _ptr(dWo), _ptr(dbqkv), _ptr(dbo), _ptr(dgamma),
         _ptr(dbeta), _stream(stream)), "tp_attn_backward")
+
+
+def tp_attn_set_rope(handle, config) -> None:
+    """config: a tp_rope_config, or None."""
+    _check(lib().tp_attn_set_rope(
+        handle, None if config is None else ctypes.byref(config)),
+        "tp_attn_set_rope")
+
+
+def tp_attn_set_qk_norm(handle, norm: int, eps: float) -> None:
+    _check(lib().tp_attn_set_qk_norm(handle, norm, eps), "tp_attn_set_qk_norm")
+
+
+def tp_attn_forward_qk(handle, tokens, X, Wqkv, Wo, bqkv, bo, ln_gamma,
+                       ln_beta, Z, workspace, workspace_bytes, training, qk,
+                       stream=None):
+    """qk: a tp_attn_qk, or None."""
+    _check(lib().tp_attn_forward_qk(
+        handle, tokens, _ptr(X), _ptr(Wqkv), _ptr(Wo), _ptr(bqkv), _ptr(bo),
+        _ptr(ln_gamma), _ptr(ln_beta), _ptr(Z), _ptr(workspace),
+        workspace_bytes, training, _ref(qk), _stream(stream)),
+        "tp_attn_forward_qk")
+
+
+def tp_attn_backward_qk(handle, tokens, dZ, X, Wqkv, Wo, ln_gamma, workspace,
+                        workspace_bytes, dX, dWqkv, dWo, dbqkv, dbo, dgamma,
+                        dbeta, qk, qk_grads, stream=None):
+    """qk: a tp_attn_qk, qk_grads: a tp_qk_norm_grads, or None."""
+    _check(lib().tp_attn_backward_qk(
+        handle, tokens, _ptr(dZ), _ptr(X), _ptr(Wqkv), _ptr(Wo),
+        _ptr(ln_gamma), _ptr(workspace), workspace_bytes, _ptr(dX),
+        _ptr(dWqkv), _ptr(dWo), _ptr(dbqkv), _ptr(dbo), _ptr(dgamma),
+        _ptr(dbeta), _ref(qk), _ref(qk_grads), _stream(stream)),
+        "tp_attn_backward_qk")
 
 
 def tp_attn_check(handle, workspace, stream=None) -> int:

@@ -739,34 +739,35 @@ cudaError_t launch_bwd(const CUtensorMap& a1, const CUtensorMap& a2,
 
 }  // namespace
 
-cudaError_t launch_attn_dkdv(const CUtensorMap& tq128, const CUtensorMap& tq64,
-                             const CUtensorMap& tdo64,
+cudaError_t launch_attn_dkdv(const CUtensorMap& tk128, const CUtensorMap& tv128,
+                             const CUtensorMap& tq64, const CUtensorMap& tdo64,
                              const CUtensorMap& tdqkv_out, const AttnArgs& a,
                              int grid, cudaStream_t s) {
   if (a.head_dim == 128)
-    return launch_bwd<128, true>(tq128, tq128, tq64, tdo64, tq128, tdqkv_out, a,
+    return launch_bwd<128, true>(tk128, tv128, tq64, tdo64, tk128, tdqkv_out, a,
                                  grid, s);
   if (a.head_dim == 96)
-    return launch_bwd<96, true>(tq128, tq128, tq64, tdo64, tq128, tdqkv_out, a,
+    return launch_bwd<96, true>(tk128, tv128, tq64, tdo64, tk128, tdqkv_out, a,
                                 grid, s);
   if (a.head_dim == 64)
-    return launch_bwd<64, true>(tq128, tq128, tq64, tdo64, tq128, tdqkv_out, a,
+    return launch_bwd<64, true>(tk128, tv128, tq64, tdo64, tk128, tdqkv_out, a,
                                 grid, s);
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_attn_dq(const CUtensorMap& tq128, const CUtensorMap& tq64,
-                           const CUtensorMap& tdo128, const CUtensorMap& tctx128,
+cudaError_t launch_attn_dq(const CUtensorMap& tq128, const CUtensorMap& tk64,
+                           const CUtensorMap& tv64, const CUtensorMap& tdo128,
+                           const CUtensorMap& tctx128,
                            const CUtensorMap& tdqkv_out, const AttnArgs& a,
                            int grid, cudaStream_t s) {
   if (a.head_dim == 128)
-    return launch_bwd<128, false>(tq128, tdo128, tq64, tq64, tctx128, tdqkv_out,
+    return launch_bwd<128, false>(tq128, tdo128, tk64, tv64, tctx128, tdqkv_out,
                                   a, grid, s);
   if (a.head_dim == 96)
-    return launch_bwd<96, false>(tq128, tdo128, tq64, tq64, tctx128, tdqkv_out,
+    return launch_bwd<96, false>(tq128, tdo128, tk64, tv64, tctx128, tdqkv_out,
                                  a, grid, s);
   if (a.head_dim == 64)
-    return launch_bwd<64, false>(tq128, tdo128, tq64, tq64, tctx128, tdqkv_out,
+    return launch_bwd<64, false>(tq128, tdo128, tk64, tv64, tctx128, tdqkv_out,
                                  a, grid, s);
   return cudaErrorInvalidValue;
 }

@@ -4,7 +4,8 @@
 // Forward (Megatron-LM explainer, "Attention: a design that parallelises
 // naturally"; Megatron-LM notes, "Self-attention block split"):
 //   [LayerNorm] -> QKV = Xn W_qkv + b_qkv (pair GEMM, one column group per
-//   shard) -> attention core per (sequence, head, query block) -> Z =
+//   shard) -> [norm and rotation of Q's and K's heads, tp_rope.h] ->
+//   attention core per (sequence, head, query block) -> Z =
 //   sum_i Ctx_i W_o,i + b_o (pair GEMM, fixed-order shard sum = g) [+ X].
 // Backward: db_o, dW_o = Ctx^T dZ, dCtx = dZ W_o^T -> dQ and delta =
 //   rowsum(dCtx * Ctx) per head (one CTA per query block) -> dK, dV (one CTA
@@ -26,7 +27,7 @@ namespace {
 struct AttnLayout {
   size_t status = 0, xn = 0, mean = 0, rstd = 0, qkv = 0, ctx = 0, lse = 0,
          dctx = 0, delta = 0, dqkv = 0, dxn = 0, part = 0, tailp = 0,
-         total = 0, lnp = 0;
+         total = 0, lnp = 0, qkr = 0, qkpart = 0;
   size_t lnsync_words = 0;   // the LayerNorm prologue's counters
   int chunks = 0;   // 256-row column-sum chunks
   int groups = 0;   // 32-row groups of the core kernels' fused db_qkv partials
@@ -34,7 +35,32 @@ struct AttnLayout {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-AttnLayout attn_layout(const tp_attn_config& c, int tokens, int training) {
+}  // namespace
+
+struct tp_attn_handle {
+  HandleCore core;
+  tp_attn_config cfg;
+  bool ln_prologue = true;   // tp_attn_set_ln_prologue
+  tp_rope_handle* rope = nullptr;   // tp_attn_set_rope
+  tp_rope_handle* plain = nullptr;  // no rotation: the norm alone
+  int qk_norm = 0;                  // tp_attn_set_qk_norm
+  float qk_eps = 0.f;
+
+  ~tp_attn_handle() {
+    tp_rope_destroy(rope);
+    tp_rope_destroy(plain);
+  }
+  // The handle the norm and the rotation run with (null: neither is set).
+  tp_rope_handle* qk() const {
+    return rope != nullptr ? rope : qk_norm != 0 ? plain : nullptr;
+  }
+};
+
+namespace {
+
+AttnLayout attn_layout(const tp_attn_handle* handle, int tokens,
+                       int training) {
+  const tp_attn_config& c = handle->cfg;
   AttnLayout L;
   const size_t T = static_cast<size_t>(tokens);
   const size_t h = static_cast<size_t>(c.hidden);
@@ -76,19 +102,16 @@ AttnLayout attn_layout(const tp_attn_config& c, int tokens, int training) {
     L.part = take((static_cast<size_t>(L.chunks) * h + rows3 * 3 * h +
                    2 * L.lnp * h) * 4);
   }
+  // Q and K as the core reads them: in place, but for a training forward with
+  // the norm, whose gradient needs them as projected too
+  L.qkr = L.qkv;
+  if (training && handle->qk_norm != 0) {
+    L.qkr = take(T * 3 * h * 2);
+    L.qkpart = take(tp_qk_norm_workspace_bytes(handle->qk()));
+  }
   L.total = off;
   return L;
 }
-
-}  // namespace
-
-struct tp_attn_handle {
-  HandleCore core;
-  tp_attn_config cfg;
-  bool ln_prologue = true;   // tp_attn_set_ln_prologue
-};
-
-namespace {
 
 GemmArgs gemm_args(const tp_attn_handle* H, char* ws, const AttnLayout& L) {
   GemmArgs a;
@@ -124,6 +147,138 @@ AttnArgs core_args(const tp_attn_handle* H, char* ws, const AttnLayout& L,
   a.status = reinterpret_cast<int*>(ws + L.status);
   a.budget_ns = H->core.budget_ns;
   return a;
+}
+
+// The heads of Q (which = 0) or K (1) in a buffer laid out as QKV.
+tp_heads qk_heads(const tp_attn_handle* H, void* qkv, int which) {
+  const tp_attn_config& c = H->cfg;
+  const int ht = c.hidden / c.shards;
+  tp_heads v;
+  v.data = static_cast<char*>(qkv) + 2LL * which * ht;
+  v.token_stride = 3LL * c.hidden;
+  v.group_stride = 3LL * ht;
+  v.head_stride = c.hidden / c.heads;
+  v.heads = c.heads;
+  v.group = c.heads / c.shards;
+  return v;
+}
+
+// Everything about qk and qk_grads that can be refused, before any launch.
+int check_qk(const tp_attn_handle* H, const tp_attn_qk* qk,
+             const tp_qk_norm_grads* g) {
+  const void* params[4] = {nullptr, nullptr, nullptr, nullptr};
+  const void* grads[4] = {nullptr, nullptr, nullptr, nullptr};
+  if (qk != nullptr) {
+    if (qk->positions_int64 != 0 && qk->positions_int64 != 1) return TPMLP_ERR_ARG;
+    if (qk->positions != nullptr && H->rope == nullptr) {
+      set_detail_msg("positions without tp_attn_set_rope");
+      return TPMLP_ERR_ARG;
+    }
+    if (reinterpret_cast<uintptr_t>(qk->positions) %
+            (qk->positions_int64 ? 8 : 4) != 0)
+      return TPMLP_ERR_ALIGN;
+    params[0] = qk->q_gamma;
+    params[1] = qk->q_beta;
+    params[2] = qk->k_gamma;
+    params[3] = qk->k_beta;
+  }
+  if (g != nullptr) {
+    grads[0] = g->q_gamma;
+    grads[1] = g->q_beta;
+    grads[2] = g->k_gamma;
+    grads[3] = g->k_beta;
+  }
+  for (int i = 0; i < 4; ++i) {
+    if (params[i] == nullptr && grads[i] == nullptr) continue;
+    if (H->qk_norm == 0) {
+      set_detail_msg("norm parameters without tp_attn_set_qk_norm");
+      return TPMLP_ERR_ARG;
+    }
+    if (H->qk_norm == TPQK_RMSNORM && i % 2 == 1) {
+      set_detail_msg("the RMS norm has no beta");
+      return TPMLP_ERR_ARG;
+    }
+    if (reinterpret_cast<uintptr_t>(params[i]) % 4 != 0 ||
+        reinterpret_cast<uintptr_t>(grads[i]) % 4 != 0)
+      return TPMLP_ERR_ALIGN;
+  }
+  return TPMLP_OK;
+}
+
+tp_positions qk_positions(const tp_attn_handle* H, const tp_attn_qk* qk) {
+  tp_positions p;
+  p.data = qk != nullptr ? qk->positions : nullptr;
+  p.is_int64 = qk != nullptr ? qk->positions_int64 : 0;
+  p.offset = 0;
+  p.seq_len = H->cfg.seq_len;
+  return p;
+}
+
+tp_qk_norm qk_norm_args(const tp_attn_handle* H, const tp_attn_qk* qk,
+                        bool beta) {
+  tp_qk_norm n;
+  std::memset(&n, 0, sizeof(n));
+  n.norm = H->qk_norm;
+  n.eps = H->qk_eps;
+  if (qk != nullptr) {
+    n.q_gamma = qk->q_gamma;
+    n.k_gamma = qk->k_gamma;
+    n.q_beta = beta ? qk->q_beta : nullptr;
+    n.k_beta = beta ? qk->k_beta : nullptr;
+  }
+  return n;
+}
+
+// A call of tp_rope.h as one of the handle's launches.
+template <class F>
+int run_qk(HandleCore* core, const char* name, cudaStream_t s, F&& call) {
+  int rc = TPMLP_OK;
+  TRY(run(core, name, s, [&] {
+    rc = call();
+    return cudaSuccess;
+  }));
+  return rc;
+}
+
+// Norm and rotation of Q and K, from `from` to `to` (both laid out as QKV).
+int qk_forward(tp_attn_handle* H, int tokens, void* from, void* to,
+               const tp_attn_qk* qk, cudaStream_t s) {
+  const tp_heads q = qk_heads(H, from, 0), k = qk_heads(H, from, 1);
+  const tp_heads q2 = qk_heads(H, to, 0), k2 = qk_heads(H, to, 1);
+  const tp_positions pos = qk_positions(H, qk);
+  if (H->qk_norm == 0)
+    return run_qk(&H->core, "rope", s, [&] {
+      return tp_rope_apply(H->rope, tokens, TPMLP_BF16, 0, &q, &q2, &k, &k2,
+                           &pos, s);
+    });
+  const tp_qk_norm n = qk_norm_args(H, qk, true);
+  return run_qk(&H->core, "qk_norm_rope", s, [&] {
+    return tp_qk_norm_forward(H->qk(), tokens, TPMLP_BF16, &n, &q, &q2, &k, &k2,
+                              &pos, s);
+  });
+}
+
+// Their gradient, in place in dqkv.
+int qk_backward(tp_attn_handle* H, int tokens, void* dqkv, void* qkv,
+                const tp_attn_qk* qk, const tp_qk_norm_grads* grads,
+                void* part, cudaStream_t s) {
+  const tp_heads dq = qk_heads(H, dqkv, 0), dk = qk_heads(H, dqkv, 1);
+  const tp_positions pos = qk_positions(H, qk);
+  if (H->qk_norm == 0)
+    return run_qk(&H->core, "rope_bwd", s, [&] {
+      return tp_rope_apply(H->rope, tokens, TPMLP_BF16, 1, &dq, &dq, &dk, &dk,
+                           &pos, s);
+    });
+  const tp_heads q = qk_heads(H, qkv, 0), k = qk_heads(H, qkv, 1);
+  const tp_qk_norm n = qk_norm_args(H, qk, false);
+  if (grads != nullptr && (grads->q_gamma || grads->q_beta || grads->k_gamma ||
+                           grads->k_beta))
+    H->core.launches++;   // the parameter gradients' sums
+  return run_qk(&H->core, "qk_norm_rope_bwd", s, [&] {
+    return tp_qk_norm_backward(H->qk(), tokens, TPMLP_BF16, &n, &dq, &q, &dq,
+                               &dk, &k, &dk, &pos, grads, part,
+                               tp_qk_norm_workspace_bytes(H->qk()), s);
+  });
 }
 
 int check_ptrs(std::initializer_list<const void*> ptrs) {
@@ -171,19 +326,20 @@ int tp_attn_destroy(tp_attn_handle* handle) {
 size_t tp_attn_workspace_bytes(const tp_attn_handle* handle, int tokens,
                                int training) {
   if (handle == nullptr || tokens < 0) return 0;
-  return attn_layout(handle->cfg, tokens, training ? 1 : 0).total;
+  return attn_layout(handle, tokens, training ? 1 : 0).total;
 }
 
 long long tp_attn_workspace_offset(const tp_attn_handle* handle, int tokens,
                                    int training, int which) {
   if (handle == nullptr || tokens < 0) return -1;
-  const AttnLayout L = attn_layout(handle->cfg, tokens, training ? 1 : 0);
+  const AttnLayout L = attn_layout(handle, tokens, training ? 1 : 0);
   switch (which) {
     case TPATTN_WS_QKV: return static_cast<long long>(L.qkv);
     case TPATTN_WS_CTX: return static_cast<long long>(L.ctx);
     case TPATTN_WS_LSE: return static_cast<long long>(L.lse);
     case TPATTN_WS_DQKV:
       return training ? static_cast<long long>(L.dqkv) : -1;
+    case TPATTN_WS_QKR: return static_cast<long long>(L.qkr);
     default: return -1;
   }
 }
@@ -193,6 +349,17 @@ int tp_attn_forward(tp_attn_handle* H, int tokens, const void* X,
                     const float* bo, const float* ln_gamma,
                     const float* ln_beta, void* Z, void* workspace,
                     size_t workspace_bytes, int training, void* stream) {
+  return tp_attn_forward_qk(H, tokens, X, Wqkv, Wo, bqkv, bo, ln_gamma, ln_beta,
+                            Z, workspace, workspace_bytes, training, nullptr,
+                            stream);
+}
+
+int tp_attn_forward_qk(tp_attn_handle* H, int tokens, const void* X,
+                       const void* Wqkv, const void* Wo, const float* bqkv,
+                       const float* bo, const float* ln_gamma,
+                       const float* ln_beta, void* Z, void* workspace,
+                       size_t workspace_bytes, int training,
+                       const tp_attn_qk* qk, void* stream) {
   if (H == nullptr) return TPMLP_ERR_ARG;
   const tp_attn_config& c = H->cfg;
   if (tokens < 0 || tokens > c.max_tokens || tokens % c.seq_len != 0)
@@ -201,7 +368,8 @@ int tp_attn_forward(tp_attn_handle* H, int tokens, const void* X,
     return TPMLP_ERR_ARG;
   if (c.use_layernorm && (!ln_gamma || !ln_beta)) return TPMLP_ERR_ARG;
   TRY(check_ptrs({X, Wqkv, Wo, bqkv, bo, ln_gamma, ln_beta, Z, workspace}));
-  const AttnLayout L = attn_layout(c, tokens, training ? 1 : 0);
+  TRY(check_qk(H, qk, nullptr));
+  const AttnLayout L = attn_layout(H, tokens, training ? 1 : 0);
   if (workspace_bytes < L.total) return TPMLP_ERR_WORKSPACE;
   int sms = 0;
   TRY(check_device(&sms));
@@ -252,10 +420,12 @@ int tp_attn_forward(tp_attn_handle* H, int tokens, const void* X,
   TRY(mnmajor_map(&tb, Wqkv, h, 3 * h));
   TRY(tc_gemm(&H->core, ln_fused ? "gemm_ln_qkv" : "gemm_qkv", s, sms,
               EPI_BIAS_BF16, false, true, ta, tb, gq));
+  if (H->qk() != nullptr)
+    TRY(qk_forward(H, T, ws + L.qkv, ws + L.qkr, qk, s));
   // attention core
   AttnArgs aa = core_args(H, ws, L, T);
   CUtensorMap tqk, tv;
-  TRY(encode_map(&tqk, ws + L.qkv, 3ULL * h, T, 3ULL * h, 128));
+  TRY(encode_map(&tqk, ws + L.qkr, 3ULL * h, T, 3ULL * h, 128));
   TRY(encode_map(&tv, ws + L.qkv, 3ULL * h, T, 3ULL * h, 64));
   // persistent forward: two CTAs per SM walk the items, one group of
   // (sequence, head) pairs per round
@@ -285,6 +455,18 @@ int tp_attn_backward(tp_attn_handle* H, int tokens, const void* dZ,
                      size_t workspace_bytes, void* dX, float* dWqkv,
                      float* dWo, float* dbqkv, float* dbo, float* dgamma,
                      float* dbeta, void* stream) {
+  return tp_attn_backward_qk(H, tokens, dZ, X, Wqkv, Wo, ln_gamma, workspace,
+                             workspace_bytes, dX, dWqkv, dWo, dbqkv, dbo, dgamma,
+                             dbeta, nullptr, nullptr, stream);
+}
+
+int tp_attn_backward_qk(tp_attn_handle* H, int tokens, const void* dZ,
+                        const void* X, const void* Wqkv, const void* Wo,
+                        const float* ln_gamma, void* workspace,
+                        size_t workspace_bytes, void* dX, float* dWqkv,
+                        float* dWo, float* dbqkv, float* dbo, float* dgamma,
+                        float* dbeta, const tp_attn_qk* qk,
+                        const tp_qk_norm_grads* qk_grads, void* stream) {
   if (H == nullptr) return TPMLP_ERR_ARG;
   const tp_attn_config& c = H->cfg;
   if (tokens < 0 || tokens > c.max_tokens || tokens % c.seq_len != 0)
@@ -295,7 +477,8 @@ int tp_attn_backward(tp_attn_handle* H, int tokens, const void* dZ,
   if (c.use_layernorm && !ln_gamma) return TPMLP_ERR_ARG;
   TRY(check_ptrs({dZ, X, Wqkv, Wo, ln_gamma, workspace, dX, dWqkv, dWo, dbqkv,
                   dbo, dgamma, dbeta}));
-  const AttnLayout L = attn_layout(c, tokens, 1);
+  TRY(check_qk(H, qk, qk_grads));
+  const AttnLayout L = attn_layout(H, tokens, 1);
   if (workspace_bytes < L.total) return TPMLP_ERR_WORKSPACE;
   int sms = 0;
   TRY(check_device(&sms));
@@ -305,10 +488,14 @@ int tp_attn_backward(tp_attn_handle* H, int tokens, const void* dZ,
   const bool ln = c.use_layernorm != 0;
 
   if (T == 0) {
+    const tp_qk_norm_grads none = {nullptr, nullptr, nullptr, nullptr};
+    const tp_qk_norm_grads& qg = qk_grads != nullptr ? *qk_grads : none;
+    const size_t d4 = size_t(h / c.heads) * 4;
     struct Zero {
       void* p;
       size_t n;
-    } zs[] = {{dWqkv, size_t(h) * 3 * h * 4}, {dWo, size_t(h) * h * 4},
+    } zs[] = {{qg.q_gamma, d4}, {qg.q_beta, d4}, {qg.k_gamma, d4}, {qg.k_beta, d4},
+              {dWqkv, size_t(h) * 3 * h * 4}, {dWo, size_t(h) * h * 4},
               {dbqkv, size_t(3) * h * 4},      {dbo, size_t(h) * 4},
               {ln ? dgamma : nullptr, size_t(h) * 4},
               {ln ? dbeta : nullptr, size_t(h) * 4}};
@@ -353,9 +540,11 @@ int tp_attn_backward(tp_attn_handle* H, int tokens, const void* dZ,
   aa.dctx = static_cast<const __nv_bfloat16*>(dctx);
   aa.delta = reinterpret_cast<float*>(ws + L.delta);
   aa.dqkv = static_cast<__nv_bfloat16*>(dqkv);
-  CUtensorMap tq128, tq64, tdo128, tdo64, tctx128, tdqkv_out;
-  TRY(encode_map(&tq128, ws + L.qkv, 3ULL * h, T, 3ULL * h, 128));
-  TRY(encode_map(&tq64, ws + L.qkv, 3ULL * h, T, 3ULL * h, 64));
+  CUtensorMap tqk128, tqk64, tv128, tv64, tdo128, tdo64, tctx128, tdqkv_out;
+  TRY(encode_map(&tqk128, ws + L.qkr, 3ULL * h, T, 3ULL * h, 128));
+  TRY(encode_map(&tqk64, ws + L.qkr, 3ULL * h, T, 3ULL * h, 64));
+  TRY(encode_map(&tv128, ws + L.qkv, 3ULL * h, T, 3ULL * h, 128));
+  TRY(encode_map(&tv64, ws + L.qkv, 3ULL * h, T, 3ULL * h, 64));
   TRY(encode_map(&tdo128, dctx, h, T, h, 128));
   TRY(encode_map(&tdo64, dctx, h, T, h, 64));
   TRY(encode_map(&tctx128, ctx, h, T, h, 128));
@@ -364,9 +553,11 @@ int tp_attn_backward(tp_attn_handle* H, int tokens, const void* dZ,
   aa.hs_group = std::max(1, sms / aa.nq);   // one backward CTA per SM
   // db_qkv = sum_T dQKV: both kernels write 32-row partials of what they
   // store (the chunks they stage for their TMA stores, and at d = 96 the
-  // 32-column tails); one fixed-order pass sums them
+  // 32-column tails); one fixed-order pass sums them.  (With a norm or a
+  // rotation the projection's dQ and dK exist only after their gradient: then
+  // a pass over dQKV makes the sums.)
   float* part3 = part + size_t(L.chunks) * h;
-  const bool fused_dbqkv = dbqkv != nullptr;
+  const bool fused_dbqkv = dbqkv != nullptr && H->qk() == nullptr;
   if (fused_dbqkv) {
     aa.colsum = part3;
     aa.ld_colsum = 3LL * h;
@@ -374,11 +565,18 @@ int tp_attn_backward(tp_attn_handle* H, int tokens, const void* dZ,
   // the query kernel also writes delta = rowsum(dCtx * Ctx), which the
   // key/value kernel reads
   TRY(run(&H->core, "attn_bwd_dq", s, [&] {
-    return launch_attn_dq(tq128, tq64, tdo128, tctx128, tdqkv_out, aa, grid, s);
+    return launch_attn_dq(tqk128, tqk64, tv64, tdo128, tctx128, tdqkv_out, aa,
+                          grid, s);
   }));
   TRY(run(&H->core, "attn_bwd_dkdv", s, [&] {
-    return launch_attn_dkdv(tq128, tq64, tdo64, tdqkv_out, aa, grid, s);
+    return launch_attn_dkdv(tqk128, tv128, tqk64, tdo64, tdqkv_out, aa, grid, s);
   }));
+  if (H->qk() != nullptr) {
+    TRY(qk_backward(H, T, dqkv, ws + L.qkv, qk, qk_grads, ws + L.qkpart, s));
+    if (dbqkv != nullptr)
+      TRY(colsum(&H->core, "colsum_dbqkv", s, true, dqkv, part3, dbqkv, T,
+                 3 * h));
+  }
   if (fused_dbqkv) {
     TRY(run(&H->core, "colsum_finalize", s, [&] {
       return launch_colsum_finalize(part3, dbqkv, L.groups, 3 * h, s);
@@ -457,6 +655,38 @@ int tp_attn_set_nvtx(tp_attn_handle* handle, int enable) {
 int tp_attn_set_ln_prologue(tp_attn_handle* handle, int enable) {
   if (handle == nullptr || (enable != 0 && enable != 1)) return TPMLP_ERR_ARG;
   handle->ln_prologue = enable != 0;
+  return TPMLP_OK;
+}
+
+int tp_attn_set_rope(tp_attn_handle* handle, const tp_rope_config* config) {
+  if (handle == nullptr) return TPMLP_ERR_ARG;
+  tp_rope_handle* r = nullptr;
+  if (config != nullptr) {
+    if (config->head_dim != handle->cfg.hidden / handle->cfg.heads) {
+      set_detail_msg("rope: head_dim is not hidden / heads");
+      return TPMLP_ERR_SHAPE;
+    }
+    TRY(tp_rope_create(config, &r));
+  }
+  tp_rope_destroy(handle->rope);
+  handle->rope = r;
+  return TPMLP_OK;
+}
+
+int tp_attn_set_qk_norm(tp_attn_handle* handle, int norm, float eps) {
+  if (handle == nullptr ||
+      (norm != 0 && norm != TPQK_RMSNORM && norm != TPQK_LAYERNORM))
+    return TPMLP_ERR_ARG;
+  if (norm != 0 && (!(eps >= 0.f) || !std::isfinite(eps))) return TPMLP_ERR_ARG;
+  if (norm != 0 && handle->plain == nullptr) {
+    tp_rope_config c;
+    std::memset(&c, 0, sizeof(c));
+    c.head_dim = handle->cfg.hidden / handle->cfg.heads;
+    c.base = 1.0;
+    TRY(tp_rope_create(&c, &handle->plain));
+  }
+  handle->qk_norm = norm;
+  handle->qk_eps = eps;
   return TPMLP_OK;
 }
 

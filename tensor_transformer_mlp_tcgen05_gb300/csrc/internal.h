@@ -171,26 +171,29 @@ struct AttnArgs {
 };
 
 // Forward: tqk maps QKV with 64 x 128 boxes (Q and K tiles), tv with
-// 64 x 64 boxes (V tiles, M/N-major operand).  Persistent: any grid of at
-// least one CTA walks the batches * H * nq items (the host launches two CTAs
-// per SM, at most one per item).
+// 64 x 64 boxes (V tiles, M/N-major operand); they may map two buffers of the
+// same layout (Q and K normalised or rotated, V as projected).  Persistent:
+// any grid of at least one CTA walks the batches * H * nq items (the host
+// launches two CTAs per SM, at most one per item).
 cudaError_t launch_attn_fwd(const CUtensorMap& tqk, const CUtensorMap& tv,
                             const AttnArgs& a, int grid, cudaStream_t stream);
 
 // Backward, key/value gradients (one CTA per 128 keys of a sequence and
-// head) and query gradients (one CTA per 128 queries).  tq128 / tq64 map
-// QKV with 64 x 128 / 64 x 64 boxes, tdo128 / tdo64 map dCtx [T, h] alike,
-// tctx128 maps the forward's Ctx [T, h] with 64 x 128 boxes, tdqkv_out maps
-// dQKV [T, 3h] with 64 x 32 store boxes (both kernels' output).
-// Both write their columns of a.dqkv; grid = batches * H * nq.  The query
-// kernel also writes delta = rowsum(dCtx * Ctx) for every (head, token), which
-// the key/value kernel reads: launch the query kernel first.
-cudaError_t launch_attn_dkdv(const CUtensorMap& tq128, const CUtensorMap& tq64,
-                             const CUtensorMap& tdo64,
+// head) and query gradients (one CTA per 128 queries).  tq / tk / tv 128 / 64
+// map QKV (Q and K, V as in the forward) with 64 x 128 / 64 x 64 boxes,
+// tdo128 / tdo64 map dCtx [T, h] alike, tctx128 maps the forward's Ctx [T, h]
+// with 64 x 128 boxes, tdqkv_out maps dQKV [T, 3h] with 64 x 32 store boxes
+// (both kernels' output).  Both write their columns of a.dqkv; grid = batches
+// * H * nq.  The query kernel also writes delta = rowsum(dCtx * Ctx) for every
+// (head, token), which the key/value kernel reads: launch the query kernel
+// first.
+cudaError_t launch_attn_dkdv(const CUtensorMap& tk128, const CUtensorMap& tv128,
+                             const CUtensorMap& tq64, const CUtensorMap& tdo64,
                              const CUtensorMap& tdqkv_out, const AttnArgs& a,
                              int grid, cudaStream_t stream);
-cudaError_t launch_attn_dq(const CUtensorMap& tq128, const CUtensorMap& tq64,
-                           const CUtensorMap& tdo128, const CUtensorMap& tctx128,
+cudaError_t launch_attn_dq(const CUtensorMap& tq128, const CUtensorMap& tk64,
+                           const CUtensorMap& tv64, const CUtensorMap& tdo128,
+                           const CUtensorMap& tctx128,
                            const CUtensorMap& tdqkv_out, const AttnArgs& a,
                            int grid, cudaStream_t stream);
 

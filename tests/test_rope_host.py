@@ -338,3 +338,87 @@ def test_wrappers_refuse_before_the_library(lib):
         C.clip_grad_norm([torch.zeros(4)], 1.0)
     with pytest.raises(ValueError):
         C.grad_norm({"dX": torch.zeros(4)})
+
+
+# --------------------------------------------------- in the attention block --
+
+def attn_handle(**kw):
+    base = dict(hidden=256, heads=4, shards=2, max_tokens=512, seq_len=256,
+                causal=1, use_layernorm=0, ln_eps=1e-5, use_residual=0)
+    base.update(kw)
+    return B.tp_attn_create(B.tp_attn_config(**base))
+
+
+def test_attention_settings_are_checked_and_replaceable(lib):
+    h = attn_handle()
+    try:
+        ok, other = rope_cfg(), rope_cfg(head_dim=32, rot_dim=32)
+        set_rope = lambda c: lib.tp_attn_set_rope(
+            h, None if c is None else ctypes.byref(c))
+        assert set_rope(other) == B.TPMLP_ERR_SHAPE
+        assert set_rope(rope_cfg(base=-1.0)) == B.TPMLP_ERR_ARG
+        for c in (ok, ok, None, ok):
+            assert set_rope(c) == B.TPMLP_OK
+        assert lib.tp_attn_set_rope(None, None) == B.TPMLP_ERR_ARG
+        assert lib.tp_attn_set_qk_norm(h, 3, 1e-6) == B.TPMLP_ERR_ARG
+        assert lib.tp_attn_set_qk_norm(h, 1, -1.0) == B.TPMLP_ERR_ARG
+        assert lib.tp_attn_set_qk_norm(h, 1, float("nan")) == B.TPMLP_ERR_ARG
+        assert lib.tp_attn_set_qk_norm(None, 1, 1e-6) == B.TPMLP_ERR_ARG
+        for n in (B.TPQK_RMSNORM, B.TPQK_LAYERNORM, 0):
+            assert lib.tp_attn_set_qk_norm(h, n, 1e-6) == B.TPMLP_OK
+    finally:
+        B.tp_attn_destroy(h)
+
+
+def test_attention_workspace_holds_q_and_k_twice_with_the_norm(lib):
+    h = attn_handle()
+    try:
+        T = 512
+        size = lambda training: B.tp_attn_workspace_bytes(h, T, training)
+        off = lambda training, w: B.tp_attn_workspace_offset(h, T, training, w)
+        plain = size(0), size(1)
+        assert off(1, B.TPATTN_WS_QKR) == off(1, B.TPATTN_WS_QKV)
+        B.tp_attn_set_rope(h, rope_cfg())
+        assert (size(0), size(1)) == plain
+        B.tp_attn_set_qk_norm(h, B.TPQK_RMSNORM, 1e-6)
+        assert size(0) == plain[0]
+        assert size(1) >= plain[1] + T * 3 * 256 * 2
+        assert off(0, B.TPATTN_WS_QKR) == off(0, B.TPATTN_WS_QKV)
+        qkr = off(1, B.TPATTN_WS_QKR)
+        assert plain[1] <= qkr and qkr + T * 3 * 256 * 2 <= size(1)
+        for w in range(4):
+            assert off(1, w) < plain[1]
+    finally:
+        B.tp_attn_destroy(h)
+
+
+def test_attention_qk_arguments_are_refused_before_any_launch(lib):
+    h = attn_handle()
+    try:
+        def calls(qk=None, grads=None):
+            ref = lambda s: None if s is None else ctypes.byref(s)
+            n = B.tp_attn_workspace_bytes(h, 256, 1)
+            p = [FAKE * (i + 1) for i in range(8)]
+            return (lib.tp_attn_forward_qk(
+                        h, 256, p[0], p[1], p[2], None, None, None, None, p[3],
+                        p[4], n, 1, ref(qk), None),
+                    lib.tp_attn_backward_qk(
+                        h, 256, p[0], p[1], p[2], p[3], None, p[4], n, p[5],
+                        p[6], p[7], None, None, None, None, ref(qk), ref(grads),
+                        None))
+        Q, G = B.tp_attn_qk, B.tp_qk_norm_grads
+        ARG, ALIGN = B.TPMLP_ERR_ARG, B.TPMLP_ERR_ALIGN
+        assert calls(Q(FAKE, 0)) == (ARG, ARG)            # no rotation set
+        assert calls(Q(None, 0, FAKE)) == (ARG, ARG)      # no norm set
+        assert calls(None, G(FAKE))[1] == ARG
+        B.tp_attn_set_rope(h, rope_cfg())
+        B.tp_attn_set_qk_norm(h, B.TPQK_RMSNORM, 1e-6)
+        assert calls(Q(FAKE, 2)) == (ARG, ARG)
+        assert calls(Q(FAKE + 4, 1)) == (ALIGN, ALIGN)
+        assert calls(Q(None, 0, FAKE + 2)) == (ALIGN, ALIGN)
+        assert calls(Q(None, 0, None, FAKE)) == (ARG, ARG)
+        assert calls(None, G(None, FAKE))[1] == ARG
+        assert calls(None, G(FAKE + 2))[1] == ALIGN
+        assert lib.tp_attn_forward_qk(None, *[0] * 14) == ARG
+    finally:
+        B.tp_attn_destroy(h)
