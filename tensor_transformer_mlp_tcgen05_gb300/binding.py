@@ -322,6 +322,30 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     return L
 
 
+_calls = None
+
+
+def tensor_calls():
+    """The module _pycall (csrc/pycall.cpp), bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        import importlib
+        if not os.path.exists(_build.PYCALL_PATH):
+            raise RuntimeError(
+                f"{_build.PYCALL_PATH} is missing: build it with "
+                "tensor_transformer_mlp_tcgen05_gb300.build.build()")
+        m = importlib.import_module("._pycall", __package__)
+        L = lib()
+        m.bind(_check, *[
+            ctypes.cast(getattr(L, n), ctypes.c_void_p).value
+            for n in ("tp_rope_apply", "tp_qk_norm_forward",
+                      "tp_qk_norm_workspace_bytes", "tp_qk_norm_backward",
+                      "tp_grad_workspace_bytes", "tp_grad_norm",
+                      "tp_grad_clip")])
+        _calls = m
+    return _calls
+
+
 def _ptr(x):
     if x is None:
         return None

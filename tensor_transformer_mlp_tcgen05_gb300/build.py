@@ -5,7 +5,9 @@ Each CUDA translation unit is compiled in parallel, then linked into
 linked statically; the driver API is reached through the runtime's entry-point
 lookup, so the library does not link libcuda).  Object files go to
 ``_build/`` at the repository root.  A rebuild is skipped when the library is
-newer than every source and header.
+newer than every source and header.  Next to it goes ``_pycall.so``, a Python
+module (host C++, built against the installed torch) with the tensor calls of
+``rotary.py`` and ``clip.py``.
 
 ``build(checks=True)`` makes the debug variant ``libtpmlp_checks.so`` (objects
 in ``_build/checks``) with ``-DTPMLP_CHECKS``: device-side checks of TMA
@@ -20,6 +22,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,6 +31,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libtpmlp.so")
 CHECKS_LIB_PATH = os.path.join(PKG, "libtpmlp_checks.so")
+PYCALL_PATH = os.path.join(PKG, "_pycall.so")
 
 SOURCES = ["gemm_tc2.cu", "rowops.cu", "simt.cu",
            "tp_mlp_host.cu", "noalloc.cu", "attn_fwd.cu", "attn_bwd.cu",
@@ -47,7 +51,7 @@ def nvcc_path() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-             if f.endswith((".cu", ".cuh", ".h"))]
+             if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
     files.append(os.path.join(INCLUDE, "tp_mlp.h"))
     files.append(os.path.join(INCLUDE, "tp_attn.h"))
     files.append(os.path.join(INCLUDE, "tp_rope.h"))
@@ -63,12 +67,40 @@ def up_to_date(lib_path: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def build_pycall(force: bool = False) -> str:
+    """Compile _pycall.so with the host compiler; returns its path."""
+    if not force and up_to_date(PYCALL_PATH):
+        return PYCALL_PATH
+    import torch
+    from torch.utils import cpp_extension
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found")
+    nvcc_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())),
+                            "include")
+    inc = [*cpp_extension.include_paths(), nvcc_inc,
+           sysconfig.get_paths()["include"], INCLUDE]
+    tmp = PYCALL_PATH + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           os.path.join(CSRC, "pycall.cpp"), "-o", tmp,
+           *["-I" + i for i in inc],
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for pycall.cpp:\n{r.stderr}")
+    os.replace(tmp, PYCALL_PATH)
+    return PYCALL_PATH
+
+
 def build(force: bool = False, verbose: bool = False,
           ptxas_info: bool = False, checks: bool = False) -> str:
     """Compile and link; returns the library path.  Raises on failure.
     checks=True builds the debug variant (see the module docstring)."""
     lib_path = CHECKS_LIB_PATH if checks else LIB_PATH
     if not force and up_to_date(lib_path):
+        build_pycall()
         return lib_path
     nvcc = nvcc_path()
     obj_dir = os.path.join(BUILD_DIR, "checks") if checks else BUILD_DIR
@@ -86,8 +118,10 @@ def build(force: bool = False, verbose: bool = False,
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        pycall = ex.submit(build_pycall, force)
         results = list(ex.map(compile_one, SOURCES))
+        pycall.result()
     if verbose or ptxas_info:
         for obj, log in results:
             if log.strip():
