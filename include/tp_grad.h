@@ -10,10 +10,10 @@
  * reported as it is and scales nothing: c = 1, so that a training step can
  * read the norm and be skipped with its gradients as they were.
  *
- * Each element's square is summed in fp32 over at most 128 elements of a
- * thread, beyond that in fp64, in a fixed order (bit-identical repeats); runs
- * of elements whose squares would leave fp32's range are squared in fp64, so
- * every finite gradient has its right norm (rounded to fp32 once).  c is
+ * Squares are summed in fp32 over at most 64 elements of a thread (a short set:
+ * then over the 32 threads of a warp), beyond that in fp64, in a fixed order (bit-identical repeats); runs of elements whose
+ * squares would leave fp32's range are squared in fp64, so every finite
+ * gradient has its right norm (rounded to fp32 once).  c is
  * rounded to fp32, c g to the gradient's type.
  */
 #ifndef TP_GRAD_H_

@@ -89,7 +89,7 @@ int tp_rope_frequencies(const tp_rope_handle* handle, double* inv_freq,
 
 /* Heads of a tensor: element c of head j of token t is at data[t *
  * token_stride + (j / group) * group_stride + (j % group) * head_stride + c]
- * (strides in elements, >= 0; d consecutive elements per head).  `group`
+ * (strides in elements, 0 .. 2^32 - 1; d consecutive elements per head).  `group`
  * heads lie head_stride apart and groups group_stride apart: the shard-grouped
  * columns of tp_attn.h's QKV are group = H / t, group_stride = 3 h / t,
  * head_stride = d, token_stride = 3 h; a plain [T, H, d] tensor is group = H.
@@ -121,7 +121,7 @@ typedef struct tp_positions {
  *   tokens  0 <= T <= 2^28 (T = 0 enqueues nothing)
  *   dtype   TPMLP_BF16 or TPMLP_FP32, of q and k
  * TPMLP_ERR_SHAPE: a head count that differs between input and output, a
- * negative stride, a group that does not divide the heads, more than 65535
+ * stride out of range, a group that does not divide the heads, more than 65535
  * heads; TPMLP_ERR_ARG: a null pointer, a bad enum, outputs that overlap;
  * TPMLP_ERR_ALIGN: a pointer off its element's alignment. */
 int tp_rope_apply(tp_rope_handle* handle, int tokens, int dtype, int inverse,

@@ -1,13 +1,19 @@
 // Global L2 norm of many gradient tensors, and clipping (tp_grad.h).
 //
 // Two passes over the data: sums of squares per block, then, each block having
-// added all blocks' sums in the same fixed order, the scaling.  The second pass
-// walks the chunks backwards, so that what the first read last is still in L2
-// (129 MB): a set of gradients smaller than that is read from DRAM once.
-// Both passes are bound by memory.
+// added all blocks' sums in the same fixed order, the scaling.  Both are bound by
+// memory; each thread has eight 16-byte loads in flight.  The second pass walks
+// the chunks backwards, so that what the first read last is still in L2 (129 MB):
+// gradients smaller than that are read from DRAM once.  Its blocks are launched
+// while the first pass drains (programmatic dependent launch) and load their
+// first chunk before they wait for its sums.
+//
+// A few short tensors are done by one launch of one cluster of eight blocks,
+// which exchange their sums through distributed shared memory.
 #include <algorithm>
 
 #include "host_common.cuh"
+#include "ptx.cuh"
 #include "tp_grad.h"
 
 using namespace tpmlp;
@@ -15,140 +21,257 @@ using namespace tpmlp::host;
 
 namespace {
 
+// 16-byte vectors a thread loads at once.
+constexpr int BATCH = 8;
 constexpr int THREADS = 256;
 constexpr int BLOCKS = 608;            // four on each of the 152 SMs
-// Bytes of a tensor that a block takes at a time: 64 (bf16: 128) elements a
-// thread.
-constexpr int CHUNK_BYTES = 65536;
+constexpr int CHUNK_BYTES = 16 * BATCH * THREADS;
 // Tensors of one launch: the table travels as a kernel parameter.
 constexpr int TABLE = 512;
+
+// One cluster: pieces of one warp's batch of SMALL_BATCH vectors a lane.
+constexpr int SMALL_BATCH = 4;
+constexpr int SMALL_THREADS = 512;
+constexpr int SMALL_BLOCKS = 8;
+constexpr int SMALL_WARPS = SMALL_BLOCKS * SMALL_THREADS / 32;
+constexpr int SMALL_PIECE_BYTES = 16 * SMALL_BATCH * 32;
+constexpr int SMALL_TABLE = 64;
 
 struct Entry {
   const void* grad;
   void* out;
   long long numel;
-  unsigned first;      // this tensor's first chunk
+  unsigned first;      // this tensor's first chunk (piece)
   int bf16;
 };
+template <int N>
 struct Table {
-  Entry e[TABLE];
+  Entry e[N];
   int count;
   unsigned chunks;
 };
 
-__device__ __forceinline__ int find_entry(const Table& t, unsigned chunk) {
+template <int N>
+__device__ __forceinline__ const Entry& entry_of(const Table<N>& t,
+                                                 unsigned chunk) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
     if (t.e[mid].first <= chunk) lo = mid;
     else hi = mid - 1;
   }
-  return lo;
+  return t.e[lo];
 }
 
-__device__ __forceinline__ bool aligned16d(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+// A chunk (or piece) of a tensor: n elements of it, of which the first nv 16-byte
+// vectors are read as such (none where a pointer is off 16 bytes).
+struct Part {
+  const char* g;
+  char* o;
+  int n, nv;
+  bool bf16;
+};
+template <int BYTES>
+__device__ __forceinline__ Part part_of(const Entry& e, unsigned chunk) {
+  Part p;
+  p.bf16 = e.bf16 != 0;
+  const int size = p.bf16 ? 2 : 4;
+  const long long at = static_cast<long long>(chunk - e.first) * BYTES;
+  p.g = static_cast<const char*>(e.grad) + at;
+  p.o = static_cast<char*>(e.out) + at;
+  p.n = static_cast<int>(
+      min(static_cast<long long>(BYTES / size), e.numel - at / size));
+  const bool aligned = ((reinterpret_cast<uintptr_t>(p.g) |
+                         reinterpret_cast<uintptr_t>(p.o)) & 15u) == 0;
+  p.nv = aligned ? p.n * size / 16 : 0;
+  return p;
 }
 
-// Squares of N values into acc (fp32), or into big (fp64) when the largest of
-// them is not in [2^-40, 2^55]: a square may then over- or underflow fp32, or
-// is not a number.  Inside that range what underflows is below 2^-46 of the
-// largest square, and the sums of 128 elements stay below 2^127.
+// Vectors first, first + STEP, ... of the part, B of them; zeros past its end.
+template <int B, int STEP>
+__device__ __forceinline__ void load_batch(const Part& p, int first,
+                                           uint4 (&v)[B]) {
+  const uint4* g = reinterpret_cast<const uint4*>(p.g);
+#pragma unroll
+  for (int k = 0; k < B; ++k) {
+    const int i = first + k * STEP;
+    v[k] = i < p.nv ? g[i] : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// Adds the squares of N values: to `sum` in fp32 where that is right, which is
+// where theirs is between 2^-60 and 2^120 (it has not overflowed, and squares that
+// underflowed, below 2^-126, are nothing beside it), else (larger, smaller but
+// not all zero, or not a number) to `wide` in fp64.  fp64 is kept out of the way:
+// an SM does two such additions per cycle.
 template <int N>
-__device__ __forceinline__ void add_squares(const float (&v)[N], float& acc,
-                                            double& big) {
-  float m = 0.f;
-  bool nan = false;
+__device__ __forceinline__ void add_squares(const float (&x)[N], float& sum,
+                                            double& wide) {
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    m = fmaxf(m, fabsf(v[i]));
-    nan = nan || v[i] != v[i];
+  for (int i = 0; i < N; ++i) a[i % 4] = fmaf(x[i], x[i], a[i % 4]);
+  const float s = (a[0] + a[1]) + (a[2] + a[3]);
+  if (s >= 0x1p-60f && s <= 0x1p120f) {
+    sum += s;
+    return;
   }
-  if (!nan && ((m >= 0x1p-40f && m <= 0x1p55f) || m == 0.f)) {
+  bool any = s != 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc = fmaf(v[i], v[i], acc);
+  for (int i = 0; i < N; ++i) any = any || x[i] != 0.f;
+  if (any) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const double v = static_cast<double>(x[i]);
+      wide += v * v;
+    }
+  }
+}
+
+template <int B>
+__device__ __forceinline__ void batch_squares(const uint4 (&v)[B], bool bf16,
+                                              float& sum, double& wide) {
+  if (bf16) {
+#pragma unroll
+    for (int k = 0; k < B; k += 4) {
+      float x[32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        unpack_bf16x2(v[k + j].x, x[8 * j], x[8 * j + 1]);
+        unpack_bf16x2(v[k + j].y, x[8 * j + 2], x[8 * j + 3]);
+        unpack_bf16x2(v[k + j].z, x[8 * j + 4], x[8 * j + 5]);
+        unpack_bf16x2(v[k + j].w, x[8 * j + 6], x[8 * j + 7]);
+      }
+      add_squares<32>(x, sum, wide);
+    }
   } else {
+    float x[4 * B];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      big += static_cast<double>(v[i]) * static_cast<double>(v[i]);
+    for (int k = 0; k < B; ++k) {
+      x[4 * k] = __uint_as_float(v[k].x);
+      x[4 * k + 1] = __uint_as_float(v[k].y);
+      x[4 * k + 2] = __uint_as_float(v[k].z);
+      x[4 * k + 3] = __uint_as_float(v[k].w);
+    }
+    add_squares<4 * B>(x, sum, wide);
   }
 }
 
-__device__ __forceinline__ void unpack16(const uint4& u, float (&v)[8]) {
-  unpack_bf16x2(u.x, v[0], v[1]);
-  unpack_bf16x2(u.y, v[2], v[3]);
-  unpack_bf16x2(u.z, v[4], v[5]);
-  unpack_bf16x2(u.w, v[6], v[7]);
+__device__ __forceinline__ float element_at(const Part& p, int i) {
+  return p.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.g)[i])
+                : reinterpret_cast<const float*>(p.g)[i];
+}
+__device__ __forceinline__ void store_at(const Part& p, int i, float x) {
+  if (p.bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[i] = __float2bfloat16_rn(x);
+  else reinterpret_cast<float*>(p.o)[i] = x;
 }
 
-// Sum over the block, in a fixed order; every thread gets it.
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double w[THREADS / 32];
+// The elements that load_batch leaves out, by `lanes` threads.
+__device__ __forceinline__ void rest_squares(const Part& p, int lane, int lanes,
+                                             float& sum, double& wide) {
+  for (int i = p.nv * (p.bf16 ? 8 : 4) + lane; i < p.n; i += lanes) {
+    const float x[1] = {element_at(p, i)};
+    add_squares<1>(x, sum, wide);
+  }
+}
+__device__ __forceinline__ void rest_scale(const Part& p, int lane, int lanes,
+                                           float c) {
+  for (int i = p.nv * (p.bf16 ? 8 : 4) + lane; i < p.n; i += lanes)
+    store_at(p, i, element_at(p, i) * c);
+}
+
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, float c) {
+  float lo, hi;
+  unpack_bf16x2(w, lo, hi);
+  return pack_bf16x2(lo * c, hi * c);
+}
+
+template <int B, int STEP>
+__device__ __forceinline__ void store_batch(const Part& p, int first,
+                                            const uint4 (&v)[B], float c) {
+  uint4* o = reinterpret_cast<uint4*>(p.o);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = v;
-  __syncthreads();
+  for (int k = 0; k < B; ++k) {
+    const int i = first + k * STEP;
+    if (i >= p.nv) continue;
+    uint4 u;
+    if (p.bf16) {
+      u = make_uint4(scale_bf16x2(v[k].x, c), scale_bf16x2(v[k].y, c),
+                     scale_bf16x2(v[k].z, c), scale_bf16x2(v[k].w, c));
+    } else {
+      u = make_uint4(__float_as_uint(__uint_as_float(v[k].x) * c),
+                     __float_as_uint(__uint_as_float(v[k].y) * c),
+                     __float_as_uint(__uint_as_float(v[k].z) * c),
+                     __float_as_uint(__uint_as_float(v[k].w) * c));
+    }
+    o[i] = u;
+  }
+}
+
+// Sum of n values at `x` (shared or global memory) by one warp, in a fixed
+// order; every lane gets it.
+__device__ __forceinline__ double warp_total(const double* x, int n) {
   double t = 0.0;
+#pragma unroll 8
+  for (int i = threadIdx.x & 31; i < n; i += 32) t += x[i];
 #pragma unroll
-  for (int i = 0; i < THREADS / 32; ++i) t += w[i];
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   return t;
 }
 
-__global__ void __launch_bounds__(THREADS)
-    grad_squares(const __grid_constant__ Table t, double* part) {
-  double total = 0.0;
-  for (unsigned chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
-    const Entry& e = t.e[find_entry(t, chunk)];
-    const long long per = e.bf16 ? CHUNK_BYTES / 2 : CHUNK_BYTES / 4;
-    const long long base = static_cast<long long>(chunk - e.first) * per;
-    const int n = static_cast<int>(min(per, e.numel - base));
-    float acc = 0.f;
-    int done = 0;
-    if (e.bf16) {
-      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(e.grad) + base;
-      if (aligned16d(g)) {
-        const uint4* gv = reinterpret_cast<const uint4*>(g);
-        const int nv = n / 8;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < nv; i += THREADS) {
-          float v[8];
-          unpack16(gv[i], v);
-          add_squares<8>(v, acc, total);
-        }
-        done = nv * 8;
-      }
-      for (int i = done + threadIdx.x; i < n; i += THREADS) {
-        const float v[1] = {__bfloat162float(g[i])};
-        add_squares<1>(v, acc, total);
-      }
-    } else {
-      const float* g = static_cast<const float*>(e.grad) + base;
-      if (aligned16d(g)) {
-        const float4* gv = reinterpret_cast<const float4*>(g);
-        const int nv = n / 4;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < nv; i += THREADS) {
-          const float4 u = gv[i];
-          const float v[4] = {u.x, u.y, u.z, u.w};
-          add_squares<4>(v, acc, total);
-        }
-        done = nv * 4;
-      }
-      for (int i = done + threadIdx.x; i < n; i += THREADS) {
-        const float v[1] = {g[i]};
-        add_squares<1>(v, acc, total);
-      }
-    }
-    total += static_cast<double>(acc);
-  }
-  total = block_sum(total);
-  if (threadIdx.x == 0) part[blockIdx.x] = total;
+// Sum over the block, on the first warp's lanes.
+__device__ __forceinline__ double block_total(double v) {
+  __shared__ double all[THREADS];
+  all[threadIdx.x] = v;
+  __syncthreads();
+  return threadIdx.x < 32 ? warp_total(all, THREADS) : 0.0;
 }
 
+// min(1, max_norm / (norm + eps)); 1 for a norm that is not finite.
+__device__ __forceinline__ float factor(double n, double max_norm, double eps) {
+  const double ratio = max_norm / (n + eps);
+  return isfinite(n) && ratio < 1.0 ? static_cast<float>(ratio) : 1.f;
+}
+
+__global__ void __launch_bounds__(THREADS, 4)
+    grad_squares(const __grid_constant__ Table<TABLE> t, double* part) {
+  // the second pass may take the SMs' free places from here on
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  double wide = 0.0;
+  for (unsigned k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+    const Part p = part_of<CHUNK_BYTES>(entry_of(t, k), k);
+    uint4 v[BATCH];
+    load_batch<BATCH, THREADS>(p, threadIdx.x, v);
+    float sum = 0.f;
+    batch_squares<BATCH>(v, p.bf16, sum, wide);
+    rest_squares(p, threadIdx.x, THREADS, sum, wide);
+    wide += static_cast<double>(sum);
+  }
+  wide = block_total(wide);
+  if (threadIdx.x == 0) part[blockIdx.x] = wide;
+}
+
+// Waits until the sums are there, and adds them: the same total in every block.
+// (Every thread loads its own few first: one warp alone, load after load, took
+// 6 us for 608 of them.)
 __device__ __forceinline__ double total_norm(const double* part, int slots) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < slots; i += THREADS) s += part[i];
-  return sqrt(block_sum(s));
+  __shared__ double norm;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int EACH = (BLOCKS + THREADS - 1) / THREADS;
+  double t = 0.0;
+  for (int i = 0; i < slots; i += EACH * THREADS) {
+    double x[EACH];
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      const int at = i + k * THREADS + threadIdx.x;
+      x[k] = at < slots ? part[at] : 0.0;
+    }
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) t += x[k];
+  }
+  t = block_total(t);
+  if (threadIdx.x == 0) norm = sqrt(t);
+  __syncthreads();
+  return norm;
 }
 
 __global__ void __launch_bounds__(THREADS)
@@ -157,58 +280,107 @@ __global__ void __launch_bounds__(THREADS)
   if (threadIdx.x == 0) *norm = static_cast<float>(n);
 }
 
-__global__ void __launch_bounds__(THREADS)
-    grad_scale(const __grid_constant__ Table t, const double* part, int slots,
-               double max_norm, double eps, float* norm) {
+__global__ void __launch_bounds__(THREADS, 4)
+    grad_scale(const __grid_constant__ Table<TABLE> t, const double* part,
+               int slots, double max_norm, double eps, float* norm) {
+  unsigned k = blockIdx.x;
+  uint4 v[BATCH];
+  Part p;
+  p.n = p.nv = 0;
+  if (k < t.chunks) {
+    const unsigned chunk = t.chunks - 1 - k;
+    p = part_of<CHUNK_BYTES>(entry_of(t, chunk), chunk);
+    load_batch<BATCH, THREADS>(p, threadIdx.x, v);
+  }
   const double n = total_norm(part, slots);
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm != nullptr)
     *norm = static_cast<float>(n);
-  // a norm that is not finite scales nothing
-  const double ratio = max_norm / (n + eps);
-  const float c = isfinite(n) && ratio < 1.0 ? static_cast<float>(ratio) : 1.f;
-  for (unsigned k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+  const float c = factor(n, max_norm, eps);
+  while (k < t.chunks) {
+    if (c != 1.f || p.g != p.o) {
+      store_batch<BATCH, THREADS>(p, threadIdx.x, v, c);
+      rest_scale(p, threadIdx.x, THREADS, c);
+    }
+    k += gridDim.x;
+    if (k >= t.chunks) break;
     const unsigned chunk = t.chunks - 1 - k;
-    const Entry& e = t.e[find_entry(t, chunk)];
-    if (c == 1.f && e.out == e.grad) continue;
-    const long long per = e.bf16 ? CHUNK_BYTES / 2 : CHUNK_BYTES / 4;
-    const long long base = static_cast<long long>(chunk - e.first) * per;
-    const int len = static_cast<int>(min(per, e.numel - base));
-    int done = 0;
-    if (e.bf16) {
-      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(e.grad) + base;
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.out) + base;
-      if (aligned16d(g) && aligned16d(o)) {
-        const uint4* gv = reinterpret_cast<const uint4*>(g);
-        uint4* ov = reinterpret_cast<uint4*>(o);
-        const int nv = len / 8;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < nv; i += THREADS) {
-          float v[8];
-          unpack16(gv[i], v);
-          ov[i] = make_uint4(pack_bf16x2(v[0] * c, v[1] * c),
-                             pack_bf16x2(v[2] * c, v[3] * c),
-                             pack_bf16x2(v[4] * c, v[5] * c),
-                             pack_bf16x2(v[6] * c, v[7] * c));
-        }
-        done = nv * 8;
-      }
-      for (int i = done + threadIdx.x; i < len; i += THREADS)
-        o[i] = __float2bfloat16_rn(__bfloat162float(g[i]) * c);
-    } else {
-      const float* g = static_cast<const float*>(e.grad) + base;
-      float* o = static_cast<float*>(e.out) + base;
-      if (aligned16d(g) && aligned16d(o)) {
-        const float4* gv = reinterpret_cast<const float4*>(g);
-        float4* ov = reinterpret_cast<float4*>(o);
-        const int nv = len / 4;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < nv; i += THREADS) {
-          const float4 v = gv[i];
-          ov[i] = make_float4(v.x * c, v.y * c, v.z * c, v.w * c);
-        }
-        done = nv * 4;
-      }
-      for (int i = done + threadIdx.x; i < len; i += THREADS) o[i] = g[i] * c;
+    p = part_of<CHUNK_BYTES>(entry_of(t, chunk), chunk);
+    if (c != 1.f || p.g != p.o)
+      load_batch<BATCH, THREADS>(p, threadIdx.x, v);
+  }
+}
+
+// Norm and (clip) scaling of at most 2 x SMALL_WARPS pieces: a warp keeps its
+// pieces in registers from the squares to the scaling.
+__global__ void __cluster_dims__(SMALL_BLOCKS, 1, 1)
+    __launch_bounds__(SMALL_THREADS)
+    grad_small(const __grid_constant__ Table<SMALL_TABLE> t, int clip,
+               double max_norm, double eps, float* norm) {
+  __shared__ double warps[SMALL_THREADS / 32];
+  __shared__ double mine;       // this block's sum
+  __shared__ float c_shared;
+  const int lane = threadIdx.x & 31;
+  const unsigned warp = blockIdx.x * (SMALL_THREADS / 32) + (threadIdx.x >> 5);
+  uint4 v[2][SMALL_BATCH];
+  Part p[2];
+  float sum = 0.f;
+  double wide = 0.0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const unsigned piece = warp + k * SMALL_WARPS;
+    p[k].g = p[k].o = nullptr;
+    p[k].n = p[k].nv = 0;
+    p[k].bf16 = false;
+    if (piece < t.chunks)
+      p[k] = part_of<SMALL_PIECE_BYTES>(entry_of(t, piece), piece);
+    load_batch<SMALL_BATCH, 32>(p[k], lane, v[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    batch_squares<SMALL_BATCH>(v[k], p[k].bf16, sum, wide);
+    rest_squares(p[k], lane, 32, sum, wide);
+  }
+  // sum is below 2^120 times the additions of a lane (2 batches, 64 single
+  // elements): a warp's total stays finite
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (__any_sync(0xffffffffu, wide != 0.0)) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      wide += __shfl_xor_sync(0xffffffffu, wide, o);
+  }
+  if (lane == 0) warps[threadIdx.x >> 5] = wide + static_cast<double>(sum);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const double b = warp_total(warps, SMALL_THREADS / 32);
+    if (lane == 0) mine = b;
+  }
+  ptx::cluster_sync();
+  if (threadIdx.x < 32) {
+    double total = 0.0;
+    if (lane < SMALL_BLOCKS) {
+      const uint32_t remote = ptx::mapa_shared(ptx::smem_u32(&mine), lane);
+      asm volatile("ld.shared::cluster.f64 %0, [%1];"
+                   : "=d"(total) : "r"(remote) : "memory");
+    }
+#pragma unroll
+    for (int o = SMALL_BLOCKS / 2; o > 0; o >>= 1)
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) {
+      const double n = sqrt(total);
+      if (blockIdx.x == 0) *norm = static_cast<float>(n);
+      c_shared = factor(n, max_norm, eps);
+    }
+  }
+  // (and no block ends while another still reads its sum)
+  ptx::cluster_sync();
+  const float c = c_shared;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (clip && p[k].n > 0 && (c != 1.f || p[k].g != p[k].o)) {
+      store_batch<SMALL_BATCH, 32>(p[k], lane, v[k], c);
+      rest_scale(p[k], lane, 32, c);
     }
   }
 }
@@ -274,22 +446,30 @@ int check_apart(int count, const tp_grad_tensor* t) {
             : bad(TPMLP_ERR_ARG, "grad: an out overlaps another tensor");
 }
 
-// Tensors [at, at + TABLE) as a kernel's table; empty ones are left out.
-int fill(Table* T, int at, int count, const tp_grad_tensor* t, bool clip) {
+long long parts_of(const tp_grad_tensor& t, int part_bytes) {
+  const long long per = part_bytes / static_cast<int>(item(t.dtype));
+  return (t.numel + per - 1) / per;
+}
+
+// Tensors [at, end) as a kernel's table, in parts of part_bytes; empty ones are
+// left out.
+template <int N>
+int fill(Table<N>* T, int at, int end, int part_bytes, const tp_grad_tensor* t,
+         bool clip) {
   T->count = 0;
   long long chunks = 0;
-  for (int i = at; i < std::min(count, at + TABLE); ++i) {
+  for (int i = at; i < end; ++i) {
     if (t[i].numel == 0) continue;
     Entry& e = T->e[T->count++];
     e.grad = t[i].grad;
-    e.out = clip ? t[i].out : nullptr;
+    // without clipping nothing is written, and `out` only has to be aligned
+    e.out = clip ? t[i].out : const_cast<void*>(t[i].grad);
     e.numel = t[i].numel;
     e.bf16 = t[i].dtype == TPMLP_BF16;
     e.first = static_cast<unsigned>(chunks);
-    const long long per = CHUNK_BYTES / static_cast<int>(item(t[i].dtype));
-    chunks += (t[i].numel + per - 1) / per;
+    chunks += parts_of(t[i], part_bytes);
     if (chunks > 0x7fffffffLL)
-      return bad(TPMLP_ERR_SHAPE, "grad: more than 2^47 bytes");
+      return bad(TPMLP_ERR_SHAPE, "grad: more than 2^46 bytes");
   }
   T->chunks = static_cast<unsigned>(chunks);
   return TPMLP_OK;
@@ -299,6 +479,23 @@ int cuda_rc(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return TPMLP_OK;
   set_detail(what, e);
   return TPMLP_ERR_CUDA;
+}
+
+// A launch that may begin while its predecessor in the stream ends (it waits
+// for it with griddepcontrol.wait).
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), int blocks, cudaStream_t s,
+                             const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 int go(int count, const tp_grad_tensor* t, bool clip, double max_norm,
@@ -314,29 +511,52 @@ int go(int count, const tp_grad_tensor* t, bool clip, double max_norm,
   int sms = 0;
   TRY(check_device(&sms));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // One cluster for up to 512 KB in up to 64 tensors (an empty list too).
+  long long pieces = 0;
+  for (int i = 0; i < count && pieces <= 2 * SMALL_WARPS; ++i)
+    pieces += parts_of(t[i], SMALL_PIECE_BYTES);
+  if (count <= SMALL_TABLE && pieces <= 2 * SMALL_WARPS) {
+    Table<SMALL_TABLE> T;
+    TRY(fill(&T, 0, count, SMALL_PIECE_BYTES, t, clip));
+    grad_small<<<SMALL_BLOCKS, SMALL_THREADS, 0, s>>>(T, clip ? 1 : 0, max_norm,
+                                                      eps, norm);
+    return cuda_rc(cudaGetLastError(), "grad_small");
+  }
   double* part = static_cast<double*>(workspace);
-  Table T;
+  Table<TABLE> T;
   const int launches = tables(count);
+  auto table = [&](int k) {
+    return fill(&T, k * TABLE, std::min(count, (k + 1) * TABLE), CHUNK_BYTES, t,
+                clip);
+  };
+  auto blocks = [&] {
+    return std::max(1, static_cast<int>(std::min<unsigned>(T.chunks, BLOCKS)));
+  };
   int slots = 0;
   for (int k = 0; k < launches; ++k) {
-    TRY(fill(&T, k * TABLE, count, t, clip));
-    const int blocks =
-        std::max(1, static_cast<int>(std::min<unsigned>(T.chunks, BLOCKS)));
-    grad_squares<<<blocks, THREADS, 0, s>>>(T, part + slots);
+    TRY(table(k));
+    grad_squares<<<blocks(), THREADS, 0, s>>>(T, part + slots);
     TRY(cuda_rc(cudaGetLastError(), "grad_squares"));
-    slots += blocks;
+    slots += blocks();
   }
-  if (!clip) {
-    grad_norm_final<<<1, THREADS, 0, s>>>(part, slots, norm);
-    return cuda_rc(cudaGetLastError(), "grad_norm_final");
-  }
+  if (!clip)
+    return cuda_rc(launch_dependent(grad_norm_final, 1, s,
+                                    static_cast<const double*>(part), slots,
+                                    norm),
+                   "grad_norm_final");
   for (int k = launches - 1; k >= 0; --k) {
-    if (launches > 1) TRY(fill(&T, k * TABLE, count, t, clip));
-    const int blocks =
-        std::max(1, static_cast<int>(std::min<unsigned>(T.chunks, BLOCKS)));
-    grad_scale<<<blocks, THREADS, 0, s>>>(T, part, slots, max_norm, eps,
-                                          k == 0 ? norm : nullptr);
-    TRY(cuda_rc(cudaGetLastError(), "grad_scale"));
+    if (launches > 1) TRY(table(k));
+    const double* sums = part;
+    float* out = k == 0 ? norm : nullptr;
+    // behind another grad_scale there is nothing to overlap with
+    if (k == launches - 1) {
+      TRY(cuda_rc(launch_dependent(grad_scale, blocks(), s, T, sums, slots,
+                                   max_norm, eps, out),
+                  "grad_scale"));
+    } else {
+      grad_scale<<<blocks(), THREADS, 0, s>>>(T, sums, slots, max_norm, eps, out);
+      TRY(cuda_rc(cudaGetLastError(), "grad_scale"));
+    }
   }
   return TPMLP_OK;
 }

@@ -8,7 +8,7 @@
 namespace tpmlp {
 namespace qk {
 
-// Threads of a block; each warp takes one task (a token's heads, or a run of
+// Threads of a block; each warp takes one task (a token's heads, or some of
 // them) at a time.
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
@@ -17,13 +17,14 @@ constexpr int MAX_PAIRS = TPROPE_MAX_HEAD_DIM / 2;
 // that the order of the parameter gradients' sums depends on the shapes only).
 constexpr int BWD_BLOCKS = 608;
 
-// tp_heads for the kernels.  A head's group is (head * magic) >> 32 with
-// magic = floor(2^32 / group) + 1: exact for heads and groups below 2^16.
+// tp_heads for the kernels.  A head's group is umulhi(head, magic) with magic =
+// ceil(2^32 / group): exact for heads below 2^16 and groups of 2 .. 2^16 - 1 (a
+// group of one head is given as one group of all heads instead).
 struct View {
   char* p;
-  long long ts, gs, hs;
-  unsigned long long magic;
-  unsigned group;
+  long long ts;          // token stride
+  unsigned gs, hs;       // group and head strides
+  unsigned group, magic;
 };
 
 struct Side {
@@ -33,8 +34,7 @@ struct Side {
   const float* gamma;    // nullable
   const float* beta;     // nullable
   int heads;
-  unsigned segs;         // tasks per token
-  int heads_per_task;
+  int steps;             // ceil(heads / Args::rows)
 };
 
 struct Args {
@@ -45,13 +45,17 @@ struct Args {
   int units;             // 2V-element units of a head row
   int rot_units;         // the first of them, which are rotated
   int rows;              // head rows a warp holds at once
-  unsigned segs;         // side[0].segs + side[1].segs
+  // forward: a task takes `per` steps of a token's q and k steps (in this
+  // order); backward: `per_side` steps of one side's
+  int per, segs;
+  int per_side[2], segs_side[2];
   const void* pos;       // nullable
   int pos64;
   long long offset;
   unsigned seq_len;      // 0: tokens are positions
   float amp, sign;       // sign: -1 turns back
   float eps, inv_d;
+  int param16;           // gamma and beta are 16-byte aligned
   float* part;           // backward: [blocks][2][d] sums of dgamma, dbeta
   int q_blocks;          // backward: blocks that take q's tasks
   unsigned long long freq[MAX_PAIRS];  // turns per position, 2^-64

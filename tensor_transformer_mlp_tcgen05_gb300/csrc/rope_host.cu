@@ -144,9 +144,8 @@ int check_view(const tp_heads& v, int tokens, int d, int size) {
                                 "65535 heads");
   if (v.token_stride < 0 || v.group_stride < 0 || v.head_stride < 0)
     return bad(TPMLP_ERR_SHAPE, "heads: negative stride");
-  // every byte offset stays below 2^62
-  if (v.token_stride > (1LL << 28) || v.group_stride > (1LL << 40) ||
-      v.head_stride > (1LL << 40))
+  if (v.token_stride > (1LL << 32) - 1 || v.group_stride > (1LL << 32) - 1 ||
+      v.head_stride > (1LL << 32) - 1)
     return bad(TPMLP_ERR_SHAPE, "heads: stride too large");
   if (v.data == nullptr && tokens > 0)
     return bad(TPMLP_ERR_ARG, "heads: null data");
@@ -211,21 +210,23 @@ int fit_vec(int vec, const tp_heads& v, int tokens, int size) {
 }
 
 qk::View kernel_view(const tp_heads& v) {
+  const bool single = v.group == 1;   // heads lie group_stride apart
   qk::View k;
   k.p = static_cast<char*>(v.data);
   k.ts = v.token_stride;
-  k.gs = v.group_stride;
-  k.hs = v.head_stride;
-  k.group = static_cast<unsigned>(v.group);
-  k.magic = (1ull << 32) / k.group + 1;
+  k.gs = static_cast<unsigned>(v.group_stride);
+  k.hs = static_cast<unsigned>(single ? v.group_stride : v.head_stride);
+  k.group = static_cast<unsigned>(single ? v.heads : v.group);
+  k.magic = k.group == 1 ? 0u   // a single head: group 0
+                         : static_cast<unsigned>(((1ull << 32) + k.group - 1) /
+                                                 k.group);
   return k;
 }
 
 // The kernel's arguments, without norm and parameter pointers.  turn_tail:
 // the elements past r are read and written too.  Returns the vector width.
 int plan(const tp_rope_handle& H, const Call& c, int tokens, int size,
-         int inverse, bool turn_tail, const tp_positions* pos,
-         long long want_tasks, qk::Args* a) {
+         int inverse, bool turn_tail, const tp_positions* pos, qk::Args* a) {
   std::memset(a, 0, sizeof(*a));
   int vec = 16 / size;
   while (vec > 1 && ((H.r / 2) % vec != 0 || H.d % vec != 0)) vec /= 2;
@@ -241,12 +242,6 @@ int plan(const tp_rope_handle& H, const Call& c, int tokens, int size,
   a->rot_units = H.r / (2 * vec);
   a->units = turn_tail ? (H.d + 2 * vec - 1) / (2 * vec) : a->rot_units;
   a->rows = 32 / std::min(a->units, 32);
-  // Tasks: whole tokens while there are enough of them, else the heads of a
-  // token spread over several warps.
-  const long long want = (want_tasks + tokens - 1) / tokens;
-  int steps[2] = {0, 0};
-  for (int s = 0; s < 2; ++s)
-    if (present(c.out[s])) steps[s] = (c.out[s]->heads + a->rows - 1) / a->rows;
   for (int s = 0; s < 2; ++s) {
     qk::Side& sd = a->side[s];
     if (!present(c.out[s])) continue;
@@ -254,12 +249,7 @@ int plan(const tp_rope_handle& H, const Call& c, int tokens, int size,
     if (c.inputs > 1) sd.x = kernel_view(*c.in[s][1]);
     sd.out = kernel_view(*c.out[s]);
     sd.heads = c.out[s]->heads;
-    long long segs = want * steps[s] / (steps[0] + steps[1]);
-    segs = std::max(1LL, std::min<long long>(segs, steps[s]));
-    const int per = static_cast<int>((steps[s] + segs - 1) / segs);
-    sd.heads_per_task = per * a->rows;
-    sd.segs = static_cast<unsigned>((steps[s] + per - 1) / per);
-    a->segs += sd.segs;
+    sd.steps = (sd.heads + a->rows - 1) / a->rows;
   }
   if (pos != nullptr) {
     a->pos = pos->data;
@@ -307,15 +297,34 @@ int check_norm(const tp_qk_norm* n) {
   return TPMLP_OK;
 }
 
+int params_aligned(const tp_qk_norm& n) {
+  return aligned16(n.q_gamma) && aligned16(n.q_beta) && aligned16(n.k_gamma) &&
+         aligned16(n.k_beta);
+}
+
 int cuda_rc(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return TPMLP_OK;
   set_detail(what, e);
   return TPMLP_ERR_CUDA;
 }
 
-// Warps that fill the GPU once over (24 a SM); fewer tokens than that are
-// split by heads.
-constexpr long long FILL_TASKS = 152 * 24;
+// Steps of a task when a token's `steps` are split so that there are at least
+// `want` tasks, as far as there are steps, and at most `most` steps in each.
+int steps_per_task(int steps, int tokens, long long want, int most) {
+  const long long segs = std::min<long long>(
+      steps, std::max<long long>((steps + most - 1) / most,
+                                 (want + tokens - 1) / tokens));
+  return static_cast<int>((steps + segs - 1) / segs);
+}
+
+// Forward: tokens are split until 12 warps a SM have work, and into tasks of at
+// most 16 steps.
+constexpr long long FORWARD_TASKS = 152 * 12;
+constexpr int FORWARD_STEPS = 16;
+// Backward: until the blocks that stay have a step for every warp, and into
+// tasks of at most 8 steps.
+constexpr long long BACKWARD_TASKS = 1LL * qk::BWD_BLOCKS * qk::WARPS;
+constexpr int BACKWARD_STEPS = 8;
 
 int run_forward(tp_rope_handle* H, int tokens, int dtype, int inverse,
                 const tp_qk_norm* norm, const tp_heads* q_in,
@@ -341,13 +350,17 @@ int run_forward(tp_rope_handle* H, int tokens, int dtype, int inverse,
     if (!tail && H->r == 0) return TPMLP_OK;
   }
   qk::Args a;
-  const int vec = plan(*H, c, tokens, size, inverse, tail, pos, FILL_TASKS, &a);
+  const int vec = plan(*H, c, tokens, size, inverse, tail, pos, &a);
+  const int steps = a.side[0].steps + a.side[1].steps;
+  a.per = steps_per_task(steps, tokens, FORWARD_TASKS, FORWARD_STEPS);
+  a.segs = (steps + a.per - 1) / a.per;
   if (norm != nullptr) {
     a.eps = norm->eps;
     a.side[0].gamma = norm->q_gamma;
     a.side[0].beta = norm->q_beta;
     a.side[1].gamma = norm->k_gamma;
     a.side[1].beta = norm->k_beta;
+    a.param16 = params_aligned(*norm);
   }
   return cuda_rc(qk::launch_forward(a, dtype == TPMLP_BF16, vec,
                                     norm ? norm->norm : 0, H->interleaved != 0,
@@ -512,25 +525,30 @@ int tp_qk_norm_backward(tp_rope_handle* H, int tokens, int dtype,
     return TPMLP_OK;
   }
   qk::Args a;
-  const int vec = plan(*H, c, tokens, size, 1, true, positions,
-                       qk::BWD_BLOCKS * qk::WARPS, &a);
+  const int vec = plan(*H, c, tokens, size, 1, true, positions, &a);
   a.eps = norm->eps;
   a.side[0].gamma = norm->q_gamma;
   a.side[1].gamma = norm->k_gamma;
+  a.param16 = params_aligned(*norm);
   a.part = params ? static_cast<float*>(workspace) : nullptr;
-  // blocks in proportion to the heads, no more than there are tasks
-  const long long hq = dq_out->heads, hk = has_k ? dk_out->heads : 0;
-  auto need = [&](int side) -> long long {
-    return (static_cast<long long>(tokens) * a.side[side].segs + qk::WARPS - 1) /
-           qk::WARPS;
-  };
-  long long bq = qk::BWD_BLOCKS;
-  if (has_k)
-    bq = std::min<long long>(qk::BWD_BLOCKS - 1,
-                             std::max(1LL, qk::BWD_BLOCKS * hq / (hq + hk)));
-  long long bk = has_k ? qk::BWD_BLOCKS - bq : 0;
-  bq = std::min(bq, need(0));
-  if (has_k) bk = std::min(bk, need(1));
+  // blocks in proportion to the steps, no more than there are tasks
+  const long long all = a.side[0].steps + a.side[1].steps;
+  long long bq = has_k ? std::min<long long>(
+                             qk::BWD_BLOCKS - 1,
+                             std::max(1LL, qk::BWD_BLOCKS * a.side[0].steps / all))
+                       : qk::BWD_BLOCKS;
+  long long side_blocks[2] = {bq, qk::BWD_BLOCKS - bq};
+  for (int i = 0; i < (has_k ? 2 : 1); ++i) {
+    const int steps = a.side[i].steps;
+    a.per_side[i] =
+        steps_per_task(steps, tokens, BACKWARD_TASKS * steps / all,
+                       BACKWARD_STEPS);
+    a.segs_side[i] = (steps + a.per_side[i] - 1) / a.per_side[i];
+    const long long tasks = static_cast<long long>(tokens) * a.segs_side[i];
+    side_blocks[i] = std::min(side_blocks[i], (tasks + qk::WARPS - 1) / qk::WARPS);
+  }
+  bq = side_blocks[0];
+  const long long bk = side_blocks[1];
   a.q_blocks = static_cast<int>(bq);
   const int blocks = static_cast<int>(bq + bk);
   TRY(cuda_rc(qk::launch_backward(a, dtype == TPMLP_BF16, vec, norm->norm,
