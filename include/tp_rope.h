@@ -89,7 +89,7 @@ int tp_rope_frequencies(const tp_rope_handle* handle, double* inv_freq,
 
 /* Heads of a tensor: element c of head j of token t is at data[t *
  * token_stride + (j / group) * group_stride + (j % group) * head_stride + c]
- * (strides in elements, 0 .. 2^32 - 1; d consecutive elements per head).  `group`
+ * (strides in elements, >= 0 and below 4 GB each; d consecutive elements per head).  `group`
  * heads lie head_stride apart and groups group_stride apart: the shard-grouped
  * columns of tp_attn.h's QKV are group = H / t, group_stride = 3 h / t,
  * head_stride = d, token_stride = 3 h; a plain [T, H, d] tensor is group = H.

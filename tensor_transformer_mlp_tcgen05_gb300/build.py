@@ -36,7 +36,8 @@ PYCALL_PATH = os.path.join(PKG, "_pycall.so")
 SOURCES = ["gemm_tc2.cu", "rowops.cu", "simt.cu",
            "tp_mlp_host.cu", "noalloc.cu", "attn_fwd.cu", "attn_bwd.cu",
            "attn_host.cu", "fp8.cu", "probe.cu",
-           "qk_rows.cu", "rope_host.cu", "grad_clip.cu"]
+           "qk_rows.cu", "qk_rows_bf16.cu", "qk_rows_fp32.cu", "rope_host.cu",
+           "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
           "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

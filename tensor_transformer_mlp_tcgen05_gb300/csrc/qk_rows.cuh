@@ -1,4 +1,5 @@
-// Arguments and launchers of the query/key head-row kernels (qk_rows.cu).
+// Arguments and launchers of the query/key head-row kernels
+// (qk_rows_kernels.cuh).
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -22,8 +23,8 @@ constexpr int BWD_BLOCKS = 608;
 // group of one head is given as one group of all heads instead).
 struct View {
   char* p;
-  long long ts;          // token stride
-  unsigned gs, hs;       // group and head strides
+  long long ts;          // token stride, in bytes
+  unsigned gs, hs;       // group and head strides, in bytes
   unsigned group, magic;
 };
 
@@ -68,6 +69,11 @@ cudaError_t launch_forward(const Args& a, bool bf16, int vec, int norm,
                            bool interleaved, cudaStream_t s);
 cudaError_t launch_backward(const Args& a, bool bf16, int vec, int norm,
                             bool interleaved, int blocks, cudaStream_t s);
+// Either of the two above, by element type.
+cudaError_t launch_bf16(const Args& a, int vec, int norm, bool interleaved,
+                        int blocks, bool backward, cudaStream_t s);
+cudaError_t launch_fp32(const Args& a, int vec, int norm, bool interleaved,
+                        int blocks, bool backward, cudaStream_t s);
 // out[side][0 dgamma, 1 dbeta], each nullable, from `blocks` blocks' sums.
 cudaError_t launch_param_sums(const float* part, int d, int q_blocks,
                               int blocks, float* const out[4], cudaStream_t s);

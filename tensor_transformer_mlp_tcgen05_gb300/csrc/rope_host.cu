@@ -144,9 +144,10 @@ int check_view(const tp_heads& v, int tokens, int d, int size) {
                                 "65535 heads");
   if (v.token_stride < 0 || v.group_stride < 0 || v.head_stride < 0)
     return bad(TPMLP_ERR_SHAPE, "heads: negative stride");
-  if (v.token_stride > (1LL << 32) - 1 || v.group_stride > (1LL << 32) - 1 ||
-      v.head_stride > (1LL << 32) - 1)
-    return bad(TPMLP_ERR_SHAPE, "heads: stride too large");
+  const Steps st = steps_of(v, tokens);
+  for (int i = 0; i < st.n; ++i)
+    if (st.stride[i] > ((1LL << 32) - 1) / size)   // 4 GB
+      return bad(TPMLP_ERR_SHAPE, "heads: stride too large");
   if (v.data == nullptr && tokens > 0)
     return bad(TPMLP_ERR_ARG, "heads: null data");
   if (reinterpret_cast<uintptr_t>(v.data) % size != 0)
@@ -209,13 +210,13 @@ int fit_vec(int vec, const tp_heads& v, int tokens, int size) {
   return vec;
 }
 
-qk::View kernel_view(const tp_heads& v) {
+qk::View kernel_view(const tp_heads& v, int size) {
   const bool single = v.group == 1;   // heads lie group_stride apart
   qk::View k;
   k.p = static_cast<char*>(v.data);
-  k.ts = v.token_stride;
-  k.gs = static_cast<unsigned>(v.group_stride);
-  k.hs = static_cast<unsigned>(single ? v.group_stride : v.head_stride);
+  k.ts = v.token_stride * size;
+  k.gs = static_cast<unsigned>(v.group_stride * size);
+  k.hs = static_cast<unsigned>((single ? v.group_stride : v.head_stride) * size);
   k.group = static_cast<unsigned>(single ? v.heads : v.group);
   k.magic = k.group == 1 ? 0u   // a single head: group 0
                          : static_cast<unsigned>(((1ull << 32) + k.group - 1) /
@@ -245,9 +246,9 @@ int plan(const tp_rope_handle& H, const Call& c, int tokens, int size,
   for (int s = 0; s < 2; ++s) {
     qk::Side& sd = a->side[s];
     if (!present(c.out[s])) continue;
-    sd.in = kernel_view(*c.in[s][0]);
-    if (c.inputs > 1) sd.x = kernel_view(*c.in[s][1]);
-    sd.out = kernel_view(*c.out[s]);
+    sd.in = kernel_view(*c.in[s][0], size);
+    if (c.inputs > 1) sd.x = kernel_view(*c.in[s][1], size);
+    sd.out = kernel_view(*c.out[s], size);
     sd.heads = c.out[s]->heads;
     sd.steps = (sd.heads + a->rows - 1) / a->rows;
   }

@@ -161,7 +161,7 @@ def test_apply_refuses_bad_arguments(lib, handle):
     refused(lib, handle, heads(FAKE, group=3), b, code=SHAPE)
     refused(lib, handle, heads(FAKE, group=0), b, code=SHAPE)
     refused(lib, handle, heads(FAKE, ts=-256), b, code=SHAPE)
-    refused(lib, handle, heads(FAKE, ts=1 << 32), b, code=SHAPE)
+    refused(lib, handle, heads(FAKE, ts=1 << 31), b, code=SHAPE)
     refused(lib, handle, heads(FAKE, H=65536), heads(2 * FAKE, H=65536),
             code=SHAPE)
 
