@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(THREADS)
 // ------------------------------------------------------------- backward --
 // With g = R^T dy, u = g gamma and e = x - mu:
 //   xh = rstd e,  dgamma += (rstd g) e,  dbeta += g,
-//   dx = rstd u - (rstd^3 sum(e u) / d) e [- rstd mean(u)].
+//   dx = (rstd g) gamma - (rstd^3 sum(e u) / d) e [- rstd mean(u)].
 // Persistent blocks, so that a lane sums its unit's parameter gradients over
 // all its rows in registers; a block takes q's tasks or k's.
 constexpr int BWD_STAGES = 4, BWD_AHEAD = 3;
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(THREADS, 4)
     for (int s = s0; s < s1; ++s) {
       ring_wait<BWD_AHEAD - 1>();
       gring.sync();
-      Pairs<V> g[NU], e[NU], u[NU];
+      Pairs<V> g[NU], e[NU];
       {
         RawUnit<T, V> graw[NU], xraw[NU];
         gring.read(s, graw);
@@ -855,42 +855,52 @@ __global__ void __launch_bounds__(THREADS, 4)
           fma<V>(g[n].a, dy.a, c[n], g[n].a);
           mul<V>(g[n].b, dy.b, c[n]);
           fma<V>(g[n].b, dy.a, sa[n], g[n].b);
-          mul<V>(u[n].a, g[n].a, gam[n].a);
-          mul<V>(u[n].b, g[n].b, gam[n].b);
         }
       }
       float mean_u = 0.f;
       if constexpr (NORM == TPQK_LAYERNORM) {
-        float m[2] = {total<V, NU>(e), total<V, NU>(u)};
+        float m[2] = {total<V, NU>(e), dot<V, NU>(g, gam)};
         row_sum<LEN>(m, ln);
 #pragma unroll
         for (int n = 0; n < NU; ++n)
           centre<V, INTER, WHOLE>(e[n], un[n], m[0] * p.inv_d);
         mean_u = m[1] * p.inv_d;
       }
-      float q[2] = {dot<V, NU>(e, e), dot<V, NU>(e, u)};
+      float q[2] = {dot<V, NU>(e, e), 0.f};
+#pragma unroll
+      for (int n = 0; n < NU; ++n) {   // sum of e u
+        float t[V], u[V];
+        mul<V>(u, g[n].a, gam[n].a);
+        mul<V>(t, u, e[n].a);
+        mul<V>(u, g[n].b, gam[n].b);
+        fma<V>(t, u, e[n].b, t);
+        q[1] += sum<V>(t);
+      }
       row_sum<LEN>(q, ln);
       const float rstd = rsqrtf(fmaf(q[0], p.inv_d, p.eps));
       const float k = -(rstd * rstd) * (q[1] * rstd * p.inv_d);
+      const float m = -rstd * mean_u;
+      Pairs<V> dx[NU];
 #pragma unroll
       for (int n = 0; n < NU; ++n) {
-        float t[V];
-        mul<V>(t, g[n].a, rstd);
-        fma<V>(dgam[n].a, t, e[n].a, dgam[n].a);
-        mul<V>(t, g[n].b, rstd);
-        fma<V>(dgam[n].b, t, e[n].b, dgam[n].b);
         if constexpr (NORM == TPQK_LAYERNORM) {
           add<V>(dbet[n].a, g[n].a);
           add<V>(dbet[n].b, g[n].b);
-          add<V>(u[n].a, -mean_u);
-          add<V>(u[n].b, -mean_u);
         }
-        mul<V>(u[n].a, u[n].a, rstd);
-        mul<V>(u[n].b, u[n].b, rstd);
-        fma<V>(u[n].a, e[n].a, k, u[n].a);
-        fma<V>(u[n].b, e[n].b, k, u[n].b);
+        mul<V>(g[n].a, g[n].a, rstd);
+        mul<V>(g[n].b, g[n].b, rstd);
+        fma<V>(dgam[n].a, g[n].a, e[n].a, dgam[n].a);
+        fma<V>(dgam[n].b, g[n].b, e[n].b, dgam[n].b);
+        mul<V>(dx[n].a, e[n].a, k);
+        mul<V>(dx[n].b, e[n].b, k);
+        if constexpr (NORM == TPQK_LAYERNORM) {
+          add<V>(dx[n].a, m);
+          add<V>(dx[n].b, m);
+        }
+        fma<V>(dx[n].a, g[n].a, gam[n].a, dx[n].a);
+        fma<V>(dx[n].b, g[n].b, gam[n].b, dx[n].b);
       }
-      gring.template put<INTER>(s, dst, h, heads, un, u);
+      gring.template put<INTER>(s, dst, h, heads, un, dx);
       gring.sync();
       gring.flush(s, dst, h, heads);
       h += p.rows;
