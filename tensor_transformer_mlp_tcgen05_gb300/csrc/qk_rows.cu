@@ -36,18 +36,18 @@ __global__ void __launch_bounds__(1024)
 
 }  // namespace
 
-cudaError_t launch_forward(const Args& a, bool bf16, int vec, int norm,
+cudaError_t launch_forward(const Args& a, bool bf16, int bits, int norm,
                            bool interleaved, cudaStream_t s) {
   const unsigned tasks = static_cast<unsigned>(a.tokens) * a.segs;
   const int blocks = static_cast<int>((tasks + WARPS - 1) / WARPS);
-  return (bf16 ? launch_bf16 : launch_fp32)(a, vec, norm, interleaved, blocks,
+  return (bf16 ? launch_bf16 : launch_fp32)(a, bits, norm, interleaved, blocks,
                                             false, s);
 }
 
-cudaError_t launch_backward(const Args& a, bool bf16, int vec, int norm,
+cudaError_t launch_backward(const Args& a, bool bf16, int bits, int norm,
                             bool interleaved, int blocks, cudaStream_t s) {
   if (norm == 0) return cudaErrorInvalidValue;
-  return (bf16 ? launch_bf16 : launch_fp32)(a, vec, norm, interleaved, blocks,
+  return (bf16 ? launch_bf16 : launch_fp32)(a, bits, norm, interleaved, blocks,
                                             true, s);
 }
 

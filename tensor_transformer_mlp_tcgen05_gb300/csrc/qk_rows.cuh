@@ -43,9 +43,12 @@ struct Args {
   int tokens;            // tokens * segs < 2^31
   int d;
   int rot;               // r
-  int units;             // 2V-element units of a head row
+  int units;             // units of a head row (at most 32)
   int rot_units;         // the first of them, which are rotated
   int rows;              // head rows a warp holds at once
+  // BITS: bytes of a piece, pieces of a row, ceil(2^32 / row_pieces) (0 for one)
+  int piece, row_pieces;
+  unsigned row_pieces_magic;
   // forward: a task takes `per` steps of a token's q and k steps (in this
   // order); backward: `per_side` steps of one side's
   int per, segs;
@@ -62,17 +65,17 @@ struct Args {
   unsigned long long freq[MAX_PAIRS];  // turns per position, 2^-64
 };
 
-// norm: 0 (rotation only), TPQK_RMSNORM or TPQK_LAYERNORM.  vec: elements of
-// one load or store, a power of two up to 16 bytes that divides r / 2, d,
-// every stride and every pointer.
-cudaError_t launch_forward(const Args& a, bool bf16, int vec, int norm,
+// norm: 0 (rotation only), TPQK_RMSNORM or TPQK_LAYERNORM.  bits: 0 for rows whose
+// units are whole 16-byte vectors, else the elements (4, 2 or 1) that are read at
+// a time (the kinds of rows in qk_rows_kernels.cuh).
+cudaError_t launch_forward(const Args& a, bool bf16, int bits, int norm,
                            bool interleaved, cudaStream_t s);
-cudaError_t launch_backward(const Args& a, bool bf16, int vec, int norm,
+cudaError_t launch_backward(const Args& a, bool bf16, int bits, int norm,
                             bool interleaved, int blocks, cudaStream_t s);
 // Either of the two above, by element type.
-cudaError_t launch_bf16(const Args& a, int vec, int norm, bool interleaved,
+cudaError_t launch_bf16(const Args& a, int bits, int norm, bool interleaved,
                         int blocks, bool backward, cudaStream_t s);
-cudaError_t launch_fp32(const Args& a, int vec, int norm, bool interleaved,
+cudaError_t launch_fp32(const Args& a, int bits, int norm, bool interleaved,
                         int blocks, bool backward, cudaStream_t s);
 // out[side][0 dgamma, 1 dbeta], each nullable, from `blocks` blocks' sums.
 cudaError_t launch_param_sums(const float* part, int d, int q_blocks,

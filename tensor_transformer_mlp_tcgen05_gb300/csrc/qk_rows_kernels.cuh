@@ -2,24 +2,30 @@
 // pass over the heads each: a head row lives in the registers of a few lanes
 // from its load to its store.
 //
-// A row of d elements is cut into units of 2 V elements, one lane each: V
-// pairs (a, b) = (i, i + r/2) or (2i, 2i + 1) that turn together, read as two
-// V-wide vectors, one from each half of the rotated part (so that the lanes of a
-// row read consecutive vectors; interleaved pairs lie in one vector either way);
-// the elements past r follow in units of 2 V that do not turn, again one vector
-// from each half.
-// A warp holds floor(32 / units) rows at once (one step), and a lane keeps its
-// unit from step to step, so that what depends on the token and the unit only
-// (angles, gamma, beta, the parameter gradients' sums) stays in registers.  Each
-// lane copies its own units of the next steps into a ring in shared memory
-// (cp.async), so that enough bytes are in flight with few registers.
+// A row of d elements is cut into units of 2 V elements, one lane each: V pairs
+// (a, b) = (i, i + r/2) or (2i, 2i + 1) that turn together; the elements past r
+// follow in units of 2 V that do not turn.  A warp holds floor(32 / units) rows at
+// once (one step), and a lane keeps its unit from step to step, so that what
+// depends on the token and the unit only (angles, gamma, beta, the parameter
+// gradients' sums) stays in registers.  The rows of the next steps are copied
+// (cp.async) into a ring in shared memory, so that enough bytes are in flight
+// with few registers.  Three kinds of rows:
+//
+//   OWN     a unit is two 16-byte vectors, one from each half of the rotated (or
+//           the other) part, and a row takes 4, 8, 16 or 32 lanes: each lane copies
+//           and stores its own vectors, which a row's lanes read in whole sectors;
+//   PIECES  as OWN with any number of lanes: the rows of a step are copied and
+//           stored as they lie in memory, in 16-byte pieces dealt to all lanes, and
+//           units are read from and written to shared memory;
+//   BITS    any r, d and alignment: copied in pieces of 2 to 16 bytes, read and
+//           written in bits of 4, 2 or 1 elements, a unit's bits lying `units`
+//           apart so that neighbouring lanes touch neighbouring bits.
 //
 // Angles: a frequency is held as turns per position in 64-bit fixed point
 // (2^-64 of a turn), so position times frequency modulo one turn is one
 // integer product; its upper 32 bits, as a signed fraction, go to sincospif.
 // No table of cosines is read, and positions may be anything.  The lanes of a
-// warp make a token's r / 2 angles once, one pair each, and share them through
-// shared memory.
+// warp make a token's r / 2 angles once and share them through shared memory.
 #pragma once
 #include "common.cuh"
 #include "qk_rows.cuh"
@@ -28,199 +34,85 @@ namespace tpmlp {
 namespace qk {
 namespace {
 
-// ------------------------------------------------------------ vectors --
-template <int BYTES> struct Raw;
-template <> struct Raw<16> { using type = uint4; };
-template <> struct Raw<8> { using type = uint2; };
-template <> struct Raw<4> { using type = uint32_t; };
-template <> struct Raw<2> { using type = uint16_t; };
-
-template <class T, int V>
-using RawT = typename Raw<V * static_cast<int>(sizeof(T))>::type;
-
-// The two vectors of a unit as loaded.
-template <class T, int V>
-struct RawUnit {
-  RawT<T, V> v[2];
-};
+// ----------------------------------------------------------- arithmetic --
+// On V values, two at a time (fma.rn.f32x2 and the like: two IEEE fp32
+// operations per instruction, the same results).
+template <int V>
+__device__ __forceinline__ void mul(float (&d)[V], const float (&x)[V],
+                                    const float (&y)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 2)
+    f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), f2_pack(y[j], y[j + 1])), d[j],
+              d[j + 1]);
+}
+template <int V>
+__device__ __forceinline__ void mul(float (&d)[V], const float (&x)[V], float y) {
+  const uint64_t yy = f2_pack(y, y);
+#pragma unroll
+  for (int j = 0; j < V; j += 2)
+    f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), yy), d[j], d[j + 1]);
+}
+// d = x y + z
+template <int V>
+__device__ __forceinline__ void fma(float (&d)[V], const float (&x)[V],
+                                    const float (&y)[V], const float (&z)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 2)
+    f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), f2_pack(y[j], y[j + 1]),
+                     f2_pack(z[j], z[j + 1])),
+              d[j], d[j + 1]);
+}
+template <int V>
+__device__ __forceinline__ void fma(float (&d)[V], const float (&x)[V], float y,
+                                    const float (&z)[V]) {
+  const uint64_t yy = f2_pack(y, y);
+#pragma unroll
+  for (int j = 0; j < V; j += 2)
+    f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), yy, f2_pack(z[j], z[j + 1])), d[j],
+              d[j + 1]);
+}
+template <int V>
+__device__ __forceinline__ void add(float (&d)[V], const float (&x)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 2)
+    f2_unpack(f2_add(f2_pack(d[j], d[j + 1]), f2_pack(x[j], x[j + 1])), d[j],
+              d[j + 1]);
+}
+template <int V>
+__device__ __forceinline__ void add(float (&d)[V], float x) {
+  const uint64_t xx = f2_pack(x, x);
+#pragma unroll
+  for (int j = 0; j < V; j += 2)
+    f2_unpack(f2_add(f2_pack(d[j], d[j + 1]), xx), d[j], d[j + 1]);
+}
+template <int V>
+__device__ __forceinline__ float sum(const float (&x)[V]) {
+  uint64_t t = f2_pack(x[0], x[1]);
+#pragma unroll
+  for (int j = 2; j < V; j += 2) t = f2_add(t, f2_pack(x[j], x[j + 1]));
+  float lo, hi;
+  f2_unpack(t, lo, hi);
+  return lo + hi;
+}
 
 // A unit's V pairs.
 template <int V>
 struct Pairs {
   float a[V], b[V];
 };
-
-// Element i (0 .. 2V - 1, memory order) of a unit: V pairs lie as all a, then
-// all b, or, interleaved, as a b a b ...
-template <int V, bool INTER>
-__device__ __forceinline__ float& element(Pairs<V>& p, int i) {
-  if constexpr (INTER) return i % 2 ? p.b[i / 2] : p.a[i / 2];
-  else return i < V ? p.a[i] : p.b[i - V];
-}
-
-template <class T, int V, bool INTER>
-__device__ __forceinline__ void unpack(const RawUnit<T, V>& raw, Pairs<V>& p) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if constexpr (sizeof(T) == 4) {
-      const float* w = reinterpret_cast<const float*>(&raw.v[h]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) element<V, INTER>(p, h * V + i) = w[i];
-    } else if constexpr (V == 1) {
-      element<V, INTER>(p, h) =
-          __uint_as_float(static_cast<uint32_t>(raw.v[h]) << 16);
-    } else {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw.v[h]);
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        element<V, INTER>(p, h * V + 2 * i) = __uint_as_float(w[i] << 16);
-        element<V, INTER>(p, h * V + 2 * i + 1) =
-            __uint_as_float(w[i] & 0xffff0000u);
-      }
-    }
-  }
-}
-
-template <class T, int V, bool INTER>
-__device__ __forceinline__ RawT<T, V> pack(Pairs<V>& p, int h) {
-  RawT<T, V> raw;
-  if constexpr (sizeof(T) == 4) {
-    float* w = reinterpret_cast<float*>(&raw);
-#pragma unroll
-    for (int i = 0; i < V; ++i) w[i] = element<V, INTER>(p, h * V + i);
-  } else if constexpr (V == 1) {
-    raw = __bfloat16_as_ushort(__float2bfloat16_rn(element<V, INTER>(p, h)));
-  } else {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&raw);
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i)
-      w[i] = pack_bf16x2(element<V, INTER>(p, h * V + 2 * i),
-                         element<V, INTER>(p, h * V + 2 * i + 1));
-  }
-  return raw;
-}
-
-// Arithmetic on V values, two at a time where V is even (fma.rn.f32x2 and the
-// like: two IEEE fp32 operations per instruction, the same results).
 template <int V>
-__device__ __forceinline__ void mul(float (&d)[V], const float (&x)[V],
-                                    const float (&y)[V]) {
-  if constexpr (V % 2 == 0) {
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-      f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), f2_pack(y[j], y[j + 1])), d[j],
-                d[j + 1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] = x[j] * y[j];
-  }
+__device__ __forceinline__ float total(const Pairs<V>& x) {
+  return sum<V>(x.a) + sum<V>(x.b);
 }
 template <int V>
-__device__ __forceinline__ void mul(float (&d)[V], const float (&x)[V], float y) {
-  if constexpr (V % 2 == 0) {
-    const uint64_t yy = f2_pack(y, y);
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-      f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), yy), d[j], d[j + 1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] = x[j] * y;
-  }
-}
-// d = x y + z
-template <int V>
-__device__ __forceinline__ void fma(float (&d)[V], const float (&x)[V],
-                                    const float (&y)[V], const float (&z)[V]) {
-  if constexpr (V % 2 == 0) {
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-      f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), f2_pack(y[j], y[j + 1]),
-                       f2_pack(z[j], z[j + 1])),
-                d[j], d[j + 1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] = fmaf(x[j], y[j], z[j]);
-  }
-}
-template <int V>
-__device__ __forceinline__ void fma(float (&d)[V], const float (&x)[V], float y,
-                                    const float (&z)[V]) {
-  if constexpr (V % 2 == 0) {
-    const uint64_t yy = f2_pack(y, y);
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-      f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), yy, f2_pack(z[j], z[j + 1])),
-                d[j], d[j + 1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] = fmaf(x[j], y, z[j]);
-  }
-}
-template <int V>
-__device__ __forceinline__ void add(float (&d)[V], const float (&x)[V]) {
-  if constexpr (V % 2 == 0) {
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-      f2_unpack(f2_add(f2_pack(d[j], d[j + 1]), f2_pack(x[j], x[j + 1])), d[j],
-                d[j + 1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] += x[j];
-  }
-}
-template <int V>
-__device__ __forceinline__ void add(float (&d)[V], float x) {
-  if constexpr (V % 2 == 0) {
-    const uint64_t xx = f2_pack(x, x);
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-      f2_unpack(f2_add(f2_pack(d[j], d[j + 1]), xx), d[j], d[j + 1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] += x;
-  }
-}
-template <int V>
-__device__ __forceinline__ float sum(const float (&x)[V]) {
-  if constexpr (V >= 4) {
-    uint64_t t = f2_pack(x[0], x[1]);
-#pragma unroll
-    for (int j = 2; j < V; j += 2) t = f2_add(t, f2_pack(x[j], x[j + 1]));
-    float lo, hi;
-    f2_unpack(t, lo, hi);
-    return lo + hi;
-  } else {
-    float s = x[0];
-#pragma unroll
-    for (int j = 1; j < V; ++j) s += x[j];
-    return s;
-  }
-}
-
-// sum over a lane's units of x y, over a and b.
-template <int V, int NU>
-__device__ __forceinline__ float dot(const Pairs<V> (&x)[NU],
-                                     const Pairs<V> (&y)[NU]) {
+__device__ __forceinline__ float dot(const Pairs<V>& x, const Pairs<V>& y) {
   float t[V];
-  mul<V>(t, x[0].a, y[0].a);
-  fma<V>(t, x[0].b, y[0].b, t);
-#pragma unroll
-  for (int n = 1; n < NU; ++n) {
-    fma<V>(t, x[n].a, y[n].a, t);
-    fma<V>(t, x[n].b, y[n].b, t);
-  }
+  mul<V>(t, x.a, y.a);
+  fma<V>(t, x.b, y.b, t);
   return sum<V>(t);
 }
 
-template <int V, int NU>
-__device__ __forceinline__ float total(const Pairs<V> (&x)[NU]) {
-  float t = 0.f;
-#pragma unroll
-  for (int n = 0; n < NU; ++n) t += sum<V>(x[n].a) + sum<V>(x[n].b);
-  return t;
-}
-
-// ------------------------------------------------------ rows and units --
+// ------------------------------------------------------- rows and lanes --
 // The heads of one token of a view, held in registers.
 template <class T>
 struct HeadRows {
@@ -239,92 +131,19 @@ struct HeadRows {
   }
 };
 
-// The two vectors of a unit: element offsets and whether they exist.  WHOLE: a
-// lane has one unit, with both vectors (or is idle).
-struct Unit {
-  int off0, off1;
-  bool ok0, ok1;
-};
-template <int V, bool INTER, bool WHOLE>
-__device__ __forceinline__ Unit unit_at(const Args& p, int u, bool lane_on) {
-  Unit n;
-  n.ok0 = lane_on && (WHOLE || u < p.units);
-  n.ok1 = n.ok0;
-  if (u < p.rot_units) {
-    if constexpr (INTER && V == 1) {   // a pair is two vectors
-      n.off0 = 2 * u;
-      n.off1 = n.off0 + 1;
-    } else {
-      n.off0 = V * u;
-      n.off1 = p.rot / 2 + n.off0;
-    }
-  } else {
-    n.off0 = p.rot + V * (u - p.rot_units);
-    n.off1 = n.off0 + V * (p.units - p.rot_units);
-    if (!WHOLE) n.ok1 = n.ok0 && n.off1 < p.d;
-  }
-  if (!n.ok0) n.off0 = 0;   // (addresses only; nothing is read or written)
-  if (!n.ok1) n.off1 = 0;
-  return n;
-}
-
-// A unit's values of an fp32 vector [d] (null: `missing` everywhere).
-template <int V, bool INTER>
-__device__ __forceinline__ void load_param(const Args& p, const float* g,
-                                           float missing, const Unit& n,
-                                           Pairs<V>& f) {
-  const bool ok0 = g != nullptr && n.ok0, ok1 = g != nullptr && n.ok1;
-  if constexpr (V % 4 == 0) {
-    if (p.param16) {   // the vectors are 16-byte aligned
-#pragma unroll
-      for (int i = 0; i < 2 * V; i += 4) {
-        float4 x = make_float4(missing, missing, missing, missing);
-        if (i < V ? ok0 : ok1)
-          x = __ldg(reinterpret_cast<const float4*>(
-              g + (i < V ? n.off0 + i : n.off1 + i - V)));
-        element<V, INTER>(f, i) = x.x;
-        element<V, INTER>(f, i + 1) = x.y;
-        element<V, INTER>(f, i + 2) = x.z;
-        element<V, INTER>(f, i + 3) = x.w;
-      }
-      return;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    element<V, INTER>(f, i) = ok0 ? __ldg(g + n.off0 + i) : missing;
-    element<V, INTER>(f, V + i) = ok1 ? __ldg(g + n.off1 + i) : missing;
-  }
-}
-
-// x - mu, zero where the row has no element.
-template <int V, bool INTER, bool WHOLE>
-__device__ __forceinline__ void centre(Pairs<V>& x, const Unit& n, float mu) {
-  if constexpr (WHOLE) {
-    add<V>(x.a, -mu);
-    add<V>(x.b, -mu);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2 * V; ++i) {
-      float& e = element<V, INTER>(x, i);
-      e = (i < V ? n.ok0 : n.ok1) ? e - mu : 0.f;
-    }
-  }
-}
-
 // What a lane knows of its place: the row it works on among the warp's rows,
-// and its first unit there (g; then g + 32, ...).  LEN > 0: a row takes exactly
-// LEN lanes, a power of two, and no lane is idle.  LEN < 0: at most 2^-LEN lanes.
+// and its unit there.  LEN > 0: a row takes exactly LEN lanes, a power of two, and
+// no lane is idle.  LEN < 0: at most 2^-LEN lanes.
 struct Lane {
-  int row, g, len, first;
+  int row, unit, len, first;
   bool on;
 };
 template <int LEN>
 __device__ __forceinline__ Lane lane_place(const Args& p, int lane) {
   Lane l;
-  l.len = LEN > 0 ? LEN : min(p.units, 32);
+  l.len = LEN > 0 ? LEN : p.units;
   l.row = lane / l.len;
-  l.g = lane - l.row * l.len;
+  l.unit = lane - l.row * l.len;
   l.first = l.row * l.len;
   l.on = LEN > 0 || l.row < p.rows;
   if (!l.on) l.first = 31;
@@ -333,9 +152,7 @@ __device__ __forceinline__ Lane lane_place(const Args& p, int lane) {
 
 // Sums over the lanes of a row, the same total on every lane, in a fixed order:
 // a butterfly (LEN > 0), or a tree over a row's len consecutive lanes and a
-// broadcast (LEN < 0: -LEN levels).  All 32 lanes call it.  The number of levels is
-// known when compiling: a loop that stopped at len cost four times as much (10
-// us of 44 at 8192 tokens of 32 + 32 heads of 96).
+// broadcast (LEN < 0: -LEN levels).  All 32 lanes call it.
 template <int LEN, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], const Lane& l) {
   if constexpr (LEN > 0) {
@@ -350,7 +167,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], const Lane& l) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float t = __shfl_down_sync(0xffffffffu, v[i], o);
-        v[i] += l.g + o < l.len ? t : 0.f;
+        v[i] += l.unit + o < l.len ? t : 0.f;
       }
     }
 #pragma unroll
@@ -358,177 +175,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], const Lane& l) {
   }
 }
 
-// ---------------------------------------------------------------- ring --
-__device__ __forceinline__ void ring_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// All groups but the last `PENDING` are there.
-template <int PENDING>
-__device__ __forceinline__ void ring_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
-}
-
-// BYTES from global to shared memory (zeros where not ok).
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint8_t* dst, const void* src,
-                                           bool ok) {
-  if constexpr (BYTES == 2) {   // below cp.async's sizes
-    *reinterpret_cast<uint16_t*>(dst) =
-        ok ? *static_cast<const uint16_t*>(src) : uint16_t(0);
-  } else {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    const int n = ok ? BYTES : 0;
-    if constexpr (BYTES == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
-                   "l"(src), "r"(n) : "memory");
-    else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d),
-                   "l"(src), "n"(BYTES), "r"(n) : "memory");
-  }
-}
-
-// A warp's ring of rows to come, STAGES steps in shared memory, and how a lane
-// moves its units between it and global memory.  A stage is copied into again
-// only after what was read from it has been used.
-//
-// LANES: each lane copies and stores its own units, held as [stage][unit]
-// [vector][lane]; its own cp.async.wait_group is all the waiting that is needed.
-// Right where a row's lanes cover whole 32-byte sectors.
-//
-// LINEAR: the rows of a step lie one after the other as in memory, and lane l
-// copies 16-byte pieces l and l + 32 of them, whichever units those hold; results
-// go back the same way.  For rows whose halves are not whole sectors or lines: 96-wide
-// heads, 48 of them rotated, took 43.7 us by LANES and XX by LINEAR (8192 tokens,
-// 32 + 32 heads).
-template <class T, int V, int NU, int STAGES, bool LINEAR>
-struct Ring;
-
-template <class T, int V, int NU, int STAGES>
-struct Ring<T, V, NU, STAGES, false> {
-  static constexpr int BYTES = V * static_cast<int>(sizeof(T));
-  static constexpr int VECTOR = 32 * BYTES;
-  static constexpr int STAGE = NU * 2 * VECTOR;
-  static constexpr int WARP = STAGES * STAGE;
-  uint8_t* mine;   // this lane's place in stage 0
-  int row;
-
-  __device__ __forceinline__ Ring(uint8_t* warp, const Args& p, const Lane& ln,
-                                  const Unit (&)[NU], int lane)
-      : mine(warp + lane * BYTES), row(ln.row) {}
-  // Rows head, head + 1, ... (those below `heads`) into the stage of `step`.
-  __device__ __forceinline__ void copy(int step, const HeadRows<const T>& src,
-                                       int head, int heads,
-                                       const Unit (&un)[NU]) {
-    const bool on = head + row < heads;
-    const T* from = src.at(on ? head + row : 0);
-    uint8_t* st = mine + (step % STAGES) * STAGE;
-#pragma unroll
-    for (int n = 0; n < NU; ++n) {
-      copy_async<BYTES>(st + 2 * n * VECTOR, from + un[n].off0,
-                        on && un[n].ok0);
-      copy_async<BYTES>(st + (2 * n + 1) * VECTOR, from + un[n].off1,
-                        on && un[n].ok1);
-    }
-  }
-  __device__ __forceinline__ void sync() const {}
-  __device__ __forceinline__ void read(int step, RawUnit<T, V> (&raw)[NU]) const {
-    const uint8_t* st = mine + (step % STAGES) * STAGE;
-#pragma unroll
-    for (int n = 0; n < NU; ++n)
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-        raw[n].v[v] = *reinterpret_cast<const RawT<T, V>*>(
-            st + (2 * n + v) * VECTOR);
-  }
-  // The lane's results of a step, and (LINEAR) their way to memory.
-  template <bool INTER>
-  __device__ __forceinline__ void put(int, const HeadRows<T>& dst, int head,
-                                      int heads, const Unit (&un)[NU],
-                                      Pairs<V> (&y)[NU]) const {
-    const bool on = head + row < heads;
-    T* to = dst.at(on ? head + row : 0);
-#pragma unroll
-    for (int n = 0; n < NU; ++n) {
-      if (on && un[n].ok0)
-        *reinterpret_cast<RawT<T, V>*>(to + un[n].off0) =
-            pack<T, V, INTER>(y[n], 0);
-      if (on && un[n].ok1)
-        *reinterpret_cast<RawT<T, V>*>(to + un[n].off1) =
-            pack<T, V, INTER>(y[n], 1);
-    }
-  }
-  __device__ __forceinline__ void flush(int, const HeadRows<T>&, int, int) const {}
-};
-
-template <class T, int V, int STAGES>
-struct Ring<T, V, 1, STAGES, true> {
-  static constexpr int STAGE = 64 * 16;
-  static constexpr int WARP = STAGES * STAGE;
-  uint8_t* warp;
-  int lane;
-  int at0, at1;        // the lane's vectors in a stage
-  int row[2], col[2];  // its pieces: row (past the step's rows: none), byte
-
-  __device__ __forceinline__ Ring(uint8_t* w, const Args& p, const Lane& ln,
-                                  const Unit (&un)[1], int lane_)
-      : warp(w), lane(lane_) {
-    const int bytes = p.d * static_cast<int>(sizeof(T)), pieces = bytes / 16;
-    at0 = ln.row * bytes + un[0].off0 * static_cast<int>(sizeof(T));
-    at1 = ln.row * bytes + un[0].off1 * static_cast<int>(sizeof(T));
-    // an idle lane reads the last piece, which then holds no row's elements
-    if (!ln.on) at0 = at1 = 63 * 16;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int i = lane + 32 * v;
-      row[v] = i / pieces;
-      col[v] = (i - row[v] * pieces) * 16;
-      if (row[v] >= p.rows) row[v] = 1 << 20;
-    }
-  }
-  __device__ __forceinline__ void copy(int step, const HeadRows<const T>& src,
-                                       int head, int heads, const Unit (&)[1]) {
-    uint8_t* st = warp + (step % STAGES) * STAGE;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const bool on = head + row[v] < heads;
-      copy_async<16>(st + (lane + 32 * v) * 16,
-                     reinterpret_cast<const uint8_t*>(
-                         src.at(on ? head + row[v] : 0)) + col[v],
-                     on);
-    }
-  }
-  // Other lanes' copies are read after this (and after each lane's wait), and
-  // copied over only after the next.
-  __device__ __forceinline__ void sync() const { __syncwarp(); }
-  __device__ __forceinline__ void read(int step, RawUnit<T, V> (&raw)[1]) const {
-    const uint8_t* st = warp + (step % STAGES) * STAGE;
-    raw[0].v[0] = *reinterpret_cast<const RawT<T, V>*>(st + at0);
-    raw[0].v[1] = *reinterpret_cast<const RawT<T, V>*>(st + at1);
-  }
-  template <bool INTER>
-  __device__ __forceinline__ void put(int step, const HeadRows<T>&, int, int,
-                                      const Unit (&un)[1],
-                                      Pairs<V> (&y)[1]) const {
-    uint8_t* st = warp + (step % STAGES) * STAGE;
-    if (un[0].ok0) {
-      *reinterpret_cast<RawT<T, V>*>(st + at0) = pack<T, V, INTER>(y[0], 0);
-      *reinterpret_cast<RawT<T, V>*>(st + at1) = pack<T, V, INTER>(y[0], 1);
-    }
-  }
-  __device__ __forceinline__ void flush(int step, const HeadRows<T>& dst,
-                                        int head, int heads) const {
-    const uint8_t* st = warp + (step % STAGES) * STAGE;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      if (head + row[v] >= heads) continue;
-      *reinterpret_cast<uint4*>(
-          reinterpret_cast<uint8_t*>(dst.at(head + row[v])) + col[v]) =
-          *reinterpret_cast<const uint4*>(st + (lane + 32 * v) * 16);
-    }
-  }
-};
-
-// ------------------------------------------------------------- angles --
+// --------------------------------------------------------------- angles --
 __device__ __forceinline__ long long position(const Args& p, int token) {
   if (p.pos != nullptr)
     return p.pos64 ? __ldg(static_cast<const long long*>(p.pos) + token)
@@ -557,44 +204,496 @@ __device__ __forceinline__ void make_angles(const Args& p,
   __syncwarp();
 }
 
-// A unit's V of them (1 and 0 for a unit that does not turn): pairs V u ..., or,
-// interleaved, V / 2 from each half.
-template <int V, bool INTER>
-__device__ __forceinline__ void load_angles(const Args& p, const Trig& t, int u,
-                                            float (&c)[V], float (&s)[V]) {
-  constexpr int RUN = INTER && V > 1 ? V / 2 : V;
-  const bool turns = u < p.rot_units;
-#pragma unroll
-  for (int h = 0; h < V / RUN; ++h) {
-    const int at = RUN * u + h * (p.rot / 4);
-    if constexpr (RUN % 4 == 0) {
-#pragma unroll
-      for (int j = 0; j < RUN; j += 4) {
-        float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (turns) {
-          x = *reinterpret_cast<const float4*>(&t.c[at + j]);
-          y = *reinterpret_cast<const float4*>(&t.s[at + j]);
-        }
-        const int k = h * RUN + j;
-        c[k] = x.x; c[k + 1] = x.y; c[k + 2] = x.z; c[k + 3] = x.w;
-        s[k] = y.x; s[k + 1] = y.y; s[k + 2] = y.z; s[k + 3] = y.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < RUN; ++j) {
-        c[h * RUN + j] = turns ? t.c[at + j] : 1.f;
-        s[h * RUN + j] = turns ? t.s[at + j] : 0.f;
-      }
-    }
-  }
-}
-
 __device__ __forceinline__ void stage_freq(const Args& p,
                                            unsigned long long* freq) {
   for (int i = threadIdx.x; i < p.rot / 2; i += THREADS) freq[i] = p.freq[i];
   __syncthreads();
 }
+
+// ---------------------------------------------------------------- units --
+// OWN and PIECES: two 16-byte vectors, at off0 and off1 of the row.  Pairs lie as
+// all a, then all b, or, interleaved, as a b a b ... in either vector.
+template <class T, bool INTER>
+struct VectorUnit {
+  static constexpr int V = 16 / static_cast<int>(sizeof(T));
+  int off0, off1, unit;
+  bool on, turns;
+
+  __device__ __forceinline__ VectorUnit(const Args& p, const Lane& l)
+      : unit(l.unit), on(l.on), turns(l.unit < p.rot_units) {
+    if (turns) {
+      off0 = V * unit;
+      off1 = p.rot / 2 + off0;
+    } else {
+      off0 = p.rot + V * (unit - p.rot_units);
+      off1 = off0 + V * (p.units - p.rot_units);
+    }
+  }
+  // Value i (0 .. 2V - 1) of a unit in memory order, and its element.
+  __device__ __forceinline__ static float& value(Pairs<V>& x, int i) {
+    if constexpr (INTER) return i % 2 ? x.b[i / 2] : x.a[i / 2];
+    else return i < V ? x.a[i] : x.b[i - V];
+  }
+  __device__ __forceinline__ int element(int i) const {
+    return i < V ? off0 + i : off1 + i - V;
+  }
+  __device__ __forceinline__ bool has(int) const { return on; }
+  __device__ __forceinline__ void centre(Pairs<V>& x, float mu) const {
+    add<V>(x.a, -mu);
+    add<V>(x.b, -mu);
+  }
+  __device__ __forceinline__ void unpack(const uint4 (&raw)[2],
+                                         Pairs<V>& x) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w[4] = {raw[h].x, raw[h].y, raw[h].z, raw[h].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          value(x, h * V + i) = __uint_as_float(w[i]);
+        } else {
+          value(x, h * V + 2 * i) = __uint_as_float(w[i] << 16);
+          value(x, h * V + 2 * i + 1) = __uint_as_float(w[i] & 0xffff0000u);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ uint4 pack(Pairs<V>& x, int h) const {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4)
+        w[i] = __float_as_uint(value(x, h * V + i));
+      else
+        w[i] = pack_bf16x2(value(x, h * V + 2 * i), value(x, h * V + 2 * i + 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // The unit's angles: pairs V unit ..., or, interleaved, V / 2 from each half (1
+  // and 0 for a unit that does not turn).
+  __device__ __forceinline__ void angles(const Args& p, const Trig& t,
+                                         float (&c)[V], float (&s)[V]) const {
+    constexpr int RUN = INTER ? V / 2 : V;
+#pragma unroll
+    for (int h = 0; h < V / RUN; ++h) {
+      const int at = RUN * unit + h * (p.rot / 4);
+      if constexpr (RUN % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < RUN; j += 4) {
+          float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (turns) {
+            x = *reinterpret_cast<const float4*>(&t.c[at + j]);
+            y = *reinterpret_cast<const float4*>(&t.s[at + j]);
+          }
+          const int k = h * RUN + j;
+          c[k] = x.x; c[k + 1] = x.y; c[k + 2] = x.z; c[k + 3] = x.w;
+          s[k] = y.x; s[k + 1] = y.y; s[k + 2] = y.z; s[k + 3] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < RUN; ++j) {
+          c[h * RUN + j] = turns ? t.c[at + j] : 1.f;
+          s[h * RUN + j] = turns ? t.s[at + j] : 0.f;
+        }
+      }
+    }
+  }
+  // The unit's values of an fp32 vector [d] (null: `missing` everywhere).
+  __device__ __forceinline__ void param(const Args& p, const float* g,
+                                        float missing, Pairs<V>& f) const {
+    const bool ok = g != nullptr && on;
+    if (p.param16) {   // the vectors are 16-byte aligned
+#pragma unroll
+      for (int i = 0; i < 2 * V; i += 4) {
+        float4 x = make_float4(missing, missing, missing, missing);
+        if (ok) x = __ldg(reinterpret_cast<const float4*>(g + element(i)));
+        value(f, i) = x.x;
+        value(f, i + 1) = x.y;
+        value(f, i + 2) = x.z;
+        value(f, i + 3) = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i)
+        value(f, i) = ok ? __ldg(g + element(i)) : missing;
+    }
+  }
+};
+
+// BITS: 16 elements as two runs of bits of W consecutive elements, `stride` apart,
+// the first at a0 and b0, of which na and nb exist: a and b, or, interleaved, the
+// first and the second half of the unit's pairs a b a b ...  A bit is read in
+// vectors of A elements.
+template <class T, bool INTER, int A>
+struct BitUnit {
+  static constexpr int V = 8;
+  static constexpr int W = INTER && A == 1 ? 2 : A;
+  static constexpr int RUN = V / W;
+  int a0, b0, stride, na, nb, d;
+  bool on, turns;
+
+  __device__ __forceinline__ BitUnit(const Args& p, const Lane& l)
+      : d(p.d), on(l.on), turns(l.unit < p.rot_units) {
+    const int u = turns ? l.unit : l.unit - p.rot_units;
+    const int n = turns ? p.rot_units : p.units - p.rot_units;   // units
+    stride = W * n;
+    if (turns && !INTER) {
+      const int bits = p.rot / 2 / W;
+      a0 = W * u;
+      b0 = p.rot / 2 + a0;
+      na = nb = (bits - u + n - 1) / n;
+    } else {
+      const int bits = ((turns ? p.rot : p.d - p.rot) + W - 1) / W;
+      const int all = (bits - u + n - 1) / n;
+      a0 = (turns ? 0 : p.rot) + W * u;
+      b0 = a0 + RUN * stride;
+      na = min(all, RUN);
+      nb = max(all - RUN, 0);
+    }
+    if (!on) na = nb = 0;
+  }
+  __device__ __forceinline__ static float& value(Pairs<V>& x, int i) {
+    if constexpr (INTER) return i % 2 ? x.b[i / 2] : x.a[i / 2];
+    else return i < V ? x.a[i] : x.b[i - V];
+  }
+  __device__ __forceinline__ int element(int i) const {
+    return i < V ? a0 + i / W * stride + i % W
+                 : b0 + (i - V) / W * stride + (i - V) % W;
+  }
+  __device__ __forceinline__ bool has(int i) const {
+    const bool bit = i < V ? i / W < na : (i - V) / W < nb;
+    // (a last bit of two may be one element of an odd row)
+    return W > A ? bit && element(i) < d : bit;
+  }
+  __device__ __forceinline__ void centre(Pairs<V>& x, float mu) const {
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i)
+      value(x, i) = has(i) ? value(x, i) - mu : 0.f;
+  }
+  __device__ __forceinline__ void angles(const Args&, const Trig& t,
+                                         float (&c)[V], float (&s)[V]) const {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = INTER ? 2 * j : j;
+      const bool ok = turns && has(i);
+      const int at = INTER ? element(i) / 2 : element(i);
+      c[j] = ok ? t.c[at] : 1.f;
+      s[j] = ok ? t.s[at] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void param(const Args&, const float* g,
+                                        float missing, Pairs<V>& f) const {
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i)
+      value(f, i) = g != nullptr && has(i) ? __ldg(g + element(i)) : missing;
+  }
+  // The unit's values from a row in shared memory (zeros where it has none), and
+  // back.
+  __device__ __forceinline__ void read(const T* row, Pairs<V>& x) const {
+#pragma unroll
+    for (int i = 0; i < 2 * V; i += A) {
+      if constexpr (sizeof(T) == 4 || A == 1) {
+        T v[A];
+        if constexpr (A == 4) {
+          const float4 w = has(i)
+              ? *reinterpret_cast<const float4*>(row + element(i))
+              : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+        } else if constexpr (A == 2) {
+          const float2 w = has(i)
+              ? *reinterpret_cast<const float2*>(row + element(i))
+              : make_float2(0.f, 0.f);
+          v[0] = w.x; v[1] = w.y;
+        } else {
+          v[0] = has(i) ? row[element(i)] : T(0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < A; ++k) value(x, i + k) = static_cast<float>(v[k]);
+      } else {
+        uint32_t w[A / 2];
+        if constexpr (A == 4) {
+          const uint2 v = has(i)
+              ? *reinterpret_cast<const uint2*>(row + element(i))
+              : make_uint2(0u, 0u);
+          w[0] = v.x; w[1] = v.y;
+        } else {
+          w[0] = has(i) ? *reinterpret_cast<const uint32_t*>(row + element(i))
+                        : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < A / 2; ++k) {
+          value(x, i + 2 * k) = __uint_as_float(w[k] << 16);
+          value(x, i + 2 * k + 1) = __uint_as_float(w[k] & 0xffff0000u);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void write(T* row, Pairs<V>& y) const {
+#pragma unroll
+    for (int i = 0; i < 2 * V; i += A) {
+      if (!has(i)) continue;
+      T* to = row + element(i);
+      if constexpr (sizeof(T) == 4 || A == 1) {
+        if constexpr (A == 4)
+          *reinterpret_cast<float4*>(to) =
+              make_float4(value(y, i), value(y, i + 1), value(y, i + 2),
+                          value(y, i + 3));
+        else if constexpr (A == 2)
+          *reinterpret_cast<float2*>(to) =
+              make_float2(value(y, i), value(y, i + 1));
+        else
+          *to = static_cast<T>(value(y, i));
+      } else if constexpr (A == 4) {
+        *reinterpret_cast<uint2*>(to) =
+            make_uint2(pack_bf16x2(value(y, i), value(y, i + 1)),
+                       pack_bf16x2(value(y, i + 2), value(y, i + 3)));
+      } else {
+        *reinterpret_cast<uint32_t*>(to) =
+            pack_bf16x2(value(y, i), value(y, i + 1));
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- rings --
+__device__ __forceinline__ void ring_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All groups but the last `PENDING` are there.
+template <int PENDING>
+__device__ __forceinline__ void ring_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// BYTES from global to shared memory (zeros where not ok).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint8_t* dst, const void* src,
+                                           bool ok) {
+  if constexpr (BYTES == 2) {   // below cp.async's sizes
+    *reinterpret_cast<uint16_t*>(dst) =
+        ok ? *static_cast<const uint16_t*>(src) : uint16_t(0);
+  } else {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int n = ok ? BYTES : 0;
+    if constexpr (BYTES == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
+                   "l"(src), "r"(n) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d),
+                   "l"(src), "n"(BYTES), "r"(n) : "memory");
+  }
+}
+
+// BITS4, BITS2, BITS1: bits read in vectors of that many elements.
+enum Kind : int { OWN, PIECES, BITS1, BITS2, BITS4 };
+constexpr bool is_bits(Kind k) { return k >= BITS1; }
+constexpr int bit_vector(Kind k) { return k == BITS4 ? 4 : k == BITS2 ? 2 : 1; }
+
+// A warp's ring of the rows to come, STAGES steps in shared memory.
+//   copy(step, rows, head, heads)  copies heads head, head + 1, ... (those below
+//                                  `heads`) into the stage of `step`
+//   read(step, x)                  the lane's unit (after ring_wait and sync)
+//   put(step, rows, head, heads, y), then sync, then flush(...): the lane's
+//                                  results to memory
+// A stage is copied into again only after what was read from it has been used:
+// one step later at least, with a sync between.
+template <class T, bool INTER, int STAGES, Kind KIND>
+struct Ring;   // defined below for BITS
+
+// Held as [stage][vector][lane]; a lane reads only what it copied itself, so its
+// own wait_group is all the waiting that is needed.
+template <class T, bool INTER, int STAGES>
+struct Ring<T, INTER, STAGES, OWN> {
+  using Unit = VectorUnit<T, INTER>;
+  static constexpr int STAGE = 2 * 32 * 16;
+  static constexpr int WARP = STAGES * STAGE;
+  const Unit& un;
+  uint8_t* mine;
+  int row;
+
+  __device__ __forceinline__ Ring(uint8_t* warp, const Args&, const Lane& ln,
+                                  const Unit& u, int lane)
+      : un(u), mine(warp + lane * 16), row(ln.row) {}
+  __device__ __forceinline__ void copy(int step, const HeadRows<const T>& src,
+                                       int head, int heads) const {
+    const bool on = head + row < heads;
+    const T* from = src.at(on ? head + row : 0);
+    uint8_t* st = mine + (step % STAGES) * STAGE;
+    copy_async<16>(st, from + un.off0, on);
+    copy_async<16>(st + 32 * 16, from + un.off1, on);
+  }
+  __device__ __forceinline__ void sync() const {}
+  __device__ __forceinline__ void read(int step, Pairs<Unit::V>& x) const {
+    const uint8_t* st = mine + (step % STAGES) * STAGE;
+    const uint4 raw[2] = {*reinterpret_cast<const uint4*>(st),
+                          *reinterpret_cast<const uint4*>(st + 32 * 16)};
+    un.unpack(raw, x);
+  }
+  __device__ __forceinline__ void put(int, const HeadRows<T>& dst, int head,
+                                      int heads, Pairs<Unit::V>& y) const {
+    if (head + row >= heads) return;
+    T* to = dst.at(head + row);
+    *reinterpret_cast<uint4*>(to + un.off0) = un.pack(y, 0);
+    *reinterpret_cast<uint4*>(to + un.off1) = un.pack(y, 1);
+  }
+  __device__ __forceinline__ void flush(int, const HeadRows<T>&, int, int) const {}
+};
+
+// A step's rows one after the other: at most 60 pieces of 16 bytes, dealt to the
+// lanes in two rounds.
+template <class T, bool INTER, int STAGES>
+struct Ring<T, INTER, STAGES, PIECES> {
+  using Unit = VectorUnit<T, INTER>;
+  static constexpr int STAGE = 64 * 16;
+  static constexpr int WARP = STAGES * STAGE;
+  const Unit& un;
+  uint8_t* mine;       // this lane's first piece in stage 0
+  uint8_t* at0;        // this lane's vectors in stage 0
+  uint8_t* at1;
+  int row[2], col[2];  // its pieces: row (past the step's rows: none), byte
+
+  __device__ __forceinline__ Ring(uint8_t* warp, const Args& p, const Lane& ln,
+                                  const Unit& u, int lane)
+      : un(u), mine(warp + lane * 16) {
+    const int bytes = p.d * static_cast<int>(sizeof(T)), pieces = bytes / 16;
+    at0 = warp + ln.row * bytes + un.off0 * static_cast<int>(sizeof(T));
+    at1 = warp + ln.row * bytes + un.off1 * static_cast<int>(sizeof(T));
+    // an idle lane reads the last piece, which then holds no row's elements
+    if (!un.on) at0 = at1 = warp + 63 * 16;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int i = lane + 32 * v;
+      row[v] = i / pieces;
+      col[v] = (i - row[v] * pieces) * 16;
+      if (row[v] >= p.rows) row[v] = 1 << 20;
+    }
+  }
+  __device__ __forceinline__ void copy(int step, const HeadRows<const T>& src,
+                                       int head, int heads) const {
+    uint8_t* st = mine + (step % STAGES) * STAGE;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const bool on = head + row[v] < heads;
+      copy_async<16>(st + 32 * 16 * v,
+                     reinterpret_cast<const uint8_t*>(
+                         src.at(on ? head + row[v] : 0)) + col[v],
+                     on);
+    }
+  }
+  // Other lanes' copies are read after this (and after each lane's wait), and
+  // copied over only after the next.
+  __device__ __forceinline__ void sync() const { __syncwarp(); }
+  __device__ __forceinline__ void read(int step, Pairs<Unit::V>& x) const {
+    const int st = (step % STAGES) * STAGE;
+    const uint4 raw[2] = {*reinterpret_cast<const uint4*>(at0 + st),
+                          *reinterpret_cast<const uint4*>(at1 + st)};
+    un.unpack(raw, x);
+  }
+  __device__ __forceinline__ void put(int step, const HeadRows<T>&, int, int,
+                                      Pairs<Unit::V>& y) const {
+    const int st = (step % STAGES) * STAGE;
+    if (!un.on) return;
+    *reinterpret_cast<uint4*>(at0 + st) = un.pack(y, 0);
+    *reinterpret_cast<uint4*>(at1 + st) = un.pack(y, 1);
+  }
+  __device__ __forceinline__ void flush(int step, const HeadRows<T>& dst,
+                                        int head, int heads) const {
+    const uint8_t* st = mine + (step % STAGES) * STAGE;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      if (head + row[v] >= heads) continue;
+      *reinterpret_cast<uint4*>(
+          reinterpret_cast<uint8_t*>(dst.at(head + row[v])) + col[v]) =
+          *reinterpret_cast<const uint4*>(st + 32 * 16 * v);
+    }
+  }
+};
+
+// The same with pieces of p.piece bytes (16, 8, 4 or 2), in as many rounds as
+// they take: at most 512 elements.
+template <class T, bool INTER, int STAGES, Kind KIND>
+struct Ring {
+  using Unit = BitUnit<T, INTER, bit_vector(KIND)>;
+  static constexpr int V = Unit::V;
+  static constexpr int STAGE = 512 * static_cast<int>(sizeof(T));
+  static constexpr int WARP = STAGES * STAGE;
+  const Unit& un;
+  const Args& p;
+  uint8_t* warp;
+  int lane, row;
+
+  __device__ __forceinline__ Ring(uint8_t* w, const Args& args, const Lane& ln,
+                                  const Unit& u, int l)
+      : un(u), p(args), warp(w), lane(l), row(un.on ? ln.row : 0) {}
+  // f(piece, its row, its byte there) for the lane's pieces of the heads head,
+  // head + 1, ... that exist.
+  template <int BYTES, class F>
+  __device__ __forceinline__ void pieces(int head, int heads, F&& f) const {
+    const int n = min(p.rows, heads - head) * p.row_pieces;
+    for (int i0 = lane; i0 < n; i0 += 64) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = i0 + 32 * k;
+        if (i >= n) break;
+        const int r = p.row_pieces == 1
+                          ? i : static_cast<int>(__umulhi(i, p.row_pieces_magic));
+        f(i, r, (i - r * p.row_pieces) * BYTES);
+      }
+    }
+  }
+  template <int BYTES>
+  __device__ __forceinline__ void copy_pieces(uint8_t* st,
+                                              const HeadRows<const T>& src,
+                                              int head, int heads) const {
+    pieces<BYTES>(head, heads, [&](int i, int r, int byte) {
+      copy_async<BYTES>(st + i * BYTES,
+                        reinterpret_cast<const uint8_t*>(src.at(head + r)) +
+                            byte,
+                        true);
+    });
+  }
+  __device__ __forceinline__ void copy(int step, const HeadRows<const T>& src,
+                                       int head, int heads) const {
+    uint8_t* st = warp + (step % STAGES) * STAGE;
+    if (p.piece == 16) copy_pieces<16>(st, src, head, heads);
+    else if (p.piece == 8) copy_pieces<8>(st, src, head, heads);
+    else if (p.piece == 4) copy_pieces<4>(st, src, head, heads);
+    else copy_pieces<2>(st, src, head, heads);
+  }
+  __device__ __forceinline__ void sync() const { __syncwarp(); }
+  __device__ __forceinline__ T* place(int step) const {
+    return reinterpret_cast<T*>(warp + (step % STAGES) * STAGE) + row * p.d;
+  }
+  // (Rows past the last head hold what was there before: they are read, and
+  // go nowhere but into the gradient's sums, which leave them out.)
+  __device__ __forceinline__ void read(int step, Pairs<V>& x) const {
+    un.read(place(step), x);
+  }
+  __device__ __forceinline__ void put(int step, const HeadRows<T>&, int, int,
+                                      Pairs<V>& y) const {
+    un.write(place(step), y);
+  }
+  template <class P>
+  __device__ __forceinline__ void flush_pieces(const uint8_t* st,
+                                               const HeadRows<T>& dst, int head,
+                                               int heads) const {
+    constexpr int BYTES = static_cast<int>(sizeof(P));
+    pieces<BYTES>(head, heads, [&](int i, int r, int byte) {
+      *reinterpret_cast<P*>(reinterpret_cast<uint8_t*>(dst.at(head + r)) +
+                            byte) =
+          *reinterpret_cast<const P*>(st + i * BYTES);
+    });
+  }
+  __device__ __forceinline__ void flush(int step, const HeadRows<T>& dst,
+                                        int head, int heads) const {
+    const uint8_t* st = warp + (step % STAGES) * STAGE;
+    if (p.piece == 16) flush_pieces<uint4>(st, dst, head, heads);
+    else if (p.piece == 8) flush_pieces<uint2>(st, dst, head, heads);
+    else if (p.piece == 4) flush_pieces<uint32_t>(st, dst, head, heads);
+    else flush_pieces<uint16_t>(st, dst, head, heads);
+  }
+};
 
 // -------------------------------------------------------------- forward --
 // What a lane multiplies a row's unit by: y_a = rstd (a ca + b sb) + za, y_b =
@@ -604,11 +703,12 @@ struct Turn {
   float ca[V], sb[V], sa[V], cb[V];
   float za[V], zb[V];
 };
-template <int V, int NORM, bool INTER>
+template <int NORM, class U>
 __device__ __forceinline__ void load_turn(const Args& p, const Side& sd,
-                                          const Trig& trig, int u,
-                                          const Unit& un, Turn<V>& t) {
-  load_angles<V, INTER>(p, trig, u, t.ca, t.sa);
+                                          const Trig& trig, const U& un,
+                                          Turn<U::V>& t) {
+  constexpr int V = U::V;
+  un.angles(p, trig, t.ca, t.sa);
   if constexpr (NORM == 0) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -617,10 +717,10 @@ __device__ __forceinline__ void load_turn(const Args& p, const Side& sd,
     }
   } else {
     Pairs<V> gam;
-    load_param<V, INTER>(p, sd.gamma, 1.f, un, gam);
+    un.param(p, sd.gamma, 1.f, gam);
     if constexpr (NORM == TPQK_LAYERNORM) {
       Pairs<V> bet;
-      load_param<V, INTER>(p, sd.beta, 0.f, un, bet);
+      un.param(p, sd.beta, 0.f, bet);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         t.za[j] = fmaf(bet.a[j], t.ca[j], -(bet.b[j] * t.sa[j]));
@@ -635,17 +735,18 @@ __device__ __forceinline__ void load_turn(const Args& p, const Side& sd,
   }
 }
 
-// Steps ahead that are being copied (one group each), and steps computed at a
-// time: two, so that two rows' chains of sums share the issue slots and the
-// lane's coefficients.
-constexpr int FWD_STAGES = 8, FWD_AHEAD = 5;
-
-template <class T, int V, int NU, int NORM, bool INTER, int LEN, bool WHOLE>
-__global__ void __launch_bounds__(THREADS)
+template <class T, Kind KIND, int NORM, bool INTER, int LEN>
+__global__ void __launch_bounds__(THREADS, 4)
     qk_rows_forward(const __grid_constant__ Args p) {
-  constexpr bool LINEAR = WHOLE && LEN < 0;
-  using R = Ring<T, V, NU, FWD_STAGES, LINEAR>;
-  constexpr int AT_ONCE = NU == 1 ? 2 : 1;
+  // Steps computed at a time (two rows' chains of sums then share the issue slots
+  // and the lane's coefficients), and steps ahead that are being copied, one
+  // group each.
+  constexpr int AT_ONCE = is_bits(KIND) ? 1 : 2;
+  constexpr int STAGES = is_bits(KIND) ? 4 : 8;
+  constexpr int AHEAD = is_bits(KIND) ? 3 : 5;
+  using R = Ring<T, INTER, STAGES, KIND>;
+  using U = typename R::Unit;
+  constexpr int V = U::V;
   __shared__ __align__(16) uint8_t ring_mem[WARPS * R::WARP];
   __shared__ unsigned long long freq[MAX_PAIRS];
   __shared__ __align__(16) Trig trig[WARPS];
@@ -657,11 +758,8 @@ __global__ void __launch_bounds__(THREADS)
   int s1 = min(s0 + p.per, mid + p.side[1].steps);
   if (token >= p.tokens) s0 = s1 = 0;
   const Lane ln = lane_place<LEN>(p, lane);
-  Unit un[NU];
-#pragma unroll
-  for (int n = 0; n < NU; ++n)
-    un[n] = unit_at<V, INTER, WHOLE>(p, ln.g + 32 * n, ln.on);
-  R ring(ring_mem + warp * R::WARP, p, ln, un, lane);
+  const U un(p, ln);
+  const R ring(ring_mem + warp * R::WARP, p, ln, un, lane);
   // The next step to copy, and its side's rows and first head.
   int sc = s0;
   HeadRows<const T> src(p.side[s0 >= mid].in, token);
@@ -674,14 +772,14 @@ __global__ void __launch_bounds__(THREADS)
         src_heads = p.side[1].heads;
         hc = 0;
       }
-      ring.copy(sc, src, hc, src_heads, un);
+      ring.copy(sc, src, hc, src_heads);
       hc += p.rows;
       ++sc;
     }
     ring_commit();
   };
 #pragma unroll
-  for (int i = 0; i < FWD_AHEAD; ++i) copy();
+  for (int i = 0; i < AHEAD; ++i) copy();
   stage_freq(p, freq);
   if (s0 >= s1) return;
   make_angles(p, freq, position(p, token), lane, trig[warp]);
@@ -695,24 +793,17 @@ __global__ void __launch_bounds__(THREADS)
     const HeadRows<T> dst(sd.out, token);
     const int heads = sd.heads;
     int h = (which ? s - mid : s) * p.rows;
-    Turn<V> t[NU];
-#pragma unroll
-    for (int n = 0; n < NU; ++n)
-      load_turn<V, NORM, INTER>(p, sd, trig[warp], ln.g + 32 * n, un[n], t[n]);
+    Turn<V> t;
+    load_turn<NORM>(p, sd, trig[warp], un, t);
 #pragma unroll 1
     while (s < end) {
       // (a second step past the end is computed for nothing)
       const int used = min(AT_ONCE, end - s);
-      ring_wait<FWD_AHEAD - AT_ONCE>();
+      ring_wait<AHEAD - AT_ONCE>();
       ring.sync();
-      Pairs<V> x[AT_ONCE][NU];
+      Pairs<V> x[AT_ONCE];
 #pragma unroll
-      for (int k = 0; k < AT_ONCE; ++k) {
-        RawUnit<T, V> raw[NU];
-        ring.read(s + k, raw);
-#pragma unroll
-        for (int n = 0; n < NU; ++n) unpack<T, V, INTER>(raw[n], x[k][n]);
-      }
+      for (int k = 0; k < AT_ONCE; ++k) ring.read(s + k, x[k]);
 #pragma unroll
       for (int k = 0; k < AT_ONCE; ++k)
         if (k < used) copy();
@@ -720,17 +811,14 @@ __global__ void __launch_bounds__(THREADS)
       if constexpr (NORM == TPQK_LAYERNORM) {
         float m[AT_ONCE];
 #pragma unroll
-        for (int k = 0; k < AT_ONCE; ++k) m[k] = total<V, NU>(x[k]);
+        for (int k = 0; k < AT_ONCE; ++k) m[k] = total<V>(x[k]);
         row_sum<LEN>(m, ln);
 #pragma unroll
-        for (int k = 0; k < AT_ONCE; ++k)
-#pragma unroll
-          for (int n = 0; n < NU; ++n)
-            centre<V, INTER, WHOLE>(x[k][n], un[n], m[k] * p.inv_d);
+        for (int k = 0; k < AT_ONCE; ++k) un.centre(x[k], m[k] * p.inv_d);
       }
       if constexpr (NORM != 0) {
 #pragma unroll
-        for (int k = 0; k < AT_ONCE; ++k) scale[k] = dot<V, NU>(x[k], x[k]);
+        for (int k = 0; k < AT_ONCE; ++k) scale[k] = dot<V>(x[k], x[k]);
         row_sum<LEN>(scale, ln);
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k)
@@ -738,24 +826,20 @@ __global__ void __launch_bounds__(THREADS)
       }
 #pragma unroll
       for (int k = 0; k < AT_ONCE; ++k) {
-        Pairs<V> y[NU];
-#pragma unroll
-        for (int n = 0; n < NU; ++n) {
-          // the rotation does not wait for the norm's sum
-          mul<V>(y[n].a, x[k][n].b, t[n].sb);
-          mul<V>(y[n].b, x[k][n].b, t[n].cb);
-          fma<V>(y[n].a, x[k][n].a, t[n].ca, y[n].a);
-          fma<V>(y[n].b, x[k][n].a, t[n].sa, y[n].b);
-          if constexpr (NORM == TPQK_LAYERNORM) {
-            fma<V>(y[n].a, y[n].a, scale[k], t[n].za);
-            fma<V>(y[n].b, y[n].b, scale[k], t[n].zb);
-          } else if constexpr (NORM != 0) {
-            mul<V>(y[n].a, y[n].a, scale[k]);
-            mul<V>(y[n].b, y[n].b, scale[k]);
-          }
+        // the rotation does not wait for the norm's sum
+        Pairs<V> y;
+        mul<V>(y.a, x[k].b, t.sb);
+        mul<V>(y.b, x[k].b, t.cb);
+        fma<V>(y.a, x[k].a, t.ca, y.a);
+        fma<V>(y.b, x[k].a, t.sa, y.b);
+        if constexpr (NORM == TPQK_LAYERNORM) {
+          fma<V>(y.a, y.a, scale[k], t.za);
+          fma<V>(y.b, y.b, scale[k], t.zb);
+        } else if constexpr (NORM != 0) {
+          mul<V>(y.a, y.a, scale[k]);
+          mul<V>(y.b, y.b, scale[k]);
         }
-        if (k < used)
-          ring.template put<INTER>(s + k, dst, h + k * p.rows, heads, un, y);
+        if (k < used) ring.put(s + k, dst, h + k * p.rows, heads, y);
       }
       ring.sync();
 #pragma unroll
@@ -773,18 +857,19 @@ __global__ void __launch_bounds__(THREADS)
 //   dx = (rstd g) gamma - (rstd^3 sum(e u) / d) e [- rstd mean(u)].
 // Persistent blocks, so that a lane sums its unit's parameter gradients over
 // all its rows in registers; a block takes q's tasks or k's.
-constexpr int BWD_STAGES = 4, BWD_AHEAD = 3;
-
-template <class T, int V, int NU, int NORM, bool INTER, int LEN, bool WHOLE>
+template <class T, Kind KIND, int NORM, bool INTER, int LEN>
 __global__ void __launch_bounds__(THREADS, 4)
     qk_rows_backward(const __grid_constant__ Args p) {
-  constexpr bool LINEAR = WHOLE && LEN < 0;
-  using R = Ring<T, V, NU, BWD_STAGES, LINEAR>;
-  constexpr int SUMS = WARPS * 32 * NU * 2 * V;   // floats
+  constexpr int STAGES = is_bits(KIND) && sizeof(T) == 4 ? 2 : 4;
+  constexpr int AHEAD = STAGES - 1;
+  using R = Ring<T, INTER, STAGES, KIND>;
+  using U = typename R::Unit;
+  constexpr int V = U::V;
   __shared__ __align__(16) uint8_t ring_mem[2 * WARPS * R::WARP];
   __shared__ unsigned long long freq[MAX_PAIRS];
   __shared__ __align__(16) Trig trig[WARPS];
-  static_assert(sizeof(ring_mem) >= SUMS * sizeof(float), "the sums reuse it");
+  // at the end it holds a sum for every element of every row slot
+  static_assert(2 * R::WARP >= 32 * 2 * V * 4, "ring_mem is too small");
   // the blocks' sums are added by a launch that may come up meanwhile
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   stage_freq(p, freq);
@@ -796,18 +881,14 @@ __global__ void __launch_bounds__(THREADS, 4)
   const unsigned segs = p.segs_side[which];
   const int per = p.per_side[which], heads = sd.heads;
   const Lane ln = lane_place<LEN>(p, lane);
-  Unit un[NU];
-  Pairs<V> gam[NU], dgam[NU], dbet[NU];
+  const U un(p, ln);
+  Pairs<V> gam, dgam, dbet;
+  un.param(p, sd.gamma, 1.f, gam);
 #pragma unroll
-  for (int n = 0; n < NU; ++n) {
-    un[n] = unit_at<V, INTER, WHOLE>(p, ln.g + 32 * n, ln.on);
-    load_param<V, INTER>(p, sd.gamma, 1.f, un[n], gam[n]);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      dgam[n].a[j] = dgam[n].b[j] = dbet[n].a[j] = dbet[n].b[j] = 0.f;
-  }
-  R gring(ring_mem + 2 * warp * R::WARP, p, ln, un, lane);
-  R xring(ring_mem + (2 * warp + 1) * R::WARP, p, ln, un, lane);
+  for (int j = 0; j < V; ++j)
+    dgam.a[j] = dgam.b[j] = dbet.a[j] = dbet.b[j] = 0.f;
+  const R gring(ring_mem + 2 * warp * R::WARP, p, ln, un, lane);
+  const R xring(ring_mem + (2 * warp + 1) * R::WARP, p, ln, un, lane);
   const unsigned tasks = static_cast<unsigned>(p.tokens) * segs;
   for (unsigned task = block * WARPS + warp; task < tasks;
        task += blocks * WARPS) {
@@ -819,93 +900,90 @@ __global__ void __launch_bounds__(THREADS, 4)
     int sc = s0, h = s0 * p.rows, hc = h;
     auto copy = [&] {
       if (sc < s1) {
-        gring.copy(sc, gsrc, hc, heads, un);
-        xring.copy(sc, xsrc, hc, heads, un);
+        gring.copy(sc, gsrc, hc, heads);
+        xring.copy(sc, xsrc, hc, heads);
         hc += p.rows;
         ++sc;
       }
       ring_commit();
     };
 #pragma unroll
-    for (int i = 0; i < BWD_AHEAD; ++i) copy();
+    for (int i = 0; i < AHEAD; ++i) copy();
     make_angles(p, freq, position(p, token), lane, trig[warp]);
-    float c[NU][V], sa[NU][V];
-#pragma unroll
-    for (int n = 0; n < NU; ++n)
-      load_angles<V, INTER>(p, trig[warp], ln.g + 32 * n, c[n], sa[n]);
+    float c[V], sa[V];
+    un.angles(p, trig[warp], c, sa);
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-      ring_wait<BWD_AHEAD - 1>();
+      ring_wait<AHEAD - 1>();
       gring.sync();
-      Pairs<V> g[NU], e[NU];
+      Pairs<V> g, e;
       {
-        RawUnit<T, V> graw[NU], xraw[NU];
-        gring.read(s, graw);
-        xring.read(s, xraw);
+        Pairs<V> dy;
+        gring.read(s, dy);
+        xring.read(s, e);
         copy();
+        // R^T (sa carries the opposite direction's sign)
+        float t[V];
+        mul<V>(t, dy.b, -1.f);
+        mul<V>(g.a, t, sa);
+        fma<V>(g.a, dy.a, c, g.a);
+        mul<V>(g.b, dy.b, c);
+        fma<V>(g.b, dy.a, sa, g.b);
+      }
+      if constexpr (is_bits(KIND)) {   // rows past the last head
+        if (h + ln.row >= heads) {
 #pragma unroll
-        for (int n = 0; n < NU; ++n) {
-          Pairs<V> dy;
-          unpack<T, V, INTER>(graw[n], dy);
-          unpack<T, V, INTER>(xraw[n], e[n]);
-          // R^T (sa carries the opposite direction's sign)
-          float t[V];
-          mul<V>(t, dy.b, -1.f);
-          mul<V>(g[n].a, t, sa[n]);
-          fma<V>(g[n].a, dy.a, c[n], g[n].a);
-          mul<V>(g[n].b, dy.b, c[n]);
-          fma<V>(g[n].b, dy.a, sa[n], g[n].b);
+          for (int j = 0; j < V; ++j) g.a[j] = g.b[j] = e.a[j] = e.b[j] = 0.f;
         }
       }
       float mean_u = 0.f;
       if constexpr (NORM == TPQK_LAYERNORM) {
-        float m[2] = {total<V, NU>(e), dot<V, NU>(g, gam)};
+        float m[2] = {total<V>(e), dot<V>(g, gam)};
         row_sum<LEN>(m, ln);
-#pragma unroll
-        for (int n = 0; n < NU; ++n)
-          centre<V, INTER, WHOLE>(e[n], un[n], m[0] * p.inv_d);
+        un.centre(e, m[0] * p.inv_d);
         mean_u = m[1] * p.inv_d;
       }
-      float q[2] = {dot<V, NU>(e, e), 0.f};
-#pragma unroll
-      for (int n = 0; n < NU; ++n) {   // sum of e u
+      float q[2] = {dot<V>(e, e), 0.f};
+      {   // sum of e u
         float t[V], u[V];
-        mul<V>(u, g[n].a, gam[n].a);
-        mul<V>(t, u, e[n].a);
-        mul<V>(u, g[n].b, gam[n].b);
-        fma<V>(t, u, e[n].b, t);
-        q[1] += sum<V>(t);
+        mul<V>(u, g.a, gam.a);
+        mul<V>(t, u, e.a);
+        mul<V>(u, g.b, gam.b);
+        fma<V>(t, u, e.b, t);
+        q[1] = sum<V>(t);
       }
       row_sum<LEN>(q, ln);
       const float rstd = rsqrtf(fmaf(q[0], p.inv_d, p.eps));
       const float k = -(rstd * rstd) * (q[1] * rstd * p.inv_d);
-      const float m = -rstd * mean_u;
-      Pairs<V> dx[NU];
-#pragma unroll
-      for (int n = 0; n < NU; ++n) {
-        if constexpr (NORM == TPQK_LAYERNORM) {
-          add<V>(dbet[n].a, g[n].a);
-          add<V>(dbet[n].b, g[n].b);
-        }
-        mul<V>(g[n].a, g[n].a, rstd);
-        mul<V>(g[n].b, g[n].b, rstd);
-        fma<V>(dgam[n].a, g[n].a, e[n].a, dgam[n].a);
-        fma<V>(dgam[n].b, g[n].b, e[n].b, dgam[n].b);
-        mul<V>(dx[n].a, e[n].a, k);
-        mul<V>(dx[n].b, e[n].b, k);
-        if constexpr (NORM == TPQK_LAYERNORM) {
-          add<V>(dx[n].a, m);
-          add<V>(dx[n].b, m);
-        }
-        fma<V>(dx[n].a, g[n].a, gam[n].a, dx[n].a);
-        fma<V>(dx[n].b, g[n].b, gam[n].b, dx[n].b);
+      if constexpr (NORM == TPQK_LAYERNORM) {
+        add<V>(dbet.a, g.a);
+        add<V>(dbet.b, g.b);
       }
-      gring.template put<INTER>(s, dst, h, heads, un, dx);
+      mul<V>(g.a, g.a, rstd);
+      mul<V>(g.b, g.b, rstd);
+      // (a row that does not exist is zero, and with eps = 0 its rstd infinite)
+      if (h + p.rows <= heads || h + ln.row < heads) {
+        fma<V>(dgam.a, g.a, e.a, dgam.a);
+        fma<V>(dgam.b, g.b, e.b, dgam.b);
+      }
+      Pairs<V> dx;
+      mul<V>(dx.a, e.a, k);
+      mul<V>(dx.b, e.b, k);
+      if constexpr (NORM == TPQK_LAYERNORM) {
+        const float m = -rstd * mean_u;
+        add<V>(dx.a, m);
+        add<V>(dx.b, m);
+      }
+      fma<V>(dx.a, g.a, gam.a, dx.a);
+      fma<V>(dx.b, g.b, gam.b, dx.b);
+      gring.put(s, dst, h, heads, dx);
       gring.sync();
       gring.flush(s, dst, h, heads);
       h += p.rows;
     }
-    // the ring is empty again: its last steps' groups hold nothing
+    // The ring is empty again: its last steps' groups hold nothing.  (Before the
+    // next task's copies, every lane has left the last stage.)
+    gring.sync();
   }
   if (p.part == nullptr) return;
   // the block's sums: element i of every row slot, in the order of the slots
@@ -915,16 +993,10 @@ __global__ void __launch_bounds__(THREADS, 4)
   for (int k = 0; k < (NORM == TPQK_LAYERNORM ? 2 : 1); ++k) {
     __syncthreads();
 #pragma unroll
-    for (int n = 0; n < NU; ++n) {
-#pragma unroll
-      for (int i = 0; i < 2 * V; ++i) {
-        const bool ok = i < V ? un[n].ok0 : un[n].ok1;
-        const int at = i < V ? un[n].off0 + i : un[n].off1 + i - V;
-        if (ok)
-          sums[(warp * p.rows + ln.row) * p.d + at] =
-              element<V, INTER>(k ? dbet[n] : dgam[n], i);
-      }
-    }
+    for (int i = 0; i < 2 * V; ++i)
+      if (un.has(i))
+        sums[(warp * p.rows + ln.row) * p.d + un.element(i)] =
+            U::value(k ? dbet : dgam, i);
     __syncthreads();
     for (int i = threadIdx.x; i < p.d; i += THREADS) {
       float t = 0.f;
@@ -935,84 +1007,58 @@ __global__ void __launch_bounds__(THREADS, 4)
 }
 
 // ------------------------------------------------------------- dispatch --
-template <class T, int V, int NU, int NORM, bool INTER, int LEN, bool WHOLE>
-void go(const Args& a, int blocks, bool backward, cudaStream_t s) {
+template <class T, Kind KIND, int NORM, bool INTER, int LEN>
+cudaError_t go(const Args& a, int blocks, bool backward, cudaStream_t s) {
   if (!backward) {
-    qk_rows_forward<T, V, NU, NORM, INTER, LEN, WHOLE>
-        <<<blocks, THREADS, 0, s>>>(a);
+    qk_rows_forward<T, KIND, NORM, INTER, LEN><<<blocks, THREADS, 0, s>>>(a);
   } else if constexpr (NORM != 0) {
-    qk_rows_backward<T, V, NU, NORM, INTER, LEN, WHOLE>
-        <<<blocks, THREADS, 0, s>>>(a);
+    qk_rows_backward<T, KIND, NORM, INTER, LEN><<<blocks, THREADS, 0, s>>>(a);
   }
+  return cudaGetLastError();
 }
 
-// Rows of 16-byte vectors without a part unit have kernels of their own, and
-// those that fill 4, 8 or 16 lanes (8, 16, 32 in fp32) one each.
-template <class T, int V, int NU, int NORM, bool INTER>
-void by_length(const Args& a, int blocks, bool backward, cudaStream_t s) {
-  if constexpr (V * sizeof(T) == 16) {
-    constexpr int SHORT = 32 / V;   // 64 elements
-    if (a.d == 2 * V * a.units) {
-      if (a.units == SHORT)
-        return go<T, V, NU, NORM, INTER, SHORT, true>(a, blocks, backward, s);
-      if (a.units == 2 * SHORT)
-        return go<T, V, NU, NORM, INTER, 2 * SHORT, true>(a, blocks, backward, s);
-      if (a.units == 4 * SHORT)
-        return go<T, V, NU, NORM, INTER, 4 * SHORT, true>(a, blocks, backward, s);
-      if (a.units <= 8)
-        return go<T, V, NU, NORM, INTER, -3, true>(a, blocks, backward, s);
-      if (a.units <= 16)
-        return go<T, V, NU, NORM, INTER, -4, true>(a, blocks, backward, s);
-      if constexpr (V == 4)
-        return go<T, V, NU, NORM, INTER, -5, true>(a, blocks, backward, s);
-    }
-  }
-  go<T, V, NU, NORM, INTER, -5, false>(a, blocks, backward, s);
+template <class T, int NORM, bool INTER>
+cudaError_t by_length(const Args& a, int bits, int blocks, bool backward,
+                      cudaStream_t s) {
+  constexpr int SHORT = 2 * static_cast<int>(sizeof(T));   // 64 elements
+  if (bits == 4)
+    return a.units <= 8 ? go<T, BITS4, NORM, INTER, -3>(a, blocks, backward, s)
+                        : go<T, BITS4, NORM, INTER, -5>(a, blocks, backward, s);
+  if (bits == 2)
+    return a.units <= 8 ? go<T, BITS2, NORM, INTER, -3>(a, blocks, backward, s)
+                        : go<T, BITS2, NORM, INTER, -5>(a, blocks, backward, s);
+  if (bits == 1)
+    return a.units <= 8 ? go<T, BITS1, NORM, INTER, -3>(a, blocks, backward, s)
+                        : go<T, BITS1, NORM, INTER, -5>(a, blocks, backward, s);
+  if (a.units == SHORT)
+    return go<T, OWN, NORM, INTER, SHORT>(a, blocks, backward, s);
+  if (a.units == 2 * SHORT)
+    return go<T, OWN, NORM, INTER, 2 * SHORT>(a, blocks, backward, s);
+  if (a.units == 4 * SHORT)
+    return go<T, OWN, NORM, INTER, 4 * SHORT>(a, blocks, backward, s);
+  if (a.units <= 8)
+    return go<T, PIECES, NORM, INTER, -3>(a, blocks, backward, s);
+  if constexpr (sizeof(T) == 4)
+    if (a.units > 16)
+      return go<T, PIECES, NORM, INTER, -5>(a, blocks, backward, s);
+  return go<T, PIECES, NORM, INTER, -4>(a, blocks, backward, s);
 }
 
-template <class T, int V, int NU>
-void by_norm(const Args& a, int norm, bool inter, int blocks, bool backward,
-             cudaStream_t s) {
-  if (norm == TPQK_RMSNORM) {
-    if (inter) by_length<T, V, NU, TPQK_RMSNORM, true>(a, blocks, backward, s);
-    else by_length<T, V, NU, TPQK_RMSNORM, false>(a, blocks, backward, s);
-  } else if (norm == TPQK_LAYERNORM) {
-    if (inter) by_length<T, V, NU, TPQK_LAYERNORM, true>(a, blocks, backward, s);
-    else by_length<T, V, NU, TPQK_LAYERNORM, false>(a, blocks, backward, s);
-  } else {
-    if (inter) by_length<T, V, NU, 0, true>(a, blocks, backward, s);
-    else by_length<T, V, NU, 0, false>(a, blocks, backward, s);
-  }
+template <class T>
+cudaError_t by_norm(const Args& a, int bits, int norm, bool inter,
+                    int blocks, bool backward, cudaStream_t s) {
+  if (norm == TPQK_RMSNORM)
+    return (inter ? by_length<T, TPQK_RMSNORM, true>
+                  : by_length<T, TPQK_RMSNORM, false>)(a, bits, blocks,
+                                                       backward, s);
+  if (norm == TPQK_LAYERNORM)
+    return (inter ? by_length<T, TPQK_LAYERNORM, true>
+                  : by_length<T, TPQK_LAYERNORM, false>)(a, bits, blocks,
+                                                         backward, s);
+  return (inter ? by_length<T, 0, true> : by_length<T, 0, false>)(
+      a, bits, blocks, backward, s);
 }
 
 }  // namespace
-
-// Units a lane may have: 256 / (2 V) / 32, at least one.
-#ifdef QK_ROWS_BF16
-cudaError_t launch_bf16(const Args& a, int vec, int norm, bool inter, int blocks,
-                        bool backward, cudaStream_t s) {
-  using T = __nv_bfloat16;
-  switch (vec) {
-    case 8: by_norm<T, 8, 1>(a, norm, inter, blocks, backward, s); break;
-    case 4: by_norm<T, 4, 1>(a, norm, inter, blocks, backward, s); break;
-    case 2: by_norm<T, 2, 2>(a, norm, inter, blocks, backward, s); break;
-    case 1: by_norm<T, 1, 4>(a, norm, inter, blocks, backward, s); break;
-    default: return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
-}
-#else
-cudaError_t launch_fp32(const Args& a, int vec, int norm, bool inter, int blocks,
-                        bool backward, cudaStream_t s) {
-  switch (vec) {
-    case 4: by_norm<float, 4, 1>(a, norm, inter, blocks, backward, s); break;
-    case 2: by_norm<float, 2, 2>(a, norm, inter, blocks, backward, s); break;
-    case 1: by_norm<float, 1, 4>(a, norm, inter, blocks, backward, s); break;
-    default: return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
-}
-#endif
-
 }  // namespace qk
 }  // namespace tpmlp

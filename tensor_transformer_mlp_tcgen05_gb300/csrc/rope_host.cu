@@ -198,16 +198,16 @@ int check_call(const Call& c, int tokens, int d, int size) {
   return TPMLP_OK;
 }
 
-// Largest power of two up to `vec` that divides every distance of the view.
-int fit_vec(int vec, const tp_heads& v, int tokens, int size) {
+// Largest power of two up to `bytes` that divides every distance of the view.
+int fit_bytes(int bytes, const tp_heads& v, int tokens, int size) {
   const Steps s = steps_of(v, tokens);
-  while (vec > 1) {
-    bool ok = reinterpret_cast<uintptr_t>(v.data) % (vec * size) == 0;
-    for (int i = 0; i < s.n; ++i) ok = ok && s.stride[i] % vec == 0;
+  while (bytes > size) {
+    bool ok = reinterpret_cast<uintptr_t>(v.data) % bytes == 0;
+    for (int i = 0; i < s.n; ++i) ok = ok && s.stride[i] * size % bytes == 0;
     if (ok) break;
-    vec /= 2;
+    bytes /= 2;
   }
-  return vec;
+  return bytes;
 }
 
 qk::View kernel_view(const tp_heads& v, int size) {
@@ -224,25 +224,45 @@ qk::View kernel_view(const tp_heads& v, int size) {
   return k;
 }
 
-// The kernel's arguments, without norm and parameter pointers.  turn_tail:
-// the elements past r are read and written too.  Returns the vector width.
+// The kernel's arguments, without norm and parameter pointers.  with_rest: the
+// elements past r are read and written too (else a row is its first r).  Returns
+// the kernels' `bits`: rows move in 16-byte vectors where r / 2, the elements past
+// r and every distance are whole ones, else in bits of as many elements as divide
+// r / 2 (interleaved: r), the elements past r and a row.
 int plan(const tp_rope_handle& H, const Call& c, int tokens, int size,
-         int inverse, bool turn_tail, const tp_positions* pos, qk::Args* a) {
+          int inverse, bool with_rest, const tp_positions* pos, qk::Args* a) {
   std::memset(a, 0, sizeof(*a));
-  int vec = 16 / size;
-  while (vec > 1 && ((H.r / 2) % vec != 0 || H.d % vec != 0)) vec /= 2;
+  int bytes = 16;
   for (int s = 0; s < 2; ++s) {
     if (!present(c.out[s])) continue;
     for (int i = 0; i < c.inputs; ++i)
-      vec = fit_vec(vec, *c.in[s][i], tokens, size);
-    vec = fit_vec(vec, *c.out[s], tokens, size);
+      bytes = fit_bytes(bytes, *c.in[s][i], tokens, size);
+    bytes = fit_bytes(bytes, *c.out[s], tokens, size);
   }
+  const int d = with_rest ? H.d : H.r;   // elements of a row that count
+  const int vec = 16 / size;
+  int bits = 0;
+  if (bytes < 16 || H.r / 2 % vec != 0 || (d - H.r) % (2 * vec) != 0) {
+    const int part = H.interleaved ? H.r : H.r / 2;
+    bits = 4;
+    while (bits > 1 && (part % bits != 0 || (d - H.r) % bits != 0 ||
+                        d % bits != 0))
+      bits /= 2;
+  }
+  const int per = bits ? 8 : vec;        // pairs of a unit
   a->tokens = tokens;
-  a->d = H.d;
+  a->d = d;
   a->rot = H.r;
-  a->rot_units = H.r / (2 * vec);
-  a->units = turn_tail ? (H.d + 2 * vec - 1) / (2 * vec) : a->rot_units;
-  a->rows = 32 / std::min(a->units, 32);
+  a->rot_units = (H.r / 2 + per - 1) / per;
+  a->units = a->rot_units + (d - H.r + 2 * per - 1) / (2 * per);
+  a->rows = 32 / a->units;
+  while (d * size % bytes != 0) bytes /= 2;   // whole pieces in a row
+  a->piece = bytes;
+  a->row_pieces = d * size / bytes;
+  a->row_pieces_magic =
+      a->row_pieces == 1 ? 0u
+                         : static_cast<unsigned>(
+                               ((1ull << 32) + a->row_pieces - 1) / a->row_pieces);
   for (int s = 0; s < 2; ++s) {
     qk::Side& sd = a->side[s];
     if (!present(c.out[s])) continue;
@@ -263,7 +283,7 @@ int plan(const tp_rope_handle& H, const Call& c, int tokens, int size,
   a->sign = inverse ? -1.f : 1.f;
   a->inv_d = 1.0f / static_cast<float>(H.d);
   for (int i = 0; i < H.r / 2; ++i) a->freq[i] = H.turns[i];
-  return vec;
+  return bits;
 }
 
 int check_common(const tp_rope_handle* H, int tokens, int dtype,
@@ -351,7 +371,7 @@ int run_forward(tp_rope_handle* H, int tokens, int dtype, int inverse,
     if (!tail && H->r == 0) return TPMLP_OK;
   }
   qk::Args a;
-  const int vec = plan(*H, c, tokens, size, inverse, tail, pos, &a);
+  const int bits = plan(*H, c, tokens, size, inverse, tail, pos, &a);
   const int steps = a.side[0].steps + a.side[1].steps;
   a.per = steps_per_task(steps, tokens, FORWARD_TASKS, FORWARD_STEPS);
   a.segs = (steps + a.per - 1) / a.per;
@@ -363,7 +383,7 @@ int run_forward(tp_rope_handle* H, int tokens, int dtype, int inverse,
     a.side[1].beta = norm->k_beta;
     a.param16 = params_aligned(*norm);
   }
-  return cuda_rc(qk::launch_forward(a, dtype == TPMLP_BF16, vec,
+  return cuda_rc(qk::launch_forward(a, dtype == TPMLP_BF16, bits,
                                     norm ? norm->norm : 0, H->interleaved != 0,
                                     static_cast<cudaStream_t>(stream)),
                  norm ? "qk_norm_forward" : "rope_apply");
@@ -526,7 +546,7 @@ int tp_qk_norm_backward(tp_rope_handle* H, int tokens, int dtype,
     return TPMLP_OK;
   }
   qk::Args a;
-  const int vec = plan(*H, c, tokens, size, 1, true, positions, &a);
+  const int bits = plan(*H, c, tokens, size, 1, true, positions, &a);
   a.eps = norm->eps;
   a.side[0].gamma = norm->q_gamma;
   a.side[1].gamma = norm->k_gamma;
@@ -552,7 +572,7 @@ int tp_qk_norm_backward(tp_rope_handle* H, int tokens, int dtype,
   const long long bk = side_blocks[1];
   a.q_blocks = static_cast<int>(bq);
   const int blocks = static_cast<int>(bq + bk);
-  TRY(cuda_rc(qk::launch_backward(a, dtype == TPMLP_BF16, vec, norm->norm,
+  TRY(cuda_rc(qk::launch_backward(a, dtype == TPMLP_BF16, bits, norm->norm,
                                   H->interleaved != 0, blocks, s),
               "qk_norm_backward"));
   if (!params) return TPMLP_OK;

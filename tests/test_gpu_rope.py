@@ -72,11 +72,14 @@ def make(T, hq, hk, d, dtype, seed, layout="plain"):
     return n(T, hq, d), n(T, hk, d)
 
 
-# (d, r): every vector width of bf16 (8, 4, 2, 1) and fp32, tails of one
-# vector and of many, head dims that leave lanes idle, the smallest and largest
+# (d, r): rows of whole 16-byte vectors that fill lanes exactly and that do not,
+# rows moved element by element in pieces of 16, 8, 4 and 2 bytes, few and many
+# elements past r, the smallest and the largest
 DIMS = [(64, 64), (128, 128), (96, 96), (80, 40), (128, 32), (256, 256),
         (256, 64), (72, 72), (100, 100), (40, 20), (36, 12), (24, 10), (10, 6),
-        (2, 2), (7, 4), (1, 0), (64, 0), (192, 48), (250, 250), (255, 254)]
+        (2, 2), (7, 4), (1, 0), (64, 0), (192, 48), (250, 250), (255, 254),
+        (160, 160), (32, 32), (16, 16), (48, 32), (112, 112), (256, 2), (8, 8),
+        (4, 2), (128, 126), (192, 192), (224, 128)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -203,6 +206,40 @@ def test_strided_views(layout, dtype):
                rows_max(flat(x)) * rstd, K_NORM, dtype)
     got = op.backward(dq, dk, q, k, seq_len=50)
     check_gradients(op, q, k, dq, dk, None, None, pos, f, False, dtype, got)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,r", DIMS)
+def test_rotation_in_place(d, r, inter, dtype):
+    """Equal to out of place; the elements past r stay as they were."""
+    T, hq, hk = 23, 5, 3
+    q, k = make(T, hq, hk, d, dtype, d + 2 * r)
+    rope = RotaryEmbedding(d, rotary_dim=r, interleaved=inter)
+    want = rope.forward(q, k, offset=9)
+    got = rope.forward(q, k, offset=9, q_out=q, k_out=k)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_parameters_off_16_bytes():
+    d = 128
+    q, k = make(50, 4, 4, d, torch.bfloat16, 6)
+    dq, dk = make(50, 4, 4, d, torch.bfloat16, 7)
+    g = torch.Generator("cuda").manual_seed(8)
+    par = [torch.randn(d, generator=g, device="cuda") for _ in range(4)]
+    room = torch.empty(4, d + 1, device="cuda")
+    off = [room[i, 1:].copy_(p) if (i % 2 == 0) else p.clone()
+           for i, p in enumerate(par)]
+    assert any(p.data_ptr() % 16 for p in off)
+    op = QKNormRotary(d, norm="layer", rotary=RotaryEmbedding(d))
+    for a, b in zip(op.forward(q, k, *par), op.forward(q, k, *off)):
+        assert torch.equal(a, b)
+    a = op.backward(dq, dk, q, k, *par[:2])
+    b = op.backward(dq, dk, q, k, *off[:2],
+                    out={"dq_gamma": room.view(-1)[3:3 + d]})
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
 
 
 @pytest.mark.parametrize("r", [96, 40])
