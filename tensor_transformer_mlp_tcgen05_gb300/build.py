@@ -87,7 +87,8 @@ def build_pycall(force: bool = False) -> str:
            os.path.join(CSRC, "pycall.cpp"), "-o", tmp,
            *["-I" + i for i in inc],
            "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for pycall.cpp:\n{r.stderr}")

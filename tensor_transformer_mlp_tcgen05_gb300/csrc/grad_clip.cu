@@ -1,12 +1,12 @@
 // Global L2 norm of many gradient tensors, and clipping (tp_grad.h).
 //
-// Two passes over the data: sums of squares per block, then, each block having
-// added all blocks' sums in the same fixed order, the scaling.  Both are bound by
-// memory; each thread has eight 16-byte loads in flight.  The second pass walks
-// the chunks backwards, so that what the first read last is still in L2 (129 MB):
-// gradients smaller than that are read from DRAM once.  Its blocks are launched
-// while the first pass drains (programmatic dependent launch) and load their
-// first chunk before they wait for its sums.
+// Three launches: sums of squares per block, their sum and the factor by one
+// block, the scaling.  The first and the last are bound by memory; each thread has
+// eight 16-byte loads in flight.  The last walks the chunks backwards, so that
+// what the first read last is still in L2 (129 MB): gradients smaller than that
+// are read from DRAM once.  Each launch comes up while its predecessor drains
+// (programmatic dependent launch), and the last loads its chunks before it
+// waits for the factor.
 //
 // A few short tensors are done by one launch of one cluster of eight blocks,
 // which exchange their sums through distributed shared memory.
@@ -26,7 +26,8 @@ constexpr int BATCH = 8;
 constexpr int THREADS = 256;
 constexpr int BLOCKS = 608;            // four on each of the 152 SMs
 constexpr int CHUNK_BYTES = 16 * BATCH * THREADS;
-// Tensors of one launch: the table travels as a kernel parameter.
+// Tensors of one launch: the table travels as a kernel parameter (16 KB; one of
+// SMALL_TABLE, 2 KB, where that is enough).
 constexpr int TABLE = 512;
 
 // One cluster: pieces of one warp's batch of SMALL_BATCH vectors a lane.
@@ -232,8 +233,9 @@ __device__ __forceinline__ float factor(double n, double max_norm, double eps) {
   return isfinite(n) && ratio < 1.0 ? static_cast<float>(ratio) : 1.f;
 }
 
+template <int N>
 __global__ void __launch_bounds__(THREADS, 4)
-    grad_squares(const __grid_constant__ Table<TABLE> t, double* part) {
+    grad_squares(const __grid_constant__ Table<N> t, double* part) {
   // the second pass may take the SMs' free places from here on
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   double wide = 0.0;
@@ -250,8 +252,7 @@ __global__ void __launch_bounds__(THREADS, 4)
   if (threadIdx.x == 0) part[blockIdx.x] = wide;
 }
 
-// Waits until the sums are there, and adds them: the same total in every block.
-// (Every thread loads its own few first: one warp alone, load after load, took
+// Waits until the sums are there, and adds them.  (Every thread loads its own few first: one warp alone, load after load, took
 // 6 us for 608 of them.)
 __device__ __forceinline__ double total_norm(const double* part, int slots) {
   __shared__ double norm;
@@ -274,40 +275,32 @@ __device__ __forceinline__ double total_norm(const double* part, int slots) {
   return norm;
 }
 
+// (c: nullable; for grad_scale.)
 __global__ void __launch_bounds__(THREADS)
-    grad_norm_final(const double* part, int slots, float* norm) {
+    grad_norm_final(const double* part, int slots, double max_norm, double eps,
+                    float* norm, float* c) {
   const double n = total_norm(part, slots);
-  if (threadIdx.x == 0) *norm = static_cast<float>(n);
+  if (threadIdx.x == 0) {
+    *norm = static_cast<float>(n);
+    if (c != nullptr) *c = factor(n, max_norm, eps);
+  }
 }
 
+// One chunk a block.  (A block that stays and walks over chunks, as in
+// grad_squares, reached 6.3 TB/s of reads and writes together, one block a chunk
+// 6.8: 578 and 545 us for all of 1.26 GB.)
+template <int N>
 __global__ void __launch_bounds__(THREADS, 4)
-    grad_scale(const __grid_constant__ Table<TABLE> t, const double* part,
-               int slots, double max_norm, double eps, float* norm) {
-  unsigned k = blockIdx.x;
+    grad_scale(const __grid_constant__ Table<N> t, const float* factor) {
+  const unsigned chunk = t.chunks - 1 - blockIdx.x;
+  const Part p = part_of<CHUNK_BYTES>(entry_of(t, chunk), chunk);
   uint4 v[BATCH];
-  Part p;
-  p.n = p.nv = 0;
-  if (k < t.chunks) {
-    const unsigned chunk = t.chunks - 1 - k;
-    p = part_of<CHUNK_BYTES>(entry_of(t, chunk), chunk);
-    load_batch<BATCH, THREADS>(p, threadIdx.x, v);
-  }
-  const double n = total_norm(part, slots);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && norm != nullptr)
-    *norm = static_cast<float>(n);
-  const float c = factor(n, max_norm, eps);
-  while (k < t.chunks) {
-    if (c != 1.f || p.g != p.o) {
-      store_batch<BATCH, THREADS>(p, threadIdx.x, v, c);
-      rest_scale(p, threadIdx.x, THREADS, c);
-    }
-    k += gridDim.x;
-    if (k >= t.chunks) break;
-    const unsigned chunk = t.chunks - 1 - k;
-    p = part_of<CHUNK_BYTES>(entry_of(t, chunk), chunk);
-    if (c != 1.f || p.g != p.o)
-      load_batch<BATCH, THREADS>(p, threadIdx.x, v);
-  }
+  load_batch<BATCH, THREADS>(p, threadIdx.x, v);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float c = *factor;
+  if (c == 1.f && p.g == p.o) return;
+  store_batch<BATCH, THREADS>(p, threadIdx.x, v, c);
+  rest_scale(p, threadIdx.x, THREADS, c);
 }
 
 // Norm and (clip) scaling of at most 2 x SMALL_WARPS pieces: a warp keeps its
@@ -417,13 +410,28 @@ int check_tensors(int count, const tp_grad_tensor* t, bool clip) {
 // Every out is its own grad or overlaps no grad and no other out: the ranges in
 // the order of their starts, each compared with the furthest out and the
 // furthest range before it.
+struct Range {
+  uintptr_t lo, hi;
+  bool out;
+};
+bool apart(Range* r, size_t n) {
+  auto before = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+  if (!std::is_sorted(r, r + n, before)) std::sort(r, r + n, before);
+  uintptr_t out_end = 0, any_end = 0;
+  for (size_t i = 0; i < n; ++i) {
+    if (r[i].lo < out_end || (r[i].out && r[i].lo < any_end)) return false;
+    any_end = std::max(any_end, r[i].hi);
+    if (r[i].out) out_end = std::max(out_end, r[i].hi);
+  }
+  return true;
+}
 int check_apart(int count, const tp_grad_tensor* t) {
-  struct Range {
-    uintptr_t lo, hi;
-    bool out;
-  };
-  Range* r = new (std::nothrow) Range[2 * static_cast<size_t>(count) + 1];
-  if (r == nullptr) return bad(TPMLP_ERR_ARG, "grad: out of host memory");
+  Range few[2 * SMALL_TABLE];
+  Range* r = few;
+  if (count > SMALL_TABLE) {
+    r = new (std::nothrow) Range[2 * static_cast<size_t>(count)];
+    if (r == nullptr) return bad(TPMLP_ERR_ARG, "grad: out of host memory");
+  }
   size_t n = 0;
   for (int i = 0; i < count; ++i) {
     if (t[i].numel == 0) continue;
@@ -433,15 +441,8 @@ int check_apart(int count, const tp_grad_tensor* t) {
     r[n++] = {o, o + bytes, true};
     if (o != g) r[n++] = {g, g + bytes, false};
   }
-  std::sort(r, r + n, [](const Range& a, const Range& b) { return a.lo < b.lo; });
-  uintptr_t out_end = 0, any_end = 0;
-  bool ok = true;
-  for (size_t i = 0; i < n && ok; ++i) {
-    ok = r[i].lo >= out_end && (!r[i].out || r[i].lo >= any_end);
-    any_end = std::max(any_end, r[i].hi);
-    if (r[i].out) out_end = std::max(out_end, r[i].hi);
-  }
-  delete[] r;
+  const bool ok = apart(r, n);
+  if (r != few) delete[] r;
   return ok ? TPMLP_OK
             : bad(TPMLP_ERR_ARG, "grad: an out overlaps another tensor");
 }
@@ -498,6 +499,46 @@ cudaError_t launch_dependent(void (*kernel)(P...), int blocks, cudaStream_t s,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The three launches, with tables of N tensors.
+template <int N>
+int run(int count, const tp_grad_tensor* t, bool clip, double max_norm,
+        double eps, float* norm, double* part, cudaStream_t s) {
+  Table<N> T;
+  const int launches = std::max(1, (count + N - 1) / N);
+  auto table = [&](int k) {
+    return fill(&T, k * N, std::min(count, (k + 1) * N), CHUNK_BYTES, t, clip);
+  };
+  int slots = 0;
+  for (int k = 0; k < launches; ++k) {
+    TRY(table(k));
+    const int blocks =
+        std::max(1, static_cast<int>(std::min<unsigned>(T.chunks, BLOCKS)));
+    grad_squares<N><<<blocks, THREADS, 0, s>>>(T, part + slots);
+    TRY(cuda_rc(cudaGetLastError(), "grad_squares"));
+    slots += blocks;
+  }
+  float* c = reinterpret_cast<float*>(part + slots);
+  TRY(cuda_rc(launch_dependent(grad_norm_final, 1, s,
+                               static_cast<const double*>(part), slots, max_norm,
+                               eps, norm, clip ? c : nullptr),
+              "grad_norm_final"));
+  if (!clip) return TPMLP_OK;
+  for (int k = launches - 1; k >= 0; --k) {
+    if (launches > 1) TRY(table(k));
+    if (T.chunks == 0) continue;
+    const float* f = c;
+    if (k == launches - 1) {
+      TRY(cuda_rc(launch_dependent(grad_scale<N>, static_cast<int>(T.chunks), s,
+                                   T, f),
+                  "grad_scale"));
+    } else {   // (its predecessor does not write what this one waits for)
+      grad_scale<N><<<T.chunks, THREADS, 0, s>>>(T, f);
+      TRY(cuda_rc(cudaGetLastError(), "grad_scale"));
+    }
+  }
+  return TPMLP_OK;
+}
+
 int go(int count, const tp_grad_tensor* t, bool clip, double max_norm,
        double eps, float* norm, void* workspace, size_t bytes, void* stream) {
   TRY(check_tensors(count, t, clip));
@@ -511,54 +552,20 @@ int go(int count, const tp_grad_tensor* t, bool clip, double max_norm,
   int sms = 0;
   TRY(check_device(&sms));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // One cluster for up to 512 KB in up to 64 tensors (an empty list too).
+  double* part = static_cast<double*>(workspace);
+  if (count > SMALL_TABLE)
+    return run<TABLE>(count, t, clip, max_norm, eps, norm, part, s);
+  // One cluster for up to 512 KB (an empty list too).
   long long pieces = 0;
   for (int i = 0; i < count && pieces <= 2 * SMALL_WARPS; ++i)
     pieces += parts_of(t[i], SMALL_PIECE_BYTES);
-  if (count <= SMALL_TABLE && pieces <= 2 * SMALL_WARPS) {
-    Table<SMALL_TABLE> T;
-    TRY(fill(&T, 0, count, SMALL_PIECE_BYTES, t, clip));
-    grad_small<<<SMALL_BLOCKS, SMALL_THREADS, 0, s>>>(T, clip ? 1 : 0, max_norm,
-                                                      eps, norm);
-    return cuda_rc(cudaGetLastError(), "grad_small");
-  }
-  double* part = static_cast<double*>(workspace);
-  Table<TABLE> T;
-  const int launches = tables(count);
-  auto table = [&](int k) {
-    return fill(&T, k * TABLE, std::min(count, (k + 1) * TABLE), CHUNK_BYTES, t,
-                clip);
-  };
-  auto blocks = [&] {
-    return std::max(1, static_cast<int>(std::min<unsigned>(T.chunks, BLOCKS)));
-  };
-  int slots = 0;
-  for (int k = 0; k < launches; ++k) {
-    TRY(table(k));
-    grad_squares<<<blocks(), THREADS, 0, s>>>(T, part + slots);
-    TRY(cuda_rc(cudaGetLastError(), "grad_squares"));
-    slots += blocks();
-  }
-  if (!clip)
-    return cuda_rc(launch_dependent(grad_norm_final, 1, s,
-                                    static_cast<const double*>(part), slots,
-                                    norm),
-                   "grad_norm_final");
-  for (int k = launches - 1; k >= 0; --k) {
-    if (launches > 1) TRY(table(k));
-    const double* sums = part;
-    float* out = k == 0 ? norm : nullptr;
-    // behind another grad_scale there is nothing to overlap with
-    if (k == launches - 1) {
-      TRY(cuda_rc(launch_dependent(grad_scale, blocks(), s, T, sums, slots,
-                                   max_norm, eps, out),
-                  "grad_scale"));
-    } else {
-      grad_scale<<<blocks(), THREADS, 0, s>>>(T, sums, slots, max_norm, eps, out);
-      TRY(cuda_rc(cudaGetLastError(), "grad_scale"));
-    }
-  }
-  return TPMLP_OK;
+  if (pieces > 2 * SMALL_WARPS)
+    return run<SMALL_TABLE>(count, t, clip, max_norm, eps, norm, part, s);
+  Table<SMALL_TABLE> T;
+  TRY(fill(&T, 0, count, SMALL_PIECE_BYTES, t, clip));
+  grad_small<<<SMALL_BLOCKS, SMALL_THREADS, 0, s>>>(T, clip ? 1 : 0, max_norm,
+                                                    eps, norm);
+  return cuda_rc(cudaGetLastError(), "grad_small");
 }
 
 }  // namespace
@@ -567,7 +574,8 @@ extern "C" {
 
 size_t tp_grad_workspace_bytes(int count) {
   if (count < 0) return 0;
-  return sizeof(double) * BLOCKS * static_cast<size_t>(tables(count));
+  // the blocks' sums and the factor
+  return sizeof(double) * (BLOCKS * static_cast<size_t>(tables(count)) + 2);
 }
 
 int tp_grad_norm(int count, const tp_grad_tensor* tensors, float* norm,

@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -135,6 +135,12 @@ void check(int status, const char* what) {
   throw Raised{};
 }
 
+// A new contiguous tensor on the current device and stream (at::empty without
+// its dispatch).
+at::Tensor make(at::IntArrayRef size, at::ScalarType type, const at::Device& d) {
+  return at::Tensor(at::detail::empty_cuda(size, type, d, std::nullopt));
+}
+
 // ---------------------------------------------------------------- heads --
 
 tp_heads heads_of(const char* name, const at::Tensor& x, long long d,
@@ -204,7 +210,7 @@ struct Heads {
         out[s].data_ptr();   // an output's own memory
         continue;
       }
-      out[s] = at::empty(in[s]->sizes(), in[s]->options());
+      out[s] = make(in[s]->sizes(), in[s]->scalar_type(), in[s]->device());
       vout[s] = heads_of(names[s], out[s], d);
     }
   }
@@ -338,12 +344,11 @@ PyObject* norm_backward(PyObject* const* a) {
   if (params < 0) throw Raised{};
   if (params) {
     const char* names[4] = {"dq_gamma", "dq_beta", "dk_gamma", "dk_beta"};
-    const auto f32 = dq.options().dtype(at::kFloat);
     for (int i = 0; i < (h.in[1] != nullptr ? 4 : 2); ++i) {
       if (i % 2 == 1 && n.norm != TPQK_LAYERNORM) continue;
       PyObject* given = a[16 + i];
       if (given == Py_None) {
-        grad[i] = at::empty({d}, f32);
+        grad[i] = make({d}, at::kFloat, dq.device());
         gp[i] = grad[i].data_ptr<float>();
       } else {
         gp[i] = param_of(names[i], given, d, dq);
@@ -353,7 +358,7 @@ PyObject* norm_backward(PyObject* const* a) {
     // a workspace of this call alone: calls on several streams, and captured
     // graphs, share no partial sums
     bytes = lib.norm_workspace_bytes(handle);
-    ws = at::empty({static_cast<int64_t>(bytes)}, dq.options().dtype(at::kByte));
+    ws = make({static_cast<int64_t>(bytes)}, at::kByte, dq.device());
   }
   const tp_qk_norm_grads g = {gp[0], gp[1], gp[2], gp[3]};
   void* wp = ws.defined() ? ws.data_ptr() : nullptr;
@@ -413,13 +418,11 @@ PyObject* grads(PyObject* const* a) {
     t.out = o.data_ptr();
   }
   Place place(dev, a[5]);
-  const auto options = at::TensorOptions().device(dev);
-  const at::Tensor norm = at::empty({}, options.dtype(at::kFloat));
+  const at::Tensor norm = make({}, at::kFloat, dev);
   const int count = static_cast<int>(n);
   const size_t bytes = lib.grad_workspace_bytes(count);
   // of this call alone, as above
-  const at::Tensor ws =
-      at::empty({static_cast<int64_t>(bytes)}, options.dtype(at::kByte));
+  const at::Tensor ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
   float* np = norm.data_ptr<float>();
   void* wp = ws.data_ptr();
   check(without_gil([&] {
