@@ -8,8 +8,13 @@
 // (programmatic dependent launch), and the last loads its chunks before it
 // waits for the factor.
 //
-// A few short tensors are done by one launch of one cluster of eight blocks,
-// which exchange their sums through distributed shared memory.
+// Up to 512 KB in up to 64 tensors are done by one launch of one cluster of eight
+// blocks, which exchange their sums through distributed shared memory: 4 KB 4.2 us
+// (three launches: 5.7), 256 KB 5.0 (6.2), 500 KB 6.0 (6.7).
+//
+// GB300: 1.26 GB of fp32 into other tensors in 546 us (1.26 GB read for the norm at
+// 7.1 TB/s, then read and written at 6.8 TB/s; the floor of one read and one write is
+// 370), 50 MB in 25.4 us (floor 14.8), 8 MB in 7.9.
 #include <algorithm>
 
 #include "host_common.cuh"
@@ -27,7 +32,8 @@ constexpr int THREADS = 256;
 constexpr int BLOCKS = 608;            // four on each of the 152 SMs
 constexpr int CHUNK_BYTES = 16 * BATCH * THREADS;
 // Tensors of one launch: the table travels as a kernel parameter (16 KB; one of
-// SMALL_TABLE, 2 KB, where that is enough).
+// SMALL_TABLE, 2 KB, where that is enough: 500 KB in 8 tensors 6.7 us, with the
+// large one 6.9).
 constexpr int TABLE = 512;
 
 // One cluster: pieces of one warp's batch of SMALL_BATCH vectors a lane.

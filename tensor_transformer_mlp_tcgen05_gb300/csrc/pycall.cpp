@@ -141,6 +141,16 @@ at::Tensor make(at::IntArrayRef size, at::ScalarType type, const at::Device& d) 
   return at::Tensor(at::detail::empty_cuda(size, type, d, std::nullopt));
 }
 
+// Row i of a new contiguous [n, d] tensor, as a tensor of its own.
+at::Tensor row_of(const at::Tensor& all, int64_t i) {
+  auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(all.storage()),
+                                                all.key_set(), all.dtype());
+  const int64_t d = all.size(1);
+  t->set_storage_offset(i * d);
+  t->set_sizes_contiguous(d);
+  return at::Tensor(std::move(t));
+}
+
 // ---------------------------------------------------------------- heads --
 
 tp_heads heads_of(const char* name, const at::Tensor& x, long long d,
@@ -344,11 +354,13 @@ PyObject* norm_backward(PyObject* const* a) {
   if (params < 0) throw Raised{};
   if (params) {
     const char* names[4] = {"dq_gamma", "dq_beta", "dk_gamma", "dk_beta"};
+    at::Tensor all;   // those that are made new: one allocation
     for (int i = 0; i < (h.in[1] != nullptr ? 4 : 2); ++i) {
       if (i % 2 == 1 && n.norm != TPQK_LAYERNORM) continue;
       PyObject* given = a[16 + i];
       if (given == Py_None) {
-        grad[i] = make({d}, at::kFloat, dq.device());
+        if (!all.defined()) all = make({4, d}, at::kFloat, dq.device());
+        grad[i] = row_of(all, i);
         gp[i] = grad[i].data_ptr<float>();
       } else {
         gp[i] = param_of(names[i], given, d, dq);

@@ -21,6 +21,20 @@
 //           written in bits of 4, 2 or 1 elements, a unit's bits lying `units`
 //           apart so that neighbouring lanes touch neighbouring bits.
 //
+// 8192 tokens, bf16, 201 MB in and out (floor 30 us; gradient 45 us), GB300, us:
+//                              rotation   RMS norm   its gradient
+//   24 + 24 heads of 128  OWN       32.4       35.0      51.2
+//                      PIECES       33.3       37.6      60.1
+//                        BITS       51.7       65.0     101.0
+//   32 + 32 heads of 96 PIECES      35.0       44.4      67.9
+//                        BITS       57.8       73.0     114.9
+//   (with 48 of the 96 rotated, lanes copying their own vectors, which are then
+//   no whole sectors, took 43.7 for the rotation, PIECES 34.9)
+//
+// What bounds it: memory, where heads fill lanes exactly; instruction issue
+// elsewhere (about 180 a step in the norm, half the issue slots used at four
+// blocks an SM, which the coefficients' registers allow).
+//
 // Angles: a frequency is held as turns per position in 64-bit fixed point
 // (2^-64 of a turn), so position times frequency modulo one turn is one
 // integer product; its upper 32 bits, as a signed fraction, go to sincospif.
@@ -696,6 +710,11 @@ struct Ring {
 };
 
 // -------------------------------------------------------------- forward --
+// GPT-3-13B-shaped layer (8192 tokens, 40 + 40 heads of 128, bf16, 336 MB in and
+// out): rotation 50.7 us, 6.6 TB/s; norm and rotation 51.8 us, 6.5 TB/s.  Before:
+// one row a lane loaded when it was needed, 61 and 71 us; with the ring, one step
+// at a time, 50.9 and 52.4.
+//
 // What a lane multiplies a row's unit by: y_a = rstd (a ca + b sb) + za, y_b =
 // rstd (a sa + b cb) + zb, with gamma folded into the rotation and beta rotated.
 template <int V>
@@ -736,7 +755,7 @@ __device__ __forceinline__ void load_turn(const Args& p, const Side& sd,
 }
 
 template <class T, Kind KIND, int NORM, bool INTER, int LEN>
-__global__ void __launch_bounds__(THREADS, 4)
+__global__ void __launch_bounds__(THREADS, NORM == 0 && !is_bits(KIND) ? 5 : 4)
     qk_rows_forward(const __grid_constant__ Args p) {
   // Steps computed at a time (two rows' chains of sums then share the issue slots
   // and the lane's coefficients), and steps ahead that are being copied, one
@@ -826,12 +845,19 @@ __global__ void __launch_bounds__(THREADS, 4)
       }
 #pragma unroll
       for (int k = 0; k < AT_ONCE; ++k) {
-        // the rotation does not wait for the norm's sum
+        // The rotation does not wait for the norm's sum.  (Values that do not
+        // turn have nothing to do with one another: an infinity among them must
+        // not meet another's zero sine.)
         Pairs<V> y;
-        mul<V>(y.a, x[k].b, t.sb);
-        mul<V>(y.b, x[k].b, t.cb);
-        fma<V>(y.a, x[k].a, t.ca, y.a);
-        fma<V>(y.b, x[k].a, t.sa, y.b);
+        if (un.turns) {
+          mul<V>(y.a, x[k].b, t.sb);
+          mul<V>(y.b, x[k].b, t.cb);
+          fma<V>(y.a, x[k].a, t.ca, y.a);
+          fma<V>(y.b, x[k].a, t.sa, y.b);
+        } else {
+          mul<V>(y.a, x[k].a, t.ca);
+          mul<V>(y.b, x[k].b, t.cb);
+        }
         if constexpr (NORM == TPQK_LAYERNORM) {
           fma<V>(y.a, y.a, scale[k], t.za);
           fma<V>(y.b, y.b, scale[k], t.zb);
@@ -856,7 +882,11 @@ __global__ void __launch_bounds__(THREADS, 4)
 //   xh = rstd e,  dgamma += (rstd g) e,  dbeta += g,
 //   dx = (rstd g) gamma - (rstd^3 sum(e u) / d) e [- rstd mean(u)].
 // Persistent blocks, so that a lane sums its unit's parameter gradients over
-// all its rows in registers; a block takes q's tasks or k's.
+// all its rows in registers; a block takes q's tasks or k's.  Four blocks an SM:
+// with three (more registers) the LayerNorm gradient of 8192 tokens of 24 + 24
+// heads of 128 takes 72 us instead of 60.
+// GPT-3-13B-shaped layer, RMS: 79.5 us with the sums, 503 MB, 6.3 TB/s (177 with
+// rows loaded when they were needed).
 template <class T, Kind KIND, int NORM, bool INTER, int LEN>
 __global__ void __launch_bounds__(THREADS, 4)
     qk_rows_backward(const __grid_constant__ Args p) {
@@ -923,12 +953,15 @@ __global__ void __launch_bounds__(THREADS, 4)
         xring.read(s, e);
         copy();
         // R^T (sa carries the opposite direction's sign)
-        float t[V];
-        mul<V>(t, dy.b, -1.f);
-        mul<V>(g.a, t, sa);
-        fma<V>(g.a, dy.a, c, g.a);
-        mul<V>(g.b, dy.b, c);
-        fma<V>(g.b, dy.a, sa, g.b);
+        g = dy;
+        if (un.turns) {
+          float t[V];
+          mul<V>(t, dy.b, -1.f);
+          mul<V>(g.a, t, sa);
+          fma<V>(g.a, dy.a, c, g.a);
+          mul<V>(g.b, dy.b, c);
+          fma<V>(g.b, dy.a, sa, g.b);
+        }
       }
       if constexpr (is_bits(KIND)) {   // rows past the last head
         if (h + ln.row >= heads) {

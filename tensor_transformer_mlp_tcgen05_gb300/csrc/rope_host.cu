@@ -338,12 +338,16 @@ int steps_per_task(int steps, int tokens, long long want, int most) {
   return static_cast<int>((steps + segs - 1) / segs);
 }
 
-// Forward: tokens are split until 12 warps a SM have work, and into tasks of at
-// most 16 steps.
+// A task's start (angles, coefficients, first loads) costs about as much as two
+// steps.  Forward: tokens are split until 12 warps a SM have work (2047 tokens of
+// 14 steps: 16.6 us whole, 17.5 in halves, 20.2 in fifths), and into tasks of at
+// most 16 steps (4096 tokens of 56 steps: 82.6 us whole, 73.2 in halves, 71.9 in
+// thirds; 8192 of 20: 54.8 whole, 52.2 in halves).
 constexpr long long FORWARD_TASKS = 152 * 12;
 constexpr int FORWARD_STEPS = 16;
-// Backward: until the blocks that stay have a step for every warp, and into
-// tasks of at most 8 steps.
+// Backward: until the resident blocks have a task for every warp, and into tasks
+// of at most 8 steps (8192 tokens of 10 steps: 82.8 us whole, 79.5 in halves, 81.2
+// in quarters).
 constexpr long long BACKWARD_TASKS = 1LL * qk::BWD_BLOCKS * qk::WARPS;
 constexpr int BACKWARD_STEPS = 8;
 

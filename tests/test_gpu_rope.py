@@ -187,8 +187,9 @@ def test_norm_gradients(d, r, inter, dtype, norm):
 
 @pytest.mark.parametrize("layout", ["shards", "fused", "major", "shifted"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_strided_views(layout, dtype):
-    T, H, d, r = 130, 6, 96, 48
+@pytest.mark.parametrize("d,r", [(96, 48), (64, 64), (7, 6), (128, 2)])
+def test_strided_views(layout, dtype, d, r):
+    T, H = 130, 6
     q, k = make(T, H, H, d, dtype, 11, layout)
     dq, dk = make(T, H, H, d, dtype, 12, layout)
     rope = RotaryEmbedding(d, rotary_dim=r)
@@ -413,6 +414,54 @@ def test_values_that_are_not_finite_stay_in_their_row():
         assert torch.equal(c[0][rows], n[0][rows])
         assert torch.equal(c[1], n[1])
         assert not torch.isfinite(n[0][3, 2]).all()
+
+
+@pytest.mark.parametrize("d,r", [(128, 64), (96, 48), (128, 32), (100, 50),
+                                 (64, 0), (72, 18)])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_values_that_are_not_finite_stay_with_their_pair(d, r, inter, bad):
+    """One bad value at a time: the rotation makes its pair bad (or, past r, the
+    value alone), the RMS norm the same (the others become zero beside an
+    infinity, and are not numbers beside a NaN), as the formula has it."""
+    q = torch.ones((d, 1, d), dtype=torch.bfloat16, device="cuda")
+    i = torch.arange(d, device="cuda")
+    q[i, 0, i] = bad                       # token t: element t
+    rope = RotaryEmbedding(d, rotary_dim=r, interleaved=inter)
+    f = torch.tensor(rope.frequencies()[0], device="cuda")
+    ang = (i + 1)[:, None] * f
+
+    def rotate(x, sign=1.0):
+        x = x[:, 0].double()
+        c, s = torch.cos(ang), sign * torch.sin(ang)
+        a, b = ((x[:, 0:r:2], x[:, 1:r:2]) if inter
+                else (x[:, :r // 2], x[:, r // 2:r]))
+        y = x.clone()
+        ya, yb = a * c - b * s, a * s + b * c
+        if inter:
+            y[:, 0:r:2], y[:, 1:r:2] = ya, yb
+        else:
+            y[:, :r // 2], y[:, r // 2:r] = ya, yb
+        return y
+
+    def kinds(t):
+        return torch.isnan(t), torch.isposinf(t), torch.isneginf(t)
+
+    y, _ = rope.forward(q, offset=1)
+    for a, b in zip(kinds(y[:, 0]), kinds(rotate(q))):
+        assert torch.equal(a, b)
+    op = QKNormRotary(d, rotary=rope)
+    y, _ = op.forward(q, offset=1)
+    x = q.float()
+    want = rotate(x * torch.rsqrt((x * x).mean(-1, keepdim=True) + op.eps))
+    assert torch.equal(torch.isnan(y[:, 0]), torch.isnan(want))
+    # the gradient of beta: a bad value of dy reaches its pair's columns only
+    op = QKNormRotary(d, norm="layer", rotary=rope)
+    x, _ = make(1, 1, 1, d, torch.bfloat16, d)
+    for t in (0, max(r - 1, 0), min(r, d - 1), d - 1):
+        g = op.backward(q[t:t + 1], None, x, None, offset=t + 1)
+        want = rotate(q, -1.0)[t]
+        assert torch.equal(torch.isfinite(g["dq_beta"]), torch.isfinite(want))
 
 
 def test_rows_of_zeros():
