@@ -285,6 +285,8 @@ __device__ __forceinline__ double total_norm(const double* part, int slots) {
 __global__ void __launch_bounds__(THREADS)
     grad_norm_final(const double* part, int slots, double max_norm, double eps,
                     float* norm, float* c) {
+  // grad_scale's blocks may come up and load (they wait for this one's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const double n = total_norm(part, slots);
   if (threadIdx.x == 0) {
     *norm = static_cast<float>(n);
