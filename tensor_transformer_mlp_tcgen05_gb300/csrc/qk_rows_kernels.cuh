@@ -711,9 +711,10 @@ struct Ring {
 
 // -------------------------------------------------------------- forward --
 // GPT-3-13B-shaped layer (8192 tokens, 40 + 40 heads of 128, bf16, 336 MB in and
-// out): rotation 50.7 us, 6.6 TB/s; norm and rotation 51.8 us, 6.5 TB/s.  Before:
-// one row a lane loaded when it was needed, 61 and 71 us; with the ring, one step
-// at a time, 50.9 and 52.4.
+// out): rotation 50.9 us, 6.6 TB/s; norm and rotation 52.0 us, 6.5 TB/s (61 and 71
+// with a row loaded when it was needed).  Two steps at a time, to share issue
+// slots, gave 50.7 and 51.8, but 37.4 instead of 34.1 for the LayerNorm of 24 +
+// 24 heads of 128 and 53 instead of 50 for 32 + 32 of 96: not kept.
 //
 // What a lane multiplies a row's unit by: y_a = rstd (a ca + b sb) + za, y_b =
 // rstd (a sa + b cb) + zb, with gamma folded into the rotation and beta rotated.
@@ -754,15 +755,22 @@ __device__ __forceinline__ void load_turn(const Args& p, const Side& sd,
   }
 }
 
+// Blocks an SM has to hold, and so registers a thread may take: five where that
+// spills nothing (RMS norm, 8192 tokens of 24 + 24 heads of 128: 33.2 us, with four
+// 34.3; of 32 + 32 heads of 96, where it spills, 61.5 and 44.6 with six and four).
+constexpr int forward_blocks(Kind kind, int norm) {
+  return (norm == 0 && !is_bits(kind)) || (norm == TPQK_RMSNORM && kind == OWN)
+             ? 5 : 4;
+}
+
 template <class T, Kind KIND, int NORM, bool INTER, int LEN>
-__global__ void __launch_bounds__(THREADS, NORM == 0 && !is_bits(KIND) ? 5 : 4)
+__global__ void __launch_bounds__(THREADS, forward_blocks(KIND, NORM))
     qk_rows_forward(const __grid_constant__ Args p) {
-  // Steps computed at a time (two rows' chains of sums then share the issue slots
-  // and the lane's coefficients), and steps ahead that are being copied, one
-  // group each.
-  constexpr int AT_ONCE = is_bits(KIND) ? 1 : 2;
-  constexpr int STAGES = is_bits(KIND) ? 4 : 8;
-  constexpr int AHEAD = is_bits(KIND) ? 3 : 5;
+  // Steps ahead that are being copied, one group each (GPT-3-13B-shaped layer, RMS:
+  // five 52.0 us, three 53.1; rows in PIECES are faster with three: 32 + 32 heads
+  // of 96 42.9 and 44.6).
+  constexpr int STAGES = KIND == OWN ? 8 : 4;
+  constexpr int AHEAD = KIND == OWN ? 5 : 3;
   using R = Ring<T, INTER, STAGES, KIND>;
   using U = typename R::Unit;
   constexpr int V = U::V;
@@ -815,64 +823,47 @@ __global__ void __launch_bounds__(THREADS, NORM == 0 && !is_bits(KIND) ? 5 : 4)
     Turn<V> t;
     load_turn<NORM>(p, sd, trig[warp], un, t);
 #pragma unroll 1
-    while (s < end) {
-      // (a second step past the end is computed for nothing)
-      const int used = min(AT_ONCE, end - s);
-      ring_wait<AHEAD - AT_ONCE>();
+    for (; s < end; ++s) {
+      ring_wait<AHEAD - 1>();
       ring.sync();
-      Pairs<V> x[AT_ONCE];
-#pragma unroll
-      for (int k = 0; k < AT_ONCE; ++k) ring.read(s + k, x[k]);
-#pragma unroll
-      for (int k = 0; k < AT_ONCE; ++k)
-        if (k < used) copy();
-      float scale[AT_ONCE];
+      Pairs<V> x;
+      ring.read(s, x);
+      copy();
+      float scale[1];
       if constexpr (NORM == TPQK_LAYERNORM) {
-        float m[AT_ONCE];
-#pragma unroll
-        for (int k = 0; k < AT_ONCE; ++k) m[k] = total<V>(x[k]);
+        float m[1] = {total<V>(x)};
         row_sum<LEN>(m, ln);
-#pragma unroll
-        for (int k = 0; k < AT_ONCE; ++k) un.centre(x[k], m[k] * p.inv_d);
+        un.centre(x, m[0] * p.inv_d);
       }
       if constexpr (NORM != 0) {
-#pragma unroll
-        for (int k = 0; k < AT_ONCE; ++k) scale[k] = dot<V>(x[k], x[k]);
+        scale[0] = dot<V>(x, x);
         row_sum<LEN>(scale, ln);
-#pragma unroll
-        for (int k = 0; k < AT_ONCE; ++k)
-          scale[k] = rsqrtf(fmaf(scale[k], p.inv_d, p.eps));
+        scale[0] = rsqrtf(fmaf(scale[0], p.inv_d, p.eps));
       }
-#pragma unroll
-      for (int k = 0; k < AT_ONCE; ++k) {
-        // The rotation does not wait for the norm's sum.  (Values that do not
-        // turn have nothing to do with one another: an infinity among them must
-        // not meet another's zero sine.)
-        Pairs<V> y;
-        if (un.turns) {
-          mul<V>(y.a, x[k].b, t.sb);
-          mul<V>(y.b, x[k].b, t.cb);
-          fma<V>(y.a, x[k].a, t.ca, y.a);
-          fma<V>(y.b, x[k].a, t.sa, y.b);
-        } else {
-          mul<V>(y.a, x[k].a, t.ca);
-          mul<V>(y.b, x[k].b, t.cb);
-        }
-        if constexpr (NORM == TPQK_LAYERNORM) {
-          fma<V>(y.a, y.a, scale[k], t.za);
-          fma<V>(y.b, y.b, scale[k], t.zb);
-        } else if constexpr (NORM != 0) {
-          mul<V>(y.a, y.a, scale[k]);
-          mul<V>(y.b, y.b, scale[k]);
-        }
-        if (k < used) ring.put(s + k, dst, h + k * p.rows, heads, y);
+      // The rotation does not wait for the norm's sum.  (Values that do not
+      // turn have nothing to do with one another: an infinity among them must
+      // not meet another's zero sine.)
+      Pairs<V> y;
+      if (un.turns) {
+        mul<V>(y.a, x.b, t.sb);
+        mul<V>(y.b, x.b, t.cb);
+        fma<V>(y.a, x.a, t.ca, y.a);
+        fma<V>(y.b, x.a, t.sa, y.b);
+      } else {
+        mul<V>(y.a, x.a, t.ca);
+        mul<V>(y.b, x.b, t.cb);
       }
+      if constexpr (NORM == TPQK_LAYERNORM) {
+        fma<V>(y.a, y.a, scale[0], t.za);
+        fma<V>(y.b, y.b, scale[0], t.zb);
+      } else if constexpr (NORM != 0) {
+        mul<V>(y.a, y.a, scale[0]);
+        mul<V>(y.b, y.b, scale[0]);
+      }
+      ring.put(s, dst, h, heads, y);
       ring.sync();
-#pragma unroll
-      for (int k = 0; k < AT_ONCE; ++k)
-        if (k < used) ring.flush(s + k, dst, h + k * p.rows, heads);
-      h += AT_ONCE * p.rows;
-      s += used;
+      ring.flush(s, dst, h, heads);
+      h += p.rows;
     }
   }
 }
