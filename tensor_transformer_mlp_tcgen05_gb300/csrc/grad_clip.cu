@@ -9,12 +9,12 @@
 // waits for the factor.
 //
 // Up to 512 KB in up to 64 tensors are done by one launch of one cluster of eight
-// blocks, which exchange their sums through distributed shared memory: 4 KB 4.2 us
-// (three launches: 5.7), 256 KB 5.0 (6.2), 500 KB 6.0 (6.7).
+// blocks, which exchange their sums through distributed shared memory: 4 KB 4.1 us
+// (three launches: 5.7), 256 KB 4.8 (6.2), 500 KB 5.8 (6.7).
 //
 // GB300: 1.26 GB of fp32 into other tensors in 546 us (1.26 GB read for the norm at
 // 7.1 TB/s, then read and written at 6.8 TB/s; the floor of one read and one write is
-// 370), 50 MB in 25.4 us (floor 14.8), 8 MB in 7.9.
+// 370), 50 MB in 24 us (floor 14.8), 8 MB in 7.5.
 #include <algorithm>
 
 #include "host_common.cuh"

@@ -23,17 +23,17 @@
 //
 // 8192 tokens, bf16, 201 MB in and out (floor 30 us; gradient 45 us), GB300, us:
 //                              rotation   RMS norm   its gradient
-//   24 + 24 heads of 128  OWN       32.4       35.0      51.2
-//                      PIECES       33.3       37.6      60.1
-//                        BITS       51.7       65.0     101.0
-//   32 + 32 heads of 96 PIECES      35.0       44.4      67.9
-//                        BITS       57.8       73.0     114.9
+//   24 + 24 heads of 128  OWN       32.8       33.5       51.5
+//                      PIECES       33.2       38.1       60.5
+//                        BITS       51.0       63.2      105.3
+//   32 + 32 heads of 96 PIECES      35.0       42.8       68.7
+//                        BITS       56.8       71.0      120.1
 //   (with 48 of the 96 rotated, lanes copying their own vectors, which are then
-//   no whole sectors, took 43.7 for the rotation, PIECES 34.9)
+//   no whole sectors, took 43.7 for the rotation, PIECES 34.7)
 //
 // What bounds it: memory, where heads fill lanes exactly; instruction issue
-// elsewhere (about 180 a step in the norm, half the issue slots used at four
-// blocks an SM, which the coefficients' registers allow).
+// elsewhere (half the issue slots are used at the four or five blocks an SM that
+// the coefficients' registers allow).
 //
 // Angles: a frequency is held as turns per position in 64-bit fixed point
 // (2^-64 of a turn), so position times frequency modulo one turn is one
