@@ -32,8 +32,14 @@ def grad_norm(tensors, stream=None) -> torch.Tensor:
 def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, out=None,
                    stream=None) -> torch.Tensor:
     """Scale all tensors by min(1, max_norm / (norm + eps)), in place or into
-    ``out`` (a list or dict of as many tensors), and return the norm they had,
-    as grad_norm.  A norm that is not finite is returned and scales nothing."""
+    ``out`` (a list of as many tensors, or for a dict a dict with its names), and
+    return the norm they had, as grad_norm.  A norm that is not finite is
+    returned and scales nothing."""
+    if isinstance(tensors, dict) and isinstance(out, dict):
+        missing = [n for n in tensors if n != "dX" and n not in out]
+        if missing:
+            raise ValueError(f"out has no {missing}")
+        out = [out[n] for n in tensors if n != "dX"]
     return B_.tensor_calls().grads(
         _listed(tensors), None if out is None else _listed(out), 1, max_norm,
         eps, stream)

@@ -88,6 +88,17 @@ def test_mixed_types_and_shapes_in_a_dict():
         assert close(t, w, t.dtype)
 
 
+def test_dicts_are_matched_by_name():
+    g = {"a": randn(50, 1), "dX": randn(7, 2), "b": randn(50, 3)}
+    out = {"b": torch.empty(50, device="cuda"), "a": torch.empty(50, device="cuda")}
+    clip_grad_norm(g, 1.0, out=out)
+    n = math.sqrt(float((g["a"].double() ** 2).sum() + (g["b"].double() ** 2).sum()))
+    for k in ("a", "b"):
+        assert close(out[k], f64(g[k]) * (1 / (n + 1e-6)), torch.float32)
+    with pytest.raises(ValueError):
+        clip_grad_norm(g, 1.0, out={"a": out["a"]})
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("shift", [1, 2, 3, 5])
 def test_tensors_off_16_bytes(dtype, shift):
