@@ -151,7 +151,8 @@ int tp_qk_norm_forward(tp_rope_handle* handle, int tokens, int dtype,
                        const tp_heads* k_out, const tp_positions* positions,
                        void* stream);
 
-/* Parameter gradients, [d] fp32 each, overwritten; each may be NULL. */
+/* Parameter gradients, [d] fp32 each, overwritten; each may be NULL; no two
+ * share memory (TPMLP_ERR_ARG). */
 typedef struct tp_qk_norm_grads {
   float* q_gamma;
   float* q_beta;   /* TPQK_LAYERNORM only */

@@ -201,6 +201,14 @@ int check_qk(const tp_attn_handle* H, const tp_attn_qk* qk,
     if (reinterpret_cast<uintptr_t>(params[i]) % 4 != 0 ||
         reinterpret_cast<uintptr_t>(grads[i]) % 4 != 0)
       return TPMLP_ERR_ALIGN;
+    for (int j = 0; j < i; ++j)
+      if (grads[i] != nullptr && grads[j] != nullptr &&
+          std::abs(static_cast<const float*>(grads[i]) -
+                   static_cast<const float*>(grads[j])) <
+              H->cfg.hidden / H->cfg.heads) {
+        set_detail_msg("two gradients of the norm share memory");
+        return TPMLP_ERR_ARG;
+      }
   }
   return TPMLP_OK;
 }

@@ -527,10 +527,14 @@ int tp_qk_norm_backward(tp_rope_handle* H, int tokens, int dtype,
   if (!has_k && (out[2] || out[3]))
     return bad(TPMLP_ERR_ARG, "norm: gradients of k without k");
   bool params = false;
-  for (float* p : out) {
-    if (reinterpret_cast<uintptr_t>(p) % 4 != 0)
+  for (int i = 0; i < 4; ++i) {
+    if (reinterpret_cast<uintptr_t>(out[i]) % 4 != 0)
       return bad(TPMLP_ERR_ALIGN, "norm: a gradient is not aligned");
-    params = params || p != nullptr;
+    params = params || out[i] != nullptr;
+    for (int j = 0; j < i; ++j)
+      if (out[i] != nullptr && out[j] != nullptr &&
+          std::llabs(out[i] - out[j]) < H->d)
+        return bad(TPMLP_ERR_ARG, "norm: two gradients share memory");
   }
   if (params && tokens > 0) {
     if (workspace == nullptr) return bad(TPMLP_ERR_ARG, "null workspace");

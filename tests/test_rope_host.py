@@ -249,6 +249,9 @@ def test_norm_refusals(lib, handle):
     assert norm_calls(lib, handle, ok, G(FAKE + 1))[1] == ALIGN
     assert norm_calls(lib, handle, N(1, 1e-6), G(None, FAKE * 10))[1] == ARG
     assert norm_calls(lib, handle, ok, G(None, None, FAKE), k=False)[1] == ARG
+    assert norm_calls(lib, handle, ok, G(FAKE * 10, FAKE * 10))[1] == ARG
+    assert norm_calls(lib, handle, ok,
+                      G(FAKE * 10, None, FAKE * 10 + 252))[1] == ARG
     assert norm_calls(lib, handle, ok, g, ws=None)[1] == ARG
     assert norm_calls(lib, handle, ok, g, ws=FAKE * 8 + 8)[1] == ALIGN
     assert norm_calls(lib, handle, ok, g, nbytes=100)[1] == \
@@ -419,6 +422,7 @@ def test_attention_qk_arguments_are_refused_before_any_launch(lib):
         assert calls(Q(None, 0, None, FAKE)) == (ARG, ARG)
         assert calls(None, G(None, FAKE))[1] == ARG
         assert calls(None, G(FAKE + 2))[1] == ALIGN
+        assert calls(None, G(FAKE, None, FAKE))[1] == ARG
         assert lib.tp_attn_forward_qk(None, *[0] * 14) == ARG
     finally:
         B.tp_attn_destroy(h)
