@@ -99,10 +99,37 @@ bool same_view(const tp_heads& a, const tp_heads& b, int tokens) {
   return true;
 }
 
-// Whether two views may share an element (false only if they share none).
-// Views of one buffer with the same token stride are compared head by head
-// modulo that stride; that needs every head inside one stride and the heads in
-// rising order.
+// Two views with the same strides whose dimensions nest: whether an element of
+// one, at sum of i_n stride_n, is one of the other, `delta` further and at sum of
+// j_n stride_n.  What is left of delta after the outer dimensions has to come from
+// the inner ones, which reach less than one outer step: j_n - i_n is one of the
+// two quotients around it.  Dimensions in falling order of their strides.
+bool lattice_meets(long long delta, const Steps& a, const Steps& b, int n,
+                   int d) {
+  if (n == a.n) return delta > -d && delta < d;
+  const long long s = a.stride[n];
+  long long q = -(delta / s);   // delta + q s is the remainder
+  for (long long k = q - 1; k <= q + 1; ++k)
+    if (k > -a.count[n] && k < b.count[n] && std::llabs(delta + k * s) < s + d &&
+        lattice_meets(delta + k * s, a, b, n + 1, d))
+      return true;
+  return false;
+}
+
+void sort_falling(Steps* s) {
+  for (int i = 0; i < s->n; ++i)
+    for (int j = i + 1; j < s->n; ++j)
+      if (s->stride[j] > s->stride[i]) {
+        std::swap(s->stride[i], s->stride[j]);
+        std::swap(s->count[i], s->count[j]);
+      }
+}
+
+// Whether two views may share an element (false only if they share none): exact
+// for views with the same strides, as those of one buffer have; views with the
+// same token stride are compared head by head modulo that stride where every
+// head is inside it and the heads lie in rising order; others of one stretch of
+// memory are taken to overlap.
 bool may_overlap(const tp_heads& a, const tp_heads& b, int tokens, int d,
                  int size) {
   const char* pa = static_cast<const char*>(a.data);
@@ -110,16 +137,30 @@ bool may_overlap(const tp_heads& a, const tp_heads& b, int tokens, int d,
   if (pa + extent(a, tokens, d) * size <= pb ||
       pb + extent(b, tokens, d) * size <= pa)
     return false;
+  if ((pb - pa) % size != 0) return true;
+  long long delta = (pb - pa) / size;
+  if (rows_apart(a, tokens, d) && rows_apart(b, tokens, d)) {
+    Steps sa = steps_of(a, tokens), sb = steps_of(b, tokens);
+    sort_falling(&sa);
+    sort_falling(&sb);
+    bool same = sa.n == sb.n;
+    for (int i = 0; same && i < sa.n; ++i) same = sa.stride[i] == sb.stride[i];
+    // (nested for the larger of the two counts, too)
+    long long inside = d;
+    for (int i = sa.n - 1; same && i >= 0; --i) {
+      same = sa.stride[i] >= inside;
+      inside += sa.stride[i] * (std::max(sa.count[i], sb.count[i]) - 1);
+    }
+    if (same) return lattice_meets(delta, sa, sb, 0, d);
+  }
   const long long ts = tokens > 1 ? a.token_stride : 0;
   if (tokens > 1 && a.token_stride != b.token_stride) return true;
-  if ((pb - pa) % size != 0) return true;
   auto rising = [&](const tp_heads& v) {
     for (int j = 1; j < v.heads; ++j)
       if (head_at(v, j) < head_at(v, j - 1)) return false;
     return ts == 0 || head_at(v, v.heads - 1) + d <= ts;
   };
   if (!rising(a) || !rising(b)) return true;
-  long long delta = (pb - pa) / size;
   if (ts > 0) delta = ((delta % ts) + ts) % ts;
   // b's heads lie delta (and, wrapped into the token before, delta - ts) after
   // a's

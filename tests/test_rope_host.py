@@ -208,6 +208,16 @@ def test_q_and_k_of_one_buffer(lib, handle):
     # head-major, [H, T, d]
     major = lambda p: heads(p, ts=64, hs=16 * 64)
     accepted(lib, handle, major(FAKE), major(2 * FAKE))
+    # head-major with q and k side by side, [H, T, 2, d], in place
+    both = lambda i: heads(FAKE + i * 64 * 2, ts=128, hs=16 * 128)
+    accepted(lib, handle, both(0), both(0), both(1), both(1))
+    refused(lib, handle, both(0), both(0), both(1),
+            heads(FAKE + 32 * 2, ts=128, hs=16 * 128), code=B.TPMLP_ERR_ARG)
+    # more query than key heads in one buffer, [T, Hq + Hk, d]
+    few = lambda j, n: heads(FAKE + j * 64 * 2, H=n, ts=6 * 64)
+    accepted(lib, handle, few(0, 4), few(0, 4), few(4, 2), few(4, 2))
+    refused(lib, handle, few(0, 4), few(0, 4), few(3, 2), few(3, 2),
+            code=B.TPMLP_ERR_ARG)
     # the last token's tail reaches into the next token's head
     refused(lib, handle, heads(FAKE, ts=300, hs=70), heads(FAKE + 2 * 290,
             ts=300, hs=70), code=B.TPMLP_ERR_ARG)
@@ -217,6 +227,39 @@ def test_views_of_any_alignment_and_broadcast_inputs_pass(lib, handle):
     accepted(lib, handle, heads(FAKE + 2, ts=257), heads(2 * FAKE + 6, ts=259))
     accepted(lib, handle, heads(FAKE, ts=0), heads(2 * FAKE))
     accepted(lib, handle, heads(FAKE, hs=0, ts=64), heads(2 * FAKE))
+
+
+def test_overlap_against_brute_force(lib, handle):
+    """Two outputs of random strides in one buffer: refused exactly when an
+    element is written twice, for views with the same strides; never accepted
+    wrongly for others."""
+    if torch.cuda.is_available():
+        pytest.skip("stand-in addresses must not reach a GPU")
+    g = np.random.default_rng(0)
+    d = 64
+    seen = {True: 0, False: 0}
+    for n in range(3000):
+        T, groups, group = (int(g.integers(1, 4)) for _ in range(3))
+        order = g.permutation(3)
+        strides, inside = [0, 0, 0], d + int(g.integers(0, 2)) * 64
+        for dim in order:                       # nested in a random order
+            strides[dim] = inside
+            inside = inside * (T, groups, group)[dim] + \
+                int(g.integers(0, 3)) * 64
+        ts, gs, hs = strides
+        shift = int(g.integers(-inside, inside))
+        if g.random() < 0.5:
+            shift -= shift % 64
+        v = lambda at: B.tp_heads(FAKE * 64 + 2 * at, ts, gs, hs,
+                                  groups * group, group)
+        rows = lambda at: {at + t * ts + i * gs + j * hs for t in range(T)
+                           for i in range(groups) for j in range(group)}
+        meets = any(abs(x - y) < d for x in rows(0) for y in rows(shift))
+        k = heads(FAKE, H=groups * group, T=T)
+        rc = apply(lib, handle, k, v(0), k, v(shift), T=T)
+        assert (rc == B.TPMLP_ERR_ARG) == meets, (T, strides, shift, rc)
+        seen[meets] += 1
+    assert min(seen.values()) > 500, seen
 
 
 def norm_calls(lib, handle, n, grads=None, ws=FAKE * 8, nbytes=None, T=16,
