@@ -6,9 +6,10 @@
  *     norm = sqrt(sum over all tensors and elements of g^2)
  *     c    = min(1, max_norm / (norm + eps)),   out = c g
  *
- * A norm that is not finite (an infinity or NaN among the gradients) is
- * reported as it is and scales nothing: c = 1, so that a training step can
- * read the norm and be skipped with its gradients as they were.
+ * A norm that is not finite in fp32 (an infinity or NaN among the gradients, or
+ * a norm beyond 3.4e38) is reported as infinity or NaN and scales nothing: c =
+ * 1, so that a training step can read the norm and be skipped with its
+ * gradients as they were.
  *
  * Squares are summed in fp32 over at most 64 elements of a thread (a short set:
  * then over the 32 threads of a warp), beyond that in fp64, in a fixed order (bit-identical repeats); runs of elements whose

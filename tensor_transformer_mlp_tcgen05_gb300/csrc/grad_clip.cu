@@ -233,10 +233,11 @@ __device__ __forceinline__ double block_total(double v) {
   return threadIdx.x < 32 ? warp_total(all, THREADS) : 0.0;
 }
 
-// min(1, max_norm / (norm + eps)); 1 for a norm that is not finite.
+// min(1, max_norm / (norm + eps)); 1 for a norm that is not finite as it is
+// reported, in fp32.
 __device__ __forceinline__ float factor(double n, double max_norm, double eps) {
   const double ratio = max_norm / (n + eps);
-  return isfinite(n) && ratio < 1.0 ? static_cast<float>(ratio) : 1.f;
+  return isfinite(static_cast<float>(n)) && ratio < 1.0 ? static_cast<float>(ratio) : 1.f;
 }
 
 template <int N>

@@ -140,6 +140,17 @@ def test_a_norm_that_is_not_finite_scales_nothing(bad, inplace):
         assert same.all()
 
 
+def test_a_norm_beyond_fp32_scales_nothing():
+    """3e38 sqrt(5000) is finite in fp64 only: reported as infinity."""
+    for g in (torch.full((5000,), 3e38, device="cuda"),
+              torch.full((300000,), 3e38, device="cuda")):
+        keep, out = g.clone(), torch.zeros_like(g)
+        assert float(clip_grad_norm([g], 1.0, out=[out])) == math.inf
+        assert torch.equal(out, keep)
+        assert float(clip_grad_norm([g], 1.0)) == math.inf
+        assert torch.equal(g, keep)
+
+
 def test_limits_of_max_norm():
     g = randn(1000, 1)
     keep = g.clone()
