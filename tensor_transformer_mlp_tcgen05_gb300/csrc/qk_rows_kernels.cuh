@@ -978,7 +978,8 @@ __global__ void __launch_bounds__(THREADS, 4)
       }
       row_sum<LEN>(q, ln);
       const float rstd = rsqrtf(fmaf(q[0], p.inv_d, p.eps));
-      const float k = -(rstd * rstd) * (q[1] * rstd * p.inv_d);
+      // (in this order: rstd^2 alone may overflow where the sum is zero)
+      const float k = -(q[1] * rstd * p.inv_d * rstd * rstd);
       if constexpr (NORM == TPQK_LAYERNORM) {
         add<V>(dbet.a, g.a);
         add<V>(dbet.b, g.b);

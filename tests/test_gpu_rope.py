@@ -480,6 +480,21 @@ def test_rows_of_zeros():
         assert (g["dq_gamma"] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 96, 10])
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+def test_rows_of_zeros_with_the_smallest_eps(dtype, d, norm):
+    """eps = 2^-130: rstd = 2^65, whose square is past fp32's range."""
+    q = torch.zeros((4, 2, d), dtype=dtype, device="cuda")
+    g = QKNormRotary(d, norm=norm, eps=2.0 ** -130).backward(
+        torch.ones_like(q), None, q, None)
+    want = 2.0 ** 65 if norm == "rms" else 0.0
+    # rsqrt is off by two steps at most; the mean of d ones by d / 2 of them
+    assert torch.allclose(g["dq"].double(), torch.full_like(g["dq"], want).double(),
+                          rtol=HALF_STEP[dtype] + (2 + d) * U, atol=2.0 ** 65 * (2 + d) * U)
+    assert (g["dq_gamma"] == 0).all()
+
+
 def test_offsets_past_32_bits():
     # token stride 2^26 elements: token 33's row starts past 2^31 elements
     T, H, d = 36, 2, 64
