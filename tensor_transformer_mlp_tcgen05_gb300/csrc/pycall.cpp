@@ -355,9 +355,14 @@ PyObject* norm_backward(PyObject* const* a) {
   if (params) {
     const char* names[4] = {"dq_gamma", "dq_beta", "dk_gamma", "dk_beta"};
     at::Tensor all;   // those that are made new: one allocation
-    for (int i = 0; i < (h.in[1] != nullptr ? 4 : 2); ++i) {
-      if (i % 2 == 1 && n.norm != TPQK_LAYERNORM) continue;
+    for (int i = 0; i < 4; ++i) {
       PyObject* given = a[16 + i];
+      if ((i % 2 == 1 && n.norm != TPQK_LAYERNORM) ||
+          (i >= 2 && h.in[1] == nullptr)) {
+        if (given != Py_None)
+          throw Refused{std::string("out: this call has no ") + names[i]};
+        continue;
+      }
       if (given == Py_None) {
         if (!all.defined()) all = make({4, d}, at::kFloat, dq.device());
         grad[i] = row_of(all, i);

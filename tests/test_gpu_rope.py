@@ -577,6 +577,7 @@ def test_refusals_of_the_wrappers():
     q, k = make(8, 4, 2, 64, torch.bfloat16, 95)
     rope = RotaryEmbedding(64)
     op = QKNormRotary(64, rotary=rope)
+    one = torch.ones(64, device="cuda")
     bad = [
         lambda: rope.forward(q.cpu(), k),
         lambda: rope.forward(q.half(), k.half()),
@@ -597,6 +598,8 @@ def test_refusals_of_the_wrappers():
         lambda: op.backward(q, None, q, k),
         lambda: op.backward(q, k, q, None),
         lambda: op.backward(q, k, q[:4], k),
+        lambda: op.backward(q, k, q, k, out={"dq_beta": one}),
+        lambda: op.backward(q, None, q, None, out={"dk_gamma": one}),
     ]
     for call in bad:
         with pytest.raises(ValueError):
