@@ -12,10 +12,10 @@
  * gradients as they were.
  *
  * Squares are summed in fp32 over at most 64 elements of a thread (a short set:
- * then over the 32 threads of a warp), beyond that in fp64, in a fixed order (bit-identical repeats); runs of elements whose
- * squares would leave fp32's range are squared in fp64, so every finite
- * gradient has its right norm (rounded to fp32 once).  c is
- * rounded to fp32, c g to the gradient's type.
+ * then over the 32 threads of a warp), beyond that in fp64, in a fixed order
+ * (bit-identical repeats); runs of elements whose squares would leave fp32's
+ * range are squared in fp64, so every finite gradient has its right norm
+ * (rounded to fp32 once).  c is rounded to fp32, c g to the gradient's type.
  */
 #ifndef TP_GRAD_H_
 #define TP_GRAD_H_
@@ -53,7 +53,7 @@ int tp_grad_norm(int count, const tp_grad_tensor* tensors, float* norm,
  * or memory that overlaps no grad and no other out (TPMLP_ERR_ARG: the same
  * tensor listed twice would be scaled twice).
  *   max_norm  >= 0 (infinity: no clipping);  eps >= 0, finite
- *   norm      as tp_grad_norm (required). */
+ *   norm      as tp_grad_norm (required); no part of a tensor. */
 int tp_grad_clip(int count, const tp_grad_tensor* tensors, double max_norm,
                  double eps, float* norm, void* workspace,
                  size_t workspace_bytes, void* stream);

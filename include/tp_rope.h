@@ -24,12 +24,13 @@
  * Conventions
  * -----------
  * - Element types: queries and keys bf16 (TPMLP_BF16) or fp32 (TPMLP_FP32),
- *   gamma, beta and their gradients fp32; all arithmetic fp32, angles exact
- *   to 2^-33 of a turn at every position (64-bit fixed point), one rounding
- *   to the element type.
+ *   gamma, beta and their gradients fp32; all arithmetic fp32, one rounding
+ *   to the element type.  Angles are made in 64-bit fixed point, within 2^-33
+ *   of a turn at every position, then rounded to fp32.
  * - Pointers are DEVICE pointers the caller owns (tp_rope_config's inv_freq
  *   and the structs are host memory, read during the call only); the library
  *   never allocates device memory.  Calls only enqueue work on `stream`.
+ *   Positions, parameters and workspace share no memory with an output.
  *   Data pointers need the alignment of their element type only; 16-byte
  *   aligned rows are read fastest.  Every function returns a status code and
  *   touches no output when argument validation fails.
@@ -89,10 +90,11 @@ int tp_rope_frequencies(const tp_rope_handle* handle, double* inv_freq,
 
 /* Heads of a tensor: element c of head j of token t is at data[t *
  * token_stride + (j / group) * group_stride + (j % group) * head_stride + c]
- * (strides in elements, >= 0 and below 4 GB each; d consecutive elements per head).  `group`
- * heads lie head_stride apart and groups group_stride apart: the shard-grouped
- * columns of tp_attn.h's QKV are group = H / t, group_stride = 3 h / t,
- * head_stride = d, token_stride = 3 h; a plain [T, H, d] tensor is group = H.
+ * (strides in elements, >= 0 and below 4 GB each; d consecutive elements per
+ * head).  `group` heads lie head_stride apart and groups group_stride apart: the
+ * shard-grouped columns of tp_attn.h's QKV are group = H / t, group_stride =
+ * 3 h / t, head_stride = d, token_stride = 3 h; a plain [T, H, d] tensor is group
+ * = H.
  * heads = 0 stands for no tensor.  An output's heads must not overlap one
  * another. */
 typedef struct tp_heads {
@@ -115,9 +117,9 @@ typedef struct tp_positions {
 } tp_positions;
 
 /* Rotate the heads of q and k (inverse = 1: the gradient, by the opposite
- * angles).  Each output is either the very view of its input (in place; the
- * elements from rot_dim on are then not touched) or shares no element with any
- * input or other output.  k may be NULL (then k_out too).
+ * angles).  Each output is either the very view of its input (in place; where
+ * both q and k are, the elements from rot_dim on are not touched) or shares no
+ * element with any input or other output.  k may be NULL (then k_out too).
  *   tokens  0 <= T <= 2^28 (T = 0 enqueues nothing)
  *   dtype   TPMLP_BF16 or TPMLP_FP32, of q and k
  * TPMLP_ERR_SHAPE: a head count that differs between input and output, a

@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(THREADS, 4)
   if (threadIdx.x == 0) part[blockIdx.x] = wide;
 }
 
-// Waits until the sums are there, and adds them.  (Every thread loads its own few first: one warp alone, load after load, took
-// 6 us for 608 of them.)
+// Waits until the sums are there, and adds them.  (Every thread loads its own few
+// first: one warp alone, load after load, took 6 us for 608 of them.)
 __device__ __forceinline__ double total_norm(const double* part, int slots) {
   __shared__ double norm;
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -713,8 +713,8 @@ struct Ring {
 // GPT-3-13B-shaped layer (8192 tokens, 40 + 40 heads of 128, bf16, 336 MB in and
 // out): rotation 50.9 us, 6.6 TB/s; norm and rotation 52.0 us, 6.5 TB/s (61 and 71
 // with a row loaded when it was needed).  Two steps at a time, to share issue
-// slots, gave 50.7 and 51.8, but 37.4 instead of 34.1 for the LayerNorm of 24 +
-// 24 heads of 128 and 53 instead of 50 for 32 + 32 of 96: not kept.
+// slots, gave 50.7 and 51.8, but for the LayerNorm 35.7 instead of 33.8 (40 + 40
+// heads of 64) and 55.2 instead of 51.4 (32 + 32 of 96): not kept.
 //
 // What a lane multiplies a row's unit by: y_a = rstd (a ca + b sb) + za, y_b =
 // rstd (a sa + b cb) + zb, with gamma folded into the rotation and beta rotated.

@@ -1,5 +1,5 @@
 // Host side of the query/key operators (tp_rope.h): frequencies, validation
-// of the views, the choice of the vector width and of the tasks.
+// of the views, the choice of the kind of rows and of the tasks.
 #include <algorithm>
 
 #include "host_common.cuh"
@@ -271,7 +271,7 @@ qk::View kernel_view(const tp_heads& v, int size) {
 // r and every distance are whole ones, else in bits of as many elements as divide
 // r / 2 (interleaved: r), the elements past r and a row.
 int plan(const tp_rope_handle& H, const Call& c, int tokens, int size,
-          int inverse, bool with_rest, const tp_positions* pos, qk::Args* a) {
+         int inverse, bool with_rest, const tp_positions* pos, qk::Args* a) {
   std::memset(a, 0, sizeof(*a));
   int bytes = 16;
   for (int s = 0; s < 2; ++s) {
