@@ -107,10 +107,11 @@ __device__ __forceinline__ void load_batch(const Part& p, int first,
 }
 
 // Adds the squares of N values: to `sum` in fp32 where that is right, which is
-// where theirs is between 2^-60 and 2^120 (it has not overflowed, and squares that
-// underflowed, below 2^-126, are nothing beside it), else (larger, smaller but
-// not all zero, or not a number) to `wide` in fp64.  fp64 is kept out of the way:
-// an SM does two such additions per cycle.
+// where theirs is between 2^-60 and 2^110 (a thread adds at most 66 of these in
+// a chunk or in its pieces, and a warp's 32 threads stay below 2^122: nothing
+// overflows; squares that underflowed, below 2^-126, are nothing beside it),
+// else (larger, smaller but not all zero, or not a number) to `wide` in fp64.
+// fp64 is kept out of the way: an SM does two such additions per cycle.
 template <int N>
 __device__ __forceinline__ void add_squares(const float (&x)[N], float& sum,
                                             double& wide) {
@@ -118,7 +119,7 @@ __device__ __forceinline__ void add_squares(const float (&x)[N], float& sum,
 #pragma unroll
   for (int i = 0; i < N; ++i) a[i % 4] = fmaf(x[i], x[i], a[i % 4]);
   const float s = (a[0] + a[1]) + (a[2] + a[3]);
-  if (s >= 0x1p-60f && s <= 0x1p120f) {
+  if (s >= 0x1p-60f && s <= 0x1p110f) {
     sum += s;
     return;
   }
@@ -342,8 +343,7 @@ __global__ void __cluster_dims__(SMALL_BLOCKS, 1, 1)
     batch_squares<SMALL_BATCH>(v[k], p[k].bf16, sum, wide);
     rest_squares(p[k], lane, 32, sum, wide);
   }
-  // sum is below 2^120 times the additions of a lane (2 batches, 64 single
-  // elements): a warp's total stays finite
+  // (2 batches and 64 single elements a lane at most: see add_squares)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     sum += __shfl_xor_sync(0xffffffffu, sum, o);

@@ -240,3 +240,19 @@ def test_streams_and_graphs():
             assert torch.equal(n, norms[k])
             for x, y in zip(ref, held):
                 assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 31, 512, 1024, 2048, 5000])
+@pytest.mark.parametrize("scale", [2.0 ** 59.5, 2.0 ** 60, 2.0 ** 55])
+@pytest.mark.parametrize("off", ["grad", "out", "both"])
+def test_large_squares_off_16_bytes(n, dtype, scale, off):
+    """Short sets of large values that are read one by one: a warp's total of
+    their squares passes 2^128 where each is below 2^120."""
+    at = lambda where: 1 if off in (where, "both") else 0
+    g = torch.full((n + 1,), scale, dtype=dtype, device="cuda")
+    g = g[at("grad"):at("grad") + n]
+    out = torch.zeros(n + 1, dtype=dtype, device="cuda")
+    out = out[at("out"):at("out") + n]
+    assert math.isfinite(check([g], scale, eps=0.0, out=[out]))
+    check([g], 1.0)
