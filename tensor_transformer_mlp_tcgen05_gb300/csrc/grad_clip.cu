@@ -71,12 +71,14 @@ __device__ __forceinline__ const Entry& entry_of(const Table<N>& t,
 }
 
 // A chunk (or piece) of a tensor: n elements of it, of which the first nv 16-byte
-// vectors are read as such (none where a pointer is off 16 bytes).
+// vectors are read as such (none where the gradient is off 16 bytes), and written
+// as such where the output is not (o16).  The output has no say in how squares are
+// read, so that clipping finds the very norm that the norm alone does.
 struct Part {
   const char* g;
   char* o;
   int n, nv;
-  bool bf16;
+  bool bf16, o16;
 };
 template <int BYTES>
 __device__ __forceinline__ Part part_of(const Entry& e, unsigned chunk) {
@@ -88,9 +90,8 @@ __device__ __forceinline__ Part part_of(const Entry& e, unsigned chunk) {
   p.o = static_cast<char*>(e.out) + at;
   p.n = static_cast<int>(
       min(static_cast<long long>(BYTES / size), e.numel - at / size));
-  const bool aligned = ((reinterpret_cast<uintptr_t>(p.g) |
-                         reinterpret_cast<uintptr_t>(p.o)) & 15u) == 0;
-  p.nv = aligned ? p.n * size / 16 : 0;
+  p.nv = (reinterpret_cast<uintptr_t>(p.g) & 15u) == 0 ? p.n * size / 16 : 0;
+  p.o16 = (reinterpret_cast<uintptr_t>(p.o) & 15u) == 0;
   return p;
 }
 
@@ -193,14 +194,30 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, float c) {
   return pack_bf16x2(lo * c, hi * c);
 }
 
+// A vector at an address that is off 16 bytes.
+__device__ __forceinline__ void store_apart(const Part& p, char* to,
+                                            const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (p.bf16) {
+      reinterpret_cast<uint16_t*>(to)[2 * j] = static_cast<uint16_t>(w[j]);
+      reinterpret_cast<uint16_t*>(to)[2 * j + 1] =
+          static_cast<uint16_t>(w[j] >> 16);
+    } else {
+      reinterpret_cast<uint32_t*>(to)[j] = w[j];
+    }
+  }
+}
+
 template <int B, int STEP>
 __device__ __forceinline__ void store_batch(const Part& p, int first,
                                             const uint4 (&v)[B], float c) {
-  uint4* o = reinterpret_cast<uint4*>(p.o);
 #pragma unroll
   for (int k = 0; k < B; ++k) {
     const int i = first + k * STEP;
     if (i >= p.nv) continue;
+    char* to = p.o + 16LL * i;
     uint4 u;
     if (p.bf16) {
       u = make_uint4(scale_bf16x2(v[k].x, c), scale_bf16x2(v[k].y, c),
@@ -211,7 +228,8 @@ __device__ __forceinline__ void store_batch(const Part& p, int first,
                      __float_as_uint(__uint_as_float(v[k].z) * c),
                      __float_as_uint(__uint_as_float(v[k].w) * c));
     }
-    o[i] = u;
+    if (p.o16) *reinterpret_cast<uint4*>(to) = u;
+    else store_apart(p, to, u);
   }
 }
 
@@ -333,7 +351,7 @@ __global__ void __cluster_dims__(SMALL_BLOCKS, 1, 1)
     const unsigned piece = warp + k * SMALL_WARPS;
     p[k].g = p[k].o = nullptr;
     p[k].n = p[k].nv = 0;
-    p[k].bf16 = false;
+    p[k].bf16 = p[k].o16 = false;
     if (piece < t.chunks)
       p[k] = part_of<SMALL_PIECE_BYTES>(entry_of(t, piece), piece);
     load_batch<SMALL_BATCH, 32>(p[k], lane, v[k]);

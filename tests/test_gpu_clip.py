@@ -256,3 +256,18 @@ def test_large_squares_off_16_bytes(n, dtype, scale, off):
     out = out[at("out"):at("out") + n]
     assert math.isfinite(check([g], scale, eps=0.0, out=[out]))
     check([g], 1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [100, 5003, 70001, 400009])
+def test_the_norm_does_not_depend_on_where_the_outputs_are(n, dtype):
+    """Outputs off 16 bytes beside gradients that are not: the same norm, bit
+    for bit, and nothing written beside them."""
+    for seed in range(4):
+        g = randn(n, seed, dtype)
+        room = torch.full((n + 9,), 7.0, dtype=dtype, device="cuda")
+        for shift in (0, 1, 3):
+            check([g], 1.0, out=[room[shift:shift + n]])
+            assert (room[:shift] == 7.0).all()
+            assert (room[shift + n:] == 7.0).all()
+            room.fill_(7.0)
