@@ -216,8 +216,10 @@ struct Heads {
       }
       if (given[s] != Py_None) {
         out[s] = tensor(names[s], given[s]);
+        heads_of(names[s], out[s], d, in[s]);
+        // a lazy copy has memory of its own from here on; then its address
+        out[s].data_ptr();
         vout[s] = heads_of(names[s], out[s], d, in[s]);
-        out[s].data_ptr();   // an output's own memory
         continue;
       }
       out[s] = make(in[s]->sizes(), in[s]->scalar_type(), in[s]->device());
@@ -368,8 +370,9 @@ PyObject* norm_backward(PyObject* const* a) {
         grad[i] = row_of(all, i);
         gp[i] = grad[i].data_ptr<float>();
       } else {
-        gp[i] = param_of(names[i], given, d, dq);
+        param_of(names[i], given, d, dq);
         grad[i] = tensor(names[i], given);
+        gp[i] = grad[i].data_ptr<float>();   // (as the heads' outputs)
       }
     }
     // a workspace of this call alone: calls on several streams, and captured
@@ -413,6 +416,9 @@ PyObject* grads(PyObject* const* a) {
   const double max_norm = real(a[3]), eps = real(a[4]);
   std::vector<tp_grad_tensor> table(static_cast<size_t>(n));
   const at::Device dev = tensor("gradient", in.at(0)).device();
+  dtype_code("a gradient", tensor("gradient", in.at(0)));
+  // (an output that is a lazy copy is copied below, on the call's stream)
+  const Place place(dev, a[5]);
   for (Py_ssize_t i = 0; i < n; ++i) {
     const at::Tensor& g = tensor("gradient", in.at(i));
     tp_grad_tensor& t = table[static_cast<size_t>(i)];
@@ -434,7 +440,6 @@ PyObject* grads(PyObject* const* a) {
     t.grad = g.const_data_ptr();
     t.out = o.data_ptr();
   }
-  Place place(dev, a[5]);
   const at::Tensor norm = make({}, at::kFloat, dev);
   const int count = static_cast<int>(n);
   const size_t bytes = lib.grad_workspace_bytes(count);

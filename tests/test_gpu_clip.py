@@ -271,3 +271,18 @@ def test_the_norm_does_not_depend_on_where_the_outputs_are(n, dtype):
             assert (room[:shift] == 7.0).all()
             assert (room[shift + n:] == 7.0).all()
             room.fill_(7.0)
+
+
+def test_a_lazy_copy_as_output_gets_memory_of_its_own():
+    g = [randn(3000, 1), randn(3000, 2)]
+    keep = [t.clone() for t in g]
+    want = [torch.empty_like(t) for t in g]
+    n = clip_grad_norm(g, 0.5, out=want)
+    lazy = [torch._lazy_clone(t) for t in g]
+    assert torch.equal(clip_grad_norm(g, 0.5, out=lazy), n)
+    for a, b, c, k in zip(lazy, want, g, keep):
+        assert torch.equal(a, b) and torch.equal(c, k)
+    lazy = [torch._lazy_clone(t) for t in g]
+    clip_grad_norm(lazy, 0.5)
+    for a, b, c, k in zip(lazy, want, g, keep):
+        assert torch.equal(a, b) and torch.equal(c, k)

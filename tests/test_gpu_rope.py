@@ -614,3 +614,35 @@ def test_refusals_of_the_wrappers():
     for call in lib_bad:
         with pytest.raises(B.TPMLPError):
             call()
+
+
+def test_lazy_copies_as_outputs_get_memory_of_their_own():
+    d = 64
+    q, k = make(50, 4, 2, d, torch.bfloat16, 101)
+    dq, dk = make(50, 4, 2, d, torch.bfloat16, 102)
+    keep = [t.clone() for t in (q, k, dq, dk)]
+    rope = RotaryEmbedding(d, rotary_dim=32)
+    op = QKNormRotary(d, norm="layer", rotary=rope)
+    for call in (rope.forward, op.forward, rope.backward):
+        want = call(q, k, offset=5)
+        outs = [torch._lazy_clone(t) for t in (q, k)]
+        got = call(q, k, offset=5, q_out=outs[0], k_out=outs[1])
+        for a, b, c in zip(outs, want, got):
+            assert torch.equal(a, b) and torch.equal(c, b)
+        # in place in a tensor that another one still shares
+        outs = [torch._lazy_clone(t) for t in (q, k)]
+        call(outs[0], outs[1], offset=5, q_out=outs[0], k_out=outs[1])
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+    want = op.backward(dq, dk, q, k)
+    par = {n: torch.full((d,), 3.0, device="cuda")
+           for n in ("dq_gamma", "dk_gamma", "dq_beta", "dk_beta")}
+    out = {n: torch._lazy_clone(t) for n, t in par.items()}
+    out.update(dq=torch._lazy_clone(q), dk=torch._lazy_clone(dk))
+    op.backward(dq, dk, q, k, out=out)
+    for n in want:
+        assert torch.equal(out[n], want[n]), n
+    for t in par.values():
+        assert (t == 3.0).all()
+    for a, b in zip((q, k, dq, dk), keep):
+        assert torch.equal(a, b)
