@@ -354,27 +354,27 @@ PyObject* norm_backward(PyObject* const* a) {
   size_t bytes = 0;
   const int params = PyObject_IsTrue(a[15]);
   if (params < 0) throw Raised{};
-  if (params) {
-    const char* names[4] = {"dq_gamma", "dq_beta", "dk_gamma", "dk_beta"};
-    at::Tensor all;   // those that are made new: one allocation
-    for (int i = 0; i < 4; ++i) {
-      PyObject* given = a[16 + i];
-      if ((i % 2 == 1 && n.norm != TPQK_LAYERNORM) ||
-          (i >= 2 && h.in[1] == nullptr)) {
-        if (given != Py_None)
-          throw Refused{std::string("out: this call has no ") + names[i]};
-        continue;
-      }
-      if (given == Py_None) {
-        if (!all.defined()) all = make({4, d}, at::kFloat, dq.device());
-        grad[i] = row_of(all, i);
-        gp[i] = grad[i].data_ptr<float>();
-      } else {
-        param_of(names[i], given, d, dq);
-        grad[i] = tensor(names[i], given);
-        gp[i] = grad[i].data_ptr<float>();   // (as the heads' outputs)
-      }
+  at::Tensor all;   // parameter gradients that are made new: one allocation
+  const char* names[4] = {"dq_gamma", "dq_beta", "dk_gamma", "dk_beta"};
+  for (int i = 0; i < 4; ++i) {
+    PyObject* given = a[16 + i];
+    if (!params || (i % 2 == 1 && n.norm != TPQK_LAYERNORM) ||
+        (i >= 2 && h.in[1] == nullptr)) {
+      if (given != Py_None)
+        throw Refused{std::string("out: this call has no ") + names[i]};
+      continue;
     }
+    if (given == Py_None) {
+      if (!all.defined()) all = make({4, d}, at::kFloat, dq.device());
+      grad[i] = row_of(all, i);
+      gp[i] = grad[i].data_ptr<float>();
+    } else {
+      param_of(names[i], given, d, dq);
+      grad[i] = tensor(names[i], given);
+      gp[i] = grad[i].data_ptr<float>();   // (as the heads' outputs)
+    }
+  }
+  if (params) {
     // a workspace of this call alone: calls on several streams, and captured
     // graphs, share no partial sums
     bytes = lib.norm_workspace_bytes(handle);

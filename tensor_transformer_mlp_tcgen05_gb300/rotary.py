@@ -135,8 +135,9 @@ class QKNormRotary:
                  param_grads: bool = True, out=None, stream=None):
         """Gradients from dq, dk (of the rotated heads) and forward's q, k: a
         dict with dq, dk and (with param_grads) dq_gamma, dk_gamma and, for
-        "layer", dq_beta, dk_beta.  ``out`` may hold any of them; out["dq"] may
-        be dq or q themselves.  dk and k are None together."""
+        "layer", dq_beta, dk_beta.  ``out`` may hold any of them, and no gradient
+        that the call does not have; out["dq"] may be dq or q themselves.  dk and
+        k are None together."""
         r = self.rotary
         g = out if out is not None else {}
         get = g.get

@@ -646,3 +646,22 @@ def test_lazy_copies_as_outputs_get_memory_of_their_own():
         assert (t == 3.0).all()
     for a, b in zip((q, k, dq, dk), keep):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+def test_without_parameter_gradients(norm):
+    """param_grads=False: dq and dk alone, the same bits; parameter gradients
+    that are given all the same are refused, not handed back unwritten."""
+    q, k = make(40, 4, 2, 64, torch.bfloat16, 103)
+    dq, dk = make(40, 4, 2, 64, torch.bfloat16, 104)
+    op = QKNormRotary(64, norm=norm, rotary=RotaryEmbedding(64))
+    want = op.backward(dq, dk, q, k)
+    got = op.backward(dq, dk, q, k, param_grads=False)
+    assert sorted(got) == ["dk", "dq"]
+    for n in got:
+        assert torch.equal(got[n], want[n])
+    for n in ("dq_gamma", "dk_gamma", "dq_beta", "dk_beta"):
+        given = torch.full((64,), 5.0, device="cuda")
+        with pytest.raises(ValueError):
+            op.backward(dq, dk, q, k, param_grads=False, out={n: given})
+        assert (given == 5.0).all()
