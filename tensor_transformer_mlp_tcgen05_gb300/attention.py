@@ -150,9 +150,15 @@ class TensorParallelAttention:
         """Gradients after a training forward on the same workspace (with the
         same q_gamma, k_gamma and positions): a dict with dX, dWqkv, dWo and
         (optionally) dbqkv, dbo, dgamma, dbeta, and with ``qk_norm`` dq_gamma,
-        dk_gamma and, for "layer", dq_beta, dk_beta."""
+        dk_gamma and, for "layer", dq_beta, dk_beta; ``out`` may hold any of
+        them, but none of the last four that the block does not have."""
         T = dZ.shape[0]
         h = self.hidden
+        names = {None: (), "rms": ("q_gamma", "k_gamma"),
+                 "layer": ("q_gamma", "k_gamma", "q_beta", "k_beta")}[self.qk_norm]
+        for n in ("q_gamma", "k_gamma", "q_beta", "k_beta"):
+            if out and out.get("d" + n) is not None and n not in names:
+                raise ValueError(f"out: this block has no d{n}")
         self._chk("dZ", dZ, (T, h), torch.bfloat16)
         dev = dZ.device
         f32 = torch.float32
@@ -169,9 +175,6 @@ class TensorParallelAttention:
         qk_grads = None
         if self.qk_norm is not None:
             d = h // self.heads
-            names = ("q_gamma", "k_gamma")
-            if self.qk_norm == "layer":
-                names += ("q_beta", "k_beta")
             qk_grads = B_.tp_qk_norm_grads()
             for n in names:
                 g.setdefault("d" + n, torch.empty(d, dtype=f32, device=dev))

@@ -275,3 +275,27 @@ def test_refusals_of_the_wrapper():
         normed.forward(inp["X"], inp["Wqkv"], inp["Wo"], q_beta=one)
     for m in (plain, normed, roped):
         m.close()
+
+
+@pytest.mark.parametrize("norm,extra", [
+    (None, "dq_gamma"), (None, "dk_beta"), ("rms", "dq_beta"),
+    ("rms", "dk_beta")])
+def test_gradients_that_the_block_does_not_have_are_refused(norm, extra):
+    """Given in `out`, they would come back in the dict as they were."""
+    w = W.ATTN_WORKLOADS["attn_tiny_d64"]
+    inp = {k: cuda(v) for k, v in W.make_attn_inputs(w, 1).items()}
+    m = TensorParallelAttention(w.hidden, w.heads, w.shards, w.tokens, w.seq,
+                                qk_norm=norm)
+    m.forward(inp["X"], inp["Wqkv"], inp["Wo"])
+    d = w.hidden // w.heads
+    given = torch.full((d,), 5.0, device="cuda")
+    with pytest.raises(ValueError):
+        m.backward(inp["dZ"], inp["X"], inp["Wqkv"], inp["Wo"],
+                   out={extra: given})
+    assert (given == 5.0).all()
+    out = {} if norm is None else {"dq_gamma": given}
+    g = m.backward(inp["dZ"], inp["X"], inp["Wqkv"], inp["Wo"], out=out)
+    assert m.check() == 0
+    assert set(n for n in g if n[1:3] in ("q_", "k_")) == \
+        (set() if norm is None else {"dq_gamma", "dk_gamma"})
+    m.close()
