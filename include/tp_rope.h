@@ -25,8 +25,9 @@
  * -----------
  * - Element types: queries and keys bf16 (TPMLP_BF16) or fp32 (TPMLP_FP32),
  *   gamma, beta and their gradients fp32; all arithmetic fp32, one rounding
- *   to the element type.  Angles are made in 64-bit fixed point, within 2^-33
- *   of a turn at every position, then rounded to fp32.
+ *   to the element type.  Angles are made in 64-bit fixed point: p f_i, f_i
+ *   being the double that tp_rope_frequencies gives (up to 2^40), is within
+ *   2^-33 + |p| 2^-64 of a turn, then rounded to fp32.
  * - Pointers are DEVICE pointers the caller owns (tp_rope_config's inv_freq
  *   and the structs are host memory, read during the call only); the library
  *   never allocates device memory.  Calls only enqueue work on `stream`.

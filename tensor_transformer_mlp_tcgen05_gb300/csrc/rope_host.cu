@@ -26,12 +26,25 @@ int bad(int code, const char* msg) {
   return code;
 }
 
-// frac(f / 2 pi) in 64-bit fixed point.  Positions are integers, so whole
-// turns drop out; a double holds the fraction to 53 bits.
+// t modulo one in 64-bit fixed point, rounded to the nearest 2^-64.
+unsigned long long fixed_fraction(double t) {
+  t -= std::nearbyint(t);                   // exact, [-1/2, 1/2]
+  const unsigned long long u = static_cast<unsigned long long>(
+      std::nearbyint(std::ldexp(std::fabs(t), 64)));
+  return t < 0 ? 0ull - u : u;
+}
+
+// frac(f / 2 pi) in 64-bit fixed point, within 2^-64 for |f| <= 2^40.  Positions
+// are integers, so whole turns drop out.  The error is multiplied by the
+// position, so the quotient is made to twice a double's bits: f times 1 / 2 pi
+// as a sum of two doubles (off by 2^-110).
 unsigned long long fixed_turns(double f) {
-  double t = f / 6.283185307179586476925286766559;
-  t -= std::floor(t);                       // [0, 1)
-  return static_cast<unsigned long long>(std::ldexp(t, 53)) << 11;
+  constexpr double HI = 0x1.45f306dc9c883p-3, LO = -0x1.6b01ec5417056p-57;
+  // (volatile: the product is rounded here, not fused into what uses it)
+  const volatile double product = f * HI;
+  const double hi = product;
+  const double lo = std::fma(f, LO, std::fma(f, HI, -hi));
+  return fixed_fraction(hi) + fixed_fraction(lo);
 }
 
 bool positive(double x) { return x > 0 && std::isfinite(x); }

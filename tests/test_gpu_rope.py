@@ -665,3 +665,60 @@ def test_without_parameter_gradients(norm):
         with pytest.raises(ValueError):
             op.backward(dq, dk, q, k, param_grads=False, out={n: given})
         assert (given == 5.0).all()
+
+
+def _turns(positions, freqs):
+    """p f / 2 pi modulo one turn, exact integer arithmetic on the doubles f and
+    1 / 2 pi to 300 bits (pi by Machin's formula), as floats of [-1/2, 1/2)."""
+    from fractions import Fraction
+    bits = 320
+
+    def arctan_inverse(n):
+        total, term, k, sign = 0, (1 << bits) // n, 1, 1
+        while term:
+            total += sign * (term // k)
+            term //= n * n
+            k += 2
+            sign = -sign
+        return total
+
+    two_pi = 8 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    assert abs(two_pi / (1 << bits) - 2 * math.pi) < 1e-15
+    out = np.empty((len(positions), len(freqs)))
+    for j, f in enumerate(freqs):
+        per = Fraction(f) * (1 << bits) / two_pi      # turns per position
+        for i, p in enumerate(positions):
+            t = (per * int(p)) % 1
+            out[i, j] = float(t if t < Fraction(1, 2) else t - 1)
+    return out
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("base", [10000.0, 500000.0, None])
+def test_angles_of_the_furthest_positions(base, inter):
+    """The angle of the frequencies as they are reported, at positions of 2^20
+    to 2^36: the phase is within 2^-33 of a turn (its 32 bits), and |p| 2^-64 from
+    the frequency's 64, 2^-28 at 2^36, together under 2^-27.9 turns, which is
+    2^-25.2 or 0.43 u of an angle.  Of the rotation's tolerance, by its own
+    derivation, (3.2 + 2 + 1 + 1) u M for each product and 1.5 u M for their sum,
+    15.9 u M, 0.9 more."""
+    d = 64
+    kw = dict(base=base) if base else dict(
+        inv_freq=[(-1) ** i * 2.0 ** (3 - i) / 3 for i in range(d // 2)])
+    rope = RotaryEmbedding(d, interleaved=inter, **kw)
+    f, amp = rope.frequencies()
+    g = torch.Generator("cuda").manual_seed(5)
+    pos = torch.cat([torch.randint(-(1 << b), 1 << b, (12,), generator=g,
+                                   device="cuda") for b in (20, 24, 28, 31, 36)] +
+                    [torch.tensor([(1 << 31) - 1, -(1 << 31), 4000000],
+                                  device="cuda")])
+    q, _ = make(len(pos), 2, 1, d, torch.float32, 105)
+    y, _ = rope.forward(q, positions=pos)
+    ang = 2 * math.pi * _turns(pos.tolist(), f)
+    c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
+    x, want = flat(q), flat(q)
+    ia, ib = ((slice(0, d, 2), slice(1, d, 2)) if inter
+              else (slice(0, d // 2), slice(d // 2, d)))
+    want[..., ia] = x[..., ia] * c - x[..., ib] * s
+    want[..., ib] = x[..., ia] * s + x[..., ib] * c
+    within(flat(y), amp * want, rows_max(x) * amp, 17, torch.float32)
