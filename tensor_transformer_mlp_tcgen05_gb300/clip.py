@@ -3,8 +3,9 @@ C ABI in include/tp_grad.h.  csrc/pycall.cpp checks the tensors; all arithmetic
 happens in libtpmlp's kernels.
 
 Gradients are contiguous bf16 or fp32 CUDA tensors of one device, of any number
-and shape, in a list or in a dict; of a dict as the blocks' ``backward`` methods
-return it, the entry ``dX`` (the gradient of the activations) is left out.
+and shape, in a list or in a dict; of a dict as the ``backward`` methods of the
+blocks and of QKNormRotary return it, the gradients of the activations (``dX``;
+``dq`` and ``dk``) are left out.
 
 With ``stream`` the work, and the norm's memory, belong to that stream;
 otherwise to the current one of the tensors' device."""
@@ -15,9 +16,12 @@ import torch
 from . import binding as B_
 
 
+_ACTIVATIONS = ("dX", "dq", "dk")
+
+
 def _listed(tensors):
     if isinstance(tensors, dict):
-        return [t for n, t in tensors.items() if n != "dX"]
+        return [t for n, t in tensors.items() if n not in _ACTIVATIONS]
     if isinstance(tensors, torch.Tensor):
         return [tensors]
     return tensors if isinstance(tensors, (list, tuple)) else list(tensors)
@@ -36,10 +40,11 @@ def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, out=None,
     return the norm they had, as grad_norm.  A norm that is not finite is
     returned and scales nothing."""
     if isinstance(tensors, dict) and isinstance(out, dict):
-        missing = [n for n in tensors if n != "dX" and n not in out]
+        names = [n for n in tensors if n not in _ACTIVATIONS]
+        missing = [n for n in names if n not in out]
         if missing:
             raise ValueError(f"out has no {missing}")
-        out = [out[n] for n in tensors if n != "dX"]
+        out = [out[n] for n in names]
     return B_.tensor_calls().grads(
         _listed(tensors), None if out is None else _listed(out), 1, max_norm,
         eps, stream)

@@ -286,3 +286,24 @@ def test_a_lazy_copy_as_output_gets_memory_of_its_own():
     clip_grad_norm(lazy, 0.5)
     for a, b, c, k in zip(lazy, want, g, keep):
         assert torch.equal(a, b) and torch.equal(c, k)
+
+
+def test_activations_gradients_are_left_out_of_the_operators_dict():
+    """The dict that the query/key norm's backward returns: dq and dk are the
+    activations' gradients, as dX is the blocks'."""
+    from tensor_transformer_mlp_tcgen05_gb300.rotary import QKNormRotary
+    x = [randn(40 * 3 * 64, i).view(40, 3, 64) for i in range(4)]
+    g = QKNormRotary(64, norm="layer").backward(*x)
+    keep = {n: t.clone() for n, t in g.items()}
+    params = ["dq_gamma", "dk_gamma", "dq_beta", "dk_beta"]
+    norm, c, _ = O.clip([f64(keep[n]) for n in params], 1.0)
+    assert c < 1.0
+    assert abs(float(grad_norm(g)) - norm) <= 65 * U * norm
+    out = {n: torch.empty_like(g[n]) for n in params}
+    assert abs(float(clip_grad_norm(g, 1.0, out=out)) - norm) <= 65 * U * norm
+    assert abs(float(clip_grad_norm(g, 1.0)) - norm) <= 65 * U * norm
+    for n in ("dq", "dk"):
+        assert torch.equal(g[n], keep[n])
+    for n in params:
+        assert torch.equal(g[n], out[n])
+        assert close(g[n], f64(keep[n]) * c, torch.float32)
