@@ -741,10 +741,13 @@ __device__ __forceinline__ void load_turn(const Args& p, const Side& sd,
     if constexpr (NORM == TPQK_LAYERNORM) {
       Pairs<V> bet;
       un.param(p, sd.beta, 0.f, bet);
+      // (a beta past r meets no other, as x does not in the loop over rows)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        t.za[j] = fmaf(bet.a[j], t.ca[j], -(bet.b[j] * t.sa[j]));
-        t.zb[j] = fmaf(bet.a[j], t.sa[j], bet.b[j] * t.ca[j]);
+        t.za[j] = un.turns ? fmaf(bet.a[j], t.ca[j], -(bet.b[j] * t.sa[j]))
+                           : bet.a[j];
+        t.zb[j] = un.turns ? fmaf(bet.a[j], t.sa[j], bet.b[j] * t.ca[j])
+                           : bet.b[j];
       }
     }
     mul<V>(t.cb, t.ca, gam.b);

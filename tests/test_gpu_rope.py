@@ -722,3 +722,25 @@ def test_angles_of_the_furthest_positions(base, inter):
     want[..., ia] = x[..., ia] * c - x[..., ib] * s
     want[..., ib] = x[..., ia] * s + x[..., ib] * c
     within(flat(y), amp * want, rows_max(x) * amp, 17, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,r", [(128, 64), (96, 48), (100, 50), (64, 0),
+                                 (72, 18)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_bias_that_is_not_finite_stays_with_its_element(d, r, inter, dtype,
+                                                          bad):
+    """Past r a bias reaches its own element only; before, its pair."""
+    rope = RotaryEmbedding(d, rotary_dim=r, interleaved=inter)
+    op = QKNormRotary(d, norm="layer", rotary=rope)
+    q, _ = make(1, 3, 1, d, dtype, 106)
+    for e in sorted({0, max(r - 1, 0), min(r, d - 1), (r + d) // 2, d - 1}):
+        beta = torch.zeros(d, device="cuda")
+        beta[e] = bad
+        y, _ = op.forward(q, q_beta=beta, offset=1)
+        hit = torch.zeros(d, dtype=torch.bool, device="cuda")
+        hit[e] = True
+        if e < r:
+            hit[e ^ 1 if inter else (e + r // 2) % r] = True
+        assert torch.equal(~torch.isfinite(y), hit.expand_as(y)), e
