@@ -5,9 +5,12 @@ Each CUDA translation unit is compiled in parallel, then linked into
 linked statically; the driver API is reached through the runtime's entry-point
 lookup, so the library does not link libcuda).  Object files go to
 ``_build/`` at the repository root.  A rebuild is skipped when the library is
-newer than every source and header.  Next to it goes ``_pycall.so``, a Python
-module (host C++, built against the installed torch) with the tensor calls of
-``rotary.py`` and ``clip.py``.
+newer than every source and header.  The library needs the CUDA toolkit only.
+
+Next to it goes ``_pycall.so``, a Python module (host C++, built against the
+installed torch) with the tensor calls of ``rotary.py`` and ``clip.py``.  Where
+torch is not installed it is left out; where it does not compile, build() says
+so once the library is linked.
 
 ``build(checks=True)`` makes the debug variant ``libtpmlp_checks.so`` (objects
 in ``_build/checks``) with ``-DTPMLP_CHECKS``: device-side checks of TMA
@@ -18,6 +21,7 @@ before the binding is imported.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -50,27 +54,36 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required")
 
 
+HEADERS = [os.path.join(INCLUDE, f) for f in ("tp_mlp.h", "tp_attn.h",
+                                              "tp_rope.h", "tp_grad.h")]
+
+
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-             if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
-    files.append(os.path.join(INCLUDE, "tp_mlp.h"))
-    files.append(os.path.join(INCLUDE, "tp_attn.h"))
-    files.append(os.path.join(INCLUDE, "tp_rope.h"))
-    files.append(os.path.join(INCLUDE, "tp_grad.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+    """What the library is made of."""
+    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)
+            if f.endswith((".cu", ".cuh", ".h"))] + HEADERS + \
+        [os.path.abspath(__file__)]
 
 
-def up_to_date(lib_path: str = LIB_PATH) -> bool:
+def _pycall_inputs():
+    return [os.path.join(CSRC, "pycall.cpp"), *HEADERS,
+            os.path.abspath(__file__)]
+
+
+def up_to_date(lib_path: str = LIB_PATH, inputs=None) -> bool:
     if not os.path.exists(lib_path):
         return False
     t = os.path.getmtime(lib_path)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return all(os.path.getmtime(f) <= t for f in inputs or _inputs())
+
+
+def has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
 
 
 def build_pycall(force: bool = False) -> str:
     """Compile _pycall.so with the host compiler; returns its path."""
-    if not force and up_to_date(PYCALL_PATH):
+    if not force and up_to_date(PYCALL_PATH, _pycall_inputs()):
         return PYCALL_PATH
     import torch
     from torch.utils import cpp_extension
@@ -102,7 +115,8 @@ def build(force: bool = False, verbose: bool = False,
     checks=True builds the debug variant (see the module docstring)."""
     lib_path = CHECKS_LIB_PATH if checks else LIB_PATH
     if not force and up_to_date(lib_path):
-        build_pycall()
+        if has_torch():
+            build_pycall()
         return lib_path
     nvcc = nvcc_path()
     obj_dir = os.path.join(BUILD_DIR, "checks") if checks else BUILD_DIR
@@ -121,9 +135,8 @@ def build(force: bool = False, verbose: bool = False,
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        pycall = ex.submit(build_pycall, force)
+        pycall = ex.submit(build_pycall, force) if has_torch() else None
         results = list(ex.map(compile_one, SOURCES))
-        pycall.result()
     if verbose or ptxas_info:
         for obj, log in results:
             if log.strip():
@@ -134,6 +147,8 @@ def build(force: bool = False, verbose: bool = False,
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, lib_path)
+    if pycall is not None:
+        pycall.result()   # (its error, where there is one)
     return lib_path
 
 

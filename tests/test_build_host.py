@@ -1,0 +1,47 @@
+"""The build's two parts, without a GPU and without compiling: the library is
+linked whether or not the Python module of the tensor calls can be made."""
+import os
+import types
+
+import pytest
+
+from tensor_transformer_mlp_tcgen05_gb300 import build as build_mod
+
+
+@pytest.fixture
+def compilers(tmp_path, monkeypatch):
+    """Compilers that write their output and succeed; all paths under
+    tmp_path.  Returns the commands that were run."""
+    runs = []
+
+    def run(cmd, **_):
+        runs.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("made")
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(build_mod.subprocess, "run", run)
+    monkeypatch.setattr(build_mod, "nvcc_path", lambda: "nvcc")
+    monkeypatch.setattr(build_mod, "BUILD_DIR", str(tmp_path / "_build"))
+    monkeypatch.setattr(build_mod, "LIB_PATH", str(tmp_path / "libtpmlp.so"))
+    return runs
+
+
+def test_the_library_does_not_need_the_python_module(compilers, monkeypatch):
+    def fails(force=False):
+        raise RuntimeError("g++ failed for pycall.cpp")
+
+    monkeypatch.setattr(build_mod, "build_pycall", fails)
+    with pytest.raises(RuntimeError, match="pycall"):
+        build_mod.build(force=True)
+    assert os.path.exists(build_mod.LIB_PATH)
+    assert len(compilers) == len(build_mod.SOURCES) + 1
+
+
+def test_without_torch_the_library_is_all_there_is(compilers, monkeypatch):
+    monkeypatch.setattr(build_mod, "has_torch", lambda: False)
+    monkeypatch.setattr(build_mod, "build_pycall", lambda force=False: 1 / 0)
+    for _ in range(2):   # made, and found made
+        assert build_mod.build() == build_mod.LIB_PATH
+    assert os.path.exists(build_mod.LIB_PATH)
+    assert len(compilers) == len(build_mod.SOURCES) + 1
