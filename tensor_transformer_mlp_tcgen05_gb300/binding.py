@@ -326,15 +326,20 @@ _calls = None
 
 
 def tensor_calls():
-    """The module _pycall (csrc/pycall.cpp), bound to the loaded library."""
+    """The module _pycall (csrc/pycall.cpp) that was built for this Python and
+    torch, bound to the loaded library."""
     global _calls
     if _calls is None:
-        import importlib
-        if not os.path.exists(_build.PYCALL_PATH):
+        from importlib import machinery, util
+        path = _build.pycall_path()
+        if not os.path.exists(path):
             raise RuntimeError(
-                f"{_build.PYCALL_PATH} is missing: build it with "
+                f"{path} is missing: build it with "
                 "tensor_transformer_mlp_tcgen05_gb300.build.build()")
-        m = importlib.import_module("._pycall", __package__)
+        loader = machinery.ExtensionFileLoader(f"{__package__}._pycall", path)
+        m = util.module_from_spec(
+            util.spec_from_file_location(loader.name, path, loader=loader))
+        loader.exec_module(m)
         L = lib()
         m.bind(_check, *[
             ctypes.cast(getattr(L, n), ctypes.c_void_p).value

@@ -7,8 +7,9 @@ lookup, so the library does not link libcuda).  Object files go to
 ``_build/`` at the repository root.  A rebuild is skipped when the library is
 newer than every source and header.  The library needs the CUDA toolkit only.
 
-Next to it goes ``_pycall.so``, a Python module (host C++, built against the
-installed torch) with the tensor calls of ``rotary.py`` and ``clip.py``.  Where
+Next to it goes ``_pycall``, a Python module (host C++, built against the
+installed torch, whose C++ layouts it holds: the versions of Python and torch are
+in its file's name) with the tensor calls of ``rotary.py`` and ``clip.py``.  Where
 torch is not installed it is left out; where it does not compile, build() says
 so once the library is linked.
 
@@ -35,7 +36,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libtpmlp.so")
 CHECKS_LIB_PATH = os.path.join(PKG, "libtpmlp_checks.so")
-PYCALL_PATH = os.path.join(PKG, "_pycall.so")
 
 SOURCES = ["gemm_tc2.cu", "rowops.cu", "simt.cu",
            "tp_mlp_host.cu", "noalloc.cu", "attn_fwd.cu", "attn_bwd.cu",
@@ -81,10 +81,18 @@ def has_torch() -> bool:
     return importlib.util.find_spec("torch") is not None
 
 
+def pycall_path() -> str:
+    """The file of the module for this Python and this torch."""
+    import torch
+    return os.path.join(PKG, f"_pycall-{sys.implementation.cache_tag}"
+                             f"-torch-{torch.__version__}.so")
+
+
 def build_pycall(force: bool = False) -> str:
-    """Compile _pycall.so with the host compiler; returns its path."""
-    if not force and up_to_date(PYCALL_PATH, _pycall_inputs()):
-        return PYCALL_PATH
+    """Compile the Python module with the host compiler; returns its path."""
+    path = pycall_path()
+    if not force and up_to_date(path, _pycall_inputs()):
+        return path
     import torch
     from torch.utils import cpp_extension
     cxx = shutil.which("g++") or shutil.which("c++")
@@ -94,7 +102,7 @@ def build_pycall(force: bool = False) -> str:
                             "include")
     inc = [*cpp_extension.include_paths(), nvcc_inc,
            sysconfig.get_paths()["include"], INCLUDE]
-    tmp = PYCALL_PATH + ".tmp"
+    tmp = path + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            os.path.join(CSRC, "pycall.cpp"), "-o", tmp,
@@ -105,8 +113,8 @@ def build_pycall(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for pycall.cpp:\n{r.stderr}")
-    os.replace(tmp, PYCALL_PATH)
-    return PYCALL_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False,

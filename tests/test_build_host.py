@@ -45,3 +45,23 @@ def test_without_torch_the_library_is_all_there_is(compilers, monkeypatch):
         assert build_mod.build() == build_mod.LIB_PATH
     assert os.path.exists(build_mod.LIB_PATH)
     assert len(compilers) == len(build_mod.SOURCES) + 1
+
+
+def test_the_python_module_is_one_torchs_and_one_pythons(monkeypatch):
+    """Built for another torch or Python it is not loaded, but asked for."""
+    import sys
+
+    import torch
+    from tensor_transformer_mlp_tcgen05_gb300 import binding
+    build_mod.build()
+    path = build_mod.pycall_path()
+    assert os.path.exists(path) and torch.__version__ in path
+    assert sys.implementation.cache_tag in os.path.basename(path)
+    assert binding.tensor_calls().__name__.endswith("._pycall")
+    for where, name in ((torch, "__version__"),
+                        (sys.implementation, "cache_tag")):
+        with monkeypatch.context() as m:
+            m.setattr(binding, "_calls", None)
+            m.setattr(where, name, "0.0.0")
+            with pytest.raises(RuntimeError, match="0.0.0.* is missing"):
+                binding.tensor_calls()
