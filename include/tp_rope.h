@@ -73,7 +73,8 @@ typedef struct tp_rope_config {
   double original_length;  /* > 0 (read by YARN)                             */
   double slow_turns;       /* YARN: usually 1                                */
   double fast_turns;       /* YARN: usually 32, > slow_turns                 */
-  double amplitude;        /* amp; 0: the default (1, for YARN above)        */
+  double amplitude;        /* amp, at most 3.4e38 in magnitude; 0: the
+                              default (1, for YARN above)                    */
   const double* inv_freq;  /* CUSTOM: host array of r / 2 finite values      */
 } tp_rope_config;
 

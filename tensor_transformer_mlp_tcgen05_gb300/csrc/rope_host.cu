@@ -474,8 +474,8 @@ int tp_rope_create(const tp_rope_config* cfg, tp_rope_handle** out) {
        !std::isfinite(cfg->fast_turns) || cfg->fast_turns <= cfg->slow_turns))
     return bad(TPMLP_ERR_ARG, "rope: YARN needs original_length > 0 and "
                               "fast_turns > slow_turns");
-  if (!std::isfinite(cfg->amplitude))
-    return bad(TPMLP_ERR_ARG, "rope: amplitude must be finite");
+  if (!(std::fabs(cfg->amplitude) <= 3.4e38))   // (the kernels' is an fp32)
+    return bad(TPMLP_ERR_ARG, "rope: amplitude must be at most 3.4e38");
   if (sc == TPROPE_SCALE_CUSTOM && r > 0 && cfg->inv_freq == nullptr)
     return bad(TPMLP_ERR_ARG, "rope: CUSTOM needs inv_freq");
   tp_rope_handle h;

@@ -469,3 +469,16 @@ def test_attention_qk_arguments_are_refused_before_any_launch(lib):
         assert lib.tp_attn_forward_qk(None, *[0] * 14) == ARG
     finally:
         B.tp_attn_destroy(h)
+
+
+@pytest.mark.parametrize("amp", [1e39, -1e39, float("nan"), -float("inf")])
+def test_create_rejects_an_amplitude_beyond_fp32(lib, amp):
+    h = ctypes.c_void_p()
+    cfg = rope_cfg(amplitude=amp)
+    assert lib.tp_rope_create(ctypes.byref(cfg),
+                              ctypes.byref(h)) == B.TPMLP_ERR_ARG
+    assert h.value is None
+    cfg = rope_cfg(amplitude=3e38)
+    assert lib.tp_rope_create(ctypes.byref(cfg),
+                              ctypes.byref(h)) == B.TPMLP_OK
+    assert lib.tp_rope_destroy(h) == B.TPMLP_OK
