@@ -554,8 +554,9 @@ struct Ring<T, INTER, STAGES, OWN> {
   __device__ __forceinline__ void flush(int, const HeadRows<T>&, int, int) const {}
 };
 
-// A step's rows one after the other: at most 60 pieces of 16 bytes, dealt to the
-// lanes in two rounds.
+// A step's rows one after the other, in 16-byte pieces dealt to the lanes in two
+// rounds: at most 62 (31 units of a row, 248 elements of fp32), so that piece 63
+// is nobody's and idle lanes may read it.
 template <class T, bool INTER, int STAGES>
 struct Ring<T, INTER, STAGES, PIECES> {
   using Unit = VectorUnit<T, INTER>;

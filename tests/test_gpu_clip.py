@@ -307,3 +307,40 @@ def test_activations_gradients_are_left_out_of_the_operators_dict():
     for n in params:
         assert torch.equal(g[n], out[n])
         assert close(g[n], f64(keep[n]) * c, torch.float32)
+
+
+def test_the_bindings_of_the_c_abi():
+    """The ctypes binding's functions give what the tensor calls give."""
+    g = [randn(5000, 1), randn(300, 2, torch.bfloat16)]
+    out = [torch.empty_like(t) for t in g]
+    want = [torch.empty_like(t) for t in g]
+    code = {torch.float32: B.TPMLP_FP32, torch.bfloat16: B.TPMLP_BF16}
+    table = (B.tp_grad_tensor * 2)(*[
+        (t.data_ptr(), o.data_ptr(), t.numel(), code[t.dtype])
+        for t, o in zip(g, out)])
+    nbytes = B.tp_grad_workspace_bytes(2)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    norm = torch.empty((), device="cuda")
+    B.tp_grad_norm(2, table, norm, ws, nbytes)
+    assert torch.equal(norm, grad_norm(g))
+    norm.zero_()
+    B.tp_grad_clip(2, table, 1.0, 1e-6, norm, ws, nbytes)
+    assert torch.equal(norm, clip_grad_norm(g, 1.0, out=want))
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+    with pytest.raises(B.TPMLPError):
+        B.tp_grad_clip(2, table, -1.0, 1e-6, norm, ws, nbytes)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_offsets_past_32_bits(dtype):
+    """2^31 + 4099 elements, all zero but a few: the norm is exactly 5."""
+    n = (1 << 31) + 4099
+    x = torch.zeros(n, dtype=dtype, device="cuda")
+    at = [0, 1 << 30, (1 << 31) - 1, 1 << 31, n - 1]
+    for i, v in zip(at, (1.0, 2.0, 2.0, 4.0, 0.0)):
+        x[i] = v
+    assert float(grad_norm([x])) == 5.0
+    assert float(clip_grad_norm([x], 2.5, eps=0.0)) == 5.0
+    assert [float(x[i]) for i in at] == [0.5, 1.0, 1.0, 2.0, 0.0]
+    assert int(torch.count_nonzero(x)) == 4

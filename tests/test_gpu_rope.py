@@ -744,3 +744,77 @@ def test_a_bias_that_is_not_finite_stays_with_its_element(d, r, inter, dtype,
         if e < r:
             hit[e ^ 1 if inter else (e + r // 2) % r] = True
         assert torch.equal(~torch.isfinite(y), hit.expand_as(y)), e
+
+
+# rows of 31 units of fp32: one lane of the warp idle, 62 pieces of 16 bytes
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,r", [(248, 248), (248, 64), (240, 240), (232, 80)])
+def test_rows_of_nearly_a_warp(d, r, inter, dtype, norm):
+    T, hq, hk = 21, 5, 3
+    q, k = make(T, hq, hk, d, dtype, d + r)
+    dq, dk = make(T, hq, hk, d, dtype, d + r + 1)
+    rope = RotaryEmbedding(d, rotary_dim=r, interleaved=inter)
+    op = QKNormRotary(d, norm=norm, eps=1e-5, rotary=rope)
+    f, pos = O.frequencies(r)[0], np.arange(T) + 2
+    turned, y = rope.forward(q, k, offset=2), op.forward(q, k, offset=2)
+    for x, a, b in zip((q, k), turned, y):
+        within(flat(a), O.rotate(flat(x), pos, f, inter), rows_max(flat(x)),
+               K_ROPE, dtype)
+        rstd = O.normal(flat(x), norm, 1e-5)[1]
+        within(flat(b), O.forward(flat(x), pos, f, norm, 1e-5, None, None, inter),
+               rows_max(flat(x)) * rstd, K_NORM, dtype)
+    got = op.backward(dq, dk, q, k, offset=2)
+    check_gradients(op, q, k, dq, dk, None, None, pos, f, inter, dtype, got)
+
+
+def test_the_bindings_of_the_c_abi():
+    """The ctypes binding's functions give what the tensor calls give."""
+    T, H, d = 33, 4, 64
+    q, k = make(T, H, H, d, torch.bfloat16, 107)
+    dq, dk = make(T, H, H, d, torch.bfloat16, 108)
+    gamma = torch.linspace(0.5, 1.5, d, device="cuda")
+    rope = RotaryEmbedding(d)
+    op = QKNormRotary(d, norm="rms", rotary=rope)
+    heads = lambda t: B.tp_heads(t.data_ptr(), H * d, 0, d, H, H)
+    at = B.tp_positions(None, 0, 3, 10)
+    where = dict(offset=3, seq_len=10)
+    out = [torch.empty_like(q) for _ in range(2)]
+    v = [heads(t) for t in (q, out[0], k, out[1])]
+    for inverse, call in ((0, rope.forward), (1, rope.backward)):
+        B.tp_rope_apply(rope.handle, T, B.TPMLP_BF16, inverse, *v, at)
+        for a, b in zip(out, call(q, k, **where)):
+            assert torch.equal(a, b)
+    n = B.tp_qk_norm(B.TPQK_RMSNORM, 1e-6, gamma.data_ptr(), None,
+                     gamma.data_ptr(), None)
+    B.tp_qk_norm_forward(rope.handle, T, B.TPMLP_BF16, n, *v, at)
+    for a, b in zip(out, op.forward(q, k, gamma, gamma, **where)):
+        assert torch.equal(a, b)
+    par = [torch.empty(d, device="cuda") for _ in range(2)]
+    grads = B.tp_qk_norm_grads(par[0].data_ptr(), None, par[1].data_ptr(), None)
+    nbytes = B.tp_qk_norm_workspace_bytes(rope.handle)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    B.tp_qk_norm_backward(rope.handle, T, B.TPMLP_BF16, n, heads(dq), heads(q),
+                          v[1], heads(dk), heads(k), v[3], at, grads, ws, nbytes)
+    want = op.backward(dq, dk, q, k, gamma, gamma, **where)
+    for a, name in zip(out + par, ("dq", "dk", "dq_gamma", "dk_gamma")):
+        assert torch.equal(a, want[name]), name
+    with pytest.raises(B.TPMLPError):
+        B.tp_rope_apply(rope.handle, T, B.TPMLP_BF16, 2, *v, at)
+
+
+def test_millions_of_tokens():
+    """2^22 tokens of one short head: the same bits as in pieces of 2^16."""
+    T, d = 1 << 22, 8
+    g = torch.Generator("cuda").manual_seed(109)
+    q, dq = (torch.randn((T, 1, d), generator=g, device="cuda").bfloat16()
+             for _ in range(2))
+    op = QKNormRotary(d, rotary=RotaryEmbedding(d, rotary_dim=4))
+    y, _ = op.forward(q)
+    dx = op.backward(dq, None, q, None, param_grads=False)["dq"]
+    for t in range(0, T, 1 << 16):
+        part = slice(t, t + (1 << 16))
+        assert torch.equal(y[part], op.forward(q[part], offset=t)[0])
+        assert torch.equal(dx[part], op.backward(
+            dq[part], None, q[part], None, offset=t, param_grads=False)["dq"])

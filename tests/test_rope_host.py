@@ -482,3 +482,47 @@ def test_create_rejects_an_amplitude_beyond_fp32(lib, amp):
     assert lib.tp_rope_create(ctypes.byref(cfg),
                               ctypes.byref(h)) == B.TPMLP_OK
     assert lib.tp_rope_destroy(h) == B.TPMLP_OK
+
+
+def test_overlap_of_views_of_different_strides_against_brute_force(lib, handle):
+    """Two outputs in one buffer, each with strides, groups and heads of its own
+    (their token strides equal in half of the cases): none that share an element
+    are accepted."""
+    if torch.cuda.is_available():
+        pytest.skip("stand-in addresses must not reach a GPU")
+    g = np.random.default_rng(5)
+    d = 64
+    seen = {}
+    for n in range(6000):
+        T = int(g.integers(1, 5))
+
+        def view():
+            groups, group = int(g.integers(1, 4)), int(g.integers(1, 4))
+            strides, inside = [0, 0, 0], d + int(g.integers(0, 3)) * 16
+            for dim in g.permutation(3):            # nested in a random order
+                strides[dim] = inside
+                inside = inside * (T, groups, group)[dim] + \
+                    int(g.integers(0, 3)) * int(g.choice([16, 64]))
+            return strides, groups, group, inside
+        a, b = view(), view()
+        if g.random() < 0.5:
+            b[0][0] = a[0][0]
+        span = max(a[3], b[3])
+        shift = int(g.integers(-span, span))
+        if g.random() < 0.6:
+            shift -= shift % 16
+        heads_at = lambda v, at: B.tp_heads(FAKE * 64 + 2 * at, *v[0],
+                                            v[1] * v[2], v[2])
+        rows = lambda v, at: sorted(
+            at + t * v[0][0] + i * v[0][1] + j * v[0][2] for t in range(T)
+            for i in range(v[1]) for j in range(v[2]))
+        ra, rb = rows(a, 0), rows(b, shift)
+        own = lambda r: any(y - x < d for x, y in zip(r, r[1:]))
+        meets = own(ra) or own(rb) or any(abs(x - y) < d
+                                          for x in ra for y in rb)
+        rc = apply(lib, handle, heads(FAKE, H=a[1] * a[2], T=T), heads_at(a, 0),
+                   heads(2 * FAKE, H=b[1] * b[2], T=T), heads_at(b, shift), T=T)
+        refused = rc == B.TPMLP_ERR_ARG
+        assert refused or not meets, (T, a, b, shift, rc)
+        seen[meets, refused] = seen.get((meets, refused), 0) + 1
+    assert seen[True, True] > 1500 and seen[False, False] > 1000, seen
