@@ -299,3 +299,79 @@ def test_gradients_that_the_block_does_not_have_are_refused(norm, extra):
     assert set(n for n in g if n[1:3] in ("q_", "k_")) == \
         (set() if norm is None else {"dq_gamma", "dk_gamma"})
     m.close()
+
+
+@pytest.mark.parametrize("norm", [None, "rms", "layer"])
+def test_without_bias_gradients(norm):
+    """bias_grads=False leaves out db_qkv's pass and changes nothing else."""
+    w = W.ATTN_WORKLOADS["attn_tiny_d64"]
+    inp = {k: cuda(v) for k, v in W.make_attn_inputs(w, 3, True).items()}
+    m = TensorParallelAttention(w.hidden, w.heads, w.shards, w.tokens, w.seq,
+                                rotary=RotaryEmbedding(w.hidden // w.heads),
+                                qk_norm=norm)
+    m.forward(inp["X"], inp["Wqkv"], inp["Wo"], inp["bqkv"], inp["bo"])
+    args = (inp["dZ"], inp["X"], inp["Wqkv"], inp["Wo"])
+    full = m.backward(*args)
+    m.forward(inp["X"], inp["Wqkv"], inp["Wo"], inp["bqkv"], inp["bo"])
+    some = m.backward(*args, bias_grads=False)
+    assert m.check() == 0
+    assert set(full) - set(some) == {"dbqkv", "dbo"}
+    for k in some:
+        assert torch.equal(some[k], full[k]), k
+    m.close()
+
+
+def test_a_rotation_of_no_elements_is_the_plain_block():
+    w = W.ATTN_WORKLOADS["attn_tiny_d64"]
+    inp = {k: cuda(v) for k, v in W.make_attn_inputs(w, 4, True).items()}
+    out = []
+    for rope in (None, RotaryEmbedding(w.hidden // w.heads, rotary_dim=0)):
+        m = TensorParallelAttention(w.hidden, w.heads, w.shards, w.tokens,
+                                    w.seq, rotary=rope)
+        Z = m.forward(inp["X"], inp["Wqkv"], inp["Wo"], inp["bqkv"], inp["bo"])
+        g = m.backward(inp["dZ"], inp["X"], inp["Wqkv"], inp["Wo"])
+        assert m.check() == 0
+        out.append(dict(g, Z=Z))
+        m.close()
+    for k in out[0]:
+        if k != "dbqkv":    # (summed in another order)
+            assert torch.equal(out[0][k], out[1][k]), k
+    rel, _ = errors(out[1]["dbqkv"], f64(out[0]["dbqkv"]))
+    # the partials are of the values before, the pass after their rounding to
+    # bf16: off by at most half a step of each of the values that are summed
+    assert rel <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("norm", [None, "layer"])
+def test_a_captured_training_step(norm):
+    """Forward, backward and clipping in a graph, replayed on fresh inputs."""
+    w = W.ATTN_WORKLOADS["attn_tiny_d64"]
+    dim = w.hidden // w.heads
+    inp = {k: cuda(v) for k, v in W.make_attn_inputs(w, 5, True).items()}
+    make = lambda: TensorParallelAttention(w.hidden, w.heads, w.shards, w.tokens,
+                                           w.seq, rotary=RotaryEmbedding(dim),
+                                           qk_norm=norm)
+
+    def step(m, d):
+        Z = m.forward(d["X"], d["Wqkv"], d["Wo"], d["bqkv"], d["bo"])
+        g = m.backward(d["dZ"], d["X"], d["Wqkv"], d["Wo"])
+        return dict(g, Z=Z, norm=clip_grad_norm(g, 0.01))
+
+    m, plain = make(), make()
+    step(m, inp)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(m, inp)
+    for seed in (6, 7):
+        for k, v in W.make_attn_inputs(w, seed, True).items():
+            if v is not None:
+                inp[k].copy_(v)
+        graph.replay()
+        want = step(plain, inp)
+        torch.cuda.synchronize()
+        assert m.check() == 0 and plain.check() == 0
+        for k in want:
+            assert torch.equal(held[k], want[k]), k
+    m.close()
+    plain.close()

@@ -818,3 +818,54 @@ def test_millions_of_tokens():
         assert torch.equal(y[part], op.forward(q[part], offset=t)[0])
         assert torch.equal(dx[part], op.backward(
             dq[part], None, q[part], None, offset=t, param_grads=False)["dq"])
+
+
+@pytest.mark.parametrize("d,r", [(64, 64), (96, 48), (10, 6)])
+def test_broadcast_inputs(d, r):
+    """One row (or one token, or one head) shown as many by strides of zero."""
+    T, H = 19, 5
+    g = torch.Generator("cuda").manual_seed(110)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    op = QKNormRotary(d, norm="layer", rotary=RotaryEmbedding(d, rotary_dim=r))
+    for shape in ((1, 1, d), (1, H, d), (T, 1, d)):
+        q, k = n(*shape).expand(T, H, d), n(*shape).expand(T, H, d)
+        dq, dk = n(*shape).expand(T, H, d), n(*shape).expand(T, H, d)
+        full = [t.contiguous() for t in (q, k, dq, dk)]
+        for call in (op.rotary.forward, op.forward):
+            for a, b in zip(call(q, k), call(*full[:2])):
+                assert torch.equal(a, b)
+        a = op.backward(dq, dk, q, k)
+        b = op.backward(full[2], full[3], full[0], full[1])
+        for name in a:
+            assert torch.equal(a[name], b[name]), name
+
+
+def test_threads_side_by_side():
+    """One object called from several threads, each with a stream of its own."""
+    import threading
+    op = QKNormRotary(96, norm="layer", rotary=RotaryEmbedding(96))
+    data = [make(500, 8, 4, 96, torch.bfloat16, 120 + i) +
+            make(500, 8, 4, 96, torch.bfloat16, 130 + i) for i in range(4)]
+    want = [op.backward(d[2], d[3], d[0], d[1], offset=i)
+            for i, d in enumerate(data)]
+    streams = [torch.cuda.Stream() for _ in data]
+    torch.cuda.synchronize()
+    got = [[] for _ in data]
+
+    def work(i):
+        d = data[i]
+        for _ in range(30):
+            got[i].append(op.backward(d[2], d[3], d[0], d[1], offset=i,
+                                      stream=streams[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert len(g) == 30
+        for made in g:
+            for n in w:
+                assert torch.equal(made[n], w[n])
