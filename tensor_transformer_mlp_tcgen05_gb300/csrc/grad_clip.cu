@@ -12,7 +12,7 @@
 // blocks, which exchange their sums through distributed shared memory: 4 KB 4.1 us
 // (three launches: 5.7), 256 KB 4.8 (6.2), 500 KB 5.8 (6.7).
 //
-// GB300: 1.26 GB of fp32 into other tensors in 546 us (1.26 GB read for the norm at
+// GB300: 1.26 GB of fp32 into other tensors in 545 us (1.26 GB read for the norm at
 // 7.1 TB/s, then read and written at 6.8 TB/s; the floor of one read and one write is
 // 370), 50 MB in 24 us (floor 14.8), 8 MB in 7.5.
 #include <algorithm>
@@ -29,7 +29,8 @@ namespace {
 // 16-byte vectors a thread loads at once.
 constexpr int BATCH = 8;
 constexpr int THREADS = 256;
-constexpr int BLOCKS = 608;            // four on each of the 152 SMs
+constexpr int BLOCKS = 608;            // four on each of a GB300's 152 SMs (a
+                                       // constant: it orders the sums)
 constexpr int CHUNK_BYTES = 16 * BATCH * THREADS;
 // Tensors of one launch: the table travels as a kernel parameter (16 KB; one of
 // SMALL_TABLE, 2 KB, where that is enough: 500 KB in 8 tensors 6.7 us, with the

@@ -3,8 +3,8 @@
 // A Python module that checks the tensors of a call, makes its outputs and
 // workspace, and calls tp_rope.h / tp_grad.h.  It computes nothing.  These
 // operators take a few microseconds on the GPU for a few tokens, and the same
-// steps in Python and ctypes took 21 us around a library call of 4 us (32
-// tokens of 16 + 16 heads, Grace host): here they take about 3.
+// steps in Python and ctypes took 21 us around a library call of 4.1 us (32
+// tokens of 16 + 16 heads, Grace host): here they take 1.6.
 //
 // The library's functions come by address from the ctypes binding (bind), so
 // that whichever build of libtpmlp the binding loaded is the one called.

@@ -14,8 +14,9 @@ namespace qk {
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int MAX_PAIRS = TPROPE_MAX_HEAD_DIM / 2;
-// Blocks of the backward kernel (four on each of the 152 SMs; a constant, so
-// that the order of the parameter gradients' sums depends on the shapes only).
+// Blocks of the backward kernel (four on each of a GB300's 152 SMs; a constant,
+// so that the order of the parameter gradients' sums depends on the shapes only
+// and not on the device).
 constexpr int BWD_BLOCKS = 608;
 
 // tp_heads for the kernels.  A head's group is umulhi(head, magic) with magic =

@@ -22,18 +22,23 @@
 //           apart so that neighbouring lanes touch neighbouring bits.
 //
 // 8192 tokens, bf16, 201 MB in and out (floor 30 us; gradient 45 us), GB300, us:
-//                              rotation   RMS norm   its gradient
-//   24 + 24 heads of 128  OWN       32.8       33.5       51.5
-//                      PIECES       33.2       38.1       60.5
-//                        BITS       51.0       63.2      105.3
-//   32 + 32 heads of 96 PIECES      35.0       42.8       68.7
-//                        BITS       56.8       71.0      120.1
+//                              rotation   RMS norm  LayerNorm  gradients of both
+//   24 + 24 heads of 128  OWN       32.8       33.5       38.5       51.4   60.0
+//                      PIECES       33.2       38.1                  60.5
+//                        BITS       51.0       63.2                 105.3
+//   32 + 32 heads of 96 PIECES      34.8       42.8       49.8       68.6   95.1
+//                        BITS       56.8       71.0                 120.1
+//   40 + 40 heads of 72   BITS      46.3       60.5       72.6      101.7  129.2
+//   (the last: 189 MB, floors 28 and 42)
 //   (with 48 of the 96 rotated, lanes copying their own vectors, which are then
 //   no whole sectors, took 43.7 for the rotation, PIECES 34.7)
 //
-// What bounds it: memory, where heads fill lanes exactly; instruction issue
-// elsewhere (half the issue slots are used at the four or five blocks an SM that
-// the coefficients' registers allow).
+// What bounds it: memory, where heads fill lanes exactly.  Elsewhere latency: a
+// step is a chain of reads from shared memory, one or two trees of dependent
+// shuffles (RMS norm, LayerNorm) and writes, and the coefficients' registers
+// leave an SM 16 to 20 warps to hide it with (LayerNorm of 2047 tokens of 32 + 32
+// heads of 96: 48 % of the issue slots used with 20 % of the warps, stalled on
+// fixed latencies and on shared memory).  BITS predicates every bit besides.
 //
 // Angles: a frequency is held as turns per position in 64-bit fixed point
 // (2^-64 of a turn), so position times frequency modulo one turn is one
@@ -879,7 +884,10 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(KIND, NORM))
 // Persistent blocks, so that a lane sums its unit's parameter gradients over
 // all its rows in registers; a block takes q's tasks or k's.  Four blocks an SM:
 // with three (more registers) the LayerNorm gradient of 8192 tokens of 24 + 24
-// heads of 128 takes 72 us instead of 60.
+// heads of 128 takes 72 us instead of 60.  Four leave 128 registers a thread, at
+// which gradients of the LayerNorm spill: OWN in bf16 4 to 12 bytes, PIECES in
+// bf16 64, BITS 44 to 120 (of the RMS norm 4 to 40); OWN and PIECES in fp32, and
+// the forward but for 4 bytes in one of its BITS variants, nothing.
 // GPT-3-13B-shaped layer, RMS: 79.5 us with the sums, 503 MB, 6.3 TB/s (177 with
 // rows loaded when they were needed).
 template <class T, Kind KIND, int NORM, bool INTER, int LEN>

@@ -393,10 +393,10 @@ int steps_per_task(int steps, int tokens, long long want, int most) {
 }
 
 // A task's start (angles, coefficients, first loads) costs about as much as two
-// steps.  Forward: tokens are split until 12 warps a SM have work (2047 tokens of
-// 14 steps: 16.6 us whole, 17.5 in halves, 20.2 in fifths), and into tasks of at
-// most 16 steps (4096 tokens of 56 steps: 82.6 us whole, 73.2 in halves, 71.9 in
-// thirds; 8192 of 20: 54.8 whole, 52.2 in halves).
+// steps.  Forward: tokens are split until 12 warps a SM (of a GB300's 152) have
+// work (2047 tokens of 14 steps: 16.6 us whole, 17.5 in halves, 20.2 in fifths),
+// and into tasks of at most 16 steps (4096 tokens of 56 steps: 82.6 us whole, 73.2
+// in halves, 71.9 in thirds; 8192 of 20: 54.8 whole, 52.2 in halves).
 constexpr long long FORWARD_TASKS = 152 * 12;
 constexpr int FORWARD_STEPS = 16;
 // Backward: until the resident blocks have a task for every warp, and into tasks
