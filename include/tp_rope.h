@@ -26,9 +26,10 @@
  * - Element types: queries and keys bf16 (TPMLP_BF16) or fp32 (TPMLP_FP32),
  *   gamma, beta and their gradients fp32; all arithmetic fp32, one rounding
  *   to the element type.  (A row's sum of squares too: a row whose root mean
- *   square is past 1e18, or below 1e-18 with an eps of 0, leaves its range.)  Angles are made in 64-bit fixed point: p f_i, f_i
- *   being the double that tp_rope_frequencies gives (up to 2^40), is within
- *   2^-33 + |p| 2^-64 of a turn, then rounded to fp32.
+ *   square is past 1e18, or below 1e-18 with an eps of 0, leaves its range.)
+ *   Angles are made in 64-bit fixed point: p f_i, f_i being the double that
+ *   tp_rope_frequencies gives (up to 2^40), is within 2^-33 + |p| 2^-64 of a
+ *   turn, then rounded to fp32.
  * - Pointers are DEVICE pointers the caller owns (tp_rope_config's inv_freq
  *   and the structs are host memory, read during the call only); the library
  *   never allocates device memory.  Calls only enqueue work on `stream`.
