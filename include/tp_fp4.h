@@ -1,0 +1,133 @@
+/*
+ * tp_fp4.h - C ABI of libtpmlp's four-bit operators on one GB300 (sm_103a):
+ * microscaled quantisation, the product of two quantised matrices, and the MLP
+ * block's forward on four-bit weights.  Status codes, tp_mlp_status_string() and
+ * tp_mlp_last_detail() are shared with tp_mlp.h.
+ *
+ * A matrix [rows, cols] is quantised along its rows in blocks of consecutive
+ * elements (the last block of a row may be short).  An element is an E2M1 code
+ * (0 .5 1 1.5 2 3 4 6 with a sign); a block has one scale:
+ *
+ *   TPFP4_NV   blocks of 16, scale s in E4M3, one power of two g for the matrix:
+ *              s    = e4m3(amax / (6 g))      nearest even, at most 448
+ *              code = e2m1(x / (s g))         nearest even, at most 6
+ *              value = code s g.  g is given, or the smallest power of two
+ *              with max |x| <= 2688 g (1 for a matrix of zeros; infinities and
+ *              NaNs are not counted).  A block whose s is 0 has codes of 0.
+ *   TPFP4_MX   blocks of 32, scale s = 2^e in E8M0 (Open Compute Project,
+ *              "Microscaling Formats (MX)", v1.0): e = floor(log2 amax) - 2, at
+ *              least -127 (s = 1 for a block of zeros), code = e2m1(x / s),
+ *              value = code s; g = 1.
+ *
+ * Quotients are not rounded before the code is chosen: every code is the one
+ * the definition gives (a code of zero may have either sign).  A block that holds
+ * an infinity or a NaN has the scale's NaN, and its values are NaN.
+ *
+ * The product of A [T, K] and B [N, K], both quantised along K in the same
+ * format, is C[t, n] = g_A g_B sum_k A[t, k] B[n, k] (+ bias[n]): the tensor
+ * cores multiply the codes and the blocks' scales exactly and add in fp32; one
+ * rounding to C's type.  Repeated calls are bit-identical.
+ *
+ * Conventions
+ * -----------
+ * - Plain matrices are bf16 (TPMLP_BF16) or fp32 (TPMLP_FP32), row-major with
+ *   any row stride >= the number of columns, aligned to their element; 32-byte
+ *   aligned rows are read fastest.  A packed matrix is one buffer of
+ *   tp_fp4_bytes bytes, 256-byte aligned, whose first 256 bytes hold g and the
+ *   status word of the products that read it as A.
+ * - rows and cols are 1 .. 2^28 (rows of a plain matrix: 0 .. 2^28).
+ * - Pointers are DEVICE pointers the caller owns; the library never allocates
+ *   device memory.  Calls only enqueue work on `stream`.  No output shares
+ *   memory with an input (TPMLP_ERR_ARG).  Every function returns a status
+ *   code and touches no output when argument validation fails.
+ */
+#ifndef TP_FP4_H_
+#define TP_FP4_H_
+
+#include <stddef.h>
+
+#include "tp_mlp.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define TPFP4_NV 0
+#define TPFP4_MX 1
+
+/* Bytes of a packed [rows, cols] matrix (0 for a bad format or size), and the
+ * offsets of its parts (-1 likewise):
+ *   TPFP4_CODES   row r at r * pitch, pitch = 16 ceil(cols / 32) bytes; element
+ *                 c in the low (c even) or high nibble of byte c / 2; zeros
+ *                 past cols
+ *   TPFP4_SCALES  one byte a block, in tiles of 128 rows x 256 columns, tile
+ *                 (r / 128, c / 256) at ((r / 128) ceil(cols / 256) + c / 256)
+ *                 * bytes of a tile (2048 NV, 1024 MX); inside it the scale of
+ *                 block b = (c mod 256) / 16 (NV) or / 32 (MX) of row r at
+ *                 (b / 4) 512 + (r mod 32) 16 + ((r mod 128) / 32) 4 + b mod 4 */
+size_t tp_fp4_bytes(long long rows, long long cols, int format);
+long long tp_fp4_offset(long long rows, long long cols, int format, int which);
+#define TPFP4_CODES  0
+#define TPFP4_SCALES 1
+
+/* Quantise x [rows, cols] along its rows into a packed [rows, cols], or
+ * (transpose = 1) along its columns into a packed [cols, rows], the transposed
+ * matrix.
+ *   scale    NV: g, a power of two from 2^-126 to 2^127, or 0 to take it from
+ *            the matrix (x is read twice); MX: 0 or 1
+ *   colsum   [cols] fp32, the sums of x's columns (a bias gradient, in a fixed
+ *            order; transpose = 1 only), or NULL
+ *   workspace  tp_fp4_colsum_workspace_bytes(rows, cols) bytes, 16-byte
+ *            aligned, used only with colsum
+ * rows = 0 (transpose = 0) enqueues nothing. */
+int tp_fp4_quantize(long long rows, long long cols, int dtype, const void* x,
+                    long long row_stride, int transpose, int format,
+                    double scale, void* packed, size_t packed_bytes,
+                    float* colsum, void* workspace, size_t workspace_bytes,
+                    void* stream);
+size_t tp_fp4_colsum_workspace_bytes(long long rows, long long cols);
+
+/* The values of a packed [rows, cols] matrix, written as `dtype` (exact in bf16
+ * too, but for values out of its range). */
+int tp_fp4_dequantize(long long rows, long long cols, int format,
+                      const void* packed, size_t packed_bytes, int dtype,
+                      void* out, long long row_stride, void* stream);
+
+/* C [T, N] (`dtype`, row stride ldc) from packed A [T, K] and B [N, K].  bias
+ * [N] fp32 or NULL.  T = 0 enqueues nothing. */
+int tp_fp4_matmul(long long T, long long N, long long K, int format,
+                  const void* A, size_t a_bytes, const void* B, size_t b_bytes,
+                  const float* bias, int dtype, void* C, long long ldc,
+                  void* stream);
+
+/* Waits for `stream`, then reads and clears the status word of a packed matrix
+ * that products read as A: TPMLP_OK, TPMLP_ERR_TIMEOUT (a bounded device wait
+ * gave up; that product's C is undefined) or TPMLP_ERR_CUDA. */
+int tp_fp4_check(void* packed, void* stream);
+
+/* ---- the MLP block's forward on four-bit weights ------------------------
+ *   Xq = quantised Xn (= LayerNorm(X) rounded to bf16, or X), H = Xq Aq + b1,
+ *   Y = GeLU(H) (fp32), Yq = quantised Y, Z = Yq Bq + b2 [+ X], one rounding to
+ * bf16.  A and B are quantised along the products' inner dimension (NV: g from
+ * each); x_scale and y_scale are NV's g of Xn and Y (MX: 0 or 1).  The t shards
+ * are consecutive ranges of the second product's one sum, so Z does not depend
+ * on t.  The handle must be TPMLP_BF16 without dropout (TPMLP_ERR_ARG). */
+size_t tp_fp4_mlp_weights_bytes(const tp_mlp_handle* handle, int format);
+int tp_fp4_mlp_pack_weights(tp_mlp_handle* handle, int format, const void* A,
+                            const void* B, void* packed, size_t packed_bytes,
+                            void* stream);
+size_t tp_fp4_mlp_workspace_bytes(const tp_mlp_handle* handle, int tokens,
+                                  int format);
+/* Arguments as tp_mlp_forward_fp8; packed and workspace 256-byte aligned;
+ * tp_mlp_check reads the status. */
+int tp_fp4_mlp_forward(tp_mlp_handle* handle, int tokens, int format,
+                       const void* X, const void* packed, const float* bias1,
+                       const float* bias2, const float* ln_gamma,
+                       const float* ln_beta, double x_scale, double y_scale,
+                       void* Z, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* TP_FP4_H_ */

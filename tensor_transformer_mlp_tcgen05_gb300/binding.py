@@ -57,13 +57,19 @@ EXPORTED = (
     "tp_attn_forward_qk", "tp_attn_backward_qk",
 )
 
-# The same for tp_rope.h and tp_grad.h.
+# The same for tp_rope.h, tp_grad.h and tp_fp4.h.
 EXPORTED_ROPE = (
     "tp_rope_create", "tp_rope_destroy", "tp_rope_frequencies",
     "tp_rope_apply", "tp_qk_norm_forward", "tp_qk_norm_workspace_bytes",
     "tp_qk_norm_backward",
 )
 EXPORTED_GRAD = ("tp_grad_workspace_bytes", "tp_grad_norm", "tp_grad_clip")
+EXPORTED_FP4 = (
+    "tp_fp4_bytes", "tp_fp4_offset", "tp_fp4_quantize",
+    "tp_fp4_colsum_workspace_bytes", "tp_fp4_dequantize", "tp_fp4_matmul",
+    "tp_fp4_check", "tp_fp4_mlp_weights_bytes", "tp_fp4_mlp_pack_weights",
+    "tp_fp4_mlp_workspace_bytes", "tp_fp4_mlp_forward",
+)
 
 TPROPE_MAX_HEAD_DIM = 256
 TPROPE_SCALE_NONE = 0
@@ -73,6 +79,11 @@ TPROPE_SCALE_YARN = 3
 TPROPE_SCALE_CUSTOM = 4
 TPQK_RMSNORM = 1
 TPQK_LAYERNORM = 2
+
+TPFP4_NV = 0
+TPFP4_MX = 1
+TPFP4_CODES = 0
+TPFP4_SCALES = 1
 
 TPMLP_FP8_PACK_SCALES = 0
 TPMLP_FP8_PACK_AQT = 1
@@ -317,6 +328,32 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.tp_grad_clip.argtypes = [_i, _vp, ctypes.c_double, ctypes.c_double, _vp,
                                _vp, _sz, _vp]
     L.tp_grad_clip.restype = _i
+    ll, dbl = ctypes.c_longlong, ctypes.c_double
+    L.tp_fp4_bytes.argtypes = [ll, ll, _i]
+    L.tp_fp4_bytes.restype = _sz
+    L.tp_fp4_offset.argtypes = [ll, ll, _i, _i]
+    L.tp_fp4_offset.restype = ll
+    L.tp_fp4_colsum_workspace_bytes.argtypes = [ll, ll]
+    L.tp_fp4_colsum_workspace_bytes.restype = _sz
+    L.tp_fp4_quantize.argtypes = [ll, ll, _i, _vp, ll, _i, _i, dbl, _vp, _sz,
+                                  _vp, _vp, _sz, _vp]
+    L.tp_fp4_quantize.restype = _i
+    L.tp_fp4_dequantize.argtypes = [ll, ll, _i, _vp, _sz, _i, _vp, ll, _vp]
+    L.tp_fp4_dequantize.restype = _i
+    L.tp_fp4_matmul.argtypes = [ll, ll, ll, _i, _vp, _sz, _vp, _sz, _vp, _i,
+                                _vp, ll, _vp]
+    L.tp_fp4_matmul.restype = _i
+    L.tp_fp4_check.argtypes = [_vp, _vp]
+    L.tp_fp4_check.restype = _i
+    L.tp_fp4_mlp_weights_bytes.argtypes = [_vp, _i]
+    L.tp_fp4_mlp_weights_bytes.restype = _sz
+    L.tp_fp4_mlp_pack_weights.argtypes = [_vp, _i, _vp, _vp, _vp, _sz, _vp]
+    L.tp_fp4_mlp_pack_weights.restype = _i
+    L.tp_fp4_mlp_workspace_bytes.argtypes = [_vp, _i, _i]
+    L.tp_fp4_mlp_workspace_bytes.restype = _sz
+    L.tp_fp4_mlp_forward.argtypes = [_vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     dbl, dbl, _vp, _vp, _sz, _vp]
+    L.tp_fp4_mlp_forward.restype = _i
     if path is None:
         _lib = L
     return L
@@ -346,7 +383,9 @@ def tensor_calls():
             for n in ("tp_rope_apply", "tp_qk_norm_forward",
                       "tp_qk_norm_workspace_bytes", "tp_qk_norm_backward",
                       "tp_grad_workspace_bytes", "tp_grad_norm",
-                      "tp_grad_clip")])
+                      "tp_grad_clip", "tp_fp4_bytes", "tp_fp4_quantize",
+                      "tp_fp4_colsum_workspace_bytes", "tp_fp4_dequantize",
+                      "tp_fp4_matmul")])
         _calls = m
     return _calls
 
@@ -766,3 +805,69 @@ def tp_grad_clip(count, tensors, max_norm, eps, norm, workspace,
     _check(lib().tp_grad_clip(count, tensors, max_norm, eps, _ptr(norm),
                               _ptr(workspace), workspace_bytes,
                               _stream(stream)), "tp_grad_clip")
+
+
+# ------------------------------------------------------------- four bits --
+
+def tp_fp4_bytes(rows: int, cols: int, format: int) -> int:
+    return int(lib().tp_fp4_bytes(rows, cols, format))
+
+
+def tp_fp4_offset(rows: int, cols: int, format: int, which: int) -> int:
+    return int(lib().tp_fp4_offset(rows, cols, format, which))
+
+
+def tp_fp4_colsum_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().tp_fp4_colsum_workspace_bytes(rows, cols))
+
+
+def tp_fp4_quantize(rows, cols, dtype, x, row_stride, transpose, format, scale,
+                    packed, packed_bytes, colsum=None, workspace=None,
+                    workspace_bytes=0, stream=None):
+    _check(lib().tp_fp4_quantize(
+        rows, cols, dtype, _ptr(x), row_stride, transpose, format, scale,
+        _ptr(packed), packed_bytes, _ptr(colsum), _ptr(workspace),
+        workspace_bytes, _stream(stream)), "tp_fp4_quantize")
+
+
+def tp_fp4_dequantize(rows, cols, format, packed, packed_bytes, dtype, out,
+                      row_stride, stream=None):
+    _check(lib().tp_fp4_dequantize(
+        rows, cols, format, _ptr(packed), packed_bytes, dtype, _ptr(out),
+        row_stride, _stream(stream)), "tp_fp4_dequantize")
+
+
+def tp_fp4_matmul(T, N, K, format, A, a_bytes, B, b_bytes, bias, dtype, C, ldc,
+                  stream=None):
+    _check(lib().tp_fp4_matmul(
+        T, N, K, format, _ptr(A), a_bytes, _ptr(B), b_bytes, _ptr(bias), dtype,
+        _ptr(C), ldc, _stream(stream)), "tp_fp4_matmul")
+
+
+def tp_fp4_check(packed, stream=None) -> int:
+    return int(lib().tp_fp4_check(_ptr(packed), _stream(stream)))
+
+
+def tp_fp4_mlp_weights_bytes(handle, format: int) -> int:
+    return int(lib().tp_fp4_mlp_weights_bytes(handle, format))
+
+
+def tp_fp4_mlp_pack_weights(handle, format, A, B, packed, packed_bytes,
+                            stream=None):
+    _check(lib().tp_fp4_mlp_pack_weights(
+        handle, format, _ptr(A), _ptr(B), _ptr(packed), packed_bytes,
+        _stream(stream)), "tp_fp4_mlp_pack_weights")
+
+
+def tp_fp4_mlp_workspace_bytes(handle, tokens: int, format: int) -> int:
+    return int(lib().tp_fp4_mlp_workspace_bytes(handle, tokens, format))
+
+
+def tp_fp4_mlp_forward(handle, tokens, format, X, packed, bias1, bias2,
+                       ln_gamma, ln_beta, x_scale, y_scale, Z, workspace,
+                       workspace_bytes, stream=None):
+    _check(lib().tp_fp4_mlp_forward(
+        handle, tokens, format, _ptr(X), _ptr(packed), _ptr(bias1),
+        _ptr(bias2), _ptr(ln_gamma), _ptr(ln_beta), x_scale, y_scale, _ptr(Z),
+        _ptr(workspace), workspace_bytes, _stream(stream)),
+        "tp_fp4_mlp_forward")

@@ -9,8 +9,8 @@ newer than every source and header.  The library needs the CUDA toolkit only.
 
 Next to it goes ``_pycall``, a Python module (host C++, built against the
 installed torch, whose C++ layouts it holds: the versions of Python and torch are
-in its file's name) with the tensor calls of ``rotary.py`` and ``clip.py``.  Where
-torch is not installed it is left out; where it does not compile, build() says
+in its file's name) with the tensor calls of ``rotary.py``, ``clip.py`` and
+``fp4.py``.  Where torch is not installed it is left out; where it does not compile, build() says
 so once the library is linked.
 
 ``build(checks=True)`` makes the debug variant ``libtpmlp_checks.so`` (objects
@@ -41,7 +41,8 @@ SOURCES = ["gemm_tc2.cu", "rowops.cu", "simt.cu",
            "tp_mlp_host.cu", "noalloc.cu", "attn_fwd.cu", "attn_bwd.cu",
            "attn_host.cu", "fp8.cu", "probe.cu",
            "qk_rows.cu", "qk_rows_bf16.cu", "qk_rows_fp32.cu", "rope_host.cu",
-           "grad_clip.cu"]
+           "grad_clip.cu", "fp4_quant.cu", "fp4_gemm.cu", "fp4_split.cu",
+           "fp4_host.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
           "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]
@@ -55,7 +56,8 @@ def nvcc_path() -> str:
 
 
 HEADERS = [os.path.join(INCLUDE, f) for f in ("tp_mlp.h", "tp_attn.h",
-                                              "tp_rope.h", "tp_grad.h")]
+                                              "tp_rope.h", "tp_grad.h",
+                                              "tp_fp4.h")]
 
 
 def _inputs():

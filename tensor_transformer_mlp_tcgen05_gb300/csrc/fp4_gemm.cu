@@ -1,0 +1,535 @@
+// The four-bit product on CTA pairs: C = g_A g_B A B^T with A [M, K] and
+// B [N, K] packed (E2M1 codes, a scale for 16 or 32 elements of K), 256 x 256
+// output tiles, persistent.
+//
+// The tensor cores take the scales with the operands (tcgen05.mma .block_scale):
+// an MMA of K = 64 reads 32 bytes of codes a row and its 4 (NV) or 2 (MX) scale
+// bytes a row from tensor memory, where tcgen05.cp puts them; the matrices'
+// layout of scales is the one that copy reads, so that they go from global to
+// tensor memory untouched.  Per k-tile (256 elements) a CTA loads its 128 rows
+// of A and of B (16 KB each), its own rows' scales (2 KB, NV) and the scales of
+// all 256 rows of B (4 KB): each SM multiplies its A rows with the B columns
+// of both.
+//
+// 12 warps: warp 0 loads (one lane), warp 1 of the even CTA copies scales and
+// issues the MMAs (one lane), warps 4-11 are the epilogue: warp w takes TMEM
+// lanes 32 (w mod 4) on and one 128-column half.
+//
+// Tensor memory: two accumulators of 256 columns would fill all 512, and the
+// scales need 48.  So the second one starts at column 208, over the last 48 of
+// the first: the MMAs of tile j + 1 may start once tile j's part of the shared
+// 48 columns has been read, which the warps that own them do first.
+//
+//   full[s]   (even CTA) bytes of stage s landed in both CTAs
+//   empty[s]  (each CTA) the MMAs have read stage s
+//   tfull     (each CTA) tile j's accumulator is ready
+//   shared    (even CTA) 16 arrivals, one a warp of the pair: it has read all of
+//             tile j - 1 and its part of tile j's shared columns.
+// Every wait is bounded, as in gemm_tc2.cu: on expiry TPMLP_ERR_TIMEOUT goes to
+// the status word, the roles stop and tensor memory is freed.
+#include <climits>
+
+#include "fp4_gemm.cuh"
+#include "host_common.cuh"
+
+namespace tpmlp {
+namespace fp4 {
+namespace {
+
+using namespace gemm;
+
+constexpr int PM = 256, PN = 256;   // a pair's tile
+constexpr int HM = 128, HN = 128;   // rows of A and of B a CTA loads
+constexpr int STAGES = 5;
+constexpr int NUM_THREADS = 384;
+constexpr int NUM_EPI_WARPS = 8;
+constexpr int FIRST_EPI_WARP = 4;
+constexpr int REGS_LAUNCH = 168;
+constexpr int REGS_CONTROL = 56;
+constexpr int REGS_EPILOGUE = 224;
+static_assert(REGS_CONTROL * 128 + REGS_EPILOGUE * 256 <=
+                  REGS_LAUNCH * NUM_THREADS,
+              "register split exceeds the launch allocation");
+constexpr uint32_t OPERAND_BYTES = HM * 128;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t ACC_STEP = 208;   // the second accumulator's first column
+constexpr uint32_t T_SA = 464, T_SB = 480;
+constexpr int NUM_BARRIERS = 2 * STAGES + 3;   // full, empty, tfull, shared, done
+constexpr uint32_t STAGING_BYTES = NUM_EPI_WARPS * STAGE_CHUNK_BYTES;
+constexpr unsigned long long ABORT_SETTLE_NS = 2000000ull;
+
+template <int FORMAT>
+constexpr uint32_t stage_bytes() {
+  return 2 * OPERAND_BYTES + 3 * tile_bytes(FORMAT);
+}
+template <int FORMAT>
+constexpr size_t smem_bytes() {
+  return 1024 + size_t(STAGES) * stage_bytes<FORMAT>() + STAGING_BYTES +
+         NUM_BARRIERS * 8 + 16;
+}
+static_assert(smem_bytes<TPFP4_NV>() <= 227 * 1024, "shared memory budget");
+
+__device__ __forceinline__ void cta_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(NUM_THREADS) : "memory");
+}
+
+// wait_bounded with cluster-scope acquire (arrivals from both CTAs).
+__device__ __forceinline__ bool wait_bounded_cluster(uint32_t bar,
+                                                     uint32_t parity,
+                                                     const Ctl& c, int role) {
+  if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (true) {
+    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    if (*c.abort_flag) return false;
+    if (ptx::globaltimer_ns() - t0 > c.budget) {
+      *c.abort_flag = 1;
+      if (atomicCAS(c.status, 0, TPMLP_ERR_TIMEOUT) == 0) {
+        c.status[1] = role;
+        c.status[2] = static_cast<int>(blockIdx.x);
+      }
+      __threadfence();
+      return false;
+    }
+  }
+}
+
+// bias[c0 .. c0 + 64) of which n are in the matrix.
+__device__ __forceinline__ void add_bias(const float* bias, int c0, int n,
+                                         float (&v)[64]) {
+  if (bias == nullptr) return;
+  if (n >= 64 && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0) {
+    add_bias_n(bias, c0, v, 64);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    if (i < n) v[i] += __ldg(bias + c0 + i);
+}
+
+// One warp's staging buffer: 32 rows of 128 bytes (16-byte unit u of row r at
+// unit u ^ r mod 8), written out by TMA, or, where the output's rows are not
+// 16-byte aligned, by the warp, row by row.
+struct Stager {
+  uint32_t buf;
+  int lane;
+
+  __device__ __forceinline__ void write(const uint32_t* w) {
+    const uint32_t row = buf + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      ptx::st_shared_v4(row + static_cast<uint32_t>(c ^ (lane & 7)) * 16u,
+                        w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
+  __device__ __forceinline__ void put_tma(const CUtensorMap* map, int c0, int r0,
+                                          const uint32_t* w) {
+    if (lane == 0) ptx::bulk_wait_read<0>();
+    __syncwarp();
+    write(w);
+    ptx::fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      ptx::tma_store_2d(map, buf, c0, r0);
+      ptx::bulk_commit();
+    }
+  }
+  // rows and cols: what of the chunk is in the matrix
+  template <bool F32>
+  __device__ __forceinline__ void put_rows(void* out, long long ld, int c0, int r0,
+                                           int rows, int cols, const uint32_t* w) {
+    __syncwarp();
+    write(w);
+    __syncwarp();
+    for (int r = 0; r < min(rows, 32); ++r) {
+      const uint32_t word = ptx::ld_shared_u32(
+          buf + static_cast<uint32_t>(r) * 128u +
+          static_cast<uint32_t>((lane >> 2) ^ (r & 7)) * 16u + (lane & 3) * 4u);
+      if constexpr (F32) {
+        if (lane < cols)
+          static_cast<float*>(out)[(r0 + r) * ld + c0 + lane] =
+              __uint_as_float(word);
+      } else {
+        auto* p = static_cast<unsigned short*>(out) + (r0 + r) * ld + c0 + 2 * lane;
+        if (2 * lane < cols) p[0] = static_cast<unsigned short>(word);
+        if (2 * lane + 1 < cols) p[1] = static_cast<unsigned short>(word >> 16);
+      }
+    }
+  }
+  __device__ __forceinline__ void drain() {
+    if (lane == 0) ptx::bulk_wait_all();
+    __syncwarp();
+  }
+};
+
+// 64 columns of a row, GeLU taken, quantised and stored.
+template <int FORMAT>
+__device__ __forceinline__ void store_fp4(const Packed& y, int row, int c0,
+                                          float inv_g, const float (&v)[64]) {
+  constexpr int BLOCK = block_size(FORMAT);
+  constexpr int BLOCKS = 64 / BLOCK;
+  uint32_t word = 0, c[8];
+#pragma unroll
+  for (int b = 0; b < BLOCKS; ++b) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < BLOCK; ++i) amax = max(amax, abs_bits(v[b * BLOCK + i]));
+    const Scale s = block_scale<FORMAT>(amax, inv_g);
+    word |= s.byte << (8 * b);
+#pragma unroll
+    for (int i = 0; i < BLOCK / 16; ++i) {
+      const uint2 w = codes16<FORMAT, true>(v + b * BLOCK + 16 * i, s);
+      c[b * BLOCK / 8 + 2 * i] = w.x;
+      c[b * BLOCK / 8 + 2 * i + 1] = w.y;
+    }
+  }
+  uint4* dst = reinterpret_cast<uint4*>(y.codes + row * y.pitch + c0 / 2);
+  dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
+  dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
+  const int block = c0 % TILE_COLS / BLOCK;
+  uint8_t* to = y.scales + scale_word(row, c0 / TILE_COLS, block / 4, y.ktiles,
+                                      tile_bytes(FORMAT)) + block % 4;
+  if constexpr (FORMAT == TPFP4_NV)
+    *reinterpret_cast<uint32_t*>(to) = word;
+  else
+    *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(word);
+}
+
+// Scales of 64 columns past the matrix, which its products read with zero codes.
+template <int FORMAT>
+__device__ __forceinline__ void store_no_scales(const Packed& y, int row, int c0) {
+  const int block = c0 % TILE_COLS / block_size(FORMAT);
+  uint8_t* to = y.scales + scale_word(row, c0 / TILE_COLS, block / 4, y.ktiles,
+                                      tile_bytes(FORMAT)) + block % 4;
+  if constexpr (FORMAT == TPFP4_NV)
+    *reinterpret_cast<uint32_t*>(to) = 0u;
+  else
+    *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(0x7f7fu);
+}
+
+template <int FORMAT, int EPI>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    product_pairs_kernel(const __grid_constant__ CUtensorMap tmA,
+                         const __grid_constant__ CUtensorMap tmSA,
+                         const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmSB,
+                         const __grid_constant__ CUtensorMap tmO,
+                         const ProductArgs args, const int tma_out,
+                         const int group_m) {
+  constexpr uint32_t TILE = tile_bytes(FORMAT);
+  constexpr uint32_t STAGE = stage_bytes<FORMAT>();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s_a = ptx::smem_u32(smem);
+  const uint32_t s_b = s_a + STAGES * OPERAND_BYTES;
+  const uint32_t s_epi = s_b + STAGES * OPERAND_BYTES;
+  const uint32_t s_sa = s_epi + STAGING_BYTES;
+  const uint32_t s_sb = s_sa + STAGES * TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + size_t(STAGES) * STAGE +
+                                               STAGING_BYTES);
+  const uint32_t full0 = ptx::smem_u32(bars);
+  const uint32_t empty0 = full0 + 8u * STAGES;
+  const uint32_t tfull = empty0 + 8u * STAGES;
+  const uint32_t shared = tfull + 8u;
+  const uint32_t done_bar = shared + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARRIERS);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t prank = ptx::cluster_ctarank();
+  const bool leader = prank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int num_pairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(full0 + 8u * s, 1);
+      ptx::mbar_init(empty0 + 8u * s, 1);
+    }
+    ptx::mbar_init(tfull, 1);
+    ptx::mbar_init(shared, 2 * NUM_EPI_WARPS);
+    ptx::mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmSA);
+    ptx::prefetch_tmap(&tmB);
+    ptx::prefetch_tmap(&tmSB);
+    if (EPI != OUT_GELU_FP4 && tma_out) ptx::prefetch_tmap(&tmO);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), TMEM_COLS);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();   // barriers of both CTAs initialised, TMEM allocated
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  const Ctl ctl{abort_flag, args.status, args.budget_ns};
+  const int num_m = (args.M + PM - 1) / PM;
+  const int num_n = (args.N + PN - 1) / PN;
+  const int tiles = num_m * num_n;
+  const int ktiles = args.a.ktiles;
+  const uint32_t lead_full0 = ptx::mapa_shared(full0, 0u);
+  const uint32_t lead_shared = ptx::mapa_shared(shared, 0u);
+
+  if (warp < FIRST_EPI_WARP) {
+    ptx::setmaxnreg_dec<REGS_CONTROL>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------- producer --
+      uint32_t stage = 0, phase = 0;
+      bool alive = true;
+      for (int tile = pair; alive && tile < tiles; tile += num_pairs) {
+        int mb, nb;
+        tile_coords(tile, num_m, num_n, group_m, mb, nb);
+        const int m0 = mb * PM + static_cast<int>(prank) * HM;
+        const int n0 = nb * PN + static_cast<int>(prank) * HN;
+        // scale tiles; ones past the matrix are filled with zeros
+        const int sa0 = (m0 / TILE_ROWS) * ktiles;
+        const int sb0 = (nb * PN / TILE_ROWS) * ktiles;
+        for (int kt = 0; kt < ktiles; ++kt) {
+          if (!wait_bounded(empty0 + 8u * stage, phase ^ 1u, ctl,
+                            ROLE_PRODUCER)) {
+            alive = false;
+            break;
+          }
+          if (leader) ptx::mbar_arrive_expect_tx(full0 + 8u * stage, 2 * STAGE);
+          const uint32_t fb = lead_full0 + 8u * stage;
+          ptx::tma_load_2d_pair(s_a + stage * OPERAND_BYTES, &tmA, fb, kt * 128, m0);
+          ptx::tma_load_2d_pair(s_b + stage * OPERAND_BYTES, &tmB, fb, kt * 128, n0);
+          ptx::tma_load_2d_pair(s_sa + stage * TILE, &tmSA, fb, 0, sa0 + kt);
+          ptx::tma_load_2d_pair(s_sb + stage * 2 * TILE, &tmSB, fb, 0, sb0 + kt);
+          ptx::tma_load_2d_pair(s_sb + stage * 2 * TILE + TILE, &tmSB, fb, 0,
+                                sb0 + ktiles + kt);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    } else if (warp == 1 && lane == 0 && leader) {
+      // -------------------------------------------------- MMA issuer --
+      constexpr uint16_t pair_mask = 0x3;
+      uint32_t stage = 0, phase = 0, j = 0;
+      bool alive = true;
+      for (int tile = pair; alive && tile < tiles; tile += num_pairs, ++j) {
+        if (j > 0 && !wait_bounded_cluster(shared, (j - 1u) & 1u, ctl, ROLE_MMA)) {
+          alive = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + (j & 1u) * ACC_STEP;
+        for (int kt = 0; kt < ktiles; ++kt) {
+          if (!wait_bounded(full0 + 8u * stage, phase, ctl, ROLE_MMA)) {
+            alive = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          ktile_mmas<FORMAT, 2, PM, PN, 2>(
+              d, s_a + stage * OPERAND_BYTES, s_b + stage * OPERAND_BYTES,
+              s_sa + stage * TILE, s_sb + stage * 2 * TILE, tmem_base + T_SA,
+              tmem_base + T_SB, kt == 0);
+          ptx::mma_commit_pair(empty0 + 8u * stage, pair_mask);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (alive) ptx::mma_commit_pair(tfull, pair_mask);
+      }
+      if (*reinterpret_cast<volatile int*>(abort_flag)) {
+        // Wait for every MMA this thread issued before TMEM is freed.
+        ptx::mma_commit_pair(done_bar, static_cast<uint16_t>(1u << prank));
+        wait_teardown(done_bar, 0);
+      }
+    }
+    // ------------------------------------------------------ teardown --
+    cta_barrier();
+    if (*reinterpret_cast<volatile int*>(abort_flag) && warp == 0 &&
+        lane == 0) {
+      // copies may still land here, counted on the peer's barrier
+      const uint64_t t0 = ptx::globaltimer_ns();
+      while (ptx::globaltimer_ns() - t0 < ABORT_SETTLE_NS) {
+      }
+    }
+    cta_barrier();
+    ptx::cluster_sync();
+    if (warp == 1) {
+      __syncwarp();
+      ptx::tc_fence_after();
+      ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+  } else {
+    ptx::setmaxnreg_inc<REGS_EPILOGUE>();
+    // ------------------------------------------------------ epilogue --
+    const int ew = warp - FIRST_EPI_WARP;
+    const int q = warp & 3;      // TMEM sub-partition this warp may read
+    const int half = ew >> 2;    // which 128-column half of the tile
+    Stager st{s_epi + static_cast<uint32_t>(ew) * STAGE_CHUNK_BYTES, lane};
+    const float g = args.a.head->g * args.b.head->g;
+    float inv_gy = 1.f;
+    if constexpr (EPI == OUT_GELU_FP4) {
+      inv_gy = exp2_of(-args.y_exponent);
+      if (blockIdx.x == 0 && threadIdx.x == FIRST_EPI_WARP * 32) {
+        args.y.head->g = exp2_of(args.y_exponent);
+        for (int i = 0; i < 4; ++i) args.y.head->status[i] = 0;
+      }
+    }
+    uint32_t j = 0;
+    for (int tile = pair; tile < tiles; tile += num_pairs, ++j) {
+      int mb, nb;
+      tile_coords(tile, num_m, num_n, group_m, mb, nb);
+      const int row0 = mb * PM + static_cast<int>(prank) * HM + q * 32;
+      const int row = row0 + lane;
+      const int col_base = nb * PN + half * 128;
+      bool ok = wait_bounded(tfull, j & 1u, ctl, ROLE_EPILOGUE);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                             (j & 1u) * ACC_STEP + half * 128;
+      // the shared columns: of the first accumulator its last 48, of the second
+      // its first
+      const bool owner = half == 1 - static_cast<int>(j & 1u);
+      auto release = [&] {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            ptx::mbar_arrive(shared);
+          else
+            ptx::mbar_arrive_cluster(lead_shared);
+        }
+      };
+      if (!owner) release();
+#pragma unroll 1
+      for (int jj = 0; jj < 2; ++jj) {
+        const int chunk = owner && half == 1 ? 1 - jj : jj;
+        const int c0 = col_base + chunk * 64;
+        uint32_t r0[32], r1[32];
+        ptx::tmem_ld_32x32b_x32(taddr + chunk * 64, r0);
+        ptx::tmem_ld_32x32b_x32(taddr + chunk * 64 + 32, r1);
+        ptx::tmem_ld_wait();
+        if (owner && jj == 0) release();
+        if (row0 >= args.M) continue;
+        if (c0 >= args.N) {
+          if constexpr (EPI == OUT_GELU_FP4) {
+            if (row < args.M && c0 < args.y.ktiles * TILE_COLS)
+              store_no_scales<FORMAT>(args.y, row, c0);
+          }
+          continue;
+        }
+        const int n = args.N - c0;
+        float v[64];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          v[i] = __uint_as_float(r0[i]) * g;
+          v[32 + i] = __uint_as_float(r1[i]) * g;
+        }
+        add_bias(args.bias, c0, n, v);
+        if constexpr (EPI == OUT_GELU_FP4) {
+#pragma unroll
+          for (int i = 0; i < 64; i += 2)
+            gelu2_f32(v[i], v[i + 1], args.gelu_mode);
+          if (row < args.M) store_fp4<FORMAT>(args.y, row, c0, inv_gy, v);
+        } else if constexpr (EPI == OUT_BF16) {
+          add_residual_bf16(args.residual, args.ldr, row, args.M, c0, v, 64);
+          uint32_t w[32];
+          pack_bf16x64(v, w);
+          if (tma_out)
+            st.put_tma(&tmO, c0, row0, w);
+          else
+            st.put_rows<false>(args.out, args.ldo, c0, row0, args.M - row0, n, w);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[32 * k + i]);
+            if (n <= 32 * k) continue;
+            if (tma_out)
+              st.put_tma(&tmO, c0 + 32 * k, row0, w);
+            else
+              st.put_rows<true>(args.out, args.ldo, c0 + 32 * k, row0,
+                                args.M - row0, n - 32 * k, w);
+          }
+        }
+      }
+    }
+    st.drain();
+    cta_barrier();
+    cta_barrier();
+    ptx::cluster_sync();
+  }
+}
+
+template <int FORMAT, int EPI>
+cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tsa,
+                         const CUtensorMap& tb, const CUtensorMap& tsb,
+                         const CUtensorMap* to, const ProductArgs& args,
+                         int max_pairs, cudaStream_t s) {
+  auto kern = product_pairs_kernel<FORMAT, EPI>;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * NUM_THREADS <
+      REGS_CONTROL * 128 + REGS_EPILOGUE * NUM_EPI_WARPS * 32)
+    return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem_bytes<FORMAT>()));
+  if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>((args.M + PM - 1) / PM) *
+                          ((args.N + PN - 1) / PN);
+  if (tiles > INT_MAX / 2) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = smem_bytes<FORMAT>();
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(
+      2 * (tiles < max_pairs ? tiles : static_cast<long long>(max_pairs))));
+  e = cudaLaunchKernelEx(&cfg, kern, ta, tsa, tb, tsb, to != nullptr ? *to : ta,
+                         args, to != nullptr ? 1 : 0, 8);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int FORMAT>
+cudaError_t launch_format(const CUtensorMap& ta, const CUtensorMap& tsa,
+                          const CUtensorMap& tb, const CUtensorMap& tsb,
+                          const CUtensorMap* to, const ProductArgs& args,
+                          int max_pairs, cudaStream_t s) {
+  switch (args.epilogue) {
+    case OUT_BF16:
+      return launch_pairs<FORMAT, OUT_BF16>(ta, tsa, tb, tsb, to, args, max_pairs, s);
+    case OUT_FP32:
+      return launch_pairs<FORMAT, OUT_FP32>(ta, tsa, tb, tsb, to, args, max_pairs, s);
+    default:
+      return launch_pairs<FORMAT, OUT_GELU_FP4>(ta, tsa, tb, tsb, nullptr, args,
+                                                max_pairs, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_product_pairs(int format, const CUtensorMap& ta,
+                                 const CUtensorMap& tsa, const CUtensorMap& tb,
+                                 const CUtensorMap& tsb, const CUtensorMap* to,
+                                 const ProductArgs& args, int max_pairs,
+                                 cudaStream_t s) {
+  return format == TPFP4_NV
+             ? launch_format<TPFP4_NV>(ta, tsa, tb, tsb, to, args, max_pairs, s)
+             : launch_format<TPFP4_MX>(ta, tsa, tb, tsb, to, args, max_pairs, s);
+}
+
+}  // namespace fp4
+}  // namespace tpmlp

@@ -1,0 +1,75 @@
+// Launchers of the four-bit kernels (host side).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fp4.cuh"
+
+namespace tpmlp {
+namespace fp4 {
+
+// "g is the matrix's own", where launches take its exponent.
+constexpr int AUTO_SCALE = 1 << 20;
+
+// head->amax = max(head->amax, the largest finite |x|) over x [rows, cols].
+cudaError_t launch_amax(bool bf16, const void* x, long long stride,
+                        long long rows, long long cols, Header* head,
+                        cudaStream_t s);
+
+// x [p.rows, p.cols] into p; g = 2^g_exponent, or from p.head->amax
+// (AUTO_SCALE).  With a given exponent the header is written whole.
+cudaError_t launch_quantize_rows(bool bf16, int format, const void* x,
+                                 long long stride, const Packed& p,
+                                 int g_exponent, cudaStream_t s);
+
+// x [x_rows = p.cols, p.rows], transposed, into p.  part (nullable):
+// [p.ktiles][p.rows] sums of x's columns over 256 rows each.
+cudaError_t launch_quantize_columns(bool bf16, int format, const void* x,
+                                    long long stride, int x_rows,
+                                    const Packed& p, int g_exponent,
+                                    float* part, cudaStream_t s);
+
+cudaError_t launch_dequantize(const Packed& p, int format, bool bf16, void* out,
+                              long long stride, cudaStream_t s);
+
+// What becomes of a product's elements.
+enum Epilogue4 : int {
+  OUT_BF16 = 0,
+  OUT_FP32 = 1,
+  OUT_GELU_FP4 = 2,   // GeLU, quantised along its rows into `y`
+};
+
+// C = g_A g_B A B^T (+ bias), then the epilogue.
+struct ProductArgs {
+  Packed a, b;          // [M, K], [N, K]
+  int M, N;
+  int epilogue;
+  void* out;            // [M, N], row stride ldo (OUT_BF16, OUT_FP32)
+  long long ldo;
+  const float* bias;    // [N] or null
+  const void* residual; // OUT_BF16: [M, N] bf16 of row stride ldr, added before
+  long long ldr;        // the rounding; or null
+  Packed y;             // OUT_GELU_FP4
+  int y_exponent;       // NV: y's g
+  int gelu_mode;
+  int* status;
+  unsigned long long budget_ns;
+};
+
+// Tiles of 256 x 256 on CTA pairs, for many rows of A and B.
+cudaError_t launch_product_pairs(int format, const CUtensorMap& ta,
+                                 const CUtensorMap& tsa, const CUtensorMap& tb,
+                                 const CUtensorMap& tsb, const CUtensorMap* to,
+                                 const ProductArgs& args, int max_pairs,
+                                 cudaStream_t s);
+
+// Tiles of 128 rows of B x up to 256 rows of A, K split over a cluster, for
+// few rows of A or few tiles.
+int split_tokens(int M);   // rows of A in a tile
+cudaError_t launch_product_split(int format, const CUtensorMap& ta,
+                                 const CUtensorMap& tsa, const CUtensorMap& tb,
+                                 const CUtensorMap& tsb, const ProductArgs& args,
+                                 int sms, cudaStream_t s);
+
+}  // namespace fp4
+}  // namespace tpmlp

@@ -1,0 +1,541 @@
+// Four-bit quantisation and its inverse: HBM-bound passes over a plain matrix.
+//
+//   rows        one read of x, codes and scales written: (2 + 9/16) bytes an
+//               element of bf16 (NV)
+//   transposed  the same, through shared memory: x is read along its rows, the
+//               codes of a column are consecutive
+//   amax        the largest finite |x| of a matrix whose g is its own
+//   dequantise  the values, as bf16 or fp32
+#include "fp4_kernels.h"
+
+namespace tpmlp {
+namespace fp4 {
+namespace {
+
+constexpr int THREADS = 256;
+
+template <class T>
+struct Raw;   // 16 elements as loaded
+template <>
+struct Raw<__nv_bfloat16> {
+  uint32_t w[8];
+  __device__ void floats(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {   // bf16 is the upper half of fp32
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw<float> {
+  uint32_t w[16];
+  __device__ void floats(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+  }
+};
+
+// LD: bytes of a load (32 and 16: every 16-element unit starts on such a
+// boundary), or 0 for loads of single elements.
+template <int LD, int WORDS>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[WORDS]) {
+  if constexpr (LD == 32) {
+#pragma unroll
+    for (int i = 0; i < WORDS / 8; ++i)
+      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[8 * i]), "=r"(w[8 * i + 1]), "=r"(w[8 * i + 2]),
+                     "=r"(w[8 * i + 3]), "=r"(w[8 * i + 4]), "=r"(w[8 * i + 5]),
+                     "=r"(w[8 * i + 6]), "=r"(w[8 * i + 7])
+                   : "l"(static_cast<const char*>(p) + 32 * i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS / 4; ++i) {
+      const uint4 u = __ldg(static_cast<const uint4*>(p) + i);
+      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t element_bits(const __nv_bfloat16* p) {
+  return static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p)))
+         << 16;
+}
+__device__ __forceinline__ uint32_t element_bits(const float* p) {
+  return __ldg(reinterpret_cast<const unsigned int*>(p));
+}
+
+// 16 elements from p, the first n of them in the row (n may be negative: none).
+template <class T, int LD>
+__device__ __forceinline__ void load16(const T* p, int n, Raw<T>& r) {
+  constexpr int WORDS = sizeof(r.w) / 4;
+  if (LD != 0 && n >= 16) {
+    load_words<LD == 0 ? 16 : LD, WORDS>(p, r.w);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      r.w[i] = i < n ? element_bits(p + i) : 0u;
+    } else {
+      const uint32_t lo = 2 * i < n ? element_bits(p + 2 * i) >> 16 : 0u;
+      const uint32_t hi = 2 * i + 1 < n ? element_bits(p + 2 * i + 1) : 0u;
+      r.w[i] = lo | hi;
+    }
+  }
+}
+
+// 1 / g, from the matrix's amax or as given; block 0 writes the header.
+__device__ __forceinline__ float inverse_g(const Packed& p, int given) {
+  const bool automatic = given == AUTO_SCALE;
+  const int e = automatic ? auto_exponent(p.head->amax) : given;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.head->g = exp2_of(e);
+    if (!automatic) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p.head->status[i] = 0;
+    }
+  }
+  return exp2_of(-e);
+}
+
+// ------------------------------------------------------------------- rows --
+
+// A thread takes 16 elements of a row (a block of NV, half of one of MX), 16
+// threads 256 columns, a block 16 rows at a time and PASSES times those.
+template <class T, int FORMAT, int LD, int PASSES>
+__global__ void __launch_bounds__(THREADS)
+    rows_kernel(const T* __restrict__ x, long long stride, const Packed p,
+                int g_exponent) {
+  const int lane = threadIdx.x & 31;
+  const int unit = threadIdx.x & 15;
+  const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.ktiles));
+  const int chunk = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.ktiles));
+  const int row0 = chunk * 16 * PASSES + static_cast<int>(threadIdx.x >> 4);
+  const int col = kt * TILE_COLS + unit * 16;
+  Raw<T> raw[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int row = row0 + 16 * i;
+    load16<T, LD>(x + row * stride + col, row < p.rows ? p.cols - col : 0,
+                  raw[i]);
+  }
+  const float inv_g = FORMAT == TPFP4_NV ? inverse_g(p, g_exponent)
+                                         : (inverse_g(p, 0), 1.f);
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int row = row0 + 16 * i;
+    float v[16];
+    raw[i].floats(v);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) amax = max(amax, abs_bits(v[k]));
+    if constexpr (FORMAT == TPFP4_MX)
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const Scale s = block_scale<FORMAT>(amax, inv_g);
+    const uint2 c = codes16<FORMAT, sizeof(T) == 4>(v, s);
+    // four blocks' scale bytes in one word
+    uint32_t word;
+    if constexpr (FORMAT == TPFP4_NV) {
+      word = s.byte << (8 * (lane & 3));
+      word |= __shfl_xor_sync(0xffffffffu, word, 1);
+      word |= __shfl_xor_sync(0xffffffffu, word, 2);
+    } else {
+      word = s.byte << (8 * ((lane >> 1) & 3));
+      word |= __shfl_xor_sync(0xffffffffu, word, 2);
+      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    }
+    if (row < p.rows) {
+      const int byte = kt * (TILE_COLS / 2) + unit * 8;
+      if (byte < p.pitch)
+        *reinterpret_cast<uint2*>(p.codes + row * p.pitch + byte) = c;
+      constexpr int THREADS_A_WORD = FORMAT == TPFP4_NV ? 4 : 8;
+      if (unit % THREADS_A_WORD == 0)
+        *reinterpret_cast<uint32_t*>(
+            p.scales + scale_word(row, kt, unit / THREADS_A_WORD, p.ktiles,
+                                  tile_bytes(FORMAT))) = word;
+    }
+  }
+}
+
+// ------------------------------------------------------------- transposed --
+
+// Two consecutive elements from p, of which n are in the row.
+template <bool PAIR>
+__device__ __forceinline__ void load2(const __nv_bfloat16* p, int n, float& a,
+                                      float& b) {
+  if (PAIR && n >= 2) {
+    const uint32_t w = __ldg(reinterpret_cast<const unsigned int*>(p));
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+    return;
+  }
+  a = n >= 1 ? __uint_as_float(element_bits(p)) : 0.f;
+  b = n >= 2 ? __uint_as_float(element_bits(p + 1)) : 0.f;
+}
+template <bool PAIR>
+__device__ __forceinline__ void load2(const float* p, int n, float& a, float& b) {
+  if (PAIR && n >= 2) {
+    const float2 w = __ldg(reinterpret_cast<const float2*>(p));
+    a = w.x, b = w.y;
+    return;
+  }
+  a = n >= 1 ? __ldg(p) : 0.f;
+  b = n >= 2 ? __ldg(p + 1) : 0.f;
+}
+
+constexpr int T_COLS = 64;   // columns of x a block takes
+
+// A block takes 256 rows (one k-tile of the packed matrix) of 64 columns, a
+// warp 32 of those rows, a lane two columns: its 32 elements of a column are
+// two blocks of NV or one of MX.  Codes and scales go through shared memory,
+// so that a packed row's 128 bytes of codes are written together.
+template <class T, int FORMAT, bool PAIR>
+__global__ void __launch_bounds__(THREADS, 2)
+    columns_kernel(const T* __restrict__ x, long long stride, int x_rows,
+                   const Packed p, int g_exponent, float* __restrict__ part) {
+  // 16-byte unit u of row n at unit u ^ (n / 2 mod 8): the lanes of a warp,
+  // two rows apart, write to different banks
+  __shared__ uint4 s_codes[T_COLS * 8];
+  __shared__ __align__(16) uint8_t s_scales[T_COLS * 16];
+  __shared__ float s_sum[8][T_COLS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = (p.rows + T_COLS - 1) / T_COLS;
+  const int n0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(tiles)) * T_COLS;
+  const int kt = static_cast<int>(blockIdx.x / static_cast<unsigned>(tiles));
+  const int k0 = kt * TILE_COLS + warp * 32;
+  const int n = n0 + 2 * lane;
+  float v[2][32];
+  const T* src = x + k0 * stride + n;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    load2<PAIR>(src + i * stride, k0 + i < x_rows ? p.rows - n : 0, v[0][i],
+                v[1][i]);
+  const float inv_g = FORMAT == TPFP4_NV ? inverse_g(p, g_exponent)
+                                         : (inverse_g(p, 0), 1.f);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = 2 * lane + j;
+    uint32_t top[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top[i / 16] = max(top[i / 16], abs_bits(v[j][i]));
+    uint2 c0, c1;
+    if constexpr (FORMAT == TPFP4_NV) {
+      const Scale a = block_scale<FORMAT>(top[0], inv_g);
+      const Scale b = block_scale<FORMAT>(top[1], inv_g);
+      c0 = codes16<FORMAT, sizeof(T) == 4>(v[j], a);
+      c1 = codes16<FORMAT, sizeof(T) == 4>(v[j] + 16, b);
+      *reinterpret_cast<uint16_t*>(s_scales + r * 16 + warp * 2) =
+          static_cast<uint16_t>(a.byte | (b.byte << 8));
+    } else {
+      const Scale a = block_scale<FORMAT>(max(top[0], top[1]), inv_g);
+      c0 = codes16<FORMAT, sizeof(T) == 4>(v[j], a);
+      c1 = codes16<FORMAT, sizeof(T) == 4>(v[j] + 16, a);
+      s_scales[r * 16 + warp] = static_cast<uint8_t>(a.byte);
+    }
+    s_codes[r * 8 + (warp ^ (lane & 7))] = make_uint4(c0.x, c0.y, c1.x, c1.y);
+    if (part != nullptr) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum += v[j][i];
+      s_sum[warp][r] = sum;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < T_COLS * 8 / THREADS; ++i) {
+    const int at = i * THREADS + threadIdx.x;
+    const int r = at >> 3, u = at & 7;
+    const int byte = kt * (TILE_COLS / 2) + u * 16;
+    if (n0 + r < p.rows && byte < p.pitch)
+      *reinterpret_cast<uint4*>(p.codes + (n0 + r) * p.pitch + byte) =
+          s_codes[r * 8 + (u ^ ((r >> 1) & 7))];
+  }
+  constexpr int WORDS = TILE_COLS / block_size(FORMAT) / 4;
+  if (threadIdx.x < T_COLS * WORDS) {
+    const int r = threadIdx.x / WORDS, q = threadIdx.x % WORDS;
+    if (n0 + r < p.rows)
+      *reinterpret_cast<uint32_t*>(
+          p.scales + scale_word(n0 + r, kt, q, p.ktiles, tile_bytes(FORMAT))) =
+          *reinterpret_cast<const uint32_t*>(s_scales + r * 16 + q * 4);
+  }
+  if (part != nullptr && threadIdx.x < T_COLS &&
+      n0 + static_cast<int>(threadIdx.x) < p.rows) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += s_sum[w][threadIdx.x];
+    part[static_cast<size_t>(kt) * p.rows + n0 + threadIdx.x] = sum;
+  }
+}
+
+// ------------------------------------------------------------------- amax --
+
+__device__ __forceinline__ uint32_t finite(uint32_t bits) {
+  return bits < 0x7f800000u ? bits : 0u;
+}
+
+// An item is AMAX_UNITS units of 16 elements in a row; a block takes every
+// gridDim-th item.  A maximum does not depend on the order, nor the result on
+// the atomics'.
+constexpr int AMAX_UNITS = 2 * THREADS;
+
+template <class T, int LD>
+__global__ void __launch_bounds__(THREADS)
+    amax_kernel(const T* __restrict__ x, long long stride, long long rows,
+                long long cols, Header* head) {
+  const long long segments = (cols + AMAX_UNITS * 16 - 1) / (AMAX_UNITS * 16);
+  uint32_t top = 0;
+  for (long long item = blockIdx.x; item < rows * segments; item += gridDim.x) {
+    const long long row = item / segments;
+    const long long c0 = (item - row * segments) * (AMAX_UNITS * 16);
+    Raw<T> raw[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long c = c0 + (i * THREADS + threadIdx.x) * 16ll;
+      load16<T, LD>(x + row * stride + c,
+                    static_cast<int>(max(0ll, min(16ll, cols - c))), raw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v[16];
+      raw[i].floats(v);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) top = max(top, finite(abs_bits(v[k])));
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  __shared__ uint32_t s_top[THREADS / 32];
+  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < THREADS / 32; ++i) top = max(top, s_top[i]);
+    atomicMax(&head->amax, top);
+  }
+}
+
+// ------------------------------------------------------------- dequantise --
+
+template <class T>
+__device__ __forceinline__ void store16(T* p, int n, bool wide,
+                                        const float (&v)[16]) {
+  if (wide && n >= 16) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(
+            pack_bf16x2(v[8 * i], v[8 * i + 1]),
+            pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+            pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+            pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<float4*>(p)[i] =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < n) {
+      if constexpr (sizeof(T) == 2)
+        p[i] = __float2bfloat16_rn(v[i]);
+      else
+        p[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ void values8(uint32_t w, float scale, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(
+        static_cast<uint8_t>(w >> (8 * i)), __NV_E2M1);
+    const float2 f = __half22float2(__half2(h));
+    v[2 * i] = f.x * scale;
+    v[2 * i + 1] = f.y * scale;
+  }
+}
+
+template <class T, int FORMAT, int PASSES>
+__global__ void __launch_bounds__(THREADS)
+    dequantize_kernel(const Packed p, T* __restrict__ out, long long stride,
+                      bool wide) {
+  const int unit = threadIdx.x & 15;
+  const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.ktiles));
+  const int chunk = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.ktiles));
+  const int row0 = chunk * 16 * PASSES + static_cast<int>(threadIdx.x >> 4);
+  const int col = kt * TILE_COLS + unit * 16;
+  if (col >= p.cols) return;
+  const float g = p.head->g;
+  uint2 c[PASSES];
+  uint32_t byte[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int row = row0 + 16 * i;
+    if (row >= p.rows) break;
+    c[i] = __ldg(reinterpret_cast<const uint2*>(p.codes + row * p.pitch + col / 2));
+    const int b = unit * 16 / block_size(FORMAT);
+    byte[i] = __ldg(p.scales + scale_word(row, kt, b / 4, p.ktiles,
+                                          tile_bytes(FORMAT)) + b % 4);
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int row = row0 + 16 * i;
+    if (row >= p.rows) break;
+    // code * s is exact; g is a power of two
+    const float s = scale_value<FORMAT>(byte[i]);
+    float v[16];
+    values8(c[i].x, s, v);
+    values8(c[i].y, s, v + 8);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] *= g;
+    store16(out + row * stride + col, p.cols - col, wide, v);
+  }
+}
+
+// ---------------------------------------------------------------- launches --
+
+bool on_boundary(const void* p, long long stride_bytes, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride_bytes)) %
+             bytes == 0;
+}
+
+// Blocks that keep all SMs busy: with fewer, a block takes fewer rows.
+constexpr long long FULL_GRID = 152 * 4;
+
+template <class T, int FORMAT, int LD>
+void rows_launch(const T* x, long long stride, const Packed& p, int g,
+                 cudaStream_t s) {
+  const long long units = (p.rows + 15ll) / 16 * p.ktiles;
+  if (units >= 4 * FULL_GRID)
+    rows_kernel<T, FORMAT, LD, 4><<<
+        static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), THREADS, 0, s>>>(
+        x, stride, p, g);
+  else
+    rows_kernel<T, FORMAT, LD, 1><<<static_cast<unsigned>(units), THREADS, 0, s>>>(
+        x, stride, p, g);
+}
+
+template <class T, int FORMAT>
+void rows_format(const T* x, long long stride, const Packed& p, int g,
+                 cudaStream_t s) {
+  const long long bytes = stride * static_cast<long long>(sizeof(T));
+  if (on_boundary(x, bytes, 32))
+    rows_launch<T, FORMAT, 32>(x, stride, p, g, s);
+  else if (on_boundary(x, bytes, 16))
+    rows_launch<T, FORMAT, 16>(x, stride, p, g, s);
+  else
+    rows_launch<T, FORMAT, 0>(x, stride, p, g, s);
+}
+
+template <class T, int FORMAT>
+void columns_format(const T* x, long long stride, int x_rows, const Packed& p,
+                    int g, float* part, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(
+      (p.rows + static_cast<long long>(T_COLS) - 1) / T_COLS * p.ktiles);
+  if (on_boundary(x, stride * static_cast<long long>(sizeof(T)), 2 * sizeof(T)))
+    columns_kernel<T, FORMAT, true>
+        <<<grid, THREADS, 0, s>>>(x, stride, x_rows, p, g, part);
+  else
+    columns_kernel<T, FORMAT, false>
+        <<<grid, THREADS, 0, s>>>(x, stride, x_rows, p, g, part);
+}
+
+template <class T>
+void amax_type(const T* x, long long stride, long long rows, long long cols,
+               Header* head, cudaStream_t s) {
+  if (stride == cols) {   // one long row
+    cols *= rows;
+    stride = cols;
+    rows = 1;
+  }
+  const long long items =
+      (cols + AMAX_UNITS * 16 - 1) / (AMAX_UNITS * 16) * rows;
+  const unsigned grid =
+      static_cast<unsigned>(items < 4 * 152 ? items : 4 * 152);
+  const long long bytes = rows == 1 ? 0 : stride * static_cast<long long>(sizeof(T));
+  if (on_boundary(x, bytes, 32))
+    amax_kernel<T, 32><<<grid, THREADS, 0, s>>>(x, stride, rows, cols, head);
+  else if (on_boundary(x, bytes, 16))
+    amax_kernel<T, 16><<<grid, THREADS, 0, s>>>(x, stride, rows, cols, head);
+  else
+    amax_kernel<T, 0><<<grid, THREADS, 0, s>>>(x, stride, rows, cols, head);
+}
+
+template <class T>
+void dequantize_type(const Packed& p, int format, T* out, long long stride,
+                     cudaStream_t s) {
+  constexpr int PASSES = 4;
+  const unsigned grid = static_cast<unsigned>(
+      (p.rows + 16ll * PASSES - 1) / (16 * PASSES) * p.ktiles);
+  const bool wide =
+      on_boundary(out, stride * static_cast<long long>(sizeof(T)), 16);
+  if (format == TPFP4_NV)
+    dequantize_kernel<T, TPFP4_NV, PASSES><<<grid, THREADS, 0, s>>>(p, out, stride, wide);
+  else
+    dequantize_kernel<T, TPFP4_MX, PASSES><<<grid, THREADS, 0, s>>>(p, out, stride, wide);
+}
+
+}  // namespace
+
+cudaError_t launch_amax(bool bf16, const void* x, long long stride,
+                        long long rows, long long cols, Header* head,
+                        cudaStream_t s) {
+  if (bf16)
+    amax_type(static_cast<const __nv_bfloat16*>(x), stride, rows, cols, head, s);
+  else
+    amax_type(static_cast<const float*>(x), stride, rows, cols, head, s);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_quantize_rows(bool bf16, int format, const void* x,
+                                 long long stride, const Packed& p,
+                                 int g_exponent, cudaStream_t s) {
+  if (bf16) {
+    const auto* b = static_cast<const __nv_bfloat16*>(x);
+    if (format == TPFP4_NV)
+      rows_format<__nv_bfloat16, TPFP4_NV>(b, stride, p, g_exponent, s);
+    else
+      rows_format<__nv_bfloat16, TPFP4_MX>(b, stride, p, g_exponent, s);
+  } else {
+    const auto* f = static_cast<const float*>(x);
+    if (format == TPFP4_NV)
+      rows_format<float, TPFP4_NV>(f, stride, p, g_exponent, s);
+    else
+      rows_format<float, TPFP4_MX>(f, stride, p, g_exponent, s);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_quantize_columns(bool bf16, int format, const void* x,
+                                    long long stride, int x_rows,
+                                    const Packed& p, int g_exponent,
+                                    float* part, cudaStream_t s) {
+  if (bf16) {
+    const auto* b = static_cast<const __nv_bfloat16*>(x);
+    if (format == TPFP4_NV)
+      columns_format<__nv_bfloat16, TPFP4_NV>(b, stride, x_rows, p, g_exponent, part, s);
+    else
+      columns_format<__nv_bfloat16, TPFP4_MX>(b, stride, x_rows, p, g_exponent, part, s);
+  } else {
+    const auto* f = static_cast<const float*>(x);
+    if (format == TPFP4_NV)
+      columns_format<float, TPFP4_NV>(f, stride, x_rows, p, g_exponent, part, s);
+    else
+      columns_format<float, TPFP4_MX>(f, stride, x_rows, p, g_exponent, part, s);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dequantize(const Packed& p, int format, bool bf16, void* out,
+                              long long stride, cudaStream_t s) {
+  if (bf16)
+    dequantize_type(p, format, static_cast<__nv_bfloat16*>(out), stride, s);
+  else
+    dequantize_type(p, format, static_cast<float*>(out), stride, s);
+  return cudaGetLastError();
+}
+
+}  // namespace fp4
+}  // namespace tpmlp

@@ -1,7 +1,7 @@
-// _pycall: the tensor calls of rotary.py and clip.py.
+// _pycall: the tensor calls of rotary.py, clip.py and fp4.py.
 //
 // A Python module that checks the tensors of a call, makes its outputs and
-// workspace, and calls tp_rope.h / tp_grad.h.  It computes nothing.  These
+// workspace, and calls tp_rope.h / tp_grad.h / tp_fp4.h.  It computes nothing.  These
 // operators take a few microseconds on the GPU for a few tokens, and the same
 // steps in Python and ctypes took 21 us around a library call of 4.1 us (32
 // tokens of 16 + 16 heads, Grace host): here they take 1.6.
@@ -21,6 +21,7 @@
 #include <string>
 #include <vector>
 
+#include "tp_fp4.h"
 #include "tp_grad.h"
 #include "tp_rope.h"
 
@@ -34,6 +35,11 @@ struct Library {
   decltype(&tp_grad_workspace_bytes) grad_workspace_bytes = nullptr;
   decltype(&tp_grad_norm) grad_norm = nullptr;
   decltype(&tp_grad_clip) grad_clip = nullptr;
+  decltype(&tp_fp4_bytes) fp4_bytes = nullptr;
+  decltype(&tp_fp4_quantize) fp4_quantize = nullptr;
+  decltype(&tp_fp4_colsum_workspace_bytes) fp4_colsum_bytes = nullptr;
+  decltype(&tp_fp4_dequantize) fp4_dequantize = nullptr;
+  decltype(&tp_fp4_matmul) fp4_matmul = nullptr;
   PyObject* check = nullptr;   // binding._check(status, what)
 } lib;
 
@@ -457,6 +463,202 @@ PyObject* grads(PyObject* const* a) {
   return wrapped(norm);
 }
 
+// ------------------------------------------------------------ four bits --
+
+// A plain matrix [rows, cols] with consecutive row elements.
+struct Matrix {
+  const at::Tensor& t;
+  int dtype;
+  long long rows, cols, stride;
+  Matrix(const char* name, const at::Tensor& x)
+      : t(x), dtype(dtype_code(name, x)) {
+    if (x.dim() != 2 || x.size(1) < 1 ||
+        (x.stride(1) != 1 && x.size(1) != 1) ||
+        (x.size(0) > 1 && x.stride(0) < x.size(1)))
+      throw Refused{std::string(name) + ": expected a matrix [rows, cols] whose "
+                    "row elements are consecutive and whose rows do not overlap, "
+                    "got " + shown(x)};
+    rows = x.size(0);
+    cols = x.size(1);
+    stride = rows > 1 ? x.stride(0) : cols;
+  }
+  const void* data() const { return rows == 0 ? nullptr : t.const_data_ptr(); }
+};
+
+// A packed matrix's buffer.
+size_t packed_of(const char* name, const at::Tensor& b, long long rows,
+                 long long cols, int format, const at::Device& dev) {
+  const size_t need = lib.fp4_bytes(rows, cols, format);
+  if (b.scalar_type() != at::kByte || b.dim() != 1 || !b.is_contiguous() ||
+      b.device() != dev || need == 0 || static_cast<size_t>(b.numel()) < need)
+    throw Refused{std::string(name) + ": expected a packed [" +
+                  std::to_string(rows) + ", " + std::to_string(cols) +
+                  "] matrix on " + dev.str() + ", got " + shown(b)};
+  return static_cast<size_t>(b.numel());
+}
+
+at::Tensor new_packed(long long rows, long long cols, int format,
+                      const at::Device& dev) {
+  const size_t n = lib.fp4_bytes(rows, cols, format);
+  if (n == 0)
+    throw Refused{"a packed matrix needs a known format and 1 to 2^28 columns"};
+  return make({static_cast<int64_t>(n)}, at::kByte, dev);
+}
+
+at::ScalarType plain_type(int code) {
+  if (code != TPMLP_BF16 && code != TPMLP_FP32)
+    throw Refused{"dtype must be torch.bfloat16 or torch.float32"};
+  return code == TPMLP_BF16 ? at::kBFloat16 : at::kFloat;
+}
+
+// The plain output [rows, cols] of a call: as given, or new.
+at::Tensor plain_out(PyObject* given, long long rows, long long cols, int dtype,
+                     const at::Device& dev) {
+  const at::Tensor* o = maybe("out", given);
+  if (o == nullptr) return make({rows, cols}, plain_type(dtype), dev);
+  const Matrix m("out", *o);
+  if (m.rows != rows || m.cols != cols || m.dtype != dtype || o->device() != dev)
+    throw Refused{"out: expected [" + std::to_string(rows) + ", " +
+                  std::to_string(cols) + "] of the call's type on " + dev.str() +
+                  ", got " + shown(*o)};
+  o->data_ptr();   // (a lazy copy has memory of its own from here on)
+  return *o;
+}
+
+long long row_stride(const at::Tensor& t) {
+  return t.size(0) > 1 ? t.stride(0) : t.size(1);
+}
+
+const float* bias_of(PyObject* o, long long n, const at::Device& dev) {
+  const at::Tensor* t = maybe("bias", o);
+  if (t == nullptr) return nullptr;
+  if (t->scalar_type() != at::kFloat || t->dim() != 1 || t->size(0) != n ||
+      t->device() != dev || !t->is_contiguous())
+    throw Refused{"bias: expected a contiguous fp32 tensor [" + std::to_string(n) +
+                  "] on " + dev.str() + ", got " + shown(*t)};
+  return static_cast<const float*>(t->const_data_ptr());
+}
+
+// fp4_quantize(x, transpose, format, scale, packed, colsum, stream)
+//   -> (packed, column sums or None)
+PyObject* fp4_quantize(PyObject* const* a) {
+  const Matrix x("x", tensor("x", a[0]));
+  const at::Device dev = x.t.device();
+  const int transpose = PyObject_IsTrue(a[1]), sums = PyObject_IsTrue(a[5]);
+  if (transpose < 0 || sums < 0) throw Raised{};
+  const int format = static_cast<int>(integer(a[2]));
+  const double scale = real(a[3]);
+  const long long rows = transpose ? x.cols : x.rows;
+  const long long cols = transpose ? x.rows : x.cols;
+  const Place place(dev, a[6]);
+  at::Tensor packed, colsum, ws;
+  if (a[4] == Py_None) {
+    packed = new_packed(rows, cols, format, dev);
+  } else {
+    packed = tensor("out", a[4]);
+    packed_of("out", packed, rows, cols, format, dev);
+  }
+  size_t bytes = 0;
+  if (sums) {
+    colsum = make({x.cols}, at::kFloat, dev);
+    bytes = lib.fp4_colsum_bytes(x.rows, x.cols);
+    ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);   // of this call
+  }
+  void* pp = packed.data_ptr();
+  float* cp = sums ? colsum.data_ptr<float>() : nullptr;
+  void* wp = sums ? ws.data_ptr() : nullptr;
+  check(without_gil([&] {
+          return lib.fp4_quantize(x.rows, x.cols, x.dtype, x.data(), x.stride,
+                                  transpose, format, scale, pp,
+                                  static_cast<size_t>(packed.numel()), cp, wp,
+                                  bytes, place.stream);
+        }),
+        "tp_fp4_quantize");
+  return tuple_of({packed, colsum});
+}
+
+// fp4_dequantize(packed, rows, cols, format, dtype, out, stream) -> values
+PyObject* fp4_dequantize(PyObject* const* a) {
+  const at::Tensor& packed = tensor("packed", a[0]);
+  const long long rows = integer(a[1]), cols = integer(a[2]);
+  const int format = static_cast<int>(integer(a[3]));
+  const int dtype = static_cast<int>(integer(a[4]));
+  const at::Device dev = packed.device();
+  if (!packed.is_cuda()) throw Refused{"packed must be a CUDA tensor"};
+  const size_t bytes = packed_of("packed", packed, rows, cols, format, dev);
+  const Place place(dev, a[6]);
+  plain_type(dtype);
+  const at::Tensor out = plain_out(a[5], rows, cols, dtype, dev);
+  const void* pp = packed.const_data_ptr();
+  void* op = rows == 0 ? nullptr : out.data_ptr();
+  check(without_gil([&] {
+          return lib.fp4_dequantize(rows, cols, format, pp, bytes, dtype, op,
+                                    row_stride(out), place.stream);
+        }),
+        "tp_fp4_dequantize");
+  return wrapped(out);
+}
+
+// fp4_matmul(a, T, b, N, K, format, bias, dtype, out, stream) -> C
+PyObject* fp4_matmul(PyObject* const* a) {
+  const at::Tensor &pa = tensor("a", a[0]), &pb = tensor("b", a[2]);
+  const long long T = integer(a[1]), N = integer(a[3]), K = integer(a[4]);
+  const int format = static_cast<int>(integer(a[5]));
+  const int dtype = static_cast<int>(integer(a[7]));
+  const at::Device dev = pa.device();
+  if (!pa.is_cuda()) throw Refused{"a must be a CUDA tensor"};
+  const size_t na = packed_of("a", pa, T, K, format, dev);
+  const size_t nb = packed_of("b", pb, N, K, format, dev);
+  const float* bias = bias_of(a[6], N, dev);
+  plain_type(dtype);
+  const Place place(dev, a[9]);
+  const at::Tensor out = plain_out(a[8], T, N, dtype, dev);
+  const void *ap = pa.const_data_ptr(), *bp = pb.const_data_ptr();
+  void* op = T == 0 ? nullptr : out.data_ptr();
+  check(without_gil([&] {
+          return lib.fp4_matmul(T, N, K, format, ap, na, bp, nb, bias, dtype, op,
+                                row_stride(out), place.stream);
+        }),
+        "tp_fp4_matmul");
+  return wrapped(out);
+}
+
+// fp4_linear(x, b, N, K, format, scale, bias, dtype, out, stream) -> C: x [T, K]
+// quantised and multiplied, in one call.
+PyObject* fp4_linear(PyObject* const* a) {
+  const Matrix x("x", tensor("x", a[0]));
+  const at::Tensor& pb = tensor("weight", a[1]);
+  const at::Device dev = x.t.device();
+  const long long N = integer(a[2]), K = integer(a[3]);
+  if (x.cols != K)
+    throw Refused{"x: expected [T, " + std::to_string(K) + "], got " + shown(x.t)};
+  const int format = static_cast<int>(integer(a[4]));
+  const double scale = real(a[5]);
+  const int dtype = static_cast<int>(integer(a[7]));
+  const size_t nb = packed_of("weight", pb, N, K, format, dev);
+  const float* bias = bias_of(a[6], N, dev);
+  plain_type(dtype);
+  const Place place(dev, a[9]);
+  const at::Tensor out = plain_out(a[8], x.rows, N, dtype, dev);
+  const at::Tensor q = new_packed(x.rows, K, format, dev);
+  void* qp = q.data_ptr();
+  const size_t nq = static_cast<size_t>(q.numel());
+  const void* bp = pb.const_data_ptr();
+  void* op = x.rows == 0 ? nullptr : out.data_ptr();
+  const char* what = "tp_fp4_quantize";
+  check(without_gil([&] {
+          const int rc = lib.fp4_quantize(x.rows, K, x.dtype, x.data(), x.stride,
+                                          0, format, scale, qp, nq, nullptr,
+                                          nullptr, 0, place.stream);
+          if (rc != TPMLP_OK) return rc;
+          what = "tp_fp4_matmul";
+          return lib.fp4_matmul(x.rows, N, K, format, qp, nq, bp, nb, bias, dtype,
+                                op, row_stride(out), place.stream);
+        }),
+        what);
+  return wrapped(out);
+}
+
 // --------------------------------------------------------------- module --
 
 // bind(check, addresses of Library's functions in its order)
@@ -472,6 +674,11 @@ PyObject* bind(PyObject* const* a) {
       reinterpret_cast<decltype(l.grad_workspace_bytes)>(at(5));
   l.grad_norm = reinterpret_cast<decltype(l.grad_norm)>(at(6));
   l.grad_clip = reinterpret_cast<decltype(l.grad_clip)>(at(7));
+  l.fp4_bytes = reinterpret_cast<decltype(l.fp4_bytes)>(at(8));
+  l.fp4_quantize = reinterpret_cast<decltype(l.fp4_quantize)>(at(9));
+  l.fp4_colsum_bytes = reinterpret_cast<decltype(l.fp4_colsum_bytes)>(at(10));
+  l.fp4_dequantize = reinterpret_cast<decltype(l.fp4_dequantize)>(at(11));
+  l.fp4_matmul = reinterpret_cast<decltype(l.fp4_matmul)>(at(12));
   Py_INCREF(a[0]);
   l.check = a[0];
   Py_XDECREF(lib.check);
@@ -507,12 +714,16 @@ PyMethodDef methods[] = {
     {"norm_forward", nullptr, 0, nullptr},
     {"norm_backward", nullptr, 0, nullptr},
     {"grads", nullptr, 0, nullptr},
+    {"fp4_quantize", nullptr, 0, nullptr},
+    {"fp4_dequantize", nullptr, 0, nullptr},
+    {"fp4_matmul", nullptr, 0, nullptr},
+    {"fp4_linear", nullptr, 0, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycall",
-                      "Tensor calls of libtpmlp's query/key and gradient "
-                      "operators.",
+                      "Tensor calls of libtpmlp's query/key, gradient and "
+                      "four-bit operators.",
                       -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -525,10 +736,14 @@ void set(int i) {
 }  // namespace
 
 PyMODINIT_FUNC PyInit__pycall() {
-  set<bind, 8>(0);
+  set<bind, 13>(0);
   set<rope, 11>(1);
   set<norm_forward, 16>(2);
   set<norm_backward, 21>(3);
   set<grads, 6>(4);
+  set<fp4_quantize, 7>(5);
+  set<fp4_dequantize, 7>(6);
+  set<fp4_matmul, 10>(7);
+  set<fp4_linear, 10>(8);
   return PyModule_Create(&module);
 }

@@ -23,6 +23,7 @@
 #include <vector>
 
 #include "host_common.cuh"
+#include "mlp_handle.h"
 
 using namespace tpmlp;
 
@@ -175,15 +176,6 @@ Fp8Layout fp8_layout(const tp_mlp_config& c, int tokens) {
 }  // namespace
 
 void tpmlp::set_last_detail(const char* msg) { set_detail_msg(msg); }
-
-// ------------------------------------------------------------- handle --
-
-struct tp_mlp_handle {
-  tpmlp::host::HandleCore core;
-  tp_mlp_config cfg;
-  unsigned long long drop_seed = 0, drop_offset = 0;
-  bool ln_prologue = true;   // tp_mlp_set_ln_prologue
-};
 
 namespace {
 

@@ -7,6 +7,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B_
+from .fp4 import _format as _fp4_format
 
 
 class TensorParallelMLP:
@@ -232,3 +233,58 @@ class TensorParallelMLP:
             n *= d
         n *= torch.tensor([], dtype=dt).element_size()
         return buf[off:off + n].view(dt).view(*shape)
+
+    # ------------------------------------------------------------- fp4 --
+    def pack_fp4_weights(self, A, B, format: str = "nvfp4",
+                         stream=None) -> "Fp4Weights":
+        """Quantize A and B to four bits along the products' inner dimension
+        (see tp_fp4_mlp_pack_weights) for forward_fp4."""
+        h, f = self.hidden, self.ffn
+        self._chk("A", A, (h, f), torch.bfloat16)
+        self._chk("B", B, (f, h), torch.bfloat16)
+        code = _fp4_format(format)
+        n = B_.tp_fp4_mlp_weights_bytes(self.handle, code)
+        if n == 0:
+            raise ValueError("the four-bit variant needs a bf16 handle without "
+                             "dropout")
+        packed = torch.empty(n, dtype=torch.uint8, device=A.device)
+        B_.tp_fp4_mlp_pack_weights(self.handle, code, A, B, packed, n, stream)
+        return Fp4Weights(packed, format, (h, f))
+
+    def forward_fp4(self, X, packed, b1=None, b2=None, gamma=None, beta=None,
+                    x_scale: float = 1.0, y_scale: float = 1.0, out=None,
+                    stream=None):
+        """Forward on weights from pack_fp4_weights (tp_fp4_mlp_forward): X (or
+        LayerNorm(X)) and Y = GeLU(H) are quantized with nvfp4's powers of two
+        ``x_scale`` and ``y_scale`` (mxfp4: 1)."""
+        T = X.shape[0]
+        h, f = self.hidden, self.ffn
+        if not isinstance(packed, Fp4Weights) or packed.shape != (h, f):
+            raise ValueError(f"packed must be the pack_fp4_weights of a block of "
+                             f"{(h, f)}")
+        self._chk("X", X, (T, h), torch.bfloat16)
+        self._chk("b1", b1, (f,), torch.float32)
+        self._chk("b2", b2, (h,), torch.float32)
+        self._chk("gamma", gamma, (h,), torch.float32)
+        self._chk("beta", beta, (h,), torch.float32)
+        Z = out if out is not None else torch.empty((T, h), dtype=torch.bfloat16,
+                                                   device=X.device)
+        self._chk("Z", Z, (T, h), torch.bfloat16)
+        code = _fp4_format(packed.format)
+        need = B_.tp_fp4_mlp_workspace_bytes(self.handle, T, code)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(max(need, 256), dtype=torch.uint8,
+                                   device=self.device)
+        B_.tp_fp4_mlp_forward(self.handle, T, code, X, packed.buffer, b1, b2, gamma,
+                              beta, x_scale, y_scale, Z, self._ws,
+                              self._ws.numel(), stream)
+        return Z
+
+
+class Fp4Weights:
+    """The packed weights of one block (TensorParallelMLP.pack_fp4_weights)."""
+
+    __slots__ = ("buffer", "format", "shape")
+
+    def __init__(self, buffer: torch.Tensor, format: str, shape):
+        self.buffer, self.format, self.shape = buffer, format, shape
