@@ -57,14 +57,17 @@ extern "C" {
 
 /* Bytes of a packed [rows, cols] matrix (0 for a bad format or size), and the
  * offsets of its parts (-1 likewise):
- *   TPFP4_CODES   row r at r * pitch, pitch = 16 ceil(cols / 32) bytes; element
- *                 c in the low (c even) or high nibble of byte c / 2; zeros
- *                 past cols
- *   TPFP4_SCALES  one byte a block, in tiles of 128 rows x 256 columns, tile
- *                 (r / 128, c / 256) at ((r / 128) ceil(cols / 256) + c / 256)
- *                 * bytes of a tile (2048 NV, 1024 MX); inside it the scale of
- *                 block b = (c mod 256) / 16 (NV) or / 32 (MX) of row r at
- *                 (b / 4) 512 + (r mod 32) 16 + ((r mod 128) / 32) 4 + b mod 4 */
+ *   TPFP4_CODES   two codes a byte, in tiles of 128 rows x 256 columns (16 KB),
+ *                 tile (r / 128, c / 256) being number n = (r / 128)
+ *                 ceil(cols / 256) + c / 256: element (r, c) at 16384 n +
+ *                 (r mod 128) 128 + (c mod 256) / 2, in the low nibble for even
+ *                 c; zeros past cols
+ *   TPFP4_SCALES  one byte a block, in tiles of the same rows and columns (2048
+ *                 bytes NV, 1024 MX): the scale of block b = (c mod 256) / 16
+ *                 (NV) or / 32 (MX) of row r at n times that + (b / 4) 512 +
+ *                 (r mod 32) 16 + ((r mod 128) / 32) 4 + b mod 4; 0 (NV) or 127
+ *                 (MX) past cols
+ * What lies in rows past the matrix is not defined. */
 size_t tp_fp4_bytes(long long rows, long long cols, int format);
 long long tp_fp4_offset(long long rows, long long cols, int format, int which);
 #define TPFP4_CODES  0

@@ -110,15 +110,18 @@ def quantized(x, fmt, scale=None):
 
 
 def pack(codes, byte, fmt):
-    """The code section and the scale section as bytes (scales of rows past the
+    """The code section and the scale section as bytes (those of rows past the
     matrix are left 0)."""
     R, C = codes.shape
-    pitch = -(-C // 32) * 16
-    full = np.zeros((R, 2 * pitch), dtype=np.uint8)
-    full[:, :C] = codes
-    out = full[:, 0::2] | (full[:, 1::2] << 4)
     per = 256 // BLOCK[fmt]
     rt, kt = -(-R // 128), -(-C // 256)
+    full = np.zeros((rt * 128, kt * 256), dtype=np.uint8)
+    full[:R, :C] = codes
+    out = np.zeros((rt, kt, 128 * 128), dtype=np.uint8)
+    for i in range(rt):
+        for j in range(kt):
+            t = full[128 * i:128 * i + 128, 256 * j:256 * j + 256]
+            out[i, j] = (t[:, 0::2] | (t[:, 1::2] << 4)).reshape(-1)
     empty = 127 if fmt == "mxfp4" else 0
     scales = np.zeros((rt, kt, 128 * per), dtype=np.uint8)
     for r in range(R):
@@ -126,7 +129,7 @@ def pack(codes, byte, fmt):
             v = byte[r, b] if b < byte.shape[1] else empty
             at = b % per // 4 * 512 + r % 32 * 16 + r % 128 // 32 * 4 + b % 4
             scales[r // 128, b // per, at] = v
-    return out, scales.reshape(-1)
+    return out.reshape(-1), scales.reshape(-1)
 
 
 def matmul(a, b, bias=None):

@@ -11,13 +11,15 @@
 namespace tpmlp {
 namespace fp4 {
 
-constexpr int TILE_ROWS = 128;   // rows of a scale tile
-constexpr int TILE_COLS = 256;   // columns of a scale tile: 128 bytes of codes
+constexpr int TILE_ROWS = 128;   // rows of a tile
+constexpr int TILE_COLS = 256;   // columns of a tile: 128 bytes of codes a row
+constexpr int CODE_TILE = TILE_ROWS * TILE_COLS / 2;
 constexpr size_t HEADER_BYTES = 256;
 
 __host__ __device__ constexpr int block_size(int format) {
   return format == TPFP4_NV ? 16 : 32;
 }
+// Bytes of the scales of a tile.
 __host__ __device__ constexpr int tile_bytes(int format) {
   return TILE_ROWS * TILE_COLS / block_size(format);
 }
@@ -31,26 +33,28 @@ struct Header {
   unsigned int amax;
 };
 
-// One packed matrix.
+// One packed matrix: tile (r / 128, c / 256) is tile number (r / 128) ktiles +
+// c / 256 of the codes and of the scales.  A product's copies are whole tiles, so
+// that a weight is read from HBM in consecutive 16 KB.
 struct Packed {
   Header* head;
   uint8_t* codes;
   uint8_t* scales;
-  long long pitch;   // bytes of a row of codes
   int rows, cols;
-  int ktiles;        // scale tiles of a row
+  int ktiles;        // tiles of a row
 };
 
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+inline size_t tiles_of(long long rows, long long cols) {
+  return static_cast<size_t>((rows + TILE_ROWS - 1) / TILE_ROWS) *
+         ((cols + TILE_COLS - 1) / TILE_COLS);
+}
 inline size_t scales_offset(long long rows, long long cols) {
-  return up256(HEADER_BYTES +
-               static_cast<size_t>(rows) * ((cols + 31) / 32 * 16));
+  return HEADER_BYTES + tiles_of(rows, cols) * CODE_TILE;
 }
 inline size_t packed_bytes(long long rows, long long cols, int format) {
-  return scales_offset(rows, cols) +
-         static_cast<size_t>((rows + TILE_ROWS - 1) / TILE_ROWS) *
-             ((cols + TILE_COLS - 1) / TILE_COLS) * tile_bytes(format);
+  return scales_offset(rows, cols) + tiles_of(rows, cols) * tile_bytes(format);
 }
 inline Packed view(const void* buffer, long long rows, long long cols) {
   char* b = static_cast<char*>(const_cast<void*>(buffer));
@@ -58,11 +62,16 @@ inline Packed view(const void* buffer, long long rows, long long cols) {
   p.head = reinterpret_cast<Header*>(b);
   p.codes = reinterpret_cast<uint8_t*>(b + HEADER_BYTES);
   p.scales = reinterpret_cast<uint8_t*>(b + scales_offset(rows, cols));
-  p.pitch = (cols + 31) / 32 * 16;
   p.rows = static_cast<int>(rows);
   p.cols = static_cast<int>(cols);
   p.ktiles = static_cast<int>((cols + TILE_COLS - 1) / TILE_COLS);
   return p;
+}
+
+// Where row r's codes of k-tile kt lie (128 bytes).
+__device__ __forceinline__ size_t code_row(int r, int kt, int ktiles) {
+  return (static_cast<size_t>(r / TILE_ROWS) * ktiles + kt) * CODE_TILE +
+         (r % TILE_ROWS) * (TILE_COLS / 2);
 }
 
 // Where the four scale bytes of row r, blocks 4q .. 4q + 3 of k-tile kt lie.
@@ -112,13 +121,15 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float inv_g) {
   if constexpr (FORMAT == TPFP4_NV) {
     s.m = inv_g;
     const float a = __uint_as_float(sticky(amax)) * inv_g;
-    // a / 6 rounded to fp32 meets a border of E4M3 only where a / 6 does
-    const float v = __fdiv_rn(a, 6.f);
+    // a / 6 rounded to 20 bits: a product with 1 / 6 is off by less than 2^-22
+    // of itself, E4M3's borders (5 bits) come out as themselves, and what is not
+    // one stays 2^-14 away
+    const float v = __uint_as_float((__float_as_uint(a * (1.f / 6.f)) + 8u) & ~15u);
     const uint32_t byte = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
     const float f = __half2float(
         __half(__nv_cvt_fp8_to_halfraw(static_cast<uint8_t>(byte), __NV_E4M3)));
     s.byte = byte;
-    s.r = byte == 0 ? 0.f : __frcp_rn(f);
+    s.r = byte == 0 ? 0.f : rcp_approx(f);
     if (amax >= 0x7f800000u) s = {0x7fu, 0.f, 0.f};
   } else {
     if (amax >= 0x7f800000u) return {0xffu, 0.f, 0.f};
@@ -134,9 +145,10 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float inv_g) {
 }
 
 // x / (s g) for the rounding to E2M1.  NV: x m is exact, and (x m) r + 96 - 96
-// rounds the quotient to a multiple of 2^-17: 1 / s's error (below 2^-21 of a
-// quotient up to 8) cannot move it off a border that it is on, nor onto one
-// that it is 2^-16 or more away from, as everything else is (sticky).  MX: exact.
+// rounds the quotient to a multiple of 2^-17: the error of 1 / s (2^-23 of
+// itself, 2^-20 of a quotient up to 8) cannot move it off a border that it is on,
+// nor onto one that it is 2^-16 or more away from, as everything else is
+// (sticky).  MX: exact.
 template <int FORMAT, bool WIDE>
 __device__ __forceinline__ float quotient(float x, const Scale& s) {
   if constexpr (FORMAT == TPFP4_NV) {

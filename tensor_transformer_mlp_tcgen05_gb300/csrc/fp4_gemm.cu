@@ -11,8 +11,8 @@
 // all 256 rows of B (4 KB): each SM multiplies its A rows with the B columns
 // of both.
 //
-// 12 warps: warp 0 loads (one lane), warp 1 of the even CTA copies scales and
-// issues the MMAs (one lane), warps 4-11 are the epilogue: warp w takes TMEM
+// 12 warps: warp 0 loads, warp 1 of the even CTA copies scales and issues the
+// MMAs (one elected lane each), warps 4-11 are the epilogue: warp w takes TMEM
 // lanes 32 (w mod 4) on and one 128-column half.
 //
 // Tensor memory: two accumulators of 256 columns would fill all 512, and the
@@ -182,7 +182,8 @@ __device__ __forceinline__ void store_fp4(const Packed& y, int row, int c0,
       c[b * BLOCK / 8 + 2 * i + 1] = w.y;
     }
   }
-  uint4* dst = reinterpret_cast<uint4*>(y.codes + row * y.pitch + c0 / 2);
+  uint4* dst = reinterpret_cast<uint4*>(
+      y.codes + code_row(row, c0 / TILE_COLS, y.ktiles) + c0 % TILE_COLS / 2);
   dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
   dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
   const int block = c0 % TILE_COLS / BLOCK;
@@ -194,9 +195,12 @@ __device__ __forceinline__ void store_fp4(const Packed& y, int row, int c0,
     *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(word);
 }
 
-// Scales of 64 columns past the matrix, which its products read with zero codes.
+// 64 columns past the matrix in its last k-tile, which its products read.
 template <int FORMAT>
-__device__ __forceinline__ void store_no_scales(const Packed& y, int row, int c0) {
+__device__ __forceinline__ void store_nothing(const Packed& y, int row, int c0) {
+  uint4* dst = reinterpret_cast<uint4*>(
+      y.codes + code_row(row, c0 / TILE_COLS, y.ktiles) + c0 % TILE_COLS / 2);
+  dst[0] = dst[1] = make_uint4(0u, 0u, 0u, 0u);
   const int block = c0 % TILE_COLS / block_size(FORMAT);
   uint8_t* to = y.scales + scale_word(row, c0 / TILE_COLS, block / 4, y.ktiles,
                                       tile_bytes(FORMAT)) + block % 4;
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (warp < FIRST_EPI_WARP) {
     ptx::setmaxnreg_dec<REGS_CONTROL>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------------------------------------------- producer --
       uint32_t stage = 0, phase = 0;
       bool alive = true;
@@ -288,62 +292,80 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tile_coords(tile, num_m, num_n, group_m, mb, nb);
         const int m0 = mb * PM + static_cast<int>(prank) * HM;
         const int n0 = nb * PN + static_cast<int>(prank) * HN;
-        // scale tiles; ones past the matrix are filled with zeros
-        const int sa0 = (m0 / TILE_ROWS) * ktiles;
+        // tile numbers; tiles past the matrix are filled with zeros
+        const int ta0 = (m0 / TILE_ROWS) * ktiles;
+        const int tb0 = (n0 / TILE_ROWS) * ktiles;
         const int sb0 = (nb * PN / TILE_ROWS) * ktiles;
         for (int kt = 0; kt < ktiles; ++kt) {
-          if (!wait_bounded(empty0 + 8u * stage, phase ^ 1u, ctl,
-                            ROLE_PRODUCER)) {
+          if (!wait_warp(empty0 + 8u * stage, phase ^ 1u, ctl, ROLE_PRODUCER)) {
             alive = false;
             break;
           }
-          if (leader) ptx::mbar_arrive_expect_tx(full0 + 8u * stage, 2 * STAGE);
-          const uint32_t fb = lead_full0 + 8u * stage;
-          ptx::tma_load_2d_pair(s_a + stage * OPERAND_BYTES, &tmA, fb, kt * 128, m0);
-          ptx::tma_load_2d_pair(s_b + stage * OPERAND_BYTES, &tmB, fb, kt * 128, n0);
-          ptx::tma_load_2d_pair(s_sa + stage * TILE, &tmSA, fb, 0, sa0 + kt);
-          ptx::tma_load_2d_pair(s_sb + stage * 2 * TILE, &tmSB, fb, 0, sb0 + kt);
-          ptx::tma_load_2d_pair(s_sb + stage * 2 * TILE + TILE, &tmSB, fb, 0,
-                                sb0 + ktiles + kt);
+          if (elect_one()) {
+            if (leader) ptx::mbar_arrive_expect_tx(full0 + 8u * stage, 2 * STAGE);
+            const uint32_t fb = lead_full0 + 8u * stage;
+            ptx::tma_load_2d_pair(s_a + stage * OPERAND_BYTES, &tmA, fb, 0,
+                                  (ta0 + kt) * TILE_ROWS);
+            ptx::tma_load_2d_pair(s_b + stage * OPERAND_BYTES, &tmB, fb, 0,
+                                  (tb0 + kt) * TILE_ROWS);
+            ptx::tma_load_2d_pair(s_sa + stage * TILE, &tmSA, fb, 0, ta0 + kt);
+            ptx::tma_load_2d_pair(s_sb + stage * 2 * TILE, &tmSB, fb, 0, sb0 + kt);
+            ptx::tma_load_2d_pair(s_sb + stage * 2 * TILE + TILE, &tmSB, fb, 0,
+                                  sb0 + ktiles + kt);
+          }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
       // -------------------------------------------------- MMA issuer --
       constexpr uint16_t pair_mask = 0x3;
+      const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+      const uint64_t desc_a = ptx::sdesc_sw128(s_a, 16, 1024);
+      const uint64_t desc_b = ptx::sdesc_sw128(s_b, 16, 1024);
+      const uint64_t desc_sa = sdesc_scales(s_sa);
+      const uint64_t desc_sb = sdesc_scales(s_sb);
       uint32_t stage = 0, phase = 0, j = 0;
       bool alive = true;
       for (int tile = pair; alive && tile < tiles; tile += num_pairs, ++j) {
-        if (j > 0 && !wait_bounded_cluster(shared, (j - 1u) & 1u, ctl, ROLE_MMA)) {
+        if (j > 0 && !__all_sync(0xffffffffu,
+                                 wait_bounded_cluster(shared, (j - 1u) & 1u, ctl,
+                                                      ROLE_MMA))) {
           alive = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t d = tmem_base + (j & 1u) * ACC_STEP;
+        const uint32_t d = tmem + (j & 1u) * ACC_STEP;
         for (int kt = 0; kt < ktiles; ++kt) {
-          if (!wait_bounded(full0 + 8u * stage, phase, ctl, ROLE_MMA)) {
+          if (!wait_warp(full0 + 8u * stage, phase, ctl, ROLE_MMA)) {
             alive = false;
             break;
           }
           ptx::tc_fence_after();
-          ktile_mmas<FORMAT, 2, PM, PN, 2>(
-              d, s_a + stage * OPERAND_BYTES, s_b + stage * OPERAND_BYTES,
-              s_sa + stage * TILE, s_sb + stage * 2 * TILE, tmem_base + T_SA,
-              tmem_base + T_SB, kt == 0);
-          ptx::mma_commit_pair(empty0 + 8u * stage, pair_mask);
+          if (elect_one()) {
+            ktile_mmas<FORMAT, 2, PM, PN, 2>(
+                d, desc_a + stage * (OPERAND_BYTES / 16),
+                desc_b + stage * (OPERAND_BYTES / 16),
+                desc_sa + stage * (TILE / 16), desc_sb + stage * (2 * TILE / 16),
+                tmem + T_SA, tmem + T_SB, kt == 0);
+            ptx::mma_commit_pair(empty0 + 8u * stage, pair_mask);
+            if (kt == ktiles - 1) ptx::mma_commit_pair(tfull, pair_mask);
+          }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (alive) ptx::mma_commit_pair(tfull, pair_mask);
       }
       if (*reinterpret_cast<volatile int*>(abort_flag)) {
-        // Wait for every MMA this thread issued before TMEM is freed.
-        ptx::mma_commit_pair(done_bar, static_cast<uint16_t>(1u << prank));
+        // Wait for every MMA issued before TMEM is freed.
+        if (elect_one())
+          ptx::mma_commit_pair(done_bar, static_cast<uint16_t>(1u << prank));
+        __syncwarp();
         wait_teardown(done_bar, 0);
       }
     }
@@ -419,7 +441,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (c0 >= args.N) {
           if constexpr (EPI == OUT_GELU_FP4) {
             if (row < args.M && c0 < args.y.ktiles * TILE_COLS)
-              store_no_scales<FORMAT>(args.y, row, c0);
+              store_nothing<FORMAT>(args.y, row, c0);
           }
           continue;
         }

@@ -75,29 +75,48 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b,
 #undef TPMLP_MMA_FP4
 }
 
+// One lane of a converged warp, the same one every time (commits cover what
+// their own thread issued).  The loops around it are the whole warp's: the
+// compiler then keeps descriptors and addresses in uniform registers, where
+// these instructions take them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(yes));
+  return yes != 0;
+}
+
+// The whole warp's wait: whether it ended for every lane.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
+                                          const gemm::Ctl& c, int role) {
+  return __all_sync(0xffffffffu, gemm::wait_bounded(bar, parity, c, role));
+}
+
 // One k-tile: its scales into tensor memory (columns t_sa and t_sb on), then
 // its four MMAs.  A copy and the MMAs issued after it, and MMAs and the copies
-// after them, run in the order of issue.  SB_TILES: 128-row tiles of B's scales.
+// after them, run in the order of issue.  a, b: descriptors of the operands'
+// tiles, sa, sb: of their scale tiles; SB_TILES: 128-row tiles of B's scales.
 template <int FORMAT, int CTAS, int M, int N, int SB_TILES>
-__device__ __forceinline__ void ktile_mmas(uint32_t d, uint32_t a, uint32_t b,
-                                           uint32_t sa, uint32_t sb,
+__device__ __forceinline__ void ktile_mmas(uint32_t d, uint64_t a, uint64_t b,
+                                           uint64_t sa, uint64_t sb,
                                            uint32_t t_sa, uint32_t t_sb,
                                            bool first) {
   constexpr int COPIES = copies_per_tile(FORMAT);
+  constexpr int TILE = tile_bytes(FORMAT);
 #pragma unroll
   for (int i = 0; i < COPIES; ++i) {
-    const uint64_t da = sdesc_scales(sa + i * 512);
     if constexpr (CTAS == 2)
-      copy_scales_pair(t_sa + 4 * i, da);
+      copy_scales_pair(t_sa + 4 * i, sa + i * 512 / 16);
     else
-      copy_scales(t_sa + 4 * i, da);
+      copy_scales(t_sa + 4 * i, sa + i * 512 / 16);
 #pragma unroll
     for (int j = 0; j < SB_TILES; ++j) {
-      const uint64_t db = sdesc_scales(sb + j * tile_bytes(FORMAT) + i * 512);
       if constexpr (CTAS == 2)
-        copy_scales_pair(t_sb + 4 * (i * SB_TILES + j), db);
+        copy_scales_pair(t_sb + 4 * (i * SB_TILES + j),
+                         sb + (j * TILE + i * 512) / 16);
       else
-        copy_scales(t_sb + 4 * (i * SB_TILES + j), db);
+        copy_scales(t_sb + 4 * (i * SB_TILES + j), sb + (j * TILE + i * 512) / 16);
     }
   }
 #pragma unroll
@@ -107,8 +126,7 @@ __device__ __forceinline__ void ktile_mmas(uint32_t d, uint32_t a, uint32_t b,
         FORMAT == TPFP4_NV
             ? idesc_fp4(FORMAT, M, N, 0)
             : (k % 2 ? idesc_fp4(FORMAT, M, N, 2) : idesc_fp4(FORMAT, M, N, 0));
-    mma_fp4<FORMAT, CTAS>(d, ptx::sdesc_sw128(a + k * 32, 16, 1024),
-                          ptx::sdesc_sw128(b + k * 32, 16, 1024), idesc,
+    mma_fp4<FORMAT, CTAS>(d, a + k * 32 / 16, b + k * 32 / 16, idesc,
                           t_sa + 4 * copy, t_sb + 4 * SB_TILES * copy,
                           first && k == 0 ? 0u : 1u);
   }

@@ -130,10 +130,13 @@ int scales_map(CUtensorMap* m, const fp4::Packed& p, int format) {
              : bad(TPMLP_ERR_CUDA, "cuTensorMapEncodeTiled failed (fp4 scales)");
 }
 
-int codes_map(CUtensorMap* m, const fp4::Packed& p, uint32_t box_rows) {
-  return encode_map_u8(m, p.codes, static_cast<uint64_t>(p.pitch),
-                       static_cast<uint64_t>(p.rows),
-                       static_cast<uint64_t>(p.pitch), box_rows);
+// Tiles of codes one below the other, boxes of up to 128 rows of one.
+int codes_map(CUtensorMap* m, const fp4::Packed& p, int box_rows) {
+  const uint64_t rows =
+      static_cast<uint64_t>((p.rows + fp4::TILE_ROWS - 1) / fp4::TILE_ROWS) *
+      p.ktiles * fp4::TILE_ROWS;
+  return encode_map_u8(m, p.codes, 128, rows, 128,
+                       static_cast<uint32_t>(std::min(box_rows, fp4::TILE_ROWS)));
 }
 
 // Whether a product goes to the kernel that splits K.
@@ -330,9 +333,9 @@ int tp_fp4_matmul(long long T, long long N, long long K, int format,
       overlap(C, nc, B, fp4::packed_bytes(N, K, format)) ||
       overlap(C, nc, bias, static_cast<size_t>(N) * 4))
     return bad(TPMLP_ERR_ARG, "fp4: C overlaps an input");
-  // scale tiles and output tiles are counted in 32 bits
+  // rows of all tiles and output tiles are counted in 32 bits
   const long long ktiles = (K + 255) / 256;
-  if ((std::max(T, N) + 127) / 128 * ktiles > INT_MAX / 2 ||
+  if ((std::max(T, N) + 127) / 128 * ktiles > INT_MAX / 256 ||
       (T + 127) / 128 * ((N + 127) / 128) > INT_MAX / 16)
     return bad(TPMLP_ERR_SHAPE, "fp4: product too large");
   int sms = 0;

@@ -114,11 +114,17 @@ __global__ void __launch_bounds__(THREADS)
   const int row0 = chunk * 16 * PASSES + static_cast<int>(threadIdx.x >> 4);
   const int col = kt * TILE_COLS + unit * 16;
   Raw<T> raw[PASSES];
+  const T* src = x + row0 * stride + col;
+  if (LD != 0 && (chunk + 1) * 16 * PASSES <= p.rows &&
+      (kt + 1) * TILE_COLS <= p.cols) {
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int row = row0 + 16 * i;
-    load16<T, LD>(x + row * stride + col, row < p.rows ? p.cols - col : 0,
-                  raw[i]);
+    for (int i = 0; i < PASSES; ++i)
+      load_words<LD == 0 ? 16 : LD>(src + 16 * i * stride, raw[i].w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+      load16<T, LD>(src + 16 * i * stride,
+                    row0 + 16 * i < p.rows ? p.cols - col : 0, raw[i]);
   }
   const float inv_g = FORMAT == TPFP4_NV ? inverse_g(p, g_exponent)
                                          : (inverse_g(p, 0), 1.f);
@@ -146,9 +152,8 @@ __global__ void __launch_bounds__(THREADS)
       word |= __shfl_xor_sync(0xffffffffu, word, 4);
     }
     if (row < p.rows) {
-      const int byte = kt * (TILE_COLS / 2) + unit * 8;
-      if (byte < p.pitch)
-        *reinterpret_cast<uint2*>(p.codes + row * p.pitch + byte) = c;
+      *reinterpret_cast<uint2*>(p.codes + code_row(row, kt, p.ktiles) + unit * 8) =
+          c;
       constexpr int THREADS_A_WORD = FORMAT == TPFP4_NV ? 4 : 8;
       if (unit % THREADS_A_WORD == 0)
         *reinterpret_cast<uint32_t*>(
@@ -160,29 +165,35 @@ __global__ void __launch_bounds__(THREADS)
 
 // ------------------------------------------------------------- transposed --
 
-// Two consecutive elements from p, of which n are in the row.
-template <bool PAIR>
-__device__ __forceinline__ void load2(const __nv_bfloat16* p, int n, float& a,
-                                      float& b) {
-  if (PAIR && n >= 2) {
-    const uint32_t w = __ldg(reinterpret_cast<const unsigned int*>(p));
-    a = __uint_as_float(w << 16);
-    b = __uint_as_float(w & 0xffff0000u);
-    return;
+// Two consecutive elements from p, as loaded; n of them are in the matrix.
+template <class T>
+struct Two;
+template <>
+struct Two<__nv_bfloat16> {
+  uint32_t w;
+  __device__ float a() const { return __uint_as_float(w << 16); }
+  __device__ float b() const { return __uint_as_float(w & 0xffff0000u); }
+  __device__ void load(const __nv_bfloat16* p) {
+    w = __ldg(reinterpret_cast<const unsigned int*>(p));
   }
-  a = n >= 1 ? __uint_as_float(element_bits(p)) : 0.f;
-  b = n >= 2 ? __uint_as_float(element_bits(p + 1)) : 0.f;
-}
-template <bool PAIR>
-__device__ __forceinline__ void load2(const float* p, int n, float& a, float& b) {
-  if (PAIR && n >= 2) {
-    const float2 w = __ldg(reinterpret_cast<const float2*>(p));
-    a = w.x, b = w.y;
-    return;
+  __device__ void load(const __nv_bfloat16* p, int n) {
+    w = n >= 1 ? element_bits(p) >> 16 : 0u;
+    if (n >= 2) w |= element_bits(p + 1);
   }
-  a = n >= 1 ? __ldg(p) : 0.f;
-  b = n >= 2 ? __ldg(p + 1) : 0.f;
-}
+};
+template <>
+struct Two<float> {
+  float2 w;
+  __device__ float a() const { return w.x; }
+  __device__ float b() const { return w.y; }
+  __device__ void load(const float* p) {
+    w = __ldg(reinterpret_cast<const float2*>(p));
+  }
+  __device__ void load(const float* p, int n) {
+    w.x = n >= 1 ? __ldg(p) : 0.f;
+    w.y = n >= 2 ? __ldg(p + 1) : 0.f;
+  }
+};
 
 constexpr int T_COLS = 64;   // columns of x a block takes
 
@@ -205,39 +216,46 @@ __global__ void __launch_bounds__(THREADS, 2)
   const int kt = static_cast<int>(blockIdx.x / static_cast<unsigned>(tiles));
   const int k0 = kt * TILE_COLS + warp * 32;
   const int n = n0 + 2 * lane;
-  float v[2][32];
+  Two<T> raw[32];
   const T* src = x + k0 * stride + n;
+  if (PAIR && n0 + T_COLS <= p.rows && (kt + 1) * TILE_COLS <= x_rows) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    load2<PAIR>(src + i * stride, k0 + i < x_rows ? p.rows - n : 0, v[0][i],
-                v[1][i]);
+    for (int i = 0; i < 32; ++i) raw[i].load(src + i * stride);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      raw[i].load(src + i * stride, k0 + i < x_rows ? p.rows - n : 0);
+  }
   const float inv_g = FORMAT == TPFP4_NV ? inverse_g(p, g_exponent)
                                          : (inverse_g(p, 0), 1.f);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int r = 2 * lane + j;
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = j == 0 ? raw[i].a() : raw[i].b();
     uint32_t top[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) top[i / 16] = max(top[i / 16], abs_bits(v[j][i]));
+    for (int i = 0; i < 32; ++i) top[i / 16] = max(top[i / 16], abs_bits(v[i]));
     uint2 c0, c1;
     if constexpr (FORMAT == TPFP4_NV) {
       const Scale a = block_scale<FORMAT>(top[0], inv_g);
       const Scale b = block_scale<FORMAT>(top[1], inv_g);
-      c0 = codes16<FORMAT, sizeof(T) == 4>(v[j], a);
-      c1 = codes16<FORMAT, sizeof(T) == 4>(v[j] + 16, b);
+      c0 = codes16<FORMAT, sizeof(T) == 4>(v, a);
+      c1 = codes16<FORMAT, sizeof(T) == 4>(v + 16, b);
       *reinterpret_cast<uint16_t*>(s_scales + r * 16 + warp * 2) =
           static_cast<uint16_t>(a.byte | (b.byte << 8));
     } else {
       const Scale a = block_scale<FORMAT>(max(top[0], top[1]), inv_g);
-      c0 = codes16<FORMAT, sizeof(T) == 4>(v[j], a);
-      c1 = codes16<FORMAT, sizeof(T) == 4>(v[j] + 16, a);
+      c0 = codes16<FORMAT, sizeof(T) == 4>(v, a);
+      c1 = codes16<FORMAT, sizeof(T) == 4>(v + 16, a);
       s_scales[r * 16 + warp] = static_cast<uint8_t>(a.byte);
     }
     s_codes[r * 8 + (warp ^ (lane & 7))] = make_uint4(c0.x, c0.y, c1.x, c1.y);
     if (part != nullptr) {
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) sum += v[j][i];
+      for (int i = 0; i < 32; ++i) sum += v[i];
       s_sum[warp][r] = sum;
     }
   }
@@ -246,9 +264,8 @@ __global__ void __launch_bounds__(THREADS, 2)
   for (int i = 0; i < T_COLS * 8 / THREADS; ++i) {
     const int at = i * THREADS + threadIdx.x;
     const int r = at >> 3, u = at & 7;
-    const int byte = kt * (TILE_COLS / 2) + u * 16;
-    if (n0 + r < p.rows && byte < p.pitch)
-      *reinterpret_cast<uint4*>(p.codes + (n0 + r) * p.pitch + byte) =
+    if (n0 + r < p.rows)
+      *reinterpret_cast<uint4*>(p.codes + code_row(n0 + r, kt, p.ktiles) + u * 16) =
           s_codes[r * 8 + (u ^ ((r >> 1) & 7))];
   }
   constexpr int WORDS = TILE_COLS / block_size(FORMAT) / 4;
@@ -316,23 +333,34 @@ __global__ void __launch_bounds__(THREADS)
 
 // ------------------------------------------------------------- dequantise --
 
+// wide: the bytes that a unit's place is a multiple of, at most 32.
 template <class T>
-__device__ __forceinline__ void store16(T* p, int n, bool wide,
+__device__ __forceinline__ void store16(T* p, int n, int wide,
                                         const float (&v)[16]) {
-  if (wide && n >= 16) {
-    if constexpr (sizeof(T) == 2) {
+  constexpr int WORDS = sizeof(T) * 4;
+  if (wide >= 16 && n >= 16) {
+    uint32_t w[WORDS];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        reinterpret_cast<uint4*>(p)[i] = make_uint4(
-            pack_bf16x2(v[8 * i], v[8 * i + 1]),
-            pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-            pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
-            pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    for (int i = 0; i < WORDS; ++i) {
+      if constexpr (sizeof(T) == 2)
+        w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      else
+        w[i] = __float_as_uint(v[i]);
+    }
+    if (wide == 32) {
+#pragma unroll
+      for (int i = 0; i < WORDS / 8; ++i)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                         reinterpret_cast<char*>(p) + 32 * i),
+                     "r"(w[8 * i]), "r"(w[8 * i + 1]), "r"(w[8 * i + 2]),
+                     "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
+                     "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                     : "memory");
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4*>(p)[i] =
-            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      for (int i = 0; i < WORDS / 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
     return;
   }
@@ -360,7 +388,7 @@ __device__ __forceinline__ void values8(uint32_t w, float scale, float* v) {
 template <class T, int FORMAT, int PASSES>
 __global__ void __launch_bounds__(THREADS)
     dequantize_kernel(const Packed p, T* __restrict__ out, long long stride,
-                      bool wide) {
+                      int wide) {
   const int unit = threadIdx.x & 15;
   const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.ktiles));
   const int chunk = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.ktiles));
@@ -370,19 +398,19 @@ __global__ void __launch_bounds__(THREADS)
   const float g = p.head->g;
   uint2 c[PASSES];
   uint32_t byte[PASSES];
+  const int b = unit * 16 / block_size(FORMAT);
+  const bool inside = (chunk + 1) * 16 * PASSES <= p.rows;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    const int row = row0 + 16 * i;
-    if (row >= p.rows) break;
-    c[i] = __ldg(reinterpret_cast<const uint2*>(p.codes + row * p.pitch + col / 2));
-    const int b = unit * 16 / block_size(FORMAT);
+    const int row = inside ? row0 + 16 * i : min(row0 + 16 * i, p.rows - 1);
+    c[i] = __ldg(reinterpret_cast<const uint2*>(
+        p.codes + code_row(row, kt, p.ktiles) + unit * 8));
     byte[i] = __ldg(p.scales + scale_word(row, kt, b / 4, p.ktiles,
                                           tile_bytes(FORMAT)) + b % 4);
   }
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int row = row0 + 16 * i;
-    if (row >= p.rows) break;
     // code * s is exact; g is a power of two
     const float s = scale_value<FORMAT>(byte[i]);
     float v[16];
@@ -390,7 +418,7 @@ __global__ void __launch_bounds__(THREADS)
     values8(c[i].y, s, v + 8);
 #pragma unroll
     for (int k = 0; k < 16; ++k) v[k] *= g;
-    store16(out + row * stride + col, p.cols - col, wide, v);
+    if (row < p.rows) store16(out + row * stride + col, p.cols - col, wide, v);
   }
 }
 
@@ -469,8 +497,9 @@ void dequantize_type(const Packed& p, int format, T* out, long long stride,
   constexpr int PASSES = 4;
   const unsigned grid = static_cast<unsigned>(
       (p.rows + 16ll * PASSES - 1) / (16 * PASSES) * p.ktiles);
-  const bool wide =
-      on_boundary(out, stride * static_cast<long long>(sizeof(T)), 16);
+  const long long bytes = stride * static_cast<long long>(sizeof(T));
+  const int wide =
+      on_boundary(out, bytes, 32) ? 32 : on_boundary(out, bytes, 16) ? 16 : 0;
   if (format == TPFP4_NV)
     dequantize_kernel<T, TPFP4_NV, PASSES><<<grid, THREADS, 0, s>>>(p, out, stride, wide);
   else

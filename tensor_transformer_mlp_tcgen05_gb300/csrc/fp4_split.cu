@@ -4,8 +4,8 @@
 //
 // A CTA takes 128 rows of B, NT rows of A and one of the cluster's ranges of K,
 // so that a product of few tiles still keeps every SM loading.  Four warps:
-// warp 0 loads (one lane), warp 1 copies scales and issues MMAs (one lane), as
-// in fp4_gemm.cu on one CTA; then all four read their 32 lanes of the
+// warp 0 loads, warp 1 copies scales and issues MMAs, as in fp4_gemm.cu on one
+// CTA; then all four read their 32 lanes of the
 // accumulator into shared memory, and after a cluster barrier CTA r adds up,
 // over all CTAs in their order, the partial sums of every CS-th row of A.  One
 // launch, no workspace, a fixed order.
@@ -84,9 +84,9 @@ __device__ __forceinline__ void finish(const ProductArgs& a, int row, int n0,
     float q[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = quotient<FORMAT, true>(v[i], s);
-    if (left > 0)
-      *reinterpret_cast<uint16_t*>(a.y.codes + row * a.y.pitch + n / 2) =
-          static_cast<uint16_t>(codes8(q));
+    uint8_t* codes = a.y.codes + code_row(row, n0 / TILE_COLS, a.y.ktiles);
+    *reinterpret_cast<uint16_t*>(codes + n % TILE_COLS / 2) =
+        static_cast<uint16_t>(codes8(q));
     uint32_t word = s.byte << (8 * (lane / LANES % 4));
     word |= __shfl_xor_sync(0xffffffffu, word, LANES);
     word |= __shfl_xor_sync(0xffffffffu, word, 2 * LANES);
@@ -97,12 +97,15 @@ __device__ __forceinline__ void finish(const ProductArgs& a, int row, int n0,
           a.y.scales + scale_word(row, kt, word_at, a.y.ktiles, tile_bytes(FORMAT))) =
           word;
     // the second half of a last k-tile that no CTA takes
-    constexpr int HALF_WORDS = 128 / (4 * block_size(FORMAT));
-    if (n0 % TILE_COLS == 0 && n0 + FM >= a.N && lane < HALF_WORDS)
-      *reinterpret_cast<uint32_t*>(
-          a.y.scales + scale_word(row, n0 / TILE_COLS, HALF_WORDS + lane,
-                                  a.y.ktiles, tile_bytes(FORMAT))) =
-          FORMAT == TPFP4_NV ? 0u : 0x7f7f7f7fu;
+    if (n0 % TILE_COLS == 0 && n0 + FM >= a.N) {
+      constexpr int HALF_WORDS = 128 / (4 * block_size(FORMAT));
+      reinterpret_cast<uint16_t*>(codes + TILE_COLS / 4)[lane] = 0;
+      if (lane < HALF_WORDS)
+        *reinterpret_cast<uint32_t*>(
+            a.y.scales + scale_word(row, n0 / TILE_COLS, HALF_WORDS + lane,
+                                    a.y.ktiles, tile_bytes(FORMAT))) =
+            FORMAT == TPFP4_NV ? 0u : 0x7f7f7f7fu;
+    }
     return;
   }
   if constexpr (EPI == OUT_BF16) {
@@ -190,44 +193,59 @@ __global__ void __launch_bounds__(NUM_THREADS)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const Ctl ctl{abort_flag, args.status, args.budget_ns};
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------ producer --
     uint32_t stage = 0, phase = 0;
-    const int sb0 = n0 / TILE_ROWS * ktiles, sa0 = t0 / TILE_ROWS * ktiles;
+    const int tb0 = n0 / TILE_ROWS * ktiles, ta0 = t0 / TILE_ROWS * ktiles;
     for (int kt = k_lo; kt < k_hi; ++kt) {
-      if (!wait_bounded(empty0 + 8u * stage, phase ^ 1u, ctl, ROLE_PRODUCER))
-        break;
-      const uint32_t fb = full0 + 8u * stage;
-      ptx::mbar_arrive_expect_tx(fb, S::STAGE);
-      ptx::tma_load_2d(s_b + stage * S::B_BYTES, &tmB, fb, kt * 128, n0);
-      ptx::tma_load_2d(s_sb + stage * S::TILE, &tmSB, fb, 0, sb0 + kt);
-      ptx::tma_load_2d(s_a + stage * S::A_BYTES, &tmA, fb, kt * 128, t0);
-      const uint32_t sa = s_sa + stage * S::A_TILES * S::TILE;
-      ptx::tma_load_2d(sa, &tmSA, fb, 0, sa0 + kt);
-      if constexpr (S::A_TILES == 2)
-        ptx::tma_load_2d(sa + S::TILE, &tmSA, fb, 0, sa0 + ktiles + kt);
+      if (!wait_warp(empty0 + 8u * stage, phase ^ 1u, ctl, ROLE_PRODUCER)) break;
+      if (elect_one()) {
+        const uint32_t fb = full0 + 8u * stage;
+        ptx::mbar_arrive_expect_tx(fb, S::STAGE);
+        ptx::tma_load_2d(s_b + stage * S::B_BYTES, &tmB, fb, 0, (tb0 + kt) * TILE_ROWS);
+        ptx::tma_load_2d(s_sb + stage * S::TILE, &tmSB, fb, 0, tb0 + kt);
+        const uint32_t da = s_a + stage * S::A_BYTES;
+        ptx::tma_load_2d(da, &tmA, fb, 0, (ta0 + kt) * TILE_ROWS);
+        if constexpr (S::A_TILES == 2)
+          ptx::tma_load_2d(da + CODE_TILE, &tmA, fb, 0,
+                           (ta0 + ktiles + kt) * TILE_ROWS);
+        const uint32_t sa = s_sa + stage * S::A_TILES * S::TILE;
+        ptx::tma_load_2d(sa, &tmSA, fb, 0, ta0 + kt);
+        if constexpr (S::A_TILES == 2)
+          ptx::tma_load_2d(sa + S::TILE, &tmSA, fb, 0, ta0 + ktiles + kt);
+      }
+      __syncwarp();
       if (++stage == S::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ---------------------------------------------------- MMA issuer --
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+    const uint64_t desc_b = ptx::sdesc_sw128(s_b, 16, 1024);
+    const uint64_t desc_a = ptx::sdesc_sw128(s_a, 16, 1024);
+    const uint64_t desc_sb = sdesc_scales(s_sb);
+    const uint64_t desc_sa = sdesc_scales(s_sa);
     uint32_t stage = 0, phase = 0;
     for (int kt = k_lo; kt < k_hi; ++kt) {
-      if (!wait_bounded(full0 + 8u * stage, phase, ctl, ROLE_MMA)) break;
+      if (!wait_warp(full0 + 8u * stage, phase, ctl, ROLE_MMA)) break;
       ptx::tc_fence_after();
-      ktile_mmas<FORMAT, 1, FM, NT, S::A_TILES>(
-          tmem_base, s_b + stage * S::B_BYTES, s_a + stage * S::A_BYTES,
-          s_sb + stage * S::TILE, s_sa + stage * S::A_TILES * S::TILE,
-          tmem_base + S::T_SB, tmem_base + S::T_SA, kt == k_lo);
-      ptx::mma_commit(empty0 + 8u * stage);
+      if (elect_one()) {
+        ktile_mmas<FORMAT, 1, FM, NT, S::A_TILES>(
+            tmem, desc_b + stage * (S::B_BYTES / 16),
+            desc_a + stage * (S::A_BYTES / 16), desc_sb + stage * (S::TILE / 16),
+            desc_sa + stage * (S::A_TILES * S::TILE / 16), tmem + S::T_SB,
+            tmem + S::T_SA, kt == k_lo);
+        ptx::mma_commit(empty0 + 8u * stage);
+      }
+      __syncwarp();
       if (++stage == S::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
-    ptx::mma_commit(done_bar);   // also after an abort, for the teardown
+    if (elect_one()) ptx::mma_commit(done_bar);   // (after an abort too)
   }
   __syncwarp();
   // -------------------------------------------- partial sums to shared --
@@ -289,6 +307,14 @@ __global__ void __launch_bounds__(NUM_THREADS)
   ptx::cluster_sync();   // no CTA leaves while its sums are being read
 }
 
+// Clusters of `size` CTAs that fit at once, `per_sm` CTAs to an SM, when a
+// cluster's SMs come from one of eight groups of at least sms / 9.  (A rule on the SM
+// count alone, so that the order of the sums, and with it the last bits, is the
+// same on every GPU of a model.)
+long long resident_clusters(int size, int per_sm, int sms) {
+  return 8ll * (sms / 9 * per_sm / size);
+}
+
 template <int FORMAT, int EPI, int NT>
 cudaError_t launch_tokens(const CUtensorMap& ta, const CUtensorMap& tsa,
                           const CUtensorMap& tb, const CUtensorMap& tsb,
@@ -302,11 +328,9 @@ cudaError_t launch_tokens(const CUtensorMap& ta, const CUtensorMap& tsa,
   const long long tokens = (args.M + NT - 1) / NT;
   if (tokens > 65535) return cudaErrorInvalidValue;
   // as many CTAs as the SMs hold at once, and a k-tile at least for each
-  const long long room = static_cast<long long>(sms) * (NT > 128 ? 1 : 2) + 16;
   int split = 1;
-  while (2 * split <= MAX_SPLIT && 2 * split <= args.a.ktiles &&
-         features * tokens * 2 * split <= room)
-    split *= 2;
+  for (int c = 2; c <= MAX_SPLIT && c <= args.a.ktiles; ++c)
+    if (features * tokens <= resident_clusters(c, NT > 128 ? 1 : 2, sms)) split = c;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -64,10 +64,12 @@ class Fp4Tensor:
             stream)
 
     def codes(self) -> torch.Tensor:
-        """[rows, 16 ceil(cols / 32)] bytes of two codes, as a view."""
-        pitch = (self.cols + 31) // 32 * 16
+        """[rows, 128 ceil(cols / 256)] bytes of two codes, gathered out of their
+        tiles."""
+        rt, kt = (self.rows + 127) // 128, (self.cols + 255) // 256
         at = B_.tp_fp4_offset(self.rows, self.cols, self._code, B_.TPFP4_CODES)
-        return self.buffer[at:at + self.rows * pitch].view(self.rows, pitch)
+        t = self.buffer[at:at + rt * kt * 16384].view(rt, kt, 128, 128)
+        return t.permute(0, 2, 1, 3).reshape(rt * 128, kt * 128)[:self.rows]
 
     def scales(self) -> torch.Tensor:
         """The scale bytes [rows, blocks], gathered out of their tiles."""

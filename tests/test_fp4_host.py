@@ -33,9 +33,8 @@ def test_every_declared_symbol_is_exported(lib):
 def test_sizes_and_offsets(fmt, tile):
     for rows, cols in ((1, 1), (0, 5), (128, 256), (129, 257), (7, 1000),
                        (1 << 20, 1 << 15)):
-        codes = rows * ((cols + 31) // 32) * 16
-        at = (256 + codes + 255) // 256 * 256
         tiles = (rows + 127) // 128 * ((cols + 255) // 256)
+        at = 256 + tiles * 16384
         assert B.tp_fp4_bytes(rows, cols, fmt) == at + tiles * tile
         assert B.tp_fp4_offset(rows, cols, fmt, B.TPFP4_CODES) == 256
         assert B.tp_fp4_offset(rows, cols, fmt, B.TPFP4_SCALES) == at
@@ -106,12 +105,12 @@ def test_calls_of_no_rows_touch_nothing():
 
 
 @pytest.mark.parametrize("code,a", [
-    (ARG, (8, 64, 9, P, 8192, BF, X, 64)), (ARG, (8, 64, NV, P, 8192, 3, X, 64)),
-    (SHAPE, (-1, 64, NV, P, 8192, BF, X, 64)), (SHAPE, (8, 0, NV, P, 8192, BF, X, 64)),
-    (SHAPE, (8, 64, NV, P, 8192, BF, X, 63)), (ARG, (8, 64, NV, None, 8192, BF, X, 64)),
-    (ALIGN, (8, 64, NV, P + 128, 8192, BF, X, 64)), (WS, (8, 64, NV, P, 700, BF, X, 64)),
-    (ARG, (8, 64, NV, P, 8192, BF, None, 64)), (ALIGN, (8, 64, NV, P, 8192, F32, X + 2, 64)),
-    (ARG, (8, 64, NV, P, 8192, BF, P + 512, 64)),
+    (ARG, (8, 64, 9, P, 1 << 16, BF, X, 64)), (ARG, (8, 64, NV, P, 1 << 16, 3, X, 64)),
+    (SHAPE, (-1, 64, NV, P, 1 << 16, BF, X, 64)), (SHAPE, (8, 0, NV, P, 1 << 16, BF, X, 64)),
+    (SHAPE, (8, 64, NV, P, 1 << 16, BF, X, 63)), (ARG, (8, 64, NV, None, 1 << 16, BF, X, 64)),
+    (ALIGN, (8, 64, NV, P + 128, 1 << 16, BF, X, 64)), (WS, (8, 64, NV, P, 700, BF, X, 64)),
+    (ARG, (8, 64, NV, P, 1 << 16, BF, None, 64)), (ALIGN, (8, 64, NV, P, 1 << 16, F32, X + 2, 64)),
+    (ARG, (8, 64, NV, P, 1 << 16, BF, P + 512, 64)),
 ])
 def test_dequantize_refusals(code, a):
     refused(code, lambda: B.tp_fp4_dequantize(*a, stream=0))

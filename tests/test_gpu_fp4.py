@@ -257,9 +257,9 @@ def test_every_pair_of_codes_and_scales():
             byte = r.integers(lo, hi, (c.shape[0], K // size))
             packed, scales = O.pack(c, byte, fmt)
             t = fp4.quantize(torch.zeros(c.shape, device="cuda"), fmt)
-            t.codes().copy_(torch.from_numpy(packed))
-            at = B.tp_fp4_offset(t.rows, t.cols, t._code, B.TPFP4_SCALES)
-            t.buffer[at:at + scales.size].copy_(torch.from_numpy(scales))
+            for part, data in ((B.TPFP4_CODES, packed), (B.TPFP4_SCALES, scales)):
+                at = B.tp_fp4_offset(t.rows, t.cols, t._code, part)
+                t.buffer[at:at + data.size].copy_(torch.from_numpy(data))
             q.append((t, O.values(c, byte, 1.0, fmt)))
         (a, va), (b, vb) = q
         assert np.array_equal(f64(a.dequantize(F32)), va)
