@@ -103,6 +103,17 @@ int tp_fp4_matmul(long long T, long long N, long long K, int format,
                   const float* bias, int dtype, void* C, long long ldc,
                   void* stream);
 
+/* Both in one call, for a layer y = x W: x [T, K] (x_dtype, x_stride) is quantised
+ * into xq (tp_fp4_bytes(T, K, format) bytes; x_scale as tp_fp4_quantize's scale),
+ * C is xq times the packed W [N, K].  The product starts to load W while x is
+ * quantised, so that a few rows take less than the two calls.  xq and C share no
+ * memory with the rest. */
+int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
+                  const void* x, long long x_stride, int format, double x_scale,
+                  void* xq, size_t xq_bytes, const void* W, size_t w_bytes,
+                  const float* bias, int dtype, void* C, long long ldc,
+                  void* stream);
+
 /* Waits for `stream`, then reads and clears the status word of a packed matrix
  * that products read as A: TPMLP_OK, TPMLP_ERR_TIMEOUT (a bounded device wait
  * gave up; that product's C is undefined) or TPMLP_ERR_CUDA. */

@@ -67,7 +67,7 @@ EXPORTED_GRAD = ("tp_grad_workspace_bytes", "tp_grad_norm", "tp_grad_clip")
 EXPORTED_FP4 = (
     "tp_fp4_bytes", "tp_fp4_offset", "tp_fp4_quantize",
     "tp_fp4_colsum_workspace_bytes", "tp_fp4_dequantize", "tp_fp4_matmul",
-    "tp_fp4_check", "tp_fp4_mlp_weights_bytes", "tp_fp4_mlp_pack_weights",
+    "tp_fp4_linear", "tp_fp4_check", "tp_fp4_mlp_weights_bytes", "tp_fp4_mlp_pack_weights",
     "tp_fp4_mlp_workspace_bytes", "tp_fp4_mlp_forward",
 )
 
@@ -343,6 +343,9 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.tp_fp4_matmul.argtypes = [ll, ll, ll, _i, _vp, _sz, _vp, _sz, _vp, _i,
                                 _vp, ll, _vp]
     L.tp_fp4_matmul.restype = _i
+    L.tp_fp4_linear.argtypes = [ll, ll, ll, _i, _vp, ll, _i, dbl, _vp, _sz,
+                                _vp, _sz, _vp, _i, _vp, ll, _vp]
+    L.tp_fp4_linear.restype = _i
     L.tp_fp4_check.argtypes = [_vp, _vp]
     L.tp_fp4_check.restype = _i
     L.tp_fp4_mlp_weights_bytes.argtypes = [_vp, _i]
@@ -385,7 +388,7 @@ def tensor_calls():
                       "tp_grad_workspace_bytes", "tp_grad_norm",
                       "tp_grad_clip", "tp_fp4_bytes", "tp_fp4_quantize",
                       "tp_fp4_colsum_workspace_bytes", "tp_fp4_dequantize",
-                      "tp_fp4_matmul")])
+                      "tp_fp4_matmul", "tp_fp4_linear")])
         _calls = m
     return _calls
 
@@ -842,6 +845,14 @@ def tp_fp4_matmul(T, N, K, format, A, a_bytes, B, b_bytes, bias, dtype, C, ldc,
     _check(lib().tp_fp4_matmul(
         T, N, K, format, _ptr(A), a_bytes, _ptr(B), b_bytes, _ptr(bias), dtype,
         _ptr(C), ldc, _stream(stream)), "tp_fp4_matmul")
+
+
+def tp_fp4_linear(T, N, K, x_dtype, x, x_stride, format, x_scale, xq, xq_bytes,
+                  W, w_bytes, bias, dtype, C, ldc, stream=None):
+    _check(lib().tp_fp4_linear(
+        T, N, K, x_dtype, _ptr(x), x_stride, format, x_scale, _ptr(xq), xq_bytes,
+        _ptr(W), w_bytes, _ptr(bias), dtype, _ptr(C), ldc, _stream(stream)),
+        "tp_fp4_linear")
 
 
 def tp_fp4_check(packed, stream=None) -> int:

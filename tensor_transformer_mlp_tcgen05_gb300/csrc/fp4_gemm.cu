@@ -39,7 +39,7 @@ namespace {
 using namespace gemm;
 
 constexpr int PM = 256, PN = 256;   // a pair's tile
-constexpr int HM = 128, HN = 128;   // rows of A and of B a CTA loads
+constexpr int HM = 128;             // rows of A a CTA loads
 constexpr int STAGES = 5;
 constexpr int NUM_THREADS = 384;
 constexpr int NUM_EPI_WARPS = 8;
@@ -92,6 +92,27 @@ __device__ __forceinline__ bool wait_bounded_cluster(uint32_t bar,
       return false;
     }
   }
+}
+
+// A unit of a pair's work: a tile, or 128 of its columns.  Where a last round of
+// tiles would leave half the pairs idle or more, its tiles are dealt out as
+// halves (8192 x 5120: 640 tiles, 8.42 rounds of 76, take 8.5 instead of 9).
+struct Item {
+  int m0, n0;    // the pair's first row and column
+  int cols;      // 256 or 128; 0: a half that lies past the matrix
+};
+template <int EPI>
+__device__ __forceinline__ Item item_of(int item, int whole, int num_m, int num_n,
+                                        int group_m, int N) {
+  const int half = item - whole;
+  int mb, nb;
+  tile_coords(half < 0 ? item : whole + half / 2, num_m, num_n, group_m, mb, nb);
+  Item it;
+  it.m0 = mb * PM;
+  it.n0 = nb * PN + (half < 0 ? 0 : half % 2 * (PN / 2));
+  // (OUT_GELU_FP4 writes what its output's last k-tile holds past the matrix)
+  it.cols = half < 0 ? PN : it.n0 < N || EPI == OUT_GELU_FP4 ? PN / 2 : 0;
+  return it;
 }
 
 // bias[c0 .. c0 + 64) of which n are in the matrix.
@@ -218,7 +239,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                          const __grid_constant__ CUtensorMap tmSB,
                          const __grid_constant__ CUtensorMap tmO,
                          const ProductArgs args, const int tma_out,
-                         const int group_m) {
+                         const int group_m, const int halves) {
   constexpr uint32_t TILE = tile_bytes(FORMAT);
   constexpr uint32_t STAGE = stage_bytes<FORMAT>();
   extern __shared__ uint8_t smem_raw[];
@@ -239,6 +260,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARRIERS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
+  let_next_launch_start();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t prank = ptx::cluster_ctarank();
@@ -276,7 +298,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const Ctl ctl{abort_flag, args.status, args.budget_ns};
   const int num_m = (args.M + PM - 1) / PM;
   const int num_n = (args.N + PN - 1) / PN;
-  const int tiles = num_m * num_n;
+  const int whole = num_m * num_n - halves;   // tiles dealt out whole
+  const int items = whole + 2 * halves;
   const int ktiles = args.a.ktiles;
   const uint32_t lead_full0 = ptx::mapa_shared(full0, 0u);
   const uint32_t lead_shared = ptx::mapa_shared(shared, 0u);
@@ -287,31 +310,54 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // ---------------------------------------------------- producer --
       uint32_t stage = 0, phase = 0;
       bool alive = true;
-      for (int tile = pair; alive && tile < tiles; tile += num_pairs) {
-        int mb, nb;
-        tile_coords(tile, num_m, num_n, group_m, mb, nb);
-        const int m0 = mb * PM + static_cast<int>(prank) * HM;
-        const int n0 = nb * PN + static_cast<int>(prank) * HN;
-        // tile numbers; tiles past the matrix are filled with zeros
-        const int ta0 = (m0 / TILE_ROWS) * ktiles;
-        const int tb0 = (n0 / TILE_ROWS) * ktiles;
-        const int sb0 = (nb * PN / TILE_ROWS) * ktiles;
+      for (int item = pair; alive && item < items; item += num_pairs) {
+        const Item it = item_of<EPI>(item, whole, num_m, num_n, group_m, args.N);
+        if (it.cols == 0) continue;
+        // tile numbers; tiles past the matrix are filled with zeros.  B comes in
+        // boxes of 64 rows: a CTA takes half of the item's columns.
+        const int ta0 =
+            (it.m0 / TILE_ROWS + static_cast<int>(prank)) * ktiles;
+        const int n0 = it.n0 + static_cast<int>(prank) * it.cols / 2;
+        const int tb0 = n0 / TILE_ROWS * ktiles, row0 = n0 % TILE_ROWS;
+        const int sb0 = it.n0 / TILE_ROWS * ktiles;
+        const bool full = it.cols == PN;
+        const uint32_t bytes =
+            full ? STAGE : OPERAND_BYTES + OPERAND_BYTES / 2 + 2 * TILE;
+        auto load_b = [&](int kt, uint32_t st) {
+          if (leader) ptx::mbar_arrive_expect_tx(full0 + 8u * st, 2 * bytes);
+          const uint32_t fb = lead_full0 + 8u * st;
+          const uint32_t db = s_b + st * OPERAND_BYTES;
+          const int rb = (tb0 + kt) * TILE_ROWS + row0;
+          ptx::tma_load_2d_pair(db, &tmB, fb, 0, rb);
+          ptx::tma_load_2d_pair(s_sb + st * 2 * TILE, &tmSB, fb, 0, sb0 + kt);
+          if (full) {
+            ptx::tma_load_2d_pair(db + OPERAND_BYTES / 2, &tmB, fb, 0, rb + 64);
+            ptx::tma_load_2d_pair(s_sb + st * 2 * TILE + TILE, &tmSB, fb, 0,
+                                  sb0 + ktiles + kt);
+          }
+        };
+        auto load_a = [&](int kt, uint32_t st) {
+          const uint32_t fb = lead_full0 + 8u * st;
+          ptx::tma_load_2d_pair(s_a + st * OPERAND_BYTES, &tmA, fb, 0,
+                                (ta0 + kt) * TILE_ROWS);
+          ptx::tma_load_2d_pair(s_sa + st * TILE, &tmSA, fb, 0, ta0 + kt);
+        };
+        int early = 0;   // k-tiles of B loaded before A may be read
+        if (item == pair) {
+          early = min(ktiles, STAGES);
+          if (elect_one())
+            for (int kt = 0; kt < early; ++kt) load_b(kt, kt);
+          __syncwarp();
+          wait_for_launch_before();
+        }
         for (int kt = 0; kt < ktiles; ++kt) {
           if (!wait_warp(empty0 + 8u * stage, phase ^ 1u, ctl, ROLE_PRODUCER)) {
             alive = false;
             break;
           }
           if (elect_one()) {
-            if (leader) ptx::mbar_arrive_expect_tx(full0 + 8u * stage, 2 * STAGE);
-            const uint32_t fb = lead_full0 + 8u * stage;
-            ptx::tma_load_2d_pair(s_a + stage * OPERAND_BYTES, &tmA, fb, 0,
-                                  (ta0 + kt) * TILE_ROWS);
-            ptx::tma_load_2d_pair(s_b + stage * OPERAND_BYTES, &tmB, fb, 0,
-                                  (tb0 + kt) * TILE_ROWS);
-            ptx::tma_load_2d_pair(s_sa + stage * TILE, &tmSA, fb, 0, ta0 + kt);
-            ptx::tma_load_2d_pair(s_sb + stage * 2 * TILE, &tmSB, fb, 0, sb0 + kt);
-            ptx::tma_load_2d_pair(s_sb + stage * 2 * TILE + TILE, &tmSB, fb, 0,
-                                  sb0 + ktiles + kt);
+            if (kt >= early) load_b(kt, stage);
+            load_a(kt, stage);
           }
           __syncwarp();
           if (++stage == STAGES) {
@@ -330,7 +376,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint64_t desc_sb = sdesc_scales(s_sb);
       uint32_t stage = 0, phase = 0, j = 0;
       bool alive = true;
-      for (int tile = pair; alive && tile < tiles; tile += num_pairs, ++j) {
+      for (int item = pair; alive && item < items; item += num_pairs) {
+        const Item it = item_of<EPI>(item, whole, num_m, num_n, group_m, args.N);
+        if (it.cols == 0) continue;
         if (j > 0 && !__all_sync(0xffffffffu,
                                  wait_bounded_cluster(shared, (j - 1u) & 1u, ctl,
                                                       ROLE_MMA))) {
@@ -346,11 +394,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           ptx::tc_fence_after();
           if (elect_one()) {
-            ktile_mmas<FORMAT, 2, PM, PN, 2>(
-                d, desc_a + stage * (OPERAND_BYTES / 16),
-                desc_b + stage * (OPERAND_BYTES / 16),
-                desc_sa + stage * (TILE / 16), desc_sb + stage * (2 * TILE / 16),
-                tmem + T_SA, tmem + T_SB, kt == 0);
+            const uint64_t da = desc_a + stage * (OPERAND_BYTES / 16);
+            const uint64_t db = desc_b + stage * (OPERAND_BYTES / 16);
+            const uint64_t dsa = desc_sa + stage * (TILE / 16);
+            const uint64_t dsb = desc_sb + stage * (2 * TILE / 16);
+            if (it.cols == PN)
+              ktile_mmas<FORMAT, 2, PM, PN, 2>(d, da, db, dsa, dsb, tmem + T_SA,
+                                               tmem + T_SB, kt == 0);
+            else
+              ktile_mmas<FORMAT, 2, PM, PN / 2, 1>(d, da, db, dsa, dsb, tmem + T_SA,
+                                                   tmem + T_SB, kt == 0);
             ptx::mma_commit_pair(empty0 + 8u * stage, pair_mask);
             if (kt == ktiles - 1) ptx::mma_commit_pair(tfull, pair_mask);
           }
@@ -360,6 +413,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             phase ^= 1u;
           }
         }
+        ++j;
       }
       if (*reinterpret_cast<volatile int*>(abort_flag)) {
         // Wait for every MMA issued before TMEM is freed.
@@ -392,6 +446,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int q = warp & 3;      // TMEM sub-partition this warp may read
     const int half = ew >> 2;    // which 128-column half of the tile
     Stager st{s_epi + static_cast<uint32_t>(ew) * STAGE_CHUNK_BYTES, lane};
+    wait_for_launch_before();
     const float g = args.a.head->g * args.b.head->g;
     float inv_gy = 1.f;
     if constexpr (EPI == OUT_GELU_FP4) {
@@ -402,21 +457,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
     uint32_t j = 0;
-    for (int tile = pair; tile < tiles; tile += num_pairs, ++j) {
-      int mb, nb;
-      tile_coords(tile, num_m, num_n, group_m, mb, nb);
-      const int row0 = mb * PM + static_cast<int>(prank) * HM + q * 32;
+    for (int item = pair; item < items; item += num_pairs) {
+      const Item it = item_of<EPI>(item, whole, num_m, num_n, group_m, args.N);
+      if (it.cols == 0) continue;
+      const int row0 = it.m0 + static_cast<int>(prank) * HM + q * 32;
       const int row = row0 + lane;
-      const int col_base = nb * PN + half * 128;
+      const int chunks = it.cols / 128;   // of 64 columns, this warp's
       bool ok = wait_bounded(tfull, j & 1u, ctl, ROLE_EPILOGUE);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                             (j & 1u) * ACC_STEP + half * 128;
-      // the shared columns: of the first accumulator its last 48, of the second
-      // its first
-      const bool owner = half == 1 - static_cast<int>(j & 1u);
+                             (j & 1u) * ACC_STEP;
+      // the shared columns: of the first accumulator its last 48 (which a half
+      // does not use), of the second its first
+      const bool owner = (j & 1u) ? half == 0 : half == 1 && chunks == 2;
+      ++j;
       auto release = [&] {
         ptx::tc_fence_before();
         __syncwarp();
@@ -429,12 +485,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       };
       if (!owner) release();
 #pragma unroll 1
-      for (int jj = 0; jj < 2; ++jj) {
+      for (int jj = 0; jj < chunks; ++jj) {
         const int chunk = owner && half == 1 ? 1 - jj : jj;
-        const int c0 = col_base + chunk * 64;
+        const int col = (half * chunks + chunk) * 64;
+        const int c0 = it.n0 + col;
         uint32_t r0[32], r1[32];
-        ptx::tmem_ld_32x32b_x32(taddr + chunk * 64, r0);
-        ptx::tmem_ld_32x32b_x32(taddr + chunk * 64 + 32, r1);
+        ptx::tmem_ld_32x32b_x32(taddr + col, r0);
+        ptx::tmem_ld_32x32b_x32(taddr + col + 32, r1);
         ptx::tmem_ld_wait();
         if (owner && jj == 0) release();
         if (row0 >= args.M) continue;
@@ -508,20 +565,25 @@ cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tsa,
                           ((args.N + PN - 1) / PN);
   if (tiles > INT_MAX / 2) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = smem_bytes<FORMAT>();
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = args.dependent ? 2 : 1;
+  const long long last = tiles % max_pairs;   // tiles of the last round
+  const long long halves = 2 * last <= max_pairs ? last : 0;
+  const long long items = tiles + halves;
   cfg.gridDim = dim3(static_cast<unsigned>(
-      2 * (tiles < max_pairs ? tiles : static_cast<long long>(max_pairs))));
+      2 * (items < max_pairs ? items : static_cast<long long>(max_pairs))));
   e = cudaLaunchKernelEx(&cfg, kern, ta, tsa, tb, tsb, to != nullptr ? *to : ta,
-                         args, to != nullptr ? 1 : 0, 8);
+                         args, to != nullptr ? 1 : 0, 8, static_cast<int>(halves));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

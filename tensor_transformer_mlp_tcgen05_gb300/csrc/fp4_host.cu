@@ -136,22 +136,28 @@ int codes_map(CUtensorMap* m, const fp4::Packed& p, int box_rows) {
       static_cast<uint64_t>((p.rows + fp4::TILE_ROWS - 1) / fp4::TILE_ROWS) *
       p.ktiles * fp4::TILE_ROWS;
   return encode_map_u8(m, p.codes, 128, rows, 128,
-                       static_cast<uint32_t>(std::min(box_rows, fp4::TILE_ROWS)));
+                       static_cast<uint32_t>(box_rows));
 }
 
 // Whether a product goes to the kernel that splits K.
-bool few(const fp4::ProductArgs& a, int sms) {
-  if (a.M <= 256) return true;
+// Times in us (graph replays of one product in L2, NV), split against pairs:
+// 1 to 64 rows of A, 1024 to 20480 rows of B, K 1024 to 20480: 4.0 to 12.5 against
+// 5.4 to 23 (equal at 64 rows and K = 1024).  More rows: split pays where the
+// pairs have few tiles with long sums: K = 20480, 20 tiles (256 x 5120): 19.5
+// against 24.1, 32 tiles (512 x 4096): 26.4 against 24.6; K = 4096, 4 tiles (256 x
+// 1024): 8.8 against 9.1, 16 tiles (256 x 4096): 10.0 against 9.4.
+bool few(const fp4::ProductArgs& a) {
+  if (a.M <= 64) return true;
   const long long tiles = ((a.M + 255ll) / 256) * ((a.N + 255ll) / 256);
-  return 2 * tiles < sms / 2;
+  return 3 * tiles <= a.a.ktiles;
 }
 
 int product(HandleCore* core, const char* name, int format,
             const fp4::ProductArgs& a, int sms, cudaStream_t s) {
   CUtensorMap ta, tsa, tb, tsb, to;
-  const bool split = few(a, sms);
+  const bool split = few(a);
   TRY(codes_map(&ta, a.a, split ? fp4::split_tokens(a.M) : 128));
-  TRY(codes_map(&tb, a.b, 128));
+  TRY(codes_map(&tb, a.b, split ? 128 : 64));
   TRY(scales_map(&tsa, a.a, format));
   TRY(scales_map(&tsb, a.b, format));
   const size_t es = a.epilogue == fp4::OUT_FP32 ? 4 : 2;
@@ -164,6 +170,101 @@ int product(HandleCore* core, const char* name, int format,
                                              tma ? &to : nullptr, a, sms / 2, s);
   };
   return core != nullptr ? run(core, name, s, launch) : launched(name, launch());
+}
+
+// tp_fp4_quantize's arguments.
+int check_quantize(long long rows, long long cols, int dtype, const void* x,
+                   long long row_stride, int transpose, int format, double scale,
+                   const void* packed, size_t packed_bytes, const float* colsum,
+                   const void* workspace, size_t workspace_bytes, int* exponent) {
+  if (!format_ok(format)) return bad(TPMLP_ERR_ARG, "fp4: unknown format");
+  TRY(dtype_ok(dtype));
+  if (transpose != 0 && transpose != 1)
+    return bad(TPMLP_ERR_ARG, "fp4: transpose must be 0 or 1");
+  if (!dim_ok(cols) || rows < transpose || rows > MAX_DIM)
+    return bad(TPMLP_ERR_SHAPE, "fp4: rows or cols out of range");
+  if (row_stride < cols || row_stride > (1ll << 40))
+    return bad(TPMLP_ERR_SHAPE, "fp4: row stride below the columns or too large");
+  TRY(scale_exponent(format, scale, true, exponent));
+  const size_t es = dtype == TPMLP_BF16 ? 2 : 4;
+  const long long prows = transpose ? cols : rows, pcols = transpose ? rows : cols;
+  TRY(packed_ok("fp4: packed is null", prows, pcols, format, packed, packed_bytes));
+  if (colsum != nullptr && !transpose)
+    return bad(TPMLP_ERR_ARG, "fp4: colsum needs transpose = 1");
+  if (rows == 0) return TPMLP_OK;
+  if (x == nullptr) return bad(TPMLP_ERR_ARG, "fp4: x is null");
+  if (!aligned(x, es) || !aligned(colsum, 4) || !aligned(workspace, 16))
+    return bad(TPMLP_ERR_ALIGN, "fp4: x, colsum or workspace off its alignment");
+  const size_t nx = extent(rows, cols, row_stride, es);
+  const size_t np = fp4::packed_bytes(prows, pcols, format);
+  const size_t ns = static_cast<size_t>(cols) * 4;
+  const size_t nw = tp_fp4_colsum_workspace_bytes(rows, cols);
+  if (overlap(x, nx, packed, np))
+    return bad(TPMLP_ERR_ARG, "fp4: packed overlaps x");
+  if (colsum != nullptr) {
+    if (workspace == nullptr) return bad(TPMLP_ERR_ARG, "fp4: workspace is null");
+    if (workspace_bytes < nw)
+      return bad(TPMLP_ERR_WORKSPACE, "fp4: workspace too small for colsum");
+    if (overlap(colsum, ns, x, nx) || overlap(colsum, ns, packed, np) ||
+        overlap(colsum, ns, workspace, nw) || overlap(workspace, nw, x, nx) ||
+        overlap(workspace, nw, packed, np))
+      return bad(TPMLP_ERR_ARG, "fp4: colsum or workspace overlaps another buffer");
+  }
+  // one block a 64-column, 256-row piece (columns) or 16 rows x 256 (rows)
+  const long long blocks = transpose
+                               ? (cols + 63) / 64 * ((rows + 255) / 256)
+                               : (rows + 15) / 16 * ((cols + 255) / 256);
+  if (blocks > INT_MAX) return bad(TPMLP_ERR_SHAPE, "fp4: matrix too large");
+  return TPMLP_OK;
+}
+
+// tp_fp4_matmul's arguments.
+int check_matmul(long long T, long long N, long long K, int format, const void* A,
+                 size_t a_bytes, const void* B, size_t b_bytes, const float* bias,
+                 int dtype, const void* C, long long ldc) {
+  if (!format_ok(format)) return bad(TPMLP_ERR_ARG, "fp4: unknown format");
+  TRY(dtype_ok(dtype));
+  if (T < 0 || T > MAX_DIM || !dim_ok(N) || !dim_ok(K))
+    return bad(TPMLP_ERR_SHAPE, "fp4: T, N or K out of range");
+  if (ldc < N || ldc > (1ll << 40))
+    return bad(TPMLP_ERR_SHAPE, "fp4: ldc below N or too large");
+  TRY(packed_ok("fp4: A is null", T, K, format, A, a_bytes));
+  TRY(packed_ok("fp4: B is null", N, K, format, B, b_bytes));
+  if (T == 0) return TPMLP_OK;
+  if (C == nullptr) return bad(TPMLP_ERR_ARG, "fp4: C is null");
+  const size_t es = dtype == TPMLP_BF16 ? 2 : 4;
+  if (!aligned(C, es) || !aligned(bias, 4))
+    return bad(TPMLP_ERR_ALIGN, "fp4: C or bias off its alignment");
+  const size_t nc = extent(T, N, ldc, es);
+  if (overlap(C, nc, A, fp4::packed_bytes(T, K, format)) ||
+      overlap(C, nc, B, fp4::packed_bytes(N, K, format)) ||
+      overlap(C, nc, bias, static_cast<size_t>(N) * 4))
+    return bad(TPMLP_ERR_ARG, "fp4: C overlaps an input");
+  // rows of all tiles and output tiles are counted in 32 bits
+  const long long ktiles = (K + 255) / 256;
+  if ((std::max(T, N) + 127) / 128 * ktiles > INT_MAX / 256 ||
+      (T + 127) / 128 * ((N + 127) / 128) > INT_MAX / 16)
+    return bad(TPMLP_ERR_SHAPE, "fp4: product too large");
+  return TPMLP_OK;
+}
+
+// A product with checked arguments.
+int matmul(long long T, long long N, long long K, int format, const void* A,
+           const void* B, const float* bias, int dtype, void* C, long long ldc,
+           int dependent, int sms, cudaStream_t s) {
+  fp4::ProductArgs a = {};
+  a.a = fp4::view(A, T, K);
+  a.b = fp4::view(B, N, K);
+  a.M = static_cast<int>(T);
+  a.N = static_cast<int>(N);
+  a.epilogue = dtype == TPMLP_BF16 ? fp4::OUT_BF16 : fp4::OUT_FP32;
+  a.out = C;
+  a.ldo = ldc;
+  a.bias = bias;
+  a.status = a.a.head->status;
+  a.budget_ns = HandleCore().budget_ns;
+  a.dependent = dependent;
+  return product(nullptr, "fp4_matmul", format, a, sms, s);
 }
 
 // ----------------------------------------------------------- MLP block --
@@ -232,45 +333,11 @@ int tp_fp4_quantize(long long rows, long long cols, int dtype, const void* x,
                     double scale, void* packed, size_t packed_bytes,
                     float* colsum, void* workspace, size_t workspace_bytes,
                     void* stream) {
-  if (!format_ok(format)) return bad(TPMLP_ERR_ARG, "fp4: unknown format");
-  TRY(dtype_ok(dtype));
-  if (transpose != 0 && transpose != 1)
-    return bad(TPMLP_ERR_ARG, "fp4: transpose must be 0 or 1");
-  if (!dim_ok(cols) || rows < transpose || rows > MAX_DIM)
-    return bad(TPMLP_ERR_SHAPE, "fp4: rows or cols out of range");
-  if (row_stride < cols || row_stride > (1ll << 40))
-    return bad(TPMLP_ERR_SHAPE, "fp4: row stride below the columns or too large");
   int exponent = 0;
-  TRY(scale_exponent(format, scale, true, &exponent));
-  const size_t es = dtype == TPMLP_BF16 ? 2 : 4;
-  const long long prows = transpose ? cols : rows, pcols = transpose ? rows : cols;
-  TRY(packed_ok("fp4: packed is null", prows, pcols, format, packed, packed_bytes));
-  if (colsum != nullptr && !transpose)
-    return bad(TPMLP_ERR_ARG, "fp4: colsum needs transpose = 1");
+  TRY(check_quantize(rows, cols, dtype, x, row_stride, transpose, format, scale,
+                     packed, packed_bytes, colsum, workspace, workspace_bytes,
+                     &exponent));
   if (rows == 0) return TPMLP_OK;
-  if (x == nullptr) return bad(TPMLP_ERR_ARG, "fp4: x is null");
-  if (!aligned(x, es) || !aligned(colsum, 4) || !aligned(workspace, 16))
-    return bad(TPMLP_ERR_ALIGN, "fp4: x, colsum or workspace off its alignment");
-  const size_t nx = extent(rows, cols, row_stride, es);
-  const size_t np = fp4::packed_bytes(prows, pcols, format);
-  const size_t ns = static_cast<size_t>(cols) * 4;
-  const size_t nw = tp_fp4_colsum_workspace_bytes(rows, cols);
-  if (overlap(x, nx, packed, np))
-    return bad(TPMLP_ERR_ARG, "fp4: packed overlaps x");
-  if (colsum != nullptr) {
-    if (workspace == nullptr) return bad(TPMLP_ERR_ARG, "fp4: workspace is null");
-    if (workspace_bytes < nw)
-      return bad(TPMLP_ERR_WORKSPACE, "fp4: workspace too small for colsum");
-    if (overlap(colsum, ns, x, nx) || overlap(colsum, ns, packed, np) ||
-        overlap(colsum, ns, workspace, nw) || overlap(workspace, nw, x, nx) ||
-        overlap(workspace, nw, packed, np))
-      return bad(TPMLP_ERR_ARG, "fp4: colsum or workspace overlaps another buffer");
-  }
-  // one block a 64-column, 256-row piece (columns) or 16 rows x 256 (rows)
-  const long long blocks = transpose
-                               ? (cols + 63) / 64 * ((rows + 255) / 256)
-                               : (rows + 15) / 16 * ((cols + 255) / 256);
-  if (blocks > INT_MAX) return bad(TPMLP_ERR_SHAPE, "fp4: matrix too large");
   int sms = 0;
   TRY(check_device(&sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -315,44 +382,36 @@ int tp_fp4_matmul(long long T, long long N, long long K, int format,
                   const void* A, size_t a_bytes, const void* B, size_t b_bytes,
                   const float* bias, int dtype, void* C, long long ldc,
                   void* stream) {
-  if (!format_ok(format)) return bad(TPMLP_ERR_ARG, "fp4: unknown format");
-  TRY(dtype_ok(dtype));
-  if (T < 0 || T > MAX_DIM || !dim_ok(N) || !dim_ok(K))
-    return bad(TPMLP_ERR_SHAPE, "fp4: T, N or K out of range");
-  if (ldc < N || ldc > (1ll << 40))
-    return bad(TPMLP_ERR_SHAPE, "fp4: ldc below N or too large");
-  TRY(packed_ok("fp4: A is null", T, K, format, A, a_bytes));
-  TRY(packed_ok("fp4: B is null", N, K, format, B, b_bytes));
+  TRY(check_matmul(T, N, K, format, A, a_bytes, B, b_bytes, bias, dtype, C, ldc));
   if (T == 0) return TPMLP_OK;
-  if (C == nullptr) return bad(TPMLP_ERR_ARG, "fp4: C is null");
-  const size_t es = dtype == TPMLP_BF16 ? 2 : 4;
-  if (!aligned(C, es) || !aligned(bias, 4))
-    return bad(TPMLP_ERR_ALIGN, "fp4: C or bias off its alignment");
-  const size_t nc = extent(T, N, ldc, es);
-  if (overlap(C, nc, A, fp4::packed_bytes(T, K, format)) ||
-      overlap(C, nc, B, fp4::packed_bytes(N, K, format)) ||
-      overlap(C, nc, bias, static_cast<size_t>(N) * 4))
-    return bad(TPMLP_ERR_ARG, "fp4: C overlaps an input");
-  // rows of all tiles and output tiles are counted in 32 bits
-  const long long ktiles = (K + 255) / 256;
-  if ((std::max(T, N) + 127) / 128 * ktiles > INT_MAX / 256 ||
-      (T + 127) / 128 * ((N + 127) / 128) > INT_MAX / 16)
-    return bad(TPMLP_ERR_SHAPE, "fp4: product too large");
   int sms = 0;
   TRY(check_device(&sms));
-  fp4::ProductArgs a = {};
-  a.a = fp4::view(A, T, K);
-  a.b = fp4::view(B, N, K);
-  a.M = static_cast<int>(T);
-  a.N = static_cast<int>(N);
-  a.epilogue = dtype == TPMLP_BF16 ? fp4::OUT_BF16 : fp4::OUT_FP32;
-  a.out = C;
-  a.ldo = ldc;
-  a.bias = bias;
-  a.status = a.a.head->status;
-  a.budget_ns = HandleCore().budget_ns;
-  return product(nullptr, "fp4_matmul", format, a, sms,
-                 static_cast<cudaStream_t>(stream));
+  return matmul(T, N, K, format, A, B, bias, dtype, C, ldc, 0, sms,
+                static_cast<cudaStream_t>(stream));
+}
+
+int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
+                  const void* x, long long x_stride, int format, double x_scale,
+                  void* xq, size_t xq_bytes, const void* W, size_t w_bytes,
+                  const float* bias, int dtype, void* C, long long ldc,
+                  void* stream) {
+  int exponent = 0;
+  TRY(check_quantize(T, K, x_dtype, x, x_stride, 0, format, x_scale, xq, xq_bytes,
+                     nullptr, nullptr, 0, &exponent));
+  TRY(check_matmul(T, N, K, format, xq, xq_bytes, W, w_bytes, bias, dtype, C, ldc));
+  if (T == 0) return TPMLP_OK;
+  const size_t nx = extent(T, K, x_stride, x_dtype == TPMLP_BF16 ? 2 : 4);
+  const size_t nq = fp4::packed_bytes(T, K, format);
+  if (overlap(xq, nq, W, fp4::packed_bytes(N, K, format)) ||
+      overlap(xq, nq, bias, static_cast<size_t>(N) * 4) ||
+      overlap(C, extent(T, N, ldc, dtype == TPMLP_BF16 ? 2 : 4), x, nx))
+    return bad(TPMLP_ERR_ARG, "fp4: xq or C overlaps an input");
+  int sms = 0;
+  TRY(check_device(&sms));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  TRY(quantize(nullptr, "fp4_quantize", T, K, x_dtype == TPMLP_BF16, x, x_stride,
+               false, format, exponent, xq, nullptr, s));
+  return matmul(T, N, K, format, xq, W, bias, dtype, C, ldc, 1, sms, s);
 }
 
 int tp_fp4_check(void* packed, void* stream) {
@@ -453,6 +512,7 @@ int tp_fp4_mlp_forward(tp_mlp_handle* H, int tokens, int format, const void* X,
   a.gelu_mode = c.gelu_mode;
   a.status = a.a.head->status;
   a.budget_ns = H->core.budget_ns;
+  a.dependent = 1;   // of the quantisation, and the second product of the first
   TRY(product(&H->core, "gemm1_gelu_fp4", format, a, sms, s));
   a.a = a.y;
   a.b = fp4::view(pk + P.b, h, f);

@@ -54,17 +54,21 @@ struct ProductArgs {
   int gelu_mode;
   int* status;
   unsigned long long budget_ns;
+  // 1: may start while the launch before it on the stream, which makes A and
+  // itself started after B was complete, still runs
+  int dependent;
 };
 
-// Tiles of 256 x 256 on CTA pairs, for many rows of A and B.
+// Tiles of 256 x 256 on CTA pairs, for many rows of A and B.  ta: boxes of 128
+// rows of A's codes, tb: of 64 rows of B's; tsa, tsb: scale tiles.
 cudaError_t launch_product_pairs(int format, const CUtensorMap& ta,
                                  const CUtensorMap& tsa, const CUtensorMap& tb,
                                  const CUtensorMap& tsb, const CUtensorMap* to,
                                  const ProductArgs& args, int max_pairs,
                                  cudaStream_t s);
 
-// Tiles of 128 rows of B x up to 256 rows of A, K split over a cluster, for
-// few rows of A or few tiles.
+// Tiles of 128 rows of B x up to 128 rows of A, K split over a cluster, for few
+// rows of A.  ta: boxes of split_tokens(M) rows, tb: of 128.
 int split_tokens(int M);   // rows of A in a tile
 cudaError_t launch_product_split(int format, const CUtensorMap& ta,
                                  const CUtensorMap& tsa, const CUtensorMap& tb,

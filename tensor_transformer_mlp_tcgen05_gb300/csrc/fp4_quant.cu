@@ -107,6 +107,8 @@ template <class T, int FORMAT, int LD, int PASSES>
 __global__ void __launch_bounds__(THREADS)
     rows_kernel(const T* __restrict__ x, long long stride, const Packed p,
                 int g_exponent) {
+  // (a product that is launched as this one's dependent starts loading weights)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int unit = threadIdx.x & 15;
   const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.ktiles));

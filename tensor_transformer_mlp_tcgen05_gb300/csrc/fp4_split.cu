@@ -1,6 +1,6 @@
 // The four-bit product for few rows of A (single tokens of a few requests), and
 // for products of few tiles: bound by the read of B, whose rows take the MMA's
-// 128 lanes while up to 256 rows of A are its columns.
+// 128 lanes while up to 128 rows of A are its columns.
 //
 // A CTA takes 128 rows of B, NT rows of A and one of the cluster's ranges of K,
 // so that a product of few tiles still keeps every SM loading.  Four warps:
@@ -27,11 +27,9 @@ constexpr int MAX_SPLIT = 8;       // CTAs of a cluster
 template <int FORMAT, int NT>
 struct Shape {
   static constexpr uint32_t TILE = tile_bytes(FORMAT);
-  static constexpr uint32_t A_TILES = NT > TILE_ROWS ? 2 : 1;   // scale tiles of A
   static constexpr uint32_t B_BYTES = FM * 128, A_BYTES = NT * 128;
-  static constexpr uint32_t STAGE = B_BYTES + A_BYTES + (1 + A_TILES) * TILE;
-  // two CTAs an SM; with 256 rows of A, one
-  static constexpr uint32_t BUDGET = NT > 128 ? 220 * 1024 : 108 * 1024;
+  static constexpr uint32_t STAGE = B_BYTES + A_BYTES + 2 * TILE;
+  static constexpr uint32_t BUDGET = 108 * 1024;   // two CTAs an SM
   static constexpr int STAGES = BUDGET / STAGE < 6 ? BUDGET / STAGE : 6;
   static constexpr int NUM_BARRIERS = 2 * STAGES + 1;
   static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE +
@@ -39,9 +37,8 @@ struct Shape {
   // tensor memory: the accumulator, then the scales of B and of A
   static constexpr uint32_t T_SB = NT;
   static constexpr uint32_t T_SA = NT + 4 * copies_per_tile(FORMAT);
-  static constexpr uint32_t T_USED =
-      T_SA + 4 * copies_per_tile(FORMAT) * A_TILES;
-  static constexpr uint32_t T_COLS = T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
+  static constexpr uint32_t T_USED = T_SA + 4 * copies_per_tile(FORMAT);
+  static constexpr uint32_t T_COLS = T_USED <= 128 ? 128 : 256;
   static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "shared memory budget");
   static_assert(NT * FM * 4 <= STAGES * STAGE, "partial sums fit the stages");
 };
@@ -158,6 +155,7 @@ __global__ void __launch_bounds__(NUM_THREADS)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::NUM_BARRIERS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
+  let_next_launch_start();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(ptx::cluster_ctarank());
@@ -197,22 +195,28 @@ __global__ void __launch_bounds__(NUM_THREADS)
     // ------------------------------------------------------ producer --
     uint32_t stage = 0, phase = 0;
     const int tb0 = n0 / TILE_ROWS * ktiles, ta0 = t0 / TILE_ROWS * ktiles;
+    auto load_b = [&](int kt, uint32_t st) {
+      const uint32_t fb = full0 + 8u * st;
+      ptx::mbar_arrive_expect_tx(fb, S::STAGE);
+      ptx::tma_load_2d(s_b + st * S::B_BYTES, &tmB, fb, 0, (tb0 + kt) * TILE_ROWS);
+      ptx::tma_load_2d(s_sb + st * S::TILE, &tmSB, fb, 0, tb0 + kt);
+    };
+    auto load_a = [&](int kt, uint32_t st) {
+      const uint32_t fb = full0 + 8u * st;
+      ptx::tma_load_2d(s_a + st * S::A_BYTES, &tmA, fb, 0,
+                       (ta0 + kt) * TILE_ROWS);
+      ptx::tma_load_2d(s_sa + st * S::TILE, &tmSA, fb, 0, ta0 + kt);
+    };
+    const int early = min(k_lo + S::STAGES, k_hi);   // B before A may be read
+    if (elect_one())
+      for (int kt = k_lo; kt < early; ++kt) load_b(kt, kt - k_lo);
+    __syncwarp();
+    wait_for_launch_before();
     for (int kt = k_lo; kt < k_hi; ++kt) {
       if (!wait_warp(empty0 + 8u * stage, phase ^ 1u, ctl, ROLE_PRODUCER)) break;
       if (elect_one()) {
-        const uint32_t fb = full0 + 8u * stage;
-        ptx::mbar_arrive_expect_tx(fb, S::STAGE);
-        ptx::tma_load_2d(s_b + stage * S::B_BYTES, &tmB, fb, 0, (tb0 + kt) * TILE_ROWS);
-        ptx::tma_load_2d(s_sb + stage * S::TILE, &tmSB, fb, 0, tb0 + kt);
-        const uint32_t da = s_a + stage * S::A_BYTES;
-        ptx::tma_load_2d(da, &tmA, fb, 0, (ta0 + kt) * TILE_ROWS);
-        if constexpr (S::A_TILES == 2)
-          ptx::tma_load_2d(da + CODE_TILE, &tmA, fb, 0,
-                           (ta0 + ktiles + kt) * TILE_ROWS);
-        const uint32_t sa = s_sa + stage * S::A_TILES * S::TILE;
-        ptx::tma_load_2d(sa, &tmSA, fb, 0, ta0 + kt);
-        if constexpr (S::A_TILES == 2)
-          ptx::tma_load_2d(sa + S::TILE, &tmSA, fb, 0, ta0 + ktiles + kt);
+        if (kt >= early) load_b(kt, stage);
+        load_a(kt, stage);
       }
       __syncwarp();
       if (++stage == S::STAGES) {
@@ -232,10 +236,10 @@ __global__ void __launch_bounds__(NUM_THREADS)
       if (!wait_warp(full0 + 8u * stage, phase, ctl, ROLE_MMA)) break;
       ptx::tc_fence_after();
       if (elect_one()) {
-        ktile_mmas<FORMAT, 1, FM, NT, S::A_TILES>(
+        ktile_mmas<FORMAT, 1, FM, NT, 1>(
             tmem, desc_b + stage * (S::B_BYTES / 16),
             desc_a + stage * (S::A_BYTES / 16), desc_sb + stage * (S::TILE / 16),
-            desc_sa + stage * (S::A_TILES * S::TILE / 16), tmem + S::T_SB,
+            desc_sa + stage * (S::TILE / 16), tmem + S::T_SB,
             tmem + S::T_SA, kt == k_lo);
         ptx::mma_commit(empty0 + 8u * stage);
       }
@@ -280,6 +284,7 @@ __global__ void __launch_bounds__(NUM_THREADS)
     ptx::tmem_dealloc(tmem_base, S::T_COLS);
   }
   // --------------------------------------------------- sums, epilogue --
+  wait_for_launch_before();
   const float g = args.a.head->g * args.b.head->g;
   float inv_gy = 1.f;
   if constexpr (EPI == OUT_GELU_FP4) {
@@ -307,12 +312,12 @@ __global__ void __launch_bounds__(NUM_THREADS)
   ptx::cluster_sync();   // no CTA leaves while its sums are being read
 }
 
-// Clusters of `size` CTAs that fit at once, `per_sm` CTAs to an SM, when a
-// cluster's SMs come from one of eight groups of at least sms / 9.  (A rule on the SM
+// Clusters of `size` CTAs that fit at once, two CTAs to an SM, when a cluster's
+// SMs come from one of eight groups of at least sms / 9.  (A rule on the SM
 // count alone, so that the order of the sums, and with it the last bits, is the
 // same on every GPU of a model.)
-long long resident_clusters(int size, int per_sm, int sms) {
-  return 8ll * (sms / 9 * per_sm / size);
+long long resident_clusters(int size, int sms) {
+  return 8ll * (sms / 9 * 2 / size);
 }
 
 template <int FORMAT, int EPI, int NT>
@@ -330,20 +335,22 @@ cudaError_t launch_tokens(const CUtensorMap& ta, const CUtensorMap& tsa,
   // as many CTAs as the SMs hold at once, and a k-tile at least for each
   int split = 1;
   for (int c = 2; c <= MAX_SPLIT && c <= args.a.ktiles; ++c)
-    if (features * tokens <= resident_clusters(c, NT > 128 ? 1 : 2, sms)) split = c;
+    if (features * tokens <= resident_clusters(c, sms)) split = c;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(split);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.gridDim = dim3(static_cast<unsigned>(features * split),
                      static_cast<unsigned>(tokens));
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = args.dependent ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, ta, tsa, tb, tsb, args, split);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -356,8 +363,7 @@ cudaError_t launch_epilogue(const CUtensorMap& ta, const CUtensorMap& tsa,
     case 16: return launch_tokens<FORMAT, EPI, 16>(ta, tsa, tb, tsb, args, sms, s);
     case 32: return launch_tokens<FORMAT, EPI, 32>(ta, tsa, tb, tsb, args, sms, s);
     case 64: return launch_tokens<FORMAT, EPI, 64>(ta, tsa, tb, tsb, args, sms, s);
-    case 128: return launch_tokens<FORMAT, EPI, 128>(ta, tsa, tb, tsb, args, sms, s);
-    default: return launch_tokens<FORMAT, EPI, 256>(ta, tsa, tb, tsb, args, sms, s);
+    default: return launch_tokens<FORMAT, EPI, 128>(ta, tsa, tb, tsb, args, sms, s);
   }
 }
 
@@ -378,7 +384,7 @@ cudaError_t launch_format(const CUtensorMap& ta, const CUtensorMap& tsa,
 }  // namespace
 
 int split_tokens(int M) {
-  return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
 }
 
 cudaError_t launch_product_split(int format, const CUtensorMap& ta,

@@ -40,6 +40,7 @@ struct Library {
   decltype(&tp_fp4_colsum_workspace_bytes) fp4_colsum_bytes = nullptr;
   decltype(&tp_fp4_dequantize) fp4_dequantize = nullptr;
   decltype(&tp_fp4_matmul) fp4_matmul = nullptr;
+  decltype(&tp_fp4_linear) fp4_linear = nullptr;
   PyObject* check = nullptr;   // binding._check(status, what)
 } lib;
 
@@ -645,17 +646,12 @@ PyObject* fp4_linear(PyObject* const* a) {
   const size_t nq = static_cast<size_t>(q.numel());
   const void* bp = pb.const_data_ptr();
   void* op = x.rows == 0 ? nullptr : out.data_ptr();
-  const char* what = "tp_fp4_quantize";
   check(without_gil([&] {
-          const int rc = lib.fp4_quantize(x.rows, K, x.dtype, x.data(), x.stride,
-                                          0, format, scale, qp, nq, nullptr,
-                                          nullptr, 0, place.stream);
-          if (rc != TPMLP_OK) return rc;
-          what = "tp_fp4_matmul";
-          return lib.fp4_matmul(x.rows, N, K, format, qp, nq, bp, nb, bias, dtype,
-                                op, row_stride(out), place.stream);
+          return lib.fp4_linear(x.rows, N, K, x.dtype, x.data(), x.stride, format,
+                                scale, qp, nq, bp, nb, bias, dtype, op,
+                                row_stride(out), place.stream);
         }),
-        what);
+        "tp_fp4_linear");
   return wrapped(out);
 }
 
@@ -679,6 +675,7 @@ PyObject* bind(PyObject* const* a) {
   l.fp4_colsum_bytes = reinterpret_cast<decltype(l.fp4_colsum_bytes)>(at(10));
   l.fp4_dequantize = reinterpret_cast<decltype(l.fp4_dequantize)>(at(11));
   l.fp4_matmul = reinterpret_cast<decltype(l.fp4_matmul)>(at(12));
+  l.fp4_linear = reinterpret_cast<decltype(l.fp4_linear)>(at(13));
   Py_INCREF(a[0]);
   l.check = a[0];
   Py_XDECREF(lib.check);
@@ -736,7 +733,7 @@ void set(int i) {
 }  // namespace
 
 PyMODINIT_FUNC PyInit__pycall() {
-  set<bind, 13>(0);
+  set<bind, 14>(0);
   set<rope, 11>(1);
   set<norm_forward, 16>(2);
   set<norm_backward, 21>(3);

@@ -142,6 +142,28 @@ def test_matmul_refusals(code, kw):
     refused(code, lambda: matmul(**kw))
 
 
+def linear(T=20, N=30, K=100, xd=BF, x=X, xs=100, fmt=NV, scale=1.0, xq=P,
+           nq=1 << 20, Wp=P2, nw=1 << 20, bias=None, dtype=BF, C=C, ldc=30):
+    B.tp_fp4_linear(T, N, K, xd, x, xs, fmt, scale, xq, nq, Wp, nw, bias, dtype, C,
+                    ldc, stream=0)
+
+
+@pytest.mark.parametrize("code,kw", [
+    (ARG, dict(fmt=3)), (ARG, dict(xd=4)), (ARG, dict(dtype=4)),
+    (SHAPE, dict(T=-1)), (SHAPE, dict(N=0)), (SHAPE, dict(K=0)),
+    (SHAPE, dict(xs=99)), (SHAPE, dict(ldc=29)), (ARG, dict(scale=3.0)),
+    (ARG, dict(x=None)), (ARG, dict(xq=None)), (ARG, dict(Wp=None)),
+    (ARG, dict(C=None)), (ALIGN, dict(x=X + 1)), (ALIGN, dict(xq=P + 16)),
+    (ALIGN, dict(Wp=P2 + 16)), (WS, dict(nq=100)), (WS, dict(nw=100)),
+    (ARG, dict(xq=X)), (ARG, dict(xq=P2)), (ARG, dict(C=X + 100)),
+    (ARG, dict(C=P + 1024)), (ARG, dict(C=P2 + 1024)), (ARG, dict(bias=C + 4)),
+    (ARG, dict(bias=P + 1024)),
+])
+def test_linear_refusals(code, kw):
+    refused(code, lambda: linear(**kw))
+    linear(T=0)
+
+
 def block(**kw):
     cfg = dict(hidden=128, ffn=512, shards=2, max_tokens=256, dtype=BF,
                use_layernorm=0, ln_eps=1e-5, gelu_mode=B.TPMLP_GELU_ERF)
