@@ -33,8 +33,8 @@
  * - Plain matrices are bf16 (TPMLP_BF16) or fp32 (TPMLP_FP32), row-major with
  *   any row stride >= the number of columns, aligned to their element; 32-byte
  *   aligned rows are read fastest.  A packed matrix is one buffer of
- *   tp_fp4_bytes bytes, 256-byte aligned, whose first 256 bytes hold g and the
- *   status word of the products that read it as A.
+ *   tp_fp4_bytes bytes, 256-byte aligned, whose first 4096 bytes hold the status
+ *   word of the products that read it as A (16 bytes), g (fp32) and scratch.
  * - rows and cols are 1 .. 2^28 (rows of a plain matrix: 0 .. 2^28).
  * - Pointers are DEVICE pointers the caller owns; the library never allocates
  *   device memory.  Calls only enqueue work on `stream`.  No output shares
@@ -78,6 +78,7 @@ long long tp_fp4_offset(long long rows, long long cols, int format, int which);
  * matrix.
  *   scale    NV: g, a power of two from 2^-126 to 2^127, or 0 to take it from
  *            the matrix (x is read twice); MX: 0 or 1
+ *   like     NV with scale = 0: a packed matrix whose g is taken instead, or NULL
  *   colsum   [cols] fp32, the sums of x's columns (a bias gradient, in a fixed
  *            order; transpose = 1 only), or NULL
  *   workspace  tp_fp4_colsum_workspace_bytes(rows, cols) bytes, 16-byte
@@ -85,9 +86,9 @@ long long tp_fp4_offset(long long rows, long long cols, int format, int which);
  * rows = 0 (transpose = 0) enqueues nothing. */
 int tp_fp4_quantize(long long rows, long long cols, int dtype, const void* x,
                     long long row_stride, int transpose, int format,
-                    double scale, void* packed, size_t packed_bytes,
-                    float* colsum, void* workspace, size_t workspace_bytes,
-                    void* stream);
+                    double scale, const void* like, void* packed,
+                    size_t packed_bytes, float* colsum, void* workspace,
+                    size_t workspace_bytes, void* stream);
 size_t tp_fp4_colsum_workspace_bytes(long long rows, long long cols);
 
 /* The values of a packed [rows, cols] matrix, written as `dtype` (exact in bf16

@@ -335,8 +335,8 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.tp_fp4_offset.restype = ll
     L.tp_fp4_colsum_workspace_bytes.argtypes = [ll, ll]
     L.tp_fp4_colsum_workspace_bytes.restype = _sz
-    L.tp_fp4_quantize.argtypes = [ll, ll, _i, _vp, ll, _i, _i, dbl, _vp, _sz,
-                                  _vp, _vp, _sz, _vp]
+    L.tp_fp4_quantize.argtypes = [ll, ll, _i, _vp, ll, _i, _i, dbl, _vp, _vp,
+                                  _sz, _vp, _vp, _sz, _vp]
     L.tp_fp4_quantize.restype = _i
     L.tp_fp4_dequantize.argtypes = [ll, ll, _i, _vp, _sz, _i, _vp, ll, _vp]
     L.tp_fp4_dequantize.restype = _i
@@ -388,7 +388,8 @@ def tensor_calls():
                       "tp_grad_workspace_bytes", "tp_grad_norm",
                       "tp_grad_clip", "tp_fp4_bytes", "tp_fp4_quantize",
                       "tp_fp4_colsum_workspace_bytes", "tp_fp4_dequantize",
-                      "tp_fp4_matmul", "tp_fp4_linear")])
+                      "tp_fp4_matmul", "tp_fp4_linear",
+                      "tp_fp4_mlp_workspace_bytes", "tp_fp4_mlp_forward")])
         _calls = m
     return _calls
 
@@ -825,11 +826,11 @@ def tp_fp4_colsum_workspace_bytes(rows: int, cols: int) -> int:
 
 
 def tp_fp4_quantize(rows, cols, dtype, x, row_stride, transpose, format, scale,
-                    packed, packed_bytes, colsum=None, workspace=None,
+                    like, packed, packed_bytes, colsum=None, workspace=None,
                     workspace_bytes=0, stream=None):
     _check(lib().tp_fp4_quantize(
         rows, cols, dtype, _ptr(x), row_stride, transpose, format, scale,
-        _ptr(packed), packed_bytes, _ptr(colsum), _ptr(workspace),
+        _ptr(like), _ptr(packed), packed_bytes, _ptr(colsum), _ptr(workspace),
         workspace_bytes, _stream(stream)), "tp_fp4_quantize")
 
 

@@ -14,7 +14,8 @@ namespace fp4 {
 constexpr int TILE_ROWS = 128;   // rows of a tile
 constexpr int TILE_COLS = 256;   // columns of a tile: 128 bytes of codes a row
 constexpr int CODE_TILE = TILE_ROWS * TILE_COLS / 2;
-constexpr size_t HEADER_BYTES = 256;
+constexpr size_t HEADER_BYTES = 4096;
+constexpr int AMAX_SLOTS = 608;  // blocks of a pass for the largest |x|
 
 __host__ __device__ constexpr int block_size(int format) {
   return format == TPFP4_NV ? 16 : 32;
@@ -24,14 +25,16 @@ __host__ __device__ constexpr int tile_bytes(int format) {
   return TILE_ROWS * TILE_COLS / block_size(format);
 }
 
-// The first 256 bytes of a packed matrix.  status: of the products that read it
-// as A (first, as in the blocks' workspaces); amax: the largest finite |x| (fp32
-// bits) of a matrix quantised with its own g.
+// The first bytes of a packed matrix.  status: of the products that read it as A
+// (first, as in the blocks' workspaces); amax: of a matrix quantised with its own
+// g, the largest finite |x| (fp32 bits) that each block of the pass before found.
 struct Header {
   int status[4];
   float g;
-  unsigned int amax;
+  int pad[59];
+  unsigned int amax[AMAX_SLOTS];
 };
+static_assert(sizeof(Header) <= HEADER_BYTES, "header");
 
 // One packed matrix: tile (r / 128, c / 256) is tile number (r / 128) ktiles +
 // c / 256 of the codes and of the scales.  A product's copies are whole tiles, so

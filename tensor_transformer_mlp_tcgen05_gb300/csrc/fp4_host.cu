@@ -49,6 +49,8 @@ int dtype_ok(int dtype) {
              : bad(TPMLP_ERR_ARG, "fp4: dtype must be TPMLP_BF16 or TPMLP_FP32");
 }
 
+constexpr int AUTO_SCALE = 1 << 20;   // "g is the matrix's own", as an exponent
+
 // The exponent of g; AUTO_SCALE for 0 (NV).
 int scale_exponent(int format, double scale, bool may_be_auto, int* e) {
   if (format == TPFP4_MX) {
@@ -58,7 +60,7 @@ int scale_exponent(int format, double scale, bool may_be_auto, int* e) {
     return TPMLP_OK;
   }
   if (scale == 0.0 && may_be_auto) {
-    *e = fp4::AUTO_SCALE;
+    *e = AUTO_SCALE;
     return TPMLP_OK;
   }
   int x = 0;
@@ -84,27 +86,26 @@ int packed_ok(const char* what, long long rows, long long cols, int format,
 // Quantise along rows or columns, arguments checked.
 int quantize(HandleCore* core, const char* name, long long rows, long long cols,
              bool bf16, const void* x, long long stride, bool transpose,
-             int format, int exponent, void* packed, float* part,
+             int format, int exponent, const void* like, void* packed, float* part,
              cudaStream_t s) {
   const fp4::Packed p = transpose ? fp4::view(packed, cols, rows)
                                   : fp4::view(packed, rows, cols);
   auto step = [&](const char* n, auto&& f) {
     return core != nullptr ? run(core, n, s, f) : launched(n, f());
   };
-  if (exponent == fp4::AUTO_SCALE) {
-    const cudaError_t e = cudaMemsetAsync(packed, 0, fp4::HEADER_BYTES, s);
-    if (e != cudaSuccess) return launched("cudaMemsetAsync(fp4 header)", e);
+  fp4::Gain g = {exponent, 0, nullptr};
+  if (exponent == AUTO_SCALE && like != nullptr) {
+    g.like = static_cast<const fp4::Header*>(like);
+  } else if (exponent == AUTO_SCALE) {
     TRY(step("fp4_amax", [&] {
-      return fp4::launch_amax(bf16, x, stride, rows, cols, p.head, s);
+      return fp4::launch_amax(bf16, x, stride, rows, cols, p.head, &g.slots, s);
     }));
   }
   return step(name, [&] {
     return transpose
                ? fp4::launch_quantize_columns(bf16, format, x, stride,
-                                              static_cast<int>(rows), p,
-                                              exponent, part, s)
-               : fp4::launch_quantize_rows(bf16, format, x, stride, p, exponent,
-                                           s);
+                                              static_cast<int>(rows), p, g, part, s)
+               : fp4::launch_quantize_rows(bf16, format, x, stride, p, g, s);
   });
 }
 
@@ -175,8 +176,9 @@ int product(HandleCore* core, const char* name, int format,
 // tp_fp4_quantize's arguments.
 int check_quantize(long long rows, long long cols, int dtype, const void* x,
                    long long row_stride, int transpose, int format, double scale,
-                   const void* packed, size_t packed_bytes, const float* colsum,
-                   const void* workspace, size_t workspace_bytes, int* exponent) {
+                   const void* like, const void* packed, size_t packed_bytes,
+                   const float* colsum, const void* workspace,
+                   size_t workspace_bytes, int* exponent) {
   if (!format_ok(format)) return bad(TPMLP_ERR_ARG, "fp4: unknown format");
   TRY(dtype_ok(dtype));
   if (transpose != 0 && transpose != 1)
@@ -186,6 +188,10 @@ int check_quantize(long long rows, long long cols, int dtype, const void* x,
   if (row_stride < cols || row_stride > (1ll << 40))
     return bad(TPMLP_ERR_SHAPE, "fp4: row stride below the columns or too large");
   TRY(scale_exponent(format, scale, true, exponent));
+  if (like != nullptr && (format != TPFP4_NV || scale != 0.0))
+    return bad(TPMLP_ERR_ARG, "fp4: like is NV's, with scale = 0");
+  if (!aligned(like, 256))
+    return bad(TPMLP_ERR_ALIGN, "fp4: a packed matrix must be 256-byte aligned");
   const size_t es = dtype == TPMLP_BF16 ? 2 : 4;
   const long long prows = transpose ? cols : rows, pcols = transpose ? rows : cols;
   TRY(packed_ok("fp4: packed is null", prows, pcols, format, packed, packed_bytes));
@@ -199,8 +205,8 @@ int check_quantize(long long rows, long long cols, int dtype, const void* x,
   const size_t np = fp4::packed_bytes(prows, pcols, format);
   const size_t ns = static_cast<size_t>(cols) * 4;
   const size_t nw = tp_fp4_colsum_workspace_bytes(rows, cols);
-  if (overlap(x, nx, packed, np))
-    return bad(TPMLP_ERR_ARG, "fp4: packed overlaps x");
+  if (overlap(x, nx, packed, np) || overlap(like, fp4::HEADER_BYTES, packed, np))
+    return bad(TPMLP_ERR_ARG, "fp4: packed overlaps x or like");
   if (colsum != nullptr) {
     if (workspace == nullptr) return bad(TPMLP_ERR_ARG, "fp4: workspace is null");
     if (workspace_bytes < nw)
@@ -330,19 +336,19 @@ size_t tp_fp4_colsum_workspace_bytes(long long rows, long long cols) {
 
 int tp_fp4_quantize(long long rows, long long cols, int dtype, const void* x,
                     long long row_stride, int transpose, int format,
-                    double scale, void* packed, size_t packed_bytes,
-                    float* colsum, void* workspace, size_t workspace_bytes,
+                    double scale, const void* like, void* packed,
+                    size_t packed_bytes, float* colsum, void* workspace, size_t workspace_bytes,
                     void* stream) {
   int exponent = 0;
   TRY(check_quantize(rows, cols, dtype, x, row_stride, transpose, format, scale,
-                     packed, packed_bytes, colsum, workspace, workspace_bytes,
+                     like, packed, packed_bytes, colsum, workspace, workspace_bytes,
                      &exponent));
   if (rows == 0) return TPMLP_OK;
   int sms = 0;
   TRY(check_device(&sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   TRY(quantize(nullptr, "fp4_quantize", rows, cols, dtype == TPMLP_BF16, x,
-               row_stride, transpose != 0, format, exponent, packed,
+               row_stride, transpose != 0, format, exponent, like, packed,
                colsum != nullptr ? static_cast<float*>(workspace) : nullptr, s));
   if (colsum == nullptr) return TPMLP_OK;
   return launched("fp4_colsum", launch_colsum_finalize(
@@ -396,8 +402,8 @@ int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
                   const float* bias, int dtype, void* C, long long ldc,
                   void* stream) {
   int exponent = 0;
-  TRY(check_quantize(T, K, x_dtype, x, x_stride, 0, format, x_scale, xq, xq_bytes,
-                     nullptr, nullptr, 0, &exponent));
+  TRY(check_quantize(T, K, x_dtype, x, x_stride, 0, format, x_scale, nullptr,
+                     xq, xq_bytes, nullptr, nullptr, 0, &exponent));
   TRY(check_matmul(T, N, K, format, xq, xq_bytes, W, w_bytes, bias, dtype, C, ldc));
   if (T == 0) return TPMLP_OK;
   const size_t nx = extent(T, K, x_stride, x_dtype == TPMLP_BF16 ? 2 : 4);
@@ -410,7 +416,7 @@ int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
   TRY(check_device(&sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   TRY(quantize(nullptr, "fp4_quantize", T, K, x_dtype == TPMLP_BF16, x, x_stride,
-               false, format, exponent, xq, nullptr, s));
+               false, format, exponent, nullptr, xq, nullptr, s));
   return matmul(T, N, K, format, xq, W, bias, dtype, C, ldc, 1, sms, s);
 }
 
@@ -443,11 +449,11 @@ int tp_fp4_mlp_pack_weights(tp_mlp_handle* H, int format, const void* A,
   TRY(check_device(&sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* pk = static_cast<char*>(packed);
-  const int e = format == TPFP4_NV ? fp4::AUTO_SCALE : 0;
+  const int e = format == TPFP4_NV ? AUTO_SCALE : 0;
   TRY(quantize(&H->core, "fp4_quantize_weights", c.hidden, c.ffn, true, A, c.ffn,
-               true, format, e, pk + p.a, nullptr, s));
+               true, format, e, nullptr, pk + p.a, nullptr, s));
   return quantize(&H->core, "fp4_quantize_weights", c.ffn, c.hidden, true, B,
-                  c.hidden, true, format, e, pk + p.b, nullptr, s);
+                  c.hidden, true, format, e, nullptr, pk + p.b, nullptr, s);
 }
 
 size_t tp_fp4_mlp_workspace_bytes(const tp_mlp_handle* H, int tokens,
@@ -499,7 +505,7 @@ int tp_fp4_mlp_forward(tp_mlp_handle* H, int tokens, int format, const void* X,
     Xop = ws + L.xn;
   }
   TRY(quantize(&H->core, "fp4_quantize_x", tokens, h, true, Xop, h, false, format,
-               xe, ws + L.xq, nullptr, s));
+               xe, nullptr, ws + L.xq, nullptr, s));
   fp4::ProductArgs a = {};
   a.a = fp4::view(ws + L.xq, tokens, h);
   a.b = fp4::view(pk + P.a, f, h);

@@ -8,25 +8,30 @@
 namespace tpmlp {
 namespace fp4 {
 
-// "g is the matrix's own", where launches take its exponent.
-constexpr int AUTO_SCALE = 1 << 20;
+// Where a quantisation takes g from: 2^exponent; or another packed matrix (like);
+// or the matrix's own largest |x|, left in `slots` words of its header by
+// launch_amax, whose dependent the launch then is.
+struct Gain {
+  int exponent;
+  int slots;
+  const Header* like;
+};
 
-// head->amax = max(head->amax, the largest finite |x|) over x [rows, cols].
+// The largest finite |x| of x [rows, cols], block by block; returns the blocks.
 cudaError_t launch_amax(bool bf16, const void* x, long long stride,
-                        long long rows, long long cols, Header* head,
+                        long long rows, long long cols, Header* head, int* slots,
                         cudaStream_t s);
 
-// x [p.rows, p.cols] into p; g = 2^g_exponent, or from p.head->amax
-// (AUTO_SCALE).  With a given exponent the header is written whole.
+// x [p.rows, p.cols] into p.
 cudaError_t launch_quantize_rows(bool bf16, int format, const void* x,
                                  long long stride, const Packed& p,
-                                 int g_exponent, cudaStream_t s);
+                                 const Gain& g, cudaStream_t s);
 
 // x [x_rows = p.cols, p.rows], transposed, into p.  part (nullable):
 // [p.ktiles][p.rows] sums of x's columns over 256 rows each.
 cudaError_t launch_quantize_columns(bool bf16, int format, const void* x,
                                     long long stride, int x_rows,
-                                    const Packed& p, int g_exponent,
+                                    const Packed& p, const Gain& g,
                                     float* part, cudaStream_t s);
 
 cudaError_t launch_dequantize(const Packed& p, int format, bool bf16, void* out,

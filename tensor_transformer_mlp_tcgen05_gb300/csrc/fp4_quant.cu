@@ -85,16 +85,22 @@ __device__ __forceinline__ void load16(const T* p, int n, Raw<T>& r) {
   }
 }
 
-// 1 / g, from the matrix's amax or as given; block 0 writes the header.
-__device__ __forceinline__ float inverse_g(const Packed& p, int given) {
-  const bool automatic = given == AUTO_SCALE;
-  const int e = automatic ? auto_exponent(p.head->amax) : given;
+// 1 / g (all threads); block 0 writes the header.
+__device__ __forceinline__ float inverse_g(const Packed& p, const Gain& gain) {
+  int e = gain.exponent;
+  if (gain.slots > 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // for the pass before
+    uint32_t top = 0;
+    for (int i = threadIdx.x & 31; i < gain.slots; i += 32)
+      top = max(top, p.head->amax[i]);
+    e = auto_exponent(__reduce_max_sync(0xffffffffu, top));
+  } else if (gain.like != nullptr) {   // a power of two
+    e = static_cast<int>(__float_as_uint(gain.like->g) >> 23) - 127;
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     p.head->g = exp2_of(e);
-    if (!automatic) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p.head->status[i] = 0;
-    }
+    for (int i = 0; i < 4; ++i) p.head->status[i] = 0;
   }
   return exp2_of(-e);
 }
@@ -106,7 +112,7 @@ __device__ __forceinline__ float inverse_g(const Packed& p, int given) {
 template <class T, int FORMAT, int LD, int PASSES>
 __global__ void __launch_bounds__(THREADS)
     rows_kernel(const T* __restrict__ x, long long stride, const Packed p,
-                int g_exponent) {
+                const Gain gain) {
   // (a product that is launched as this one's dependent starts loading weights)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -128,8 +134,7 @@ __global__ void __launch_bounds__(THREADS)
       load16<T, LD>(src + 16 * i * stride,
                     row0 + 16 * i < p.rows ? p.cols - col : 0, raw[i]);
   }
-  const float inv_g = FORMAT == TPFP4_NV ? inverse_g(p, g_exponent)
-                                         : (inverse_g(p, 0), 1.f);
+  const float inv_g = inverse_g(p, gain);
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int row = row0 + 16 * i;
@@ -206,7 +211,8 @@ constexpr int T_COLS = 64;   // columns of x a block takes
 template <class T, int FORMAT, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 2)
     columns_kernel(const T* __restrict__ x, long long stride, int x_rows,
-                   const Packed p, int g_exponent, float* __restrict__ part) {
+                   const Packed p, const Gain gain, float* __restrict__ part) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // 16-byte unit u of row n at unit u ^ (n / 2 mod 8): the lanes of a warp,
   // two rows apart, write to different banks
   __shared__ uint4 s_codes[T_COLS * 8];
@@ -228,8 +234,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int i = 0; i < 32; ++i)
       raw[i].load(src + i * stride, k0 + i < x_rows ? p.rows - n : 0);
   }
-  const float inv_g = FORMAT == TPFP4_NV ? inverse_g(p, g_exponent)
-                                         : (inverse_g(p, 0), 1.f);
+  const float inv_g = inverse_g(p, gain);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int r = 2 * lane + j;
@@ -294,14 +299,15 @@ __device__ __forceinline__ uint32_t finite(uint32_t bits) {
 }
 
 // An item is AMAX_UNITS units of 16 elements in a row; a block takes every
-// gridDim-th item.  A maximum does not depend on the order, nor the result on
-// the atomics'.
+// gridDim-th item and leaves its maximum in a slot of its own: nothing to clear
+// before, no atomics.
 constexpr int AMAX_UNITS = 2 * THREADS;
 
 template <class T, int LD>
 __global__ void __launch_bounds__(THREADS)
     amax_kernel(const T* __restrict__ x, long long stride, long long rows,
                 long long cols, Header* head) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long segments = (cols + AMAX_UNITS * 16 - 1) / (AMAX_UNITS * 16);
   uint32_t top = 0;
   for (long long item = blockIdx.x; item < rows * segments; item += gridDim.x) {
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(THREADS)
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int i = 1; i < THREADS / 32; ++i) top = max(top, s_top[i]);
-    atomicMax(&head->amax, top);
+    head->amax[blockIdx.x] = top;
   }
 }
 
@@ -434,47 +440,59 @@ bool on_boundary(const void* p, long long stride_bytes, int bytes) {
 // Blocks that keep all SMs busy: with fewer, a block takes fewer rows.
 constexpr long long FULL_GRID = 152 * 4;
 
+// A launch, as the dependent of the amax pass where there is one.
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, const Gain& gain,
+                   cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = gain.slots > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <class T, int FORMAT, int LD>
-void rows_launch(const T* x, long long stride, const Packed& p, int g,
-                 cudaStream_t s) {
+cudaError_t rows_launch(const T* x, long long stride, const Packed& p,
+                        const Gain& g, cudaStream_t s) {
   const long long units = (p.rows + 15ll) / 16 * p.ktiles;
   if (units >= 4 * FULL_GRID)
-    rows_kernel<T, FORMAT, LD, 4><<<
-        static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), THREADS, 0, s>>>(
-        x, stride, p, g);
-  else
-    rows_kernel<T, FORMAT, LD, 1><<<static_cast<unsigned>(units), THREADS, 0, s>>>(
-        x, stride, p, g);
+    return launch(rows_kernel<T, FORMAT, LD, 4>,
+                  static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), g, s, x,
+                  stride, p, g);
+  return launch(rows_kernel<T, FORMAT, LD, 1>, static_cast<unsigned>(units), g, s,
+                x, stride, p, g);
 }
 
 template <class T, int FORMAT>
-void rows_format(const T* x, long long stride, const Packed& p, int g,
-                 cudaStream_t s) {
+cudaError_t rows_format(const T* x, long long stride, const Packed& p,
+                        const Gain& g, cudaStream_t s) {
   const long long bytes = stride * static_cast<long long>(sizeof(T));
-  if (on_boundary(x, bytes, 32))
-    rows_launch<T, FORMAT, 32>(x, stride, p, g, s);
-  else if (on_boundary(x, bytes, 16))
-    rows_launch<T, FORMAT, 16>(x, stride, p, g, s);
-  else
-    rows_launch<T, FORMAT, 0>(x, stride, p, g, s);
+  if (on_boundary(x, bytes, 32)) return rows_launch<T, FORMAT, 32>(x, stride, p, g, s);
+  if (on_boundary(x, bytes, 16)) return rows_launch<T, FORMAT, 16>(x, stride, p, g, s);
+  return rows_launch<T, FORMAT, 0>(x, stride, p, g, s);
 }
 
 template <class T, int FORMAT>
-void columns_format(const T* x, long long stride, int x_rows, const Packed& p,
-                    int g, float* part, cudaStream_t s) {
+cudaError_t columns_format(const T* x, long long stride, int x_rows,
+                           const Packed& p, const Gain& g, float* part,
+                           cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(
       (p.rows + static_cast<long long>(T_COLS) - 1) / T_COLS * p.ktiles);
-  if (on_boundary(x, stride * static_cast<long long>(sizeof(T)), 2 * sizeof(T)))
-    columns_kernel<T, FORMAT, true>
-        <<<grid, THREADS, 0, s>>>(x, stride, x_rows, p, g, part);
-  else
-    columns_kernel<T, FORMAT, false>
-        <<<grid, THREADS, 0, s>>>(x, stride, x_rows, p, g, part);
+  const bool pairs =
+      on_boundary(x, stride * static_cast<long long>(sizeof(T)), 2 * sizeof(T));
+  return launch(pairs ? columns_kernel<T, FORMAT, true>
+                      : columns_kernel<T, FORMAT, false>,
+                grid, g, s, x, stride, x_rows, p, g, part);
 }
 
 template <class T>
-void amax_type(const T* x, long long stride, long long rows, long long cols,
-               Header* head, cudaStream_t s) {
+int amax_type(const T* x, long long stride, long long rows, long long cols,
+              Header* head, cudaStream_t s) {
   if (stride == cols) {   // one long row
     cols *= rows;
     stride = cols;
@@ -482,8 +500,7 @@ void amax_type(const T* x, long long stride, long long rows, long long cols,
   }
   const long long items =
       (cols + AMAX_UNITS * 16 - 1) / (AMAX_UNITS * 16) * rows;
-  const unsigned grid =
-      static_cast<unsigned>(items < 4 * 152 ? items : 4 * 152);
+  const int grid = static_cast<int>(items < AMAX_SLOTS ? items : AMAX_SLOTS);
   const long long bytes = rows == 1 ? 0 : stride * static_cast<long long>(sizeof(T));
   if (on_boundary(x, bytes, 32))
     amax_kernel<T, 32><<<grid, THREADS, 0, s>>>(x, stride, rows, cols, head);
@@ -491,6 +508,7 @@ void amax_type(const T* x, long long stride, long long rows, long long cols,
     amax_kernel<T, 16><<<grid, THREADS, 0, s>>>(x, stride, rows, cols, head);
   else
     amax_kernel<T, 0><<<grid, THREADS, 0, s>>>(x, stride, rows, cols, head);
+  return grid;
 }
 
 template <class T>
@@ -511,52 +529,45 @@ void dequantize_type(const Packed& p, int format, T* out, long long stride,
 }  // namespace
 
 cudaError_t launch_amax(bool bf16, const void* x, long long stride,
-                        long long rows, long long cols, Header* head,
+                        long long rows, long long cols, Header* head, int* slots,
                         cudaStream_t s) {
-  if (bf16)
-    amax_type(static_cast<const __nv_bfloat16*>(x), stride, rows, cols, head, s);
-  else
-    amax_type(static_cast<const float*>(x), stride, rows, cols, head, s);
+  *slots = bf16 ? amax_type(static_cast<const __nv_bfloat16*>(x), stride, rows,
+                            cols, head, s)
+                : amax_type(static_cast<const float*>(x), stride, rows, cols, head,
+                            s);
   return cudaGetLastError();
 }
 
 cudaError_t launch_quantize_rows(bool bf16, int format, const void* x,
                                  long long stride, const Packed& p,
-                                 int g_exponent, cudaStream_t s) {
+                                 const Gain& g, cudaStream_t s) {
   if (bf16) {
     const auto* b = static_cast<const __nv_bfloat16*>(x);
-    if (format == TPFP4_NV)
-      rows_format<__nv_bfloat16, TPFP4_NV>(b, stride, p, g_exponent, s);
-    else
-      rows_format<__nv_bfloat16, TPFP4_MX>(b, stride, p, g_exponent, s);
-  } else {
-    const auto* f = static_cast<const float*>(x);
-    if (format == TPFP4_NV)
-      rows_format<float, TPFP4_NV>(f, stride, p, g_exponent, s);
-    else
-      rows_format<float, TPFP4_MX>(f, stride, p, g_exponent, s);
+    return format == TPFP4_NV
+               ? rows_format<__nv_bfloat16, TPFP4_NV>(b, stride, p, g, s)
+               : rows_format<__nv_bfloat16, TPFP4_MX>(b, stride, p, g, s);
   }
-  return cudaGetLastError();
+  const auto* f = static_cast<const float*>(x);
+  return format == TPFP4_NV ? rows_format<float, TPFP4_NV>(f, stride, p, g, s)
+                            : rows_format<float, TPFP4_MX>(f, stride, p, g, s);
 }
 
 cudaError_t launch_quantize_columns(bool bf16, int format, const void* x,
                                     long long stride, int x_rows,
-                                    const Packed& p, int g_exponent,
+                                    const Packed& p, const Gain& g,
                                     float* part, cudaStream_t s) {
   if (bf16) {
     const auto* b = static_cast<const __nv_bfloat16*>(x);
-    if (format == TPFP4_NV)
-      columns_format<__nv_bfloat16, TPFP4_NV>(b, stride, x_rows, p, g_exponent, part, s);
-    else
-      columns_format<__nv_bfloat16, TPFP4_MX>(b, stride, x_rows, p, g_exponent, part, s);
-  } else {
-    const auto* f = static_cast<const float*>(x);
-    if (format == TPFP4_NV)
-      columns_format<float, TPFP4_NV>(f, stride, x_rows, p, g_exponent, part, s);
-    else
-      columns_format<float, TPFP4_MX>(f, stride, x_rows, p, g_exponent, part, s);
+    return format == TPFP4_NV
+               ? columns_format<__nv_bfloat16, TPFP4_NV>(b, stride, x_rows, p, g,
+                                                         part, s)
+               : columns_format<__nv_bfloat16, TPFP4_MX>(b, stride, x_rows, p, g,
+                                                         part, s);
   }
-  return cudaGetLastError();
+  const auto* f = static_cast<const float*>(x);
+  return format == TPFP4_NV
+             ? columns_format<float, TPFP4_NV>(f, stride, x_rows, p, g, part, s)
+             : columns_format<float, TPFP4_MX>(f, stride, x_rows, p, g, part, s);
 }
 
 cudaError_t launch_dequantize(const Packed& p, int format, bool bf16, void* out,

@@ -1,4 +1,5 @@
-// _pycall: the tensor calls of rotary.py, clip.py and fp4.py.
+// _pycall: the tensor calls of rotary.py, clip.py, fp4.py and the four-bit part of
+// mlp.py.
 //
 // A Python module that checks the tensors of a call, makes its outputs and
 // workspace, and calls tp_rope.h / tp_grad.h / tp_fp4.h.  It computes nothing.  These
@@ -17,6 +18,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
 #include <sstream>
 #include <string>
 #include <vector>
@@ -41,6 +43,8 @@ struct Library {
   decltype(&tp_fp4_dequantize) fp4_dequantize = nullptr;
   decltype(&tp_fp4_matmul) fp4_matmul = nullptr;
   decltype(&tp_fp4_linear) fp4_linear = nullptr;
+  decltype(&tp_fp4_mlp_workspace_bytes) fp4_mlp_workspace_bytes = nullptr;
+  decltype(&tp_fp4_mlp_forward) fp4_mlp_forward = nullptr;
   PyObject* check = nullptr;   // binding._check(status, what)
 } lib;
 
@@ -540,42 +544,38 @@ const float* bias_of(PyObject* o, long long n, const at::Device& dev) {
   return static_cast<const float*>(t->const_data_ptr());
 }
 
-// fp4_quantize(x, transpose, format, scale, packed, colsum, stream)
-//   -> (packed, column sums or None)
+// fp4_quantize(x, transpose, format, scale, like, packed, stream) -> packed
 PyObject* fp4_quantize(PyObject* const* a) {
   const Matrix x("x", tensor("x", a[0]));
   const at::Device dev = x.t.device();
-  const int transpose = PyObject_IsTrue(a[1]), sums = PyObject_IsTrue(a[5]);
-  if (transpose < 0 || sums < 0) throw Raised{};
+  const int transpose = PyObject_IsTrue(a[1]);
+  if (transpose < 0) throw Raised{};
   const int format = static_cast<int>(integer(a[2]));
   const double scale = real(a[3]);
+  const at::Tensor* like = maybe("scale", a[4]);
+  if (like != nullptr && (like->scalar_type() != at::kByte || !like->is_contiguous() ||
+                          like->numel() < 4096 || like->device() != dev))
+    throw Refused{"scale: expected a packed matrix on " + dev.str()};
   const long long rows = transpose ? x.cols : x.rows;
   const long long cols = transpose ? x.rows : x.cols;
   const Place place(dev, a[6]);
-  at::Tensor packed, colsum, ws;
-  if (a[4] == Py_None) {
+  at::Tensor packed;
+  if (a[5] == Py_None) {
     packed = new_packed(rows, cols, format, dev);
   } else {
-    packed = tensor("out", a[4]);
+    packed = tensor("out", a[5]);
     packed_of("out", packed, rows, cols, format, dev);
   }
-  size_t bytes = 0;
-  if (sums) {
-    colsum = make({x.cols}, at::kFloat, dev);
-    bytes = lib.fp4_colsum_bytes(x.rows, x.cols);
-    ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);   // of this call
-  }
+  const void* lp = like != nullptr ? like->const_data_ptr() : nullptr;
   void* pp = packed.data_ptr();
-  float* cp = sums ? colsum.data_ptr<float>() : nullptr;
-  void* wp = sums ? ws.data_ptr() : nullptr;
   check(without_gil([&] {
           return lib.fp4_quantize(x.rows, x.cols, x.dtype, x.data(), x.stride,
-                                  transpose, format, scale, pp,
-                                  static_cast<size_t>(packed.numel()), cp, wp,
-                                  bytes, place.stream);
+                                  transpose, format, scale, lp, pp,
+                                  static_cast<size_t>(packed.numel()), nullptr,
+                                  nullptr, 0, place.stream);
         }),
         "tp_fp4_quantize");
-  return tuple_of({packed, colsum});
+  return wrapped(packed);
 }
 
 // fp4_dequantize(packed, rows, cols, format, dtype, out, stream) -> values
@@ -655,6 +655,132 @@ PyObject* fp4_linear(PyObject* const* a) {
   return wrapped(out);
 }
 
+// fp4_backward(dy, x, weight_rows, format, dy_scale, x_scale, dtype, bias_grad,
+//              stream) -> (dx, dw, db or None): the gradients of fp4_linear, for
+// at least one token; weight_rows is W [K, N] packed along N.
+PyObject* fp4_backward(PyObject* const* a) {
+  const Matrix dy("dy", tensor("dy", a[0])), x("x", tensor("x", a[1]));
+  const at::Tensor& w = tensor("weight_rows", a[2]);
+  const at::Device dev = dy.t.device();
+  const long long T = dy.rows, N = dy.cols, K = x.cols;
+  const int format = static_cast<int>(integer(a[3]));
+  const double dy_scale = real(a[4]), x_scale = real(a[5]);
+  const int dtype = static_cast<int>(integer(a[6]));
+  const int sums = PyObject_IsTrue(a[7]);
+  if (sums < 0) throw Raised{};
+  if (x.rows != T || x.t.device() != dev)
+    throw Refused{"dy and x differ in tokens or device: " + shown(dy.t) + ", " +
+                  shown(x.t)};
+  const size_t nw = packed_of("weight_rows", w, K, N, format, dev);
+  const Place place(dev, a[8]);
+  const at::Tensor dx = make({T, K}, plain_type(dtype), dev);
+  const at::Tensor dw = make({K, N}, at::kFloat, dev);
+  at::Tensor db, ws;
+  // the packed operands belong to this call: calls on several streams, and
+  // captured graphs, share none
+  const at::Tensor q = new_packed(T, N, format, dev);
+  const at::Tensor dyt = new_packed(N, T, format, dev);
+  const at::Tensor xt = new_packed(K, T, format, dev);
+  size_t wsn = 0;
+  if (sums) {
+    db = make({N}, at::kFloat, dev);
+    wsn = lib.fp4_colsum_bytes(T, N);
+    ws = make({static_cast<int64_t>(wsn)}, at::kByte, dev);
+  }
+  auto size = [](const at::Tensor& t) { return static_cast<size_t>(t.numel()); };
+  void *qp = q.data_ptr(), *yp = dyt.data_ptr(), *xp = xt.data_ptr();
+  void *dxp = dx.data_ptr(), *dwp = dw.data_ptr();
+  float* dbp = sums ? db.data_ptr<float>() : nullptr;
+  void* wsp = sums ? ws.data_ptr() : nullptr;
+  const void* wp = w.const_data_ptr();
+  // dy's own g serves both of its quantisations
+  const void* like = format == TPFP4_NV && dy_scale == 0.0 ? qp : nullptr;
+  const char* what = "tp_fp4_linear";
+  check(without_gil([&] {
+          int rc = lib.fp4_linear(T, K, N, dy.dtype, dy.data(), dy.stride, format,
+                                  dy_scale, qp, size(q), wp, nw, nullptr, dtype,
+                                  dxp, K, place.stream);
+          if (rc != TPMLP_OK) return rc;
+          what = "tp_fp4_quantize";
+          rc = lib.fp4_quantize(T, N, dy.dtype, dy.data(), dy.stride, 1, format,
+                                dy_scale, like, yp, size(dyt), dbp, wsp, wsn,
+                                place.stream);
+          if (rc != TPMLP_OK) return rc;
+          rc = lib.fp4_quantize(T, K, x.dtype, x.data(), x.stride, 1, format,
+                                x_scale, nullptr, xp, size(xt), nullptr, nullptr, 0,
+                                place.stream);
+          if (rc != TPMLP_OK) return rc;
+          what = "tp_fp4_matmul";
+          return lib.fp4_matmul(K, N, T, format, xp, size(xt), yp, size(dyt),
+                                nullptr, TPMLP_FP32, dwp, N, place.stream);
+        }),
+        what);
+  return tuple_of({dx, dw, db});
+}
+
+// A tensor argument of the block: its shape and type, contiguous, or null.
+const void* block_of(const char* name, PyObject* o, at::IntArrayRef size,
+                     at::ScalarType type, const at::Device& dev) {
+  const at::Tensor* t = maybe(name, o);
+  if (t == nullptr) return nullptr;
+  if (t->sizes() != size || t->scalar_type() != type || !t->is_contiguous() ||
+      t->device() != dev) {
+    std::ostringstream s;
+    s << name << ": expected a contiguous " << size << " " << c10::toString(type)
+      << " tensor on " << dev << ", got " << shown(*t);
+    throw Refused{s.str()};
+  }
+  return t->numel() == 0 ? nullptr : t->const_data_ptr();
+}
+
+// fp4_mlp(handle, h, f, format, X, packed, b1, b2, gamma, beta, x_scale, y_scale,
+//         out, workspace or None, stream) -> (Z, workspace)
+PyObject* fp4_mlp(PyObject* const* a) {
+  auto* handle = reinterpret_cast<tp_mlp_handle*>(integer(a[0]));
+  const long long h = integer(a[1]), f = integer(a[2]);
+  const int format = static_cast<int>(integer(a[3]));
+  const at::Tensor& X = tensor("X", a[4]);
+  if (!X.is_cuda() || X.dim() != 2 || X.size(0) > INT_MAX)
+    throw Refused{"X: expected a CUDA tensor [T, " + std::to_string(h) + "], got " +
+                  shown(X)};
+  const at::Device dev = X.device();
+  const int64_t T = X.size(0);
+  const void* xp = block_of("X", a[4], {T, h}, at::kBFloat16, dev);
+  const at::Tensor& packed = tensor("packed", a[5]);
+  if (packed.device() != dev) throw Refused{"packed and X differ in device"};
+  auto vec = [&](const char* n, PyObject* o, long long size) {
+    return static_cast<const float*>(block_of(n, o, {size}, at::kFloat, dev));
+  };
+  const float *b1 = vec("b1", a[6], f), *b2 = vec("b2", a[7], h);
+  const float *gamma = vec("gamma", a[8], h), *beta = vec("beta", a[9], h);
+  const double xs = real(a[10]), ys = real(a[11]);
+  const Place place(dev, a[14]);
+  at::Tensor Z;
+  if (a[12] == Py_None) {
+    Z = make({T, h}, at::kBFloat16, dev);
+  } else {
+    block_of("Z", a[12], {T, h}, at::kBFloat16, dev);
+    Z = tensor("Z", a[12]);
+  }
+  const size_t need =
+      lib.fp4_mlp_workspace_bytes(handle, static_cast<int>(T), format);
+  at::Tensor ws;
+  if (a[13] != Py_None) ws = tensor("workspace", a[13]);
+  if (!ws.defined() || static_cast<size_t>(ws.numel()) < need ||
+      ws.device() != dev)
+    ws = make({static_cast<int64_t>(need > 256 ? need : 256)}, at::kByte, dev);
+  const void* pp = packed.const_data_ptr();
+  void* zp = T == 0 ? nullptr : Z.data_ptr();
+  void* wp = ws.data_ptr();
+  check(without_gil([&] {
+          return lib.fp4_mlp_forward(handle, static_cast<int>(T), format, xp, pp,
+                                     b1, b2, gamma, beta, xs, ys, zp, wp,
+                                     static_cast<size_t>(ws.numel()), place.stream);
+        }),
+        "tp_fp4_mlp_forward");
+  return tuple_of({Z, ws});
+}
+
 // --------------------------------------------------------------- module --
 
 // bind(check, addresses of Library's functions in its order)
@@ -676,6 +802,9 @@ PyObject* bind(PyObject* const* a) {
   l.fp4_dequantize = reinterpret_cast<decltype(l.fp4_dequantize)>(at(11));
   l.fp4_matmul = reinterpret_cast<decltype(l.fp4_matmul)>(at(12));
   l.fp4_linear = reinterpret_cast<decltype(l.fp4_linear)>(at(13));
+  l.fp4_mlp_workspace_bytes =
+      reinterpret_cast<decltype(l.fp4_mlp_workspace_bytes)>(at(14));
+  l.fp4_mlp_forward = reinterpret_cast<decltype(l.fp4_mlp_forward)>(at(15));
   Py_INCREF(a[0]);
   l.check = a[0];
   Py_XDECREF(lib.check);
@@ -715,6 +844,8 @@ PyMethodDef methods[] = {
     {"fp4_dequantize", nullptr, 0, nullptr},
     {"fp4_matmul", nullptr, 0, nullptr},
     {"fp4_linear", nullptr, 0, nullptr},
+    {"fp4_backward", nullptr, 0, nullptr},
+    {"fp4_mlp", nullptr, 0, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
@@ -733,7 +864,7 @@ void set(int i) {
 }  // namespace
 
 PyMODINIT_FUNC PyInit__pycall() {
-  set<bind, 14>(0);
+  set<bind, 16>(0);
   set<rope, 11>(1);
   set<norm_forward, 16>(2);
   set<norm_backward, 21>(3);
@@ -742,5 +873,7 @@ PyMODINIT_FUNC PyInit__pycall() {
   set<fp4_dequantize, 7>(6);
   set<fp4_matmul, 10>(7);
   set<fp4_linear, 10>(8);
+  set<fp4_backward, 9>(9);
+  set<fp4_mlp, 15>(10);
   return PyModule_Create(&module);
 }

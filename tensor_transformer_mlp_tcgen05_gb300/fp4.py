@@ -93,24 +93,28 @@ class Fp4Tensor:
             return B_.tp_fp4_check(self.buffer, stream)
 
 
-def quantize(x, format: str = "nvfp4", scale: float | None = None,
+def quantize(x, format: str = "nvfp4", scale: "float | Fp4Tensor | None" = None,
              transpose: bool = False, out: Fp4Tensor | None = None,
              stream=None) -> Fp4Tensor:
     """x [rows, cols] quantised along its rows, or with ``transpose`` along its
     columns as a packed [cols, rows].  ``scale``: nvfp4's power of two for the
-    whole matrix, by default taken from it (x is then read twice); mxfp4 has
-    none (None or 1).  ``out``: a packed matrix of that shape and format, which is
-    overwritten."""
+    whole matrix, a packed matrix whose own is taken (on the device), or by default
+    the one x needs (x is then read twice); mxfp4 has none (None or 1).  ``out``: a
+    packed matrix of that shape and format, which is overwritten."""
     code = _format(format)
-    buffer = None
+    like = buffer = None
+    if isinstance(scale, Fp4Tensor):
+        if scale.format != format:
+            raise ValueError(f"scale is in {scale.format}, not in {format}")
+        scale, like = None, scale.buffer
     if out is not None:
         shape = (x.shape[1], x.shape[0]) if transpose else tuple(x.shape)
         if out.shape != shape or out.format != format:
             raise ValueError(f"out: expected a packed {shape} in {format}, got "
                              f"{out.shape} in {out.format}")
         buffer = out.buffer
-    buffer, _ = B_.tensor_calls().fp4_quantize(x, transpose, code, _scale(scale),
-                                               buffer, False, stream)
+    buffer = B_.tensor_calls().fp4_quantize(x, transpose, code, _scale(scale),
+                                            like, buffer, stream)
     if out is not None:
         return out
     rows, cols = x.shape
@@ -164,22 +168,15 @@ class Fp4Linear:
             raise ValueError(f"expected dy [T, {self.outputs}] and x [T, "
                              f"{self.inputs}], got {tuple(dy.shape)} and "
                              f"{tuple(x.shape)}")
-        T = dy.shape[0]
         bias_grad = bias_grad and self.bias is not None
-        if T == 0:
+        if dy.shape[0] == 0:
             dx = calls.fp4_linear(dy, self.weight_rows.buffer, self.inputs,
                                   self.outputs, code, 1.0, None, _dtype(dtype),
                                   None, stream)
             dw = dy.new_zeros((self.inputs, self.outputs), dtype=torch.float32)
             db = dy.new_zeros(self.outputs, dtype=torch.float32)
             return {"dx": dx, "dw": dw, "db": db if bias_grad else None}
-        s = _scale(dy_scale)
-        dx = calls.fp4_linear(dy, self.weight_rows.buffer, self.inputs,
-                              self.outputs, code, s, None, _dtype(dtype), None,
-                              stream)
-        cols, db = calls.fp4_quantize(dy, True, code, s, None, bias_grad, stream)
-        xt, _ = calls.fp4_quantize(x, True, code, _scale(x_scale), None, False,
-                                   stream)
-        dw = calls.fp4_matmul(xt, self.inputs, cols, self.outputs, T, code, None,
-                              B_.TPMLP_FP32, None, stream)
+        dx, dw, db = calls.fp4_backward(dy, x, self.weight_rows.buffer, code,
+                                        _scale(dy_scale), _scale(x_scale),
+                                        _dtype(dtype), bias_grad, stream)
         return {"dx": dx, "dw": dw, "db": db}

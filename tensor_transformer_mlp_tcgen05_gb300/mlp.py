@@ -257,27 +257,13 @@ class TensorParallelMLP:
         """Forward on weights from pack_fp4_weights (tp_fp4_mlp_forward): X (or
         LayerNorm(X)) and Y = GeLU(H) are quantized with nvfp4's powers of two
         ``x_scale`` and ``y_scale`` (mxfp4: 1)."""
-        T = X.shape[0]
         h, f = self.hidden, self.ffn
         if not isinstance(packed, Fp4Weights) or packed.shape != (h, f):
             raise ValueError(f"packed must be the pack_fp4_weights of a block of "
                              f"{(h, f)}")
-        self._chk("X", X, (T, h), torch.bfloat16)
-        self._chk("b1", b1, (f,), torch.float32)
-        self._chk("b2", b2, (h,), torch.float32)
-        self._chk("gamma", gamma, (h,), torch.float32)
-        self._chk("beta", beta, (h,), torch.float32)
-        Z = out if out is not None else torch.empty((T, h), dtype=torch.bfloat16,
-                                                   device=X.device)
-        self._chk("Z", Z, (T, h), torch.bfloat16)
-        code = _fp4_format(packed.format)
-        need = B_.tp_fp4_mlp_workspace_bytes(self.handle, T, code)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(max(need, 256), dtype=torch.uint8,
-                                   device=self.device)
-        B_.tp_fp4_mlp_forward(self.handle, T, code, X, packed.buffer, b1, b2, gamma,
-                              beta, x_scale, y_scale, Z, self._ws,
-                              self._ws.numel(), stream)
+        Z, self._ws = B_.tensor_calls().fp4_mlp(
+            self.handle, h, f, _fp4_format(packed.format), X, packed.buffer, b1, b2,
+            gamma, beta, x_scale, y_scale, out, self._ws, stream)
         return Z
 
 

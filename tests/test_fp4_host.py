@@ -34,9 +34,9 @@ def test_sizes_and_offsets(fmt, tile):
     for rows, cols in ((1, 1), (0, 5), (128, 256), (129, 257), (7, 1000),
                        (1 << 20, 1 << 15)):
         tiles = (rows + 127) // 128 * ((cols + 255) // 256)
-        at = 256 + tiles * 16384
+        at = 4096 + tiles * 16384
         assert B.tp_fp4_bytes(rows, cols, fmt) == at + tiles * tile
-        assert B.tp_fp4_offset(rows, cols, fmt, B.TPFP4_CODES) == 256
+        assert B.tp_fp4_offset(rows, cols, fmt, B.TPFP4_CODES) == 4096
         assert B.tp_fp4_offset(rows, cols, fmt, B.TPFP4_SCALES) == at
         assert B.tp_fp4_offset(rows, cols, fmt, 2) == -1
     for rows, cols, f in ((-1, 5, fmt), (5, 0, fmt), (5, 5, 2),
@@ -48,12 +48,12 @@ def test_sizes_and_offsets(fmt, tile):
 
 
 def quantize(rows=100, cols=300, dtype=BF, x=X, stride=300, transpose=0,
-             fmt=NV, scale=1.0, packed=P, nbytes=None, colsum=None, ws=None,
-             ws_bytes=0):
+             fmt=NV, scale=1.0, like=None, packed=P, nbytes=None, colsum=None,
+             ws=None, ws_bytes=0):
     if nbytes is None:
         r, c = (cols, rows) if transpose else (rows, cols)
         nbytes = B.tp_fp4_bytes(r, c, fmt)
-    B.tp_fp4_quantize(rows, cols, dtype, x, stride, transpose, fmt, scale,
+    B.tp_fp4_quantize(rows, cols, dtype, x, stride, transpose, fmt, scale, like,
                       packed, nbytes, colsum, ws, ws_bytes, stream=0)
 
 
@@ -79,6 +79,8 @@ ARG, SHAPE, ALIGN, WS = (B.TPMLP_ERR_ARG, B.TPMLP_ERR_SHAPE, B.TPMLP_ERR_ALIGN,
     (ARG, dict(scale=float("inf"))), (ARG, dict(scale=float("nan"))),
     (ARG, dict(scale=2.0 ** 128)), (ARG, dict(scale=2.0 ** -127)),
     (ARG, dict(fmt=MX, scale=2.0)),
+    (ARG, dict(like=P2)), (ARG, dict(fmt=MX, scale=0.0, like=P2)),
+    (ALIGN, dict(scale=0.0, like=P2 + 16)), (ARG, dict(scale=0.0, like=P)),
     (ARG, dict(packed=None)), (ALIGN, dict(packed=P + 16)), (WS, dict(nbytes=100)),
     (ARG, dict(x=None)), (ALIGN, dict(x=X + 1)), (ALIGN, dict(x=X + 2, dtype=F32)),
     (ARG, dict(colsum=C, ws=W, ws_bytes=1 << 20)),

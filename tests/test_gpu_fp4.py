@@ -174,6 +174,16 @@ def test_strides_and_alignment(fmt, dtype, off, pad):
     assert (view[:, cols:] == 7).all() and (out[:off] == 7).all()
 
 
+def test_scale_of_another_matrix():
+    """g taken from a packed matrix on the device: codes as with that power of
+    two given."""
+    x, y = randn(70, 300, seed=1, scale=100.0), randn(40, 200, seed=2)
+    q = fp4.quantize(x)
+    for t in (False, True):
+        got = fp4.quantize(y, scale=q, transpose=t)
+        check_quantized(got, f64(y.t() if t else y), float(q.tensor_scale()))
+
+
 def test_column_sums():
     """The bias gradient of Fp4Linear.backward: 32 rows in order, 8 such sums, then
     256-row sums; each addition off by at most 2^-24 of the sum of magnitudes so
@@ -611,6 +621,7 @@ def test_refusals_on_tensors():
         lambda: fp4.matmul(q, q, dtype=torch.float16),
         lambda: q.dequantize(torch.float16),
         lambda: q.dequantize(out=randn(8, 63)),
+        lambda: fp4.quantize(x, scale=fp4.quantize(x, "mxfp4")),
         lambda: fp4.matmul(fp4.Fp4Tensor(q.buffer[:256], 8, 64, "nvfp4"), q),
         lambda: fp4.Fp4Linear(randn(64, 8)).forward(randn(2, 63)),
         lambda: fp4.Fp4Linear(randn(64, 8)).backward(randn(2, 8), randn(3, 64)),
