@@ -97,10 +97,38 @@ __device__ __forceinline__ bool elect_one() {
   return yes != 0;
 }
 
-// The whole warp's wait: whether it ended for every lane.
+// Arrive on a barrier of the pair's other CTA, for tensor memory that has been
+// read: no memory of this thread's is handed over, so the arrival does not wait
+// for its earlier stores (a release at cluster scope did, 1600 cycles a tile).
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   cluster_addr)
+               : "memory");
+}
+
+// The whole warp's bounded wait (see gemm::wait_bounded): whether the phase
+// completed.  The clock and the abort flag are read only after some tries.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
                                           const gemm::Ctl& c, int role) {
-  return __all_sync(0xffffffffu, gemm::wait_bounded(bar, parity, c, role));
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    if (n < 32) continue;
+    if (__any_sync(0xffffffffu, *c.abort_flag != 0)) return false;
+    const uint64_t t = ptx::globaltimer_ns();
+    if (n == 32) t0 = t;
+    if (!__any_sync(0xffffffffu, t - t0 > c.budget)) continue;
+    if ((threadIdx.x & 31) == 0) {
+      *c.abort_flag = 1;
+      if (atomicCAS(c.status, 0, TPMLP_ERR_TIMEOUT) == 0) {
+        c.status[1] = role;
+        c.status[2] = static_cast<int>(blockIdx.x);
+      }
+      __threadfence();
+    }
+    __syncwarp();
+    return false;
+  }
 }
 
 // One k-tile: its scales into tensor memory (columns t_sa and t_sb on), then

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(NUM_THREADS)
   // done: every MMA of this CTA has finished, and with them every copy that
   // they waited for; after an abort copies may be in flight, and the stages are
   // left alone.
-  bool ok = wait_bounded(done_bar, 0, ctl, ROLE_EPILOGUE);
+  bool ok = wait_warp(done_bar, 0, ctl, ROLE_EPILOGUE);
   ok = __syncthreads_and(ok && *reinterpret_cast<volatile int*>(abort_flag) == 0);
   ptx::tc_fence_after();
   if (ok) {
