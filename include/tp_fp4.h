@@ -59,9 +59,10 @@ extern "C" {
  * offsets of its parts (-1 likewise):
  *   TPFP4_CODES   two codes a byte, in tiles of 128 rows x 256 columns (16 KB),
  *                 tile (r / 128, c / 256) being number n = (r / 128)
- *                 ceil(cols / 256) + c / 256: element (r, c) at 16384 n +
- *                 (r mod 128) 128 + (c mod 256) / 2, in the low nibble for even
- *                 c; zeros past cols
+ *                 ceil(cols / 256) + c / 256: columns 32 u .. 32 u + 31 of row r
+ *                 (u of the tile) are the 16 bytes at 16384 n + (r mod 128) 128 +
+ *                 (u xor (r mod 8)) 16 (shared memory's 128-byte swizzle), two
+ *                 columns a byte, the even one in the low nibble; zeros past cols
  *   TPFP4_SCALES  one byte a block, in tiles of the same rows and columns (2048
  *                 bytes NV, 1024 MX): the scale of block b = (c mod 256) / 16
  *                 (NV) or / 32 (MX) of row r at n times that + (b / 4) 512 +
@@ -104,11 +105,11 @@ int tp_fp4_matmul(long long T, long long N, long long K, int format,
                   const float* bias, int dtype, void* C, long long ldc,
                   void* stream);
 
-/* Both in one call, for a layer y = x W: x [T, K] (x_dtype, x_stride) is quantised
- * into xq (tp_fp4_bytes(T, K, format) bytes; x_scale as tp_fp4_quantize's scale),
- * C is xq times the packed W [N, K].  The product starts to load W while x is
- * quantised, so that a few rows take less than the two calls.  xq and C share no
- * memory with the rest. */
+/* Both in one call, for a layer y = x W: x [T, K] (x_dtype, x_stride) quantised
+ * (x_scale as tp_fp4_quantize's scale) times the packed W [N, K].  xq is scratch of
+ * tp_fp4_bytes(T, K, format) bytes; its status word is the call's.  The product
+ * starts to load W while x is quantised, and up to 4 rows with a given x_scale
+ * are quantised by the product itself.  xq and C share no memory with the rest. */
 int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
                   const void* x, long long x_stride, int format, double x_scale,
                   void* xq, size_t xq_bytes, const void* W, size_t w_bytes,

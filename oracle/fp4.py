@@ -121,7 +121,11 @@ def pack(codes, byte, fmt):
     for i in range(rt):
         for j in range(kt):
             t = full[128 * i:128 * i + 128, 256 * j:256 * j + 256]
-            out[i, j] = (t[:, 0::2] | (t[:, 1::2] << 4)).reshape(-1)
+            b = t[:, 0::2] | (t[:, 1::2] << 4)
+            for r in range(128):
+                for u in range(8):
+                    at = r * 128 + (u ^ (r % 8)) * 16
+                    out[i, j, at:at + 16] = b[r, 16 * u:16 * u + 16]
     empty = 127 if fmt == "mxfp4" else 0
     scales = np.zeros((rt, kt, 128 * per), dtype=np.uint8)
     for r in range(R):

@@ -42,7 +42,7 @@ SOURCES = ["gemm_tc2.cu", "rowops.cu", "simt.cu",
            "attn_host.cu", "fp8.cu", "probe.cu",
            "qk_rows.cu", "qk_rows_bf16.cu", "qk_rows_fp32.cu", "rope_host.cu",
            "grad_clip.cu", "fp4_quant.cu", "fp4_gemm.cu", "fp4_split.cu",
-           "fp4_host.cu"]
+           "fp4_plain.cu", "fp4_host.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
           "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

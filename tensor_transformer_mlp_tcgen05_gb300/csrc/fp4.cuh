@@ -71,10 +71,16 @@ inline Packed view(const void* buffer, long long rows, long long cols) {
   return p;
 }
 
-// Where row r's codes of k-tile kt lie (128 bytes).
+// Where row r's codes of k-tile kt lie (128 bytes), and in them those of its
+// columns 32 u .. 32 u + 31: the order of shared memory's 128-byte swizzle, so that
+// an operand's rows are one plain copy away from the MMA.
 __device__ __forceinline__ size_t code_row(int r, int kt, int ktiles) {
   return (static_cast<size_t>(r / TILE_ROWS) * ktiles + kt) * CODE_TILE +
          (r % TILE_ROWS) * (TILE_COLS / 2);
+}
+
+__device__ __forceinline__ int code_unit(int r, int u) {
+  return (u ^ (r & 7)) * 16;
 }
 
 // Where the four scale bytes of row r, blocks 4q .. 4q + 3 of k-tile kt lie.
@@ -147,19 +153,24 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float inv_g) {
   return s;
 }
 
-// x / (s g) for the rounding to E2M1.  NV: x m is exact, and (x m) r + 96 - 96
-// rounds the quotient to a multiple of 2^-17: the error of 1 / s (2^-23 of
-// itself, 2^-20 of a quotient up to 8) cannot move it off a border that it is on,
-// nor onto one that it is 2^-16 or more away from, as everything else is
-// (sticky).  MX: exact.
+// x / (s g) of two elements for the rounding to E2M1.  NV: x m is exact, and
+// (x m) r + 96 - 96 rounds the quotient to a multiple of 2^-17: the error of 1 / s
+// (2^-23 of itself, 2^-20 of a quotient up to 8) cannot move it off a border that
+// it is on, nor onto one that it is 2^-16 or more away from, as everything else is
+// (sticky).  MX: exact.  (Packed arithmetic: each half is the IEEE operation.)
 template <int FORMAT, bool WIDE>
-__device__ __forceinline__ float quotient(float x, const Scale& s) {
-  if constexpr (FORMAT == TPFP4_NV) {
-    const float t = (WIDE ? __uint_as_float(sticky(__float_as_uint(x))) : x) * s.m;
-    return __fadd_rn(fmaf(t, s.r, 96.f), -96.f);
-  } else {
-    return x * s.m;
+__device__ __forceinline__ void quotient2(float x0, float x1, const Scale& s,
+                                          float& q0, float& q1) {
+  if constexpr (FORMAT == TPFP4_NV && WIDE) {
+    x0 = __uint_as_float(sticky(__float_as_uint(x0)));
+    x1 = __uint_as_float(sticky(__float_as_uint(x1)));
   }
+  uint64_t t = f2_mul(f2_pack(x0, x1), f2_pack(s.m, s.m));
+  if constexpr (FORMAT == TPFP4_NV) {
+    t = f2_fma(t, f2_pack(s.r, s.r), f2_pack(96.f, 96.f));
+    t = f2_add(t, f2_pack(-96.f, -96.f));
+  }
+  f2_unpack(t, q0, q1);
 }
 
 // Eight quotients to codes, the first in the lowest nibble (nearest even,
@@ -184,10 +195,12 @@ __device__ __forceinline__ uint2 codes16(const float* x, const Scale& s) {
   float q[8];
   uint2 w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = quotient<FORMAT, WIDE>(x[i], s);
+  for (int i = 0; i < 8; i += 2)
+    quotient2<FORMAT, WIDE>(x[i], x[i + 1], s, q[i], q[i + 1]);
   w.x = codes8(q);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = quotient<FORMAT, WIDE>(x[8 + i], s);
+  for (int i = 0; i < 8; i += 2)
+    quotient2<FORMAT, WIDE>(x[8 + i], x[9 + i], s, q[i], q[i + 1]);
   w.y = codes8(q);
   return w;
 }

@@ -185,10 +185,12 @@ __device__ __forceinline__ void store_fp4(const Packed& y, int row, int c0,
       c[b * BLOCK / 8 + 2 * i + 1] = w.y;
     }
   }
-  uint4* dst = reinterpret_cast<uint4*>(
-      y.codes + code_row(row, c0 / TILE_COLS, y.ktiles) + c0 % TILE_COLS / 2);
-  dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
-  dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
+  uint8_t* dst = y.codes + code_row(row, c0 / TILE_COLS, y.ktiles);
+  const int unit = c0 % TILE_COLS / 32;
+  *reinterpret_cast<uint4*>(dst + code_unit(row, unit)) =
+      make_uint4(c[0], c[1], c[2], c[3]);
+  *reinterpret_cast<uint4*>(dst + code_unit(row, unit + 1)) =
+      make_uint4(c[4], c[5], c[6], c[7]);
   const int block = c0 % TILE_COLS / BLOCK;
   uint8_t* to = y.scales + scale_word(row, c0 / TILE_COLS, block / 4, y.ktiles,
                                       tile_bytes(FORMAT)) + block % 4;
@@ -201,9 +203,12 @@ __device__ __forceinline__ void store_fp4(const Packed& y, int row, int c0,
 // 64 columns past the matrix in its last k-tile, which its products read.
 template <int FORMAT>
 __device__ __forceinline__ void store_nothing(const Packed& y, int row, int c0) {
-  uint4* dst = reinterpret_cast<uint4*>(
-      y.codes + code_row(row, c0 / TILE_COLS, y.ktiles) + c0 % TILE_COLS / 2);
-  dst[0] = dst[1] = make_uint4(0u, 0u, 0u, 0u);
+  uint8_t* dst = y.codes + code_row(row, c0 / TILE_COLS, y.ktiles);
+  const int unit = c0 % TILE_COLS / 32;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<uint4*>(dst + code_unit(row, unit + i)) =
+        make_uint4(0u, 0u, 0u, 0u);
   const int block = c0 % TILE_COLS / block_size(FORMAT);
   uint8_t* to = y.scales + scale_word(row, c0 / TILE_COLS, block / 4, y.ktiles,
                                       tile_bytes(FORMAT)) + block % 4;

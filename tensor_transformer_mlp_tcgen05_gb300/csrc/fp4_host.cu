@@ -109,38 +109,39 @@ int quantize(HandleCore* core, const char* name, long long rows, long long cols,
   });
 }
 
-// Scale tiles as rows of 8-byte elements.
-int scales_map(CUtensorMap* m, const fp4::Packed& p, int format) {
+// Tiles of `inner` bytes or rows of them, one below the other: `rows` rows, boxes
+// of `box`.  In 8-byte elements (a box has at most 256 a side); rows past the end
+// are filled with zeros.
+int tiles_map(CUtensorMap* m, const void* base, size_t inner, size_t rows,
+              int box) {
   EncodeTiledFn enc = get_encoder();
   if (enc == nullptr)
     return bad(TPMLP_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
-  const cuuint64_t tile = static_cast<cuuint64_t>(fp4::tile_bytes(format));
-  const cuuint64_t tiles =
-      static_cast<cuuint64_t>((p.rows + fp4::TILE_ROWS - 1) / fp4::TILE_ROWS) *
-      p.ktiles;
-  const cuuint64_t dims[2] = {tile / 8, tiles};
-  const cuuint64_t strides[1] = {tile};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(tile / 8), 1};
+  const cuuint64_t dims[2] = {inner / 8, rows};
+  const cuuint64_t strides[1] = {inner};
+  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(inner / 8),
+                               static_cast<cuuint32_t>(box)};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r =
-      enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, p.scales, dims, strides, box,
-          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<void*>(base), dims,
+          strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS
              ? TPMLP_OK
-             : bad(TPMLP_ERR_CUDA, "cuTensorMapEncodeTiled failed (fp4 scales)");
+             : bad(TPMLP_ERR_CUDA, "cuTensorMapEncodeTiled failed (fp4 tiles)");
 }
 
-// Tiles of codes one below the other, boxes of up to 128 rows of one.
+int scales_map(CUtensorMap* m, const fp4::Packed& p, int format) {
+  return tiles_map(m, p.scales, fp4::tile_bytes(format),
+                   fp4::tiles_of(p.rows, p.cols), 1);
+}
+
 int codes_map(CUtensorMap* m, const fp4::Packed& p, int box_rows) {
-  const uint64_t rows =
-      static_cast<uint64_t>((p.rows + fp4::TILE_ROWS - 1) / fp4::TILE_ROWS) *
-      p.ktiles * fp4::TILE_ROWS;
-  return encode_map_u8(m, p.codes, 128, rows, 128,
-                       static_cast<uint32_t>(box_rows));
+  return tiles_map(m, p.codes, fp4::TILE_COLS / 2,
+                   fp4::tiles_of(p.rows, p.cols) * fp4::TILE_ROWS, box_rows);
 }
 
-// Whether a product goes to the kernel that splits K.
 // Times in us (graph replays of one product in L2, NV), split against pairs:
 // 1 to 64 rows of A, 1024 to 20480 rows of B, K 1024 to 20480: 4.0 to 12.5 against
 // 5.4 to 23 (equal at 64 rows and K = 1024).  More rows: split pays where the
@@ -155,22 +156,48 @@ bool few(const fp4::ProductArgs& a) {
 
 int product(HandleCore* core, const char* name, int format,
             const fp4::ProductArgs& a, int sms, cudaStream_t s) {
+  auto step = [&](auto&& f) {
+    return core != nullptr ? run(core, name, s, f) : launched(name, f());
+  };
+  if (a.x != nullptr || few(a))
+    return step([&] { return fp4::launch_product_split(format, a, sms, s); });
   CUtensorMap ta, tsa, tb, tsb, to;
-  const bool split = few(a);
-  TRY(codes_map(&ta, a.a, split ? fp4::split_tokens(a.M) : 128));
-  TRY(codes_map(&tb, a.b, split ? 128 : 64));
+  TRY(codes_map(&ta, a.a, 128));
+  TRY(codes_map(&tb, a.b, 64));
   TRY(scales_map(&tsa, a.a, format));
   TRY(scales_map(&tsb, a.b, format));
   const size_t es = a.epilogue == fp4::OUT_FP32 ? 4 : 2;
-  const bool tma = !split && a.epilogue != fp4::OUT_GELU_FP4 &&
-                   aligned16(a.out) && a.ldo * es % 16 == 0;
+  const bool tma = a.epilogue != fp4::OUT_GELU_FP4 && aligned16(a.out) &&
+                   a.ldo * es % 16 == 0;
   if (tma) TRY(out_map(&to, a.out, es == 4, a.M, a.N, a.ldo));
-  auto launch = [&] {
-    return split ? fp4::launch_product_split(format, ta, tsa, tb, tsb, a, sms, s)
-                 : fp4::launch_product_pairs(format, ta, tsa, tb, tsb,
-                                             tma ? &to : nullptr, a, sms / 2, s);
-  };
-  return core != nullptr ? run(core, name, s, launch) : launched(name, launch());
+  return step([&] {
+    return fp4::launch_product_pairs(format, ta, tsa, tb, tsb, tma ? &to : nullptr,
+                                     a, sms / 2, s);
+  });
+}
+
+// x [rows, cols] as the left operand of a product: quantised first, or by the
+// product itself where that is a product of very few rows with a given g.  One
+// launch instead of two: one token of 1024 x 4096 takes 4.4 us on the GPU instead
+// of 5.0, and 4.9 us of the host instead of 7.9; 8 rows took 9.8 instead of 9.0 (a
+// block of 1024 x 4096).  `xq` keeps the quantised rows and the status word.
+int left_operand(HandleCore* core, const char* name, long long rows,
+                 long long cols, bool bf16, const void* x, long long stride,
+                 int format, int exponent, void* xq, fp4::ProductArgs* a,
+                 cudaStream_t s) {
+  a->a = fp4::view(xq, rows, cols);
+  a->status = a->a.head->status;
+  if (rows <= fp4::PLAIN_ROWS && exponent != AUTO_SCALE) {
+    a->x = x;
+    a->x_bf16 = bf16 ? 1 : 0;
+    a->x_stride = stride;
+    a->x_exponent = exponent;
+    a->dependent = 0;
+    return TPMLP_OK;
+  }
+  a->dependent = 1;
+  return quantize(core, name, rows, cols, bf16, x, stride, false, format, exponent,
+                  nullptr, xq, nullptr, s);
 }
 
 // tp_fp4_quantize's arguments.
@@ -254,12 +281,11 @@ int check_matmul(long long T, long long N, long long K, int format, const void* 
   return TPMLP_OK;
 }
 
-// A product with checked arguments.
-int matmul(long long T, long long N, long long K, int format, const void* A,
-           const void* B, const float* bias, int dtype, void* C, long long ldc,
-           int dependent, int sms, cudaStream_t s) {
+// A product's fields but its left operand's, arguments checked.
+fp4::ProductArgs matmul_args(long long T, long long N, long long K, const void* B,
+                             const float* bias, int dtype, void* C,
+                             long long ldc) {
   fp4::ProductArgs a = {};
-  a.a = fp4::view(A, T, K);
   a.b = fp4::view(B, N, K);
   a.M = static_cast<int>(T);
   a.N = static_cast<int>(N);
@@ -267,10 +293,8 @@ int matmul(long long T, long long N, long long K, int format, const void* A,
   a.out = C;
   a.ldo = ldc;
   a.bias = bias;
-  a.status = a.a.head->status;
   a.budget_ns = HandleCore().budget_ns;
-  a.dependent = dependent;
-  return product(nullptr, "fp4_matmul", format, a, sms, s);
+  return a;
 }
 
 // ----------------------------------------------------------- MLP block --
@@ -392,8 +416,11 @@ int tp_fp4_matmul(long long T, long long N, long long K, int format,
   if (T == 0) return TPMLP_OK;
   int sms = 0;
   TRY(check_device(&sms));
-  return matmul(T, N, K, format, A, B, bias, dtype, C, ldc, 0, sms,
-                static_cast<cudaStream_t>(stream));
+  fp4::ProductArgs a = matmul_args(T, N, K, B, bias, dtype, C, ldc);
+  a.a = fp4::view(A, T, K);
+  a.status = a.a.head->status;
+  return product(nullptr, "fp4_matmul", format, a, sms,
+                 static_cast<cudaStream_t>(stream));
 }
 
 int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
@@ -415,9 +442,10 @@ int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
   int sms = 0;
   TRY(check_device(&sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  TRY(quantize(nullptr, "fp4_quantize", T, K, x_dtype == TPMLP_BF16, x, x_stride,
-               false, format, exponent, nullptr, xq, nullptr, s));
-  return matmul(T, N, K, format, xq, W, bias, dtype, C, ldc, 1, sms, s);
+  fp4::ProductArgs a = matmul_args(T, N, K, W, bias, dtype, C, ldc);
+  TRY(left_operand(nullptr, "fp4_quantize", T, K, x_dtype == TPMLP_BF16, x,
+                   x_stride, format, exponent, xq, &a, s));
+  return product(nullptr, "fp4_matmul", format, a, sms, s);
 }
 
 int tp_fp4_check(void* packed, void* stream) {
@@ -504,10 +532,9 @@ int tp_fp4_mlp_forward(tp_mlp_handle* H, int tokens, int format, const void* X,
     }));
     Xop = ws + L.xn;
   }
-  TRY(quantize(&H->core, "fp4_quantize_x", tokens, h, true, Xop, h, false, format,
-               xe, nullptr, ws + L.xq, nullptr, s));
   fp4::ProductArgs a = {};
-  a.a = fp4::view(ws + L.xq, tokens, h);
+  TRY(left_operand(&H->core, "fp4_quantize_x", tokens, h, true, Xop, h, format, xe,
+                   ws + L.xq, &a, s));
   a.b = fp4::view(pk + P.a, f, h);
   a.M = tokens;
   a.N = f;
@@ -516,11 +543,11 @@ int tp_fp4_mlp_forward(tp_mlp_handle* H, int tokens, int format, const void* X,
   a.y = fp4::view(ws + L.yq, tokens, f);
   a.y_exponent = ye;
   a.gelu_mode = c.gelu_mode;
-  a.status = a.a.head->status;
   a.budget_ns = H->core.budget_ns;
-  a.dependent = 1;   // of the quantisation, and the second product of the first
   TRY(product(&H->core, "gemm1_gelu_fp4", format, a, sms, s));
   a.a = a.y;
+  a.x = nullptr;
+  a.dependent = 1;
   a.b = fp4::view(pk + P.b, h, f);
   a.N = h;
   a.epilogue = fp4::OUT_BF16;

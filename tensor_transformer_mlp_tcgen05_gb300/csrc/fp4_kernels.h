@@ -48,6 +48,13 @@ enum Epilogue4 : int {
 struct ProductArgs {
   Packed a, b;          // [M, K], [N, K]
   int M, N;
+  // instead of a's codes, scales and g: the plain matrix x that the product
+  // quantises itself, g = 2^x_exponent (M <= PLAIN_ROWS; a then has its sizes, and
+  // the status word is cleared by the product); or null
+  const void* x;
+  int x_bf16;
+  long long x_stride;
+  int x_exponent;
   int epilogue;
   void* out;            // [M, N], row stride ldo (OUT_BF16, OUT_FP32)
   long long ldo;
@@ -73,12 +80,12 @@ cudaError_t launch_product_pairs(int format, const CUtensorMap& ta,
                                  cudaStream_t s);
 
 // Tiles of 128 rows of B x up to 128 rows of A, K split over a cluster, for few
-// rows of A.  ta: boxes of split_tokens(M) rows, tb: of 128.
-int split_tokens(int M);   // rows of A in a tile
-cudaError_t launch_product_split(int format, const CUtensorMap& ta,
-                                 const CUtensorMap& tsa, const CUtensorMap& tb,
-                                 const CUtensorMap& tsb, const ProductArgs& args,
-                                 int sms, cudaStream_t s);
+// rows of A.
+constexpr int PLAIN_ROWS = 4;
+cudaError_t launch_product_split(int format, const ProductArgs& args, int sms,
+                                 cudaStream_t s);
+cudaError_t launch_product_plain(int format, const ProductArgs& args, int sms,
+                                 cudaStream_t s);
 
 }  // namespace fp4
 }  // namespace tpmlp

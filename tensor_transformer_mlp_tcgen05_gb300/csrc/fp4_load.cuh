@@ -1,0 +1,93 @@
+// Sixteen elements of a plain matrix's row, as the quantising kernels load them.
+#pragma once
+#include "fp4.cuh"
+
+namespace tpmlp {
+namespace fp4 {
+
+template <class T>
+struct Raw;   // 16 elements as loaded
+template <>
+struct Raw<__nv_bfloat16> {
+  uint32_t w[8];
+  // bits of the largest |x| as fp32: magnitudes compare as whole numbers
+  __device__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    return max(m << 16, m & 0xffff0000u);
+  }
+  __device__ void floats(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {   // bf16 is the upper half of fp32
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw<float> {
+  uint32_t w[16];
+  __device__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7fffffffu);
+    return m;
+  }
+  __device__ void floats(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+  }
+};
+
+// LD: bytes of a load (32 and 16: every 16-element unit starts on such a
+// boundary), or 0 for loads of single elements.
+template <int LD, int WORDS>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[WORDS]) {
+  if constexpr (LD == 32) {
+#pragma unroll
+    for (int i = 0; i < WORDS / 8; ++i)
+      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[8 * i]), "=r"(w[8 * i + 1]), "=r"(w[8 * i + 2]),
+                     "=r"(w[8 * i + 3]), "=r"(w[8 * i + 4]), "=r"(w[8 * i + 5]),
+                     "=r"(w[8 * i + 6]), "=r"(w[8 * i + 7])
+                   : "l"(static_cast<const char*>(p) + 32 * i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS / 4; ++i) {
+      const uint4 u = __ldg(static_cast<const uint4*>(p) + i);
+      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t element_bits(const __nv_bfloat16* p) {
+  return static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p)))
+         << 16;
+}
+__device__ __forceinline__ uint32_t element_bits(const float* p) {
+  return __ldg(reinterpret_cast<const unsigned int*>(p));
+}
+
+// 16 elements from p, the first n of them in the row (n may be negative: none).
+template <class T, int LD>
+__device__ __forceinline__ void load16(const T* p, int n, Raw<T>& r) {
+  constexpr int WORDS = sizeof(r.w) / 4;
+  if (LD != 0 && n >= 16) {
+    load_words<LD == 0 ? 16 : LD, WORDS>(p, r.w);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      r.w[i] = i < n ? element_bits(p + i) : 0u;
+    } else {
+      const uint32_t lo = 2 * i < n ? element_bits(p + 2 * i) >> 16 : 0u;
+      const uint32_t hi = 2 * i + 1 < n ? element_bits(p + 2 * i + 1) : 0u;
+      r.w[i] = lo | hi;
+    }
+  }
+}
+
+}  // namespace fp4
+}  // namespace tpmlp

@@ -7,83 +7,13 @@
 //   amax        the largest finite |x| of a matrix whose g is its own
 //   dequantise  the values, as bf16 or fp32
 #include "fp4_kernels.h"
+#include "fp4_load.cuh"
 
 namespace tpmlp {
 namespace fp4 {
 namespace {
 
 constexpr int THREADS = 256;
-
-template <class T>
-struct Raw;   // 16 elements as loaded
-template <>
-struct Raw<__nv_bfloat16> {
-  uint32_t w[8];
-  __device__ void floats(float (&v)[16]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {   // bf16 is the upper half of fp32
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-};
-template <>
-struct Raw<float> {
-  uint32_t w[16];
-  __device__ void floats(float (&v)[16]) const {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
-  }
-};
-
-// LD: bytes of a load (32 and 16: every 16-element unit starts on such a
-// boundary), or 0 for loads of single elements.
-template <int LD, int WORDS>
-__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[WORDS]) {
-  if constexpr (LD == 32) {
-#pragma unroll
-    for (int i = 0; i < WORDS / 8; ++i)
-      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=r"(w[8 * i]), "=r"(w[8 * i + 1]), "=r"(w[8 * i + 2]),
-                     "=r"(w[8 * i + 3]), "=r"(w[8 * i + 4]), "=r"(w[8 * i + 5]),
-                     "=r"(w[8 * i + 6]), "=r"(w[8 * i + 7])
-                   : "l"(static_cast<const char*>(p) + 32 * i));
-  } else {
-#pragma unroll
-    for (int i = 0; i < WORDS / 4; ++i) {
-      const uint4 u = __ldg(static_cast<const uint4*>(p) + i);
-      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-    }
-  }
-}
-
-__device__ __forceinline__ uint32_t element_bits(const __nv_bfloat16* p) {
-  return static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p)))
-         << 16;
-}
-__device__ __forceinline__ uint32_t element_bits(const float* p) {
-  return __ldg(reinterpret_cast<const unsigned int*>(p));
-}
-
-// 16 elements from p, the first n of them in the row (n may be negative: none).
-template <class T, int LD>
-__device__ __forceinline__ void load16(const T* p, int n, Raw<T>& r) {
-  constexpr int WORDS = sizeof(r.w) / 4;
-  if (LD != 0 && n >= 16) {
-    load_words<LD == 0 ? 16 : LD, WORDS>(p, r.w);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < WORDS; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      r.w[i] = i < n ? element_bits(p + i) : 0u;
-    } else {
-      const uint32_t lo = 2 * i < n ? element_bits(p + 2 * i) >> 16 : 0u;
-      const uint32_t hi = 2 * i + 1 < n ? element_bits(p + 2 * i + 1) : 0u;
-      r.w[i] = lo | hi;
-    }
-  }
-}
 
 // 1 / g (all threads); block 0 writes the header.
 __device__ __forceinline__ float inverse_g(const Packed& p, const Gain& gain) {
@@ -140,9 +70,7 @@ __global__ void __launch_bounds__(THREADS)
     const int row = row0 + 16 * i;
     float v[16];
     raw[i].floats(v);
-    uint32_t amax = 0;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) amax = max(amax, abs_bits(v[k]));
+    uint32_t amax = raw[i].amax();
     if constexpr (FORMAT == TPFP4_MX)
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     const Scale s = block_scale<FORMAT>(amax, inv_g);
@@ -159,8 +87,8 @@ __global__ void __launch_bounds__(THREADS)
       word |= __shfl_xor_sync(0xffffffffu, word, 4);
     }
     if (row < p.rows) {
-      *reinterpret_cast<uint2*>(p.codes + code_row(row, kt, p.ktiles) + unit * 8) =
-          c;
+      *reinterpret_cast<uint2*>(p.codes + code_row(row, kt, p.ktiles) +
+                                code_unit(row, unit / 2) + unit % 2 * 8) = c;
       constexpr int THREADS_A_WORD = FORMAT == TPFP4_NV ? 4 : 8;
       if (unit % THREADS_A_WORD == 0)
         *reinterpret_cast<uint32_t*>(
@@ -178,6 +106,14 @@ struct Two;
 template <>
 struct Two<__nv_bfloat16> {
   uint32_t w;
+  // bits of the largest |a| and |b| of 16
+  static __device__ void amax(const Two* t, uint32_t& a, uint32_t& b) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = __vmaxu2(m, t[i].w & 0x7fff7fffu);
+    a = m << 16;
+    b = m & 0xffff0000u;
+  }
   __device__ float a() const { return __uint_as_float(w << 16); }
   __device__ float b() const { return __uint_as_float(w & 0xffff0000u); }
   __device__ void load(const __nv_bfloat16* p) {
@@ -191,6 +127,14 @@ struct Two<__nv_bfloat16> {
 template <>
 struct Two<float> {
   float2 w;
+  static __device__ void amax(const Two* t, uint32_t& a, uint32_t& b) {
+    a = b = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      a = max(a, abs_bits(t[i].w.x));
+      b = max(b, abs_bits(t[i].w.y));
+    }
+  }
   __device__ float a() const { return w.x; }
   __device__ float b() const { return w.y; }
   __device__ void load(const float* p) {
@@ -208,8 +152,10 @@ constexpr int T_COLS = 64;   // columns of x a block takes
 // warp 32 of those rows, a lane two columns: its 32 elements of a column are
 // two blocks of NV or one of MX.  Codes and scales go through shared memory,
 // so that a packed row's 128 bytes of codes are written together.
+// (three blocks an SM for bf16, 85 registers: 57 -> 47 us for 5120 x 20480; four
+// spill)
 template <class T, int FORMAT, bool PAIR>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 3 : 2)
     columns_kernel(const T* __restrict__ x, long long stride, int x_rows,
                    const Packed p, const Gain gain, float* __restrict__ part) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -235,15 +181,16 @@ __global__ void __launch_bounds__(THREADS, 2)
       raw[i].load(src + i * stride, k0 + i < x_rows ? p.rows - n : 0);
   }
   const float inv_g = inverse_g(p, gain);
+  uint32_t tops[2][2];   // [column][16 rows]
+  Two<T>::amax(raw, tops[0][0], tops[1][0]);
+  Two<T>::amax(raw + 16, tops[0][1], tops[1][1]);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int r = 2 * lane + j;
+    const uint32_t* top = tops[j];
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = j == 0 ? raw[i].a() : raw[i].b();
-    uint32_t top[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 32; ++i) top[i / 16] = max(top[i / 16], abs_bits(v[i]));
     uint2 c0, c1;
     if constexpr (FORMAT == TPFP4_NV) {
       const Scale a = block_scale<FORMAT>(top[0], inv_g);
@@ -272,7 +219,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int at = i * THREADS + threadIdx.x;
     const int r = at >> 3, u = at & 7;
     if (n0 + r < p.rows)
-      *reinterpret_cast<uint4*>(p.codes + code_row(n0 + r, kt, p.ktiles) + u * 16) =
+      *reinterpret_cast<uint4*>(p.codes + code_row(n0 + r, kt, p.ktiles) +
+                                code_unit(n0 + r, u)) =
           s_codes[r * 8 + (u ^ ((r >> 1) & 7))];
   }
   constexpr int WORDS = TILE_COLS / block_size(FORMAT) / 4;
@@ -322,10 +270,15 @@ __global__ void __launch_bounds__(THREADS)
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float v[16];
-      raw[i].floats(v);
+      const uint32_t m = raw[i].amax();
+      if (m < 0x7f800000u) {
+        top = max(top, m);
+      } else {   // infinities or NaNs among them: the others
+        float v[16];
+        raw[i].floats(v);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) top = max(top, finite(abs_bits(v[k])));
+        for (int k = 0; k < 16; ++k) top = max(top, finite(abs_bits(v[k])));
+      }
     }
   }
   top = __reduce_max_sync(0xffffffffu, top);
@@ -412,7 +365,8 @@ __global__ void __launch_bounds__(THREADS)
   for (int i = 0; i < PASSES; ++i) {
     const int row = inside ? row0 + 16 * i : min(row0 + 16 * i, p.rows - 1);
     c[i] = __ldg(reinterpret_cast<const uint2*>(
-        p.codes + code_row(row, kt, p.ktiles) + unit * 8));
+        p.codes + code_row(row, kt, p.ktiles) + code_unit(row, unit / 2) +
+        unit % 2 * 8));
     byte[i] = __ldg(p.scales + scale_word(row, kt, b / 4, p.ktiles,
                                           tile_bytes(FORMAT)) + b % 4);
   }

@@ -65,11 +65,15 @@ class Fp4Tensor:
 
     def codes(self) -> torch.Tensor:
         """[rows, 128 ceil(cols / 256)] bytes of two codes, gathered out of their
-        tiles."""
+        tiles and units."""
         rt, kt = (self.rows + 127) // 128, (self.cols + 255) // 256
         at = B_.tp_fp4_offset(self.rows, self.cols, self._code, B_.TPFP4_CODES)
-        t = self.buffer[at:at + rt * kt * 16384].view(rt, kt, 128, 128)
-        return t.permute(0, 2, 1, 3).reshape(rt * 128, kt * 128)[:self.rows]
+        t = self.buffer[at:at + rt * kt * 16384].view(rt, kt, 16, 8, 8, 16)
+        r = torch.arange(8, device=t.device)
+        # [row tile, k tile, row / 8, row % 8, unit, byte]
+        t = t[:, :, :, r[:, None], r[None, :] ^ r[:, None]]
+        t = t.permute(0, 2, 3, 1, 4, 5)
+        return t.reshape(rt * 128, kt * 128)[:self.rows]
 
     def scales(self) -> torch.Tensor:
         """The scale bytes [rows, blocks], gathered out of their tiles."""

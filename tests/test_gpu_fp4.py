@@ -349,7 +349,8 @@ def test_poisoned_buffers():
 # ---------------------------------------------------------- linear layer --
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("T,K,N", [(1, 128, 96), (40, 300, 200), (777, 1024, 1000)])
+@pytest.mark.parametrize("T,K,N", [(1, 128, 96), (16, 1000, 130), (9, 2055, 640),
+                                   (3, 5, 4), (40, 300, 200), (777, 1024, 1000)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_linear_layer_and_its_gradients(fmt, T, K, N, dtype):
     W = randn(K, N, seed=1, dtype=dtype, scale=K ** -0.5)
@@ -404,6 +405,50 @@ def test_gradients_by_differences():
             assert loss(x, W2) - base == float(g["dw"][k, n] * (W2 - W)[k, n])
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_few_rows_quantised_by_the_product(fmt, dtype):
+    """1 to 6 rows, strided and unaligned, with borders, zeros and values that are
+    not finite: the same bits as the two steps one by one."""
+    N, K = 200, 1100
+    lin = fp4.Fp4Linear(randn(K, N, seed=1, scale=K ** -0.5), randn(N, dtype=F32),
+                        format=fmt)
+    one = 1.0 if fmt == "nvfp4" else None
+    for T in range(1, 7):
+        for off, pad in ((0, 0), (0, 4), (3, 1)):
+            buf = randn(T * (K + pad) + off, seed=T, dtype=dtype)
+            x = buf[off:].view(T, K + pad)[:, :K]
+            x[0, :64] = 0
+            x[-1, 64:80] = torch.arange(16, device="cuda") * 0.25
+            x[T // 2, 500] = (math.inf, math.nan, 1e30)[T % 3]
+            want = fp4.matmul(fp4.quantize(x, fmt, scale=one), lin.weight, lin.bias)
+            assert torch.equal(lin.forward(x).nan_to_num(7.0), want.nan_to_num(7.0))
+            got = lin.forward(x, dtype=F32)
+            want = fp4.matmul(fp4.quantize(x, fmt, scale=one), lin.weight, lin.bias,
+                              dtype=F32)
+            assert torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_few_rows_over_a_long_ring(fmt, dtype):
+    """More k-tiles a CTA than twice the stages (N of 130 x 128: K is not split),
+    rows quantised by the product and before it."""
+    N, K = 130 * 128, 5200
+    lin = fp4.Fp4Linear(randn(K, N, seed=1, scale=K ** -0.5), format=fmt)
+    one = 1.0 if fmt == "nvfp4" else None
+    for T in (1, 3, 4, 16):
+        x = randn(T, K, seed=T, dtype=dtype)
+        q = fp4.quantize(x, fmt, scale=one)
+        want = fp4.matmul(q, lin.weight, dtype=F32)
+        for _ in range(5):
+            assert torch.equal(lin.forward(x, dtype=F32), want)
+        some = slice(5000, 5100)
+        w = fp4.quantize(randn(K, N, seed=1, scale=K ** -0.5)[:, some].t().contiguous(),
+                         fmt, scale=lin.weight if fmt == "nvfp4" else None)
+        close_product(want[:, some], f64(q.dequantize(F32)), f64(w.dequantize(F32)))
+
+
 def test_no_tokens():
     lin = fp4.Fp4Linear(randn(64, 48), randn(48, dtype=F32))
     x = randn(0, 64)
@@ -440,7 +485,9 @@ def check_block(m, Z, X, Xn, A, Bw, b1, b2, fmt, gelu="erf", residual=False):
     f = A.shape[1]
     one = 1.0 if fmt == "nvfp4" else None
     code = fp4._FORMATS[fmt]
-    xq = fp4.Fp4Tensor(m._ws, T, h, fmt)
+    # (up to 4 rows are quantised inside the product)
+    xq = (fp4.quantize(Xn, fmt, scale=one) if T <= 4
+          else fp4.Fp4Tensor(m._ws, T, h, fmt))
     yq = fp4.Fp4Tensor(m._ws[up(B.tp_fp4_bytes(T, h, code)):], T, f, fmt)
     check_quantized(xq, f64(Xn), one)
     H = f64(xq.dequantize(F32)) @ O.quantized(f64(A).T, fmt).T
@@ -462,7 +509,7 @@ def check_block(m, Z, X, Xn, A, Bw, b1, b2, fmt, gelu="erf", residual=False):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,h,f,t", [(1, 64, 64, 1), (8, 128, 512, 2),
-                                     (33, 192, 320, 1), (130, 256, 1088, 1),
+                                     (4, 256, 1088, 1), (33, 192, 320, 1), (130, 256, 1088, 1),
                                      (300, 320, 640, 2), (700, 512, 2048, 4),
                                      (2500, 256, 4160, 1)])
 @pytest.mark.parametrize("gelu", ["erf", "tanh"])

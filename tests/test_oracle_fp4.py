@@ -133,9 +133,11 @@ def test_packed_layout_by_hand():
     codes[129, 3], codes[129, 4] = 5, 9
     byte[129, 16], byte[37, 6] = 77, 33
     c, s = O.pack(codes, byte, "nvfp4")
-    # row 129: row 1 of the second row tile, whose first k-tile is number 2
+    # row 129: row 1 of the second row tile, whose first k-tile is number 2; its
+    # unit 0 (columns 0 - 31) is the second 16 bytes
     assert c.size == 4 * 16384
-    assert c[2 * 16384 + 128 + 1] == 0x50 and c[2 * 16384 + 128 + 2] == 0x09
+    at = 2 * 16384 + 128 + 16
+    assert c[at + 1] == 0x50 and c[at + 2] == 0x09
     assert np.count_nonzero(c) == 2
     assert s.size == 2 * 2 * 2048
     # row 129: second row tile, row 1 of it; block 16: second k-tile, block 0
