@@ -117,6 +117,16 @@ __device__ __forceinline__ float exp2_of(int e) {   // e from -149 to 127
                    : __uint_as_float(1u << (e + 149));
 }
 
+// g_A g_B as factors (x, y): the product and 1, or where fp32 does not hold it,
+// halves of its exponent: a sum times the one, then the other leaves fp32's range
+// only where the result does.
+__device__ __forceinline__ float2 gain_factors(float ga, float gb) {
+  const int e = static_cast<int>(__float_as_uint(ga) >> 23) +
+                static_cast<int>(__float_as_uint(gb) >> 23) - 254;
+  const int h = e < -126 || e > 127 ? e >> 1 : e;
+  return make_float2(exp2_of(h), exp2_of(e - h));
+}
+
 // A block's scale byte, and what its elements are multiplied by: m (a power of
 // two, exact) and then r = 1 / s rounded.  `amax`: bits of the largest |x|.
 struct Scale {

@@ -107,17 +107,16 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
 }
 
 // The whole warp's bounded wait (see gemm::wait_bounded): whether the phase
-// completed.  The clock and the abort flag are read only after some tries.
+// completed.  (A try suspends for 10 to 20 us, so that budgets below that are
+// those; spinning on test_wait instead: 8192 x 5120 x 20480 250 us, not 241.)
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
                                           const gemm::Ctl& c, int role) {
-  uint64_t t0 = 0;
-  for (uint32_t n = 0;; ++n) {
+  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (true) {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
-    if (n < 32) continue;
     if (__any_sync(0xffffffffu, *c.abort_flag != 0)) return false;
-    const uint64_t t = ptx::globaltimer_ns();
-    if (n == 32) t0 = t;
-    if (!__any_sync(0xffffffffu, t - t0 > c.budget)) continue;
+    if (!__any_sync(0xffffffffu, ptx::globaltimer_ns() - t0 > c.budget)) continue;
     if ((threadIdx.x & 31) == 0) {
       *c.abort_flag = 1;
       if (atomicCAS(c.status, 0, TPMLP_ERR_TIMEOUT) == 0) {

@@ -513,6 +513,17 @@ int tp_fp4_mlp_forward(tp_mlp_handle* H, int tokens, int format, const void* X,
     return bad(TPMLP_ERR_ALIGN, "fp4: packed and workspace: 256-byte alignment");
   const MlpLayout L = mlp_layout(c, tokens, format);
   if (workspace_bytes < L.total) return TPMLP_ERR_WORKSPACE;
+  const MlpPack P = mlp_pack(c, format);
+  const size_t nx = static_cast<size_t>(tokens) * c.hidden * 2;
+  const size_t nh = static_cast<size_t>(c.hidden) * 4;
+  const struct { const void* p; size_t n; } inputs[] = {
+      {X, nx}, {packed, P.total}, {bias1, static_cast<size_t>(c.ffn) * 4},
+      {bias2, nh}, {ln_gamma, nh}, {ln_beta, nh}};
+  for (const auto& in : inputs)
+    if (overlap(Z, nx, in.p, in.n) || overlap(workspace, L.total, in.p, in.n))
+      return bad(TPMLP_ERR_ARG, "fp4: Z or workspace overlaps an input");
+  if (overlap(Z, nx, workspace, L.total))
+    return bad(TPMLP_ERR_ARG, "fp4: Z overlaps the workspace");
   int sms = 0;
   TRY(check_device(&sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -520,7 +531,6 @@ int tp_fp4_mlp_forward(tp_mlp_handle* H, int tokens, int format, const void* X,
   const char* pk = static_cast<const char*>(packed);
   if (tokens == 0)
     return launched("cudaMemsetAsync(status)", cudaMemsetAsync(ws, 0, 16, s));
-  const MlpPack P = mlp_pack(c, format);
   const int h = c.hidden, f = c.ffn;
   const void* Xop = X;
   if (c.use_layernorm) {

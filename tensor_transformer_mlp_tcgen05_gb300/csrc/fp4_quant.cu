@@ -15,7 +15,12 @@ namespace {
 
 constexpr int THREADS = 256;
 
-// 1 / g (all threads); block 0 writes the header.
+// Block 0 clears the status word, before a product may start that writes to it.
+__device__ __forceinline__ void clear_status(const Packed& p) {
+  if (blockIdx.x == 0 && threadIdx.x < 4) p.head->status[threadIdx.x] = 0;
+}
+
+// 1 / g (all threads); block 0 writes g.
 __device__ __forceinline__ float inverse_g(const Packed& p, const Gain& gain) {
   int e = gain.exponent;
   if (gain.slots > 0) {
@@ -27,11 +32,7 @@ __device__ __forceinline__ float inverse_g(const Packed& p, const Gain& gain) {
   } else if (gain.like != nullptr) {   // a power of two
     e = static_cast<int>(__float_as_uint(gain.like->g) >> 23) - 127;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    p.head->g = exp2_of(e);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p.head->status[i] = 0;
-  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.head->g = exp2_of(e);
   return exp2_of(-e);
 }
 
@@ -43,6 +44,7 @@ template <class T, int FORMAT, int LD, int PASSES>
 __global__ void __launch_bounds__(THREADS)
     rows_kernel(const T* __restrict__ x, long long stride, const Packed p,
                 const Gain gain) {
+  clear_status(p);
   // (a product that is launched as this one's dependent starts loading weights)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -158,6 +160,7 @@ template <class T, int FORMAT, bool PAIR>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 3 : 2)
     columns_kernel(const T* __restrict__ x, long long stride, int x_rows,
                    const Packed p, const Gain gain, float* __restrict__ part) {
+  clear_status(p);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // 16-byte unit u of row n at unit u ^ (n / 2 mod 8): the lanes of a warp,
   // two rows apart, write to different banks

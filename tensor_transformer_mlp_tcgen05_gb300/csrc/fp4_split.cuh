@@ -380,13 +380,10 @@ __global__ void __launch_bounds__(threads_of(SRC), 2)
     ptx::tmem_dealloc(tmem_base, S::T_COLS);
   }
   // --------------------------------------------------- sums, epilogue --
-  float g = args.b.head->g;
-  if (SRC == PACKED) {
-    wait_for_launch_before();
-    g *= args.a.head->g;
-  } else {
-    g *= exp2_of(args.x_exponent);
-  }
+  if (SRC == PACKED) wait_for_launch_before();
+  const float2 g =
+      gain_factors(SRC == PACKED ? args.a.head->g : exp2_of(args.x_exponent),
+                   args.b.head->g);
   float inv_gy = 1.f;
   if constexpr (EPI == OUT_GELU_FP4) {
     inv_gy = exp2_of(-args.y_exponent);
@@ -407,7 +404,7 @@ __global__ void __launch_bounds__(threads_of(SRC), 2)
     for (int c = 1; c < MAX_SPLIT; ++c)
       if (c < split) v[0] += p[c].x, v[1] += p[c].y, v[2] += p[c].z, v[3] += p[c].w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] *= g;
+    for (int i = 0; i < 4; ++i) v[i] = v[i] * g.x * g.y;
     finish<FORMAT, EPI>(args, t0 + t, n0, lane, inv_gy, v);
   }
   ptx::cluster_sync();   // no CTA leaves while its sums are being read

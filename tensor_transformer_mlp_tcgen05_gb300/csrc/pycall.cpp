@@ -734,7 +734,7 @@ const void* block_of(const char* name, PyObject* o, at::IntArrayRef size,
 }
 
 // fp4_mlp(handle, h, f, format, X, packed, b1, b2, gamma, beta, x_scale, y_scale,
-//         out, workspace or None, stream) -> (Z, workspace)
+//         out, stream) -> (Z, workspace, of this call alone)
 PyObject* fp4_mlp(PyObject* const* a) {
   auto* handle = reinterpret_cast<tp_mlp_handle*>(integer(a[0]));
   const long long h = integer(a[1]), f = integer(a[2]);
@@ -754,7 +754,7 @@ PyObject* fp4_mlp(PyObject* const* a) {
   const float *b1 = vec("b1", a[6], f), *b2 = vec("b2", a[7], h);
   const float *gamma = vec("gamma", a[8], h), *beta = vec("beta", a[9], h);
   const double xs = real(a[10]), ys = real(a[11]);
-  const Place place(dev, a[14]);
+  const Place place(dev, a[13]);
   at::Tensor Z;
   if (a[12] == Py_None) {
     Z = make({T, h}, at::kBFloat16, dev);
@@ -764,11 +764,8 @@ PyObject* fp4_mlp(PyObject* const* a) {
   }
   const size_t need =
       lib.fp4_mlp_workspace_bytes(handle, static_cast<int>(T), format);
-  at::Tensor ws;
-  if (a[13] != Py_None) ws = tensor("workspace", a[13]);
-  if (!ws.defined() || static_cast<size_t>(ws.numel()) < need ||
-      ws.device() != dev)
-    ws = make({static_cast<int64_t>(need > 256 ? need : 256)}, at::kByte, dev);
+  const at::Tensor ws =
+      make({static_cast<int64_t>(need > 256 ? need : 256)}, at::kByte, dev);
   const void* pp = packed.const_data_ptr();
   void* zp = T == 0 ? nullptr : Z.data_ptr();
   void* wp = ws.data_ptr();
@@ -874,6 +871,6 @@ PyMODINIT_FUNC PyInit__pycall() {
   set<fp4_matmul, 10>(7);
   set<fp4_linear, 10>(8);
   set<fp4_backward, 9>(9);
-  set<fp4_mlp, 15>(10);
+  set<fp4_mlp, 14>(10);
   return PyModule_Create(&module);
 }

@@ -41,6 +41,7 @@ class TensorParallelMLP:
         self.device = torch.device(device or "cuda")
         self._ws = None
         self._ws_tokens = None
+        self._fp4_ws = None   # of the last forward_fp4
 
     def close(self):
         if self.handle:
@@ -116,9 +117,12 @@ class TensorParallelMLP:
 
     def check(self, stream=None) -> int:
         """Synchronise and return the device status (TPMLP_OK or an error)."""
-        if self._ws is None:
-            return B_.TPMLP_OK
-        return B_.tp_mlp_check(self.handle, self._ws, stream)
+        for ws in (self._fp4_ws, self._ws):
+            rc = (B_.TPMLP_OK if ws is None else
+                  B_.tp_mlp_check(self.handle, ws, stream))
+            if rc != B_.TPMLP_OK:
+                return rc
+        return B_.TPMLP_OK
 
     # ------------------------------------------------------------- fp8 --
     def pack_fp8_weights(self, A, B, stream=None) -> torch.Tensor:
@@ -256,14 +260,16 @@ class TensorParallelMLP:
                     stream=None):
         """Forward on weights from pack_fp4_weights (tp_fp4_mlp_forward): X (or
         LayerNorm(X)) and Y = GeLU(H) are quantized with nvfp4's powers of two
-        ``x_scale`` and ``y_scale`` (mxfp4: 1)."""
+        ``x_scale`` and ``y_scale`` (mxfp4: 1).  Its workspace is of this call alone:
+        what forward() keeps for backward() stays."""
         h, f = self.hidden, self.ffn
         if not isinstance(packed, Fp4Weights) or packed.shape != (h, f):
             raise ValueError(f"packed must be the pack_fp4_weights of a block of "
                              f"{(h, f)}")
-        Z, self._ws = B_.tensor_calls().fp4_mlp(
+        self._fp4_ws = None
+        Z, self._fp4_ws = B_.tensor_calls().fp4_mlp(
             self.handle, h, f, _fp4_format(packed.format), X, packed.buffer, b1, b2,
-            gamma, beta, x_scale, y_scale, out, self._ws, stream)
+            gamma, beta, x_scale, y_scale, out, stream)
         return Z
 
 

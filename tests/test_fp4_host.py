@@ -199,6 +199,9 @@ def test_block_sizes_and_refusals():
             (ARG, dict(ws=None)), (ALIGN, dict(X=X + 8)), (ALIGN, dict(Z=C + 2)),
             (ALIGN, dict(b1=W + 4)), (ALIGN, dict(packed=P + 16)),
             (ALIGN, dict(ws=P2 + 16)), (WS, dict(ws_bytes=100)),
+            (ARG, dict(Z=X)), (ARG, dict(Z=P + 512)), (ARG, dict(Z=P2 + 512)),
+            (ARG, dict(ws=X - 256)), (ARG, dict(ws=P)), (ARG, dict(b1=P2 + 64)),
+            (ARG, dict(b2=C)),
             (ARG, dict(xs=0.0)), (ARG, dict(ys=5.0)), (ARG, dict(fmt=MX, xs=2.0))):
         refused(code, lambda: forward(h, **kw))
     refused(ARG, lambda: forward(block(use_layernorm=1)))

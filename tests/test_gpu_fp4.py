@@ -250,6 +250,27 @@ def test_product_of_many_rows(fmt, T, N, K, dtype):
     assert torch.equal(got, fp4.matmul(a, b, bias, dtype=dtype))
 
 
+@pytest.mark.parametrize("T", [1, 20, 600])
+def test_scales_of_whole_matrices_far_from_one(T):
+    """g_A g_B below and above fp32's range, the results within it (or zero)."""
+    N, K = 300, 640
+    for sx, sw in ((1e-20, 1e-19), (1e-25, 1e-12), (1e25, 1e10), (1e-30, 1e30)):
+        x, W = randn(T, K, seed=T, dtype=F32), randn(K, N, seed=1, dtype=F32)
+        x[0, :300] = 0
+        lin = fp4.Fp4Linear(W * sw)
+        q = fp4.quantize(x * sx)
+        va, vb = f64(q.dequantize(F32)), f64(lin.weight.dequantize(F32))
+        for y in (fp4.matmul(q, lin.weight, dtype=F32),
+                  lin.forward(x * sx, x_scale=None, dtype=F32),
+                  lin.forward(x * sx, x_scale=float(q.tensor_scale()), dtype=F32)):
+            close_product(y, va, vb)
+    # 2^127 and 2^120: the codes of small x are zeros, and so is y
+    x, W = randn(T, K, seed=T), torch.full((K, N), 2.0 ** 126, device="cuda")
+    lin = fp4.Fp4Linear(W)
+    assert not fp4.matmul(fp4.quantize(x, scale=2.0 ** 127), lin.weight).any()
+    assert not lin.forward(x, x_scale=2.0 ** 127).any()
+
+
 def test_every_pair_of_codes_and_scales():
     """Each row of A holds one code in one block, B all codes: every product of
     two codes under many scales, exact in fp32."""
@@ -487,8 +508,8 @@ def check_block(m, Z, X, Xn, A, Bw, b1, b2, fmt, gelu="erf", residual=False):
     code = fp4._FORMATS[fmt]
     # (up to 4 rows are quantised inside the product)
     xq = (fp4.quantize(Xn, fmt, scale=one) if T <= 4
-          else fp4.Fp4Tensor(m._ws, T, h, fmt))
-    yq = fp4.Fp4Tensor(m._ws[up(B.tp_fp4_bytes(T, h, code)):], T, f, fmt)
+          else fp4.Fp4Tensor(m._fp4_ws, T, h, fmt))
+    yq = fp4.Fp4Tensor(m._fp4_ws[up(B.tp_fp4_bytes(T, h, code)):], T, f, fmt)
     check_quantized(xq, f64(Xn), one)
     H = f64(xq.dequantize(F32)) @ O.quantized(f64(A).T, fmt).T
     H = H if b1 is None else H + f64(b1)
@@ -533,7 +554,7 @@ def test_block_with_layernorm_and_residual(fmt, T):
     assert m.check() == 0
     code = fp4._FORMATS[fmt]
     at = up(B.tp_fp4_bytes(T, h, code)) + up(B.tp_fp4_bytes(T, f, code))
-    Xn = m._ws[at:at + 2 * T * h].view(BF).view(T, h)
+    Xn = m._fp4_ws[at:at + 2 * T * h].view(BF).view(T, h)
     want = OM.layernorm_forward(f64(X), f64(gamma), f64(beta))[0]
     # one rounding to bf16, and fp32's: a few in 2^-24 of values of order 4
     assert (np.abs(f64(Xn) - want) <= 2.0 ** -8 * np.abs(want) + 1e-5).all()
@@ -565,6 +586,72 @@ def test_block_scales_and_no_tokens():
 
 
 # ---------------------------------------------- streams, graphs, threads --
+
+def test_block_in_two_graphs_and_beside_a_training_step():
+    """Two captured graphs of one block, replayed at the same time; and a
+    forward_fp4 between a training forward and its backward changes no gradient."""
+    m, X, A, Bw, b1, b2 = block_case(300, 256, 1024, 2)
+    p = m.pack_fp4_weights(A, Bw)
+    graphs = []
+    for i in range(2):
+        xi, g = X.clone(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = m.forward_fp4(xi, p, b1, b2)
+        graphs.append((g, xi, out, torch.cuda.Stream()))
+    for rep in range(5):
+        new = [randn(300, 256, seed=20 + 2 * rep + i) for i in range(2)]
+        for (g, xi, out, s), n in zip(graphs, new):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                xi.copy_(n)
+                g.replay()
+        torch.cuda.synchronize()
+        for (g, xi, out, s), n in zip(graphs, new):
+            assert torch.equal(out, m.forward_fp4(n, p, b1, b2))
+    dZ = randn(300, 256, seed=40)
+    m.forward(X, A, Bw, b1, b2)
+    want = {k: v.clone() for k, v in m.backward(dZ, X, A, Bw).items()}
+    m.forward(X, A, Bw, b1, b2)
+    m.forward_fp4(randn(300, 256, seed=41), p, b1, b2)
+    got = m.backward(dZ, X, A, Bw)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    assert m.check() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,h,f", [(2, 16384, 32768), (16, 16384, 32768),
+                                   (2000, 2048, 8192)])
+def test_wait_timeout_is_reported_and_context_survives(fmt, T, h, f):
+    """Every kind of product: its bounded waits give up, the status says so, and the
+    same block then computes what it did before.  (A wait gives up after two tries,
+    which last up to 20 us each: the weights of few rows are read in 45 us or more,
+    300 MB at 6.7 TB/s.)"""
+    m, X, A, Bw, b1, b2 = block_case(T, h, f, 1)
+    p = m.pack_fp4_weights(A, Bw, format=fmt)
+    want = m.forward_fp4(X, p, b1, b2)
+    assert m.check() == B.TPMLP_OK
+    B.tp_mlp_set_wait_budget(m.handle, 1)
+    m.forward_fp4(X, p, b1, b2)
+    assert m.check() == B.TPMLP_ERR_TIMEOUT
+    assert m.check() == B.TPMLP_OK
+    B.tp_mlp_set_wait_budget(m.handle, 2_000_000_000)
+    assert torch.equal(m.forward_fp4(X, p, b1, b2), want)
+    assert m.check() == B.TPMLP_OK
+
+
+def test_products_at_once_on_the_same_operands():
+    a, b, va, vb = operands(700, 900, 640, "nvfp4")
+    few = fp4.quantize(randn(20, 640, seed=5))
+    want = [fp4.matmul(a, b), fp4.matmul(few, b), fp4.matmul(a, a)]
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [fp4.matmul((a, few, a)[i % 3], (b, b, a)[i % 3], stream=s)
+           for _ in range(10) for i, s in enumerate(streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
+    assert a.check() == 0 and few.check() == 0
+
 
 def test_other_streams_and_captured_graphs():
     T, K, N = 600, 512, 1300
