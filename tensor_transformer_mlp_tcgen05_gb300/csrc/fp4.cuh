@@ -92,6 +92,22 @@ __device__ __forceinline__ size_t scale_word(int r, int kt, int q, int ktiles,
 
 // ------------------------------------------------------------- arithmetic --
 
+// Every kernel here is launched so that it may start while the launch before it on
+// the stream still runs, and lets the next one start.  Two kinds:
+//   - a call's first kernel waits for the launch before it, then lets the next
+//     start: what the next one finds complete is all that came before the call;
+//   - a call's later kernel (the quantisation after its amax, a product after the
+//     quantisation or product that makes A) lets the next one start, loads what
+//     was there before the call, and waits before it reads or writes the rest.
+// So none reads what an earlier call may still write, and none ends before all that
+// came before it.
+__device__ __forceinline__ void wait_for_launch_before() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_launch_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // x rounded to 14 significant bits "to odd": a value that is not one of them
 // gets the neighbour whose last bit is set.  It compares with every number of
 // 13 significant bits or fewer as x itself does, so codes and scales, whose

@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARRIERS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
+  if (!args.dependent) wait_for_launch_before();
   let_next_launch_start();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -563,7 +564,7 @@ cudaError_t launch_pairs(const CUtensorMap& ta, const CUtensorMap& tsa,
   cfg.dynamicSmemBytes = smem_bytes<FORMAT>();
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = args.dependent ? 2 : 1;
+  cfg.numAttrs = 2;
   const long long last = tiles % max_pairs;   // tiles of the last round
   const long long halves = 2 * last <= max_pairs ? last : 0;
   const long long items = tiles + halves;

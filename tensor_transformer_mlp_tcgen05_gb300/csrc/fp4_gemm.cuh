@@ -7,16 +7,6 @@
 namespace tpmlp {
 namespace fp4 {
 
-// A product launched with `dependent` may start while the launch before it (which
-// makes A: a quantisation, or the product before) still runs.  B, which was
-// complete before that one started, is loaded at once; A, g and all stores wait.
-__device__ __forceinline__ void wait_for_launch_before() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void let_next_launch_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // A k-tile is 256 elements, 128 bytes of codes: four MMAs of K = 64.
 constexpr int KSTEPS = 4;
 

@@ -10,14 +10,14 @@ namespace fp4 {
 
 // Where a quantisation takes g from: 2^exponent; or another packed matrix (like);
 // or the matrix's own largest |x|, left in `slots` words of its header by
-// launch_amax, whose dependent the launch then is.
+// launch_amax, the launch before.
 struct Gain {
   int exponent;
   int slots;
   const Header* like;
 };
 
-// The largest finite |x| of x [rows, cols], block by block; returns the blocks.
+// The largest finite |x| of x [rows, cols], block by block; slots: the blocks.
 cudaError_t launch_amax(bool bf16, const void* x, long long stride,
                         long long rows, long long cols, Header* head, int* slots,
                         cudaStream_t s);
@@ -66,8 +66,8 @@ struct ProductArgs {
   int gelu_mode;
   int* status;
   unsigned long long budget_ns;
-  // 1: may start while the launch before it on the stream, which makes A and
-  // itself started after B was complete, still runs
+  // 1: a call's later kernel: the launch before it makes A, and B was complete
+  // before the call (see wait_for_launch_before)
   int dependent;
 };
 

@@ -24,7 +24,7 @@ __device__ __forceinline__ void clear_status(const Packed& p) {
 __device__ __forceinline__ float inverse_g(const Packed& p, const Gain& gain) {
   int e = gain.exponent;
   if (gain.slots > 0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // for the pass before
+    wait_for_launch_before();   // the pass before
     uint32_t top = 0;
     for (int i = threadIdx.x & 31; i < gain.slots; i += 32)
       top = max(top, p.head->amax[i]);
@@ -44,9 +44,9 @@ template <class T, int FORMAT, int LD, int PASSES>
 __global__ void __launch_bounds__(THREADS)
     rows_kernel(const T* __restrict__ x, long long stride, const Packed p,
                 const Gain gain) {
+  if (gain.slots == 0) wait_for_launch_before();
   clear_status(p);
-  // (a product that is launched as this one's dependent starts loading weights)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_launch_start();
   const int lane = threadIdx.x & 31;
   const int unit = threadIdx.x & 15;
   const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.ktiles));
@@ -160,8 +160,9 @@ template <class T, int FORMAT, bool PAIR>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 3 : 2)
     columns_kernel(const T* __restrict__ x, long long stride, int x_rows,
                    const Packed p, const Gain gain, float* __restrict__ part) {
+  if (gain.slots == 0) wait_for_launch_before();
   clear_status(p);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_launch_start();
   // 16-byte unit u of row n at unit u ^ (n / 2 mod 8): the lanes of a warp,
   // two rows apart, write to different banks
   __shared__ uint4 s_codes[T_COLS * 8];
@@ -258,7 +259,8 @@ template <class T, int LD>
 __global__ void __launch_bounds__(THREADS)
     amax_kernel(const T* __restrict__ x, long long stride, long long rows,
                 long long cols, Header* head) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_launch_before();
+  let_next_launch_start();
   const long long segments = (cols + AMAX_UNITS * 16 - 1) / (AMAX_UNITS * 16);
   uint32_t top = 0;
   for (long long item = blockIdx.x; item < rows * segments; item += gridDim.x) {
@@ -353,6 +355,8 @@ template <class T, int FORMAT, int PASSES>
 __global__ void __launch_bounds__(THREADS)
     dequantize_kernel(const Packed p, T* __restrict__ out, long long stride,
                       int wide) {
+  wait_for_launch_before();
+  let_next_launch_start();
   const int unit = threadIdx.x & 15;
   const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.ktiles));
   const int chunk = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.ktiles));
@@ -397,10 +401,8 @@ bool on_boundary(const void* p, long long stride_bytes, int bytes) {
 // Blocks that keep all SMs busy: with fewer, a block takes fewer rows.
 constexpr long long FULL_GRID = 152 * 4;
 
-// A launch, as the dependent of the amax pass where there is one.
 template <class... P, class... A>
-cudaError_t launch(void (*kernel)(P...), unsigned grid, const Gain& gain,
-                   cudaStream_t s, A... args) {
+cudaError_t launch(void (*kernel)(P...), unsigned grid, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -409,7 +411,7 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, const Gain& gain,
   cfg.blockDim = dim3(THREADS);
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = gain.slots > 0 ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -419,9 +421,9 @@ cudaError_t rows_launch(const T* x, long long stride, const Packed& p,
   const long long units = (p.rows + 15ll) / 16 * p.ktiles;
   if (units >= 4 * FULL_GRID)
     return launch(rows_kernel<T, FORMAT, LD, 4>,
-                  static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), g, s, x,
+                  static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), s, x,
                   stride, p, g);
-  return launch(rows_kernel<T, FORMAT, LD, 1>, static_cast<unsigned>(units), g, s,
+  return launch(rows_kernel<T, FORMAT, LD, 1>, static_cast<unsigned>(units), s,
                 x, stride, p, g);
 }
 
@@ -444,12 +446,12 @@ cudaError_t columns_format(const T* x, long long stride, int x_rows,
       on_boundary(x, stride * static_cast<long long>(sizeof(T)), 2 * sizeof(T));
   return launch(pairs ? columns_kernel<T, FORMAT, true>
                       : columns_kernel<T, FORMAT, false>,
-                grid, g, s, x, stride, x_rows, p, g, part);
+                grid, s, x, stride, x_rows, p, g, part);
 }
 
 template <class T>
-int amax_type(const T* x, long long stride, long long rows, long long cols,
-              Header* head, cudaStream_t s) {
+cudaError_t amax_type(const T* x, long long stride, long long rows, long long cols,
+                      Header* head, int* slots, cudaStream_t s) {
   if (stride == cols) {   // one long row
     cols *= rows;
     stride = cols;
@@ -457,30 +459,26 @@ int amax_type(const T* x, long long stride, long long rows, long long cols,
   }
   const long long items =
       (cols + AMAX_UNITS * 16 - 1) / (AMAX_UNITS * 16) * rows;
-  const int grid = static_cast<int>(items < AMAX_SLOTS ? items : AMAX_SLOTS);
+  *slots = static_cast<int>(items < AMAX_SLOTS ? items : AMAX_SLOTS);
   const long long bytes = rows == 1 ? 0 : stride * static_cast<long long>(sizeof(T));
-  if (on_boundary(x, bytes, 32))
-    amax_kernel<T, 32><<<grid, THREADS, 0, s>>>(x, stride, rows, cols, head);
-  else if (on_boundary(x, bytes, 16))
-    amax_kernel<T, 16><<<grid, THREADS, 0, s>>>(x, stride, rows, cols, head);
-  else
-    amax_kernel<T, 0><<<grid, THREADS, 0, s>>>(x, stride, rows, cols, head);
-  return grid;
+  auto kernel = on_boundary(x, bytes, 32)   ? amax_kernel<T, 32>
+                : on_boundary(x, bytes, 16) ? amax_kernel<T, 16>
+                                            : amax_kernel<T, 0>;
+  return launch(kernel, static_cast<unsigned>(*slots), s, x, stride, rows, cols, head);
 }
 
 template <class T>
-void dequantize_type(const Packed& p, int format, T* out, long long stride,
-                     cudaStream_t s) {
+cudaError_t dequantize_type(const Packed& p, int format, T* out, long long stride,
+                            cudaStream_t s) {
   constexpr int PASSES = 4;
   const unsigned grid = static_cast<unsigned>(
       (p.rows + 16ll * PASSES - 1) / (16 * PASSES) * p.ktiles);
   const long long bytes = stride * static_cast<long long>(sizeof(T));
   const int wide =
       on_boundary(out, bytes, 32) ? 32 : on_boundary(out, bytes, 16) ? 16 : 0;
-  if (format == TPFP4_NV)
-    dequantize_kernel<T, TPFP4_NV, PASSES><<<grid, THREADS, 0, s>>>(p, out, stride, wide);
-  else
-    dequantize_kernel<T, TPFP4_MX, PASSES><<<grid, THREADS, 0, s>>>(p, out, stride, wide);
+  return launch(format == TPFP4_NV ? dequantize_kernel<T, TPFP4_NV, PASSES>
+                                   : dequantize_kernel<T, TPFP4_MX, PASSES>,
+                grid, s, p, out, stride, wide);
 }
 
 }  // namespace
@@ -488,11 +486,10 @@ void dequantize_type(const Packed& p, int format, T* out, long long stride,
 cudaError_t launch_amax(bool bf16, const void* x, long long stride,
                         long long rows, long long cols, Header* head, int* slots,
                         cudaStream_t s) {
-  *slots = bf16 ? amax_type(static_cast<const __nv_bfloat16*>(x), stride, rows,
-                            cols, head, s)
-                : amax_type(static_cast<const float*>(x), stride, rows, cols, head,
-                            s);
-  return cudaGetLastError();
+  return bf16 ? amax_type(static_cast<const __nv_bfloat16*>(x), stride, rows, cols,
+                          head, slots, s)
+              : amax_type(static_cast<const float*>(x), stride, rows, cols, head,
+                          slots, s);
 }
 
 cudaError_t launch_quantize_rows(bool bf16, int format, const void* x,
@@ -529,11 +526,9 @@ cudaError_t launch_quantize_columns(bool bf16, int format, const void* x,
 
 cudaError_t launch_dequantize(const Packed& p, int format, bool bf16, void* out,
                               long long stride, cudaStream_t s) {
-  if (bf16)
-    dequantize_type(p, format, static_cast<__nv_bfloat16*>(out), stride, s);
-  else
-    dequantize_type(p, format, static_cast<float*>(out), stride, s);
-  return cudaGetLastError();
+  return bf16 ? dequantize_type(p, format, static_cast<__nv_bfloat16*>(out), stride,
+                                s)
+              : dequantize_type(p, format, static_cast<float*>(out), stride, s);
 }
 
 }  // namespace fp4

@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(threads_of(SRC), 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::NUM_BARRIERS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
+  if (!args.dependent) wait_for_launch_before();
   let_next_launch_start();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -446,7 +447,7 @@ cudaError_t launch_tokens(const ProductArgs& args, int sms, cudaStream_t s) {
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = args.dependent ? 2 : 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, args, split);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
