@@ -247,8 +247,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARRIERS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
-  if (!args.dependent) wait_for_launch_before();
-  let_next_launch_start();
+  if (args.dependent) let_next_launch_start();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t prank = ptx::cluster_ctarank();
@@ -283,6 +282,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
+  if (!args.dependent) {
+    wait_for_launch_before();
+    let_next_launch_start();
+  }
   const Ctl ctl{abort_flag, args.status, args.budget_ns};
   const int num_m = (args.M + PM - 1) / PM;
   const int num_n = (args.N + PN - 1) / PN;

@@ -244,8 +244,7 @@ __global__ void __launch_bounds__(threads_of(SRC), 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::NUM_BARRIERS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
-  if (!args.dependent) wait_for_launch_before();
-  let_next_launch_start();
+  if (args.dependent) let_next_launch_start();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(ptx::cluster_ctarank());
@@ -265,9 +264,6 @@ __global__ void __launch_bounds__(threads_of(SRC), 2)
     ptx::mbar_init(done_bar, 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();
-    if (SRC != PACKED && blockIdx.x == 0 && blockIdx.y == 0) {
-      for (int i = 0; i < 4; ++i) args.status[i] = 0;
-    }
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), S::T_COLS);
@@ -278,6 +274,12 @@ __global__ void __launch_bounds__(threads_of(SRC), 2)
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const Ctl ctl{abort_flag, args.status, args.budget_ns};
+  if (!args.dependent) {
+    wait_for_launch_before();
+    let_next_launch_start();
+  }
+  if (SRC != PACKED && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 4)
+    args.status[threadIdx.x] = 0;
 
   if (warp == 0) {
     // ------------------------------------------------------ producer --

@@ -689,6 +689,64 @@ def test_other_streams_and_captured_graphs():
     assert torch.equal(grads["dw"], lin.backward(dy, x)["dw"])
 
 
+def test_launches_among_other_work():
+    """The kernels start early only where what they read is complete: weights packed
+    right before they are used, copies and joined streams before a call, many calls
+    in a row, eagerly and in a captured graph."""
+    T, h = 32, 1024
+    Ws = [randn(h, h, seed=i, scale=h ** -0.5) for i in range(4)]
+    x = randn(T, h, seed=9)
+    rows = (1, 4, 8, 32)
+
+    def chain(x, side):
+        out = []
+        for n in rows:
+            y = torch.empty_like(x[:n]).copy_(x[:n])
+            for W in Ws:      # packed, used, overwritten in the next round
+                lin = fp4.Fp4Linear(W)
+                y = lin.forward(y)
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                z = fp4.quantize(y).dequantize()
+            main.wait_stream(side)
+            m = fp4.matmul(fp4.quantize(z), fp4.quantize(Ws[0]))
+            m.record_stream(main)
+            out.append(m)
+        return out
+
+    def steps(x):
+        """The same, one by one."""
+        out = []
+        for n in rows:
+            y = x[:n].clone()
+            for W in Ws:
+                w = fp4.quantize(W, transpose=True)
+                torch.cuda.synchronize()
+                q = fp4.quantize(y, scale=1.0)
+                torch.cuda.synchronize()
+                y = fp4.matmul(q, w)
+                torch.cuda.synchronize()
+            z = fp4.quantize(y).dequantize()
+            torch.cuda.synchronize()
+            a, b = fp4.quantize(z), fp4.quantize(Ws[0])
+            torch.cuda.synchronize()
+            out.append(fp4.matmul(a, b))
+        return out
+
+    side = torch.cuda.Stream()
+    want = steps(x)
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(chain(x, side), want))
+    g, xi = torch.cuda.CUDAGraph(), x.clone()
+    with torch.cuda.graph(g):
+        got = chain(xi, side)
+    for i in range(10):
+        xi.copy_(randn(T, h, seed=50 + i))
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, steps(xi)))
+
+
 def test_several_threads():
     from concurrent.futures import ThreadPoolExecutor
     lin = fp4.Fp4Linear(randn(300, 700, seed=1))
