@@ -92,6 +92,15 @@ int tp_fp4_quantize(long long rows, long long cols, int dtype, const void* x,
                     size_t workspace_bytes, void* stream);
 size_t tp_fp4_colsum_workspace_bytes(long long rows, long long cols);
 
+/* x [rows >= 1, cols] both ways in one pass: along its rows into `packed`
+ * [rows, cols], along its columns into packed_t [cols, rows]; the rest as above.
+ * The same results as the two calls one by one. */
+int tp_fp4_quantize_both(long long rows, long long cols, int dtype, const void* x,
+                         long long row_stride, int format, double scale,
+                         void* packed, size_t packed_bytes, void* packed_t,
+                         size_t packed_t_bytes, float* colsum, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* The values of a packed [rows, cols] matrix, written as `dtype` (exact in bf16
  * too, but for values out of its range). */
 int tp_fp4_dequantize(long long rows, long long cols, int format,

@@ -66,9 +66,9 @@ EXPORTED_ROPE = (
 EXPORTED_GRAD = ("tp_grad_workspace_bytes", "tp_grad_norm", "tp_grad_clip")
 EXPORTED_FP4 = (
     "tp_fp4_bytes", "tp_fp4_offset", "tp_fp4_quantize",
-    "tp_fp4_colsum_workspace_bytes", "tp_fp4_dequantize", "tp_fp4_matmul",
-    "tp_fp4_linear", "tp_fp4_check", "tp_fp4_mlp_weights_bytes", "tp_fp4_mlp_pack_weights",
-    "tp_fp4_mlp_workspace_bytes", "tp_fp4_mlp_forward",
+    "tp_fp4_colsum_workspace_bytes", "tp_fp4_quantize_both", "tp_fp4_dequantize",
+    "tp_fp4_matmul", "tp_fp4_linear", "tp_fp4_check", "tp_fp4_mlp_weights_bytes",
+    "tp_fp4_mlp_pack_weights", "tp_fp4_mlp_workspace_bytes", "tp_fp4_mlp_forward",
 )
 
 TPROPE_MAX_HEAD_DIM = 256
@@ -338,6 +338,9 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.tp_fp4_quantize.argtypes = [ll, ll, _i, _vp, ll, _i, _i, dbl, _vp, _vp,
                                   _sz, _vp, _vp, _sz, _vp]
     L.tp_fp4_quantize.restype = _i
+    L.tp_fp4_quantize_both.argtypes = [ll, ll, _i, _vp, ll, _i, dbl, _vp, _sz, _vp,
+                                       _sz, _vp, _vp, _sz, _vp]
+    L.tp_fp4_quantize_both.restype = _i
     L.tp_fp4_dequantize.argtypes = [ll, ll, _i, _vp, _sz, _i, _vp, ll, _vp]
     L.tp_fp4_dequantize.restype = _i
     L.tp_fp4_matmul.argtypes = [ll, ll, ll, _i, _vp, _sz, _vp, _sz, _vp, _i,
@@ -387,8 +390,8 @@ def tensor_calls():
                       "tp_qk_norm_workspace_bytes", "tp_qk_norm_backward",
                       "tp_grad_workspace_bytes", "tp_grad_norm",
                       "tp_grad_clip", "tp_fp4_bytes", "tp_fp4_quantize",
-                      "tp_fp4_colsum_workspace_bytes", "tp_fp4_dequantize",
-                      "tp_fp4_matmul", "tp_fp4_linear",
+                      "tp_fp4_colsum_workspace_bytes", "tp_fp4_quantize_both",
+                      "tp_fp4_dequantize", "tp_fp4_matmul", "tp_fp4_linear",
                       "tp_fp4_mlp_workspace_bytes", "tp_fp4_mlp_forward")])
         _calls = m
     return _calls
@@ -832,6 +835,15 @@ def tp_fp4_quantize(rows, cols, dtype, x, row_stride, transpose, format, scale,
         rows, cols, dtype, _ptr(x), row_stride, transpose, format, scale,
         _ptr(like), _ptr(packed), packed_bytes, _ptr(colsum), _ptr(workspace),
         workspace_bytes, _stream(stream)), "tp_fp4_quantize")
+
+
+def tp_fp4_quantize_both(rows, cols, dtype, x, row_stride, format, scale, packed,
+                         packed_bytes, packed_t, packed_t_bytes, colsum=None,
+                         workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().tp_fp4_quantize_both(
+        rows, cols, dtype, _ptr(x), row_stride, format, scale, _ptr(packed),
+        packed_bytes, _ptr(packed_t), packed_t_bytes, _ptr(colsum), _ptr(workspace),
+        workspace_bytes, _stream(stream)), "tp_fp4_quantize_both")
 
 
 def tp_fp4_dequantize(rows, cols, format, packed, packed_bytes, dtype, out,

@@ -83,13 +83,15 @@ int packed_ok(const char* what, long long rows, long long cols, int format,
   return TPMLP_OK;
 }
 
-// Quantise along rows or columns, arguments checked.
+// Quantise along rows or columns, arguments checked.  both (nullable, with
+// transpose): along the rows too, into it.
 int quantize(HandleCore* core, const char* name, long long rows, long long cols,
              bool bf16, const void* x, long long stride, bool transpose,
              int format, int exponent, const void* like, void* packed, float* part,
-             cudaStream_t s) {
+             cudaStream_t s, void* both = nullptr) {
   const fp4::Packed p = transpose ? fp4::view(packed, cols, rows)
                                   : fp4::view(packed, rows, cols);
+  const fp4::Packed rp = both != nullptr ? fp4::view(both, rows, cols) : p;
   auto step = [&](const char* n, auto&& f) {
     return core != nullptr ? run(core, n, s, f) : launched(n, f());
   };
@@ -104,7 +106,8 @@ int quantize(HandleCore* core, const char* name, long long rows, long long cols,
   return step(name, [&] {
     return transpose
                ? fp4::launch_quantize_columns(bf16, format, x, stride,
-                                              static_cast<int>(rows), p, g, part, s)
+                                              static_cast<int>(rows), p, g, part,
+                                              both != nullptr ? &rp : nullptr, s)
                : fp4::launch_quantize_rows(bf16, format, x, stride, p, g, s);
   });
 }
@@ -200,6 +203,15 @@ int left_operand(HandleCore* core, const char* name, long long rows,
                   nullptr, xq, nullptr, s);
 }
 
+// A column quantisation's sums over 256 rows each, added up.
+int finish_colsum(const void* part, float* colsum, long long rows, long long cols,
+                  cudaStream_t s) {
+  return launched("fp4_colsum",
+                  launch_colsum_finalize(static_cast<const float*>(part), colsum,
+                                         static_cast<int>((rows + 255) / 256),
+                                         static_cast<int>(cols), s));
+}
+
 // tp_fp4_quantize's arguments.
 int check_quantize(long long rows, long long cols, int dtype, const void* x,
                    long long row_stride, int transpose, int format, double scale,
@@ -243,9 +255,10 @@ int check_quantize(long long rows, long long cols, int dtype, const void* x,
         overlap(workspace, nw, packed, np))
       return bad(TPMLP_ERR_ARG, "fp4: colsum or workspace overlaps another buffer");
   }
-  // one block a 64-column, 256-row piece (columns) or 16 rows x 256 (rows)
+  // one block a 64-column, 256-row piece (columns, up to a multiple of 256) or 16
+  // rows x 256 (rows)
   const long long blocks = transpose
-                               ? (cols + 63) / 64 * ((rows + 255) / 256)
+                               ? (cols + 255) / 256 * 4 * ((rows + 255) / 256)
                                : (rows + 15) / 16 * ((cols + 255) / 256);
   if (blocks > INT_MAX) return bad(TPMLP_ERR_SHAPE, "fp4: matrix too large");
   return TPMLP_OK;
@@ -374,11 +387,36 @@ int tp_fp4_quantize(long long rows, long long cols, int dtype, const void* x,
   TRY(quantize(nullptr, "fp4_quantize", rows, cols, dtype == TPMLP_BF16, x,
                row_stride, transpose != 0, format, exponent, like, packed,
                colsum != nullptr ? static_cast<float*>(workspace) : nullptr, s));
-  if (colsum == nullptr) return TPMLP_OK;
-  return launched("fp4_colsum", launch_colsum_finalize(
-                                    static_cast<const float*>(workspace), colsum,
-                                    static_cast<int>((rows + 255) / 256),
-                                    static_cast<int>(cols), s));
+  return colsum == nullptr ? TPMLP_OK
+                           : finish_colsum(workspace, colsum, rows, cols, s);
+}
+
+int tp_fp4_quantize_both(long long rows, long long cols, int dtype, const void* x,
+                         long long row_stride, int format, double scale,
+                         void* packed, size_t packed_bytes, void* packed_t,
+                         size_t packed_t_bytes, float* colsum, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  int exponent = 0;
+  TRY(check_quantize(rows, cols, dtype, x, row_stride, 1, format, scale, nullptr,
+                     packed_t, packed_t_bytes, colsum, workspace, workspace_bytes,
+                     &exponent));
+  TRY(check_quantize(rows, cols, dtype, x, row_stride, 0, format, scale, nullptr,
+                     packed, packed_bytes, nullptr, nullptr, 0, &exponent));
+  const size_t np = fp4::packed_bytes(rows, cols, format);
+  if (overlap(packed, np, packed_t, fp4::packed_bytes(cols, rows, format)) ||
+      overlap(packed, np, colsum, static_cast<size_t>(cols) * 4) ||
+      (colsum != nullptr &&
+       overlap(packed, np, workspace, tp_fp4_colsum_workspace_bytes(rows, cols))))
+    return bad(TPMLP_ERR_ARG, "fp4: packed overlaps another output");
+  int sms = 0;
+  TRY(check_device(&sms));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  TRY(quantize(nullptr, "fp4_quantize_both", rows, cols, dtype == TPMLP_BF16, x,
+               row_stride, true, format, exponent, nullptr, packed_t,
+               colsum != nullptr ? static_cast<float*>(workspace) : nullptr, s,
+               packed));
+  return colsum == nullptr ? TPMLP_OK
+                           : finish_colsum(workspace, colsum, rows, cols, s);
 }
 
 int tp_fp4_dequantize(long long rows, long long cols, int format,

@@ -28,11 +28,13 @@ cudaError_t launch_quantize_rows(bool bf16, int format, const void* x,
                                  const Gain& g, cudaStream_t s);
 
 // x [x_rows = p.cols, p.rows], transposed, into p.  part (nullable):
-// [p.ktiles][p.rows] sums of x's columns over 256 rows each.
+// [p.ktiles][p.rows] sums of x's columns over 256 rows each.  rp (nullable): x along
+// its rows, in the same launch.
 cudaError_t launch_quantize_columns(bool bf16, int format, const void* x,
                                     long long stride, int x_rows,
                                     const Packed& p, const Gain& g,
-                                    float* part, cudaStream_t s);
+                                    float* part, const Packed* rp,
+                                    cudaStream_t s);
 
 cudaError_t launch_dequantize(const Packed& p, int format, bool bf16, void* out,
                               long long stride, cudaStream_t s);

@@ -15,13 +15,14 @@ namespace {
 
 constexpr int THREADS = 256;
 
-// Block 0 clears the status word, before a product may start that writes to it.
+// Block 0 clears a status word, before a product may start that writes to it.
 __device__ __forceinline__ void clear_status(const Packed& p) {
   if (blockIdx.x == 0 && threadIdx.x < 4) p.head->status[threadIdx.x] = 0;
 }
 
-// 1 / g (all threads); block 0 writes g.
-__device__ __forceinline__ float inverse_g(const Packed& p, const Gain& gain) {
+// 1 / g (all threads); block 0 writes g, to `also` too.
+__device__ __forceinline__ float inverse_g(const Packed& p, const Gain& gain,
+                                           Header* also = nullptr) {
   int e = gain.exponent;
   if (gain.slots > 0) {
     wait_for_launch_before();   // the pass before
@@ -32,7 +33,10 @@ __device__ __forceinline__ float inverse_g(const Packed& p, const Gain& gain) {
   } else if (gain.like != nullptr) {   // a power of two
     e = static_cast<int>(__float_as_uint(gain.like->g) >> 23) - 127;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.head->g = exp2_of(e);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.head->g = exp2_of(e);
+    if (also != nullptr) also->g = exp2_of(e);
+  }
   return exp2_of(-e);
 }
 
@@ -150,18 +154,78 @@ struct Two<float> {
 
 constexpr int T_COLS = 64;   // columns of x a block takes
 
+// Where 16-byte piece c of row r of a block's elements lies in shared memory: a
+// lane writes two elements of a row, then reads the pieces of a unit of 16, the
+// lanes of a quarter warp those of two rows by four units, from different banks.
+template <class T>
+__device__ __forceinline__ int staged(int r, int c) {
+  constexpr int PIECES = T_COLS * sizeof(T) / 16;
+  const int x = sizeof(T) == 2 ? r & 1 : (c >> 3) | ((r & 1) << 1);
+  return (r * PIECES + (c ^ x)) * 16;
+}
+
+// A warp's 32 rows (from k0 on) of a block's 64 columns (from n0 on), quantised
+// along the rows into p: a lane takes four units of 16.
+template <class T, int FORMAT>
+__device__ __forceinline__ void quantize_staged(const uint8_t* s_x, const Packed& p,
+                                                int k0, int n0, float inv_g) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int unit = lane & 3;
+  const int kt = n0 / TILE_COLS, unit0 = n0 % TILE_COLS / 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2), row = k0 + r;
+    Raw<T> raw;
+    constexpr int PIECES = sizeof(T);   // of a unit
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4*>(
+          s_x + staged<T>(warp * 32 + r, unit * PIECES + j));
+      raw.w[4 * j] = u.x, raw.w[4 * j + 1] = u.y;
+      raw.w[4 * j + 2] = u.z, raw.w[4 * j + 3] = u.w;
+    }
+    float v[16];
+    raw.floats(v);
+    uint32_t amax = raw.amax();
+    if constexpr (FORMAT == TPFP4_MX)
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const Scale s = block_scale<FORMAT>(amax, inv_g);
+    const uint2 w = codes16<FORMAT, sizeof(T) == 4>(v, s);
+    constexpr int UNITS = block_size(FORMAT) / 16;
+    uint32_t word = s.byte << (8 * (unit / UNITS));
+    word |= __shfl_xor_sync(0xffffffffu, word, UNITS);
+    if constexpr (FORMAT == TPFP4_NV) word |= __shfl_xor_sync(0xffffffffu, word, 2);
+    if (row >= p.rows) continue;
+    const int u = unit0 + unit;
+    *reinterpret_cast<uint2*>(p.codes + code_row(row, kt, p.ktiles) +
+                              code_unit(row, u / 2) + u % 2 * 8) = w;
+    const int block = unit0 / UNITS;   // the first of four (NV) or two (MX)
+    uint8_t* to = p.scales + scale_word(row, kt, block / 4, p.ktiles,
+                                        tile_bytes(FORMAT)) + block % 4;
+    if (unit == 0) {
+      if constexpr (FORMAT == TPFP4_NV)
+        *reinterpret_cast<uint32_t*>(to) = word;
+      else
+        *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(word);
+    }
+  }
+}
+
 // A block takes 256 rows (one k-tile of the packed matrix) of 64 columns, a
 // warp 32 of those rows, a lane two columns: its 32 elements of a column are
 // two blocks of NV or one of MX.  Codes and scales go through shared memory,
 // so that a packed row's 128 bytes of codes are written together.
 // (three blocks an SM for bf16, 85 registers: 57 -> 47 us for 5120 x 20480; four
 // spill)
-template <class T, int FORMAT, bool PAIR>
+// BOTH: the elements, read once, are quantised along the rows of x into rp too.
+template <class T, int FORMAT, bool PAIR, bool BOTH>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 3 : 2)
     columns_kernel(const T* __restrict__ x, long long stride, int x_rows,
-                   const Packed p, const Gain gain, float* __restrict__ part) {
+                   const Packed p, const Gain gain, float* __restrict__ part,
+                   const Packed rp) {
   if (gain.slots == 0) wait_for_launch_before();
   clear_status(p);
+  if (BOTH) clear_status(rp);
   let_next_launch_start();
   // 16-byte unit u of row n at unit u ^ (n / 2 mod 8): the lanes of a warp,
   // two rows apart, write to different banks
@@ -169,7 +233,9 @@ __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 3 : 2)
   __shared__ __align__(16) uint8_t s_scales[T_COLS * 16];
   __shared__ float s_sum[8][T_COLS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tiles = (p.rows + T_COLS - 1) / T_COLS;
+  // (both: up to the end of rp's last k-tile, which its products read)
+  const int tiles = BOTH ? rp.ktiles * (TILE_COLS / T_COLS)
+                         : (p.rows + T_COLS - 1) / T_COLS;
   const int n0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(tiles)) * T_COLS;
   const int kt = static_cast<int>(blockIdx.x / static_cast<unsigned>(tiles));
   const int k0 = kt * TILE_COLS + warp * 32;
@@ -184,7 +250,17 @@ __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 3 : 2)
     for (int i = 0; i < 32; ++i)
       raw[i].load(src + i * stride, k0 + i < x_rows ? p.rows - n : 0);
   }
-  const float inv_g = inverse_g(p, gain);
+  extern __shared__ uint4 s_x[];   // both: [256][64] elements, see staged
+  if constexpr (BOTH) {
+    constexpr int LANES = 8 / sizeof(T);   // of a piece
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      *reinterpret_cast<Two<T>*>(reinterpret_cast<uint8_t*>(s_x) +
+                                 staged<T>(warp * 32 + i, lane / LANES) +
+                                 lane % LANES * sizeof(Two<T>)) = raw[i];
+    __syncwarp();
+  }
+  const float inv_g = inverse_g(p, gain, BOTH ? rp.head : nullptr);
   uint32_t tops[2][2];   // [column][16 rows]
   Two<T>::amax(raw, tops[0][0], tops[1][0]);
   Two<T>::amax(raw + 16, tops[0][1], tops[1][1]);
@@ -217,6 +293,9 @@ __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 3 : 2)
       s_sum[warp][r] = sum;
     }
   }
+  if constexpr (BOTH)
+    quantize_staged<T, FORMAT>(reinterpret_cast<const uint8_t*>(s_x), rp, k0, n0,
+                               inv_g);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < T_COLS * 8 / THREADS; ++i) {
@@ -402,13 +481,15 @@ bool on_boundary(const void* p, long long stride_bytes, int bytes) {
 constexpr long long FULL_GRID = 152 * 4;
 
 template <class... P, class... A>
-cudaError_t launch(void (*kernel)(P...), unsigned grid, cudaStream_t s, A... args) {
+cudaError_t launch(void (*kernel)(P...), unsigned grid, size_t smem, cudaStream_t s,
+                   A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -421,9 +502,9 @@ cudaError_t rows_launch(const T* x, long long stride, const Packed& p,
   const long long units = (p.rows + 15ll) / 16 * p.ktiles;
   if (units >= 4 * FULL_GRID)
     return launch(rows_kernel<T, FORMAT, LD, 4>,
-                  static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), s, x,
+                  static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), 0, s, x,
                   stride, p, g);
-  return launch(rows_kernel<T, FORMAT, LD, 1>, static_cast<unsigned>(units), s,
+  return launch(rows_kernel<T, FORMAT, LD, 1>, static_cast<unsigned>(units), 0, s,
                 x, stride, p, g);
 }
 
@@ -436,17 +517,33 @@ cudaError_t rows_format(const T* x, long long stride, const Packed& p,
   return rows_launch<T, FORMAT, 0>(x, stride, p, g, s);
 }
 
+template <class T, int FORMAT, bool BOTH>
+cudaError_t columns_launch(const T* x, long long stride, int x_rows,
+                           const Packed& p, const Gain& g, float* part,
+                           const Packed& rp, cudaStream_t s) {
+  const long long tiles = BOTH ? rp.ktiles * static_cast<long long>(TILE_COLS / T_COLS)
+                               : (p.rows + static_cast<long long>(T_COLS) - 1) / T_COLS;
+  const bool pairs =
+      on_boundary(x, stride * static_cast<long long>(sizeof(T)), 2 * sizeof(T));
+  auto kernel = pairs ? columns_kernel<T, FORMAT, true, BOTH>
+                      : columns_kernel<T, FORMAT, false, BOTH>;
+  const size_t smem = BOTH ? T_COLS * TILE_COLS * sizeof(T) : 0;
+  if (BOTH) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch(kernel, static_cast<unsigned>(tiles * p.ktiles), smem, s, x, stride,
+                x_rows, p, g, part, rp);
+}
+
 template <class T, int FORMAT>
 cudaError_t columns_format(const T* x, long long stride, int x_rows,
                            const Packed& p, const Gain& g, float* part,
-                           cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(
-      (p.rows + static_cast<long long>(T_COLS) - 1) / T_COLS * p.ktiles);
-  const bool pairs =
-      on_boundary(x, stride * static_cast<long long>(sizeof(T)), 2 * sizeof(T));
-  return launch(pairs ? columns_kernel<T, FORMAT, true>
-                      : columns_kernel<T, FORMAT, false>,
-                grid, s, x, stride, x_rows, p, g, part);
+                           const Packed* rp, cudaStream_t s) {
+  return rp != nullptr
+             ? columns_launch<T, FORMAT, true>(x, stride, x_rows, p, g, part, *rp, s)
+             : columns_launch<T, FORMAT, false>(x, stride, x_rows, p, g, part, p, s);
 }
 
 template <class T>
@@ -464,7 +561,8 @@ cudaError_t amax_type(const T* x, long long stride, long long rows, long long co
   auto kernel = on_boundary(x, bytes, 32)   ? amax_kernel<T, 32>
                 : on_boundary(x, bytes, 16) ? amax_kernel<T, 16>
                                             : amax_kernel<T, 0>;
-  return launch(kernel, static_cast<unsigned>(*slots), s, x, stride, rows, cols, head);
+  return launch(kernel, static_cast<unsigned>(*slots), 0, s, x, stride, rows, cols,
+                head);
 }
 
 template <class T>
@@ -478,7 +576,7 @@ cudaError_t dequantize_type(const Packed& p, int format, T* out, long long strid
       on_boundary(out, bytes, 32) ? 32 : on_boundary(out, bytes, 16) ? 16 : 0;
   return launch(format == TPFP4_NV ? dequantize_kernel<T, TPFP4_NV, PASSES>
                                    : dequantize_kernel<T, TPFP4_MX, PASSES>,
-                grid, s, p, out, stride, wide);
+                grid, 0, s, p, out, stride, wide);
 }
 
 }  // namespace
@@ -509,19 +607,20 @@ cudaError_t launch_quantize_rows(bool bf16, int format, const void* x,
 cudaError_t launch_quantize_columns(bool bf16, int format, const void* x,
                                     long long stride, int x_rows,
                                     const Packed& p, const Gain& g,
-                                    float* part, cudaStream_t s) {
+                                    float* part, const Packed* rp,
+                                    cudaStream_t s) {
   if (bf16) {
     const auto* b = static_cast<const __nv_bfloat16*>(x);
     return format == TPFP4_NV
                ? columns_format<__nv_bfloat16, TPFP4_NV>(b, stride, x_rows, p, g,
-                                                         part, s)
+                                                         part, rp, s)
                : columns_format<__nv_bfloat16, TPFP4_MX>(b, stride, x_rows, p, g,
-                                                         part, s);
+                                                         part, rp, s);
   }
   const auto* f = static_cast<const float*>(x);
   return format == TPFP4_NV
-             ? columns_format<float, TPFP4_NV>(f, stride, x_rows, p, g, part, s)
-             : columns_format<float, TPFP4_MX>(f, stride, x_rows, p, g, part, s);
+             ? columns_format<float, TPFP4_NV>(f, stride, x_rows, p, g, part, rp, s)
+             : columns_format<float, TPFP4_MX>(f, stride, x_rows, p, g, part, rp, s);
 }
 
 cudaError_t launch_dequantize(const Packed& p, int format, bool bf16, void* out,

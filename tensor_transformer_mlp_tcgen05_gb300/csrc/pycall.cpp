@@ -40,6 +40,7 @@ struct Library {
   decltype(&tp_fp4_bytes) fp4_bytes = nullptr;
   decltype(&tp_fp4_quantize) fp4_quantize = nullptr;
   decltype(&tp_fp4_colsum_workspace_bytes) fp4_colsum_bytes = nullptr;
+  decltype(&tp_fp4_quantize_both) fp4_quantize_both = nullptr;
   decltype(&tp_fp4_dequantize) fp4_dequantize = nullptr;
   decltype(&tp_fp4_matmul) fp4_matmul = nullptr;
   decltype(&tp_fp4_linear) fp4_linear = nullptr;
@@ -578,6 +579,27 @@ PyObject* fp4_quantize(PyObject* const* a) {
   return wrapped(packed);
 }
 
+// fp4_quantize_both(x, format, scale, stream) -> (packed, packed_t)
+PyObject* fp4_quantize_both(PyObject* const* a) {
+  const Matrix x("x", tensor("x", a[0]));
+  const at::Device dev = x.t.device();
+  const int format = static_cast<int>(integer(a[1]));
+  const double scale = real(a[2]);
+  if (x.rows < 1) throw Refused{"x: expected at least one row, got " + shown(x.t)};
+  const Place place(dev, a[3]);
+  const at::Tensor r = new_packed(x.rows, x.cols, format, dev);
+  const at::Tensor t = new_packed(x.cols, x.rows, format, dev);
+  void *rp = r.data_ptr(), *tp = t.data_ptr();
+  check(without_gil([&] {
+          return lib.fp4_quantize_both(
+              x.rows, x.cols, x.dtype, x.data(), x.stride, format, scale, rp,
+              static_cast<size_t>(r.numel()), tp, static_cast<size_t>(t.numel()),
+              nullptr, nullptr, 0, place.stream);
+        }),
+        "tp_fp4_quantize_both");
+  return tuple_of({r, t});
+}
+
 // fp4_dequantize(packed, rows, cols, format, dtype, out, stream) -> values
 PyObject* fp4_dequantize(PyObject* const* a) {
   const at::Tensor& packed = tensor("packed", a[0]);
@@ -693,24 +715,21 @@ PyObject* fp4_backward(PyObject* const* a) {
   float* dbp = sums ? db.data_ptr<float>() : nullptr;
   void* wsp = sums ? ws.data_ptr() : nullptr;
   const void* wp = w.const_data_ptr();
-  // dy's own g serves both of its quantisations
-  const void* like = format == TPFP4_NV && dy_scale == 0.0 ? qp : nullptr;
-  const char* what = "tp_fp4_linear";
+  const char* what = "tp_fp4_quantize_both";
   check(without_gil([&] {
-          int rc = lib.fp4_linear(T, K, N, dy.dtype, dy.data(), dy.stride, format,
-                                  dy_scale, qp, size(q), wp, nw, nullptr, dtype,
-                                  dxp, K, place.stream);
+          int rc = lib.fp4_quantize_both(T, N, dy.dtype, dy.data(), dy.stride, format,
+                                         dy_scale, qp, size(q), yp, size(dyt), dbp,
+                                         wsp, wsn, place.stream);
           if (rc != TPMLP_OK) return rc;
           what = "tp_fp4_quantize";
-          rc = lib.fp4_quantize(T, N, dy.dtype, dy.data(), dy.stride, 1, format,
-                                dy_scale, like, yp, size(dyt), dbp, wsp, wsn,
-                                place.stream);
-          if (rc != TPMLP_OK) return rc;
           rc = lib.fp4_quantize(T, K, x.dtype, x.data(), x.stride, 1, format,
                                 x_scale, nullptr, xp, size(xt), nullptr, nullptr, 0,
                                 place.stream);
           if (rc != TPMLP_OK) return rc;
           what = "tp_fp4_matmul";
+          rc = lib.fp4_matmul(T, K, N, format, qp, size(q), wp, nw, nullptr, dtype,
+                              dxp, K, place.stream);
+          if (rc != TPMLP_OK) return rc;
           return lib.fp4_matmul(K, N, T, format, xp, size(xt), yp, size(dyt),
                                 nullptr, TPMLP_FP32, dwp, N, place.stream);
         }),
@@ -796,12 +815,13 @@ PyObject* bind(PyObject* const* a) {
   l.fp4_bytes = reinterpret_cast<decltype(l.fp4_bytes)>(at(8));
   l.fp4_quantize = reinterpret_cast<decltype(l.fp4_quantize)>(at(9));
   l.fp4_colsum_bytes = reinterpret_cast<decltype(l.fp4_colsum_bytes)>(at(10));
-  l.fp4_dequantize = reinterpret_cast<decltype(l.fp4_dequantize)>(at(11));
-  l.fp4_matmul = reinterpret_cast<decltype(l.fp4_matmul)>(at(12));
-  l.fp4_linear = reinterpret_cast<decltype(l.fp4_linear)>(at(13));
+  l.fp4_quantize_both = reinterpret_cast<decltype(l.fp4_quantize_both)>(at(11));
+  l.fp4_dequantize = reinterpret_cast<decltype(l.fp4_dequantize)>(at(12));
+  l.fp4_matmul = reinterpret_cast<decltype(l.fp4_matmul)>(at(13));
+  l.fp4_linear = reinterpret_cast<decltype(l.fp4_linear)>(at(14));
   l.fp4_mlp_workspace_bytes =
-      reinterpret_cast<decltype(l.fp4_mlp_workspace_bytes)>(at(14));
-  l.fp4_mlp_forward = reinterpret_cast<decltype(l.fp4_mlp_forward)>(at(15));
+      reinterpret_cast<decltype(l.fp4_mlp_workspace_bytes)>(at(15));
+  l.fp4_mlp_forward = reinterpret_cast<decltype(l.fp4_mlp_forward)>(at(16));
   Py_INCREF(a[0]);
   l.check = a[0];
   Py_XDECREF(lib.check);
@@ -843,6 +863,7 @@ PyMethodDef methods[] = {
     {"fp4_linear", nullptr, 0, nullptr},
     {"fp4_backward", nullptr, 0, nullptr},
     {"fp4_mlp", nullptr, 0, nullptr},
+    {"fp4_quantize_both", nullptr, 0, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
@@ -861,7 +882,7 @@ void set(int i) {
 }  // namespace
 
 PyMODINIT_FUNC PyInit__pycall() {
-  set<bind, 16>(0);
+  set<bind, 17>(0);
   set<rope, 11>(1);
   set<norm_forward, 16>(2);
   set<norm_backward, 21>(3);
@@ -872,5 +893,6 @@ PyMODINIT_FUNC PyInit__pycall() {
   set<fp4_linear, 10>(8);
   set<fp4_backward, 9>(9);
   set<fp4_mlp, 14>(10);
+  set<fp4_quantize_both, 4>(11);
   return PyModule_Create(&module);
 }

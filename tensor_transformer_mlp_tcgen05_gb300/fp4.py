@@ -126,6 +126,17 @@ def quantize(x, format: str = "nvfp4", scale: "float | Fp4Tensor | None" = None,
             else Fp4Tensor(buffer, rows, cols, format))
 
 
+def quantize_both(x, format: str = "nvfp4", scale: float | None = None,
+                  stream=None) -> "tuple[Fp4Tensor, Fp4Tensor]":
+    """x [rows >= 1, cols] quantised along its rows, [rows, cols], and along its
+    columns, [cols, rows], in one pass: quantize(x) and quantize(x, transpose=True),
+    which share their g."""
+    r, t = B_.tensor_calls().fp4_quantize_both(x, _format(format), _scale(scale),
+                                               stream)
+    rows, cols = x.shape
+    return Fp4Tensor(r, rows, cols, format), Fp4Tensor(t, cols, rows, format)
+
+
 def matmul(a: Fp4Tensor, b: Fp4Tensor, bias=None, dtype=torch.bfloat16, out=None,
            stream=None) -> torch.Tensor:
     """a [T, K] times the transpose of b [N, K], plus bias [N] (fp32): [T, N],
@@ -149,8 +160,8 @@ class Fp4Linear:
         self.format, self._code = format, _format(format)
         self.inputs, self.outputs = W.shape
         self.bias = bias
-        self.weight = quantize(W, format, transpose=True)    # [N, K]
-        self.weight_rows = quantize(W, format)               # [K, N], for dx
+        # [K, N], for dx, and [N, K]
+        self.weight_rows, self.weight = quantize_both(W, format)
         self._calls = B_.tensor_calls()
 
     def forward(self, x, x_scale: float | None = 1.0, dtype=torch.bfloat16,

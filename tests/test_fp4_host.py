@@ -99,6 +99,31 @@ def test_quantize_refusals(code, kw):
     refused(code, lambda: quantize(**kw))
 
 
+def both(rows=100, cols=300, dtype=BF, x=X, stride=300, fmt=NV, scale=1.0, packed=P,
+         n=1 << 20, packed_t=P2, nt=1 << 20, colsum=None, ws=None, ws_bytes=0):
+    B.tp_fp4_quantize_both(rows, cols, dtype, x, stride, fmt, scale, packed, n,
+                           packed_t, nt, colsum, ws, ws_bytes, stream=0)
+
+
+@pytest.mark.parametrize("code,kw", [
+    (ARG, dict(fmt=7)), (ARG, dict(dtype=5)), (SHAPE, dict(rows=0)),
+    (SHAPE, dict(cols=0)), (SHAPE, dict(stride=299)), (ARG, dict(scale=3.0)),
+    (ARG, dict(fmt=MX, scale=2.0)), (ARG, dict(packed=None)),
+    (ARG, dict(packed_t=None)), (ALIGN, dict(packed=P + 16)),
+    (ALIGN, dict(packed_t=P2 + 16)), (WS, dict(n=100)), (WS, dict(nt=100)),
+    (ARG, dict(x=None)), (ALIGN, dict(x=X + 1)), (ARG, dict(packed=X)),
+    (ARG, dict(packed_t=X)), (ARG, dict(packed_t=P + 4096)),
+    (WS, dict(colsum=C, ws=W, ws_bytes=100)), (ARG, dict(colsum=C)),
+    (ARG, dict(colsum=P + 64, ws=W, ws_bytes=1 << 20)),
+    (ARG, dict(colsum=P2 + 64, ws=W, ws_bytes=1 << 20)),
+    (ARG, dict(colsum=C, ws=P + 64, ws_bytes=1 << 20)),
+    (SHAPE, dict(rows=1 << 28, cols=1 << 28, stride=1 << 28, x=1 << 60,
+                 packed=1 << 56, n=1 << 56, packed_t=1 << 58, nt=1 << 56)),
+])
+def test_quantize_both_refusals(code, kw):
+    refused(code, lambda: both(**kw))
+
+
 def test_calls_of_no_rows_touch_nothing():
     quantize(rows=0)
     quantize(rows=0, x=None, scale=0.0)

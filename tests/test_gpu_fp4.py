@@ -184,6 +184,37 @@ def test_scale_of_another_matrix():
         check_quantized(got, f64(y.t() if t else y), float(q.tensor_scale()))
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_both_ways_in_one_pass(fmt, dtype):
+    """quantize_both is quantize along the rows and along the columns, in memory
+    full of ones before; odd sizes, strides and alignments; g given or x's own."""
+    for rows, cols, off, pad in ((1, 1, 0, 0), (3, 16, 1, 0), (300, 70, 0, 2),
+                                 (129, 515, 3, 5), (1000, 257, 0, 0), (256, 256, 0, 0),
+                                 (700, 1100, 16, 16)):
+        buf = randn(rows * (cols + pad) + off, seed=rows, dtype=dtype)
+        x = buf[off:].view(rows, cols + pad)[:, :cols]
+        x[rows // 2, cols // 3] = (math.nan, 0.0, 3e4)[rows % 3]
+        for scale in (None, 4.0) if fmt == "nvfp4" else (None,):
+            torch.full((4 << 20,), 255, dtype=torch.uint8, device="cuda")
+            r, t = fp4.quantize_both(x, fmt, scale)
+            check_quantized(r, f64(x), scale)
+            check_quantized(t, f64(x.t()), scale)
+            assert r.check() == 0 and t.check() == 0
+    code = fp4._FORMATS[fmt]
+    x = randn(700, 130, dtype=dtype)   # with the sums of its columns
+    n, nt = B.tp_fp4_bytes(700, 130, code), B.tp_fp4_bytes(130, 700, code)
+    ws = B.tp_fp4_colsum_workspace_bytes(700, 130)
+    got = [torch.empty(k, dtype=torch.uint8, device="cuda")
+           for k in (n, nt, nt, 520, 520, ws)]
+    dt = B.TPMLP_BF16 if dtype == BF else B.TPMLP_FP32
+    B.tp_fp4_quantize_both(700, 130, dt, x, 130, code, 1.0, got[0], n, got[1], nt,
+                           got[3], got[5], ws)
+    B.tp_fp4_quantize(700, 130, dt, x, 130, 1, code, 1.0, None, got[2], nt, got[4],
+                      got[5], ws)
+    assert torch.equal(got[3], got[4])
+
+
 def test_column_sums():
     """The bias gradient of Fp4Linear.backward: 32 rows in order, 8 such sums, then
     256-row sums; each addition off by at most 2^-24 of the sum of magnitudes so
@@ -804,6 +835,9 @@ def test_refusals_on_tensors():
         lambda: fp4.quantize(x, out=fp4.quantize(x, "mxfp4")),
         lambda: fp4.quantize(x, out=fp4.quantize(randn(8, 32))),
         lambda: fp4.quantize(x[:0], transpose=True),
+        lambda: fp4.quantize_both(x[:0]),
+        lambda: fp4.quantize_both(x, "nvfp4", 0.0),
+        lambda: fp4.quantize_both(x.half()),
         lambda: fp4.matmul(q, fp4.quantize(randn(4, 32))),
         lambda: fp4.matmul(q, fp4.quantize(randn(4, 64), "mxfp4")),
         lambda: fp4.matmul(q, q, bias=randn(8)),
