@@ -27,6 +27,14 @@
 //             tile j - 1 and its part of tile j's shared columns.
 // Every wait is bounded, as in gemm_tc2.cu: on expiry TPMLP_ERR_TIMEOUT goes to
 // the status word, the roles stop and tensor memory is freed.
+//
+// Measured: 8192 x 15360 x 5120 187 us NV (6.9 PFLOP/s), 180 MX; 8192 x 5120 x 20480
+// 236 NV (7.3 PFLOP/s), 222 MX (7.7).  A k-tile's MMAs take 512 cycles.  With 12
+// pairs it takes 591: 38 KB are copied into shared memory and as much is read from
+// it, 594 cycles at 128 bytes each.  With all 76 it takes 690 at 2070 MHz (operands
+// of zeros: no power cap): L2, 17 TB/s.  Operands of random values run into the power
+// cap instead: at 1.6 GHz, after seconds of them, 622 cycles.  256 x 256 is the
+// largest tile whose accumulators leave tensor memory for the scales.
 #include <climits>
 
 #include "fp4_gemm.cuh"
@@ -78,7 +86,8 @@ __device__ __forceinline__ void cta_barrier() {
 
 // A unit of a pair's work: a tile, or 128 of its columns.  Where a last round of
 // tiles would leave half the pairs idle or more, its tiles are dealt out as
-// halves (8192 x 5120: 640 tiles, 8.42 rounds of 76, take 8.5 instead of 9).
+// halves (8192 x 5120 x 5120: 640 tiles, 8.42 rounds of 76, 66.5 us instead of 68.1;
+// 512 x 4096 x 4096: 32 tiles, 8.3 instead of 9.2).
 struct Item {
   int m0, n0;    // the pair's first row and column
   int cols;      // 256 or 128; 0: a half that lies past the matrix
@@ -112,7 +121,7 @@ __device__ __forceinline__ void add_bias(const float* bias, int c0, int n,
 
 // One warp's staging buffer: 32 rows of 128 bytes (16-byte unit u of row r at
 // unit u ^ r mod 8), written out by TMA, or, where the output's rows are not
-// 16-byte aligned, by the warp, row by row.
+// 16-byte aligned, by the warp, row by row (8192 x 5120 x 5120: 66 and 71 us).
 struct Stager {
   uint32_t buf;
   int lane;

@@ -145,16 +145,24 @@ int codes_map(CUtensorMap* m, const fp4::Packed& p, int box_rows) {
                    fp4::tiles_of(p.rows, p.cols) * fp4::TILE_ROWS, box_rows);
 }
 
-// Times in us (graph replays of one product in L2, NV), split against pairs:
-// 1 to 64 rows of A, 1024 to 20480 rows of B, K 1024 to 20480: 4.0 to 12.5 against
-// 5.4 to 23 (equal at 64 rows and K = 1024).  More rows: split pays where the
-// pairs have few tiles with long sums: K = 20480, 20 tiles (256 x 5120): 19.5
-// against 24.1, 32 tiles (512 x 4096): 26.4 against 24.6; K = 4096, 4 tiles (256 x
-// 1024): 8.8 against 9.1, 16 tiles (256 x 4096): 10.0 against 9.4.
+// Rows of A up to which the split kernel is the faster one.  Times in us (NV, one
+// product in L2, launches back to back), split against pairs:
+//   up to 32 rows (B of 1024 to 20480 rows, K 1024 to 20480): 2.9 to 40 against 4.1
+//     to 55;
+//   64 rows, K = 4096: 4.9 to 11.8 against 7.0 to 11.9; K = 1024: 4.5 to 8.1 against
+//     4.4 to 6.7;
+//   128 rows, 7 tiles of 256 x 256 and 16 k-tiles: 6.5 against 8.3; 16 tiles: 9.4
+//     against 7.4; 20 tiles and 80 k-tiles: 14.1 against 21.5;
+//   more: few tiles with long sums: 20 tiles (256 x 5120) and 80 k-tiles 19.0
+//     against 21.4, 32 tiles 24.3 against 21.8; 4 tiles and 16 k-tiles 8.1 against
+//     7.3.
 bool few(const fp4::ProductArgs& a) {
-  if (a.M <= 64) return true;
   const long long tiles = ((a.M + 255ll) / 256) * ((a.N + 255ll) / 256);
-  return 3 * tiles <= a.a.ktiles;
+  const int ktiles = a.a.ktiles;
+  if (a.M <= 32) return true;
+  if (a.M <= 64) return ktiles >= 8;
+  if (a.M <= 128) return ktiles >= 16 && 2 * tiles <= ktiles;
+  return ktiles >= 64 && 4 * tiles <= ktiles;
 }
 
 int product(HandleCore* core, const char* name, int format,

@@ -4,8 +4,15 @@
 //               element of bf16 (NV)
 //   transposed  the same, through shared memory: x is read along its rows, the
 //               codes of a column are consecutive
+//   both        one read for the two
 //   amax        the largest finite |x| of a matrix whose g is its own
 //   dequantise  the values, as bf16 or fp32
+//
+// Measured, 5120 x 20480 bf16 NV (268 MB of traffic, 39.7 us at the copy rate):
+// rows 42 us (6.4 TB/s), transposed 46 (5.8), dequantise 41 (6.5), amax 35 (6.0);
+// 8192 x 15360: both 87 us (4.5 TB/s) where the two took 111.  What is left: the
+// arithmetic (some 9 instructions an element one way, with 16 to 24 warps an SM to
+// hide loads behind).  Rows off a 32-byte boundary are in the comments below.
 #include "fp4_kernels.h"
 #include "fp4_load.cuh"
 
@@ -59,16 +66,26 @@ __global__ void __launch_bounds__(THREADS)
   const int col = kt * TILE_COLS + unit * 16;
   Raw<T> raw[PASSES];
   const T* src = x + row0 * stride + col;
-  if (LD != 0 && (chunk + 1) * 16 * PASSES <= p.rows &&
-      (kt + 1) * TILE_COLS <= p.cols) {
+  // (loads behind conditions wait for one another: whole tiles have none.  Any
+  // alignment: those but the matrix's first and last rows', whose pieces may pass
+  // its ends.)
+  bool inside = (chunk + 1) * 16 * PASSES <= p.rows && (kt + 1) * TILE_COLS <= p.cols;
+  if (LD == 0)
+    inside = inside && chunk > 0 && (chunk + 1) * 16 * PASSES < p.rows;
+  if (inside) {
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i)
-      load_words<LD == 0 ? 16 : LD>(src + 16 * i * stride, raw[i].w);
+    for (int i = 0; i < PASSES; ++i) {
+      if constexpr (LD == 0)
+        load_shifted(src + 16 * i * stride, raw[i].w);
+      else
+        load_words<LD>(src + 16 * i * stride, raw[i].w);
+    }
   } else {
+    const Extent e = extent_of(x, stride, p.rows, p.cols);
 #pragma unroll
     for (int i = 0; i < PASSES; ++i)
       load16<T, LD>(src + 16 * i * stride,
-                    row0 + 16 * i < p.rows ? p.cols - col : 0, raw[i]);
+                    row0 + 16 * i < p.rows ? p.cols - col : 0, e, raw[i]);
   }
   const float inv_g = inverse_g(p, gain);
 #pragma unroll
@@ -216,7 +233,8 @@ __device__ __forceinline__ void quantize_staged(const uint8_t* s_x, const Packed
 // two blocks of NV or one of MX.  Codes and scales go through shared memory,
 // so that a packed row's 128 bytes of codes are written together.
 // (three blocks an SM for bf16, 85 registers: 57 -> 47 us for 5120 x 20480; four
-// spill)
+// spill.  PAIR: a lane's two columns in one load; else, 8192 x 5120 takes 33 us
+// instead of 19.)
 // BOTH: the elements, read once, are quantised along the rows of x into rp too.
 template <class T, int FORMAT, bool PAIR, bool BOTH>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 3 : 2)
@@ -341,6 +359,7 @@ __global__ void __launch_bounds__(THREADS)
   wait_for_launch_before();
   let_next_launch_start();
   const long long segments = (cols + AMAX_UNITS * 16 - 1) / (AMAX_UNITS * 16);
+  const Extent e = extent_of(x, stride, rows, cols);
   uint32_t top = 0;
   for (long long item = blockIdx.x; item < rows * segments; item += gridDim.x) {
     const long long row = item / segments;
@@ -350,7 +369,7 @@ __global__ void __launch_bounds__(THREADS)
     for (int i = 0; i < 2; ++i) {
       const long long c = c0 + (i * THREADS + threadIdx.x) * 16ll;
       load16<T, LD>(x + row * stride + c,
-                    static_cast<int>(max(0ll, min(16ll, cols - c))), raw[i]);
+                    static_cast<int>(max(0ll, min(16ll, cols - c))), e, raw[i]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -378,45 +397,48 @@ __global__ void __launch_bounds__(THREADS)
 
 // ------------------------------------------------------------- dequantise --
 
-// wide: the bytes that a unit's place is a multiple of, at most 32.
+// A unit whose 32 bytes (fp32: 64) start on a 32-byte boundary.
 template <class T>
-__device__ __forceinline__ void store16(T* p, int n, int wide,
-                                        const float (&v)[16]) {
-  constexpr int WORDS = sizeof(T) * 4;
-  if (wide >= 16 && n >= 16) {
-    uint32_t w[WORDS];
+__device__ __forceinline__ void store_unit(T* p, const uint32_t (&w)[sizeof(T) * 4]) {
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      if constexpr (sizeof(T) == 2)
-        w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      else
-        w[i] = __float_as_uint(v[i]);
-    }
-    if (wide == 32) {
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                     reinterpret_cast<char*>(p) + 32 * i),
+                 "r"(w[8 * i]), "r"(w[8 * i + 1]), "r"(w[8 * i + 2]),
+                 "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
+                 "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                 : "memory");
+}
+
+// Elements 0 .. n - 1 (n <= 256) of a row piece in shared memory to p, by a warp, in
+// 16-byte pieces or words that are aligned in memory: of bf16 off a word's boundary
+// the first and the last element are stored alone.
+template <class T>
+__device__ __forceinline__ void store_row(T* p, int n, const uint8_t* s) {
+  const int lane = threadIdx.x & 31;
+  if (n == TILE_COLS && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
 #pragma unroll
-      for (int i = 0; i < WORDS / 8; ++i)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                         reinterpret_cast<char*>(p) + 32 * i),
-                     "r"(w[8 * i]), "r"(w[8 * i + 1]), "r"(w[8 * i + 2]),
-                     "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
-                     "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
-                     : "memory");
-    } else {
-#pragma unroll
-      for (int i = 0; i < WORDS / 4; ++i)
-        reinterpret_cast<uint4*>(p)[i] =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      reinterpret_cast<uint4*>(p)[32 * i + lane] =
+          reinterpret_cast<const uint4*>(s)[32 * i + lane];
     return;
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < n) {
-      if constexpr (sizeof(T) == 2)
-        p[i] = __float2bfloat16_rn(v[i]);
-      else
-        p[i] = v[i];
+  if constexpr (sizeof(T) == 4) {
+    for (int i = lane; i < n; i += 32)
+      reinterpret_cast<uint32_t*>(p)[i] = reinterpret_cast<const uint32_t*>(s)[i];
+  } else {
+    auto* out = reinterpret_cast<uint16_t*>(p);
+    const auto* in = reinterpret_cast<const uint16_t*>(s);
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1 & 1u);
+    const int words = (n - odd) / 2;
+    for (int i = lane; i < words; i += 32) {
+      const int k = 2 * i + odd;
+      *reinterpret_cast<uint32_t*>(out + k) =
+          in[k] | static_cast<uint32_t>(in[k + 1]) << 16;
     }
+    if (lane == 0 && odd) out[0] = in[0];
+    if (lane == 1 && odd + 2 * words < n) out[n - 1] = in[n - 1];
+  }
 }
 
 __device__ __forceinline__ void values8(uint32_t w, float scale, float* v) {
@@ -430,18 +452,21 @@ __device__ __forceinline__ void values8(uint32_t w, float scale, float* v) {
   }
 }
 
-template <class T, int FORMAT, int PASSES>
+// ALIGNED: every unit of 16 starts on a 32-byte boundary.  Otherwise, and in a last
+// k-tile, a warp's two rows go through shared memory (bf16 off its alignment: unit
+// by unit, 8192 x 5120 took 217 us).
+template <class T, int FORMAT, int PASSES, bool ALIGNED>
 __global__ void __launch_bounds__(THREADS)
-    dequantize_kernel(const Packed p, T* __restrict__ out, long long stride,
-                      int wide) {
+    dequantize_kernel(const Packed p, T* __restrict__ out, long long stride) {
   wait_for_launch_before();
   let_next_launch_start();
+  __shared__ __align__(16) uint8_t s_rows[THREADS / 16][TILE_COLS * sizeof(T)];
   const int unit = threadIdx.x & 15;
   const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.ktiles));
   const int chunk = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.ktiles));
   const int row0 = chunk * 16 * PASSES + static_cast<int>(threadIdx.x >> 4);
-  const int col = kt * TILE_COLS + unit * 16;
-  if (col >= p.cols) return;
+  const int cols = min(TILE_COLS, p.cols - kt * TILE_COLS);   // of this k-tile
+  const bool direct = ALIGNED && cols == TILE_COLS;
   const float g = p.head->g;
   uint2 c[PASSES];
   uint32_t byte[PASSES];
@@ -466,7 +491,34 @@ __global__ void __launch_bounds__(THREADS)
     values8(c[i].y, s, v + 8);
 #pragma unroll
     for (int k = 0; k < 16; ++k) v[k] *= g;
-    if (row < p.rows) store16(out + row * stride + col, p.cols - col, wide, v);
+    constexpr int WORDS = sizeof(T) * 4;
+    uint32_t w[WORDS];
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k) {
+      if constexpr (sizeof(T) == 2)
+        w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+      else
+        w[k] = __float_as_uint(v[k]);
+    }
+    T* to = out + row * stride + kt * TILE_COLS;
+    if (direct) {
+      if (row < p.rows) store_unit(to + unit * 16, w);
+      continue;
+    }
+    const int own = threadIdx.x >> 4;
+#pragma unroll
+    for (int k = 0; k < WORDS / 4; ++k)
+      *reinterpret_cast<uint4*>(&s_rows[own][unit * 16 * sizeof(T) + 16 * k]) =
+          make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // the warp's rows
+      const int r = (own & ~1) + h;
+      const int at = chunk * 16 * PASSES + 16 * i + r;
+      if (at < p.rows)
+        store_row(out + at * stride + kt * TILE_COLS, cols, s_rows[r]);
+    }
+    __syncwarp();
   }
 }
 
@@ -477,7 +529,8 @@ bool on_boundary(const void* p, long long stride_bytes, int bytes) {
              bytes == 0;
 }
 
-// Blocks that keep all SMs busy: with fewer, a block takes fewer rows.
+// Blocks that keep all SMs busy: with fewer, a block takes 16 rows, not 64 (1003 x
+// 1000: 1.8 us, not 3.1; 1024 x 4096 2.8 and 2.7; 8192 x 5120 19.2 and 16.9).
 constexpr long long FULL_GRID = 152 * 4;
 
 template <class... P, class... A>
@@ -572,11 +625,13 @@ cudaError_t dequantize_type(const Packed& p, int format, T* out, long long strid
   const unsigned grid = static_cast<unsigned>(
       (p.rows + 16ll * PASSES - 1) / (16 * PASSES) * p.ktiles);
   const long long bytes = stride * static_cast<long long>(sizeof(T));
-  const int wide =
-      on_boundary(out, bytes, 32) ? 32 : on_boundary(out, bytes, 16) ? 16 : 0;
-  return launch(format == TPFP4_NV ? dequantize_kernel<T, TPFP4_NV, PASSES>
-                                   : dequantize_kernel<T, TPFP4_MX, PASSES>,
-                grid, 0, s, p, out, stride, wide);
+  const bool aligned = on_boundary(out, bytes, 32);
+  auto kernel = format == TPFP4_NV
+                    ? (aligned ? dequantize_kernel<T, TPFP4_NV, PASSES, true>
+                               : dequantize_kernel<T, TPFP4_NV, PASSES, false>)
+                    : (aligned ? dequantize_kernel<T, TPFP4_MX, PASSES, true>
+                               : dequantize_kernel<T, TPFP4_MX, PASSES, false>);
+  return launch(kernel, grid, 0, s, p, out, stride);
 }
 
 }  // namespace

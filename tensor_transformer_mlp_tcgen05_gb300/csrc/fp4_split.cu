@@ -7,6 +7,8 @@ namespace {
 
 using namespace split;
 
+// Columns of the MMA, and with them A's share of a stage, by A's rows (128 columns
+// for 8 rows: 8 x 5120 x 20480 in L2 9.7 us, not 7.8; for 64: 11.7, not 10.7).
 template <int FORMAT, int EPI>
 cudaError_t launch_epilogue(const ProductArgs& args, int sms, cudaStream_t s) {
   if (args.M <= 16) return launch_tokens<FORMAT, EPI, 16, PACKED>(args, sms, s);

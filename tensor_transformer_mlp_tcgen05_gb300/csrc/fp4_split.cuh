@@ -10,6 +10,11 @@
 // barrier the CTAs add up, row by row of A and in the CTAs' order, the partial
 // sums.  One launch, no workspace, a fixed order.  Up to 4 rows of A may come as
 // they are: four more warps quantise them (every CTA those of its range of K).
+//
+// Measured (NV, B not in L2, launches back to back): 1 x 4096 x 1024 3.5 us, 32 x
+// 5120 x 20480 13.3 us (59 MB, 8.7 us at the copy rate), 32 x 20480 x 20480 42.6 us
+// (236 MB, 5.5 TB/s).  Bound by the read of B and, below 100 MB, by some 4 us of
+// launch, first loads, the cluster's barrier and the joint sums.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -35,7 +40,8 @@ struct Shape {
   static constexpr uint32_t TILE = tile_bytes(FORMAT);
   static constexpr uint32_t B_BYTES = FM * 128, A_BYTES = NT * 128;
   static constexpr uint32_t STAGE = B_BYTES + A_BYTES + 2 * TILE;
-  static constexpr uint32_t BUDGET = 108 * 1024;   // two CTAs an SM
+  // two CTAs an SM (one with twice the stages: 32 x 5120 x 20480 18.1 us, not 13.3)
+  static constexpr uint32_t BUDGET = 108 * 1024;
   static constexpr int STAGES = BUDGET / STAGE < 6 ? BUDGET / STAGE : 6;
   static constexpr int NUM_BARRIERS = 2 * STAGES + 1;
   static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE +
@@ -166,6 +172,7 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, int k_lo,
                      static_cast<uintptr_t>(a.x_stride * sizeof(T))) % 16 == 0;
   const T* src = static_cast<const T*>(a.x) + row0 * a.x_stride + unit * 16;
   const float inv_g = exp2_of(-a.x_exponent);
+  const Extent e = extent_of(static_cast<const T*>(a.x), a.x_stride, a.M, a.a.cols);
   auto load = [&](int i, Raw<T> (&raw)[2]) {
     const int col = (k_lo + i) * TILE_COLS;
 #pragma unroll
@@ -174,9 +181,9 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, int k_lo,
       const T* p = src + 2 * j * a.x_stride + col;
       const int n = row0 + 2 * j < a.M ? a.a.cols - col - unit * 16 : 0;
       if (wide)
-        load16<T, 16>(p, n, raw[j]);
+        load16<T, 16>(p, n, e, raw[j]);
       else
-        load16<T, 0>(p, n, raw[j]);
+        load16<T, 0>(p, n, e, raw[j]);
     }
   };
   auto store = [&](uint32_t stage, const Raw<T> (&raw)[2]) {
@@ -413,6 +420,8 @@ __global__ void __launch_bounds__(threads_of(SRC), 2)
   ptx::cluster_sync();   // no CTA leaves while its sums are being read
 }
 
+// (K split over clusters, not at all: 32 x 5120 x 20480 13.3 us and 25.4, 8 x 20480 x
+// 5120, whose 160 CTAs fill the SMs, 13.3 and 13.1.)
 // Clusters of `size` CTAs that fit at once, two CTAs to an SM, when a cluster's
 // SMs come from one of eight groups of at least sms / 9.  (A rule on the SM
 // count alone, so that the order of the sums, and with it the last bits, is the

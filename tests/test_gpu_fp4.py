@@ -174,6 +174,37 @@ def test_strides_and_alignment(fmt, dtype, off, pad):
     assert (view[:, cols:] == 7).all() and (out[:off] == 7).all()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols", [(70, 515), (2500, 4099)])
+def test_any_alignment_is_the_same(fmt, dtype, rows, cols):
+    """Rows that start on every boundary (an odd stride, and every first element of
+    a 32-byte piece): the same codes and the same values as of an aligned copy."""
+    wide = -(-cols // 16) * 16
+    x = torch.zeros(rows, wide, dtype=dtype, device="cuda")[:, :cols]
+    x.copy_(randn(rows, cols, seed=cols, dtype=dtype))
+    x[0, 0], x[-1, -1] = 1e3, -2e3
+    auto = fp4.quantize(x, fmt)
+    want = auto.codes(), auto.scales(), auto.dequantize(dtype)
+    for off in range(0, 32 // x.element_size(), 1 if rows < 100 else 5):
+        # (the view ends where its memory does)
+        buf = torch.full((off + rows * (cols + 2) - 2,), math.nan, dtype=dtype,
+                         device="cuda")
+        y = buf.as_strided((rows, cols), (cols + 2, 1), off)
+        y.copy_(x)
+        q = fp4.quantize(y, fmt)
+        r, t = fp4.quantize_both(y, fmt)
+        for p in (q, r):
+            assert float(p.tensor_scale()) == float(auto.tensor_scale())
+            assert torch.equal(p.codes(), want[0]) and torch.equal(p.scales(), want[1])
+        assert torch.equal(t.dequantize(F32), fp4.quantize(x, fmt, transpose=True)
+                           .dequantize(F32))
+        buf.fill_(7.0)
+        assert torch.equal(q.dequantize(dtype, out=y), want[2])
+        y.fill_(7.0)
+        assert (buf == 7).all()   # nothing beside the rows
+
+
 def test_scale_of_another_matrix():
     """g taken from a packed matrix on the device: codes as with that power of
     two given."""
