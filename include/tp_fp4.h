@@ -84,7 +84,7 @@ long long tp_fp4_offset(long long rows, long long cols, int format, int which);
  *            order; transpose = 1 only), or NULL
  *   workspace  tp_fp4_colsum_workspace_bytes(rows, cols) bytes, 16-byte
  *            aligned, used only with colsum
- * rows = 0 (transpose = 0) enqueues nothing. */
+ * rows = 0 (transpose = 0) enqueues nothing, and leaves the header as it is. */
 int tp_fp4_quantize(long long rows, long long cols, int dtype, const void* x,
                     long long row_stride, int transpose, int format,
                     double scale, const void* like, void* packed,
@@ -108,27 +108,29 @@ int tp_fp4_dequantize(long long rows, long long cols, int format,
                       void* out, long long row_stride, void* stream);
 
 /* C [T, N] (`dtype`, row stride ldc) from packed A [T, K] and B [N, K].  bias
- * [N] fp32 or NULL.  T = 0 enqueues nothing. */
+ * [N] fp32 or NULL.  status: 16 bytes that the caller zeroed, where the first error
+ * of all calls that are given them stays until tp_fp4_check, or NULL for A's status
+ * word.  T = 0 enqueues nothing. */
 int tp_fp4_matmul(long long T, long long N, long long K, int format,
                   const void* A, size_t a_bytes, const void* B, size_t b_bytes,
                   const float* bias, int dtype, void* C, long long ldc,
-                  void* stream);
+                  void* status, void* stream);
 
 /* Both in one call, for a layer y = x W: x [T, K] (x_dtype, x_stride) quantised
  * (x_scale as tp_fp4_quantize's scale) times the packed W [N, K].  xq is scratch of
- * tp_fp4_bytes(T, K, format) bytes; its status word is the call's.  The product
+ * tp_fp4_bytes(T, K, format) bytes; status as above (NULL: xq's).  The product
  * starts to load W while x is quantised, and up to 4 rows with a given x_scale
  * are quantised by the product itself.  xq and C share no memory with the rest. */
 int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
                   const void* x, long long x_stride, int format, double x_scale,
                   void* xq, size_t xq_bytes, const void* W, size_t w_bytes,
                   const float* bias, int dtype, void* C, long long ldc,
-                  void* stream);
+                  void* status, void* stream);
 
-/* Waits for `stream`, then reads and clears the status word of a packed matrix
- * that products read as A: TPMLP_OK, TPMLP_ERR_TIMEOUT (a bounded device wait
+/* Waits for `stream`, then reads and clears a status word: that of a packed matrix
+ * that products read as A, or one given to the calls: TPMLP_OK, TPMLP_ERR_TIMEOUT (a bounded device wait
  * gave up; that product's C is undefined) or TPMLP_ERR_CUDA. */
-int tp_fp4_check(void* packed, void* stream);
+int tp_fp4_check(void* status, void* stream);
 
 /* ---- the MLP block's forward on four-bit weights ------------------------
  *   Xq = quantised Xn (= LayerNorm(X) rounded to bf16, or X), H = Xq Aq + b1,

@@ -344,10 +344,10 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.tp_fp4_dequantize.argtypes = [ll, ll, _i, _vp, _sz, _i, _vp, ll, _vp]
     L.tp_fp4_dequantize.restype = _i
     L.tp_fp4_matmul.argtypes = [ll, ll, ll, _i, _vp, _sz, _vp, _sz, _vp, _i,
-                                _vp, ll, _vp]
+                                _vp, ll, _vp, _vp]
     L.tp_fp4_matmul.restype = _i
     L.tp_fp4_linear.argtypes = [ll, ll, ll, _i, _vp, ll, _i, dbl, _vp, _sz,
-                                _vp, _sz, _vp, _i, _vp, ll, _vp]
+                                _vp, _sz, _vp, _i, _vp, ll, _vp, _vp]
     L.tp_fp4_linear.restype = _i
     L.tp_fp4_check.argtypes = [_vp, _vp]
     L.tp_fp4_check.restype = _i
@@ -854,22 +854,22 @@ def tp_fp4_dequantize(rows, cols, format, packed, packed_bytes, dtype, out,
 
 
 def tp_fp4_matmul(T, N, K, format, A, a_bytes, B, b_bytes, bias, dtype, C, ldc,
-                  stream=None):
+                  status=None, stream=None):
     _check(lib().tp_fp4_matmul(
         T, N, K, format, _ptr(A), a_bytes, _ptr(B), b_bytes, _ptr(bias), dtype,
-        _ptr(C), ldc, _stream(stream)), "tp_fp4_matmul")
+        _ptr(C), ldc, _ptr(status), _stream(stream)), "tp_fp4_matmul")
 
 
 def tp_fp4_linear(T, N, K, x_dtype, x, x_stride, format, x_scale, xq, xq_bytes,
-                  W, w_bytes, bias, dtype, C, ldc, stream=None):
+                  W, w_bytes, bias, dtype, C, ldc, status=None, stream=None):
     _check(lib().tp_fp4_linear(
         T, N, K, x_dtype, _ptr(x), x_stride, format, x_scale, _ptr(xq), xq_bytes,
-        _ptr(W), w_bytes, _ptr(bias), dtype, _ptr(C), ldc, _stream(stream)),
-        "tp_fp4_linear")
+        _ptr(W), w_bytes, _ptr(bias), dtype, _ptr(C), ldc, _ptr(status),
+        _stream(stream)), "tp_fp4_linear")
 
 
-def tp_fp4_check(packed, stream=None) -> int:
-    return int(lib().tp_fp4_check(_ptr(packed), _stream(stream)))
+def tp_fp4_check(status, stream=None) -> int:
+    return int(lib().tp_fp4_check(_ptr(status), _stream(stream)))
 
 
 def tp_fp4_mlp_weights_bytes(handle, format: int) -> int:

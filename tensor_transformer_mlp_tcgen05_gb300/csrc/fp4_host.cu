@@ -275,7 +275,7 @@ int check_quantize(long long rows, long long cols, int dtype, const void* x,
 // tp_fp4_matmul's arguments.
 int check_matmul(long long T, long long N, long long K, int format, const void* A,
                  size_t a_bytes, const void* B, size_t b_bytes, const float* bias,
-                 int dtype, const void* C, long long ldc) {
+                 int dtype, const void* C, long long ldc, const void* status) {
   if (!format_ok(format)) return bad(TPMLP_ERR_ARG, "fp4: unknown format");
   TRY(dtype_ok(dtype));
   if (T < 0 || T > MAX_DIM || !dim_ok(N) || !dim_ok(K))
@@ -287,9 +287,13 @@ int check_matmul(long long T, long long N, long long K, int format, const void* 
   if (T == 0) return TPMLP_OK;
   if (C == nullptr) return bad(TPMLP_ERR_ARG, "fp4: C is null");
   const size_t es = dtype == TPMLP_BF16 ? 2 : 4;
-  if (!aligned(C, es) || !aligned(bias, 4))
-    return bad(TPMLP_ERR_ALIGN, "fp4: C or bias off its alignment");
+  if (!aligned(C, es) || !aligned(bias, 4) || !aligned(status, 16))
+    return bad(TPMLP_ERR_ALIGN, "fp4: C, bias or status off its alignment");
   const size_t nc = extent(T, N, ldc, es);
+  if (overlap(status, 16, C, nc) || overlap(status, 16, bias, size_t(N) * 4) ||
+      overlap(status, 16, A, fp4::packed_bytes(T, K, format)) ||
+      overlap(status, 16, B, fp4::packed_bytes(N, K, format)))
+    return bad(TPMLP_ERR_ARG, "fp4: status overlaps another buffer");
   if (overlap(C, nc, A, fp4::packed_bytes(T, K, format)) ||
       overlap(C, nc, B, fp4::packed_bytes(N, K, format)) ||
       overlap(C, nc, bias, static_cast<size_t>(N) * 4))
@@ -457,14 +461,15 @@ int tp_fp4_dequantize(long long rows, long long cols, int format,
 int tp_fp4_matmul(long long T, long long N, long long K, int format,
                   const void* A, size_t a_bytes, const void* B, size_t b_bytes,
                   const float* bias, int dtype, void* C, long long ldc,
-                  void* stream) {
-  TRY(check_matmul(T, N, K, format, A, a_bytes, B, b_bytes, bias, dtype, C, ldc));
+                  void* status, void* stream) {
+  TRY(check_matmul(T, N, K, format, A, a_bytes, B, b_bytes, bias, dtype, C, ldc,
+                   status));
   if (T == 0) return TPMLP_OK;
   int sms = 0;
   TRY(check_device(&sms));
   fp4::ProductArgs a = matmul_args(T, N, K, B, bias, dtype, C, ldc);
   a.a = fp4::view(A, T, K);
-  a.status = a.a.head->status;
+  a.status = status != nullptr ? static_cast<int*>(status) : a.a.head->status;
   return product(nullptr, "fp4_matmul", format, a, sms,
                  static_cast<cudaStream_t>(stream));
 }
@@ -473,11 +478,12 @@ int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
                   const void* x, long long x_stride, int format, double x_scale,
                   void* xq, size_t xq_bytes, const void* W, size_t w_bytes,
                   const float* bias, int dtype, void* C, long long ldc,
-                  void* stream) {
+                  void* status, void* stream) {
   int exponent = 0;
   TRY(check_quantize(T, K, x_dtype, x, x_stride, 0, format, x_scale, nullptr,
                      xq, xq_bytes, nullptr, nullptr, 0, &exponent));
-  TRY(check_matmul(T, N, K, format, xq, xq_bytes, W, w_bytes, bias, dtype, C, ldc));
+  TRY(check_matmul(T, N, K, format, xq, xq_bytes, W, w_bytes, bias, dtype, C, ldc,
+                   status));
   if (T == 0) return TPMLP_OK;
   const size_t nx = extent(T, K, x_stride, x_dtype == TPMLP_BF16 ? 2 : 4);
   const size_t nq = fp4::packed_bytes(T, K, format);
@@ -491,12 +497,13 @@ int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
   fp4::ProductArgs a = matmul_args(T, N, K, W, bias, dtype, C, ldc);
   TRY(left_operand(nullptr, "fp4_quantize", T, K, x_dtype == TPMLP_BF16, x,
                    x_stride, format, exponent, xq, &a, s));
+  if (status != nullptr) a.status = static_cast<int*>(status);
   return product(nullptr, "fp4_matmul", format, a, sms, s);
 }
 
-int tp_fp4_check(void* packed, void* stream) {
-  if (packed == nullptr) return TPMLP_ERR_ARG;
-  return check_status(packed, static_cast<cudaStream_t>(stream));
+int tp_fp4_check(void* status, void* stream) {
+  if (status == nullptr) return TPMLP_ERR_ARG;
+  return check_status(status, static_cast<cudaStream_t>(stream));
 }
 
 size_t tp_fp4_mlp_weights_bytes(const tp_mlp_handle* H, int format) {

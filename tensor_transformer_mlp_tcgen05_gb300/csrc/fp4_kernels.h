@@ -52,7 +52,7 @@ struct ProductArgs {
   int M, N;
   // instead of a's codes, scales and g: the plain matrix x that the product
   // quantises itself, g = 2^x_exponent (M <= PLAIN_ROWS; a then has its sizes, and
-  // the status word is cleared by the product); or null
+  // a's status word is cleared by the product); or null
   const void* x;
   int x_bf16;
   long long x_stride;

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(threads_of(SRC), 2)
     let_next_launch_start();
   }
   if (SRC != PACKED && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 4)
-    args.status[threadIdx.x] = 0;
+    args.a.head->status[threadIdx.x] = 0;
 
   if (warp == 0) {
     // ------------------------------------------------------ producer --

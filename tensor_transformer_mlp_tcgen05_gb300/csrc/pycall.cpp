@@ -640,14 +640,23 @@ PyObject* fp4_matmul(PyObject* const* a) {
   void* op = T == 0 ? nullptr : out.data_ptr();
   check(without_gil([&] {
           return lib.fp4_matmul(T, N, K, format, ap, na, bp, nb, bias, dtype, op,
-                                row_stride(out), place.stream);
+                                row_stride(out), nullptr, place.stream);
         }),
         "tp_fp4_matmul");
   return wrapped(out);
 }
 
-// fp4_linear(x, b, N, K, format, scale, bias, dtype, out, stream) -> C: x [T, K]
-// quantised and multiplied, in one call.
+// The four words of a layer's status.
+void* status_of(PyObject* o, const at::Device& dev) {
+  const at::Tensor& t = tensor("status", o);
+  if (t.scalar_type() != at::kInt || t.numel() != 4 || !t.is_contiguous() ||
+      t.device() != dev)
+    throw Refused{"the layer and its input differ in device"};
+  return t.data_ptr();
+}
+
+// fp4_linear(x, b, N, K, format, scale, bias, dtype, out, status, stream) -> C:
+// x [T, K] quantised and multiplied, in one call.
 PyObject* fp4_linear(PyObject* const* a) {
   const Matrix x("x", tensor("x", a[0]));
   const at::Tensor& pb = tensor("weight", a[1]);
@@ -661,7 +670,8 @@ PyObject* fp4_linear(PyObject* const* a) {
   const size_t nb = packed_of("weight", pb, N, K, format, dev);
   const float* bias = bias_of(a[6], N, dev);
   plain_type(dtype);
-  const Place place(dev, a[9]);
+  void* status = status_of(a[9], dev);
+  const Place place(dev, a[10]);
   const at::Tensor out = plain_out(a[8], x.rows, N, dtype, dev);
   const at::Tensor q = new_packed(x.rows, K, format, dev);
   void* qp = q.data_ptr();
@@ -671,14 +681,14 @@ PyObject* fp4_linear(PyObject* const* a) {
   check(without_gil([&] {
           return lib.fp4_linear(x.rows, N, K, x.dtype, x.data(), x.stride, format,
                                 scale, qp, nq, bp, nb, bias, dtype, op,
-                                row_stride(out), place.stream);
+                                row_stride(out), status, place.stream);
         }),
         "tp_fp4_linear");
   return wrapped(out);
 }
 
 // fp4_backward(dy, x, weight_rows, format, dy_scale, x_scale, dtype, bias_grad,
-//              stream) -> (dx, dw, db or None): the gradients of fp4_linear, for
+//              status, stream) -> (dx, dw, db or None): the gradients of fp4_linear, for
 // at least one token; weight_rows is W [K, N] packed along N.
 PyObject* fp4_backward(PyObject* const* a) {
   const Matrix dy("dy", tensor("dy", a[0])), x("x", tensor("x", a[1]));
@@ -694,7 +704,8 @@ PyObject* fp4_backward(PyObject* const* a) {
     throw Refused{"dy and x differ in tokens or device: " + shown(dy.t) + ", " +
                   shown(x.t)};
   const size_t nw = packed_of("weight_rows", w, K, N, format, dev);
-  const Place place(dev, a[8]);
+  void* status = status_of(a[8], dev);
+  const Place place(dev, a[9]);
   const at::Tensor dx = make({T, K}, plain_type(dtype), dev);
   const at::Tensor dw = make({K, N}, at::kFloat, dev);
   at::Tensor db, ws;
@@ -728,10 +739,10 @@ PyObject* fp4_backward(PyObject* const* a) {
           if (rc != TPMLP_OK) return rc;
           what = "tp_fp4_matmul";
           rc = lib.fp4_matmul(T, K, N, format, qp, size(q), wp, nw, nullptr, dtype,
-                              dxp, K, place.stream);
+                              dxp, K, status, place.stream);
           if (rc != TPMLP_OK) return rc;
           return lib.fp4_matmul(K, N, T, format, xp, size(xt), yp, size(dyt),
-                                nullptr, TPMLP_FP32, dwp, N, place.stream);
+                                nullptr, TPMLP_FP32, dwp, N, status, place.stream);
         }),
         what);
   return tuple_of({dx, dw, db});
@@ -890,8 +901,8 @@ PyMODINIT_FUNC PyInit__pycall() {
   set<fp4_quantize, 7>(5);
   set<fp4_dequantize, 7>(6);
   set<fp4_matmul, 10>(7);
-  set<fp4_linear, 10>(8);
-  set<fp4_backward, 9>(9);
+  set<fp4_linear, 11>(8);
+  set<fp4_backward, 10>(9);
   set<fp4_mlp, 14>(10);
   set<fp4_quantize_both, 4>(11);
   return PyModule_Create(&module);

@@ -93,6 +93,8 @@ class Fp4Tensor:
     def check(self, stream=None) -> int:
         """Synchronise and return the status of the products that read this
         matrix as ``a`` (TPMLP_OK or an error)."""
+        if self.rows == 0:   # (nothing was written)
+            return B_.TPMLP_OK
         with torch.cuda.device(self.buffer.device):
             return B_.tp_fp4_check(self.buffer, stream)
 
@@ -162,7 +164,14 @@ class Fp4Linear:
         self.bias = bias
         # [K, N], for dx, and [N, K]
         self.weight_rows, self.weight = quantize_both(W, format)
+        self._status = torch.zeros(4, dtype=torch.int32, device=W.device)
         self._calls = B_.tensor_calls()
+
+    def check(self, stream=None) -> int:
+        """Synchronise and return the first error of the calls so far, then forget
+        it (TPMLP_OK or an error)."""
+        with torch.cuda.device(self._status.device):
+            return B_.tp_fp4_check(self._status, stream)
 
     def forward(self, x, x_scale: float | None = 1.0, dtype=torch.bfloat16,
                 out=None, stream=None) -> torch.Tensor:
@@ -170,7 +179,7 @@ class Fp4Linear:
         to take it from x."""
         return self._calls.fp4_linear(
             x, self.weight.buffer, self.outputs, self.inputs, self._code,
-            _scale(x_scale), self.bias, _dtype(dtype), out, stream)
+            _scale(x_scale), self.bias, _dtype(dtype), out, self._status, stream)
 
     def backward(self, dy, x, x_scale: float | None = 1.0,
                  dy_scale: float | None = None, dtype=torch.bfloat16,
@@ -187,11 +196,12 @@ class Fp4Linear:
         if dy.shape[0] == 0:
             dx = calls.fp4_linear(dy, self.weight_rows.buffer, self.inputs,
                                   self.outputs, code, 1.0, None, _dtype(dtype),
-                                  None, stream)
+                                  None, self._status, stream)
             dw = dy.new_zeros((self.inputs, self.outputs), dtype=torch.float32)
             db = dy.new_zeros(self.outputs, dtype=torch.float32)
             return {"dx": dx, "dw": dw, "db": db if bias_grad else None}
         dx, dw, db = calls.fp4_backward(dy, x, self.weight_rows.buffer, code,
                                         _scale(dy_scale), _scale(x_scale),
-                                        _dtype(dtype), bias_grad, stream)
+                                        _dtype(dtype), bias_grad, self._status,
+                                        stream)
         return {"dx": dx, "dw": dw, "db": db}

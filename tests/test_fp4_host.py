@@ -144,10 +144,10 @@ def test_dequantize_refusals(code, a):
 
 
 def matmul(T=20, N=30, K=100, fmt=NV, A=P, na=None, Bp=P2, nb=None, bias=None,
-           dtype=BF, C=C, ldc=30):
+           dtype=BF, C=C, ldc=30, st=None):
     na = B.tp_fp4_bytes(max(T, 0), K, fmt) if na is None else na
     nb = B.tp_fp4_bytes(N, K, fmt) if nb is None else nb
-    B.tp_fp4_matmul(T, N, K, fmt, A, na, Bp, nb, bias, dtype, C, ldc, stream=0)
+    B.tp_fp4_matmul(T, N, K, fmt, A, na, Bp, nb, bias, dtype, C, ldc, st, stream=0)
 
 
 @pytest.mark.parametrize("code,kw", [
@@ -159,7 +159,8 @@ def matmul(T=20, N=30, K=100, fmt=NV, A=P, na=None, Bp=P2, nb=None, bias=None,
     (WS, dict(na=10)), (WS, dict(nb=10)), (ARG, dict(C=None)),
     (ALIGN, dict(C=C + 1)), (ALIGN, dict(C=C + 2, dtype=F32)),
     (ALIGN, dict(bias=W + 2)), (ARG, dict(C=P + 256)), (ARG, dict(C=P2 + 512)),
-    (ARG, dict(bias=C + 8)),
+    (ARG, dict(bias=C + 8)), (ALIGN, dict(st=W + 8)), (ARG, dict(st=C + 32)),
+    (ARG, dict(st=P)), (ARG, dict(st=P2 + 64)), (ARG, dict(st=W, bias=W)),
     (SHAPE, dict(T=1 << 28, N=1 << 28, K=1, na=1 << 50, nb=1 << 50, ldc=1 << 28,
                  A=1 << 50, Bp=1 << 53, C=1 << 59)),
     (SHAPE, dict(T=1 << 28, K=1 << 28, na=1 << 60, nb=1 << 60, A=1 << 57,
@@ -170,9 +171,9 @@ def test_matmul_refusals(code, kw):
 
 
 def linear(T=20, N=30, K=100, xd=BF, x=X, xs=100, fmt=NV, scale=1.0, xq=P,
-           nq=1 << 20, Wp=P2, nw=1 << 20, bias=None, dtype=BF, C=C, ldc=30):
+           nq=1 << 20, Wp=P2, nw=1 << 20, bias=None, dtype=BF, C=C, ldc=30, st=None):
     B.tp_fp4_linear(T, N, K, xd, x, xs, fmt, scale, xq, nq, Wp, nw, bias, dtype, C,
-                    ldc, stream=0)
+                    ldc, st, stream=0)
 
 
 @pytest.mark.parametrize("code,kw", [
@@ -184,7 +185,8 @@ def linear(T=20, N=30, K=100, xd=BF, x=X, xs=100, fmt=NV, scale=1.0, xq=P,
     (ALIGN, dict(Wp=P2 + 16)), (WS, dict(nq=100)), (WS, dict(nw=100)),
     (ARG, dict(xq=X)), (ARG, dict(xq=P2)), (ARG, dict(C=X + 100)),
     (ARG, dict(C=P + 1024)), (ARG, dict(C=P2 + 1024)), (ARG, dict(bias=C + 4)),
-    (ARG, dict(bias=P + 1024)),
+    (ARG, dict(bias=P + 1024)), (ALIGN, dict(st=W + 4)), (ARG, dict(st=C)),
+    (ARG, dict(st=P + 16)),
 ])
 def test_linear_refusals(code, kw):
     refused(code, lambda: linear(**kw))

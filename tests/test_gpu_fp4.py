@@ -288,7 +288,8 @@ def operands(T, N, K, fmt, seed=0, dtype=BF):
 @pytest.mark.parametrize("T,N,K", [(5, 128, 256), (1, 1, 1), (16, 64, 512),
                                    (17, 100, 300), (33, 129, 1000), (1, 4096, 1024),
                                    (65, 257, 33), (128, 640, 2048), (200, 300, 4096),
-                                   (8, 1280, 5120)])
+                                   (8, 1280, 5120), (64, 257, 2100), (128, 600, 4200),
+                                   (300, 700, 16500)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_product_of_few_rows(fmt, T, N, K, dtype):
     a, b, va, vb = operands(T, N, K, fmt, seed=T + N)
@@ -540,6 +541,9 @@ def test_no_tokens():
     assert g["dx"].shape == (0, 64) and g["dx"].dtype == BF
     assert g["dw"].shape == (64, 48) and not g["dw"].any() and not g["db"].any()
     assert fp4.quantize(x).dequantize().shape == (0, 64)
+    q = fp4.quantize(x)
+    assert fp4.matmul(q, lin.weight).shape == (0, 48)
+    assert q.check() == 0 and lin.check() == 0
 
 
 # -------------------------------------------------------------- MLP block --
@@ -592,7 +596,9 @@ def check_block(m, Z, X, Xn, A, Bw, b1, b2, fmt, gelu="erf", residual=False):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,h,f,t", [(1, 64, 64, 1), (8, 128, 512, 2),
-                                     (4, 256, 1088, 1), (33, 192, 320, 1), (130, 256, 1088, 1),
+                                     (4, 256, 1088, 1), (33, 192, 320, 1),
+                                     (50, 2048, 320, 1), (100, 4096, 576, 1),
+                                     (130, 256, 1088, 1),
                                      (300, 320, 640, 2), (700, 512, 2048, 4),
                                      (2500, 256, 4160, 1)])
 @pytest.mark.parametrize("gelu", ["erf", "tanh"])
@@ -699,6 +705,21 @@ def test_wait_timeout_is_reported_and_context_survives(fmt, T, h, f):
     B.tp_mlp_set_wait_budget(m.handle, 2_000_000_000)
     assert torch.equal(m.forward_fp4(X, p, b1, b2), want)
     assert m.check() == B.TPMLP_OK
+
+
+def test_a_layer_keeps_its_first_error_until_it_is_asked():
+    """An error in the layer's status word (as a product would leave it) stays over
+    further calls, which are right, and is gone once it was read."""
+    lin = fp4.Fp4Linear(randn(256, 320), randn(320, dtype=F32))
+    x = randn(20, 256)
+    want = lin.forward(x)
+    assert lin.check() == B.TPMLP_OK
+    lin._status[0] = B.TPMLP_ERR_TIMEOUT
+    lin.forward(x[:1])
+    assert torch.equal(lin.forward(x), want)
+    lin.backward(randn(20, 320), x)
+    assert lin.check() == B.TPMLP_ERR_TIMEOUT
+    assert lin.check() == B.TPMLP_OK
 
 
 def test_products_at_once_on_the_same_operands():
