@@ -397,17 +397,38 @@ __global__ void __launch_bounds__(THREADS)
 
 // ------------------------------------------------------------- dequantise --
 
-// A unit whose 32 bytes (fp32: 64) start on a 32-byte boundary.
+// wide: the bytes that a unit's place is a multiple of, at most 32.
 template <class T>
-__device__ __forceinline__ void store_unit(T* p, const uint32_t (&w)[sizeof(T) * 4]) {
+__device__ __forceinline__ void store16(T* p, int n, int wide,
+                                        const uint32_t (&w)[sizeof(T) * 4],
+                                        const float (&v)[16]) {
+  constexpr int WORDS = sizeof(T) * 4;
+  if (wide >= 16 && n >= 16) {
+    if (wide == 32) {
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                     reinterpret_cast<char*>(p) + 32 * i),
-                 "r"(w[8 * i]), "r"(w[8 * i + 1]), "r"(w[8 * i + 2]),
-                 "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
-                 "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
-                 : "memory");
+      for (int i = 0; i < WORDS / 8; ++i)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                         reinterpret_cast<char*>(p) + 32 * i),
+                     "r"(w[8 * i]), "r"(w[8 * i + 1]), "r"(w[8 * i + 2]),
+                     "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
+                     "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < WORDS / 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < n) {
+      if constexpr (sizeof(T) == 2)
+        p[i] = __float2bfloat16_rn(v[i]);
+      else
+        p[i] = v[i];
+    }
 }
 
 // Elements 0 .. n - 1 (n <= 256) of a row piece in shared memory to p, by a warp, in
@@ -452,21 +473,21 @@ __device__ __forceinline__ void values8(uint32_t w, float scale, float* v) {
   }
 }
 
-// ALIGNED: every unit of 16 starts on a 32-byte boundary.  Otherwise, and in a last
-// k-tile, a warp's two rows go through shared memory (bf16 off its alignment: unit
-// by unit, 8192 x 5120 took 217 us).
-template <class T, int FORMAT, int PASSES, bool ALIGNED>
+// STAGED: a warp's two rows go through shared memory and out in consecutive pieces,
+// not unit by unit.
+template <class T, int FORMAT, int PASSES, bool STAGED>
 __global__ void __launch_bounds__(THREADS)
-    dequantize_kernel(const Packed p, T* __restrict__ out, long long stride) {
+    dequantize_kernel(const Packed p, T* __restrict__ out, long long stride,
+                      int wide) {
   wait_for_launch_before();
   let_next_launch_start();
-  __shared__ __align__(16) uint8_t s_rows[THREADS / 16][TILE_COLS * sizeof(T)];
+  __shared__ __align__(16)
+      uint8_t s_rows[STAGED ? THREADS / 16 : 1][STAGED ? TILE_COLS * sizeof(T) : 16];
   const int unit = threadIdx.x & 15;
   const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.ktiles));
   const int chunk = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.ktiles));
   const int row0 = chunk * 16 * PASSES + static_cast<int>(threadIdx.x >> 4);
   const int cols = min(TILE_COLS, p.cols - kt * TILE_COLS);   // of this k-tile
-  const bool direct = ALIGNED && cols == TILE_COLS;
   const float g = p.head->g;
   uint2 c[PASSES];
   uint32_t byte[PASSES];
@@ -501,8 +522,8 @@ __global__ void __launch_bounds__(THREADS)
         w[k] = __float_as_uint(v[k]);
     }
     T* to = out + row * stride + kt * TILE_COLS;
-    if (direct) {
-      if (row < p.rows) store_unit(to + unit * 16, w);
+    if constexpr (!STAGED) {
+      if (row < p.rows) store16(to + unit * 16, cols - unit * 16, wide, w, v);
       continue;
     }
     const int own = threadIdx.x >> 4;
@@ -533,19 +554,24 @@ bool on_boundary(const void* p, long long stride_bytes, int bytes) {
 // 1000: 1.8 us, not 3.1; 1024 x 4096 2.8 and 2.7; 8192 x 5120 19.2 and 16.9).
 constexpr long long FULL_GRID = 152 * 4;
 
+// small: a grid of few loads, which needs no L1 but runs sooner where the SMs need
+// not change their shared memory's size between kernels that use some and others
+// (1003 x 1001 quantised and back 6.1 us, not 11.3).  Large ones do need L1 (8192 x 5120: 16.9 us, 22.5 without).
 template <class... P, class... A>
-cudaError_t launch(void (*kernel)(P...), unsigned grid, size_t smem, cudaStream_t s,
-                   A... args) {
+cudaError_t launch(void (*kernel)(P...), unsigned grid, bool small, size_t smem,
+                   cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+  attr[1].val.sharedMemCarveout = cudaSharedmemCarveoutMaxShared;
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = small ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -555,9 +581,9 @@ cudaError_t rows_launch(const T* x, long long stride, const Packed& p,
   const long long units = (p.rows + 15ll) / 16 * p.ktiles;
   if (units >= 4 * FULL_GRID)
     return launch(rows_kernel<T, FORMAT, LD, 4>,
-                  static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), 0, s, x,
+                  static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), false, 0, s, x,
                   stride, p, g);
-  return launch(rows_kernel<T, FORMAT, LD, 1>, static_cast<unsigned>(units), 0, s,
+  return launch(rows_kernel<T, FORMAT, LD, 1>, static_cast<unsigned>(units), true, 0, s,
                 x, stride, p, g);
 }
 
@@ -586,7 +612,8 @@ cudaError_t columns_launch(const T* x, long long stride, int x_rows,
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  return launch(kernel, static_cast<unsigned>(tiles * p.ktiles), smem, s, x, stride,
+  return launch(kernel, static_cast<unsigned>(tiles * p.ktiles),
+                tiles * p.ktiles < FULL_GRID, smem, s, x, stride,
                 x_rows, p, g, part, rp);
 }
 
@@ -614,7 +641,8 @@ cudaError_t amax_type(const T* x, long long stride, long long rows, long long co
   auto kernel = on_boundary(x, bytes, 32)   ? amax_kernel<T, 32>
                 : on_boundary(x, bytes, 16) ? amax_kernel<T, 16>
                                             : amax_kernel<T, 0>;
-  return launch(kernel, static_cast<unsigned>(*slots), 0, s, x, stride, rows, cols,
+  return launch(kernel, static_cast<unsigned>(*slots), items < AMAX_SLOTS, 0, s, x,
+                stride, rows, cols,
                 head);
 }
 
@@ -625,13 +653,18 @@ cudaError_t dequantize_type(const Packed& p, int format, T* out, long long strid
   const unsigned grid = static_cast<unsigned>(
       (p.rows + 16ll * PASSES - 1) / (16 * PASSES) * p.ktiles);
   const long long bytes = stride * static_cast<long long>(sizeof(T));
-  const bool aligned = on_boundary(out, bytes, 32);
+  const int wide =
+      on_boundary(out, bytes, 32) ? 32 : on_boundary(out, bytes, 16) ? 16 : 0;
+  // Through shared memory: 8192 x 5120 of bf16 on odd rows 29 us instead of 217, of
+  // fp32 33 instead of 183, on 16-byte boundaries 33 instead of 49 (bf16 there: 26
+  // instead of 20.5).
+  const bool staged = wide == 0 || (wide == 16 && sizeof(T) == 4);
   auto kernel = format == TPFP4_NV
-                    ? (aligned ? dequantize_kernel<T, TPFP4_NV, PASSES, true>
-                               : dequantize_kernel<T, TPFP4_NV, PASSES, false>)
-                    : (aligned ? dequantize_kernel<T, TPFP4_MX, PASSES, true>
-                               : dequantize_kernel<T, TPFP4_MX, PASSES, false>);
-  return launch(kernel, grid, 0, s, p, out, stride);
+                    ? (staged ? dequantize_kernel<T, TPFP4_NV, PASSES, true>
+                              : dequantize_kernel<T, TPFP4_NV, PASSES, false>)
+                    : (staged ? dequantize_kernel<T, TPFP4_MX, PASSES, true>
+                              : dequantize_kernel<T, TPFP4_MX, PASSES, false>);
+  return launch(kernel, grid, grid < FULL_GRID, 0, s, p, out, stride, wide);
 }
 
 }  // namespace
