@@ -32,7 +32,8 @@
  * -----------
  * - Plain matrices are bf16 (TPMLP_BF16) or fp32 (TPMLP_FP32), row-major with
  *   any row stride >= the number of columns, aligned to their element; 32-byte
- *   aligned rows are read fastest.  A packed matrix is one buffer of
+ *   aligned rows are read fastest.  What lies between rows may be read, and is
+ *   never written.  A packed matrix is one buffer of
  *   tp_fp4_bytes bytes, 256-byte aligned, whose first 4096 bytes hold the status
  *   word of the products that read it as A (16 bytes), g (fp32) and scratch.
  * - rows and cols are 1 .. 2^28 (rows of a plain matrix: 0 .. 2^28).

@@ -583,8 +583,9 @@ cudaError_t rows_launch(const T* x, long long stride, const Packed& p,
     return launch(rows_kernel<T, FORMAT, LD, 4>,
                   static_cast<unsigned>((p.rows + 63ll) / 64 * p.ktiles), false, 0, s, x,
                   stride, p, g);
-  return launch(rows_kernel<T, FORMAT, LD, 1>, static_cast<unsigned>(units), true, 0, s,
-                x, stride, p, g);
+  const bool small = units * static_cast<long long>(sizeof(T)) < 4 * FULL_GRID;
+  return launch(rows_kernel<T, FORMAT, LD, 1>, static_cast<unsigned>(units), small, 0,
+                s, x, stride, p, g);
 }
 
 template <class T, int FORMAT>

@@ -546,6 +546,41 @@ def test_no_tokens():
     assert q.check() == 0 and lin.check() == 0
 
 
+def test_offsets_past_32_bits():
+    """A matrix of 8.6e9 elements (17 GB of bf16, 4.3 GB of codes): its last rows,
+    quantised and read back, and in products as the many rows and as the weight."""
+    rows, cols, fresh = 132096, 65536, 512
+    part = randn(fresh, cols, seed=1)
+    x = part.repeat(rows // fresh, 1)
+    last = slice(rows - fresh, rows)
+    want = fp4.quantize(part, scale=1.0)
+    q = fp4.quantize(x, scale=1.0)
+    assert q.buffer.numel() > 2 ** 32
+    tail = rows // 128 * 256     # tiles; those of the last rows
+    codes = q.buffer[4096:4096 + tail * 16384].view(-1, 16384)
+    assert torch.equal(codes[-1024:], want.buffer[4096:4096 + 1024 * 16384]
+                       .view(-1, 16384))
+    out = q.dequantize()
+    assert torch.equal(out[last], want.dequantize())
+    del out
+    qt = fp4.quantize(x, scale=1.0, transpose=True)     # [cols, rows]
+    rows_of = qt.dequantize()[:, last]
+    assert torch.equal(rows_of, fp4.quantize(part, scale=1.0, transpose=True)
+                       .dequantize())
+    del qt, rows_of, x
+    w = fp4.quantize(randn(300, cols, seed=2), scale=1.0)
+    got = fp4.matmul(q, w, dtype=F32)
+    vp, vw = f64(want.dequantize(F32)), f64(w.dequantize(F32))
+    close_product(got[:fresh], vp, vw)
+    close_product(got[last], vp, vw)
+    for T in (2, 30, 300):
+        a = fp4.quantize(randn(T, cols, seed=3), scale=1.0)
+        got = fp4.matmul(a, q, dtype=F32)
+        va = f64(a.dequantize(F32))
+        close_product(got[:, :fresh], va, vp)
+        close_product(got[:, last], va, vp)
+
+
 # -------------------------------------------------------------- MLP block --
 
 def block_case(T, h, f, t, seed=0, bias=True, **kw):
