@@ -120,8 +120,8 @@ int tp_fp4_matmul(long long T, long long N, long long K, int format,
 /* Both in one call, for a layer y = x W: x [T, K] (x_dtype, x_stride) quantised
  * (x_scale as tp_fp4_quantize's scale) times the packed W [N, K].  xq is scratch of
  * tp_fp4_bytes(T, K, format) bytes; status as above (NULL: xq's).  The product
- * starts to load W while x is quantised, and up to 4 rows with a given x_scale
- * are quantised by the product itself.  xq and C share no memory with the rest. */
+ * starts to load W while x is quantised, and up to 8 rows of bf16 (4 of
+ * fp32) with a given x_scale are quantised by the product itself.  xq and C share no memory with the rest. */
 int tp_fp4_linear(long long T, long long N, long long K, int x_dtype,
                   const void* x, long long x_stride, int format, double x_scale,
                   void* xq, size_t xq_bytes, const void* W, size_t w_bytes,

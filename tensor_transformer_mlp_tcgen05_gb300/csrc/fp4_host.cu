@@ -188,17 +188,19 @@ int product(HandleCore* core, const char* name, int format,
 }
 
 // x [rows, cols] as the left operand of a product: quantised first, or by the
-// product itself where that is a product of very few rows with a given g.  One
-// launch instead of two: one token of 1024 x 4096 takes 4.4 us on the GPU instead
-// of 5.0, and 4.9 us of the host instead of 7.9; 8 rows took 9.8 instead of 9.0 (a
-// block of 1024 x 4096).  `xq` keeps the quantised rows and the status word.
+// product itself where that is a product of very few rows with a given g: one launch
+// instead of two.  In us, weights not in L2, launches back to back: 1 x 1024 x 4096
+// 3.5 and 5.0, 1 x 5120 x 20480 12.6 and 14.1, 8 (bf16) x 1024 x 4096 4.1 and 5.2, 8 x
+// 5120 x 20480 13.7 and 14.4 (in L2: 10.6 and 9.5).  `xq` keeps the quantised rows and
+// the status word.
 int left_operand(HandleCore* core, const char* name, long long rows,
                  long long cols, bool bf16, const void* x, long long stride,
                  int format, int exponent, void* xq, fp4::ProductArgs* a,
                  cudaStream_t s) {
   a->a = fp4::view(xq, rows, cols);
   a->status = a->a.head->status;
-  if (rows <= fp4::PLAIN_ROWS && exponent != AUTO_SCALE) {
+  const int most = bf16 ? fp4::PLAIN_ROWS_BF16 : fp4::PLAIN_ROWS_FP32;
+  if (rows <= most && exponent != AUTO_SCALE) {
     a->x = x;
     a->x_bf16 = bf16 ? 1 : 0;
     a->x_stride = stride;

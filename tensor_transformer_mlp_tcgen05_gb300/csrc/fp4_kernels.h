@@ -51,7 +51,7 @@ struct ProductArgs {
   Packed a, b;          // [M, K], [N, K]
   int M, N;
   // instead of a's codes, scales and g: the plain matrix x that the product
-  // quantises itself, g = 2^x_exponent (M <= PLAIN_ROWS; a then has its sizes, and
+  // quantises itself, g = 2^x_exponent (M <= PLAIN_ROWS_*; a then has its sizes, and
   // a's status word is cleared by the product); or null
   const void* x;
   int x_bf16;
@@ -83,7 +83,8 @@ cudaError_t launch_product_pairs(int format, const CUtensorMap& ta,
 
 // Tiles of 128 rows of B x up to 128 rows of A, K split over a cluster, for few
 // rows of A.
-constexpr int PLAIN_ROWS = 4;
+// Rows that the product quantises itself.
+constexpr int PLAIN_ROWS_BF16 = 8, PLAIN_ROWS_FP32 = 4;
 cudaError_t launch_product_split(int format, const ProductArgs& args, int sms,
                                  cudaStream_t s);
 cudaError_t launch_product_plain(int format, const ProductArgs& args, int sms,

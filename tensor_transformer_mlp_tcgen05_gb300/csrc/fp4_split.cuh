@@ -8,7 +8,7 @@
 // scales and issues MMAs, as in fp4_gemm.cu on one CTA; then warps 0 to 3 read
 // their 32 lanes of the accumulator into shared memory, and after a cluster
 // barrier the CTAs add up, row by row of A and in the CTAs' order, the partial
-// sums.  One launch, no workspace, a fixed order.  Up to 4 rows of A may come as
+// sums.  One launch, no workspace, a fixed order.  Up to 8 rows of A may come as
 // they are: four more warps quantise them (every CTA those of its range of K).
 //
 // Measured (NV, B not in L2, launches back to back): 1 x 4096 x 1024 3.5 us, 32 x
@@ -29,7 +29,8 @@ namespace split {
 using namespace gemm;
 
 constexpr int FM = 128;            // rows of B ("features") a CTA takes
-enum Source : int { PACKED = 0, PLAIN_BF16 = 1, PLAIN_FP32 = 2 };   // of A
+// Of A: packed, or up to 4 rows, or (bf16) up to 8.
+enum Source : int { PACKED = 0, PLAIN_BF16 = 1, PLAIN_FP32 = 2, PLAIN_BF16_8 = 3 };
 __host__ __device__ constexpr int threads_of(Source src) {
   return src == PACKED ? 128 : 256;
 }
@@ -148,10 +149,10 @@ __device__ __forceinline__ void finish(const ProductArgs& a, int row, int n0,
 }
 
 // Warps 4 to 7 of a product that quantises A itself, a k-tile each in turn.  A lane
-// takes two units of 16 elements, of rows lane / 16 and that + 2, and puts their
-// codes and scales where the copies of a packed A would; its next k-tile's are
-// loaded meanwhile, so that those of eight k-tiles are in flight (with all warps on
-// one k-tile, 8 x 5120 x 20480 took 16 us instead of 10).
+// takes two (of 8 rows four) units of 16 elements, of rows lane / 16, that + 2 and so
+// on, and puts their codes and scales where the copies of a packed A would; its next
+// k-tile's are loaded meanwhile, so that those of eight k-tiles are in flight (with
+// all warps on one k-tile, 8 x 5120 x 20480 took 16 us instead of 10).
 //
 // No more warps than stages: a warp's last k-tile i - QUANT_WARPS had stage
 // i - QUANT_WARPS - STAGES free, so that of this stage's uses all but the last are
@@ -164,7 +165,7 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, int k_lo,
                                               uint32_t empty0, const Ctl& ctl) {
   using S = Shape<FORMAT, NT>;
   static_assert(QUANT_WARPS <= S::STAGES, "parities tell two phases apart");
-  static_assert(PLAIN_ROWS == 4, "two units a lane");
+  constexpr int UNITS = SRC == PLAIN_BF16_8 ? 4 : 2;
   using T = std::conditional_t<SRC == PLAIN_FP32, float, __nv_bfloat16>;
   const int lane = threadIdx.x & 31;
   const int unit = lane & 15, row0 = lane >> 4;
@@ -173,10 +174,10 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, int k_lo,
   const T* src = static_cast<const T*>(a.x) + row0 * a.x_stride + unit * 16;
   const float inv_g = exp2_of(-a.x_exponent);
   const Extent e = extent_of(static_cast<const T*>(a.x), a.x_stride, a.M, a.a.cols);
-  auto load = [&](int i, Raw<T> (&raw)[2]) {
+  auto load = [&](int i, Raw<T> (&raw)[UNITS]) {
     const int col = (k_lo + i) * TILE_COLS;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < UNITS; ++j) {
       if (2 * j >= a.M) break;   // both of the warp's rows
       const T* p = src + 2 * j * a.x_stride + col;
       const int n = row0 + 2 * j < a.M ? a.a.cols - col - unit * 16 : 0;
@@ -186,9 +187,9 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, int k_lo,
         load16<T, 0>(p, n, e, raw[j]);
     }
   };
-  auto store = [&](uint32_t stage, const Raw<T> (&raw)[2]) {
+  auto store = [&](uint32_t stage, const Raw<T> (&raw)[UNITS]) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < UNITS; ++j) {
       if (2 * j >= a.M) break;
       const int row = row0 + 2 * j;
       float v[16];
@@ -203,19 +204,19 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, int k_lo,
       asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(c.x), "r"(c.y)
                    : "memory");
       // four blocks' scale bytes in one word, as in the row kernel
-      constexpr int UNITS = block_size(FORMAT) / 16;
-      uint32_t word = s.byte << (8 * (lane / UNITS & 3));
-      word |= __shfl_xor_sync(0xffffffffu, word, UNITS);
-      word |= __shfl_xor_sync(0xffffffffu, word, 2 * UNITS);
-      if (unit % (4 * UNITS) == 0)
+      constexpr int LANES = block_size(FORMAT) / 16;   // of a block
+      uint32_t word = s.byte << (8 * (lane / LANES & 3));
+      word |= __shfl_xor_sync(0xffffffffu, word, LANES);
+      word |= __shfl_xor_sync(0xffffffffu, word, 2 * LANES);
+      if (unit % (4 * LANES) == 0)
         asm volatile(
             "st.shared.b32 [%0], %1;" ::"r"(s_sa + stage * S::TILE +
-                                            unit / (4 * UNITS) * 512 + row * 16),
+                                            unit / (4 * LANES) * 512 + row * 16),
             "r"(word)
             : "memory");
     }
   };
-  Raw<T> now[2], next[2];
+  Raw<T> now[UNITS], next[UNITS];
   int i = static_cast<int>(threadIdx.x >> 5) - 4;
   if (k_lo + i < k_hi) load(i, now);
   for (; k_lo + i < k_hi; i += QUANT_WARPS) {
@@ -228,7 +229,7 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, int k_lo,
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(full0 + 8u * stage);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) now[j] = next[j];
+    for (int j = 0; j < UNITS; ++j) now[j] = next[j];
   }
 }
 

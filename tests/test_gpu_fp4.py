@@ -492,13 +492,13 @@ def test_gradients_by_differences():
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_few_rows_quantised_by_the_product(fmt, dtype):
-    """1 to 6 rows, strided and unaligned, with borders, zeros and values that are
+    """1 to 10 rows, strided and unaligned, with borders, zeros and values that are
     not finite: the same bits as the two steps one by one."""
     N, K = 200, 1100
     lin = fp4.Fp4Linear(randn(K, N, seed=1, scale=K ** -0.5), randn(N, dtype=F32),
                         format=fmt)
     one = 1.0 if fmt == "nvfp4" else None
-    for T in range(1, 7):
+    for T in range(1, 11):
         for off, pad in ((0, 0), (0, 4), (3, 1)):
             buf = randn(T * (K + pad) + off, seed=T, dtype=dtype)
             x = buf[off:].view(T, K + pad)[:, :K]
@@ -521,7 +521,7 @@ def test_few_rows_over_a_long_ring(fmt, dtype):
     N, K = 130 * 128, 5200
     lin = fp4.Fp4Linear(randn(K, N, seed=1, scale=K ** -0.5), format=fmt)
     one = 1.0 if fmt == "nvfp4" else None
-    for T in (1, 3, 4, 16):
+    for T in (1, 3, 4, 7, 8, 16):
         x = randn(T, K, seed=T, dtype=dtype)
         q = fp4.quantize(x, fmt, scale=one)
         want = fp4.matmul(q, lin.weight, dtype=F32)
@@ -607,8 +607,8 @@ def check_block(m, Z, X, Xn, A, Bw, b1, b2, fmt, gelu="erf", residual=False):
     f = A.shape[1]
     one = 1.0 if fmt == "nvfp4" else None
     code = fp4._FORMATS[fmt]
-    # (up to 4 rows are quantised inside the product)
-    xq = (fp4.quantize(Xn, fmt, scale=one) if T <= 4
+    # (up to 8 rows are quantised inside the product)
+    xq = (fp4.quantize(Xn, fmt, scale=one) if T <= 8
           else fp4.Fp4Tensor(m._fp4_ws, T, h, fmt))
     yq = fp4.Fp4Tensor(m._fp4_ws[up(B.tp_fp4_bytes(T, h, code)):], T, f, fmt)
     check_quantized(xq, f64(Xn), one)
@@ -722,7 +722,8 @@ def test_block_in_two_graphs_and_beside_a_training_step():
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("T,h,f", [(2, 16384, 32768), (16, 16384, 32768),
+@pytest.mark.parametrize("T,h,f", [(2, 16384, 32768), (8, 16384, 32768),
+                                   (16, 16384, 32768),
                                    (2000, 2048, 8192)])
 def test_wait_timeout_is_reported_and_context_survives(fmt, T, h, f):
     """Every kind of product: its bounded waits give up, the status says so, and the
