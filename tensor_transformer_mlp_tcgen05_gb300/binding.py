@@ -392,7 +392,8 @@ def tensor_calls():
                       "tp_grad_clip", "tp_fp4_bytes", "tp_fp4_quantize",
                       "tp_fp4_colsum_workspace_bytes", "tp_fp4_quantize_both",
                       "tp_fp4_dequantize", "tp_fp4_matmul", "tp_fp4_linear",
-                      "tp_fp4_mlp_workspace_bytes", "tp_fp4_mlp_forward")])
+                      "tp_fp4_mlp_workspace_bytes", "tp_fp4_mlp_forward",
+                      "tp_fp4_mlp_weights_bytes", "tp_fp4_mlp_pack_weights")])
         _calls = m
     return _calls
 

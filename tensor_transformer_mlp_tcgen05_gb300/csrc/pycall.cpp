@@ -46,6 +46,8 @@ struct Library {
   decltype(&tp_fp4_linear) fp4_linear = nullptr;
   decltype(&tp_fp4_mlp_workspace_bytes) fp4_mlp_workspace_bytes = nullptr;
   decltype(&tp_fp4_mlp_forward) fp4_mlp_forward = nullptr;
+  decltype(&tp_fp4_mlp_weights_bytes) fp4_mlp_weights_bytes = nullptr;
+  decltype(&tp_fp4_mlp_pack_weights) fp4_mlp_pack_weights = nullptr;
   PyObject* check = nullptr;   // binding._check(status, what)
 } lib;
 
@@ -763,6 +765,31 @@ const void* block_of(const char* name, PyObject* o, at::IntArrayRef size,
   return t->numel() == 0 ? nullptr : t->const_data_ptr();
 }
 
+// fp4_mlp_pack(handle, h, f, format, A, B, stream) -> packed: it belongs to the
+// stream that writes it.
+PyObject* fp4_mlp_pack(PyObject* const* a) {
+  auto* handle = reinterpret_cast<tp_mlp_handle*>(integer(a[0]));
+  const long long h = integer(a[1]), f = integer(a[2]);
+  const int format = static_cast<int>(integer(a[3]));
+  const at::Tensor &A = tensor("A", a[4]), &B = tensor("B", a[5]);
+  if (!A.is_cuda()) throw Refused{"A must be a CUDA tensor, got " + shown(A)};
+  const at::Device dev = A.device();
+  const void* ap = block_of("A", a[4], {h, f}, at::kBFloat16, dev);
+  const void* bp = block_of("B", a[5], {f, h}, at::kBFloat16, dev);
+  const size_t n = lib.fp4_mlp_weights_bytes(handle, format);
+  if (n == 0)
+    throw Refused{"the four-bit variant needs a bf16 handle without dropout"};
+  const Place place(dev, a[6]);
+  const at::Tensor packed = make({static_cast<int64_t>(n)}, at::kByte, dev);
+  void* pp = packed.data_ptr();
+  check(without_gil([&] {
+          return lib.fp4_mlp_pack_weights(handle, format, ap, bp, pp, n,
+                                          place.stream);
+        }),
+        "tp_fp4_mlp_pack_weights");
+  return wrapped(packed);
+}
+
 // fp4_mlp(handle, h, f, format, X, packed, b1, b2, gamma, beta, x_scale, y_scale,
 //         out, stream) -> (Z, workspace, of this call alone)
 PyObject* fp4_mlp(PyObject* const* a) {
@@ -833,6 +860,10 @@ PyObject* bind(PyObject* const* a) {
   l.fp4_mlp_workspace_bytes =
       reinterpret_cast<decltype(l.fp4_mlp_workspace_bytes)>(at(15));
   l.fp4_mlp_forward = reinterpret_cast<decltype(l.fp4_mlp_forward)>(at(16));
+  l.fp4_mlp_weights_bytes =
+      reinterpret_cast<decltype(l.fp4_mlp_weights_bytes)>(at(17));
+  l.fp4_mlp_pack_weights =
+      reinterpret_cast<decltype(l.fp4_mlp_pack_weights)>(at(18));
   Py_INCREF(a[0]);
   l.check = a[0];
   Py_XDECREF(lib.check);
@@ -875,6 +906,7 @@ PyMethodDef methods[] = {
     {"fp4_backward", nullptr, 0, nullptr},
     {"fp4_mlp", nullptr, 0, nullptr},
     {"fp4_quantize_both", nullptr, 0, nullptr},
+    {"fp4_mlp_pack", nullptr, 0, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
@@ -893,7 +925,7 @@ void set(int i) {
 }  // namespace
 
 PyMODINIT_FUNC PyInit__pycall() {
-  set<bind, 17>(0);
+  set<bind, 19>(0);
   set<rope, 11>(1);
   set<norm_forward, 16>(2);
   set<norm_backward, 21>(3);
@@ -905,5 +937,6 @@ PyMODINIT_FUNC PyInit__pycall() {
   set<fp4_backward, 10>(9);
   set<fp4_mlp, 14>(10);
   set<fp4_quantize_both, 4>(11);
+  set<fp4_mlp_pack, 7>(12);
   return PyModule_Create(&module);
 }

@@ -242,17 +242,11 @@ class TensorParallelMLP:
     def pack_fp4_weights(self, A, B, format: str = "nvfp4",
                          stream=None) -> "Fp4Weights":
         """Quantize A and B to four bits along the products' inner dimension
-        (see tp_fp4_mlp_pack_weights) for forward_fp4."""
+        (see tp_fp4_mlp_pack_weights) for forward_fp4.  The work, and the packed
+        memory, belong to ``stream``, or to the current one of A's device."""
         h, f = self.hidden, self.ffn
-        self._chk("A", A, (h, f), torch.bfloat16)
-        self._chk("B", B, (f, h), torch.bfloat16)
-        code = _fp4_format(format)
-        n = B_.tp_fp4_mlp_weights_bytes(self.handle, code)
-        if n == 0:
-            raise ValueError("the four-bit variant needs a bf16 handle without "
-                             "dropout")
-        packed = torch.empty(n, dtype=torch.uint8, device=A.device)
-        B_.tp_fp4_mlp_pack_weights(self.handle, code, A, B, packed, n, stream)
+        packed = B_.tensor_calls().fp4_mlp_pack(self.handle, h, f,
+                                                _fp4_format(format), A, B, stream)
         return Fp4Weights(packed, format, (h, f))
 
     def forward_fp4(self, X, packed, b1=None, b2=None, gamma=None, beta=None,

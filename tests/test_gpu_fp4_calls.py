@@ -1,0 +1,55 @@
+"""The four-bit operators' calls on streams, from threads, on empty and on wrong
+inputs: what belongs to whom, and which errors are reported when."""
+import pytest
+import torch
+
+from tensor_transformer_mlp_tcgen05_gb300 import binding as B
+from tensor_transformer_mlp_tcgen05_gb300 import fp4
+from tensor_transformer_mlp_tcgen05_gb300.mlp import TensorParallelMLP
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = ["nvfp4", "mxfp4"]
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def randn(*shape, seed=0, dtype=BF, scale=1.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return (scale * torch.randn(shape, generator=g, device="cuda")).to(dtype)
+
+
+def block_case(T, h, f, **kw):
+    m = TensorParallelMLP(h, f, 1, T, **kw)
+    return (m, randn(T, h, seed=1), randn(h, f, seed=2, scale=h ** -0.5),
+            randn(f, h, seed=3, scale=f ** -0.5))
+
+
+def owner(t):
+    """The handle of the stream that t's memory belongs to."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("memory of no segment")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_packed_weights_belong_to_the_stream_that_writes_them(fmt):
+    """(Of the current stream's memory, a block that its pending kernels still use
+    could be overwritten.)"""
+    m, X, A, Bw = block_case(40, 256, 512)
+    want = m.pack_fp4_weights(A, Bw, format=fmt)
+    assert owner(want.buffer) == torch.cuda.current_stream().cuda_stream
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        p = m.pack_fp4_weights(A, Bw, format=fmt, stream=stream)
+        assert owner(p.buffer) == side.cuda_stream
+        assert p.shape == (256, 512) and p.format == fmt
+        Z = m.forward_fp4(X, p, stream=stream)
+        assert owner(Z) == side.cuda_stream
+        side.synchronize()
+        assert torch.equal(Z, m.forward_fp4(X, want))
+    for bad in ((A.cpu(), Bw), (A, Bw.cpu()), (A.float(), Bw), (A.t(), Bw),
+                (A, Bw[:, :8])):
+        with pytest.raises(ValueError):
+            m.pack_fp4_weights(*bad, format=fmt)
