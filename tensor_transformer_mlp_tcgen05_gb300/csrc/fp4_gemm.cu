@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint64_t desc_sb = sdesc_scales(s_sb);
       uint32_t stage = 0, phase = 0, j = 0;
       bool alive = true;
+      wait_for_launch_before();   // not on a bounded wait's budget
       for (int item = pair; alive && item < items; item += num_pairs) {
         const Item it = item_of<EPI>(item, whole, num_m, num_n, group_m, args.N);
         if (it.cols == 0) continue;

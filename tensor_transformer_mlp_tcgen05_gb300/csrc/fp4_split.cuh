@@ -289,6 +289,10 @@ __global__ void __launch_bounds__(threads_of(SRC), 2)
   if (SRC != PACKED && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 4)
     args.a.head->status[threadIdx.x] = 0;
 
+  // The producer alone runs ahead of the launch before: the others' bounded waits
+  // start after it, so that a budget counts waits of this kernel only.
+  if (SRC == PACKED && warp != 0) wait_for_launch_before();
+
   if (warp == 0) {
     // ------------------------------------------------------ producer --
     uint32_t stage = 0, phase = 0;

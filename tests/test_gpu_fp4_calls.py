@@ -53,3 +53,30 @@ def test_packed_weights_belong_to_the_stream_that_writes_them(fmt):
                 (A, Bw[:, :8])):
         with pytest.raises(ValueError):
             m.pack_fp4_weights(*bad, format=fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_budget_counts_waits_of_its_own_kernel(fmt):
+    """The block's second product is resident while the first one runs (48 places of
+    304 are left by the first's 256 CTAs).  A budget that each of the two fits in, but
+    not both together: nothing is stuck, and nothing is reported.  (Both read 604 MB
+    of weights, MX 570: about 100 us each, of which the budget is one and a half.)"""
+    h = f = 32768
+    m, X, A, Bw = block_case(16, h, f)
+    p = m.pack_fp4_weights(A, Bw, format=fmt)
+    del A, Bw
+    want = m.forward_fp4(X, p)
+    assert m.check() == B.TPMLP_OK
+    times = []
+    for _ in range(5):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        m.forward_fp4(X, p)
+        end.record()
+        end.synchronize()
+        times.append(start.elapsed_time(end) * 1e6)
+    B.tp_mlp_set_wait_budget(m.handle, int(0.75 * min(times)))
+    for _ in range(5):
+        Z = m.forward_fp4(X, p)
+        assert m.check() == B.TPMLP_OK
+        assert torch.equal(Z, want)
