@@ -805,6 +805,11 @@ PyObject* fp4_mlp(PyObject* const* a) {
   const void* xp = block_of("X", a[4], {T, h}, at::kBFloat16, dev);
   const at::Tensor& packed = tensor("packed", a[5]);
   if (packed.device() != dev) throw Refused{"packed and X differ in device"};
+  const size_t nw = lib.fp4_mlp_weights_bytes(handle, format);
+  if (packed.scalar_type() != at::kByte || !packed.is_contiguous() ||
+      static_cast<size_t>(packed.numel()) < nw)
+    throw Refused{"packed: expected the " + std::to_string(nw) + " contiguous bytes of "
+                  "the block's weights in this format, got " + shown(packed)};
   auto vec = [&](const char* n, PyObject* o, long long size) {
     return static_cast<const float*>(block_of(n, o, {size}, at::kFloat, dev));
   };

@@ -5,7 +5,7 @@ import torch
 
 from tensor_transformer_mlp_tcgen05_gb300 import binding as B
 from tensor_transformer_mlp_tcgen05_gb300 import fp4
-from tensor_transformer_mlp_tcgen05_gb300.mlp import TensorParallelMLP
+from tensor_transformer_mlp_tcgen05_gb300.mlp import Fp4Weights, TensorParallelMLP
 
 pytestmark = pytest.mark.gpu
 
@@ -53,6 +53,23 @@ def test_packed_weights_belong_to_the_stream_that_writes_them(fmt):
                 (A, Bw[:, :8])):
         with pytest.raises(ValueError):
             m.pack_fp4_weights(*bad, format=fmt)
+
+
+def test_weights_of_too_few_bytes_are_refused():
+    """As after a checkpoint that was cut off, or was written in another format: the
+    products would read past the buffer."""
+    m, X, A, Bw = block_case(10, 256, 512)
+    mx = m.pack_fp4_weights(A, Bw, format="mxfp4").buffer
+    nv = m.pack_fp4_weights(A, Bw, format="nvfp4").buffer
+    assert mx.numel() < nv.numel()
+    for buffer, fmt in ((mx, "nvfp4"), (nv[:-1], "nvfp4"), (mx[:4096], "mxfp4"),
+                        (mx.view(torch.int32), "mxfp4"), (nv[:0], "nvfp4"),
+                        (mx.repeat(2)[::2], "mxfp4")):
+        with pytest.raises(ValueError):
+            m.forward_fp4(X, Fp4Weights(buffer, fmt, (256, 512)))
+    want = m.forward_fp4(X, Fp4Weights(mx, "mxfp4", (256, 512)))
+    assert torch.equal(m.forward_fp4(X, Fp4Weights(mx.clone(), "mxfp4", (256, 512))),
+                       want)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
