@@ -118,8 +118,10 @@ class TensorParallelMLP:
     def check(self, stream=None) -> int:
         """Synchronise and return the device status (TPMLP_OK or an error)."""
         for ws in (self._fp4_ws, self._ws):
-            rc = (B_.TPMLP_OK if ws is None else
-                  B_.tp_mlp_check(self.handle, ws, stream))
+            if ws is None:
+                continue
+            with torch.cuda.device(ws.device):
+                rc = B_.tp_mlp_check(self.handle, ws, stream)
             if rc != B_.TPMLP_OK:
                 return rc
         return B_.TPMLP_OK

@@ -1,0 +1,37 @@
+"""Calls of the four-bit operators that need no GPU."""
+import contextlib
+
+import torch
+
+from tensor_transformer_mlp_tcgen05_gb300 import binding as B
+from tensor_transformer_mlp_tcgen05_gb300 import build as build_mod
+from tensor_transformer_mlp_tcgen05_gb300.mlp import TensorParallelMLP
+
+
+def block(**kw):
+    build_mod.build()
+    return TensorParallelMLP(128, 512, 1, 16, **kw)
+
+
+class Memory:
+    """Of a workspace on a device that is not the current one."""
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+def test_check_runs_on_its_workspaces_device(monkeypatch):
+    m, current, seen = block(), [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        current.append(d.index)
+        yield
+        current.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(B, "tp_mlp_check", lambda handle, ws, stream=None:
+                        seen.append((ws.device.index, current[-1])) or 0)
+    m._fp4_ws, m._ws = Memory(1), Memory(2)
+    assert m.check() == B.TPMLP_OK
+    assert seen == [(1, 1), (2, 2)] and current == [0]
