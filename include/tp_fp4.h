@@ -146,8 +146,14 @@ int tp_fp4_mlp_pack_weights(tp_mlp_handle* handle, int format, const void* A,
                             void* stream);
 size_t tp_fp4_mlp_workspace_bytes(const tp_mlp_handle* handle, int tokens,
                                   int format);
+/* status: 16 bytes of device memory, 16-byte aligned, that the caller zeroed, where
+ * the first error of all the handle's tp_fp4_mlp_forward calls from here on stays
+ * until tp_fp4_check reads it; or NULL, as a new handle has it: a call's error is left
+ * in its own workspace, where the next call on that workspace clears it. */
+int tp_fp4_mlp_set_status(tp_mlp_handle* handle, void* status);
 /* Arguments as tp_mlp_forward_fp8; packed and workspace 256-byte aligned;
- * tp_mlp_check reads the status. */
+ * tp_mlp_check reads the workspace's status, where tp_fp4_mlp_set_status has not
+ * given another place. */
 int tp_fp4_mlp_forward(tp_mlp_handle* handle, int tokens, int format,
                        const void* X, const void* packed, const float* bias1,
                        const float* bias2, const float* ln_gamma,

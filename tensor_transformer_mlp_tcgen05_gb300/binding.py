@@ -68,7 +68,8 @@ EXPORTED_FP4 = (
     "tp_fp4_bytes", "tp_fp4_offset", "tp_fp4_quantize",
     "tp_fp4_colsum_workspace_bytes", "tp_fp4_quantize_both", "tp_fp4_dequantize",
     "tp_fp4_matmul", "tp_fp4_linear", "tp_fp4_check", "tp_fp4_mlp_weights_bytes",
-    "tp_fp4_mlp_pack_weights", "tp_fp4_mlp_workspace_bytes", "tp_fp4_mlp_forward",
+    "tp_fp4_mlp_pack_weights", "tp_fp4_mlp_workspace_bytes",
+    "tp_fp4_mlp_set_status", "tp_fp4_mlp_forward",
 )
 
 TPROPE_MAX_HEAD_DIM = 256
@@ -357,6 +358,8 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.tp_fp4_mlp_pack_weights.restype = _i
     L.tp_fp4_mlp_workspace_bytes.argtypes = [_vp, _i, _i]
     L.tp_fp4_mlp_workspace_bytes.restype = _sz
+    L.tp_fp4_mlp_set_status.argtypes = [_vp, _vp]
+    L.tp_fp4_mlp_set_status.restype = _i
     L.tp_fp4_mlp_forward.argtypes = [_vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp,
                                      dbl, dbl, _vp, _vp, _sz, _vp]
     L.tp_fp4_mlp_forward.restype = _i
@@ -886,6 +889,11 @@ def tp_fp4_mlp_pack_weights(handle, format, A, B, packed, packed_bytes,
 
 def tp_fp4_mlp_workspace_bytes(handle, tokens: int, format: int) -> int:
     return int(lib().tp_fp4_mlp_workspace_bytes(handle, tokens, format))
+
+
+def tp_fp4_mlp_set_status(handle, status):
+    _check(lib().tp_fp4_mlp_set_status(handle, _ptr(status)),
+           "tp_fp4_mlp_set_status")
 
 
 def tp_fp4_mlp_forward(handle, tokens, format, X, packed, bias1, bias2,

@@ -342,7 +342,8 @@ MlpPack mlp_pack(const tp_mlp_config& c, int format) {
 struct MlpLayout {
   size_t xq = 0, yq = 0, xn = 0, mean = 0, rstd = 0, total = 0;
 };
-// Xq [T, h], whose header's status word is the call's | Yq [T, f] | [Xn bf16,
+// Xq [T, h], whose header's status word is the call's (but for
+// tp_fp4_mlp_set_status) | Yq [T, f] | [Xn bf16,
 // mean, rstd]
 MlpLayout mlp_layout(const tp_mlp_config& c, int tokens, int format) {
   MlpLayout l;
@@ -546,6 +547,14 @@ size_t tp_fp4_mlp_workspace_bytes(const tp_mlp_handle* H, int tokens,
   return mlp_layout(H->cfg, tokens, format).total;
 }
 
+int tp_fp4_mlp_set_status(tp_mlp_handle* H, void* status) {
+  if (H == nullptr) return TPMLP_ERR_ARG;
+  if (!aligned16(status))
+    return bad(TPMLP_ERR_ALIGN, "fp4: status must be 16-byte aligned");
+  H->fp4_status = static_cast<int*>(status);
+  return TPMLP_OK;
+}
+
 int tp_fp4_mlp_forward(tp_mlp_handle* H, int tokens, int format, const void* X,
                        const void* packed, const float* bias1,
                        const float* bias2, const float* ln_gamma,
@@ -574,6 +583,9 @@ int tp_fp4_mlp_forward(tp_mlp_handle* H, int tokens, int format, const void* X,
   const struct { const void* p; size_t n; } inputs[] = {
       {X, nx}, {packed, P.total}, {bias1, static_cast<size_t>(c.ffn) * 4},
       {bias2, nh}, {ln_gamma, nh}, {ln_beta, nh}};
+  int* const status = H->fp4_status;   // (null: the workspace's)
+  if (overlap(status, 16, Z, nx) || overlap(status, 16, workspace, L.total))
+    return bad(TPMLP_ERR_ARG, "fp4: Z or workspace overlaps the status");
   for (const auto& in : inputs)
     if (overlap(Z, nx, in.p, in.n) || overlap(workspace, L.total, in.p, in.n))
       return bad(TPMLP_ERR_ARG, "fp4: Z or workspace overlaps an input");
@@ -600,6 +612,7 @@ int tp_fp4_mlp_forward(tp_mlp_handle* H, int tokens, int format, const void* X,
   fp4::ProductArgs a = {};
   TRY(left_operand(&H->core, "fp4_quantize_x", tokens, h, true, Xop, h, format, xe,
                    ws + L.xq, &a, s));
+  if (status != nullptr) a.status = status;
   a.b = fp4::view(pk + P.a, f, h);
   a.M = tokens;
   a.N = f;

@@ -7,4 +7,5 @@ struct tp_mlp_handle {
   tp_mlp_config cfg;
   unsigned long long drop_seed = 0, drop_offset = 0;
   bool ln_prologue = true;   // tp_mlp_set_ln_prologue
+  int* fp4_status = nullptr; // tp_fp4_mlp_set_status
 };

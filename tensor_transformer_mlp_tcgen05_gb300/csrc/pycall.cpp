@@ -13,6 +13,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -765,8 +767,23 @@ const void* block_of(const char* name, PyObject* o, at::IntArrayRef size,
   return t->numel() == 0 ? nullptr : t->const_data_ptr();
 }
 
-// fp4_mlp_pack(handle, h, f, format, A, B, stream) -> packed: it belongs to the
-// stream that writes it.
+bool capturing() {   // the current stream
+  return c10::cuda::currentStreamCaptureStatusMayInitCtx() !=
+         c10::cuda::CaptureStatus::None;
+}
+
+// The four words of a new status, zero on every stream once this returns.
+at::Tensor new_status(const at::Device& dev) {
+  const at::Tensor t =
+      at::zeros({4}, at::TensorOptions().dtype(at::kInt).device(dev));
+  const auto stream = c10::cuda::getCurrentCUDAStream(dev.index());
+  without_gil([&] { return stream.synchronize(), 0; });
+  return t;
+}
+
+// fp4_mlp_pack(handle, h, f, format, A, B, status, stream) -> (packed, status or
+// None): packed belongs to the stream that writes it; with status, a new one for the
+// block, but not during a capture (of this stream or of the caller's).
 PyObject* fp4_mlp_pack(PyObject* const* a) {
   auto* handle = reinterpret_cast<tp_mlp_handle*>(integer(a[0]));
   const long long h = integer(a[1]), f = integer(a[2]);
@@ -779,7 +796,12 @@ PyObject* fp4_mlp_pack(PyObject* const* a) {
   const size_t n = lib.fp4_mlp_weights_bytes(handle, format);
   if (n == 0)
     throw Refused{"the four-bit variant needs a bf16 handle without dropout"};
-  const Place place(dev, a[6]);
+  int with_status = PyObject_IsTrue(a[6]);
+  if (with_status < 0) throw Raised{};
+  with_status = with_status && !capturing();
+  const Place place(dev, a[7]);
+  const at::Tensor status =
+      with_status && !capturing() ? new_status(dev) : at::Tensor();
   const at::Tensor packed = make({static_cast<int64_t>(n)}, at::kByte, dev);
   void* pp = packed.data_ptr();
   check(without_gil([&] {
@@ -787,7 +809,7 @@ PyObject* fp4_mlp_pack(PyObject* const* a) {
                                           place.stream);
         }),
         "tp_fp4_mlp_pack_weights");
-  return wrapped(packed);
+  return tuple_of({packed, status});
 }
 
 // fp4_mlp(handle, h, f, format, X, packed, b1, b2, gamma, beta, x_scale, y_scale,
@@ -942,6 +964,6 @@ PyMODINIT_FUNC PyInit__pycall() {
   set<fp4_backward, 10>(9);
   set<fp4_mlp, 14>(10);
   set<fp4_quantize_both, 4>(11);
-  set<fp4_mlp_pack, 7>(12);
+  set<fp4_mlp_pack, 8>(12);
   return PyModule_Create(&module);
 }

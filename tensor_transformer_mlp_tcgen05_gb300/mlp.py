@@ -4,6 +4,8 @@ tp_mlp_backward.  All arithmetic happens in libtpmlp's kernels; PyTorch only
 provides device memory and the stream."""
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import binding as B_
@@ -42,6 +44,8 @@ class TensorParallelMLP:
         self._ws = None
         self._ws_tokens = None
         self._fp4_ws = None   # of the last forward_fp4
+        self._fp4_status = None   # where their first error stays
+        self._fp4_lock = threading.Lock()
 
     def close(self):
         if self.handle:
@@ -116,12 +120,17 @@ class TensorParallelMLP:
         return g
 
     def check(self, stream=None) -> int:
-        """Synchronise and return the device status (TPMLP_OK or an error)."""
-        for ws in (self._fp4_ws, self._ws):
-            if ws is None:
+        """Synchronise and return the device status, TPMLP_OK or an error: the first
+        one of forward_fp4's calls since the last check (in a block that never called
+        pack_fp4_weights, of the last such call), then of the last other call."""
+        block = lambda ws, s: B_.tp_mlp_check(self.handle, ws, s)
+        fp4 = ((self._fp4_ws, block) if self._fp4_status is None
+               else (self._fp4_status, B_.tp_fp4_check))
+        for at, read in (fp4, (self._ws, block)):
+            if at is None:
                 continue
-            with torch.cuda.device(ws.device):
-                rc = B_.tp_mlp_check(self.handle, ws, stream)
+            with torch.cuda.device(at.device):
+                rc = read(at, stream)
             if rc != B_.TPMLP_OK:
                 return rc
         return B_.TPMLP_OK
@@ -247,8 +256,13 @@ class TensorParallelMLP:
         (see tp_fp4_mlp_pack_weights) for forward_fp4.  The work, and the packed
         memory, belong to ``stream``, or to the current one of A's device."""
         h, f = self.hidden, self.ffn
-        packed = B_.tensor_calls().fp4_mlp_pack(self.handle, h, f,
-                                                _fp4_format(format), A, B, stream)
+        packed, status = B_.tensor_calls().fp4_mlp_pack(
+            self.handle, h, f, _fp4_format(format), A, B, self._fp4_status is None,
+            stream)
+        with self._fp4_lock:
+            if self._fp4_status is None and status is not None:
+                B_.tp_fp4_mlp_set_status(self.handle, status)
+                self._fp4_status = status
         return Fp4Weights(packed, format, (h, f))
 
     def forward_fp4(self, X, packed, b1=None, b2=None, gamma=None, beta=None,
@@ -257,7 +271,8 @@ class TensorParallelMLP:
         """Forward on weights from pack_fp4_weights (tp_fp4_mlp_forward): X (or
         LayerNorm(X)) and Y = GeLU(H) are quantized with nvfp4's powers of two
         ``x_scale`` and ``y_scale`` (mxfp4: 1).  Its workspace is of this call alone:
-        what forward() keeps for backward() stays."""
+        what forward() keeps for backward() stays.  A captured graph of it needs the
+        block as it needs its tensors: the block keeps the status of its calls."""
         h, f = self.hidden, self.ffn
         if not isinstance(packed, Fp4Weights) or packed.shape != (h, f):
             raise ValueError(f"packed must be the pack_fp4_weights of a block of "

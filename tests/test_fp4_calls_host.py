@@ -1,6 +1,7 @@
 """Calls of the four-bit operators that need no GPU."""
 import contextlib
 
+import pytest
 import torch
 
 from tensor_transformer_mlp_tcgen05_gb300 import binding as B
@@ -35,3 +36,26 @@ def test_check_runs_on_its_workspaces_device(monkeypatch):
     m._fp4_ws, m._ws = Memory(1), Memory(2)
     assert m.check() == B.TPMLP_OK
     assert seen == [(1, 1), (2, 2)] and current == [0]
+
+
+def test_status_of_a_block_and_its_refusals():
+    """A status word has to be aligned, and lies in nothing that a call writes."""
+    m = block()
+
+    def refused(code, call):
+        with pytest.raises(B.TPMLPError) as e:
+            call()
+        assert e.value.code == code
+
+    X, P, Z, W, S = (i << 32 for i in range(1, 6))   # far apart
+
+    def forward(status):
+        B.tp_fp4_mlp_set_status(m.handle, status)
+        B.tp_fp4_mlp_forward(m.handle, 10, B.TPFP4_NV, X, P, None, None, None, None,
+                             1.0, 1.0, Z, W, 1 << 30, stream=0)
+
+    refused(B.TPMLP_ERR_ALIGN, lambda: B.tp_fp4_mlp_set_status(m.handle, S + 8))
+    refused(B.TPMLP_ERR_ARG, lambda: B.tp_fp4_mlp_set_status(None, S))
+    refused(B.TPMLP_ERR_ARG, lambda: forward(Z + 16))
+    refused(B.TPMLP_ERR_ARG, lambda: forward(W))
+    B.tp_fp4_mlp_set_status(m.handle, None)

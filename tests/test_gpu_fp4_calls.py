@@ -72,6 +72,45 @@ def test_weights_of_too_few_bytes_are_refused():
                        want)
 
 
+def test_a_block_keeps_its_first_error_until_it_is_asked():
+    """A call that gave up, and right ones after it."""
+    T, h, f = 2000, 2048, 8192
+    m, X, A, Bw = block_case(T, h, f)
+    p = m.pack_fp4_weights(A, Bw)
+    q = m.pack_fp4_weights(A, Bw, format="mxfp4")   # keeps the status there is
+    want = m.forward_fp4(X, p)
+    assert m.check() == B.TPMLP_OK
+    B.tp_mlp_set_wait_budget(m.handle, 1)
+    m.forward_fp4(X, p)
+    torch.cuda.synchronize()
+    B.tp_mlp_set_wait_budget(m.handle, 2_000_000_000)
+    assert torch.equal(m.forward_fp4(X, p), want)
+    m.forward_fp4(X[:3], q)
+    assert m.forward_fp4(X[:0], p).shape == (0, h)
+    assert m.check() == B.TPMLP_ERR_TIMEOUT
+    assert m.check() == B.TPMLP_OK
+    assert torch.equal(m.forward_fp4(X, p), want) and m.check() == B.TPMLP_OK
+
+
+def test_a_block_that_packed_nothing_reports_its_last_call():
+    """Weights of another block, and weights packed in a captured graph."""
+    T, h, f = 2000, 2048, 8192
+    m, X, A, Bw = block_case(T, h, f)
+    p = m.pack_fp4_weights(A, Bw)
+    want = m.forward_fp4(X, p)
+    other = TensorParallelMLP(h, f, 1, T)
+    assert torch.equal(other.forward_fp4(X, p), want) and other.check() == B.TPMLP_OK
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        Z = other.forward_fp4(X, other.pack_fp4_weights(A, Bw))
+    g.replay()
+    assert torch.equal(Z, want) and other._fp4_status is None
+    B.tp_mlp_set_wait_budget(other.handle, 1)
+    other.forward_fp4(X, p)
+    assert other.check() == B.TPMLP_ERR_TIMEOUT
+    assert other.check() == B.TPMLP_OK and m.check() == B.TPMLP_OK
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_a_budget_counts_waits_of_its_own_kernel(fmt):
     """The block's second product is resident while the first one runs (48 places of
