@@ -692,8 +692,8 @@ PyObject* fp4_linear(PyObject* const* a) {
 }
 
 // fp4_backward(dy, x, weight_rows, format, dy_scale, x_scale, dtype, bias_grad,
-//              status, stream) -> (dx, dw, db or None): the gradients of fp4_linear, for
-// at least one token; weight_rows is W [K, N] packed along N.
+//              status, stream) -> (dx, dw, db or None): the gradients of fp4_linear;
+// weight_rows is W [K, N] packed along N.
 PyObject* fp4_backward(PyObject* const* a) {
   const Matrix dy("dy", tensor("dy", a[0])), x("x", tensor("x", a[1]));
   const at::Tensor& w = tensor("weight_rows", a[2]);
@@ -711,6 +711,19 @@ PyObject* fp4_backward(PyObject* const* a) {
   void* status = status_of(a[8], dev);
   const Place place(dev, a[9]);
   const at::Tensor dx = make({T, K}, plain_type(dtype), dev);
+  if (T == 0) {   // sums of nothing; the scales are checked all the same
+    void* wp = w.data_ptr();
+    auto check_scale = [&](long long cols, int type, double scale) {
+      check(lib.fp4_quantize(0, cols, type, nullptr, cols, 0, format, scale, nullptr,
+                             wp, nw, nullptr, nullptr, 0, place.stream),
+            "tp_fp4_quantize");
+    };
+    check_scale(N, dy.dtype, dy_scale);
+    check_scale(K, x.dtype, x_scale);
+    const auto fp32 = at::TensorOptions().dtype(at::kFloat).device(dev);
+    return tuple_of({dx, at::zeros({K, N}, fp32),
+                     sums ? at::zeros({N}, fp32) : at::Tensor()});
+  }
   const at::Tensor dw = make({K, N}, at::kFloat, dev);
   at::Tensor db, ws;
   // the packed operands belong to this call: calls on several streams, and

@@ -193,13 +193,6 @@ class Fp4Linear:
                              f"{self.inputs}], got {tuple(dy.shape)} and "
                              f"{tuple(x.shape)}")
         bias_grad = bias_grad and self.bias is not None
-        if dy.shape[0] == 0:
-            dx = calls.fp4_linear(dy, self.weight_rows.buffer, self.inputs,
-                                  self.outputs, code, 1.0, None, _dtype(dtype),
-                                  None, self._status, stream)
-            dw = dy.new_zeros((self.inputs, self.outputs), dtype=torch.float32)
-            db = dy.new_zeros(self.outputs, dtype=torch.float32)
-            return {"dx": dx, "dw": dw, "db": db if bias_grad else None}
         dx, dw, db = calls.fp4_backward(dy, x, self.weight_rows.buffer, code,
                                         _scale(dy_scale), _scale(x_scale),
                                         _dtype(dtype), bias_grad, self._status,

@@ -55,6 +55,36 @@ def test_packed_weights_belong_to_the_stream_that_writes_them(fmt):
             m.pack_fp4_weights(*bad, format=fmt)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_gradients_of_no_tokens(fmt):
+    """Their zeros are written on the call's stream and belong to it, and the arguments
+    are checked as for any number of tokens."""
+    lin = fp4.Fp4Linear(randn(64, 48), randn(48, dtype=F32), format=fmt)
+    x, dy = randn(0, 64), randn(0, 48)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        g = lin.backward(dy, x, stream=stream)
+        side.synchronize()
+        assert owner(g["dw"]) == owner(g["db"]) == side.cuda_stream
+        assert g["dx"].shape == (0, 64) and g["dx"].dtype == BF
+        assert g["dw"].shape == (64, 48) and g["db"].shape == (48,)
+        assert g["dw"].dtype == g["db"].dtype == F32
+        assert not g["dw"].any() and not g["db"].any()
+    assert lin.backward(dy, x, bias_grad=False)["db"] is None
+    assert lin.backward(dy, x, dtype=F32)["dx"].dtype == F32
+    for bad in (lambda: lin.backward(dy.half(), x), lambda: lin.backward(dy, x.half()),
+                lambda: lin.backward(dy.cpu(), x), lambda: lin.backward(dy, x.cpu()),
+                lambda: lin.backward(dy, x, dtype=torch.float16),
+                lambda: lin.backward(dy, x, x_scale=-1.0)):
+        with pytest.raises(ValueError):
+            bad()
+    for kw in (dict(dy_scale=3.0), dict(x_scale=3.0)):
+        with pytest.raises(B.TPMLPError) as e:
+            lin.backward(dy, x, **kw)
+        assert e.value.code == B.TPMLP_ERR_ARG
+
+
 def test_weights_of_too_few_bytes_are_refused():
     """As after a checkpoint that was cut off, or was written in another format: the
     products would read past the buffer."""
