@@ -87,7 +87,9 @@ class Fp4Tensor:
         return t[:self.rows, :(self.cols + block - 1) // block]
 
     def tensor_scale(self) -> torch.Tensor:
-        """g, a view of one fp32 value."""
+        """g, a view of one fp32 value (a matrix of no rows has none)."""
+        if self.rows == 0:
+            raise ValueError("a packed matrix of no rows has no scale")
         return self.buffer[16:20].view(torch.float32)
 
     def check(self, stream=None) -> int:
@@ -112,6 +114,8 @@ def quantize(x, format: str = "nvfp4", scale: "float | Fp4Tensor | None" = None,
     if isinstance(scale, Fp4Tensor):
         if scale.format != format:
             raise ValueError(f"scale is in {scale.format}, not in {format}")
+        if scale.rows == 0:   # (nothing was written)
+            raise ValueError("scale is a packed matrix of no rows, which has none")
         scale, like = None, scale.buffer
     if out is not None:
         shape = (x.shape[1], x.shape[0]) if transpose else tuple(x.shape)

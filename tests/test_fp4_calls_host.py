@@ -6,6 +6,7 @@ import torch
 
 from tensor_transformer_mlp_tcgen05_gb300 import binding as B
 from tensor_transformer_mlp_tcgen05_gb300 import build as build_mod
+from tensor_transformer_mlp_tcgen05_gb300 import fp4
 from tensor_transformer_mlp_tcgen05_gb300.mlp import TensorParallelMLP
 
 
@@ -59,3 +60,15 @@ def test_status_of_a_block_and_its_refusals():
     refused(B.TPMLP_ERR_ARG, lambda: forward(Z + 16))
     refused(B.TPMLP_ERR_ARG, lambda: forward(W))
     B.tp_fp4_mlp_set_status(m.handle, None)
+
+
+def test_a_matrix_of_no_rows_has_no_scale(monkeypatch):
+    """Quantising one writes nothing, its header included: what lies there is not
+    taken for g."""
+    none = fp4.Fp4Tensor(torch.empty(4096, dtype=torch.uint8), 0, 64, "nvfp4")
+    monkeypatch.setattr(B, "tensor_calls", lambda: pytest.fail("the call was made"))
+    with pytest.raises(ValueError):
+        fp4.quantize(torch.zeros(4, 64), scale=none)
+    with pytest.raises(ValueError):
+        none.tensor_scale()
+    assert none.check() == B.TPMLP_OK
