@@ -166,3 +166,205 @@ def test_a_budget_counts_waits_of_its_own_kernel(fmt):
         Z = m.forward_fp4(X, p)
         assert m.check() == B.TPMLP_OK
         assert torch.equal(Z, want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [8, 300])
+def test_memory_that_is_written_and_read_again_and_again(fmt, T):
+    """One buffer that a product writes and the next launches read, over and over, and
+    one packed matrix likewise: every launch starts while the one before it runs, and
+    none reads what an earlier round left (in a cache of its SM, say)."""
+    N, K, rounds = 1024, 512, 12
+    b = fp4.quantize(randn(N, K, seed=1, scale=K ** -0.5), fmt)
+    As = [fp4.quantize(randn(T, K, seed=10 + i), fmt) for i in range(rounds)]
+    biases = [randn(N, seed=30 + i, dtype=F32) for i in range(rounds)]
+    one = 1.0 if fmt == "nvfp4" else None
+    buf = torch.empty(T, N, dtype=BF, device="cuda")
+    bias = torch.empty(N, device="cuda")
+    P = fp4.quantize(torch.zeros(T, N, device="cuda"), fmt)
+
+    def launches(step):
+        out = []
+        for a, v in zip(As, biases):
+            bias.copy_(v)
+            step()
+            fp4.matmul(a, b, bias, out=buf)
+            step()
+            p = fp4.quantize(buf, fmt, scale=one, out=P)
+            step()
+            out.append(p.dequantize())
+            step()
+            for x in fp4.quantize_both(buf, fmt):
+                step()
+                out.append(x.dequantize(F32))
+            step()
+            fp4.matmul(a, b, out=buf)
+            step()
+            out.append(fp4.quantize(buf, fmt, transpose=True).dequantize(F32))
+            step()
+        return out
+
+    want = launches(torch.cuda.synchronize)
+    for _ in range(5):
+        got = launches(lambda: None)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = launches(lambda: None)
+    for _ in range(20):
+        g.replay()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert all(a.check() == 0 for a in As)
+
+
+# ------------------------------------------------------- the block's calls --
+
+def test_the_block_on_given_streams_and_from_several_threads():
+    """forward_fp4 of one block on several streams at once, from one thread and from
+    several, in both formats: the results of the calls one by one."""
+    from concurrent.futures import ThreadPoolExecutor
+    m, _, A, Bw = block_case(900, 256, 1024)
+    b1, b2 = randn(1024, seed=4, dtype=F32), randn(256, seed=5, dtype=F32)
+    packed = [m.pack_fp4_weights(A, Bw, format=f) for f in FORMATS]
+    xs = [randn(t, 256, seed=t) for t in (1, 8, 20, 100, 300, 900)]
+    want = [[m.forward_fp4(x, p, b1, b2) for p in packed] for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [m.forward_fp4(x, p, b1, b2, stream=(s, s.cuda_stream)[i % 2])
+           for i in range(6) for x, s in zip(xs, streams) for p in packed]
+    torch.cuda.synchronize()
+    assert all(torch.equal(z, w) for z, w in zip(got, 6 * sum(want, [])))
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for n in range(20):
+            z = m.forward_fp4(xs[i], packed[n % 2], b1, b2, stream=s)
+            s.synchronize()
+            assert torch.equal(z, want[i][n % 2])
+
+    with ThreadPoolExecutor(6) as ex:
+        list(ex.map(work, range(6)))
+    assert m.check() == B.TPMLP_OK
+
+
+# ------------------------------------------------- exact sums, large offsets --
+
+VALUES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def whole(rows, cols, seed, dtype=BF):
+    """E2M1 values of random signs, a 6 in every 16 columns: a matrix that is its own
+    quantisation (every scale is 1) in both formats, along its rows."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    v = torch.tensor(VALUES, dtype=dtype, device="cuda")
+    x = v[torch.randint(0, 8, (rows, cols), generator=g, device="cuda")]
+    x[:, ::16] = 6
+    sign = torch.randint(0, 2, (rows, cols), generator=g, device="cuda")
+    return torch.where(sign.bool(), x, -x)
+
+
+def exact_product(a, b):
+    """a b^T in 64 bits."""
+    return a.double() @ b.double().t()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,N,K", [(1, 1, 1), (1, 4096, 1024), (2, 300, 20480),
+                                   (8, 700, 16500), (16, 64, 512), (33, 129, 1000),
+                                   (64, 257, 2100), (128, 600, 4200),
+                                   (300, 700, 16500), (257, 300, 33), (700, 1001, 600),
+                                   (1500, 2500, 256), (1100, 2600, 16500),
+                                   (2100, 5000, 1040), (4096, 4096, 768)])
+def test_products_of_whole_numbers_are_exact(fmt, T, N, K):
+    """Multiples of 1/4, sums below 36 K = 2^19.5 (in quarters 2^21.5): fp32 holds every
+    one, in whatever order, so that one k-tile, row or scale out of place shows."""
+    x, w = whole(T, K, 1), whole(N, K, 2)
+    want = exact_product(x, w)
+    a, b = fp4.quantize(x, fmt), fp4.quantize(w, fmt)
+    assert torch.equal(a.dequantize(), x) and torch.equal(b.dequantize(), w)
+    assert torch.equal(fp4.matmul(a, b, dtype=F32).double(), want)
+    assert torch.equal(fp4.matmul(a, b), want.to(BF))
+    lin = fp4.Fp4Linear(w.t().contiguous(), format=fmt)
+    assert torch.equal(lin.weight.dequantize(), w)
+    assert torch.equal(lin.forward(x, dtype=F32).double(), want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_offsets_past_32_bits_of_unlike_rows(fmt):
+    """A matrix of 8.7e9 elements (17 GB of bf16, more than 4.3 GB of codes) whose rows
+    past 2^31 and 2^32 bytes, elements and bytes of codes are like no others: a read or
+    a write that wrapped would not find them.  Quantised along rows, columns and both,
+    read back, and in products as the many rows and as the weight, whose sums are exact
+    (at most 36 x 65536 = 2^21.2, in quarters 2^23.2)."""
+    rows, cols, some = 132096, 65536, 256
+    # rows at these wrap to row 0 or to one another: 2^31 and 2^32 bytes, 2^32 elements
+    # (2^31 bytes of codes), 2^32 bytes of codes; the last ends with the matrix
+    starts = (16384, 32768, 65536, 131072, rows - some)
+    one = 1.0 if fmt == "nvfp4" else None
+    x = whole(512, cols, 1).repeat(rows // 512, 1)
+    own = {}
+    for i, at in enumerate((0, *starts)):
+        own[at] = whole(some, cols, 10 + i)
+        x[at:at + some] = own[at]
+    q = fp4.quantize(x, fmt, scale=one)
+    assert q.buffer.numel() > 2 ** 32
+    r, t = fp4.quantize_both(x, fmt, one)
+    for p in (q, r):
+        out = p.dequantize()
+        assert all(torch.equal(out[at:at + some], v) for at, v in own.items())
+        del out
+    del r
+    # along the columns the blocks are of 16 or 32 rows, and starts multiples of 256
+    out = t.dequantize()
+    for at, v in own.items():
+        u = fp4.quantize(v, fmt, scale=one, transpose=True)
+        assert torch.equal(out[:, at:at + some], u.dequantize())
+    del out
+    t2 = fp4.quantize(x, fmt, scale=one, transpose=True)
+    kt = 16384 * 512 * (rows // 256)      # bytes of codes
+    assert torch.equal(t.buffer[4096:4096 + kt], t2.buffer[4096:4096 + kt])
+    del t, t2
+    w = whole(300, cols, 3)
+    got = fp4.matmul(q, fp4.quantize(w, fmt, scale=one), dtype=F32)
+    for at, v in own.items():
+        assert torch.equal(got[at:at + some].double(), exact_product(v, w))
+    for T in (2, 30, 300):    # quantised by the product, split, on pairs
+        a = whole(T, cols, 5)
+        got = fp4.matmul(fp4.quantize(a, fmt, scale=one), q, dtype=F32)
+        for at, v in own.items():
+            assert torch.equal(got[:, at:at + some].double(), exact_product(a, v))
+    del x, q
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 16), (300, 70), (129, 515),
+                                       (256, 256), (700, 1100), (257, 1000)])
+def test_both_ways_over_any_memory(fmt, rows, cols):
+    """quantize_both over packed buffers full of ones: everything that its products
+    read is written, and only the matrix's own."""
+    code, x = fp4._FORMATS[fmt], randn(rows, cols, seed=rows)
+    sizes = B.tp_fp4_bytes(rows, cols, code), B.tp_fp4_bytes(cols, rows, code)
+    res = []
+    for fill in (0xff, 0):
+        bufs = [torch.full((n + 256,), fill, dtype=torch.uint8, device="cuda")
+                for n in sizes]
+        B.tp_fp4_quantize_both(rows, cols, B.TPMLP_BF16, x, cols, code, 0.0, bufs[0],
+                               sizes[0], bufs[1], sizes[1])
+        assert all((b[n:] == fill).all() for b, n in zip(bufs, sizes))
+        r = fp4.Fp4Tensor(bufs[0][:sizes[0]], rows, cols, fmt)
+        t = fp4.Fp4Tensor(bufs[1][:sizes[1]], cols, rows, fmt)
+        assert r.check() == 0 and t.check() == 0
+        res.append((r, t))
+    for p, o, ref in zip(*res, (fp4.quantize(x, fmt),
+                                fp4.quantize(x, fmt, transpose=True))):
+        # codes to the end of the last k-tile, and its scales past the columns
+        assert torch.equal(p.codes(), o.codes()) and torch.equal(p.codes(), ref.codes())
+        assert torch.equal(p.scales(), ref.scales())
+        assert torch.equal(p.tensor_scale(), ref.tensor_scale())
+        block = 16 if fmt == "nvfp4" else 32
+        wide = [fp4.Fp4Tensor(m.buffer, m.rows, -(-m.cols // 256) * 256, fmt)
+                for m in (p, o, ref)]
+        past = [m.scales()[:, -(-p.cols // block):] for m in wide]
+        assert (past[0] == (0 if fmt == "nvfp4" else 127)).all()
+        assert torch.equal(past[0], past[1]) and torch.equal(past[0], past[2])
+        assert torch.equal(fp4.matmul(p, p), fp4.matmul(ref, ref))
