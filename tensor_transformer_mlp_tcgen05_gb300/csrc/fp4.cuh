@@ -108,6 +108,41 @@ __device__ __forceinline__ void let_next_launch_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Loads of what the launch before may have written.  (__ldg, a const restrict pointer
+// and ld.global.nc stand for memory that nothing writes as long as the kernel runs: a
+// compiler may move them before the wait, and the hardware need not see the writes.
+// Volatile, as the wait is, these stay behind it.)
+__device__ __forceinline__ uint32_t load_u8(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_u16(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_u32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float load_f32(const float* p) {
+  return __uint_as_float(load_u32(p));
+}
+__device__ __forceinline__ uint2 load_u32x2(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 load_u32x4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // x rounded to 14 significant bits "to odd": a value that is not one of them
 // gets the neighbour whose last bit is set.  It compares with every number of
 // 13 significant bits or fewer as x itself does, so codes and scales, whose

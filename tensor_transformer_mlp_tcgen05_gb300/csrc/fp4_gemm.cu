@@ -111,12 +111,19 @@ __device__ __forceinline__ void add_bias(const float* bias, int c0, int n,
                                          float (&v)[64]) {
   if (bias == nullptr) return;
   if (n >= 64 && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0) {
-    add_bias_n(bias, c0, v, 64);
+#pragma unroll
+    for (int i = 0; i < 64; i += 4) {
+      const uint4 u = load_u32x4(bias + c0 + i);
+      v[i] += __uint_as_float(u.x);
+      v[i + 1] += __uint_as_float(u.y);
+      v[i + 2] += __uint_as_float(u.z);
+      v[i + 3] += __uint_as_float(u.w);
+    }
     return;
   }
 #pragma unroll
   for (int i = 0; i < 64; ++i)
-    if (i < n) v[i] += __ldg(bias + c0 + i);
+    if (i < n) v[i] += load_f32(bias + c0 + i);
 }
 
 // One warp's staging buffer: 32 rows of 128 bytes (16-byte unit u of row r at

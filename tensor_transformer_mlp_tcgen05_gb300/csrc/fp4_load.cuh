@@ -47,7 +47,7 @@ __device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[WORDS]) 
   if constexpr (LD == 32) {
 #pragma unroll
     for (int i = 0; i < WORDS / 8; ++i)
-      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=r"(w[8 * i]), "=r"(w[8 * i + 1]), "=r"(w[8 * i + 2]),
                      "=r"(w[8 * i + 3]), "=r"(w[8 * i + 4]), "=r"(w[8 * i + 5]),
                      "=r"(w[8 * i + 6]), "=r"(w[8 * i + 7])
@@ -55,18 +55,17 @@ __device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[WORDS]) 
   } else {
 #pragma unroll
     for (int i = 0; i < WORDS / 4; ++i) {
-      const uint4 u = __ldg(static_cast<const uint4*>(p) + i);
+      const uint4 u = load_u32x4(static_cast<const uint4*>(p) + i);
       w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
     }
   }
 }
 
 __device__ __forceinline__ uint32_t element_bits(const __nv_bfloat16* p) {
-  return static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p)))
-         << 16;
+  return load_u16(p) << 16;
 }
 __device__ __forceinline__ uint32_t element_bits(const float* p) {
-  return __ldg(reinterpret_cast<const unsigned int*>(p));
+  return load_u32(p);
 }
 
 // The bytes of a matrix, from its first to past its last element.

@@ -53,7 +53,7 @@ __device__ __forceinline__ float inverse_g(const Packed& p, const Gain& gain,
 // threads 256 columns, a block 16 rows at a time and PASSES times those.
 template <class T, int FORMAT, int LD, int PASSES>
 __global__ void __launch_bounds__(THREADS)
-    rows_kernel(const T* __restrict__ x, long long stride, const Packed p,
+    rows_kernel(const T* x, long long stride, const Packed p,
                 const Gain gain) {
   if (gain.slots == 0) wait_for_launch_before();
   clear_status(p);
@@ -140,7 +140,7 @@ struct Two<__nv_bfloat16> {
   __device__ float a() const { return __uint_as_float(w << 16); }
   __device__ float b() const { return __uint_as_float(w & 0xffff0000u); }
   __device__ void load(const __nv_bfloat16* p) {
-    w = __ldg(reinterpret_cast<const unsigned int*>(p));
+    w = load_u32(p);
   }
   __device__ void load(const __nv_bfloat16* p, int n) {
     w = n >= 1 ? element_bits(p) >> 16 : 0u;
@@ -161,11 +161,12 @@ struct Two<float> {
   __device__ float a() const { return w.x; }
   __device__ float b() const { return w.y; }
   __device__ void load(const float* p) {
-    w = __ldg(reinterpret_cast<const float2*>(p));
+    const uint2 u = load_u32x2(p);
+    w = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
   }
   __device__ void load(const float* p, int n) {
-    w.x = n >= 1 ? __ldg(p) : 0.f;
-    w.y = n >= 2 ? __ldg(p + 1) : 0.f;
+    w.x = n >= 1 ? load_f32(p) : 0.f;
+    w.y = n >= 2 ? load_f32(p + 1) : 0.f;
   }
 };
 
@@ -238,8 +239,8 @@ __device__ __forceinline__ void quantize_staged(const uint8_t* s_x, const Packed
 // BOTH: the elements, read once, are quantised along the rows of x into rp too.
 template <class T, int FORMAT, bool PAIR, bool BOTH>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 3 : 2)
-    columns_kernel(const T* __restrict__ x, long long stride, int x_rows,
-                   const Packed p, const Gain gain, float* __restrict__ part,
+    columns_kernel(const T* x, long long stride, int x_rows, const Packed p,
+                   const Gain gain, float* __restrict__ part,
                    const Packed rp) {
   if (gain.slots == 0) wait_for_launch_before();
   clear_status(p);
@@ -354,7 +355,7 @@ constexpr int AMAX_UNITS = 2 * THREADS;
 
 template <class T, int LD>
 __global__ void __launch_bounds__(THREADS)
-    amax_kernel(const T* __restrict__ x, long long stride, long long rows,
+    amax_kernel(const T* x, long long stride, long long rows,
                 long long cols, Header* head) {
   wait_for_launch_before();
   let_next_launch_start();
@@ -496,11 +497,10 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int row = inside ? row0 + 16 * i : min(row0 + 16 * i, p.rows - 1);
-    c[i] = __ldg(reinterpret_cast<const uint2*>(
-        p.codes + code_row(row, kt, p.ktiles) + code_unit(row, unit / 2) +
-        unit % 2 * 8));
-    byte[i] = __ldg(p.scales + scale_word(row, kt, b / 4, p.ktiles,
-                                          tile_bytes(FORMAT)) + b % 4);
+    c[i] = load_u32x2(p.codes + code_row(row, kt, p.ktiles) +
+                      code_unit(row, unit / 2) + unit % 2 * 8);
+    byte[i] = load_u8(p.scales + scale_word(row, kt, b / 4, p.ktiles,
+                                            tile_bytes(FORMAT)) + b % 4);
   }
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {

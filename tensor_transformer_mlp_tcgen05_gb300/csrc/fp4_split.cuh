@@ -74,7 +74,7 @@ __device__ __forceinline__ void finish(const ProductArgs& a, int row, int n0,
   if (a.bias != nullptr) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < left) v[i] += __ldg(a.bias + n + i);
+      if (i < left) v[i] += load_f32(a.bias + n + i);
   }
   if constexpr (EPI == OUT_GELU_FP4) {
     // N is a multiple of 64: a lane's four are all in the matrix or none

@@ -1,5 +1,7 @@
 """Calls of the four-bit operators that need no GPU."""
 import contextlib
+import os
+import re
 
 import pytest
 import torch
@@ -72,3 +74,12 @@ def test_a_matrix_of_no_rows_has_no_scale(monkeypatch):
     with pytest.raises(ValueError):
         none.tensor_scale()
     assert none.check() == B.TPMLP_OK
+
+
+def test_kernels_that_start_early_read_memory_that_may_change():
+    """They run while the launch before them still writes, so that no load may be one
+    of memory that stays the same as long as the kernel runs."""
+    csrc = os.path.dirname(build_mod.__file__) + "/csrc/"
+    for name in sorted(n for n in os.listdir(csrc) if n.startswith("fp4")):
+        text = re.sub(r"//[^\n]*", "", open(csrc + name).read())
+        assert not re.search(r"__ldg|global\.nc|const \w+\s*\*\s*__restrict__", text), name
