@@ -178,8 +178,10 @@ int product(HandleCore* core, const char* name, int format,
   TRY(scales_map(&tsa, a.a, format));
   TRY(scales_map(&tsb, a.b, format));
   const size_t es = a.epilogue == fp4::OUT_FP32 ? 4 : 2;
+  // (a TMA store ends a row at the next 16-byte boundary, not at the map's last
+  // element: rows that end elsewhere would overwrite what lies behind them)
   const bool tma = a.epilogue != fp4::OUT_GELU_FP4 && aligned16(a.out) &&
-                   a.ldo * es % 16 == 0;
+                   a.ldo * es % 16 == 0 && a.N * es % 16 == 0;
   if (tma) TRY(out_map(&to, a.out, es == 4, a.M, a.N, a.ldo));
   return step([&] {
     return fp4::launch_product_pairs(format, ta, tsa, tb, tsb, tma ? &to : nullptr,

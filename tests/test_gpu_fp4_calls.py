@@ -247,6 +247,29 @@ def test_the_block_on_given_streams_and_from_several_threads():
     assert m.check() == B.TPMLP_OK
 
 
+@pytest.mark.parametrize("dtype,N,pad", [(BF, 55, 1), (BF, 1501, 3), (BF, 1502, 2),
+                                         (BF, 1500, 4), (BF, 1500, 12), (BF, 1504, 8),
+                                         (F32, 3, 1), (F32, 1501, 3), (F32, 1502, 2),
+                                         (F32, 1503, 1), (F32, 1503, 5),
+                                         (F32, 1504, 4)])
+@pytest.mark.parametrize("T", [7, 74, 700])
+def test_rows_that_end_off_16_bytes_leave_what_lies_behind_them(dtype, N, pad, T):
+    """Columns of a wider matrix whose rows are 16-byte aligned: products of every kind
+    write them, and neither the columns behind them nor what follows the last row."""
+    K = 320
+    x, w = whole(T, K, 1), whole(N, K, 2)
+    a, b = fp4.quantize(x), fp4.quantize(w)
+    lin = fp4.Fp4Linear(w.t().contiguous())
+    want = exact_product(x, w).to(dtype)
+    for call in (lambda out: fp4.matmul(a, b, dtype=dtype, out=out),
+                 lambda out: lin.forward(x, dtype=dtype, out=out)):
+        buf = torch.full((T * (N + pad) + 16,), 5.0, dtype=dtype, device="cuda")
+        rows = buf[:T * (N + pad)].view(T, N + pad)
+        assert torch.equal(call(rows[:, :N]), want)
+        assert torch.equal(rows[:, :N], want)
+        assert (rows[:, N:] == 5).all() and (buf[rows.numel():] == 5).all()
+
+
 # ------------------------------------------------- exact sums, large offsets --
 
 VALUES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
