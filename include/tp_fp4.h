@@ -19,6 +19,10 @@
  *              least -127 (s = 1 for a block of zeros), code = e2m1(x / s),
  *              value = code s; g = 1.
  *
+ * With a g far above what a matrix needs small blocks are lost: one whose largest |x|
+ * is at most 6 g 2^-10 (0.0059 for g = 1) has s = 0 and values of 0, and below 6 g 2^-6
+ * (0.094) s is one of E4M3's few subnormal numbers.
+ *
  * Quotients are not rounded before the code is chosen: every code is the one
  * the definition gives (a code of zero may have either sign).  A block that holds
  * an infinity or a NaN has the scale's NaN, and its values are NaN.
@@ -135,9 +139,12 @@ int tp_fp4_check(void* status, void* stream);
 
 /* ---- the MLP block's forward on four-bit weights ------------------------
  *   Xq = quantised Xn (= LayerNorm(X) rounded to bf16, or X), H = Xq Aq + b1,
- *   Y = GeLU(H) (fp32), Yq = quantised Y, Z = Yq Bq + b2 [+ X], one rounding to
+ *   Y = GeLU(H) (fp32, within 2.2e-7 in all and 4e-3 of itself down to H = -6),
+ *   Yq = quantised Y, Z = Yq Bq + b2 [+ X], one rounding to
  * bf16.  A and B are quantised along the products' inner dimension (NV: g from
- * each); x_scale and y_scale are NV's g of Xn and Y (MX: 0 or 1).  The t shards
+ * each); x_scale and y_scale are NV's g of Xn and Y (MX: 0 or 1): powers of two that
+ * the caller knows, not taken from Xn and Y; blocks far below 448 g are held coarsely
+ * or not at all (see TPFP4_NV).  The t shards
  * are consecutive ranges of the second product's one sum, so Z does not depend
  * on t.  The handle must be TPMLP_BF16 without dropout (TPMLP_ERR_ARG). */
 size_t tp_fp4_mlp_weights_bytes(const tp_mlp_handle* handle, int format);

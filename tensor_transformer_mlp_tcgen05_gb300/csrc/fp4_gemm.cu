@@ -30,11 +30,14 @@
 //
 // Measured: 8192 x 15360 x 5120 187 us NV (6.9 PFLOP/s), 180 MX; 8192 x 5120 x 20480
 // 236 NV (7.3 PFLOP/s), 222 MX (7.7).  A k-tile's MMAs take 512 cycles.  With 12
-// pairs it takes 591: 38 KB are copied into shared memory and as much is read from
-// it, 594 cycles at 128 bytes each.  With all 76 it takes 690 at 2070 MHz (operands
-// of zeros: no power cap): L2, 17 TB/s.  Operands of random values run into the power
-// cap instead: at 1.6 GHz, after seconds of them, 622 cycles.  256 x 256 is the
-// largest tile whose accumulators leave tensor memory for the scales.
+// pairs it takes 591, with all 76 690 at 2070 MHz (operands of zeros: no power cap;
+// 17 TB/s out of L2).  Operands of random values run into the power cap: at 1.6 GHz,
+// after seconds of them, 622 cycles.  What holds the cycles past 512 is not shown: the
+// profiler has the tensor pipe as the busiest unit (67 % of a launch of 8.4 rounds), L2
+// at 47 % and L1 and shared memory at 41 %; one write and one read of a stage's 38912
+// bytes (NV) at 128 bytes a cycle would be 608 cycles if the two excluded one another,
+// more than the 591 measured.  256 x 256 is the largest tile whose accumulators leave
+// tensor memory for the scales.
 #include <climits>
 
 #include "fp4_gemm.cuh"

@@ -106,7 +106,8 @@ def quantize(x, format: str = "nvfp4", scale: "float | Fp4Tensor | None" = None,
              stream=None) -> Fp4Tensor:
     """x [rows, cols] quantised along its rows, or with ``transpose`` along its
     columns as a packed [cols, rows].  ``scale``: nvfp4's power of two for the
-    whole matrix, a packed matrix whose own is taken (on the device), or by default
+    whole matrix (blocks with a largest |x| up to 6 * 2^-10 of it become zeros), a
+    packed matrix whose own is taken (on the device), or by default
     the one x needs (x is then read twice); mxfp4 has none (None or 1).  ``out``: a
     packed matrix of that shape and format, which is overwritten."""
     code = _format(format)
@@ -156,7 +157,8 @@ def matmul(a: Fp4Tensor, b: Fp4Tensor, bias=None, dtype=torch.bfloat16, out=None
 
 class Fp4Linear:
     """y = x W + bias on four-bit operands: W [K, N] (bf16 or fp32) is packed
-    once, x is quantised in every call.
+    once (both ways: the copy along N is the gradients'), x is quantised in every
+    call.
 
     The gradients are products of quantised matrices too, each quantised along the
     sum it takes part in: dx = dy W^T along N, dW = x^T dy along the tokens (the
@@ -179,8 +181,11 @@ class Fp4Linear:
 
     def forward(self, x, x_scale: float | None = 1.0, dtype=torch.bfloat16,
                 out=None, stream=None) -> torch.Tensor:
-        """x [T, K] -> [T, N].  ``x_scale``: nvfp4's power of two for x, or None
-        to take it from x."""
+        """x [T, K] -> [T, N].  ``x_scale``: nvfp4's power of two g for x, or None
+        to take it from x (which is then read twice, and up to 8 rows are quantised in
+        a launch of their own).  With the default of 1 a block of 16 whose largest |x|
+        is at most 0.0059 becomes zeros, and below 0.094 its scale is coarse:
+        activations that small want a smaller g, or None."""
         return self._calls.fp4_linear(
             x, self.weight.buffer, self.outputs, self.inputs, self._code,
             _scale(x_scale), self.bias, _dtype(dtype), out, self._status, stream)
@@ -188,7 +193,8 @@ class Fp4Linear:
     def backward(self, dy, x, x_scale: float | None = 1.0,
                  dy_scale: float | None = None, dtype=torch.bfloat16,
                  bias_grad: bool = True, stream=None) -> dict:
-        """From dy [T, N] and forward's x: a dict with dx [T, K] (``dtype``), dw
+        """From dy [T, N] and forward's x (``x_scale`` as there; ``dy_scale`` is taken
+        from dy by default): a dict with dx [T, K] (``dtype``), dw
         [K, N] (fp32) and, for a layer with a bias, db [N] (fp32), each new."""
         calls, code = self._calls, self._code
         if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0] or \
