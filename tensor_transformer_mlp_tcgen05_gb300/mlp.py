@@ -11,6 +11,8 @@ import torch
 from . import binding as B_
 from .fp4 import _format as _fp4_format
 
+_status_lock = threading.Lock()
+
 
 class TensorParallelMLP:
     """Megatron-style column/row-split MLP block with t logical shards
@@ -45,7 +47,6 @@ class TensorParallelMLP:
         self._ws_tokens = None
         self._fp4_ws = None   # of the last forward_fp4
         self._fp4_status = None   # where their first error stays
-        self._fp4_lock = threading.Lock()
 
     def close(self):
         if self.handle:
@@ -259,7 +260,7 @@ class TensorParallelMLP:
         packed, status = B_.tensor_calls().fp4_mlp_pack(
             self.handle, h, f, _fp4_format(format), A, B, self._fp4_status is None,
             stream)
-        with self._fp4_lock:
+        with _status_lock:   # (two threads may pack a block's first weights)
             if self._fp4_status is None and status is not None:
                 B_.tp_fp4_mlp_set_status(self.handle, status)
                 self._fp4_status = status
